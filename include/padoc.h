@@ -53,7 +53,7 @@ enum {
   PADOC_ERR_DEVICE_TIMEOUT = -5  /* a kernel gave up a bounded wait */
 };
 
-enum { PADOC_F32 = 0, PADOC_BF16 = 1 };
+enum { PADOC_F32 = 0, PADOC_BF16 = 1, PADOC_I4 = 2 /* KV pools only: 4-bit codes with scales */ };
 
 /* Packing of one page's tokens in the packed (THD) token stream.  The pages
  * fix no order; attention results per logical token do not depend on it. */
@@ -134,8 +134,9 @@ PADOC_API int padoc_tree_attn_varlen(padoc_tree_desc* desc, const void* q, const
  * ---------------------------------------------------------------------- */
 typedef struct padoc_kv_pool padoc_kv_pool;
 
-/* block_size must be 16; d must be 128; dtype PADOC_BF16.  max_seqs and
- * max_blocks_per_seq size the device block table (allocated on first device
+/* block_size must be 16; d must be 128; dtype PADOC_BF16 or PADOC_I4.  K and V
+ * storage each hold padoc_kv_storage_bytes bytes; the library zeroes them once,
+ * at the pool's first device use.  max_seqs and max_blocks_per_seq size the device block table (allocated on first device
  * use, see padoc_kv_pool_sync).  The environment variable
  * PADOC_FAULT_ALLOC_AFTER=n makes the n-th later block allocation fail with
  * PADOC_ERR_OOM (host fault injection for tests). */
@@ -143,12 +144,37 @@ PADOC_API int padoc_kv_pool_create(padoc_kv_pool** out, void* k_pool, void* v_po
                          int32_t block_size, int32_t Hkv, int32_t d, int32_t dtype,
                          int32_t max_seqs, int32_t max_blocks_per_seq);
 PADOC_API int padoc_kv_pool_destroy(padoc_kv_pool* pool);
+/* Bytes of a pool's K storage (and, again, of its V storage). */
+PADOC_API int padoc_kv_storage_bytes(int32_t num_blocks, int32_t Hkv, int32_t d, int32_t dtype, size_t* bytes);
+
+/* ---- The 4-bit pool (PADOC_I4). ----
+ * Storage [num_blocks, Hkv, 1152 bytes]; it is written from bf16 rows by every
+ * call that writes a bf16 pool (append, commit, padoc_kv_write) and read by
+ * every decode call and padoc_kv_gather, so only the dtype differs for a user.
+ * Each token's 128 dims of a kv head are cut into 8 groups of 16.  A group with
+ * largest magnitude a gets the scale s = a / 7 rounded to three mantissa bits
+ * (ties to even; steps of 2^-17 below 2^-14; at most 896) and every x the code
+ * n = x / s rounded to the nearest integer (ties to even), clamped to [-7, 7];
+ * the cache then holds n * s, exactly representable in bf16.  Magnitudes above
+ * 6272 saturate; a group below about 2^-18 * 7 reads back as zero.  A NaN or an
+ * infinity in a token's K or V of a head poisons the token for that head: its K
+ * reads back as NaN in the first group and zero elsewhere, its V as zero, so
+ * the queries that see the token get NaN and no others do.  (A bf16 value to be
+ * stored is not changed by the pool; the rotation of padoc_kv_write comes
+ * first, and its f32 result is quantised without a rounding to bf16 between.)
+ *
+ * The layout of the 1152 bytes of one (block, kv head), slot t = 0..15: a
+ * 32-bit word holds dims 8w .. 8w+7, nibble j (bits 4j..4j+3) the dim 8w + 2j,
+ * nibble 4 + j the dim 8w + 2j + 1, each as n + 8; a scale byte is bits 14..7
+ * of the scale as an fp16 number.
+ *   K: byte 256 c + 16 t: dims 32c .. 32c+31 (4 words), c = 0..3; byte 1024 + 8 t + g: scale of group g
+ *   V: byte 128 g + 8 t: dims 16g .. 16g+15 (2 words), g = 0..7; byte 1024 + 16 g + t: scale of group g */
 
 /* New empty sequence with room reserved for n_tokens (>= 0) tokens.
  * On PADOC_ERR_OOM nothing changes. */
 PADOC_API int padoc_kv_alloc(padoc_kv_pool* pool, int32_t n_tokens, int32_t* seq);
 
-/* Appends n tokens (device [n, Hkv, d] each for k and v, pool dtype) to the
+/* Appends n tokens (device [n, Hkv, d] each for k and v, bf16) to the
  * end of seq, growing it by fresh blocks if needed.  A forked sequence never
  * writes into a shared block: its own tokens start in a fresh block.
  * On PADOC_ERR_OOM nothing changes.  The copy runs on `stream`. */
@@ -199,6 +225,94 @@ PADOC_API int padoc_kv_pool_device(const padoc_kv_pool* pool, int32_t* device);
  * device-mismatch rejection.  Restore the true device before any decode
  * call is meant to run.  PADOC_ERR_INVALID before the first sync. */
 PADOC_API int padoc_debug_kv_pool_rehome(padoc_kv_pool* pool, int32_t device);
+
+/* ------------------------------------------------------------------------
+ * Rows in and out of the cache.  A rows handle names token ranges of
+ * sequences; one launch then writes them all from packed K / V rows, with the
+ * position rotation applied on the way, or reads them all back dense.  (The
+ * pages' serving loop writes each step's tokens to the branches' own blocks:
+ * HPD-Parsing, inference workflow; the rotation is the decoder's own.)
+ *
+ *   padoc_kv_rows_create   host only.  Sequence seqs[i] takes tokens [first[i],
+ *                          first[i] + n_i), n_i = row_offsets[i + 1] -
+ *                          row_offsets[i], and rows [row_offsets[i],
+ *                          row_offsets[i + 1]) of the tensors; first NULL
+ *                          means each sequence's current length.  The tokens
+ *                          must have slots already (padoc_kv_reserve).
+ *                          positions: host [n] or NULL, the position of each
+ *                          row (>= 0; draft siblings share one); NULL means
+ *                          the token's index in its sequence.
+ *   padoc_kv_rows_ws_size  device workspace bytes; 0 for short lists
+ *   padoc_kv_rows_upload   copies the lists into ws (16-byte aligned); once,
+ *                          before the first write or gather.  Those then only
+ *                          launch a kernel, so they may be captured.
+ *   padoc_kv_rows_free
+ * A handle stays valid, and may be used any number of times and for pools of
+ * other layers' storage only through handles of their own, until one of its
+ * sequences is released or trims the slots (the calls then return
+ * PADOC_ERR_INVALID).  Creating a handle changes nothing in the pool.
+ * ---------------------------------------------------------------------- */
+typedef struct padoc_kv_rows padoc_kv_rows;
+PADOC_API int padoc_kv_rows_create(padoc_kv_pool* pool, int32_t n_seqs, const int32_t* seqs, const int32_t* first,
+                                   const int32_t* row_offsets, const int32_t* positions, padoc_kv_rows** out);
+PADOC_API int padoc_kv_rows_ws_size(const padoc_kv_rows* rows, size_t* bytes);
+PADOC_API int padoc_kv_rows_upload(padoc_kv_rows* rows, void* ws, size_t ws_bytes, padoc_stream_t stream);
+PADOC_API int padoc_kv_rows_free(padoc_kv_rows* rows);
+
+/* Rotation by position.  Row p of cos_sin holds the rot_dim / 2 cosines, then
+ * the rot_dim / 2 sines, of position p's angles (f32; any base, scaling or
+ * amplitude is the table's).  The first rot_dim dims of a head turn, the rest
+ * stay; pair i is dims (i, i + rot_dim / 2), or (2i, 2i + 1) when interleaved:
+ *   (a, b) -> (a c - b s, b c + a s), in f32. */
+typedef struct {
+  const float* cos_sin; /* device [n_pos, rot_dim], 16-byte aligned */
+  int32_t n_pos;
+  int32_t rot_dim;      /* multiple of 16 in [0, d] */
+  int32_t interleaved;
+} padoc_rope;
+
+/* One step's projected rows.  Strides are elements between rows (multiples of
+ * 8), so q, k and v may be slices of one fused projection.  q / q_rot and k_rot
+ * are optional (NULL): the rotated rows out in bf16, dense, as
+ * padoc_branch_decode (q, k_new) and padoc_tree_attn_varlen take them.  q_rot
+ * may be q itself when q is dense, k_rot likewise k. */
+typedef struct {
+  const void* q; /* device [n, Hq, d] bf16, or NULL */
+  int64_t q_stride;
+  int32_t Hq;
+  void* q_rot;   /* device [n, Hq, d] bf16, or NULL */
+  const void* k; /* device [n, Hkv, d] bf16 */
+  int64_t k_stride;
+  const void* v; /* device [n, Hkv, d] bf16 */
+  int64_t v_stride;
+  void* k_rot;   /* device [n, Hkv, d] bf16, or NULL */
+} padoc_kv_step;
+
+/* Writes the rows' K (rotated) and V into their slots, bf16 or 4-bit as the
+ * pool is; rope NULL means no rotation.  Sequence lengths do not change: count
+ * the rows with padoc_kv_advance once they are meant to be seen.  Each sequence
+ * at most once in the handle; no row may be shared with the fork parent, and
+ * one that counts already may be rewritten only while no fork holds its block.
+ * Positions must lie inside the table.  Other slots of the blocks are left as
+ * they are.  One launch. */
+PADOC_API int padoc_kv_write(const padoc_kv_rows* rows, const padoc_rope* rope, const padoc_kv_step* step, void* ws,
+                             padoc_stream_t stream);
+
+/* Reads counted rows back: k, v device [n, Hkv, d] bf16, dense (what a chunked
+ * prefill gives padoc_tree_attn_varlen next to its new rows).  K comes as
+ * stored, that is rotated.  A sequence may be named several times, and rows
+ * shared with the fork parent may be read.  One launch. */
+PADOC_API int padoc_kv_gather(const padoc_kv_rows* rows, void* k, void* v, void* ws, padoc_stream_t stream);
+
+/* Reserve, write and advance in one call: appends rows [row_offsets[i],
+ * row_offsets[i + 1]) to sequence seqs[i] (each at most once).  ws: device,
+ * 16-byte aligned, 16 bytes for each block touched when those are more than
+ * 224, plus 4 bytes a row with positions; may be NULL when that is 0.  Not in
+ * use by a running call.  Validation and block reservation come first: on any
+ * refusal and on PADOC_ERR_OOM the pool is as it was. */
+PADOC_API int padoc_kv_append_rope(padoc_kv_pool* pool, int32_t n_seqs, const int32_t* seqs, const int32_t* row_offsets,
+                                   const int32_t* positions, const padoc_rope* rope, const padoc_kv_step* step,
+                                   void* ws, size_t ws_bytes, padoc_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * Backward of the packed tree-varlen forward (training; PaDoc, "Training
@@ -258,14 +372,14 @@ typedef struct {
 PADOC_API int padoc_branch_decode_ws_size(const padoc_kv_pool* pool, const padoc_decode_batch* batch,
                                 int32_t Hq, size_t* bytes);
 
-/*   q         device [nq, Hq, d] pool dtype; nq = q_offsets[n_branches]
- *   k_new     device [nq, Hkv, d]: keys of the step's own query tokens (not yet in the
+/*   q         device [nq, Hq, d] bf16; nq = q_offsets[n_branches]
+ *   k_new     device [nq, Hkv, d] bf16: keys of the step's own query tokens (not yet in the
  *   v_new               cache; commit accepted ones later with padoc_kv_append)
  *   tree_bits device [nq] uint16 or NULL: bit j of row i (within its branch) set iff
  *             query token j of the same branch is visible to token i; NULL means a chain
  *             (j <= i).  Bit i must be set for every row.  padoc_tree_mask_build fills it
  *             from a parent array.
- *   o         device [nq, Hq, d] pool dtype
+ *   o         device [nq, Hq, d] bf16
  *   lse       device [nq, Hq] f32, natural log
  *   ws        device workspace of at least padoc_branch_decode_ws_size bytes, 256-byte
  *             aligned, not shared with a call still running
@@ -370,7 +484,7 @@ PADOC_API int padoc_verify_accept(const void* logits, int32_t nq, int32_t vocab,
  *   row_offsets host [n_seqs + 1], row_offsets[0] = 0, non-decreasing:
  *               sequence i takes rows[row_offsets[i] .. row_offsets[i+1])
  *   rows        host: row indices into k_new / v_new, each in [0, n_src_rows)
- *   k_new/v_new device [n_src_rows, Hkv, d] pool dtype, 16-byte aligned
+ *   k_new/v_new device [n_src_rows, Hkv, d] bf16, 16-byte aligned
  *   ws          device, at least 16 * row_offsets[n_seqs] bytes, 16-byte
  *               aligned, not in use by a call still running
  * Blocks for every sequence are reserved before anything changes, so on

@@ -567,6 +567,7 @@ struct Seq {
   int32_t len = 0;       // tokens
   int32_t fork_len = 0;  // leading tokens shared from the fork parent
   int32_t n_shared = 0;  // leading blocks shared from the fork parent
+  uint64_t serial = 0;   // which sequence of the pool's life holds this slot
   std::vector<int32_t> blocks;
 };
 
@@ -584,6 +585,7 @@ struct padoc_kv_pool {
   std::vector<int32_t> free_seqs;    // stack
   int64_t fault_after = -1;          // fail the allocation that would exceed this count
   int64_t allocated = 0;             // blocks handed out so far
+  uint64_t serials = 0;              // sequences created so far
   // device mirror of the block table
   int device = -1;
   int32_t* d_table = nullptr;
@@ -602,6 +604,10 @@ struct padoc_kv_pool {
     }
   }
   bool seq_ok(int32_t s) const { return s >= 0 && s < max_seqs && seqs[s].live; }
+  size_t storage_bytes() const {
+    const size_t units = static_cast<size_t>(nb) * Hkv;
+    return dtype == PADOC_I4 ? units * kI4UnitBytes : units * bs * d * 2;
+  }
   int32_t own_blocks(const Seq& s) const { return static_cast<int32_t>(s.blocks.size()) - s.n_shared; }
   void mark(int32_t s) {
     if (!dirty[s]) {
@@ -635,6 +641,7 @@ struct padoc_kv_pool {
     free_seqs.pop_back();
     seqs[s] = Seq();
     seqs[s].live = true;
+    seqs[s].serial = ++serials;
     return s;
   }
 };
@@ -646,7 +653,8 @@ extern "C" int padoc_kv_pool_create(padoc_kv_pool** out, void* k_pool, void* v_p
   *out = nullptr;
   if (block_size != 16) return fail(PADOC_ERR_UNSUPPORTED, "kv_pool_create: block_size must be 16");
   if (d != 128) return fail(PADOC_ERR_UNSUPPORTED, "kv_pool_create: d must be 128");
-  if (dtype != PADOC_BF16) return fail(PADOC_ERR_UNSUPPORTED, "kv_pool_create: dtype must be bf16");
+  if (dtype != PADOC_BF16 && dtype != PADOC_I4)
+    return fail(PADOC_ERR_UNSUPPORTED, "kv_pool_create: dtype must be bf16 or i4");
   if (num_blocks <= 0 || Hkv <= 0 || max_seqs <= 0 || max_blocks_per_seq <= 0)
     return fail(PADOC_ERR_INVALID, "kv_pool_create: sizes must be positive");
   if (static_cast<int64_t>(num_blocks) * Hkv * block_size >= (int64_t(1) << 31))
@@ -836,7 +844,7 @@ static int pool_sync(padoc_kv_pool* pool, cudaStream_t stream) {
   if (!pool->zeroed && pool->k && pool->v) {
     // Unwritten slots of a partly filled block are read (and masked) by the
     // kernels; zeroing once keeps them finite.
-    const size_t bytes = static_cast<size_t>(pool->nb) * pool->Hkv * pool->bs * pool->d * 2;
+    const size_t bytes = pool->storage_bytes();
     e = cudaMemsetAsync(pool->k, 0, bytes, stream);
     if (e == cudaSuccess) e = cudaMemsetAsync(pool->v, 0, bytes, stream);
     if (e != cudaSuccess) return cuda_fail(e, "kv pool zero fill");
@@ -913,6 +921,23 @@ extern "C" int padoc_kv_append(padoc_kv_pool* pool, int32_t seq, const void* k, 
   int rc = pool_sync(pool, reinterpret_cast<cudaStream_t>(stream));
   if (rc) return rc;
   std::string err;
+  if (pool->dtype == PADOC_I4) {
+    RowsArgs a{};
+    a.table_row = pool->d_table + static_cast<size_t>(seq) * pool->max_bps + s.n_shared;
+    a.seq_first = own;
+    a.n_rows = n;
+    a.n_recs = static_cast<int32_t>((need_tokens + pool->bs - 1) / pool->bs) - own / pool->bs;
+    a.i4 = true;
+    a.k_pool = pool->k;
+    a.v_pool = pool->v;
+    a.Hkv = pool->Hkv;
+    a.k = static_cast<const __nv_bfloat16*>(k);
+    a.v = static_cast<const __nv_bfloat16*>(v);
+    a.k_stride = a.v_stride = static_cast<int64_t>(pool->Hkv) * pool->d;
+    rc = launch_kv_write(a, reinterpret_cast<cudaStream_t>(stream), &err);
+    if (rc) return fail(rc, "kv_append: %s", err.c_str());
+    return PADOC_OK;
+  }
   rc = launch_kv_append(pool->k, pool->v, pool->d_table + static_cast<size_t>(seq) * pool->max_bps + s.n_shared, own, n,
                         pool->Hkv, pool->d, k, v, reinterpret_cast<cudaStream_t>(stream), &err);
   if (rc) return fail(rc, "kv_append: %s", err.c_str());
@@ -979,6 +1004,7 @@ extern "C" int padoc_kv_commit(padoc_kv_pool* pool, int32_t n_seqs, const int32_
         e[0] = rows[j];
         e[1] = s.blocks[s.n_shared + t / pool->bs];
         e[2] = t % pool->bs;
+        if (pool->dtype == PADOC_I4) e[2] |= 1 << 8;  // a row record of one row
       }
       s.len += row_offsets[i + 1] - row_offsets[i];
       pool->mark(seqs[i]);
@@ -991,8 +1017,369 @@ extern "C" int padoc_kv_commit(padoc_kv_pool* pool, int32_t n_seqs, const int32_
   const cudaError_t e = cudaMemcpyAsync(ws, plan.data(), plan.size() * sizeof(int32_t), cudaMemcpyHostToDevice, st);
   if (e != cudaSuccess) return cuda_fail(e, "kv_commit: row list upload");
   std::string err;
+  if (pool->dtype == PADOC_I4) {
+    RowsArgs a{};
+    a.recs = static_cast<const RowRec*>(ws);
+    a.n_recs = static_cast<int32_t>(total);
+    a.n_rows = total;
+    a.i4 = true;
+    a.k_pool = pool->k;
+    a.v_pool = pool->v;
+    a.Hkv = pool->Hkv;
+    a.k = static_cast<const __nv_bfloat16*>(k_new);
+    a.v = static_cast<const __nv_bfloat16*>(v_new);
+    a.k_stride = a.v_stride = static_cast<int64_t>(pool->Hkv) * pool->d;
+    rc = launch_kv_write(a, st, &err);
+    if (rc) return fail(rc, "kv_commit: %s", err.c_str());
+    return PADOC_OK;
+  }
   rc = launch_commit(pool->k, pool->v, ws, total, pool->Hkv, k_new, v_new, st, &err);
   if (rc) return fail(rc, "kv_commit: %s", err.c_str());
+  return PADOC_OK;
+}
+
+extern "C" int padoc_kv_storage_bytes(int32_t num_blocks, int32_t Hkv, int32_t d, int32_t dtype, size_t* bytes) {
+  if (!bytes) return fail(PADOC_ERR_INVALID, "kv_storage_bytes: null bytes");
+  if (num_blocks <= 0 || Hkv <= 0) return fail(PADOC_ERR_INVALID, "kv_storage_bytes: sizes must be positive");
+  if (d != 128 || (dtype != PADOC_BF16 && dtype != PADOC_I4))
+    return fail(PADOC_ERR_UNSUPPORTED, "kv_storage_bytes: d must be 128 and dtype bf16 or i4");
+  padoc_kv_pool shape;
+  shape.nb = num_blocks;
+  shape.Hkv = Hkv;
+  shape.d = d;
+  shape.dtype = dtype;
+  *bytes = shape.storage_bytes();
+  return PADOC_OK;
+}
+
+// ============================================================== cache rows
+
+struct padoc_kv_rows {
+  padoc_kv_pool* pool = nullptr;
+  struct Range {
+    int32_t seq, first, n;
+    uint64_t serial;
+  };
+  std::vector<Range> ranges;
+  std::vector<RowRec> recs;
+  std::vector<int32_t> positions;  // as given, or empty
+  int64_t n_rows = 0;
+  int32_t max_pos = -1;            // largest position of any row
+  bool distinct = true;            // no sequence appears twice
+  bool uploaded = false;
+  std::vector<uint8_t> host;       // records, then positions, as laid out in ws
+  size_t off_pos = 0;
+};
+
+static int rows_build(padoc_kv_pool* pool, int32_t n_seqs, const int32_t* seqs, const int32_t* first,
+                      const int32_t* row_offsets, const int32_t* positions, padoc_kv_rows* r) {
+  r->pool = pool;
+  std::vector<uint8_t> seen(pool->max_seqs, 0);
+  const int32_t bs = pool->bs;
+  r->n_rows = n_seqs ? row_offsets[n_seqs] : 0;
+  for (int32_t i = 0; i < n_seqs; ++i) {
+    const int32_t q = seqs[i], n = row_offsets[i + 1] - row_offsets[i];
+    if (n < 0) return fail(PADOC_ERR_INVALID, "kv_rows: row_offsets decrease at %d", i);
+    if (!pool->seq_ok(q)) return fail(PADOC_ERR_INVALID, "kv_rows: %d is not a live sequence", q);
+    const Seq& s = pool->seqs[q];
+    const int32_t f = first ? first[i] : s.len;
+    const int64_t cap = s.fork_len + static_cast<int64_t>(pool->own_blocks(s)) * bs;
+    if (f < 0 || static_cast<int64_t>(f) + n > cap)
+      return fail(PADOC_ERR_INVALID, "kv_rows: tokens [%d, %lld) of sequence %d outside its %lld reserved slots", f,
+                  static_cast<long long>(f) + n, q, static_cast<long long>(cap));
+    if (n == 0) continue;
+    if (seen[q]) r->distinct = false;
+    seen[q] = 1;
+    r->ranges.push_back({q, f, n, s.serial});
+    // token t < fork_len sits at block t / bs of the shared blocks, an own
+    // token at (t - fork_len) / bs of the own ones
+    int32_t t = f, row = row_offsets[i];
+    const int32_t end = f + n;
+    while (t < end) {
+      const bool shared = t < s.fork_len;
+      const int32_t x = shared ? t : t - s.fork_len;
+      const int32_t run = std::min(std::min(end, shared ? s.fork_len : end) - t, bs - x % bs);
+      r->recs.push_back({row, s.blocks[(shared ? 0 : s.n_shared) + x / bs], (x % bs) | (run << 8), t});
+      t += run;
+      row += run;
+    }
+    r->max_pos = std::max(r->max_pos, end - 1);
+  }
+  if (positions) {
+    r->max_pos = -1;
+    for (int64_t j = 0; j < r->n_rows; ++j) {
+      if (positions[j] < 0) return fail(PADOC_ERR_INVALID, "kv_rows: positions[%lld] < 0", static_cast<long long>(j));
+      r->max_pos = std::max(r->max_pos, positions[j]);
+    }
+    r->positions.assign(positions, positions + r->n_rows);
+  }
+  const bool inlined = r->recs.size() <= static_cast<size_t>(kInlineRecs);
+  const size_t rec_bytes = inlined ? 0 : r->recs.size() * sizeof(RowRec);
+  r->off_pos = rec_bytes;
+  r->host.resize(rec_bytes + r->positions.size() * sizeof(int32_t));
+  if (rec_bytes) std::memcpy(r->host.data(), r->recs.data(), rec_bytes);
+  if (!r->positions.empty())
+    std::memcpy(r->host.data() + r->off_pos, r->positions.data(), r->positions.size() * sizeof(int32_t));
+  return PADOC_OK;
+}
+
+extern "C" int padoc_kv_rows_create(padoc_kv_pool* pool, int32_t n_seqs, const int32_t* seqs, const int32_t* first,
+                                    const int32_t* row_offsets, const int32_t* positions, padoc_kv_rows** out) {
+  if (!out) return fail(PADOC_ERR_INVALID, "kv_rows_create: null out");
+  *out = nullptr;
+  if (!pool) return fail(PADOC_ERR_INVALID, "kv_rows_create: null pool");
+  if (n_seqs < 0) return fail(PADOC_ERR_INVALID, "kv_rows_create: n_seqs < 0");
+  if (n_seqs > 0 && (!seqs || !row_offsets)) return fail(PADOC_ERR_INVALID, "kv_rows_create: null seqs / row_offsets");
+  if (n_seqs > 0 && row_offsets[0] != 0) return fail(PADOC_ERR_INVALID, "kv_rows_create: row_offsets[0] must be 0");
+  padoc_kv_rows* res = nullptr;
+  PADOC_TRY({
+    std::unique_ptr<padoc_kv_rows> r(new padoc_kv_rows());
+    const int rc = rows_build(pool, n_seqs, seqs, first, row_offsets, positions, r.get());
+    if (rc) return rc;
+    res = r.release();
+  });
+  *out = res;
+  return PADOC_OK;
+}
+
+extern "C" int padoc_kv_rows_free(padoc_kv_rows* rows) {
+  delete rows;
+  return PADOC_OK;
+}
+
+extern "C" int padoc_kv_rows_ws_size(const padoc_kv_rows* rows, size_t* bytes) {
+  if (!rows || !bytes) return fail(PADOC_ERR_INVALID, "kv_rows_ws_size: null argument");
+  *bytes = rows->host.size();
+  return PADOC_OK;
+}
+
+static int rows_check_ws(const padoc_kv_rows* rows, const void* ws, size_t ws_bytes) {
+  if (rows->host.empty()) return PADOC_OK;
+  if (!ws || !aligned16(ws)) return fail(PADOC_ERR_INVALID, "kv_rows: ws must be a 16-byte aligned device pointer");
+  if (ws_bytes < rows->host.size())
+    return fail(PADOC_ERR_INVALID, "kv_rows: workspace %zu bytes, need %zu", ws_bytes, rows->host.size());
+  return PADOC_OK;
+}
+
+extern "C" int padoc_kv_rows_upload(padoc_kv_rows* rows, void* ws, size_t ws_bytes, padoc_stream_t stream) {
+  if (!rows) return fail(PADOC_ERR_INVALID, "kv_rows_upload: null rows");
+  if (rows->n_rows == 0) {
+    rows->uploaded = true;
+    return PADOC_OK;
+  }
+  int rc = rows_check_ws(rows, ws, ws_bytes);
+  if (rc) return rc;
+  if (!rows->pool->k || !rows->pool->v) return fail(PADOC_ERR_INVALID, "kv_rows_upload: pool has no storage");
+  rc = padoc::pool_check_device(rows->pool, "kv_rows_upload");
+  if (rc) return rc;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  rc = pool_sync(rows->pool, st);  // the storage is zeroed once, before any row is written
+  if (rc) return rc;
+  if (!rows->host.empty()) {
+    const cudaError_t e = cudaMemcpyAsync(ws, rows->host.data(), rows->host.size(), cudaMemcpyHostToDevice, st);
+    if (e != cudaSuccess) return cuda_fail(e, "kv_rows_upload");
+  }
+  rows->uploaded = true;
+  return PADOC_OK;
+}
+
+// The checks a pass makes on the pool as it is now; `write` wants slots that
+// no other sequence can see, a read wants rows that have been counted.
+static int rows_check(const padoc_kv_rows* rows, const char* what, bool write, const void* ws) {
+  if (!rows->uploaded) return fail(PADOC_ERR_INVALID, "%s: the rows were not uploaded", what);
+  int rc = rows_check_ws(rows, ws, SIZE_MAX);
+  if (rc) return rc;
+  const padoc_kv_pool* pool = rows->pool;
+  rc = padoc::pool_check_device(pool, what);
+  if (rc) return rc;
+  if (write && !rows->distinct) return fail(PADOC_ERR_INVALID, "%s: a sequence is listed twice", what);
+  for (const auto& g : rows->ranges) {
+    if (!pool->seq_ok(g.seq) || pool->seqs[g.seq].serial != g.serial)
+      return fail(PADOC_ERR_INVALID, "%s: sequence %d was released since the rows were made", what, g.seq);
+    const Seq& s = pool->seqs[g.seq];
+    if (static_cast<int64_t>(g.first) + g.n > s.fork_len + static_cast<int64_t>(pool->own_blocks(s)) * pool->bs)
+      return fail(PADOC_ERR_INVALID, "%s: sequence %d gave up slots of the rows", what, g.seq);
+    if (!write) {
+      if (g.first + g.n > s.len)
+        return fail(PADOC_ERR_INVALID, "%s: tokens [%d, %d) of sequence %d, which holds %d", what, g.first, g.first + g.n,
+                    g.seq, s.len);
+      continue;
+    }
+    if (g.first < s.fork_len)
+      return fail(PADOC_ERR_INVALID, "%s: token %d of sequence %d is shared with its parent", what, g.first, g.seq);
+    if (g.first < s.len) {
+      // tokens that count already: only while no fork holds their blocks
+      const int32_t b0 = (g.first - s.fork_len) / pool->bs;
+      const int32_t b1 = (std::min(g.first + g.n, s.len) - 1 - s.fork_len) / pool->bs;
+      for (int32_t b = b0; b <= b1; ++b)
+        if (pool->refcnt[s.blocks[s.n_shared + b]] > 1)
+          return fail(PADOC_ERR_INVALID, "%s: counted tokens of sequence %d are shared with a fork", what, g.seq);
+    }
+  }
+  return PADOC_OK;
+}
+
+static RowsArgs rows_args(const padoc_kv_rows* rows, const void* ws) {
+  const padoc_kv_pool* pool = rows->pool;
+  RowsArgs a{};
+  if (rows->off_pos)
+    a.recs = static_cast<const RowRec*>(ws);
+  else
+    a.host_recs = rows->recs.data();
+  if (!rows->positions.empty())
+    a.positions = reinterpret_cast<const int32_t*>(static_cast<const uint8_t*>(ws) + rows->off_pos);
+  a.n_recs = static_cast<int32_t>(rows->recs.size());
+  a.n_rows = rows->n_rows;
+  a.i4 = pool->dtype == PADOC_I4;
+  a.k_pool = pool->k;
+  a.v_pool = pool->v;
+  a.Hkv = pool->Hkv;
+  return a;
+}
+
+static int check_step(const padoc_kv_pool* pool, const padoc_rope* rope, int32_t max_pos, const padoc_kv_step* st,
+                      const char* what) {
+  const int64_t row = static_cast<int64_t>(pool->Hkv) * pool->d;
+  if (!st) return fail(PADOC_ERR_INVALID, "%s: null step", what);
+  if (!st->k || !st->v || !aligned16(st->k) || !aligned16(st->v) || !aligned16(st->k_rot))
+    return fail(PADOC_ERR_INVALID, "%s: k/v/k_rot must be 16-byte aligned device pointers", what);
+  if (st->k_stride < row || st->v_stride < row || st->k_stride % 8 || st->v_stride % 8)
+    return fail(PADOC_ERR_INVALID, "%s: k/v row strides must be multiples of 8 of at least Hkv * d", what);
+  if (st->q || st->q_rot) {
+    if (!st->q || !st->q_rot || !aligned16(st->q) || !aligned16(st->q_rot))
+      return fail(PADOC_ERR_INVALID, "%s: q and q_rot must both be 16-byte aligned device pointers", what);
+    if (st->Hq <= 0) return fail(PADOC_ERR_INVALID, "%s: Hq must be positive", what);
+    if (st->q_stride < static_cast<int64_t>(st->Hq) * pool->d || st->q_stride % 8)
+      return fail(PADOC_ERR_INVALID, "%s: the q row stride must be a multiple of 8 of at least Hq * d", what);
+  }
+  if (!rope) return PADOC_OK;
+  if (rope->rot_dim < 0 || rope->rot_dim > pool->d || rope->rot_dim % 16)
+    return fail(PADOC_ERR_INVALID, "%s: rot_dim must be a multiple of 16 in [0, d]", what);
+  if (rope->rot_dim == 0) return PADOC_OK;
+  if (!rope->cos_sin || !aligned16(rope->cos_sin))
+    return fail(PADOC_ERR_INVALID, "%s: cos_sin must be a 16-byte aligned device pointer", what);
+  if (max_pos >= rope->n_pos)
+    return fail(PADOC_ERR_INVALID, "%s: position %d outside the table's %d", what, max_pos, rope->n_pos);
+  return PADOC_OK;
+}
+
+extern "C" int padoc_kv_write(const padoc_kv_rows* rows, const padoc_rope* rope, const padoc_kv_step* step, void* ws,
+                              padoc_stream_t stream) {
+  if (!rows) return fail(PADOC_ERR_INVALID, "kv_write: null rows");
+  int rc = check_step(rows->pool, rope, rows->max_pos, step, "kv_write");
+  if (rc) return rc;
+  if (rows->n_rows == 0) return PADOC_OK;
+  rc = rows_check(rows, "kv_write", true, ws);
+  if (rc) return rc;
+  RowsArgs a = rows_args(rows, ws);
+  if (rope && rope->rot_dim) {
+    a.cos_sin = rope->cos_sin;
+    a.rot_dim = rope->rot_dim;
+    a.interleaved = rope->interleaved != 0;
+  }
+  a.q = static_cast<const __nv_bfloat16*>(step->q);
+  a.k = static_cast<const __nv_bfloat16*>(step->k);
+  a.v = static_cast<const __nv_bfloat16*>(step->v);
+  a.q_stride = step->q_stride;
+  a.k_stride = step->k_stride;
+  a.v_stride = step->v_stride;
+  a.q_rot = static_cast<__nv_bfloat16*>(step->q_rot);
+  a.k_rot = static_cast<__nv_bfloat16*>(step->k_rot);
+  a.Hq = step->q ? step->Hq : 0;
+  std::string err;
+  rc = launch_kv_write(a, reinterpret_cast<cudaStream_t>(stream), &err);
+  if (rc) return fail(rc, "kv_write: %s", err.c_str());
+  return PADOC_OK;
+}
+
+extern "C" int padoc_kv_gather(const padoc_kv_rows* rows, void* k, void* v, void* ws, padoc_stream_t stream) {
+  if (!rows) return fail(PADOC_ERR_INVALID, "kv_gather: null rows");
+  if (rows->n_rows == 0) return PADOC_OK;
+  if (!k || !v || !aligned16(k) || !aligned16(v))
+    return fail(PADOC_ERR_INVALID, "kv_gather: k/v must be 16-byte aligned device pointers");
+  int rc = rows_check(rows, "kv_gather", false, ws);
+  if (rc) return rc;
+  RowsArgs a = rows_args(rows, ws);
+  a.k_out = static_cast<__nv_bfloat16*>(k);
+  a.v_out = static_cast<__nv_bfloat16*>(v);
+  std::string err;
+  rc = launch_kv_gather(a, reinterpret_cast<cudaStream_t>(stream), &err);
+  if (rc) return fail(rc, "kv_gather: %s", err.c_str());
+  return PADOC_OK;
+}
+
+extern "C" int padoc_kv_append_rope(padoc_kv_pool* pool, int32_t n_seqs, const int32_t* seqs, const int32_t* row_offsets,
+                                    const int32_t* positions, const padoc_rope* rope, const padoc_kv_step* step,
+                                    void* ws, size_t ws_bytes, padoc_stream_t stream) {
+  if (!pool) return fail(PADOC_ERR_INVALID, "kv_append_rope: null pool");
+  if (n_seqs < 0) return fail(PADOC_ERR_INVALID, "kv_append_rope: n_seqs < 0");
+  if (n_seqs == 0) return PADOC_OK;
+  if (!seqs || !row_offsets) return fail(PADOC_ERR_INVALID, "kv_append_rope: null seqs / row_offsets");
+  if (row_offsets[0] != 0) return fail(PADOC_ERR_INVALID, "kv_append_rope: row_offsets[0] must be 0");
+  padoc_kv_rows rows;
+  PADOC_TRY({
+    // everything that can be refused is, before a block is taken
+    std::vector<uint8_t> seen(pool->max_seqs, 0);
+    std::vector<int32_t> extra(n_seqs, 0);
+    int64_t extra_total = 0;
+    int32_t max_pos = -1;
+    for (int32_t i = 0; i < n_seqs; ++i) {
+      const int32_t q = seqs[i];
+      const int64_t n = static_cast<int64_t>(row_offsets[i + 1]) - row_offsets[i];
+      if (n < 0) return fail(PADOC_ERR_INVALID, "kv_append_rope: row_offsets decrease at %d", i);
+      if (!pool->seq_ok(q)) return fail(PADOC_ERR_INVALID, "kv_append_rope: %d is not a live sequence", q);
+      if (seen[q]) return fail(PADOC_ERR_INVALID, "kv_append_rope: sequence %d listed twice", q);
+      seen[q] = 1;
+      const Seq& s = pool->seqs[q];
+      const int64_t need = (static_cast<int64_t>(s.len - s.fork_len) + n + pool->bs - 1) / pool->bs;
+      if (s.n_shared + need > pool->max_bps)
+        return fail(PADOC_ERR_INVALID, "kv_append_rope: sequence %d would exceed max_blocks_per_seq", q);
+      extra[i] = static_cast<int32_t>(std::max<int64_t>(0, need - pool->own_blocks(s)));
+      extra_total += extra[i];
+      if (n > 0 && !positions) max_pos = std::max<int32_t>(max_pos, static_cast<int32_t>(s.len + n - 1));
+    }
+    const int64_t total = row_offsets[n_seqs];
+    for (int64_t j = 0; positions && j < total; ++j) {
+      if (positions[j] < 0) return fail(PADOC_ERR_INVALID, "kv_append_rope: positions[%lld] < 0", static_cast<long long>(j));
+      max_pos = std::max(max_pos, positions[j]);
+    }
+    int rc = check_step(pool, rope, max_pos, step, "kv_append_rope");
+    if (rc) return rc;
+    if (total == 0) return PADOC_OK;
+    if (!pool->k || !pool->v) return fail(PADOC_ERR_INVALID, "kv_append_rope: pool has no storage");
+    rc = padoc::pool_check_device(pool, "kv_append_rope");
+    if (rc) return rc;
+    // a bound on what the rows take in ws: a record for each block touched, a position a row
+    int64_t recs = 0;
+    for (int32_t i = 0; i < n_seqs; ++i)
+      if (row_offsets[i + 1] > row_offsets[i]) {
+        const int64_t own = pool->seqs[seqs[i]].len - pool->seqs[seqs[i]].fork_len;
+        recs += (own + row_offsets[i + 1] - row_offsets[i] + pool->bs - 1) / pool->bs - own / pool->bs;
+      }
+    const size_t need_ws = (recs > kInlineRecs ? static_cast<size_t>(recs) * sizeof(RowRec) : 0) +
+                           (positions ? static_cast<size_t>(total) * sizeof(int32_t) : 0);
+    if (need_ws && (!ws || !aligned16(ws) || ws_bytes < need_ws))
+      return fail(PADOC_ERR_INVALID, "kv_append_rope: ws must be 16-byte aligned and hold %zu bytes", need_ws);
+    std::vector<int32_t> fresh;
+    if (extra_total > static_cast<int64_t>(pool->free_blocks.size()) ||
+        !pool->take_blocks(static_cast<int32_t>(extra_total), &fresh))
+      return fail(PADOC_ERR_OOM, "kv_append_rope: out of blocks (%lld wanted)", static_cast<long long>(extra_total));
+    size_t next = 0;
+    for (int32_t i = 0; i < n_seqs; ++i)
+      if (extra[i]) {
+        Seq& s = pool->seqs[seqs[i]];
+        s.blocks.insert(s.blocks.end(), fresh.begin() + next, fresh.begin() + next + extra[i]);
+        next += extra[i];
+        pool->mark(seqs[i]);
+      }
+    rc = rows_build(pool, n_seqs, seqs, nullptr, row_offsets, positions, &rows);
+    if (rc) return rc;
+  });
+  int rc = padoc_kv_rows_upload(&rows, ws, ws_bytes, stream);
+  if (rc) return rc;
+  rc = padoc_kv_write(&rows, rope, step, ws, stream);
+  if (rc) return rc;
+  for (const auto& g : rows.ranges) pool->seqs[g.seq].len += g.n;
   return PADOC_OK;
 }
 
@@ -1009,11 +1396,144 @@ struct DecodePlan {
   int64_t part_rows = 0;
   bool tc_own = false;  // own pass on tensor cores (several query rows per branch and kv head)
   bool fused = false;   // verify: own suffix and query block walked by the prefix pass's units
+  // 4-bit pool: units of the prefix pass, then of the own pass, each by row count
+  std::vector<I4Unit> units;
+  std::vector<I4Merge> merges;
+  int32_t pre_first[4] = {0, 0, 0, 0}, own_first[4] = {0, 0, 0, 0};
+  size_t off_units = 0, off_merges = 0;
   size_t off_pages = 0, off_items = 0, off_branches = 0, off_qplen = 0, off_qbranch = 0, off_part_o = 0, off_part_lse = 0,
          off_work = 0, total = 0;
 };
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+// Units with at most 8, 16 and 32 rows, in this order; first[] are their bounds in `all`.
+void add_units(const std::vector<I4Unit> (&by_rows)[3], std::vector<I4Unit>* all, int32_t (&first)[4]) {
+  for (int i = 0; i < 3; ++i) {
+    first[i] = static_cast<int32_t>(all->size());
+    all->insert(all->end(), by_rows[i].begin(), by_rows[i].end());
+  }
+  first[3] = static_cast<int32_t>(all->size());
+}
+
+// The plan over a 4-bit pool.  The batch has been checked; P[p] is the longest
+// prefix a branch of page p sees.
+int plan_i4(const padoc_kv_pool* pool, const padoc_decode_batch* b, int32_t Hq, int n_sms, const std::vector<int32_t>& P,
+            DecodePlan* pl) {
+  const int32_t G = Hq / pool->Hkv, bs = pool->bs, nq = static_cast<int32_t>(pl->q_plen.size());
+  auto tile_of = [](int32_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; };
+  auto blocks = [bs](int64_t n) { return (n + bs - 1) / bs; };
+  // Chunks of keys: about two units for each CTA the GPU holds, within [8, 128]
+  // blocks (a unit's four warps then take at least two blocks each).
+  int64_t pre_steps = 0, own_steps = 0;
+  for (int32_t p = 0; p < b->n_pages; ++p) {
+    const int32_t b0 = b->branch_offsets[p], b1 = b->branch_offsets[p + 1];
+    if (b1 == b0) continue;
+    const int32_t rows = (b->q_offsets[b1] - b->q_offsets[b0]) * G, tr = tile_of(rows);
+    pre_steps += (rows + tr - 1) / tr * blocks(P[p]) * pool->Hkv;
+    for (int32_t i = b0; i < b1; ++i) {
+      const Seq& s = pool->seqs[b->branch_seq[i]];
+      const int32_t r = (b->q_offsets[i + 1] - b->q_offsets[i]) * G, t = tile_of(r);
+      own_steps += (r + t - 1) / t * blocks(s.len - s.fork_len) * pool->Hkv;
+    }
+  }
+  const int64_t slots = 8 * static_cast<int64_t>(n_sms);
+  const int64_t pre_chunk = std::max<int64_t>(8, std::min<int64_t>(128, pre_steps / slots));
+  const int64_t own_chunk = std::max<int64_t>(16, std::min<int64_t>(128, own_steps / slots));
+  std::vector<I4Unit> pre[3], own[3];
+  auto put = [](std::vector<I4Unit> (&to)[3], const I4Unit& u, int32_t tile) { to[tile == 8 ? 0 : tile == 16 ? 1 : 2].push_back(u); };
+  int64_t rows = 0;
+  for (int32_t p = 0; p < b->n_pages; ++p) {
+    const int32_t b0 = b->branch_offsets[p], b1 = b->branch_offsets[p + 1];
+    if (b1 == b0) continue;
+    const int32_t q0 = b->q_offsets[b0], nqp = b->q_offsets[b1] - q0;
+    const int64_t steps = blocks(P[p]);
+    const int32_t n_chunks = static_cast<int32_t>((steps + pre_chunk - 1) / pre_chunk);
+    const int64_t per = n_chunks ? (steps + n_chunks - 1) / n_chunks : 0;
+    const int64_t pre_base = rows, stride = static_cast<int64_t>(nqp) * Hq;
+    int32_t made = 0;
+    for (int32_t c = 0; c < n_chunks; ++c) {
+      const int64_t k0 = c * per * bs, k1 = std::min<int64_t>(P[p], (c + 1) * per * bs);
+      if (k1 <= k0) break;
+      // blocks of the page's sequence: its own tokens start in a fresh block
+      // only where its shared part ends on one (checked), so key k is in block k / bs
+      ++made;
+      const int32_t tr = tile_of(nqp * G);
+      for (int32_t r0 = 0; r0 < nqp * G; r0 += tr) {
+        I4Unit u{};
+        u.seq = b->page_seq[p];
+        u.blk0 = static_cast<int32_t>(k0 / bs);
+        u.key0 = static_cast<int32_t>(k0);
+        u.n_keys = static_cast<int32_t>(k1 - k0);
+        u.q_first = q0;
+        u.row0 = r0;
+        u.rows = std::min(tr, nqp * G - r0);
+        u.branch = -1;
+        u.part = pre_base + c * stride;
+        put(pre, u, tr);
+      }
+    }
+    rows += made * stride;
+    for (int32_t i = b0; i < b1; ++i) {
+      const Seq& s = pool->seqs[b->branch_seq[i]];
+      const int32_t qf = b->q_offsets[i], ql = b->q_offsets[i + 1] - qf, own_len = s.len - s.fork_len;
+      for (int32_t r = qf; r < qf + ql; ++r) pl->q_plen[r] = s.fork_len;
+      const int64_t osteps = blocks(own_len);
+      const int32_t oc = std::max<int32_t>(1, static_cast<int32_t>((osteps + own_chunk - 1) / own_chunk));
+      const int64_t oper = (osteps + oc - 1) / oc;
+      const int32_t n_own = oper ? static_cast<int32_t>((osteps + oper - 1) / oper) : 1;
+      // Few partial results join in the own unit's epilogue (one after another
+      // there); many in the merge kernel.
+      const bool merge = n_own > 1 || made > 8;
+      const int64_t pre_at = pre_base + static_cast<int64_t>(qf - q0) * Hq;
+      const int64_t own_base = rows, own_stride = static_cast<int64_t>(ql) * Hq;
+      if (merge) rows += n_own * own_stride;
+      const int32_t tr = tile_of(ql * G);
+      for (int32_t c = 0; c < n_own; ++c)
+        for (int32_t r0 = 0; r0 < ql * G; r0 += tr) {
+          I4Unit u{};
+          u.seq = b->branch_seq[i];
+          u.blk0 = s.n_shared + static_cast<int32_t>(c * oper);
+          u.key0 = static_cast<int32_t>(c * oper * bs);
+          u.n_keys = static_cast<int32_t>(std::min<int64_t>(own_len, (c + 1) * oper * bs)) - u.key0;
+          u.q_first = qf;
+          u.row0 = r0;
+          u.rows = std::min(tr, ql * G - r0);
+          u.branch = i;
+          u.qb_first = qf;
+          u.q_len = c + 1 == n_own ? ql : 0;
+          u.part = merge ? own_base + c * own_stride : -1;
+          u.n_pre = merge ? 0 : made;
+          u.pre = pre_at;
+          u.pre_stride = stride;
+          put(own, u, tr);
+        }
+      if (merge)
+        for (int32_t r = 0; r < ql; ++r)
+          pl->merges.push_back({qf + r, made, n_own, 0, pre_at + static_cast<int64_t>(r) * Hq, stride,
+                                own_base + static_cast<int64_t>(r) * Hq, own_stride});
+    }
+  }
+  add_units(pre, &pl->units, pl->pre_first);
+  add_units(own, &pl->units, pl->own_first);
+  if (static_cast<int64_t>(pl->units.size()) * pool->Hkv >= (int64_t(1) << 31) ||
+      static_cast<int64_t>(nq) * Hq >= (int64_t(1) << 31))
+    return fail(PADOC_ERR_UNSUPPORTED, "branch_decode: batch too large");
+  pl->part_rows = rows;
+  size_t off = 0;
+  pl->off_units = off;
+  off = align_up(off + pl->units.size() * sizeof(I4Unit), 256);
+  pl->off_merges = off;
+  off = align_up(off + pl->merges.size() * sizeof(I4Merge), 256);
+  pl->off_qplen = off;
+  off = align_up(off + pl->q_plen.size() * sizeof(int32_t), 256);
+  pl->off_part_o = off;
+  off = align_up(off + static_cast<size_t>(rows) * kHeadDim * sizeof(float), 256);
+  pl->off_part_lse = off;
+  off = align_up(off + static_cast<size_t>(rows) * sizeof(float), 256);
+  pl->total = off;
+  return PADOC_OK;
+}
 
 int plan_decode(const padoc_kv_pool* pool, const padoc_decode_batch* b, int32_t Hq, int n_sms, DecodePlan* pl) {
   if (!pool || !b) return fail(PADOC_ERR_INVALID, "branch_decode: null argument");
@@ -1082,6 +1602,7 @@ int plan_decode(const padoc_kv_pool* pool, const padoc_decode_batch* b, int32_t 
     const int32_t rt = (nqp * G + kTileRows - 1) / kTileRows;
     work_tiles += static_cast<int64_t>(rt) * ((P[p] + kTileKeys - 1) / kTileKeys) * pool->Hkv;
   }
+  if (pool->dtype == PADOC_I4) return plan_i4(pool, b, Hq, n_sms, P, pl);
   int64_t ct = work_tiles / (2 * static_cast<int64_t>(n_sms));
   ct = std::max<int64_t>(8, std::min<int64_t>(kMaxChunkTiles, ct));
   if (want_fused) {
@@ -1214,6 +1735,16 @@ extern "C" int padoc_decode_plan_create(padoc_kv_pool* pool, const padoc_decode_
     p->n_pages = batch->n_pages;
     p->n_branches = batch->n_branches;
     p->host.assign(p->pl.off_part_o, 0);
+    if (pool->dtype == PADOC_I4) {
+      const DecodePlan& pl = p->pl;
+      if (!pl.units.empty()) std::memcpy(p->host.data() + pl.off_units, pl.units.data(), pl.units.size() * sizeof(I4Unit));
+      if (!pl.merges.empty())
+        std::memcpy(p->host.data() + pl.off_merges, pl.merges.data(), pl.merges.size() * sizeof(I4Merge));
+      if (!pl.q_plen.empty())
+        std::memcpy(p->host.data() + pl.off_qplen, pl.q_plen.data(), pl.q_plen.size() * sizeof(int32_t));
+      *out = p.release();
+      return PADOC_OK;
+    }
     std::memcpy(p->host.data() + p->pl.off_pages, p->pl.pages.data(), p->pl.pages.size() * sizeof(DecPage));
     std::memcpy(p->host.data() + p->pl.off_items, p->pl.items.data(), p->pl.items.size() * sizeof(DecItem));
     std::memcpy(p->host.data() + p->pl.off_branches, p->pl.branches.data(),
@@ -1304,15 +1835,51 @@ static DecodeArgs decode_args(const padoc_decode_plan* plan, const void* q, cons
   return a;
 }
 
+static I4Args i4_args(const padoc_decode_plan* plan, const void* q, const void* k_new, const void* v_new,
+                      const uint16_t* tree_bits, void* o, float* lse, float scale, void* ws) {
+  const DecodePlan& pl = plan->pl;
+  const padoc_kv_pool* pool = plan->pool;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  I4Args a{};
+  a.units = reinterpret_cast<const I4Unit*>(w + pl.off_units);
+  a.merges = reinterpret_cast<const I4Merge*>(w + pl.off_merges);
+  a.q_plen = reinterpret_cast<const int32_t*>(w + pl.off_qplen);
+  a.table = pool->d_table;
+  a.max_bps = pool->max_bps;
+  a.Hq = plan->Hq;
+  a.Hkv = pool->Hkv;
+  a.group = plan->Hq / pool->Hkv;
+  a.sl2 = (scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(pool->d))) * 1.44269504088896340736f;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k_new = static_cast<const __nv_bfloat16*>(k_new);
+  a.v_new = static_cast<const __nv_bfloat16*>(v_new);
+  a.tree_bits = tree_bits;
+  a.o = static_cast<__nv_bfloat16*>(o);
+  a.lse = lse;
+  a.part_o = reinterpret_cast<float*>(w + pl.off_part_o);
+  a.part_lse = reinterpret_cast<float*>(w + pl.off_part_lse);
+  a.k_pool = pool->k;
+  a.v_pool = pool->v;
+  return a;
+}
+
 extern "C" int padoc_decode_prefix_pass(const padoc_decode_plan* plan, const void* q, float scale, void* ws,
                                         padoc_stream_t stream) {
   if (!plan) return fail(PADOC_ERR_INVALID, "decode_prefix_pass: null plan");
-  if (plan->n_branches == 0 || plan->pl.items.empty()) return PADOC_OK;
+  const bool i4 = plan->pool->dtype == PADOC_I4;
+  if (plan->n_branches == 0 || (i4 ? plan->pl.pre_first[3] == 0 : plan->pl.items.empty())) return PADOC_OK;
   if (plan->pl.fused) return PADOC_OK;  // the own pass walks the prefix too
   int rc = check_ws(plan, ws, SIZE_MAX);
   if (rc) return rc;
   if (!q || !aligned16(q)) return fail(PADOC_ERR_INVALID, "decode_prefix_pass: q must be a 16-byte aligned device pointer");
   if (!plan->pool->d_table) return fail(PADOC_ERR_INVALID, "decode_prefix_pass: plan was not uploaded");
+  if (i4) {
+    const I4Args a = i4_args(plan, q, nullptr, nullptr, nullptr, nullptr, nullptr, scale, ws);
+    std::string err;
+    rc = launch_i4_units(a, plan->pl.pre_first, reinterpret_cast<cudaStream_t>(stream), &err);
+    if (rc) return fail(rc, "decode_prefix_pass: %s", err.c_str());
+    return PADOC_OK;
+  }
   const DecodeArgs a = decode_args(plan, q, nullptr, nullptr, nullptr, nullptr, nullptr, scale, ws);
   std::string err;
   rc = launch_decode_prefix(a, reinterpret_cast<cudaStream_t>(stream), &err);
@@ -1331,6 +1898,15 @@ extern "C" int padoc_decode_own_pass(const padoc_decode_plan* plan, const void* 
   if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(o) || !aligned16(lse))
     return fail(PADOC_ERR_INVALID, "decode_own_pass: tensors must be 16-byte aligned");
   if (!plan->pool->d_table) return fail(PADOC_ERR_INVALID, "decode_own_pass: plan was not uploaded");
+  if (plan->pool->dtype == PADOC_I4) {
+    const I4Args a = i4_args(plan, q, k_new, v_new, tree_bits, o, lse, scale, ws);
+    std::string err;
+    rc = launch_i4_units(a, plan->pl.own_first, reinterpret_cast<cudaStream_t>(stream), &err);
+    if (!rc)
+      rc = launch_i4_merge(a, static_cast<int32_t>(plan->pl.merges.size()), reinterpret_cast<cudaStream_t>(stream), &err);
+    if (rc) return fail(rc, "decode_own_pass: %s", err.c_str());
+    return PADOC_OK;
+  }
   const DecodeArgs a = decode_args(plan, q, k_new, v_new, tree_bits, o, lse, scale, ws);
   std::string err;
   // Several query rows per (branch, kv head) (verify): tensor cores.  With

@@ -3,6 +3,7 @@
 #include <cstdint>
 #include <string>
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 namespace padoc {
@@ -32,6 +33,7 @@ constexpr int kTileKeys = 128;  // keys per K/V tile
 constexpr int kTileRows = 128;  // MMA M: query rows (tokens x heads of a GQA group)
 constexpr int kMaxChunkTiles = 40;  // prefix pass: key tiles in one chunk of a page's prefix, at most
 constexpr int kHeadDim = 128;   // d of the tensor-core path
+constexpr int kI4UnitBytes = 1152;  // one (block, kv head) of a 4-bit pool, K or V (kv_i4.cuh)
 
 struct FwdPlan {
   const QSeg* qsegs;
@@ -146,6 +148,83 @@ struct DecodeArgs {
   int64_t num_blocks;
 };
 
+// ---------------------------------------------------------------- decode over a 4-bit pool
+// One kv head's work of a CTA: query rows against a run of cached keys.  Rows
+// are (token, head of the group): row R is token q_first + R / G.
+struct I4Unit {
+  int32_t seq, blk0;       // block-table row and the place in it of the first key's block
+  int32_t key0, n_keys;    // first key (prefix: its position in the page's prefix) and keys
+  int32_t q_first, row0, rows;
+  int32_t branch;          // own keys of this branch; -1: keys of a page's prefix
+  int32_t q_len, qb_first; // query tokens of the branch when the unit takes its query block, else 0
+  int32_t n_pre, pad;      // prefix partial results merged here, one each pre_stride from pre
+  int64_t pre, pre_stride; // partial rows, counted from (q_first, head 0)
+  int64_t part;            // where the unit's partial rows go (as pre), or -1: write o and lse
+};
+// A query token whose partial results the merge kernel joins.
+struct I4Merge {
+  int32_t token, n_pre, n_own, pad;
+  int64_t pre, pre_stride, own, own_stride;
+};
+struct I4Args {
+  const I4Unit* units;
+  const I4Merge* merges;
+  const int32_t* q_plen;  // [nq] prefix tokens visible to each query token
+  const int32_t* table;
+  int32_t max_bps, unit0;
+  int32_t Hq, Hkv, group;
+  float sl2;  // scale * log2(e)
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k_new;
+  const __nv_bfloat16* v_new;
+  const uint16_t* tree_bits;
+  __nv_bfloat16* o;
+  float* lse;
+  float* part_o;    // [rows][d] normalised
+  float* part_lse;  // [rows] log2 units
+  const void* k_pool;
+  const void* v_pool;
+};
+
+// ---------------------------------------------------------------- cache rows
+// Up to 16 consecutive rows of one pool block: source / destination rows
+// [row, row + n) are its slots [slot, slot + n).  slot_n = slot | n << 8; pos
+// is the first row's position when the rows have no position array.
+struct RowRec {
+  int32_t row, block, slot_n, pos;
+};
+// Records of a list up to this long ride in the kernel's parameters (with the
+// arguments below 4 KB).
+constexpr int kInlineRecs = 224;
+
+struct RowsArgs {
+  const RowRec* recs;       // device, or null
+  const RowRec* host_recs;  // host, at most kInlineRecs, or null
+  // neither: the rows [seq_first, seq_first + n_rows) of one sequence's own
+  // tokens, through its row of the block table (from its first own block)
+  const int32_t* table_row;
+  int32_t seq_first;
+  int32_t n_recs;
+  int64_t n_rows;
+  bool i4;
+  void* k_pool;
+  void* v_pool;
+  int32_t Hkv, Hq;
+  // write
+  const int32_t* positions;  // device [n_rows], or null: RowRec::pos
+  const float* cos_sin;      // [position][cosines, then sines]
+  int32_t rot_dim, interleaved;
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  int64_t q_stride, k_stride, v_stride;  // elements between rows
+  __nv_bfloat16* q_rot;
+  __nv_bfloat16* k_rot;
+  // gather
+  __nv_bfloat16* k_out;
+  __nv_bfloat16* v_out;
+};
+
 // Launchers (return 0 or a PADOC_ERR_* code, message in *err).
 int launch_fwd_bf16(const FwdArgs& a, cudaStream_t s, std::string* err);
 int launch_fwd_f32(const FwdArgs& a, cudaStream_t s, std::string* err);
@@ -168,6 +247,12 @@ int launch_accept(const void* logits, int64_t V, int32_t nq, const int32_t* toke
 // plan: device int4 per row {source row, block, slot, 0}
 int launch_commit(void* k_pool, void* v_pool, const void* plan, int64_t n_rows, int32_t Hkv, const void* k,
                   const void* v, cudaStream_t s, std::string* err);
+
+// Units [first[0], first[1]) have at most 8 rows, [first[1], first[2]) 16, [first[2], first[3]) 32.
+int launch_i4_units(const I4Args& a, const int32_t (&first)[4], cudaStream_t s, std::string* err);
+int launch_i4_merge(const I4Args& a, int32_t n_merges, cudaStream_t s, std::string* err);
+int launch_kv_write(const RowsArgs& a, cudaStream_t s, std::string* err);
+int launch_kv_gather(const RowsArgs& a, cudaStream_t s, std::string* err);
 
 int launch_bwd_core(const BwdArgs& a, int32_t dtype, cudaStream_t s, std::string* err);
 int launch_bwd_delta(const BwdArgs& a, int32_t dtype, cudaStream_t s, std::string* err);

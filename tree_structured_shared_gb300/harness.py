@@ -156,8 +156,9 @@ class Decode:
     block, all resident on the GPU."""
 
     def __init__(self, w: wl.DecodeWorkload, vals: Optional[wl.DecodeValues] = None, seed: int = 0,
-                 device="cuda", tree: bool = True, slack_blocks: int = 8, fragment: bool = False):
-        """fragment: the pool has twice the blocks, every other one held by a
+                 device="cuda", tree: bool = True, slack_blocks: int = 8, fragment: bool = False,
+                 dtype: int = padoc.BF16):
+        """dtype: of the pool (padoc.BF16 or padoc.I4).  fragment: the pool has twice the blocks, every other one held by a
         spacer sequence and the rest handed out in a shuffled order, so no
         two blocks of a sequence are physically consecutive by design."""
         self.w = w
@@ -167,11 +168,14 @@ class Decode:
         n_spacers = nb if fragment else 0
         nb += n_spacers
         max_bps = max([(p.prefix_len + 15) // 16 + (max(p.own_len or [0]) + 15) // 16 + 2 for p in w.pages] + [4])
-        self.k_pool = torch.empty(nb, Hkv, 16, d, dtype=torch.bfloat16, device=device)
-        self.v_pool = torch.empty(nb, Hkv, 16, d, dtype=torch.bfloat16, device=device)
+        size = padoc.kv_storage_bytes(nb, Hkv, d, dtype)
+        self.k_pool = torch.empty(size, dtype=torch.uint8, device=device)
+        self.v_pool = torch.empty(size, dtype=torch.uint8, device=device)
+        if dtype == padoc.BF16:
+            self.k_pool, self.v_pool = (x.view(torch.bfloat16).view(nb, Hkv, 16, d) for x in (self.k_pool, self.v_pool))
         self.pool = padoc.KVPool(self.k_pool, self.v_pool, nb, Hkv, d,
                                  max_seqs=len(w.pages) + w.n_branches + 8 + (nb if fragment else 0),
-                                 max_blocks_per_seq=max_bps)
+                                 max_blocks_per_seq=max_bps, dtype=dtype)
         self.pool.sync()
         if fragment:
             spacers = [self.pool.alloc(16) for _ in range(nb)]

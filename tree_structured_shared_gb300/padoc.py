@@ -17,7 +17,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libpadoc.so")
 
 OK, ERR_INVALID, ERR_OOM, ERR_CUDA, ERR_UNSUPPORTED, ERR_DEVICE_TIMEOUT = 0, -1, -2, -3, -4, -5
-F32, BF16 = 0, 1
+F32, BF16, I4 = 0, 1, 2
 PACK_CANONICAL, PACK_DOCUMENT = 0, 1
 
 EXPORTED = [
@@ -33,7 +33,9 @@ EXPORTED = [
     "padoc_draft_trie", "padoc_draft_trie_batch", "padoc_tree_attn_varlen_bwd_ws_size",
     "padoc_tree_attn_varlen_bwd", "padoc_tree_desc_bwd_plan", "padoc_kv_reserve", "padoc_kv_advance", "padoc_kv_trim",
     "padoc_sched_create", "padoc_sched_destroy", "padoc_sched_submit", "padoc_sched_schedule", "padoc_sched_update",
-    "padoc_sched_request", "padoc_sched_output",
+    "padoc_sched_request", "padoc_sched_output", "padoc_kv_storage_bytes", "padoc_kv_rows_create",
+    "padoc_kv_rows_ws_size", "padoc_kv_rows_upload", "padoc_kv_rows_free", "padoc_kv_write", "padoc_kv_gather",
+    "padoc_kv_append_rope",
 ]
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
@@ -66,6 +68,16 @@ class DecodeBatch(C.Structure):
     _fields_ = [("n_pages", C.c_int32), ("n_branches", C.c_int32), ("page_seq", C.POINTER(C.c_int32)),
                 ("branch_offsets", C.POINTER(C.c_int32)), ("branch_seq", C.POINTER(C.c_int32)),
                 ("q_offsets", C.POINTER(C.c_int32))]
+
+
+class RopeSpec(C.Structure):
+    _fields_ = [("cos_sin", C.c_void_p), ("n_pos", C.c_int32), ("rot_dim", C.c_int32), ("interleaved", C.c_int32)]
+
+
+class KVStep(C.Structure):
+    _fields_ = [("q", C.c_void_p), ("q_stride", C.c_int64), ("Hq", C.c_int32), ("q_rot", C.c_void_p),
+                ("k", C.c_void_p), ("k_stride", C.c_int64), ("v", C.c_void_p), ("v_stride", C.c_int64),
+                ("k_rot", C.c_void_p)]
 
 
 _lib = None
@@ -134,6 +146,15 @@ def lib() -> C.CDLL:
             "padoc_tree_attn_varlen_bwd": (C.c_int, [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32,
                                                      f32, vp, C.c_size_t, vp]),
             "padoc_tree_desc_bwd_plan": (C.c_int, [vp, p32, p32, p64, p64]),
+            "padoc_kv_storage_bytes": (C.c_int, [i32, i32, i32, i32, C.POINTER(C.c_size_t)]),
+            "padoc_kv_rows_create": (C.c_int, [vp, i32, p32, p32, p32, p32, C.POINTER(vp)]),
+            "padoc_kv_rows_ws_size": (C.c_int, [vp, C.POINTER(C.c_size_t)]),
+            "padoc_kv_rows_upload": (C.c_int, [vp, vp, C.c_size_t, vp]),
+            "padoc_kv_rows_free": (C.c_int, [vp]),
+            "padoc_kv_write": (C.c_int, [vp, C.POINTER(RopeSpec), C.POINTER(KVStep), vp, vp]),
+            "padoc_kv_gather": (C.c_int, [vp, vp, vp, vp, vp]),
+            "padoc_kv_append_rope": (C.c_int, [vp, i32, p32, p32, p32, C.POINTER(RopeSpec), C.POINTER(KVStep), vp,
+                                               C.c_size_t, vp]),
             "padoc_draft_index_create": (C.c_int, [p32, p64, i32, i32, C.POINTER(vp)]),
             "padoc_draft_index_free": (C.c_int, [vp]),
             "padoc_draft_trie": (C.c_int, [vp, p32, i32, i32, i32, p32, p32, p32]),
@@ -341,6 +362,16 @@ class KVPool:
         _check(lib().padoc_kv_commit(self.handle, len(seqs), _p32(a), _p32(b), _p32(c), n_src_rows, _ptr(k_new),
                                      _ptr(v_new), _ptr(ws), int(ws_bytes), _stream(stream)))
 
+    def append_rope(self, seqs: Sequence[int], row_offsets: Sequence[int], k, v, ws=None, ws_bytes: int = 0, *,
+                    positions=None, rope: Optional["Rope"] = None, stream=None, **step):
+        """padoc_kv_append_rope: reserve, write and advance; step as in KVRows.write."""
+        a, b = _i32(seqs if len(seqs) else [0]), _i32(row_offsets)
+        p = None if positions is None else _i32(positions)
+        st = _kv_step(self, k, v, **step)
+        _check(lib().padoc_kv_append_rope(self.handle, len(seqs), _p32(a), _p32(b), None if p is None else _p32(p),
+                                          None if rope is None else C.byref(rope.c), C.byref(st), _ptr(ws),
+                                          int(ws_bytes), _stream(stream)))
+
     def destroy(self):
         if self.handle:
             lib().padoc_kv_pool_destroy(self.handle)
@@ -349,6 +380,78 @@ class KVPool:
     def __del__(self):
         try:
             self.destroy()
+        except Exception:
+            pass
+
+
+def kv_storage_bytes(num_blocks: int, Hkv: int, d: int = 128, dtype: int = BF16) -> int:
+    """Bytes of a pool's K storage (and, again, of its V storage)."""
+    n = C.c_size_t()
+    _check(lib().padoc_kv_storage_bytes(num_blocks, Hkv, d, dtype, C.byref(n)))
+    return n.value
+
+
+class Rope:
+    """Rotation by position (padoc_rope): cos_sin is a device f32 table
+    [n_pos, rot_dim], cosines then sines."""
+
+    def __init__(self, cos_sin, rot_dim: int, interleaved: bool = False, n_pos: Optional[int] = None):
+        self._table = cos_sin
+        if n_pos is None:
+            n_pos = int(cos_sin.shape[0])
+        self.c = RopeSpec(_ptr(cos_sin), n_pos, rot_dim, int(bool(interleaved)))
+
+
+def _kv_step(pool: "KVPool", k, v, *, k_stride=None, v_stride=None, q=None, Hq: int = 0, q_stride=None, q_rot=None,
+             k_rot=None) -> KVStep:
+    row = pool.Hkv * pool.d
+    return KVStep(_ptr(q), Hq * pool.d if q_stride is None else int(q_stride), Hq, _ptr(q_rot),
+                  _ptr(k), row if k_stride is None else int(k_stride), _ptr(v),
+                  row if v_stride is None else int(v_stride), _ptr(k_rot))
+
+
+class KVRows:
+    """Token ranges of sequences (padoc_kv_rows): written from, or read back
+    into, packed rows in one launch."""
+
+    def __init__(self, pool: KVPool, seqs: Sequence[int], first: Optional[Sequence[int]], row_offsets: Sequence[int],
+                 positions=None):
+        a, b = _i32(seqs if len(seqs) else [0]), _i32(row_offsets)
+        f = None if first is None else _i32(first if len(first) else [0])
+        p = None if positions is None else _i32(positions)
+        h = C.c_void_p()
+        _check(lib().padoc_kv_rows_create(pool.handle, len(seqs), _p32(a), None if f is None else _p32(f), _p32(b),
+                                          None if p is None else _p32(p), C.byref(h)))
+        self.handle = h
+        self.n = int(b[-1]) if len(seqs) else 0
+        self._pool = pool
+
+    def ws_size(self) -> int:
+        n = C.c_size_t()
+        _check(lib().padoc_kv_rows_ws_size(self.handle, C.byref(n)))
+        return n.value
+
+    def upload(self, ws=None, ws_bytes: int = 0, stream=None):
+        _check(lib().padoc_kv_rows_upload(self.handle, _ptr(ws), int(ws_bytes), _stream(stream)))
+
+    def write(self, k, v, ws=None, *, rope: Optional[Rope] = None, stream=None, **step):
+        """padoc_kv_write.  Optional: q with Hq and q_rot, k_rot, and the row
+        strides k_stride, v_stride, q_stride in elements (dense by default)."""
+        st = _kv_step(self._pool, k, v, **step)
+        _check(lib().padoc_kv_write(self.handle, None if rope is None else C.byref(rope.c), C.byref(st), _ptr(ws),
+                                    _stream(stream)))
+
+    def gather(self, k, v, ws=None, stream=None):
+        _check(lib().padoc_kv_gather(self.handle, _ptr(k), _ptr(v), _ptr(ws), _stream(stream)))
+
+    def free(self):
+        if self.handle:
+            lib().padoc_kv_rows_free(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.free()
         except Exception:
             pass
 
