@@ -1400,6 +1400,7 @@ struct DecodePlan {
   std::vector<I4Unit> units;
   std::vector<I4Merge> merges;
   int32_t pre_first[4] = {0, 0, 0, 0}, own_first[4] = {0, 0, 0, 0};
+  int32_t n_tc = 0;  // prefix units of up to 128 rows: the first of all
   size_t off_units = 0, off_merges = 0;
   size_t off_pages = 0, off_items = 0, off_branches = 0, off_qplen = 0, off_qbranch = 0, off_part_o = 0, off_part_lse = 0,
          off_work = 0, total = 0;
@@ -1422,6 +1423,7 @@ int plan_i4(const padoc_kv_pool* pool, const padoc_decode_batch* b, int32_t Hq, 
             DecodePlan* pl) {
   const int32_t G = Hq / pool->Hkv, bs = pool->bs, nq = static_cast<int32_t>(pl->q_plen.size());
   auto tile_of = [](int32_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; };
+  auto on_tc = [](int32_t rows) { return rows > 16; };  // prefix units on the tcgen05 kernel
   auto blocks = [bs](int64_t n) { return (n + bs - 1) / bs; };
   // Chunks of keys: about two units for each CTA the GPU holds, within [8, 128]
   // blocks (a unit's four warps then take at least two blocks each).
@@ -1430,7 +1432,7 @@ int plan_i4(const padoc_kv_pool* pool, const padoc_decode_batch* b, int32_t Hq, 
     const int32_t b0 = b->branch_offsets[p], b1 = b->branch_offsets[p + 1];
     if (b1 == b0) continue;
     const int32_t rows = (b->q_offsets[b1] - b->q_offsets[b0]) * G, tr = tile_of(rows);
-    pre_steps += (rows + tr - 1) / tr * blocks(P[p]) * pool->Hkv;
+    if (!on_tc(rows)) pre_steps += (rows + tr - 1) / tr * blocks(P[p]) * pool->Hkv;
     for (int32_t i = b0; i < b1; ++i) {
       const Seq& s = pool->seqs[b->branch_seq[i]];
       const int32_t r = (b->q_offsets[i + 1] - b->q_offsets[i]) * G, t = tile_of(r);
@@ -1440,6 +1442,24 @@ int plan_i4(const padoc_kv_pool* pool, const padoc_decode_batch* b, int32_t Hq, 
   const int64_t slots = 8 * static_cast<int64_t>(n_sms);
   const int64_t pre_chunk = std::max<int64_t>(8, std::min<int64_t>(128, pre_steps / slots));
   const int64_t own_chunk = std::max<int64_t>(16, std::min<int64_t>(128, own_steps / slots));
+  // The tcgen05 kernel runs one unit an SM at a time, in rounds: of all chunk
+  // lengths the one whose rounds take the fewest tiles, with about two tiles'
+  // time for starting and ending a unit.
+  int64_t tc_chunk = 4, tc_best = INT64_MAX;
+  for (int64_t ct = 4; ct <= 64; ++ct) {
+    int64_t units = 0;
+    for (int32_t p = 0; p < b->n_pages; ++p) {
+      const int32_t b0 = b->branch_offsets[p], b1 = b->branch_offsets[p + 1];
+      const int32_t rows = b1 > b0 ? (b->q_offsets[b1] - b->q_offsets[b0]) * G : 0;
+      const int64_t tiles = (P[p] + kTileKeys - 1) / kTileKeys;
+      if (on_tc(rows)) units += (rows + kTileRows - 1) / kTileRows * pool->Hkv * ((tiles + ct - 1) / ct);
+    }
+    const int64_t cost = (units + n_sms - 1) / n_sms * (ct + 2);
+    if (cost < tc_best) {
+      tc_best = cost;
+      tc_chunk = ct;
+    }
+  }
   std::vector<I4Unit> pre[3], own[3];
   auto put = [](std::vector<I4Unit> (&to)[3], const I4Unit& u, int32_t tile) { to[tile == 8 ? 0 : tile == 16 ? 1 : 2].push_back(u); };
   int64_t rows = 0;
@@ -1447,18 +1467,20 @@ int plan_i4(const padoc_kv_pool* pool, const padoc_decode_batch* b, int32_t Hq, 
     const int32_t b0 = b->branch_offsets[p], b1 = b->branch_offsets[p + 1];
     if (b1 == b0) continue;
     const int32_t q0 = b->q_offsets[b0], nqp = b->q_offsets[b1] - q0;
-    const int64_t steps = blocks(P[p]);
-    const int32_t n_chunks = static_cast<int32_t>((steps + pre_chunk - 1) / pre_chunk);
-    const int64_t per = n_chunks ? (steps + n_chunks - 1) / n_chunks : 0;
+    const bool tc = on_tc(nqp * G);
+    const int64_t unit_keys = tc ? kTileKeys : bs, most = tc ? tc_chunk : pre_chunk;
+    const int64_t steps = (P[p] + unit_keys - 1) / unit_keys;
+    const int32_t n_chunks = static_cast<int32_t>((steps + most - 1) / most);
+    const int64_t per = (n_chunks ? (steps + n_chunks - 1) / n_chunks : 0) * unit_keys;  // keys
     const int64_t pre_base = rows, stride = static_cast<int64_t>(nqp) * Hq;
     int32_t made = 0;
     for (int32_t c = 0; c < n_chunks; ++c) {
-      const int64_t k0 = c * per * bs, k1 = std::min<int64_t>(P[p], (c + 1) * per * bs);
+      const int64_t k0 = c * per, k1 = std::min<int64_t>(P[p], (c + 1) * per);
       if (k1 <= k0) break;
       // blocks of the page's sequence: its own tokens start in a fresh block
       // only where its shared part ends on one (checked), so key k is in block k / bs
       ++made;
-      const int32_t tr = tile_of(nqp * G);
+      const int32_t tr = tc ? kTileRows : tile_of(nqp * G);
       for (int32_t r0 = 0; r0 < nqp * G; r0 += tr) {
         I4Unit u{};
         u.seq = b->page_seq[p];
@@ -1470,7 +1492,10 @@ int plan_i4(const padoc_kv_pool* pool, const padoc_decode_batch* b, int32_t Hq, 
         u.rows = std::min(tr, nqp * G - r0);
         u.branch = -1;
         u.part = pre_base + c * stride;
-        put(pre, u, tr);
+        if (tc)
+          pl->units.push_back(u);
+        else
+          put(pre, u, tr);
       }
     }
     rows += made * stride;
@@ -1514,6 +1539,7 @@ int plan_i4(const padoc_kv_pool* pool, const padoc_decode_batch* b, int32_t Hq, 
                                 own_base + static_cast<int64_t>(r) * Hq, own_stride});
     }
   }
+  pl->n_tc = static_cast<int32_t>(pl->units.size());
   add_units(pre, &pl->units, pl->pre_first);
   add_units(own, &pl->units, pl->own_first);
   if (static_cast<int64_t>(pl->units.size()) * pool->Hkv >= (int64_t(1) << 31) ||
@@ -1876,7 +1902,8 @@ extern "C" int padoc_decode_prefix_pass(const padoc_decode_plan* plan, const voi
   if (i4) {
     const I4Args a = i4_args(plan, q, nullptr, nullptr, nullptr, nullptr, nullptr, scale, ws);
     std::string err;
-    rc = launch_i4_units(a, plan->pl.pre_first, reinterpret_cast<cudaStream_t>(stream), &err);
+    rc = launch_i4_prefix_tc(a, 0, plan->pl.n_tc, reinterpret_cast<cudaStream_t>(stream), &err);
+    if (!rc) rc = launch_i4_units(a, plan->pl.pre_first, reinterpret_cast<cudaStream_t>(stream), &err);
     if (rc) return fail(rc, "decode_prefix_pass: %s", err.c_str());
     return PADOC_OK;
   }
@@ -2018,12 +2045,13 @@ extern "C" int padoc_depths(const int32_t* layout_len, const int32_t* content_le
 }
 
 extern "C" int padoc_device_status(padoc_stream_t stream) {
-  unsigned w = 0, wb = 0, wo = 0;
+  unsigned w = 0, wb = 0, wo = 0, wi = 0;
   int rc = read_and_clear_tc_error(reinterpret_cast<cudaStream_t>(stream), &w);
   if (!rc) rc = read_and_clear_bwd_error(reinterpret_cast<cudaStream_t>(stream), &wb);
   if (!rc) rc = read_and_clear_own_error(reinterpret_cast<cudaStream_t>(stream), &wo);
+  if (!rc) rc = read_and_clear_i4_error(reinterpret_cast<cudaStream_t>(stream), &wi);
   if (rc) return fail(rc, "device_status: could not read the device error word");
-  w |= wb | wo;
+  w |= wb | wo | wi;
   if (w) return fail(PADOC_ERR_DEVICE_TIMEOUT, "a kernel gave up a bounded wait (site mask 0x%x)", w);
   return PADOC_OK;
 }
