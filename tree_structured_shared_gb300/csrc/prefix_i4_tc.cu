@@ -3,29 +3,31 @@
 //
 // A unit is 128 query rows (the rows of every branch of a page, token R / G,
 // head R % G of the group) of one kv head against a chunk of the page's shared
-// prefix in tiles of 128 keys.  The cache's codes become fp16 operands on the
-// way to shared memory: one warpgroup decodes K, one V, each thread taking its
-// 72 bytes of a tile straight from global memory into registers a tile ahead,
-// so the codes are read once a row tile and no wider copy exists outside the
-// SM.  fp16 holds every decoded value exactly; Q's rows are scaled by a power
-// of two each (largest magnitude in [2^14, 2^15)), and the scale joins the
-// row's softmax.
+// prefix in tiles of 128 keys.  Two warpgroups turn a tile's codes into fp16
+// operand tiles in shared memory, each thread from the 72 bytes it copied there
+// itself three tiles ahead; no wider copy exists outside the SM.  fp16 holds
+// every decoded value exactly; Q's rows are scaled by a power of two each
+// (largest magnitude in [2^14, 2^15)), and the scale joins the row's softmax.
 //
-// Roles (512 threads, one persistent CTA per SM):
-//   warps 0-3   softmax: thread r owns TMEM lane r = query row r; it also lays
-//               out its row of Q, the next unit's before this unit's epilogue
-//   warps 4-7   K: thread t decodes key t of the tile (128 dims)
-//   warps 8-11  V: thread t decodes 8 keys of one group of 16 dims
-//   warp 12     MMA issuer (one thread): S = Q K^T two tiles ahead of O += P V
-//   warps 13-15 idle (they complete the warpgroup that gives its registers to
-//               the softmax)
-// TMEM: three S tiles (P in fp16 written over each) and O, 512 columns.
-// Shared memory (128-byte swizzle, two 64-column halves a tile):
-//   Q 2 x 32 KB | K 2 x 32 KB | V 2 x 32 KB | barriers
+// Roles (544 threads, one persistent CTA per SM):
+//   warps 0-3    softmax of the even tiles (numbered across all units of the
+//                CTA): thread r owns TMEM lane r = query row r; epilogue
+//   warps 4-7    softmax of the odd tiles; lays out the next unit's Q
+//   warps 8-11   K: thread t decodes key t of the tile (128 dims)
+//   warps 12-15  V: thread t decodes two slots of one group of 16 dims, four times
+//   warp 16      MMA issuer (one thread)
+// Even and odd tiles have a running maximum, a sum and an O of their own, joined
+// at the unit's end, so neither softmax waits for the other; both halves of TMEM
+// hold an S tile (P in fp16 is written over it) and an O.
+// Shared memory (operand tiles in two 64-column halves, 128-byte swizzle):
+//   Q 32 KB | K 2 x 32 KB | V 2 x 32 KB | codes 3 x 19 KB | row data | barriers
+// The decoders and the softmax walk their tiles in short loops: long straight-
+// line streams, three a scheduler, starved on instruction fetches (3300 cycles a
+// tile at 0.4 instructions a cycle).
 //
 // Softmax: P = 2^(x - m + 10) against a running maximum m that moves only when
-// exceeded by 2^4 (then O is rescaled in TMEM), so P stays in fp16's range and
-// what rounds to zero is below 2^-34 of the row's largest weight.
+// exceeded by 2^4: at most 2^14, so P stays in fp16's range, and what rounds to
+// zero is below 2^-34 of the row's largest weight.
 // Every wait is bounded; a role that gives up raises the CTA's abort flag and
 // the device error word, and all roles leave their loops.
 #include <cuda_bf16.h>
@@ -46,29 +48,37 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 544;
 constexpr int kHalf = 16384;  // one 64-column half of a 128-row tile
 constexpr int kTileBytes = 2 * kHalf;
-constexpr int kQBufs = 2, kKStages = 2, kVStages = 2, kSBufs = 3;
+constexpr int kCStages = 3;          // ring of codes
+constexpr int kCodes = 4 * 128 * 16;  // a tile's codes, K or V: [4 pieces][thread][16 bytes]
+constexpr int kKStage = kCodes + 128 * 8, kVStage = kCodes + 4 * 128 * 4;  // and its scales
 constexpr int SM_Q = 0;
-constexpr int SM_K = SM_Q + kQBufs * kTileBytes;
-constexpr int SM_V = SM_K + kKStages * kTileBytes;
-constexpr int SM_BAR = SM_V + kVStages * kTileBytes;
+constexpr int SM_K = SM_Q + kTileBytes;
+constexpr int SM_V = SM_K + 2 * kTileBytes;
+constexpr int SM_CK = SM_V + 2 * kTileBytes;
+constexpr int SM_CV = SM_CK + kCStages * kKStage;
+constexpr int SM_ROW = SM_CV + kCStages * kVStage;  // per unit parity: sl2, m and l of the odd tiles [128] f32
+constexpr int kRowBuf = 3 * 128 * 4;
+constexpr int SM_BAR = SM_ROW + 2 * kRowBuf;
 enum {
-  B_Q_FULL = 0,    // +buffer (2), count 4: the unit's Q rows are laid out
-  B_K_FULL = 2,    // +stage (2), count 4
-  B_K_EMPTY = 4,   // +stage
-  B_V_FULL = 6,    // +stage (2), count 4
-  B_V_EMPTY = 8,   // +stage: P V of the tile has run
-  B_S_FULL = 10,   // +buffer (3): S of the tile is in TMEM
-  B_P_FULL = 13,   // +buffer (3), count 4: P of the tile is in TMEM
-  B_DRAIN = 16,
-  N_BARS = 17
+  B_Q_FULL = 0,    // count 4: the unit's Q rows are laid out
+  B_ML_FULL = 1,   // count 4: the odd tiles' m and l are in shared memory
+  B_O_FREE = 2,    // count 4: the epilogue has read both O
+  B_K_FULL = 3,    // +stage (2), count 4
+  B_K_EMPTY = 5,   // +stage: S of the tile has run
+  B_V_FULL = 7,    // +stage (2), count 4
+  B_PV_DONE = 9,   // +stage: P V of the tile has run
+  B_S_FULL = 11,   // +half (2): S of the tile is in TMEM
+  B_P_FULL = 13,   // +half (2), count 4: P of the tile is in TMEM
+  B_DRAIN = 15,
+  N_BARS = 16
 };
 constexpr int SM_MISC = SM_BAR + N_BARS * 8;
 constexpr int kSmemBytes = SM_MISC + 16 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
-constexpr uint32_t kTmemO = 384;
+constexpr uint32_t kTmemO = 256;  // S / P of half h at 128 h, O at 256 + 128 h
 constexpr float kPShift = 10.f, kPSlack = 4.f;
 
 // kind::f16 with fp16 A and B and f32 accumulation; b_mn selects an MN-major B.
@@ -77,42 +87,40 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-template <int R>
-__device__ __forceinline__ void regs_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
-}
-template <int R>
-__device__ __forceinline__ void regs_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
-}
-
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ uint4 ld_cached(const void* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
+// N bytes from global to shared memory; with ok false the N bytes become zero.
+template <int N>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool ok) {
+  const uint32_t n = ok ? N : 0;
+  if (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(n), "n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
 
 __device__ __forceinline__ void raise_abort(volatile int* abort, unsigned site) {
   *abort = 1;
   atomicOr(&g_i4_err, site);
 }
 
-// Eight dims of a word as one 16-byte piece of a swizzled tile row.
-__device__ __forceinline__ void put_word(uint32_t row_addr, int piece, int sw, uint32_t w, uint32_t s2, uint32_t off) {
-  // piece 0..15: 16-byte piece of the row's 256 bytes; sw = row & 7
-  st_shared_v4(row_addr + (piece >> 3) * kHalf + (((piece & 7) ^ sw) << 4), i4_pair<0>(w, s2, off), i4_pair<1>(w, s2, off),
-               i4_pair<2>(w, s2, off), i4_pair<3>(w, s2, off));
+// The eight dims of a word of codes as one 16-byte piece of an operand tile.
+__device__ __forceinline__ void put_word(uint32_t addr, uint32_t w, uint32_t s2, uint32_t off) {
+  st_shared_v4(addr, i4_pair<0>(w, s2, off), i4_pair<1>(w, s2, off), i4_pair<2>(w, s2, off), i4_pair<3>(w, s2, off));
 }
-
-struct KRegs {
-  uint4 c[4];
-  uint2 s;
-};
-struct VRegs {
-  uint4 c[4];
-  uint2 s;
-};
 
 __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a, const int n_work) {
   extern __shared__ uint8_t smem_raw[];
@@ -126,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a, 
   if (threadIdx.x == 0) {
     for (int i = 0; i < N_BARS; ++i) {
       uint32_t cnt = 1;
-      if (i < B_K_EMPTY || (i >= B_V_FULL && i < B_V_EMPTY) || (i >= B_P_FULL && i < B_DRAIN)) cnt = 4;
+      if (i < B_K_EMPTY || (i >= B_V_FULL && i < B_PV_DONE) || (i >= B_P_FULL && i < B_DRAIN)) cnt = 4;
       mbar_init(bar(i), cnt);
     }
     *abort = 0;
@@ -144,151 +152,175 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a, 
 
   auto unit_of = [&](int w) -> const I4Unit& { return a.units[a.unit0 + w / a.Hkv]; };
 
-  if (warp >= 4 && warp < 12) {
-    // ------------------------------------------------------------ decoders of K (warps 4-7) and V (8-11)
-    regs_dec<104>();
-    const bool is_k = warp < 8;
+  if (warp >= 8 && warp < 16) {
+    // ------------------------------------------------------------ decoders of K (warps 8-11) and V (12-15)
+    const bool is_k = warp < 12;
     const int t = threadIdx.x & 127;
-    // V: thread t takes block t >> 4, group (t >> 1) & 7, slots 8 (t & 1) .. + 7
-    const int tb = t >> 4;  // block of the tile, K and V alike
-    const int vg = (t >> 1) & 7, vh = t & 1;
-    const uint8_t* pool = static_cast<const uint8_t*>(is_k ? a.k_pool : a.v_pool);
-    const int b_full = is_k ? B_K_FULL : B_V_FULL, b_empty = is_k ? B_K_EMPTY : B_V_EMPTY;
-    const uint32_t ring = sbase + (is_k ? SM_K : SM_V);
+    const int b_full = is_k ? B_K_FULL : B_V_FULL, b_empty = is_k ? B_K_EMPTY : B_PV_DONE;
+    const uint32_t stage0 = sbase + (is_k ? SM_CK : SM_CV);
+    const int stage_bytes = is_k ? kKStage : kVStage;
+    // V: piece x * 128 + t is block 2 x + (t >> 6), group (t >> 3) & 7, slots 2 (t & 7), + 1
+    const int vg = (t >> 3) & 7, sp = t & 7;
+    // the copies' own walk over the CTA's tiles, three ahead of the decoding
+    int lw = blockIdx.x, lk0 = 0, l_keys = 0;
+    const int32_t* l_ids = nullptr;
+    const uint8_t* l_pool = nullptr;
+    int32_t id[4] = {0, 0, 0, 0};  // K: block of key t; V: blocks of the four pieces
+    auto open_unit = [&]() {
+      if (lw >= n_work) return;
+      const I4Unit& un = unit_of(lw);
+      l_keys = un.n_keys;
+      l_ids = a.table + static_cast<int64_t>(un.seq) * a.max_bps + un.blk0;
+      l_pool = static_cast<const uint8_t*>(is_k ? a.k_pool : a.v_pool) + (lw % a.Hkv) * kI4Unit;
+    };
+    auto block_of = [&](int x) { return (lk0 >> 4) + (is_k ? t >> 4 : 2 * x + (t >> 6)); };
+    auto read_ids = [&]() {
+      if (lw >= n_work) return;
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        if (x == 0 || !is_k) id[x] = block_of(x) * 16 < l_keys ? __ldg(l_ids + block_of(x)) : 0;
+    };
+    auto copy_tile = [&](int cs) {
+      if (lw < n_work) {
+        const uint32_t dst = stage0 + cs * stage_bytes;
+        const int64_t stride = static_cast<int64_t>(a.Hkv) * kI4Unit;
+        if (is_k) {
+          const uint8_t* p = l_pool + id[0] * stride;
+          const bool ok = block_of(0) * 16 < l_keys;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) copy_async<16>(dst + x * 2048 + t * 16, p + x * 256 + (t & 15) * 16, ok);
+          copy_async<8>(dst + kCodes + t * 8, p + kI4Scales + (t & 15) * 8, ok);
+        } else {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const uint8_t* p = l_pool + id[x] * stride;
+            const bool ok = block_of(x) * 16 < l_keys;
+            copy_async<16>(dst + x * 2048 + t * 16, p + vg * 128 + sp * 16, ok);
+            copy_async<4>(dst + kCodes + x * 512 + t * 4, p + kI4Scales + vg * 16 + (sp >> 1) * 4, ok);
+          }
+        }
+        lk0 += kTileKeys;
+        if (lk0 >= l_keys) {
+          lk0 = 0;
+          lw += gridDim.x;
+          open_unit();
+        }
+        read_ids();
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    open_unit();
+    read_ids();
+    for (int cs = 0; cs < kCStages; ++cs) copy_tile(cs);
     uint32_t kt = 0;
+    int cs = 0;
     bool failed = false;
     for (int w = blockIdx.x; w < n_work && !failed; w += gridDim.x) {
-      const I4Unit& un = unit_of(w);
-      const int g = w % a.Hkv, n_keys = un.n_keys;
-      const int32_t* ids = a.table + static_cast<int64_t>(un.seq) * a.max_bps + un.blk0;
-      const int n_tiles = (n_keys + kTileKeys - 1) / kTileKeys, n_blocks = (n_keys + 15) >> 4;
-      // the thread's bytes of tile j; blocks past the end read as zero codes of zero scale
-      auto load = [&](int j, uint4 (&c)[4], uint2& s, int id) {
-        if (j * 8 + tb >= n_blocks || j >= n_tiles) {
-#pragma unroll
-          for (int x = 0; x < 4; ++x) c[x] = make_uint4(0, 0, 0, 0);
-          s = make_uint2(0, 0);
-          return;
+      const int n_keys = unit_of(w).n_keys;
+      for (int k0 = 0; k0 < n_keys; k0 += kTileKeys, ++kt) {
+        const int st = kt & 1;
+        asm volatile("cp.async.wait_group %0;" ::"n"(kCStages - 1) : "memory");
+        if (!__all_sync(0xffffffffu, mbar_wait(bar(b_empty + st), ((kt >> 1) & 1) ^ 1, abort))) {
+          failed = true;
+          break;
         }
-        const uint8_t* p = pool + (static_cast<int64_t>(id) * a.Hkv + g) * kI4Unit;
+        const uint32_t codes = stage0 + cs * stage_bytes;
+        const uint32_t tile = sbase + (is_k ? SM_K : SM_V) + st * kTileBytes;
         if (is_k) {
-          const int slot = t & 15;
-#pragma unroll
-          for (int x = 0; x < 4; ++x) c[x] = ld_cached(p + x * 256 + slot * 16);
-          s = __ldg(reinterpret_cast<const uint2*>(p + kI4Scales + slot * 8));
-        } else {
-#pragma unroll
-          for (int x = 0; x < 4; ++x) c[x] = ld_cached(p + vg * 128 + vh * 64 + x * 16);
-          s = __ldg(reinterpret_cast<const uint2*>(p + kI4Scales + vg * 16 + vh * 8));
-        }
-      };
-      auto id_of = [&](int j) { return j * 8 + tb < n_blocks ? __ldg(ids + j * 8 + tb) : 0; };
-      // write tile j's operands into the ring from the thread's registers
-      auto emit = [&](int j, const uint4 (&c)[4], const uint2& s) -> bool {
-        const int st = kt % 2;
-        if (!__all_sync(0xffffffffu, mbar_wait(bar(b_empty + st), ((kt >> 1) & 1) ^ 1, abort))) return false;
-        const uint32_t base = ring + st * kTileBytes;
-        if (is_k) {
-          const uint32_t row = base + t * 128;
-#pragma unroll
+          // keys past the end are zero or old bytes: their scores are masked
+          const uint32_t row = tile + t * 128;
+          const int sw = t & 7;
+#pragma unroll 1
           for (int x = 0; x < 4; ++x) {
-            const uint32_t wd[4] = {c[x].x, c[x].y, c[x].z, c[x].w};
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const uint32_t b = ((x < 2 ? s.x : s.y) >> (8 * ((2 * x + y) & 3))) & 0xffu;
-              const uint32_t s2 = i4_scale_pair(b, b), off = i4_offset(s2);
-              put_word(row, 4 * x + 2 * y, t & 7, wd[2 * y], s2, off);
-              put_word(row, 4 * x + 2 * y + 1, t & 7, wd[2 * y + 1], s2, off);
-            }
+            const uint4 c = ld_shared_v4(codes + x * 2048 + t * 16);
+            const uint32_t sc = ld_shared_u32(codes + kCodes + t * 8 + (x >> 1) * 4) >> (16 * (x & 1));
+            const uint32_t half = row + (x >> 1) * kHalf;
+            const int p0 = (x & 1) * 4;
+            uint32_t s2 = i4_scale_pair(sc & 0xffu, sc & 0xffu), off = i4_offset(s2);
+            put_word(half + (((p0 + 0) ^ sw) << 4), c.x, s2, off);
+            put_word(half + (((p0 + 1) ^ sw) << 4), c.y, s2, off);
+            s2 = i4_scale_pair((sc >> 8) & 0xffu, (sc >> 8) & 0xffu);
+            off = i4_offset(s2);
+            put_word(half + (((p0 + 2) ^ sw) << 4), c.z, s2, off);
+            put_word(half + (((p0 + 3) ^ sw) << 4), c.w, s2, off);
           }
         } else {
-          // keys past the end may hold old bytes: their rows become zero
-          const int valid = n_keys - j * kTileKeys - tb * 16 - vh * 8;  // of the thread's 8 slots
-          const int swap = vh;  // odd threads take the two slots of a load the other way round: no bank twice
-#pragma unroll
+          // the upper four pairs of slots go the other way round, so that eight
+          // neighbours write eight different banks' pieces
+          const int swap = sp >> 2;
+          const uint32_t half = tile + (vg >> 2) * kHalf;
+          const int p0 = (vg & 3) * 2;
+#pragma unroll 1
           for (int x = 0; x < 4; ++x) {
-            const uint32_t lo[2] = {swap ? c[x].z : c[x].x, swap ? c[x].w : c[x].y};
-            const uint32_t hi[2] = {swap ? c[x].x : c[x].z, swap ? c[x].y : c[x].w};
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const int slot = 2 * x + (y ^ swap);  // of the thread's 8
-              const int key = tb * 16 + vh * 8 + slot;
-              uint32_t b = ((x < 2 ? s.x : s.y) >> (8 * (slot & 3))) & 0xffu;
-              if (slot >= valid) b = 0;
-              const uint32_t s2 = i4_scale_pair(b, b), off = i4_offset(s2);
-              const uint32_t row = base + key * 128;
-              put_word(row, 2 * vg, key & 7, y ? hi[0] : lo[0], s2, off);
-              put_word(row, 2 * vg + 1, key & 7, y ? hi[1] : lo[1], s2, off);
-            }
+            const uint4 c = ld_shared_v4(codes + x * 2048 + t * 16);
+            const uint32_t sc = ld_shared_u32(codes + kCodes + x * 512 + t * 4) >> (16 * (sp & 1));
+            const int key = (2 * x + (t >> 6)) * 16 + sp * 2;
+            // keys past the end may hold old bytes and must not be NaN: a scale of zero
+            const uint32_t b0 = k0 + key < n_keys ? sc & 0xffu : 0u, b1 = k0 + key + 1 < n_keys ? (sc >> 8) & 0xffu : 0u;
+            const int ka = key + swap, kb = key + 1 - swap;
+            const uint32_t ba = swap ? b1 : b0, bb = swap ? b0 : b1;
+            uint32_t s2 = i4_scale_pair(ba, ba), off = i4_offset(s2);
+            put_word(half + ka * 128 + (((p0 + 0) ^ (ka & 7)) << 4), swap ? c.z : c.x, s2, off);
+            put_word(half + ka * 128 + (((p0 + 1) ^ (ka & 7)) << 4), swap ? c.w : c.y, s2, off);
+            s2 = i4_scale_pair(bb, bb);
+            off = i4_offset(s2);
+            put_word(half + kb * 128 + (((p0 + 0) ^ (kb & 7)) << 4), swap ? c.x : c.z, s2, off);
+            put_word(half + kb * 128 + (((p0 + 1) ^ (kb & 7)) << 4), swap ? c.y : c.w, s2, off);
           }
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(b_full + st));
-        ++kt;
-        return true;
-      };
-      // two tiles in registers: a tile's loads have two tiles' time to land
-      uint4 c0[4], c1[4];
-      uint2 s0, s1;
-      load(0, c0, s0, id_of(0));
-      load(1, c1, s1, id_of(1));
-      int id2 = id_of(2), id3 = id_of(3);
-      for (int j = 0; j < n_tiles; j += 2) {
-        if (!emit(j, c0, s0)) { failed = true; break; }
-        load(j + 2, c0, s0, id2);
-        id2 = id_of(j + 4);
-        if (j + 1 < n_tiles) {
-          if (!emit(j + 1, c1, s1)) { failed = true; break; }
-          load(j + 3, c1, s1, id3);
-          id3 = id_of(j + 5);
-        }
+        copy_tile(cs);  // the thread has read its bytes of this stage
+        if (++cs == kCStages) cs = 0;
       }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     if (failed && lane == 0) raise_abort(abort, is_k ? 0x10000 : 0x20000);
-  } else if (warp >= 12) {
+  } else if (warp == 16) {
     // ------------------------------------------------------------ MMA issuer
-    regs_dec<56>();
-    if (warp == 12 && lane == 0) {
+    if (lane == 0) {
       constexpr uint32_t id_qk = idesc_f16(128, 128, false), id_pv = idesc_f16(128, 128, true);
       uint32_t ks = 0, kp = 0;  // tiles whose S / P V are issued
       int iu = 0;
       bool failed = false;
+      const uint64_t d_q = sdesc_sw128(sbase + SM_Q, 16, 1024);
+      // S of the next tile.  Its half of TMEM last held P of the tile two back,
+      // whose P V this thread has issued before (tcgen05.mma runs in issue order).
+      auto issue_s = [&]() -> bool {
+        const int st = ks & 1;
+        if (!mbar_wait_relaxed(bar(B_K_FULL + st), (ks >> 1) & 1, abort)) return false;
+        tc_fence_after();
+        const uint64_t d_k = sdesc_sw128(sbase + SM_K + st * kTileBytes, 16, 1024);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint64_t off = static_cast<uint64_t>(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4);
+          mma_bf16_ss(tmem + st * 128, d_q + off, d_k + off, id_qk, kk > 0);
+        }
+        mma_commit(bar(B_S_FULL + st));
+        mma_commit(bar(B_K_EMPTY + st));
+        ++ks;
+        return true;
+      };
       for (int w = blockIdx.x; w < n_work && !failed; w += gridDim.x, ++iu) {
         const int n = (unit_of(w).n_keys + kTileKeys - 1) / kTileKeys;
-        if (!mbar_wait_relaxed(bar(B_Q_FULL + (iu & 1)), (iu >> 1) & 1, abort)) { failed = true; break; }
-        const uint64_t d_q = sdesc_sw128(sbase + SM_Q + (iu & 1) * kTileBytes, 16, 1024);
-        auto issue_s = [&]() -> bool {
-          const int st = ks % 2, sb = ks % kSBufs;
-          if (!mbar_wait_relaxed(bar(B_K_FULL + st), (ks >> 1) & 1, abort)) return false;
-          tc_fence_after();
-          const uint64_t d_k = sdesc_sw128(sbase + SM_K + st * kTileBytes, 16, 1024);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint64_t off = static_cast<uint64_t>(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4);
-            mma_bf16_ss(tmem + sb * 128, d_q + off, d_k + off, id_qk, kk > 0);
-          }
-          mma_commit(bar(B_S_FULL + sb));
-          mma_commit(bar(B_K_EMPTY + st));
-          ++ks;
-          return true;
-        };
+        if (!mbar_wait_relaxed(bar(B_Q_FULL), iu & 1, abort)) { failed = true; break; }
         if (!issue_s() || (n > 1 && !issue_s())) { failed = true; break; }
-        for (int j = 0; j < n; ++j) {
-          const int pb = kp % kSBufs, st = kp % 2;
-          if (!mbar_wait_relaxed(bar(B_P_FULL + pb), (kp / kSBufs) & 1, abort)) { failed = true; break; }
-          tc_fence_after();
-          // the S buffer of tile j + 2 last held P of tile j - 1, whose P V was issued before
-          if (j + 2 < n && !issue_s()) { failed = true; break; }
-          if (!mbar_wait_relaxed(bar(B_V_FULL + st), (kp >> 1) & 1, abort)) { failed = true; break; }
+        for (int j = 0; j < n; ++j, ++kp) {
+          const int st = kp & 1;
+          if (!mbar_wait_relaxed(bar(B_V_FULL + st), (kp >> 1) & 1, abort) ||
+              !mbar_wait_relaxed(bar(B_P_FULL + st), (kp >> 1) & 1, abort)) {
+            failed = true;
+            break;
+          }
           tc_fence_after();
           const uint64_t d_v = sdesc_sw128(sbase + SM_V + st * kTileBytes, kHalf, 1024);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            mma_bf16_ts(tmem + kTmemO, tmem + pb * 128 + kk * 8, d_v + static_cast<uint64_t>(kk * (2048 >> 4)), id_pv,
-                        (j > 0 || kk > 0) ? 1u : 0u);
-          mma_commit(bar(B_V_EMPTY + st));
-          ++kp;
+            mma_bf16_ts(tmem + kTmemO + st * 128, tmem + st * 128 + kk * 8, d_v + static_cast<uint64_t>(kk * (2048 >> 4)), id_pv,
+                        (j > 1 || kk > 0) ? 1u : 0u);
+          mma_commit(bar(B_PV_DONE + st));
+          if (j + 2 < n && !issue_s()) { failed = true; break; }
         }
       }
       if (failed) raise_abort(abort, 0x40000);
@@ -297,189 +329,229 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a, 
       int never = 0;
       mbar_wait(bar(B_DRAIN), 0, &never);
     }
-  } else {
-    // ------------------------------------------------------------ softmax (warps 0-3)
-    regs_inc<232>();
-    const int r = threadIdx.x;
-    const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
-    uint32_t kt = 0;
+  } else if (warp < 8) {
+    // ------------------------------------------------------------ softmax
+    const int odd = warp >> 2;  // this warpgroup's tiles, its half of TMEM
+    const int r = threadIdx.x & 127, wq = warp & 3;
+    const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
+    const uint32_t t_s = tmem + lane_base + odd * 128, t_o = tmem + kTmemO + lane_base;
+    uint32_t kt0 = 0;  // number of the unit's first tile
     bool failed = false;
-    // lays out row r of a unit's Q in buffer qb; returns the row's softmax factor
-    auto lay_q = [&](int w, int qb) -> float {
+    auto row_buf = [&](int iu) { return reinterpret_cast<float*>(smem + SM_ROW + (iu & 1) * kRowBuf); };
+    // odd tiles' threads: row r of a unit's Q into shared memory, and its softmax factor
+    auto lay_q = [&](int w, int iu) {
       const I4Unit& un = unit_of(w);
       const int g = w % a.Hkv, R = un.row0 + r;
       float sl2 = a.sl2;
       if (r < un.rows) {
         const uint4* src = reinterpret_cast<const uint4*>(
             a.q + (static_cast<int64_t>(un.q_first + R / G) * a.Hq + g * G + R % G) * kHeadDim);
-        uint4 v[16];
-#pragma unroll
-        for (int x = 0; x < 16; ++x) v[x] = src[x];
+        // twice over the row (the second time from L1), a few registers at a time
         float amax = 0.f;
         auto most = [&](uint32_t u) {
           const float lo = fabsf(__uint_as_float(u << 16)), hi = fabsf(__uint_as_float(u & 0xffff0000u));
           amax = fmaxf(amax, lo <= 3.4028235e38f ? lo : 0.f);
           amax = fmaxf(amax, hi <= 3.4028235e38f ? hi : 0.f);
         };
-#pragma unroll
+#pragma unroll 8
         for (int x = 0; x < 16; ++x) {
-          most(v[x].x);
-          most(v[x].y);
-          most(v[x].z);
-          most(v[x].w);
+          const uint4 v = __ldg(src + x);
+          most(v.x);
+          most(v.y);
+          most(v.z);
+          most(v.w);
         }
         const int kexp = amax > 0.f ? min(100, 14 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127)) : 0;
         const float qf = __uint_as_float(static_cast<uint32_t>(127 + kexp) << 23);
         sl2 = a.sl2 * __uint_as_float(static_cast<uint32_t>(127 - kexp) << 23);
         auto h = [&](uint32_t u) { return pack_f16x2(__uint_as_float(u << 16) * qf, __uint_as_float(u & 0xffff0000u) * qf); };
-        const uint32_t row = sbase + SM_Q + qb * kTileBytes + r * 128;
-#pragma unroll
-        for (int x = 0; x < 16; ++x)
-          st_shared_v4(row + (x >> 3) * kHalf + (((x & 7) ^ (r & 7)) << 4), h(v[x].x), h(v[x].y), h(v[x].z), h(v[x].w));
+        const uint32_t row = sbase + SM_Q + r * 128;
+#pragma unroll 4
+        for (int x = 0; x < 16; ++x) {
+          const uint4 v = __ldg(src + x);
+          st_shared_v4(row + (x >> 3) * kHalf + (((x & 7) ^ (r & 7)) << 4), h(v.x), h(v.y), h(v.z), h(v.w));
+        }
       }
       // rows past the unit's keep what the buffer held: their results are not read
+      row_buf(iu)[r] = sl2;
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(B_Q_FULL + qb));
-      return sl2;
+      if (lane == 0) mbar_arrive(bar(B_Q_FULL));
     };
-    float sl2_next = blockIdx.x < n_work ? lay_q(blockIdx.x, 0) : 0.f;
+    if (odd && blockIdx.x < n_work) lay_q(blockIdx.x, 0);
     int iu = 0;
     for (int w = blockIdx.x; w < n_work && !failed; w += gridDim.x, ++iu) {
-      const I4Unit un = unit_of(w);
-      const int g = w % a.Hkv;
-      const int n = (un.n_keys + kTileKeys - 1) / kTileKeys;
-      const float sl2 = sl2_next;
-      const bool valid = r < un.rows, warp_valid = warp * 32 < un.rows;
+      const I4Unit& un = unit_of(w);
+      const int rows = un.rows, n_keys = un.n_keys;
+      const int n = (n_keys + kTileKeys - 1) / kTileKeys;
+      const bool valid = r < rows, warp_valid = wq * 32 < rows;
       const int R = un.row0 + r;
-      const int limit = valid ? min(un.n_keys, a.q_plen[un.q_first + R / G] - un.key0) : un.n_keys;
+      const int limit = valid ? min(n_keys, a.q_plen[un.q_first + R / G] - un.key0) : n_keys;
+      if (!__all_sync(0xffffffffu, mbar_wait(bar(B_Q_FULL), iu & 1, abort))) {
+        failed = true;
+        break;
+      }
+      const float sl2 = row_buf(iu)[r];
+      const int j0 = (kt0 & 1) == odd ? 0 : 1;  // the unit's first tile of this parity
       float m_run = -INFINITY, l_run = 0.f;
-      for (int j = 0; j < n; ++j, ++kt) {
-        const int sb = kt % kSBufs;
-        if (!__all_sync(0xffffffffu, mbar_wait_relaxed(bar(B_S_FULL + sb), (kt / kSBufs) & 1, abort))) {
+      for (int j = j0; j < n; j += 2) {
+        const uint32_t kt = kt0 + j;
+        if (!__all_sync(0xffffffffu, mbar_wait_relaxed(bar(B_S_FULL + odd), (kt >> 1) & 1, abort))) {
           failed = true;
           break;
         }
         tc_fence_after();
         if (warp_valid) {
-          float s[128];
-          {
-            uint32_t v0[32], v1[32], v2[32], v3[32];
-            tmem_ld32(tmem + lane_base + sb * 128 + 0, v0);
-            tmem_ld32(tmem + lane_base + sb * 128 + 32, v1);
-            tmem_ld32(tmem + lane_base + sb * 128 + 64, v2);
-            tmem_ld32(tmem + lane_base + sb * 128 + 96, v3);
-            tmem_wait_ld();
+          const int vis = limit - j * kTileKeys;  // keys [0, vis) of the tile are visible
+          auto mask32 = [&](int c, uint32_t (&v)[32]) {
+            const int left = vis - c * 32;
+            if (left < 32) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              s[i] = __uint_as_float(v0[i]);
-              s[32 + i] = __uint_as_float(v1[i]);
-              s[64 + i] = __uint_as_float(v2[i]);
-              s[96 + i] = __uint_as_float(v3[i]);
+              for (int i = 0; i < 32; ++i)
+                if (i >= left) v[i] = 0xff800000u;
             }
+          };
+          float mx = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < 4; c += 2) {
+            uint32_t v0[32], v1[32];
+            tmem_ld32(t_s + c * 32, v0);
+            tmem_ld32(t_s + c * 32 + 32, v1);
+            tmem_wait_ld();
+            mask32(c, v0);
+            mask32(c + 1, v1);
+            float m4[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) m4[k] = max3f(m4[k], __uint_as_float(v0[i + k]), __uint_as_float(v1[i + k]));
+            mx = fmaxf(max3f(m4[0], m4[1], m4[2]), m4[3]);
           }
-          const int vis = limit - j * kTileKeys;
-          if (vis < kTileKeys) {
-#pragma unroll
-            for (int c = 0; c < 128; ++c)
-              if (c >= vis) s[c] = -INFINITY;
-          }
-          float m8[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) m8[i] = s[i];
-#pragma unroll
-          for (int c = 8; c < 120; c += 16)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) m8[i] = max3f(m8[i], s[c + i], s[c + 8 + i]);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) m8[i] = fmaxf(m8[i], s[120 + i]);
-          const float tmax = max3f(max3f(m8[0], m8[1], m8[2]), max3f(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
-          const float mt = tmax * sl2;
+          const float mt = mx * sl2;
           const bool grow = mt > m_run + kPSlack;
           const float alpha = grow ? fast_exp2(m_run - mt) : 1.f;  // 0 while m_run is -inf
           if (grow) {
             l_run *= alpha;
             m_run = mt;
           }
-          const float m_use = (m_run == -INFINITY ? 0.f : m_run) - kPShift;
-          {
-            const uint64_t sl2x2 = f2pack(sl2, sl2), negm = f2pack(-m_use, -m_use);
-            uint64_t l2[4] = {0, 0, 0, 0};
-#pragma unroll
-            for (int c = 0; c < 128; c += 2) {
-              float x0, x1;
-              f2unpack(fma2(f2pack(s[c], s[c + 1]), sl2x2, negm), x0, x1);
-              s[c] = fast_exp2(x0);
-              s[c + 1] = fast_exp2(x1);
-              l2[(c >> 1) & 3] = add2(l2[(c >> 1) & 3], f2pack(s[c], s[c + 1]));
-            }
-            float l8[8];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) f2unpack(l2[k], l8[2 * k], l8[2 * k + 1]);
-            l_run += ((l8[0] + l8[1]) + (l8[2] + l8[3])) + ((l8[4] + l8[5]) + (l8[6] + l8[7]));
-          }
-          if (j > 0 && __any_sync(0xffffffffu, grow)) {
+          if (j > j0 && __any_sync(0xffffffffu, grow)) {
             // O holds sums against the old maximum: rescale once P V of the previous tile has run
-            const uint32_t q = kt - 1;
-            if (!__all_sync(0xffffffffu, mbar_wait_relaxed(bar(B_V_EMPTY + (q & 1)), (q >> 1) & 1, abort))) {
+            if (!__all_sync(0xffffffffu, mbar_wait_relaxed(bar(B_PV_DONE + odd), ((kt - 2) >> 1) & 1, abort))) {
               failed = true;
               break;
             }
             tc_fence_after();
-            uint32_t v[32];
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < 4; ++c) {
-              tmem_ld32(tmem + kTmemO + lane_base + c * 32, v);
+              uint32_t v[32];
+              tmem_ld32(t_o + odd * 128 + c * 32, v);
               tmem_wait_ld();
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
-              tmem_st32(tmem + kTmemO + lane_base + c * 32, v);
+              tmem_st32(t_o + odd * 128 + c * 32, v);
             }
             tmem_wait_st();
           }
-          uint32_t pk[64];
+          const float m_use = (m_run == -INFINITY ? 0.f : m_run) - kPShift;
+          const uint64_t sl2x2 = f2pack(sl2, sl2), negm = f2pack(-m_use, -m_use);
+          uint64_t l2[2] = {0, 0};
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t v[32], pk[16];
+            tmem_ld32(t_s + c * 32, v);
+            tmem_wait_ld();
+            mask32(c, v);
 #pragma unroll
-          for (int c = 0; c < 64; ++c) pk[c] = pack_f16x2(s[2 * c], s[2 * c + 1]);
-          tmem_st64(tmem + lane_base + sb * 128, pk);
+            for (int i = 0; i < 32; i += 2) {
+              float x0, x1;
+              f2unpack(fma2(f2pack(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), sl2x2, negm), x0, x1);
+              x0 = fast_exp2(x0);
+              x1 = fast_exp2(x1);
+              l2[(i >> 1) & 1] = add2(l2[(i >> 1) & 1], f2pack(x0, x1));
+              pk[i >> 1] = pack_f16x2(x0, x1);
+            }
+            // over columns of S that this loop has read
+            tmem_st16(t_s + c * 16, pk);
+          }
+          float l4[4];
+          f2unpack(l2[0], l4[0], l4[1]);
+          f2unpack(l2[1], l4[2], l4[3]);
+          l_run += (l4[0] + l4[1]) + (l4[2] + l4[3]);
           tmem_wait_st();
+        }
+        if (odd && j == j0 && iu > 0 &&
+            !__all_sync(0xffffffffu, mbar_wait(bar(B_O_FREE), (iu - 1) & 1, abort))) {
+          failed = true;  // P V may overwrite the odd tiles' O once the last epilogue has read it
+          break;
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B_P_FULL + sb));
+        if (lane == 0) mbar_arrive(bar(B_P_FULL + odd));
       }
       if (failed) break;
-      // the next unit's Q goes out first, so its S runs while O is read here
-      if (w + static_cast<int>(gridDim.x) < n_work) sl2_next = lay_q(w + gridDim.x, (iu + 1) & 1);
-      const uint32_t q = kt - 1;
-      if (!__all_sync(0xffffffffu, mbar_wait_relaxed(bar(B_V_EMPTY + (q & 1)), (q >> 1) & 1, abort))) {
+      // the unit's last tile, and the last of the other parity (if it has one)
+      const uint32_t last = kt0 + n - 1;
+      kt0 += n;
+      if (odd) {
+        row_buf(iu)[128 + r] = m_run;
+        row_buf(iu)[256 + r] = l_run;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_ML_FULL));
+        if (w + static_cast<int>(gridDim.x) < n_work) {
+          // Q is free once every S of this unit has run; the even tiles' last one
+          // is waited for here (its barrier cannot move on before the next Q is out)
+          const uint32_t k = (last & 1) ? last - 1 : last;
+          if ((n > 1 || !(last & 1)) &&
+              !__all_sync(0xffffffffu, mbar_wait_relaxed(bar(B_S_FULL), (k >> 1) & 1, abort))) {
+            failed = true;
+            break;
+          }
+          lay_q(w + gridDim.x, iu + 1);
+        }
+        continue;
+      }
+      const uint32_t ke = (last & 1) ? last - 1 : last, ko = (last & 1) ? last : last - 1;  // last even, last odd tile
+      const bool has_e = n > 1 || !(last & 1), has_o = n > 1 || (last & 1);
+      if ((has_e && !__all_sync(0xffffffffu, mbar_wait_relaxed(bar(B_PV_DONE), (ke >> 1) & 1, abort))) ||
+          (has_o && !__all_sync(0xffffffffu, mbar_wait_relaxed(bar(B_PV_DONE + 1), (ko >> 1) & 1, abort))) ||
+          !__all_sync(0xffffffffu, mbar_wait(bar(B_ML_FULL), iu & 1, abort))) {
         failed = true;
         break;
       }
       tc_fence_after();
       if (warp_valid) {
-        const bool any = !(l_run == 0.f);
-        const float inv = any ? 1.f / l_run : 0.f;
-        const int64_t row = un.part + static_cast<int64_t>(R / G) * a.Hq + g * G + R % G;
+        const float m_o = row_buf(iu)[128 + r], l_o = row_buf(iu)[256 + r];
+        const bool any_e = !(l_run == 0.f), any_o = !(l_o == 0.f);  // NaN counts
+        const float M = fmaxf(any_e ? m_run : -INFINITY, any_o ? m_o : -INFINITY);
+        const float we = any_e ? fast_exp2(m_run - M) : 0.f, wo = any_o ? fast_exp2(m_o - M) : 0.f;
+        const float L = (any_e ? l_run * we : 0.f) + (any_o ? l_o * wo : 0.f);
+        const float fe = any_e ? we / L : 0.f, fo = any_o ? wo / L : 0.f;
+        const int64_t row = un.part + static_cast<int64_t>(R / G) * a.Hq + (w % a.Hkv) * G + R % G;
         float* dst = a.part_o + row * kHeadDim;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < 4; ++c) {
-          uint32_t v[32];
-          tmem_ld32(tmem + kTmemO + lane_base + c * 32, v);
+          uint32_t ve[32], vo[32];
+          tmem_ld32(t_o + c * 32, ve);
+          tmem_ld32(t_o + 128 + c * 32, vo);
           tmem_wait_ld();
           if (valid) {
+            // an O that no tile of this unit wrote holds old values: its factor is 0 and it is left out
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
               uint32_t x[8];
 #pragma unroll
-              for (int i = 0; i < 8; ++i) x[i] = __float_as_uint(__uint_as_float(v[8 * h + i]) * inv);
+              for (int i = 0; i < 8; ++i)
+                x[i] = __float_as_uint((any_e ? __uint_as_float(ve[8 * h + i]) * fe : 0.f) +
+                                       (any_o ? __uint_as_float(vo[8 * h + i]) * fo : 0.f));
               st_global_v8(dst + c * 32 + h * 8, x);
             }
           }
         }
-        if (valid) a.part_lse[row] = any ? m_run - kPShift + __log2f(l_run) : -INFINITY;
+        if (valid) a.part_lse[row] = any_e || any_o ? M - kPShift + __log2f(L) : -INFINITY;
       }
-      // O is read: this warp's next P_FULL arrival (after its
-      // tcgen05.fence::before_thread_sync) lets P V overwrite it
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_O_FREE));
     }
     if (failed && lane == 0) raise_abort(abort, 0x80000);
   }
