@@ -4,9 +4,10 @@
 // the group, row R = token R / G, head R % G) and a run of cached keys: a chunk
 // of a page's shared prefix with the rows of all its branches (each prefix
 // token is read from HBM once a page), or a branch's own suffix with its own
-// rows and query block.  Four warps share a unit: each takes every fourth
-// 16-token block with a running softmax of its own, and the partial results
-// meet in shared memory.
+// rows and query block.  W warps share a unit and are a CTA: each takes every
+// W-th 16-token block with a running softmax of its own, and their results meet
+// in shared memory as register images (a warp's n-tile against the others').
+// One warp a unit costs least when there are units enough to fill the GPU.
 //
 // Keys go on the matrix instruction's M side, so one query token (G <= 8 rows)
 // fills its N side and a key costs one instruction of each product a row tile:
@@ -41,10 +42,7 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
 constexpr float kLn2 = 0.69314718055994530942f;
-constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kPShift = 10.f;  // log2 of P's weight at the running maximum
 constexpr float kPSlack = 4.f;   // how far (log2) a score may exceed it
 constexpr float kNoMax = -3.0e38f;  // reference of a row that has seen no key: any score exceeds it
@@ -100,57 +98,74 @@ __device__ __forceinline__ BlockRegs load_block(const uint8_t* kp, const uint8_t
   return b;
 }
 
-template <int NT>
+// What the warps of a unit exchange: per warp and row tile the lane's 32 sums of O
+// (8 float4) and, of its two rows, the reference and the sum.
+template <int NT, int W>
 struct Smem {
-  float o[kWarps][8 * NT][kHeadDim];
-  float m[kWarps][8 * NT], l[kWarps][8 * NT];
+  float4 o[W][NT][8][32];
+  float4 ml[W][NT][32];
+  uint4 q[NT > 2 ? NT : 1][4][32];  // Q fragments of large units
+};
+template <int NT>
+struct Smem<NT, 1> {
+  uint4 q[NT][4][32];
 };
 
-template <int NT>
-__global__ void __launch_bounds__(kThreads) decode_i4_kernel(const I4Args a) {
+template <int NT, int W>
+__global__ void __launch_bounds__(32 * W) decode_i4_kernel(const I4Args a) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  Smem<NT>& sm = *reinterpret_cast<Smem<NT>*>(smem_raw);
+  Smem<NT, W>& sm = *reinterpret_cast<Smem<NT, W>*>(smem_raw);
+  constexpr bool kQInSmem = NT > 2;
   const int u = a.unit0 + blockIdx.x / a.Hkv, g = blockIdx.x % a.Hkv;
-  const I4Unit un = a.units[u];
+  const I4Unit& un = a.units[u];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int i = lane >> 2, c = lane & 3;
   const int G = a.group;
   const int key_a = 4 * (i >> 1) + (i & 1);
   const int32_t* ids = a.table + static_cast<int64_t>(un.seq) * a.max_bps + un.blk0;
   const int n_keys = un.n_keys, n_steps = (n_keys + 15) >> 4;
+  const int rows = un.rows, row0 = un.row0, q_first = un.q_first, branch = un.branch;
 
-  // the first block's bytes are on their way while Q is laid out
-  auto block_ptr = [&](const void* pool, int step) {
-    return static_cast<const uint8_t*>(pool) + (static_cast<int64_t>(ids[step]) * a.Hkv + g) * kI4Unit;
+  // lane l holds the block of the warp's step l of the current 32
+  int32_t id_reg = warp + W * lane < n_steps ? ids[warp + W * lane] : 0;
+  auto load_step = [&](int k) {  // the warp's k-th step
+    const int32_t id = __shfl_sync(0xffffffffu, id_reg, k & 31);
+    const int64_t at = (static_cast<int64_t>(id) * a.Hkv + g) * kI4Unit;
+    return load_block(static_cast<const uint8_t*>(a.k_pool) + at, static_cast<const uint8_t*>(a.v_pool) + at, key_a, i, c);
   };
+  // the first block's bytes are on their way while Q is laid out
   BlockRegs nx{};
-  if (warp < n_steps) nx = load_block(block_ptr(a.k_pool, warp), block_ptr(a.v_pool, warp), key_a, i, c);
+  if (warp < n_steps) nx = load_step(0);
 
   // Q^T fragments: row nt * 8 + i, dims 32 c .. 32 c + 31
-  auto q_row = [&](int nt) -> const __nv_bfloat16* {
-    const int R = un.row0 + nt * 8 + i;
-    return nt * 8 + i < un.rows
-               ? a.q + (static_cast<int64_t>(un.q_first + R / G) * a.Hq + g * G + R % G) * kHeadDim + 32 * c
-               : nullptr;
+  auto q_row = [&](int nt) -> const uint4* {
+    const int R = row0 + nt * 8 + i;
+    return reinterpret_cast<const uint4*>(
+        nt * 8 + i < rows ? a.q + (static_cast<int64_t>(q_first + R / G) * a.Hq + g * G + R % G) * kHeadDim + 32 * c : nullptr);
   };
-  uint32_t q[NT][16];
+  uint32_t q[kQInSmem ? 1 : NT][16];
   float amax = 0.f;
+  auto most = [&](uint32_t v) {
+    const float lo = fabsf(__uint_as_float(v << 16)), hi = fabsf(__uint_as_float(v & 0xffff0000u));
+    amax = fmaxf(amax, lo <= 3.4028235e38f ? lo : 0.f);
+    amax = fmaxf(amax, hi <= 3.4028235e38f ? hi : 0.f);
+  };
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const __nv_bfloat16* p = q_row(nt);
+    const uint4* p = q_row(nt);
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      const uint4 v = p ? reinterpret_cast<const uint4*>(p)[x] : make_uint4(0, 0, 0, 0);
-      q[nt][4 * x] = v.x;
-      q[nt][4 * x + 1] = v.y;
-      q[nt][4 * x + 2] = v.z;
-      q[nt][4 * x + 3] = v.w;
-    }
-#pragma unroll
-    for (int x = 0; x < 16; ++x) {
-      const float lo = fabsf(__uint_as_float(q[nt][x] << 16)), hi = fabsf(__uint_as_float(q[nt][x] & 0xffff0000u));
-      amax = fmaxf(amax, lo <= 3.4028235e38f ? lo : 0.f);
-      amax = fmaxf(amax, hi <= 3.4028235e38f ? hi : 0.f);
+      const uint4 v = p ? p[x] : make_uint4(0, 0, 0, 0);
+      most(v.x);
+      most(v.y);
+      most(v.z);
+      most(v.w);
+      if (!kQInSmem) {
+        q[nt][4 * x] = v.x;
+        q[nt][4 * x + 1] = v.y;
+        q[nt][4 * x + 2] = v.z;
+        q[nt][4 * x + 3] = v.w;
+      }
     }
   }
 #pragma unroll
@@ -158,37 +173,49 @@ __global__ void __launch_bounds__(kThreads) decode_i4_kernel(const I4Args a) {
   const int kexp = amax > 0.f ? min(100, 14 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127)) : 0;
   const float qf = __uint_as_float(static_cast<uint32_t>(127 + kexp) << 23);
   const float sl2q = a.sl2 * __uint_as_float(static_cast<uint32_t>(127 - kexp) << 23);
+  auto half2 = [&](uint32_t v) { return pack_f16x2(__uint_as_float(v << 16) * qf, __uint_as_float(v & 0xffff0000u) * qf); };
+  if constexpr (kQInSmem) {
+#pragma unroll 1
+    for (int nt = warp; nt < NT; nt += W) {
+      const uint4* p = q_row(nt);
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+      for (int x = 0; x < 4; ++x) {
+        const uint4 v = p ? p[x] : make_uint4(0, 0, 0, 0);
+        sm.q[nt][x][lane] = make_uint4(half2(v.x), half2(v.y), half2(v.z), half2(v.w));
+      }
+    }
+    __syncthreads();
+  } else {
 #pragma unroll
-    for (int x = 0; x < 16; ++x)
-      q[nt][x] = pack_f16x2(__uint_as_float(q[nt][x] << 16) * qf, __uint_as_float(q[nt][x] & 0xffff0000u) * qf);
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int x = 0; x < 16; ++x) q[nt][x] = half2(q[nt][x]);
+  }
 
-  // rows 2c, 2c + 1 of each tile: keys they may see, running reference (log2, less kPShift), sums
-  int lim[NT][2];
+  // rows 2c, 2c + 1 of each tile: running reference (log2, less kPShift), sums
   float mo[NT][2], l[NT][2];
   float o[NT][8][4];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+  for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int r = nt * 8 + 2 * c + e;
-      lim[nt][e] = n_keys;
-      if (un.branch < 0 && r < un.rows)
-        lim[nt][e] = min(n_keys, a.q_plen[un.q_first + (un.row0 + r) / G] - un.key0);
       mo[nt][e] = kNoMax;
       l[nt][e] = 0.f;
     }
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
     for (int x = 0; x < 8; ++x)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[nt][x][e] = 0.f;
+  }
+  // keys a row of a page's prefix may see; a branch's own keys are seen by all its rows
+  auto limit_of = [&](int r) {
+    return branch < 0 && r < rows ? min(n_keys, a.q_plen[q_first + (row0 + r) / G] - un.key0) : n_keys;
+  };
   int lim_min = n_keys;
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) lim_min = min(lim_min, min(lim[nt][0], lim[nt][1]));
-  lim_min = __reduce_min_sync(0xffffffffu, lim_min);
+  if (branch < 0) {
+    if (lane < 8 * NT) lim_min = limit_of(lane);
+    lim_min = __reduce_min_sync(0xffffffffu, lim_min);
+  }
 
   // P of one tile of scores (log2 units) against the running references, which
   // move first where a score exceeds them by more than kPSlack
@@ -229,10 +256,16 @@ __global__ void __launch_bounds__(kThreads) decode_i4_kernel(const I4Args a) {
       }
   };
 
-  for (int step = warp; step < n_steps; step += kWarps) {
+#pragma unroll 1
+  for (int step = warp, k = 0; step < n_steps; step += W, ++k) {
     const BlockRegs b = nx;
-    if (step + kWarps < n_steps)
-      nx = load_block(block_ptr(a.k_pool, step + kWarps), block_ptr(a.v_pool, step + kWarps), key_a, i, c);
+    if (step + W < n_steps) {
+      if (((k + 1) & 31) == 0) {
+        const int at = step + W + W * lane;
+        id_reg = at < n_steps ? ids[at] : 0;
+      }
+      nx = load_step(k + 1);
+    }
     float s[NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -252,22 +285,31 @@ __global__ void __launch_bounds__(kThreads) decode_i4_kernel(const I4Args a) {
                                 i4_pair<3>(wb[w], sb, fb)};
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          mma_f16(s[nt], f0, q[nt][4 * w], q[nt][4 * w + 1]);
-          mma_f16(s[nt], f1, q[nt][4 * w + 2], q[nt][4 * w + 3]);
+          if constexpr (kQInSmem) {
+            const uint4 qv = sm.q[nt][w][lane];
+            mma_f16(s[nt], f0, qv.x, qv.y);
+            mma_f16(s[nt], f1, qv.z, qv.w);
+          } else {
+            mma_f16(s[nt], f0, q[nt][4 * w], q[nt][4 * w + 1]);
+            mma_f16(s[nt], f1, q[nt][4 * w + 2], q[nt][4 * w + 3]);
+          }
         }
       }
     }
-    const int key0 = step * 16 + key_a;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[nt][e] *= sl2q;
     if (step * 16 + 16 > lim_min) {
+      const int key0 = step * 16 + key_a;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (key0 + (e >> 1) * 2 >= lim[nt][e & 1]) s[nt][e] = -INFINITY;
+        for (int e = 0; e < 2; ++e) {
+          const int lim = limit_of(nt * 8 + 2 * c + e);
+          if (key0 >= lim) s[nt][e] = -INFINITY;
+          if (key0 + 2 >= lim) s[nt][2 + e] = -INFINITY;
+        }
     }
     softmax(s);
     uint32_t p[NT][2];
@@ -299,29 +341,32 @@ __global__ void __launch_bounds__(kThreads) decode_i4_kernel(const I4Args a) {
   }
 
   // ---------------------------------------------------------------- query block
-  // scores of all 16 keys by every warp; warp w then takes the keys j % 4 == w
-  if (un.branch >= 0 && un.q_len > 0) {
+  // scores of all 16 keys by every warp; warp w then takes the keys j % W == w
+  const int q_len = un.q_len;
+  if (q_len > 0) {
     float s[NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
     const int64_t krow = static_cast<int64_t>(a.Hkv) * kHeadDim;
-    const __nv_bfloat16* kn = a.k_new + un.qb_first * krow + g * kHeadDim + 32 * c;
+    const int64_t at = un.qb_first * krow + g * kHeadDim;
+    const __nv_bfloat16* kn = a.k_new + at + 32 * c;
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
       const uint4 z = make_uint4(0, 0, 0, 0);
-      const uint4 va = key_a < un.q_len ? *reinterpret_cast<const uint4*>(kn + key_a * krow + 8 * x) : z;
-      const uint4 vb = key_a + 2 < un.q_len ? *reinterpret_cast<const uint4*>(kn + (key_a + 2) * krow + 8 * x) : z;
+      const uint4 va = key_a < q_len ? *reinterpret_cast<const uint4*>(kn + key_a * krow + 8 * x) : z;
+      const uint4 vb = key_a + 2 < q_len ? *reinterpret_cast<const uint4*>(kn + (key_a + 2) * krow + 8 * x) : z;
       const uint32_t f0[4] = {va.x, vb.x, va.y, vb.y}, f1[4] = {va.z, vb.z, va.w, vb.w};
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const __nv_bfloat16* p = q_row(nt);
-        const uint4 qv = p ? reinterpret_cast<const uint4*>(p)[x] : z;
+        const uint4* p = q_row(nt);
+        const uint4 qv = p ? p[x] : z;
         mma_bf16(s[nt], f0, qv.x, qv.y);
         mma_bf16(s[nt], f1, qv.z, qv.w);
       }
     }
+    constexpr uint32_t kMine = W == 1 ? 0xffffu : W == 2 ? 0x5555u : W == 4 ? 0x1111u : 0x0101u;
     uint32_t vis[NT][2];  // bit j: the row sees key j, one of this warp's
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -329,11 +374,11 @@ __global__ void __launch_bounds__(kThreads) decode_i4_kernel(const I4Args a) {
       for (int e = 0; e < 2; ++e) {
         const int r = nt * 8 + 2 * c + e;
         uint32_t bits = 0;
-        if (r < un.rows) {
-          const int qi = (un.row0 + r) / G;
+        if (r < rows) {
+          const int qi = (row0 + r) / G;
           bits = a.tree_bits ? static_cast<uint32_t>(a.tree_bits[un.qb_first + qi]) : (2u << qi) - 1u;
         }
-        vis[nt][e] = bits & ((1u << un.q_len) - 1u) & (0x1111u << warp);
+        vis[nt][e] = bits & ((1u << q_len) - 1u) & (kMine << warp);
       }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -341,17 +386,18 @@ __global__ void __launch_bounds__(kThreads) decode_i4_kernel(const I4Args a) {
       for (int e = 0; e < 4; ++e)
         s[nt][e] = ((vis[nt][e & 1] >> (key_a + (e >> 1) * 2)) & 1u) ? s[nt][e] * a.sl2 : -INFINITY;
     softmax(s);
-    const __nv_bfloat16* vn = a.v_new + un.qb_first * krow + g * kHeadDim + 16 * i;
-    for (int j = warp; j < un.q_len; j += 4) {
+    const __nv_bfloat16* vn = a.v_new + at + 16 * i;
+#pragma unroll 1
+    for (int j = warp; j < q_len; j += W) {
       // key j's P sits in lane row 2 (j / 4) + j % 2, first or second register pair
-      const int from = ((2 * (j >> 2) + (warp & 1)) << 2) | c;
+      const int from = ((2 * (j >> 2) + (j & 1)) << 2) | c;
       const uint4 x0 = *reinterpret_cast<const uint4*>(vn + j * krow), x1 = *reinterpret_cast<const uint4*>(vn + j * krow + 8);
       const uint32_t xv[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float pj = __shfl_sync(0xffffffffu, warp < 2 ? s[nt][e] : s[nt][2 + e], from);
+          const float pj = __shfl_sync(0xffffffffu, (j & 2) ? s[nt][2 + e] : s[nt][e], from);
           if ((vis[nt][e] >> j) & 1u) {
 #pragma unroll
             for (int x = 0; x < 8; ++x) {
@@ -363,59 +409,106 @@ __global__ void __launch_bounds__(kThreads) decode_i4_kernel(const I4Args a) {
     }
   }
 
-  // ---------------------------------------------------------------- the four warps' results
+  // ---------------------------------------------------------------- results
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
+    for (int e = 0; e < 2; ++e)
 #pragma unroll
       for (int k = 4; k < 32; k <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], k);
+  if constexpr (W > 1) {
+    // tile nt is finished by warp nt % W: the others leave their image of it
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+      if (nt % W != warp) {
+#pragma unroll
+        for (int x = 0; x < 8; ++x) sm.o[warp][nt][x][lane] = make_float4(o[nt][x][0], o[nt][x][1], o[nt][x][2], o[nt][x][3]);
+        sm.ml[warp][nt][lane] = make_float4(mo[nt][0], mo[nt][1], l[nt][0], l[nt][1]);
+      }
+    __syncthreads();
+  }
+  const int n_pre = un.n_pre;
+  const int64_t pre = un.pre, pre_stride = un.pre_stride, part = un.part;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    if (W > 1 && nt % W != warp) continue;
+    if constexpr (W > 1) {
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        if (w == nt % W) continue;
+        const float4 ml = sm.ml[w][nt][lane];
+        const float m2[2] = {ml.x, ml.y}, l2[2] = {ml.z, ml.w};
+        float f1[2], f2[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          // a side that has seen nothing has kNoMax and zero sums
+          const float M = fmaxf(mo[nt][e], m2[e]);
+          f1[e] = fast_exp2(mo[nt][e] - M);
+          f2[e] = fast_exp2(m2[e] - M);
+          mo[nt][e] = M;
+          l[nt][e] = l[nt][e] * f1[e] + l2[e] * f2[e];
+        }
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          const float4 v = sm.o[w][nt][x][lane];
+          o[nt][x][0] = fmaf(v.x, f2[0], o[nt][x][0] * f1[0]);
+          o[nt][x][1] = fmaf(v.y, f2[1], o[nt][x][1] * f1[1]);
+          o[nt][x][2] = fmaf(v.z, f2[0], o[nt][x][2] * f1[0]);
+          o[nt][x][3] = fmaf(v.w, f2[1], o[nt][x][3] * f1[1]);
+        }
+      }
+    }
+    // the lane's two rows: dims 16 i .. 16 i + 15 of each
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
       const int r = nt * 8 + 2 * c + e;
-      if (i == 0) {
-        sm.m[warp][r] = mo[nt][e];
-        sm.l[warp][r] = l[nt][e];
-      }
+      if (r >= rows) continue;
+      const int R = row0 + r;
+      const int64_t qh = static_cast<int64_t>(R / G) * a.Hq + g * G + R % G;  // (token, head) from q_first
+      float M = mo[nt][e], L = l[nt][e];
+      float acc[16];
 #pragma unroll
-      for (int x = 0; x < 4; ++x)
-        *reinterpret_cast<float4*>(&sm.o[warp][r][16 * i + 4 * x]) =
-            make_float4(o[nt][2 * x][e], o[nt][2 * x][2 + e], o[nt][2 * x + 1][e], o[nt][2 * x + 1][2 + e]);
-    }
-  __syncthreads();
-  // thread t is head dim t
-  const int t = threadIdx.x;
-  for (int r = 0; r < un.rows; ++r) {
-    const int R = un.row0 + r;
-    const int64_t qh = static_cast<int64_t>(R / G) * a.Hq + g * G + R % G;  // (token, head) from q_first
-    float M = kNoMax, L = 0.f, acc = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w)
-      if (!(sm.l[w][r] == 0.f)) M = fmaxf(M, sm.m[w][r]);
-    const int n_pre = un.n_pre;
-    for (int k = 0; k < n_pre; ++k) M = fmaxf(M, a.part_lse[un.pre + k * un.pre_stride + qh]);
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w)
-      if (!(sm.l[w][r] == 0.f)) {
-        const float e = fast_exp2(sm.m[w][r] - M);
-        L = fmaf(sm.l[w][r], e, L);
-        acc = fmaf(sm.o[w][r][t], e, acc);
+      for (int x = 0; x < 8; ++x) {
+        acc[2 * x] = o[nt][x][e];
+        acc[2 * x + 1] = o[nt][x][2 + e];
       }
-    for (int k = 0; k < n_pre; ++k) {
-      const int64_t row = un.pre + k * un.pre_stride + qh;
-      const float e = fast_exp2(a.part_lse[row] - M);
-      if (e > 0.f || !(e == e)) {
-        L += e;
-        acc = fmaf(a.part_o[row * kHeadDim + t], e, acc);
+#pragma unroll 1
+      for (int k = 0; k < n_pre; ++k) {
+        const int64_t row = pre + k * pre_stride + qh;
+        const float m2 = a.part_lse[row];
+        const float4* src = reinterpret_cast<const float4*>(a.part_o + row * kHeadDim + 16 * i);
+        const float4 v[4] = {src[0], src[1], src[2], src[3]};
+        if (m2 == -INFINITY) continue;  // the row saw nothing there
+        const float Mn = fmaxf(M, m2);
+        const float f1 = fast_exp2(M - Mn), f2 = fast_exp2(m2 - Mn);
+        M = Mn;
+        L = fmaf(L, f1, f2);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          acc[4 * x] = fmaf(v[x].x, f2, acc[4 * x] * f1);
+          acc[4 * x + 1] = fmaf(v[x].y, f2, acc[4 * x + 1] * f1);
+          acc[4 * x + 2] = fmaf(v[x].z, f2, acc[4 * x + 2] * f1);
+          acc[4 * x + 3] = fmaf(v[x].w, f2, acc[4 * x + 3] * f1);
+        }
       }
-    }
-    const bool any = !(L == 0.f);
-    const float out = any ? acc / L : 0.f;
-    if (un.part >= 0) {
-      a.part_o[(un.part + qh) * kHeadDim + t] = out;
-      if (t == 0) a.part_lse[un.part + qh] = any ? M + __log2f(L) : -INFINITY;
-    } else {
-      const int64_t row = static_cast<int64_t>(un.q_first) * a.Hq + qh;
-      a.o[row * kHeadDim + t] = __float2bfloat16_rn(out);
-      if (t == 0) a.lse[row] = any ? (M + __log2f(L)) * kLn2 : -INFINITY;
+      const bool any = !(L == 0.f);  // NaN counts
+      const float inv = any ? 1.f / L : 0.f;
+      if (part >= 0) {
+        float4* dst = reinterpret_cast<float4*>(a.part_o + (part + qh) * kHeadDim + 16 * i);
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          dst[x] = make_float4(acc[4 * x] * inv, acc[4 * x + 1] * inv, acc[4 * x + 2] * inv, acc[4 * x + 3] * inv);
+        if (i == 0) a.part_lse[part + qh] = any ? M + __log2f(L) : -INFINITY;
+      } else {
+        const int64_t row = static_cast<int64_t>(q_first) * a.Hq + qh;
+        uint4* dst = reinterpret_cast<uint4*>(a.o + row * kHeadDim + 16 * i);
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          dst[x] = make_uint4(pack_bf16x2(acc[8 * x] * inv, acc[8 * x + 1] * inv), pack_bf16x2(acc[8 * x + 2] * inv, acc[8 * x + 3] * inv),
+                              pack_bf16x2(acc[8 * x + 4] * inv, acc[8 * x + 5] * inv),
+                              pack_bf16x2(acc[8 * x + 6] * inv, acc[8 * x + 7] * inv));
+        if (i == 0) a.lse[row] = any ? (M + __log2f(L)) * kLn2 : -INFINITY;
+      }
     }
   }
 }
@@ -460,29 +553,36 @@ int launch_error(const char* what, std::string* err) {
   return PADOC_ERR_CUDA;
 }
 
-template <int NT>
+template <int NT, int W>
 int launch_units(I4Args a, int32_t unit0, int32_t n, cudaStream_t s, std::string* err) {
-  if (n == 0) return PADOC_OK;
-  const int bytes = sizeof(Smem<NT>);
+  const int bytes = W > 1 ? sizeof(Smem<NT, W>) : NT > 2 ? NT * 4 * 32 * 16 : 0;
   if (bytes > 48 * 1024) {
     // per device, so set at each launch (a host call of well under a microsecond)
-    const cudaError_t e = cudaFuncSetAttribute(decode_i4_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    const cudaError_t e = cudaFuncSetAttribute(decode_i4_kernel<NT, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) {
       *err = std::string("cudaFuncSetAttribute: ") + cudaGetErrorString(e);
       return PADOC_ERR_CUDA;
     }
   }
   a.unit0 = unit0;
-  decode_i4_kernel<NT><<<static_cast<unsigned>(n) * a.Hkv, kThreads, bytes, s>>>(a);
+  decode_i4_kernel<NT, W><<<static_cast<unsigned>(n) * a.Hkv, 32 * W, bytes, s>>>(a);
   return launch_error("i4 decode launch", err);
+}
+
+template <int NT>
+int launch_rows(const I4Args& a, int32_t unit0, int32_t n, int warps, cudaStream_t s, std::string* err) {
+  if (n == 0) return PADOC_OK;
+  if (warps == 1) return launch_units<NT, 1>(a, unit0, n, s, err);
+  if (warps == 2) return launch_units<NT, 2>(a, unit0, n, s, err);
+  return launch_units<NT, 4>(a, unit0, n, s, err);
 }
 
 }  // namespace
 
-int launch_i4_units(const I4Args& a, const int32_t (&first)[4], cudaStream_t s, std::string* err) {
-  int rc = launch_units<1>(a, first[0], first[1] - first[0], s, err);
-  if (!rc) rc = launch_units<2>(a, first[1], first[2] - first[1], s, err);
-  if (!rc) rc = launch_units<4>(a, first[2], first[3] - first[2], s, err);
+int launch_i4_units(const I4Args& a, const int32_t (&first)[4], int warps, cudaStream_t s, std::string* err) {
+  int rc = launch_rows<1>(a, first[0], first[1] - first[0], warps, s, err);
+  if (!rc) rc = launch_rows<2>(a, first[1], first[2] - first[1], warps, s, err);
+  if (!rc) rc = launch_rows<4>(a, first[2], first[3] - first[2], warps, s, err);
   return rc;
 }
 

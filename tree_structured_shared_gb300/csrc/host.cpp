@@ -1400,6 +1400,7 @@ struct DecodePlan {
   std::vector<I4Unit> units;
   std::vector<I4Merge> merges;
   int32_t pre_first[4] = {0, 0, 0, 0}, own_first[4] = {0, 0, 0, 0};
+  int32_t pre_warps = 4, own_warps = 4;  // warps that share a unit
   int32_t n_tc = 0;  // prefix units of up to 128 rows: the first of all
   size_t off_units = 0, off_merges = 0;
   size_t off_pages = 0, off_items = 0, off_branches = 0, off_qplen = 0, off_qbranch = 0, off_part_o = 0, off_part_lse = 0,
@@ -1542,6 +1543,11 @@ int plan_i4(const padoc_kv_pool* pool, const padoc_decode_batch* b, int32_t Hq, 
   pl->n_tc = static_cast<int32_t>(pl->units.size());
   add_units(pre, &pl->units, pl->pre_first);
   add_units(own, &pl->units, pl->own_first);
+  // One warp a unit once that fills the GPU's 16 warps an SM twice over; fewer
+  // units are shared by two or four (decode of 2176 branches a page batch: 799,
+  // 837 and 966 us with one, two and four).
+  const int64_t own_n = static_cast<int64_t>(pl->own_first[3] - pl->own_first[0]) * pool->Hkv;
+  pl->own_warps = own_n >= 32 * static_cast<int64_t>(n_sms) ? 1 : own_n >= 8 * static_cast<int64_t>(n_sms) ? 2 : 4;
   if (static_cast<int64_t>(pl->units.size()) * pool->Hkv >= (int64_t(1) << 31) ||
       static_cast<int64_t>(nq) * Hq >= (int64_t(1) << 31))
     return fail(PADOC_ERR_UNSUPPORTED, "branch_decode: batch too large");
@@ -1903,7 +1909,7 @@ extern "C" int padoc_decode_prefix_pass(const padoc_decode_plan* plan, const voi
     const I4Args a = i4_args(plan, q, nullptr, nullptr, nullptr, nullptr, nullptr, scale, ws);
     std::string err;
     rc = launch_i4_prefix_tc(a, 0, plan->pl.n_tc, reinterpret_cast<cudaStream_t>(stream), &err);
-    if (!rc) rc = launch_i4_units(a, plan->pl.pre_first, reinterpret_cast<cudaStream_t>(stream), &err);
+    if (!rc) rc = launch_i4_units(a, plan->pl.pre_first, plan->pl.pre_warps, reinterpret_cast<cudaStream_t>(stream), &err);
     if (rc) return fail(rc, "decode_prefix_pass: %s", err.c_str());
     return PADOC_OK;
   }
@@ -1928,7 +1934,7 @@ extern "C" int padoc_decode_own_pass(const padoc_decode_plan* plan, const void* 
   if (plan->pool->dtype == PADOC_I4) {
     const I4Args a = i4_args(plan, q, k_new, v_new, tree_bits, o, lse, scale, ws);
     std::string err;
-    rc = launch_i4_units(a, plan->pl.own_first, reinterpret_cast<cudaStream_t>(stream), &err);
+    rc = launch_i4_units(a, plan->pl.own_first, plan->pl.own_warps, reinterpret_cast<cudaStream_t>(stream), &err);
     if (!rc)
       rc = launch_i4_merge(a, static_cast<int32_t>(plan->pl.merges.size()), reinterpret_cast<cudaStream_t>(stream), &err);
     if (rc) return fail(rc, "decode_own_pass: %s", err.c_str());
