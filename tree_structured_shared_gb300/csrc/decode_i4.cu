@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(32 * W) decode_i4_kernel(const I4Args a) {
   for (int s = 16; s; s >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, s));
   const int kexp = amax > 0.f ? min(100, 14 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127)) : 0;
   const float qf = __uint_as_float(static_cast<uint32_t>(127 + kexp) << 23);
-  const float sl2q = a.sl2 * __uint_as_float(static_cast<uint32_t>(127 - kexp) << 23);
+  const float sl2q = a.sl2 * kI4Unscale * __uint_as_float(static_cast<uint32_t>(127 - kexp) << 23);
   auto half2 = [&](uint32_t v) { return pack_f16x2(__uint_as_float(v << 16) * qf, __uint_as_float(v & 0xffff0000u) * qf); };
   if constexpr (kQInSmem) {
 #pragma unroll 1
@@ -220,12 +220,11 @@ __global__ void __launch_bounds__(32 * W) decode_i4_kernel(const I4Args a) {
   // P of one tile of scores (log2 units) against the running references, which
   // move first where a score exceeds them by more than kPSlack
   auto softmax = [&](float (&s)[NT][4]) {
-    bool grow = false;
+    float most = -INFINITY;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) grow |= s[nt][e] - mo[nt][e & 1] > kPShift + kPSlack;
-    if (__any_sync(0xffffffffu, grow)) {
+      most = max3f(most, fmaxf(s[nt][0], s[nt][2]) - mo[nt][0], fmaxf(s[nt][1], s[nt][3]) - mo[nt][1]);
+    if (__any_sync(0xffffffffu, most > kPShift + kPSlack)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float al[2];
@@ -272,17 +271,18 @@ __global__ void __launch_bounds__(32 * W) decode_i4_kernel(const I4Args a) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
     {
+      const I4Scale sa0 = i4_scale_both<0>(b.sa), sa1 = i4_scale_both<1>(b.sa);
+      const I4Scale sb0 = i4_scale_both<0>(b.sb), sb1 = i4_scale_both<1>(b.sb);
       const uint32_t wa[4] = {b.ka.x, b.ka.y, b.ka.z, b.ka.w}, wb[4] = {b.kb.x, b.kb.y, b.kb.z, b.kb.w};
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         // words 0, 1 of the chunk are its first group, 2, 3 its second
-        const uint32_t ba = w < 2 ? b.sa & 0xffu : b.sa >> 8, bb = w < 2 ? b.sb & 0xffu : b.sb >> 8;
-        const uint32_t sa = i4_scale_pair(ba, ba), sb = i4_scale_pair(bb, bb);
-        const uint32_t fa = i4_offset(sa), fb = i4_offset(sb);
-        const uint32_t f0[4] = {i4_pair<0>(wa[w], sa, fa), i4_pair<0>(wb[w], sb, fb), i4_pair<1>(wa[w], sa, fa),
-                                i4_pair<1>(wb[w], sb, fb)};
-        const uint32_t f1[4] = {i4_pair<2>(wa[w], sa, fa), i4_pair<2>(wb[w], sb, fb), i4_pair<3>(wa[w], sa, fa),
-                                i4_pair<3>(wb[w], sb, fb)};
+        const I4Scale &sa = w < 2 ? sa0 : sa1, &sb = w < 2 ? sb0 : sb1;
+        const uint32_t va = wa[w] >> 8, vb = wb[w] >> 8;
+        const uint32_t f0[4] = {i4_pair<0>(wa[w], va, sa), i4_pair<0>(wb[w], vb, sb), i4_pair<1>(wa[w], va, sa),
+                                i4_pair<1>(wb[w], vb, sb)};
+        const uint32_t f1[4] = {i4_pair<2>(wa[w], va, sa), i4_pair<2>(wb[w], vb, sb), i4_pair<3>(wa[w], va, sa),
+                                i4_pair<3>(wb[w], vb, sb)};
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           if constexpr (kQInSmem) {
@@ -318,9 +318,7 @@ __global__ void __launch_bounds__(32 * W) decode_i4_kernel(const I4Args a) {
       p[nt][0] = transpose8(pack_f16x2(s[nt][0], s[nt][1]));
       p[nt][1] = transpose8(pack_f16x2(s[nt][2], s[nt][3]));
     }
-    const uint32_t s01 = i4_scale_pair(b.sv & 0xffu, (b.sv >> 8) & 0xffu);
-    const uint32_t s23 = i4_scale_pair((b.sv >> 16) & 0xffu, b.sv >> 24);
-    const uint32_t f01 = i4_offset(s01), f23 = i4_offset(s23);
+    const I4Scale s01 = i4_scale_two<0>(b.sv), s23 = i4_scale_two<2>(b.sv);
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
       // low halves: even dims of two keys side by side; high halves: odd dims
@@ -328,15 +326,16 @@ __global__ void __launch_bounds__(32 * W) decode_i4_kernel(const I4Args a) {
       const uint32_t k2 = w ? b.v1.y : b.v1.x, k3 = w ? b.v1.w : b.v1.z;
       const uint32_t e01 = __byte_perm(k0, k1, 0x5410), d01 = __byte_perm(k0, k1, 0x7632);
       const uint32_t e23 = __byte_perm(k2, k3, 0x5410), d23 = __byte_perm(k2, k3, 0x7632);
+      const uint32_t e01v = e01 >> 8, d01v = d01 >> 8, e23v = e23 >> 8, d23v = d23 >> 8;
       auto pv = [&](int mt, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
         const uint32_t f[4] = {a0, a1, a2, a3};
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) mma_f16(o[nt][mt], f, p[nt][0], p[nt][1]);
       };
-      pv(4 * w + 0, i4_pair<0>(e01, s01, f01), i4_pair<0>(d01, s01, f01), i4_pair<0>(e23, s23, f23), i4_pair<0>(d23, s23, f23));
-      pv(4 * w + 1, i4_pair<1>(e01, s01, f01), i4_pair<1>(d01, s01, f01), i4_pair<1>(e23, s23, f23), i4_pair<1>(d23, s23, f23));
-      pv(4 * w + 2, i4_pair<2>(e01, s01, f01), i4_pair<2>(d01, s01, f01), i4_pair<2>(e23, s23, f23), i4_pair<2>(d23, s23, f23));
-      pv(4 * w + 3, i4_pair<3>(e01, s01, f01), i4_pair<3>(d01, s01, f01), i4_pair<3>(e23, s23, f23), i4_pair<3>(d23, s23, f23));
+      pv(4 * w + 0, i4_pair<0>(e01, e01v, s01), i4_pair<0>(d01, d01v, s01), i4_pair<0>(e23, e23v, s23), i4_pair<0>(d23, d23v, s23));
+      pv(4 * w + 1, i4_pair<1>(e01, e01v, s01), i4_pair<1>(d01, d01v, s01), i4_pair<1>(e23, e23v, s23), i4_pair<1>(d23, d23v, s23));
+      pv(4 * w + 2, i4_pair<2>(e01, e01v, s01), i4_pair<2>(d01, d01v, s01), i4_pair<2>(e23, e23v, s23), i4_pair<2>(d23, d23v, s23));
+      pv(4 * w + 3, i4_pair<3>(e01, e01v, s01), i4_pair<3>(d01, d01v, s01), i4_pair<3>(e23, e23v, s23), i4_pair<3>(d23, d23v, s23));
     }
   }
 
@@ -397,7 +396,8 @@ __global__ void __launch_bounds__(32 * W) decode_i4_kernel(const I4Args a) {
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float pj = __shfl_sync(0xffffffffu, (j & 2) ? s[nt][2 + e] : s[nt][e], from);
+          // (O of cached keys lacks the factor kI4Unscale)
+          const float pj = __shfl_sync(0xffffffffu, (j & 2) ? s[nt][2 + e] : s[nt][e], from) * (1.f / kI4Unscale);
           if ((vis[nt][e] >> j) & 1u) {
 #pragma unroll
             for (int x = 0; x < 8; ++x) {
@@ -469,8 +469,8 @@ __global__ void __launch_bounds__(32 * W) decode_i4_kernel(const I4Args a) {
       float acc[16];
 #pragma unroll
       for (int x = 0; x < 8; ++x) {
-        acc[2 * x] = o[nt][x][e];
-        acc[2 * x + 1] = o[nt][x][2 + e];
+        acc[2 * x] = o[nt][x][e] * kI4Unscale;
+        acc[2 * x + 1] = o[nt][x][2 + e] * kI4Unscale;
       }
 #pragma unroll 1
       for (int k = 0; k < n_pre; ++k) {

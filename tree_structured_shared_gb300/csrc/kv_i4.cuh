@@ -14,8 +14,8 @@
 // A scale is one byte, bits 14..7 of an fp16 number (5 exponent and 3 mantissa
 // bits, no sign): n has 3 significant bits and s has 4, so every value n * s
 // is exact in fp16 (and bf16), and no second-level scale is needed for
-// magnitudes from 2^-17 to 7 * 896.  Scales stop at 896 so that 72 * s, the
-// offset of the decode below, stays finite in fp16.
+// magnitudes from 2^-17 to 7 * 896.  Scales stop at 896 so that the decode's
+// offsets below stay finite in fp16.
 #pragma once
 #include <cstdint>
 #include <cuda_fp16.h>
@@ -42,9 +42,6 @@ __device__ __forceinline__ float i4_scale_value(uint32_t byte) {
   return __half2float(__ushort_as_half(static_cast<unsigned short>(byte << 7)));
 }
 
-// Two scale bytes as an fp16 pair: lo's in the low half.
-__device__ __forceinline__ uint32_t i4_scale_pair(uint32_t lo, uint32_t hi) { return (lo << 7) | (hi << 23); }
-
 __device__ __forceinline__ uint32_t h2_fma(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t d;
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
@@ -55,16 +52,41 @@ __device__ __forceinline__ uint32_t h2_mul(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-// -72 s, the offset that i4_pair wants next to s.
-__device__ __forceinline__ uint32_t i4_offset(uint32_t s2) { return h2_mul(s2, 0xD480D480u); }
 
-// The pair of values in nibbles j and 4 + j of w.  The nibble in mantissa bits
-// 7..4 of 64.0 makes 64 + n + 8; one fma takes (72 + n) s - 72 s = n s, exact
-// (72 s has 7 significant bits, n s has 7).
+// Decoding.  A nibble or-ed into the mantissa of a power of two makes that power
+// plus n + 8 without a conversion: bits 3..0 of a half under 1024, bits 7..4
+// under 64.  One fma then takes the bias off and the scale on,
+//   (1032 + n) s' - 1032 s' = n s',   (72 + n) s' - 72 s' = n s',
+// exact with s' = s / 16: 1032 s' has at most 11 significant bits (129 times a
+// 4-bit mantissa) and stays below 65504 for every s up to 896, n s' has 7, and
+// s' of the smallest s is still a multiple of 2^-21.  The factor 16 joins the
+// softmax's scale (K) or the output's (V).  A word so costs one shift, four
+// masks and four fmas; the integer pipe, half as wide as the others, is what the
+// decode kernels fill first (three shifts a word: 60 % of its cycles in the own
+// pass at 58 % issue).
+constexpr float kI4Unscale = 16.f;
+struct I4Scale {
+  uint32_t s, lo, hi;  // s', -1032 s', -72 s', for the two halves of a register
+};
+// pair: two scale bytes in bits 7..0 and 23..16.
+__device__ __forceinline__ I4Scale i4_scale(uint32_t pair) {
+  const uint32_t h = pair * 128u;  // bits 14..7 of each half; a multiply, off the integer pipe
+  return I4Scale{h2_mul(h, 0x2C002C00u), h2_mul(h, 0xD408D408u), h2_mul(h, 0xC480C480u)};
+}
+// Byte B of x for both halves of a register, or bytes B and B + 1 for one each.
+template <int B>
+__device__ __forceinline__ I4Scale i4_scale_both(uint32_t x) {
+  return i4_scale(__byte_perm(x, 0u, 0x4040u | B | (B << 8)));
+}
+template <int B>
+__device__ __forceinline__ I4Scale i4_scale_two(uint32_t x) {
+  return i4_scale(__byte_perm(x, 0u, 0x4040u | B | ((B + 1) << 8)));
+}
+// n s' of nibbles J and 4 + J of w in the halves of a register, v = w >> 8.
 template <int J>
-__device__ __forceinline__ uint32_t i4_pair(uint32_t w, uint32_t s2, uint32_t off2) {
-  const uint32_t x = J == 0 ? w << 4 : J == 1 ? w : J == 2 ? w >> 4 : w >> 8;
-  return h2_fma((x & 0x00F000F0u) | 0x54005400u, s2, off2);
+__device__ __forceinline__ uint32_t i4_pair(uint32_t w, uint32_t v, const I4Scale& s) {
+  const uint32_t x = J < 2 ? w : v;
+  return (J & 1) ? h2_fma((x & 0x00F000F0u) | 0x54005400u, s.s, s.hi) : h2_fma((x & 0x000F000Fu) | 0x64006400u, s.s, s.lo);
 }
 
 }  // namespace padoc

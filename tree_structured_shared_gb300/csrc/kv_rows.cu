@@ -214,14 +214,14 @@ __global__ void __launch_bounds__(kThreads) kv_gather_kernel(const __grid_consta
       const uint32_t w = *reinterpret_cast<const uint32_t*>(
           half ? s + (l >> 1) * 128 + slot * 8 + (l & 1) * 4 : s + (l >> 2) * 256 + slot * 16 + (l & 3) * 4);
       const uint32_t b = half ? s[kI4Scales + (l >> 1) * 16 + slot] : s[kI4Scales + slot * 8 + (l >> 1)];
-      const uint32_t s2 = i4_scale_pair(b, b), off = i4_offset(s2);
-      const uint32_t p[4] = {i4_pair<0>(w, s2, off), i4_pair<1>(w, s2, off), i4_pair<2>(w, s2, off),
-                             i4_pair<3>(w, s2, off)};
+      const I4Scale sc = i4_scale(b | b << 16);
+      const uint32_t p[4] = {i4_pair<0>(w, w >> 8, sc), i4_pair<1>(w, w >> 8, sc), i4_pair<2>(w, w >> 8, sc),
+                             i4_pair<3>(w, w >> 8, sc)};
       uint32_t o[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p[i]));
-        o[i] = pack_bf16x2(f.x, f.y);  // exact: a value has at most 7 significant bits
+        o[i] = pack_bf16x2(f.x * kI4Unscale, f.y * kI4Unscale);  // exact: a value has at most 7 significant bits
       }
       out = make_uint4(o[0], o[1], o[2], o[3]);
     }

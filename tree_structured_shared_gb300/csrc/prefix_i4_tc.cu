@@ -6,7 +6,7 @@
 // prefix in tiles of 128 keys.  Two warpgroups turn a tile's codes into fp16
 // operand tiles in shared memory, each thread from the 72 bytes it copied there
 // itself three tiles ahead; no wider copy exists outside the SM.  fp16 holds
-// every decoded value exactly; Q's rows are scaled by a power of two each
+// every decoded value exactly (kv_i4.cuh); Q's rows are scaled by a power of two each
 // (largest magnitude in [2^14, 2^15)), and the scale joins the row's softmax.
 //
 // Roles (544 threads, one persistent CTA per SM):
@@ -118,8 +118,9 @@ __device__ __forceinline__ void raise_abort(volatile int* abort, unsigned site) 
 }
 
 // The eight dims of a word of codes as one 16-byte piece of an operand tile.
-__device__ __forceinline__ void put_word(uint32_t addr, uint32_t w, uint32_t s2, uint32_t off) {
-  st_shared_v4(addr, i4_pair<0>(w, s2, off), i4_pair<1>(w, s2, off), i4_pair<2>(w, s2, off), i4_pair<3>(w, s2, off));
+__device__ __forceinline__ void put_word(uint32_t addr, uint32_t w, const I4Scale& s) {
+  const uint32_t v = w >> 8;
+  st_shared_v4(addr, i4_pair<0>(w, v, s), i4_pair<1>(w, v, s), i4_pair<2>(w, v, s), i4_pair<3>(w, v, s));
 }
 
 __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a, const int n_work) {
@@ -236,13 +237,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a, 
             const uint32_t sc = ld_shared_u32(codes + kCodes + t * 8 + (x >> 1) * 4) >> (16 * (x & 1));
             const uint32_t half = row + (x >> 1) * kHalf;
             const int p0 = (x & 1) * 4;
-            uint32_t s2 = i4_scale_pair(sc & 0xffu, sc & 0xffu), off = i4_offset(s2);
-            put_word(half + (((p0 + 0) ^ sw) << 4), c.x, s2, off);
-            put_word(half + (((p0 + 1) ^ sw) << 4), c.y, s2, off);
-            s2 = i4_scale_pair((sc >> 8) & 0xffu, (sc >> 8) & 0xffu);
-            off = i4_offset(s2);
-            put_word(half + (((p0 + 2) ^ sw) << 4), c.z, s2, off);
-            put_word(half + (((p0 + 3) ^ sw) << 4), c.w, s2, off);
+            const I4Scale s0 = i4_scale_both<0>(sc), s1 = i4_scale_both<1>(sc);
+            put_word(half + (((p0 + 0) ^ sw) << 4), c.x, s0);
+            put_word(half + (((p0 + 1) ^ sw) << 4), c.y, s0);
+            put_word(half + (((p0 + 2) ^ sw) << 4), c.z, s1);
+            put_word(half + (((p0 + 3) ^ sw) << 4), c.w, s1);
           }
         } else {
           // the upper four pairs of slots go the other way round, so that eight
@@ -256,16 +255,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a, 
             const uint32_t sc = ld_shared_u32(codes + kCodes + x * 512 + t * 4) >> (16 * (sp & 1));
             const int key = (2 * x + (t >> 6)) * 16 + sp * 2;
             // keys past the end may hold old bytes and must not be NaN: a scale of zero
-            const uint32_t b0 = k0 + key < n_keys ? sc & 0xffu : 0u, b1 = k0 + key + 1 < n_keys ? (sc >> 8) & 0xffu : 0u;
+            const uint32_t b0 = k0 + key < n_keys ? sc & 0xffu : 0u, b1 = k0 + key + 1 < n_keys ? sc & 0xff00u : 0u;
+            const uint32_t two = swap ? __byte_perm(b0 | b1, 0u, 0x4401u) : b0 | b1;
             const int ka = key + swap, kb = key + 1 - swap;
-            const uint32_t ba = swap ? b1 : b0, bb = swap ? b0 : b1;
-            uint32_t s2 = i4_scale_pair(ba, ba), off = i4_offset(s2);
-            put_word(half + ka * 128 + (((p0 + 0) ^ (ka & 7)) << 4), swap ? c.z : c.x, s2, off);
-            put_word(half + ka * 128 + (((p0 + 1) ^ (ka & 7)) << 4), swap ? c.w : c.y, s2, off);
-            s2 = i4_scale_pair(bb, bb);
-            off = i4_offset(s2);
-            put_word(half + kb * 128 + (((p0 + 0) ^ (kb & 7)) << 4), swap ? c.x : c.z, s2, off);
-            put_word(half + kb * 128 + (((p0 + 1) ^ (kb & 7)) << 4), swap ? c.y : c.w, s2, off);
+            const I4Scale s0 = i4_scale_both<0>(two), s1 = i4_scale_both<1>(two);
+            put_word(half + ka * 128 + (((p0 + 0) ^ (ka & 7)) << 4), swap ? c.z : c.x, s0);
+            put_word(half + ka * 128 + (((p0 + 1) ^ (ka & 7)) << 4), swap ? c.w : c.y, s0);
+            put_word(half + kb * 128 + (((p0 + 0) ^ (kb & 7)) << 4), swap ? c.x : c.z, s1);
+            put_word(half + kb * 128 + (((p0 + 1) ^ (kb & 7)) << 4), swap ? c.y : c.w, s1);
           }
         }
         fence_proxy_async_smem();
@@ -363,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a, 
         }
         const int kexp = amax > 0.f ? min(100, 14 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127)) : 0;
         const float qf = __uint_as_float(static_cast<uint32_t>(127 + kexp) << 23);
-        sl2 = a.sl2 * __uint_as_float(static_cast<uint32_t>(127 - kexp) << 23);
+        sl2 = a.sl2 * kI4Unscale * __uint_as_float(static_cast<uint32_t>(127 - kexp) << 23);
         auto h = [&](uint32_t u) { return pack_f16x2(__uint_as_float(u << 16) * qf, __uint_as_float(u & 0xffff0000u) * qf); };
         const uint32_t row = sbase + SM_Q + r * 128;
 #pragma unroll 4
@@ -525,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a, 
         const float M = fmaxf(any_e ? m_run : -INFINITY, any_o ? m_o : -INFINITY);
         const float we = any_e ? fast_exp2(m_run - M) : 0.f, wo = any_o ? fast_exp2(m_o - M) : 0.f;
         const float L = (any_e ? l_run * we : 0.f) + (any_o ? l_o * wo : 0.f);
-        const float fe = any_e ? we / L : 0.f, fo = any_o ? wo / L : 0.f;
+        const float fe = any_e ? we * kI4Unscale / L : 0.f, fo = any_o ? wo * kI4Unscale / L : 0.f;
         const int64_t row = un.part + static_cast<int64_t>(R / G) * a.Hq + (w % a.Hkv) * G + R % G;
         float* dst = a.part_o + row * kHeadDim;
 #pragma unroll 1
