@@ -30,6 +30,7 @@
 // that see the key, so a NaN in a hidden draft token stays there.
 #include <cuda_bf16.h>
 
+#include <algorithm>
 #include <string>
 
 #include "../../include/padoc.h"
@@ -70,14 +71,6 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ uint4 ld_stream(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
-
 // One 16-token block of a kv head as a lane holds it.
 struct BlockRegs {
   uint4 ka, kb;      // chunk c of the keys 4 (i / 2) + i % 2 and + 2
@@ -86,15 +79,62 @@ struct BlockRegs {
   uint32_t sv;       // the four keys' scales of group i
 };
 
-__device__ __forceinline__ BlockRegs load_block(const uint8_t* kp, const uint8_t* vp, int key_a, int i, int c) {
+// A block in a warp's ring in shared memory: K codes with 32 bytes between the
+// 256-byte chunks, K scales, V codes with the halves of the odd groups' 32-byte
+// pieces swapped, V scales.  Eight neighbouring lanes of a 16-byte read then
+// touch every bank once.
+// Blocks of a warp's ring; all but one are on their way while one is worked on.
+// Large units of four warps keep three, so that two CTAs fit an SM.
+__host__ __device__ constexpr int ring_of(int NT, int W) { return NT * W >= 16 ? 3 : 4; }
+constexpr int kRingKS = 4 * 288, kRingV = kRingKS + 128, kRingVS = kRingV + 1024, kRingBlock = kRingVS + 128;
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// Starts the copy of a block's 144 16-byte pieces (72 of K, then 72 of V).
+__device__ __forceinline__ void copy_block(uint32_t dst, const uint8_t* kp, const uint8_t* vp, int lane) {
+  const int k2 = 64 + lane;  // the third round: the last pieces of K, the first of V
+  copy16(dst + lane * 16 + (lane >> 4) * 32, kp + lane * 16);
+  copy16(dst + 512 + 64 + lane * 16 + (lane >> 4) * 32, kp + 512 + lane * 16);
+  {
+    const int v = k2 - 72;
+    const uint32_t d = lane < 8 ? kRingKS + lane * 16 : kRingV + ((v * 16) ^ (((v >> 3) & 1) << 4));
+    copy16(dst + d, lane < 8 ? kp + k2 * 16 : vp + v * 16);
+  }
+  {
+    const int v = lane + 24;
+    copy16(dst + kRingV + ((v * 16) ^ (((v >> 3) & 1) << 4)), vp + v * 16);
+  }
+  if (lane < 16) {
+    const int v = lane + 56;
+    copy16(dst + kRingV + (v < 64 ? (v * 16) ^ (((v >> 3) & 1) << 4) : v * 16), vp + v * 16);
+  }
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ BlockRegs read_block(uint32_t src, int key_a, int i, int c) {
   BlockRegs b;
-  b.ka = ld_stream(kp + c * 256 + key_a * 16);
-  b.kb = ld_stream(kp + c * 256 + key_a * 16 + 32);
-  b.sa = *reinterpret_cast<const uint16_t*>(kp + kI4Scales + key_a * 8 + 2 * c);
-  b.sb = *reinterpret_cast<const uint16_t*>(kp + kI4Scales + key_a * 8 + 16 + 2 * c);
-  b.v0 = ld_stream(vp + i * 128 + c * 32);
-  b.v1 = ld_stream(vp + i * 128 + c * 32 + 16);
-  b.sv = *reinterpret_cast<const uint32_t*>(vp + kI4Scales + i * 16 + c * 4);
+  b.ka = lds128(src + c * 288 + key_a * 16);
+  b.kb = lds128(src + c * 288 + key_a * 16 + 32);
+  b.sa = lds16(src + kRingKS + key_a * 8 + 2 * c);
+  b.sb = lds16(src + kRingKS + key_a * 8 + 16 + 2 * c);
+  const uint32_t v = src + kRingV + i * 128 + c * 32 + ((i & 1) << 4);
+  b.v0 = lds128(v);
+  b.v1 = lds128(v ^ 16);
+  b.sv = lds32(src + kRingVS + i * 16 + c * 4);
   return b;
 }
 
@@ -102,40 +142,89 @@ __device__ __forceinline__ BlockRegs load_block(const uint8_t* kp, const uint8_t
 // (8 float4) and, of its two rows, the reference and the sum.
 template <int NT, int W>
 struct Smem {
+  uint4 ring[W][ring_of(NT, W) * kRingBlock / 16];
   float4 o[W][NT][8][32];
   float4 ml[W][NT][32];
-  uint4 q[NT > 2 ? NT : 1][4][32];  // Q fragments of large units
+  uint4 q[NT > 2 ? NT : 1][NT > 2 ? 4 : 1][32];  // Q fragments of large units
 };
 template <int NT>
 struct Smem<NT, 1> {
-  uint4 q[NT][4][32];
+  uint4 ring[1][ring_of(NT, 1) * kRingBlock / 16];
+  uint4 q[NT > 2 ? NT : 1][NT > 2 ? 4 : 1][32];
 };
 
+// A persistent CTA's k-th unit: units come longest first and are dealt back and
+// forth, so that every CTA gets about the same number of keys.
+__device__ __forceinline__ int nth_work(int k) {
+  return k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+}
+
 template <int NT, int W>
-__global__ void __launch_bounds__(32 * W) decode_i4_kernel(const I4Args a) {
+__global__ void __launch_bounds__(32 * W, NT == 1 ? 18 / W : 1) decode_i4_kernel(const I4Args a, const int n_work) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   Smem<NT, W>& sm = *reinterpret_cast<Smem<NT, W>*>(smem_raw);
   constexpr bool kQInSmem = NT > 2;
-  const int u = a.unit0 + blockIdx.x / a.Hkv, g = blockIdx.x % a.Hkv;
-  const I4Unit& un = a.units[u];
+  constexpr int kRing = ring_of(NT, W);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int i = lane >> 2, c = lane & 3;
   const int G = a.group;
   const int key_a = 4 * (i >> 1) + (i & 1);
-  const int32_t* ids = a.table + static_cast<int64_t>(un.seq) * a.max_bps + un.blk0;
+
+  // The copies' own walk over the warp's blocks, kRing - 1 ahead of the work: unit
+  // number, its step, its ids (lane l: step l of the current 32), and the next
+  // unit's record and first ids, read while this one's blocks are copied.
+  const uint32_t ring = smem_u32(&sm.ring[warp][0]);
+  int ck = 0, cstep = 0, csteps = 0, cid = 0, cg = 0;
+  const int32_t* cids = nullptr;
+  int nsteps = 0, nid = 0;
+  const int32_t* nids = nullptr;
+  auto read_next = [&](int k) {  // the record and the ids of the warp's k-th unit
+    const int w = nth_work(k);
+    nsteps = 0;
+    if (w >= n_work) return;
+    const I4Unit& un = a.units[a.unit0 + w / a.Hkv];
+    nids = a.table + static_cast<int64_t>(un.seq) * a.max_bps + un.blk0 + warp;
+    const int n = (un.n_keys + 15) >> 4;
+    nsteps = n > warp ? (n - warp + W - 1) / W : 0;
+    nid = lane < nsteps ? nids[W * lane] : 0;
+  };
+  auto open_next = [&]() {  // to the next unit that has a block for this warp
+    do {
+      cids = nids;
+      cid = nid;
+      csteps = nsteps;
+      cstep = 0;
+      const int w = nth_work(ck);
+      if (w >= n_work) return;
+      cg = w % a.Hkv;
+      ++ck;
+      read_next(ck);
+    } while (csteps == 0);
+  };
+  auto copy_next = [&](int stage) {
+    if (cstep < csteps) {
+      const int32_t id = __shfl_sync(0xffffffffu, cid, cstep & 31);
+      const int64_t at = (static_cast<int64_t>(id) * a.Hkv + cg) * kI4Unit;
+      copy_block(ring + stage * kRingBlock, static_cast<const uint8_t*>(a.k_pool) + at,
+                 static_cast<const uint8_t*>(a.v_pool) + at, lane);
+      if (++cstep == csteps)
+        open_next();
+      else if ((cstep & 31) == 0)
+        cid = cstep + lane < csteps ? cids[W * (cstep + lane)] : 0;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  read_next(0);
+  open_next();
+#pragma unroll 1
+  for (int st = 0; st < kRing - 1; ++st) copy_next(st);
+  int stage = 0;
+
+  for (int wk = 0, w0 = nth_work(0); w0 < n_work; w0 = nth_work(++wk)) {
+  const int g = w0 % a.Hkv;
+  const I4Unit& un = a.units[a.unit0 + w0 / a.Hkv];
   const int n_keys = un.n_keys, n_steps = (n_keys + 15) >> 4;
   const int rows = un.rows, row0 = un.row0, q_first = un.q_first, branch = un.branch;
-
-  // lane l holds the block of the warp's step l of the current 32
-  int32_t id_reg = warp + W * lane < n_steps ? ids[warp + W * lane] : 0;
-  auto load_step = [&](int k) {  // the warp's k-th step
-    const int32_t id = __shfl_sync(0xffffffffu, id_reg, k & 31);
-    const int64_t at = (static_cast<int64_t>(id) * a.Hkv + g) * kI4Unit;
-    return load_block(static_cast<const uint8_t*>(a.k_pool) + at, static_cast<const uint8_t*>(a.v_pool) + at, key_a, i, c);
-  };
-  // the first block's bytes are on their way while Q is laid out
-  BlockRegs nx{};
-  if (warp < n_steps) nx = load_step(0);
 
   // Q^T fragments: row nt * 8 + i, dims 32 c .. 32 c + 31
   auto q_row = [&](int nt) -> const uint4* {
@@ -256,15 +345,13 @@ __global__ void __launch_bounds__(32 * W) decode_i4_kernel(const I4Args a) {
   };
 
 #pragma unroll 1
-  for (int step = warp, k = 0; step < n_steps; step += W, ++k) {
-    const BlockRegs b = nx;
-    if (step + W < n_steps) {
-      if (((k + 1) & 31) == 0) {
-        const int at = step + W + W * lane;
-        id_reg = at < n_steps ? ids[at] : 0;
-      }
-      nx = load_step(k + 1);
-    }
+  for (int step = warp; step < n_steps; step += W) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
+    __syncwarp();
+    const BlockRegs b = read_block(ring + stage * kRingBlock, key_a, i, c);
+    // into the stage that the step before this one has read
+    copy_next(stage == 0 ? kRing - 1 : stage - 1);
+    stage = stage + 1 == kRing ? 0 : stage + 1;
     float s[NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -511,6 +598,9 @@ __global__ void __launch_bounds__(32 * W) decode_i4_kernel(const I4Args a) {
       }
     }
   }
+  if (W > 1) __syncthreads();  // the exchange area is free for the next unit
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // Rows of branches whose partial results are many: one CTA a (token, head),
@@ -555,17 +645,18 @@ int launch_error(const char* what, std::string* err) {
 
 template <int NT, int W>
 int launch_units(I4Args a, int32_t unit0, int32_t n, cudaStream_t s, std::string* err) {
-  const int bytes = W > 1 ? sizeof(Smem<NT, W>) : NT > 2 ? NT * 4 * 32 * 16 : 0;
-  if (bytes > 48 * 1024) {
-    // per device, so set at each launch (a host call of well under a microsecond)
-    const cudaError_t e = cudaFuncSetAttribute(decode_i4_kernel<NT, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) {
-      *err = std::string("cudaFuncSetAttribute: ") + cudaGetErrorString(e);
-      return PADOC_ERR_CUDA;
-    }
+  const int bytes = sizeof(Smem<NT, W>);
+  int per_sm = 0;
+  // per device, so asked at each launch (host calls of about a microsecond)
+  cudaError_t e = cudaFuncSetAttribute(decode_i4_kernel<NT, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, decode_i4_kernel<NT, W>, 32 * W, bytes);
+  if (e != cudaSuccess || per_sm < 1) {
+    *err = std::string("i4 decode occupancy: ") + cudaGetErrorString(e);
+    return PADOC_ERR_CUDA;
   }
   a.unit0 = unit0;
-  decode_i4_kernel<NT, W><<<static_cast<unsigned>(n) * a.Hkv, 32 * W, bytes, s>>>(a);
+  const int n_work = n * a.Hkv;
+  decode_i4_kernel<NT, W><<<std::min(n_work, per_sm * num_sms()), 32 * W, bytes, s>>>(a, n_work);
   return launch_error("i4 decode launch", err);
 }
 

@@ -1410,10 +1410,18 @@ struct DecodePlan {
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // Units with at most 8, 16 and 32 rows, in this order; first[] are their bounds in `all`.
+// Within each the longest come first (a counting sort by blocks of keys): the
+// kernel deals them out back and forth.
 void add_units(const std::vector<I4Unit> (&by_rows)[3], std::vector<I4Unit>* all, int32_t (&first)[4]) {
   for (int i = 0; i < 3; ++i) {
     first[i] = static_cast<int32_t>(all->size());
-    all->insert(all->end(), by_rows[i].begin(), by_rows[i].end());
+    int32_t most = 0;
+    for (const I4Unit& u : by_rows[i]) most = std::max(most, (u.n_keys + 15) / 16);
+    std::vector<int32_t> at(static_cast<size_t>(most) + 2, 0);
+    for (const I4Unit& u : by_rows[i]) ++at[most - (u.n_keys + 15) / 16 + 1];
+    for (int32_t k = 0; k <= most; ++k) at[k + 1] += at[k];
+    all->resize(first[i] + by_rows[i].size());
+    for (const I4Unit& u : by_rows[i]) (*all)[first[i] + at[most - (u.n_keys + 15) / 16]++] = u;
   }
   first[3] = static_cast<int32_t>(all->size());
 }
