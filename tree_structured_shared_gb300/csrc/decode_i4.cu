@@ -91,24 +91,37 @@ constexpr int kRingKS = 4 * 288, kRingV = kRingKS + 128, kRingVS = kRingV + 1024
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-// Starts the copy of a block's 144 16-byte pieces (72 of K, then 72 of V).
-__device__ __forceinline__ void copy_block(uint32_t dst, const uint8_t* kp, const uint8_t* vp, int lane) {
-  const int k2 = 64 + lane;  // the third round: the last pieces of K, the first of V
-  copy16(dst + lane * 16 + (lane >> 4) * 32, kp + lane * 16);
-  copy16(dst + 512 + 64 + lane * 16 + (lane >> 4) * 32, kp + 512 + lane * 16);
-  {
-    const int v = k2 - 72;
-    const uint32_t d = lane < 8 ? kRingKS + lane * 16 : kRingV + ((v * 16) ^ (((v >> 3) & 1) << 4));
-    copy16(dst + d, lane < 8 ? kp + k2 * 16 : vp + v * 16);
-  }
-  {
-    const int v = lane + 24;
-    copy16(dst + kRingV + ((v * 16) ^ (((v >> 3) & 1) << 4)), vp + v * 16);
-  }
-  if (lane < 16) {
-    const int v = lane + 56;
-    copy16(dst + kRingV + (v < 64 ? (v * 16) ^ (((v >> 3) & 1) << 4) : v * 16), vp + v * 16);
-  }
+// A lane's share of a block's 144 16-byte pieces (72 of K, then 72 of V): pieces
+// lane, 32 + lane of K; a third that is K's for lanes 0-7, V's for the rest; and
+// two of V.  What depends on the lane alone is kept: three source addresses of the
+// unit's kv head, four offsets within a stage.
+struct CopyLane {
+  const uint8_t *k, *m, *v;
+  uint32_t dk, dm, dv, dw;
+};
+__device__ __forceinline__ CopyLane copy_lane(int lane) {
+  auto v_at = [](int p) { return static_cast<uint32_t>(kRingV + (p < 64 ? (p * 16) ^ (((p >> 3) & 1) << 4) : p * 16)); };
+  CopyLane l;
+  l.dk = lane * 16 + (lane >> 4) * 32;
+  l.dm = lane < 8 ? kRingKS + lane * 16 : v_at(lane - 8);
+  l.dv = v_at(lane + 24);
+  l.dw = v_at(lane + 56);
+  return l;
+}
+__device__ __forceinline__ void copy_unit(CopyLane& l, const void* k_pool, const void* v_pool, int g, int lane) {
+  const uint8_t* k = static_cast<const uint8_t*>(k_pool) + g * kI4Unit;
+  const uint8_t* v = static_cast<const uint8_t*>(v_pool) + g * kI4Unit;
+  l.k = k + lane * 16;
+  l.m = lane < 8 ? k + (64 + lane) * 16 : v + (lane - 8) * 16;
+  l.v = v + (24 + lane) * 16;
+}
+// Starts the copy of a block (at = its number * the pool's block stride).
+__device__ __forceinline__ void copy_block(const CopyLane& l, uint32_t dst, int64_t at, int lane) {
+  copy16(dst + l.dk, l.k + at);
+  copy16(dst + l.dk + 576, l.k + at + 512);
+  copy16(dst + l.dm, l.m + at);
+  copy16(dst + l.dv, l.v + at);
+  if (lane < 16) copy16(dst + l.dw, l.v + at + 512);
 }
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 v;
@@ -174,7 +187,9 @@ __global__ void __launch_bounds__(32 * W, NT == 1 ? 18 / W : 1) decode_i4_kernel
   // number, its step, its ids (lane l: step l of the current 32), and the next
   // unit's record and first ids, read while this one's blocks are copied.
   const uint32_t ring = smem_u32(&sm.ring[warp][0]);
-  int ck = 0, cstep = 0, csteps = 0, cid = 0, cg = 0;
+  int ck = 0, cstep = 0, csteps = 0, cid = 0;
+  CopyLane cl = copy_lane(lane);
+  const int64_t block_stride = static_cast<int64_t>(a.Hkv) * kI4Unit;
   const int32_t* cids = nullptr;
   int nsteps = 0, nid = 0;
   const int32_t* nids = nullptr;
@@ -196,17 +211,14 @@ __global__ void __launch_bounds__(32 * W, NT == 1 ? 18 / W : 1) decode_i4_kernel
       cstep = 0;
       const int w = nth_work(ck);
       if (w >= n_work) return;
-      cg = w % a.Hkv;
+      copy_unit(cl, a.k_pool, a.v_pool, w % a.Hkv, lane);
       ++ck;
       read_next(ck);
     } while (csteps == 0);
   };
-  auto copy_next = [&](int stage) {
+  auto copy_next = [&](uint32_t dst) {
     if (cstep < csteps) {
-      const int32_t id = __shfl_sync(0xffffffffu, cid, cstep & 31);
-      const int64_t at = (static_cast<int64_t>(id) * a.Hkv + cg) * kI4Unit;
-      copy_block(ring + stage * kRingBlock, static_cast<const uint8_t*>(a.k_pool) + at,
-                 static_cast<const uint8_t*>(a.v_pool) + at, lane);
+      copy_block(cl, dst, __shfl_sync(0xffffffffu, cid, cstep & 31) * block_stride, lane);
       if (++cstep == csteps)
         open_next();
       else if ((cstep & 31) == 0)
@@ -217,8 +229,8 @@ __global__ void __launch_bounds__(32 * W, NT == 1 ? 18 / W : 1) decode_i4_kernel
   read_next(0);
   open_next();
 #pragma unroll 1
-  for (int st = 0; st < kRing - 1; ++st) copy_next(st);
-  int stage = 0;
+  for (int st = 0; st < kRing - 1; ++st) copy_next(ring + st * kRingBlock);
+  uint32_t stage = ring, freed = ring + (kRing - 1) * kRingBlock;
 
   for (int wk = 0, w0 = nth_work(0); w0 < n_work; w0 = nth_work(++wk)) {
   const int g = w0 % a.Hkv;
@@ -348,10 +360,10 @@ __global__ void __launch_bounds__(32 * W, NT == 1 ? 18 / W : 1) decode_i4_kernel
   for (int step = warp; step < n_steps; step += W) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
     __syncwarp();
-    const BlockRegs b = read_block(ring + stage * kRingBlock, key_a, i, c);
-    // into the stage that the step before this one has read
-    copy_next(stage == 0 ? kRing - 1 : stage - 1);
-    stage = stage + 1 == kRing ? 0 : stage + 1;
+    const BlockRegs b = read_block(stage, key_a, i, c);
+    copy_next(freed);  // the stage that the step before this one has read
+    freed = stage;
+    stage = stage == ring + (kRing - 1) * kRingBlock ? ring : stage + kRingBlock;
     float s[NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)

@@ -82,11 +82,18 @@ template <int B>
 __device__ __forceinline__ I4Scale i4_scale_two(uint32_t x) {
   return i4_scale(__byte_perm(x, 0u, 0x4040u | B | ((B + 1) << 8)));
 }
+// (x & mask) | bits in one instruction.
+__device__ __forceinline__ uint32_t mask_or(uint32_t x, uint32_t mask, uint32_t bits) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(x), "r"(mask), "r"(bits));
+  return d;
+}
 // n s' of nibbles J and 4 + J of w in the halves of a register, v = w >> 8.
 template <int J>
 __device__ __forceinline__ uint32_t i4_pair(uint32_t w, uint32_t v, const I4Scale& s) {
   const uint32_t x = J < 2 ? w : v;
-  return (J & 1) ? h2_fma((x & 0x00F000F0u) | 0x54005400u, s.s, s.hi) : h2_fma((x & 0x000F000Fu) | 0x64006400u, s.s, s.lo);
+  return (J & 1) ? h2_fma(mask_or(x, 0x00F000F0u, 0x54005400u), s.s, s.hi)
+                 : h2_fma(mask_or(x, 0x000F000Fu, 0x64006400u), s.s, s.lo);
 }
 
 }  // namespace padoc
