@@ -72,9 +72,11 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 // One 16-token block of a kv head as a lane holds it.
-struct BlockRegs {
+struct KRegs {
   uint4 ka, kb;      // chunk c of the keys 4 (i / 2) + i % 2 and + 2
   uint32_t sa, sb;   // their scales of groups 2c, 2c + 1
+};
+struct VRegs {
   uint4 v0, v1;      // group i of the keys 4c, 4c + 1 and 4c + 2, 4c + 3
   uint32_t sv;       // the four keys' scales of group i
 };
@@ -83,9 +85,7 @@ struct BlockRegs {
 // 256-byte chunks, K scales, V codes with the halves of the odd groups' 32-byte
 // pieces swapped, V scales.  Eight neighbouring lanes of a 16-byte read then
 // touch every bank once.
-// Blocks of a warp's ring; all but one are on their way while one is worked on.
-// Large units of four warps keep three, so that two CTAs fit an SM.
-__host__ __device__ constexpr int ring_of(int NT, int W) { return NT * W >= 16 ? 3 : 4; }
+constexpr int kRing = 4;  // blocks of a warp's ring: a pair is worked on, a pair is on its way
 constexpr int kRingKS = 4 * 288, kRingV = kRingKS + 128, kRingVS = kRingV + 1024, kRingBlock = kRingVS + 128;
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
@@ -138,12 +138,16 @@ __device__ __forceinline__ uint32_t lds16(uint32_t addr) {
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
   return v;
 }
-__device__ __forceinline__ BlockRegs read_block(uint32_t src, int key_a, int i, int c) {
-  BlockRegs b;
+__device__ __forceinline__ KRegs read_k(uint32_t src, int key_a, int c) {
+  KRegs b;
   b.ka = lds128(src + c * 288 + key_a * 16);
   b.kb = lds128(src + c * 288 + key_a * 16 + 32);
   b.sa = lds16(src + kRingKS + key_a * 8 + 2 * c);
   b.sb = lds16(src + kRingKS + key_a * 8 + 16 + 2 * c);
+  return b;
+}
+__device__ __forceinline__ VRegs read_v(uint32_t src, int i, int c) {
+  VRegs b;
   const uint32_t v = src + kRingV + i * 128 + c * 32 + ((i & 1) << 4);
   b.v0 = lds128(v);
   b.v1 = lds128(v ^ 16);
@@ -155,16 +159,21 @@ __device__ __forceinline__ BlockRegs read_block(uint32_t src, int key_a, int i, 
 // (8 float4) and, of its two rows, the reference and the sum.
 template <int NT, int W>
 struct Smem {
-  uint4 ring[W][ring_of(NT, W) * kRingBlock / 16];
+  uint4 ring[W][kRing * kRingBlock / 16];
   float4 o[W][NT][8][32];
   float4 ml[W][NT][32];
   uint4 q[NT > 2 ? NT : 1][NT > 2 ? 4 : 1][32];  // Q fragments of large units
 };
 template <int NT>
 struct Smem<NT, 1> {
-  uint4 ring[1][ring_of(NT, 1) * kRingBlock / 16];
+  uint4 ring[1][kRing * kRingBlock / 16];
   uint4 q[NT > 2 ? NT : 1][NT > 2 ? 4 : 1][32];
 };
+
+// x / G for x below 2^29 (g_inv = 2^32 / G rounded up; 0 for G = 1).
+__device__ __forceinline__ int div_g(int x, uint32_t g_inv) {
+  return g_inv ? static_cast<int>(__umulhi(static_cast<uint32_t>(x), g_inv)) : x;
+}
 
 // A persistent CTA's k-th unit: units come longest first and are dealt back and
 // forth, so that every CTA gets about the same number of keys.
@@ -173,17 +182,16 @@ __device__ __forceinline__ int nth_work(int k) {
 }
 
 template <int NT, int W>
-__global__ void __launch_bounds__(32 * W, NT == 1 ? 18 / W : 1) decode_i4_kernel(const I4Args a, const int n_work) {
+__global__ void __launch_bounds__(32 * W, NT == 1 ? 16 / W : 1) decode_i4_kernel(const I4Args a, const int n_work) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   Smem<NT, W>& sm = *reinterpret_cast<Smem<NT, W>*>(smem_raw);
   constexpr bool kQInSmem = NT > 2;
-  constexpr int kRing = ring_of(NT, W);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int i = lane >> 2, c = lane & 3;
   const int G = a.group;
   const int key_a = 4 * (i >> 1) + (i & 1);
 
-  // The copies' own walk over the warp's blocks, kRing - 1 ahead of the work: unit
+  // The copies' own walk over the warp's blocks, a pair ahead of the work: unit
   // number, its step, its ids (lane l: step l of the current 32), and the next
   // unit's record and first ids, read while this one's blocks are copied.
   const uint32_t ring = smem_u32(&sm.ring[warp][0]);
@@ -216,10 +224,13 @@ __global__ void __launch_bounds__(32 * W, NT == 1 ? 18 / W : 1) decode_i4_kernel
       read_next(ck);
     } while (csteps == 0);
   };
-  auto copy_next = [&](uint32_t dst) {
+  auto copy_pair = [&](uint32_t dst) {
     if (cstep < csteps) {
       copy_block(cl, dst, __shfl_sync(0xffffffffu, cid, cstep & 31) * block_stride, lane);
-      if (++cstep == csteps)
+      if (cstep + 1 < csteps)
+        copy_block(cl, dst + kRingBlock, __shfl_sync(0xffffffffu, cid, (cstep & 31) + 1) * block_stride, lane);
+      cstep += 2;
+      if (cstep >= csteps)
         open_next();
       else if ((cstep & 31) == 0)
         cid = cstep + lane < csteps ? cids[W * (cstep + lane)] : 0;
@@ -228,9 +239,9 @@ __global__ void __launch_bounds__(32 * W, NT == 1 ? 18 / W : 1) decode_i4_kernel
   };
   read_next(0);
   open_next();
-#pragma unroll 1
-  for (int st = 0; st < kRing - 1; ++st) copy_next(ring + st * kRingBlock);
-  uint32_t stage = ring, freed = ring + (kRing - 1) * kRingBlock;
+  copy_pair(ring);
+  copy_pair(ring + 2 * kRingBlock);
+  uint32_t stage = ring;
 
   for (int wk = 0, w0 = nth_work(0); w0 < n_work; w0 = nth_work(++wk)) {
   const int g = w0 % a.Hkv;
@@ -240,17 +251,14 @@ __global__ void __launch_bounds__(32 * W, NT == 1 ? 18 / W : 1) decode_i4_kernel
 
   // Q^T fragments: row nt * 8 + i, dims 32 c .. 32 c + 31
   auto q_row = [&](int nt) -> const uint4* {
-    const int R = row0 + nt * 8 + i;
+    const int R = row0 + nt * 8 + i, t = div_g(R, a.g_inv);
     return reinterpret_cast<const uint4*>(
-        nt * 8 + i < rows ? a.q + (static_cast<int64_t>(q_first + R / G) * a.Hq + g * G + R % G) * kHeadDim + 32 * c : nullptr);
+        nt * 8 + i < rows ? a.q + (static_cast<int64_t>(q_first + t) * a.Hq + g * G + R - t * G) * kHeadDim + 32 * c : nullptr);
   };
   uint32_t q[kQInSmem ? 1 : NT][16];
-  float amax = 0.f;
-  auto most = [&](uint32_t v) {
-    const float lo = fabsf(__uint_as_float(v << 16)), hi = fabsf(__uint_as_float(v & 0xffff0000u));
-    amax = fmaxf(amax, lo <= 3.4028235e38f ? lo : 0.f);
-    amax = fmaxf(amax, hi <= 3.4028235e38f ? hi : 0.f);
-  };
+  // the largest magnitude as its bf16 bits, which order as the magnitudes do
+  uint32_t most2 = 0;
+  auto most = [&](uint32_t v) { most2 = __vmaxu2(most2, v & 0x7fff7fffu); };
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const uint4* p = q_row(nt);
@@ -269,8 +277,22 @@ __global__ void __launch_bounds__(32 * W, NT == 1 ? 18 / W : 1) decode_i4_kernel
       }
     }
   }
-#pragma unroll
-  for (int s = 16; s; s >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, s));
+  uint32_t mx = __reduce_max_sync(0xffffffffu, max(most2 & 0xffffu, most2 >> 16));
+  if (mx >= 0x7f80u) {
+    // an infinity or a NaN: the largest finite one sets the factor
+    uint32_t m = 0;
+    for (int nt = 0; nt < NT; ++nt) {
+      const uint4* p = q_row(nt);
+      if (p)
+        for (int x = 0; x < 16; ++x) {
+          const uint32_t v = reinterpret_cast<const uint32_t*>(p)[x];
+          const uint32_t lo = v & 0x7fffu, hi = (v >> 16) & 0x7fffu;
+          m = max(m, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+        }
+    }
+    mx = __reduce_max_sync(0xffffffffu, m);
+  }
+  const float amax = __uint_as_float(mx << 16);
   const int kexp = amax > 0.f ? min(100, 14 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127)) : 0;
   const float qf = __uint_as_float(static_cast<uint32_t>(127 + kexp) << 23);
   const float sl2q = a.sl2 * kI4Unscale * __uint_as_float(static_cast<uint32_t>(127 - kexp) << 23);
@@ -310,7 +332,7 @@ __global__ void __launch_bounds__(32 * W, NT == 1 ? 18 / W : 1) decode_i4_kernel
   }
   // keys a row of a page's prefix may see; a branch's own keys are seen by all its rows
   auto limit_of = [&](int r) {
-    return branch < 0 && r < rows ? min(n_keys, a.q_plen[q_first + (row0 + r) / G] - un.key0) : n_keys;
+    return branch < 0 && r < rows ? min(n_keys, a.q_plen[q_first + div_g(row0 + r, a.g_inv)] - un.key0) : n_keys;
   };
   int lim_min = n_keys;
   if (branch < 0) {
@@ -318,20 +340,25 @@ __global__ void __launch_bounds__(32 * W, NT == 1 ? 18 / W : 1) decode_i4_kernel
     lim_min = __reduce_min_sync(0xffffffffu, lim_min);
   }
 
-  // P of one tile of scores (log2 units) against the running references, which
+  // P of H tiles of scores (log2 units) against the running references, which
   // move first where a score exceeds them by more than kPSlack
-  auto softmax = [&](float (&s)[NT][4]) {
+  auto softmax = [&](auto& s) {
+    constexpr int H = sizeof(s) / sizeof(s[0]);
     float most = -INFINITY;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-      most = max3f(most, fmaxf(s[nt][0], s[nt][2]) - mo[nt][0], fmaxf(s[nt][1], s[nt][3]) - mo[nt][1]);
+    for (int h = 0; h < H; ++h)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        most = max3f(most, fmaxf(s[h][nt][0], s[h][nt][2]) - mo[nt][0], fmaxf(s[h][nt][1], s[h][nt][3]) - mo[nt][1]);
     if (__any_sync(0xffffffffu, most > kPShift + kPSlack)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float al[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float t = fmaxf(s[nt][e], s[nt][2 + e]);
+          float t = fmaxf(s[0][nt][e], s[0][nt][2 + e]);
+#pragma unroll
+          for (int h = 1; h < H; ++h) t = max3f(t, s[h][nt][e], s[h][nt][2 + e]);
 #pragma unroll
           for (int k = 4; k < 32; k <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, k));
           al[e] = 1.f;
@@ -348,69 +375,49 @@ __global__ void __launch_bounds__(32 * W, NT == 1 ? 18 / W : 1) decode_i4_kernel
       }
     }
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int h = 0; h < H; ++h)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        s[nt][e] = fast_exp2(s[nt][e] - mo[nt][e & 1]);
-        l[nt][e & 1] += s[nt][e];
-      }
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[h][nt][e] = fast_exp2(s[h][nt][e] - mo[nt][e & 1]);
+          l[nt][e & 1] += s[h][nt][e];
+        }
   };
-
-#pragma unroll 1
-  for (int step = warp; step < n_steps; step += W) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
-    __syncwarp();
-    const BlockRegs b = read_block(stage, key_a, i, c);
-    copy_next(freed);  // the stage that the step before this one has read
-    freed = stage;
-    stage = stage == ring + (kRing - 1) * kRingBlock ? ring : stage + kRingBlock;
-    float s[NT][4];
+  // S^T of a block, and O^T += V^T P^T of one
+  auto scores = [&](uint32_t src, float (&s)[NT][4]) {
+    const KRegs b = read_k(src, key_a, c);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
-    {
-      const I4Scale sa0 = i4_scale_both<0>(b.sa), sa1 = i4_scale_both<1>(b.sa);
-      const I4Scale sb0 = i4_scale_both<0>(b.sb), sb1 = i4_scale_both<1>(b.sb);
-      const uint32_t wa[4] = {b.ka.x, b.ka.y, b.ka.z, b.ka.w}, wb[4] = {b.kb.x, b.kb.y, b.kb.z, b.kb.w};
+    const I4Scale sa0 = i4_scale_both<0>(b.sa), sa1 = i4_scale_both<1>(b.sa);
+    const I4Scale sb0 = i4_scale_both<0>(b.sb), sb1 = i4_scale_both<1>(b.sb);
+    const uint32_t wa[4] = {b.ka.x, b.ka.y, b.ka.z, b.ka.w}, wb[4] = {b.kb.x, b.kb.y, b.kb.z, b.kb.w};
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        // words 0, 1 of the chunk are its first group, 2, 3 its second
-        const I4Scale &sa = w < 2 ? sa0 : sa1, &sb = w < 2 ? sb0 : sb1;
-        const uint32_t va = wa[w] >> 8, vb = wb[w] >> 8;
-        const uint32_t f0[4] = {i4_pair<0>(wa[w], va, sa), i4_pair<0>(wb[w], vb, sb), i4_pair<1>(wa[w], va, sa),
-                                i4_pair<1>(wb[w], vb, sb)};
-        const uint32_t f1[4] = {i4_pair<2>(wa[w], va, sa), i4_pair<2>(wb[w], vb, sb), i4_pair<3>(wa[w], va, sa),
-                                i4_pair<3>(wb[w], vb, sb)};
+    for (int w = 0; w < 4; ++w) {
+      // words 0, 1 of the chunk are its first group, 2, 3 its second
+      const I4Scale &sa = w < 2 ? sa0 : sa1, &sb = w < 2 ? sb0 : sb1;
+      const uint32_t va = wa[w] >> 8, vb = wb[w] >> 8;
+      const uint32_t f0[4] = {i4_pair<0>(wa[w], va, sa), i4_pair<0>(wb[w], vb, sb), i4_pair<1>(wa[w], va, sa),
+                              i4_pair<1>(wb[w], vb, sb)};
+      const uint32_t f1[4] = {i4_pair<2>(wa[w], va, sa), i4_pair<2>(wb[w], vb, sb), i4_pair<3>(wa[w], va, sa),
+                              i4_pair<3>(wb[w], vb, sb)};
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          if constexpr (kQInSmem) {
-            const uint4 qv = sm.q[nt][w][lane];
-            mma_f16(s[nt], f0, qv.x, qv.y);
-            mma_f16(s[nt], f1, qv.z, qv.w);
-          } else {
-            mma_f16(s[nt], f0, q[nt][4 * w], q[nt][4 * w + 1]);
-            mma_f16(s[nt], f1, q[nt][4 * w + 2], q[nt][4 * w + 3]);
-          }
+      for (int nt = 0; nt < NT; ++nt) {
+        if constexpr (kQInSmem) {
+          const uint4 qv = sm.q[nt][w][lane];
+          mma_f16(s[nt], f0, qv.x, qv.y);
+          mma_f16(s[nt], f1, qv.z, qv.w);
+        } else {
+          mma_f16(s[nt], f0, q[nt][4 * w], q[nt][4 * w + 1]);
+          mma_f16(s[nt], f1, q[nt][4 * w + 2], q[nt][4 * w + 3]);
         }
       }
     }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[nt][e] *= sl2q;
-    if (step * 16 + 16 > lim_min) {
-      const int key0 = step * 16 + key_a;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int lim = limit_of(nt * 8 + 2 * c + e);
-          if (key0 >= lim) s[nt][e] = -INFINITY;
-          if (key0 + 2 >= lim) s[nt][2 + e] = -INFINITY;
-        }
-    }
-    softmax(s);
+  };
+  auto add_values = [&](uint32_t src, const float (&s)[NT][4]) {
+    const VRegs b = read_v(src, i, c);
     uint32_t p[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -436,13 +443,55 @@ __global__ void __launch_bounds__(32 * W, NT == 1 ? 18 / W : 1) decode_i4_kernel
       pv(4 * w + 2, i4_pair<2>(e01, e01v, s01), i4_pair<2>(d01, d01v, s01), i4_pair<2>(e23, e23v, s23), i4_pair<2>(d23, d23v, s23));
       pv(4 * w + 3, i4_pair<3>(e01, e01v, s01), i4_pair<3>(d01, d01v, s01), i4_pair<3>(e23, e23v, s23), i4_pair<3>(d23, d23v, s23));
     }
+  };
+
+#pragma unroll 1
+  for (int step = warp; step < n_steps; step += 2 * W) {
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    __syncwarp();
+    const bool two = step + W < n_steps;  // an odd count's last pair has one block
+    float s[2][NT][4];
+    scores(stage, s[0]);
+    if (two) {
+      scores(stage + kRingBlock, s[1]);
+    } else {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[1][nt][e] = -INFINITY;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[h][nt][e] *= sl2q;
+    if ((step + W) * 16 + 16 > lim_min) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int lim = limit_of(nt * 8 + 2 * c + e), key0 = (step + h * W) * 16 + key_a;
+            if (key0 >= lim) s[h][nt][e] = -INFINITY;
+            if (key0 + 2 >= lim) s[h][nt][2 + e] = -INFINITY;
+          }
+    }
+    softmax(s);
+    add_values(stage, s[0]);
+    if (two) add_values(stage + kRingBlock, s[1]);
+    __syncwarp();
+    copy_pair(stage);
+    stage = stage == ring ? ring + 2 * kRingBlock : ring;
   }
 
   // ---------------------------------------------------------------- query block
   // scores of all 16 keys by every warp; warp w then takes the keys j % W == w
   const int q_len = un.q_len;
   if (q_len > 0) {
-    float s[NT][4];
+    float s1[1][NT][4];
+    auto& s = s1[0];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -473,7 +522,7 @@ __global__ void __launch_bounds__(32 * W, NT == 1 ? 18 / W : 1) decode_i4_kernel
         const int r = nt * 8 + 2 * c + e;
         uint32_t bits = 0;
         if (r < rows) {
-          const int qi = (row0 + r) / G;
+          const int qi = div_g(row0 + r, a.g_inv);
           bits = a.tree_bits ? static_cast<uint32_t>(a.tree_bits[un.qb_first + qi]) : (2u << qi) - 1u;
         }
         vis[nt][e] = bits & ((1u << q_len) - 1u) & (kMine << warp);
@@ -483,7 +532,7 @@ __global__ void __launch_bounds__(32 * W, NT == 1 ? 18 / W : 1) decode_i4_kernel
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         s[nt][e] = ((vis[nt][e & 1] >> (key_a + (e >> 1) * 2)) & 1u) ? s[nt][e] * a.sl2 : -INFINITY;
-    softmax(s);
+    softmax(s1);
     const __nv_bfloat16* vn = a.v_new + at + 16 * i;
 #pragma unroll 1
     for (int j = warp; j < q_len; j += W) {
@@ -562,8 +611,8 @@ __global__ void __launch_bounds__(32 * W, NT == 1 ? 18 / W : 1) decode_i4_kernel
     for (int e = 0; e < 2; ++e) {
       const int r = nt * 8 + 2 * c + e;
       if (r >= rows) continue;
-      const int R = row0 + r;
-      const int64_t qh = static_cast<int64_t>(R / G) * a.Hq + g * G + R % G;  // (token, head) from q_first
+      const int R = row0 + r, t = div_g(R, a.g_inv);
+      const int64_t qh = static_cast<int64_t>(t) * a.Hq + g * G + R - t * G;  // (token, head) from q_first
       float M = mo[nt][e], L = l[nt][e];
       float acc[16];
 #pragma unroll

@@ -1889,6 +1889,7 @@ static I4Args i4_args(const padoc_decode_plan* plan, const void* q, const void* 
   a.Hq = plan->Hq;
   a.Hkv = pool->Hkv;
   a.group = plan->Hq / pool->Hkv;
+  a.g_inv = a.group > 1 ? static_cast<uint32_t>(((uint64_t(1) << 32) + a.group - 1) / a.group) : 0;
   a.sl2 = (scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(pool->d))) * 1.44269504088896340736f;
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.k_new = static_cast<const __nv_bfloat16*>(k_new);

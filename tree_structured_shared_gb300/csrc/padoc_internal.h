@@ -173,7 +173,8 @@ struct I4Args {
   const int32_t* table;
   int32_t max_bps, unit0;
   int32_t Hq, Hkv, group;
-  float sl2;  // scale * log2(e)
+  uint32_t g_inv;  // 2^32 / group rounded up, 0 when group is 1
+  float sl2;       // scale * log2(e)
   const __nv_bfloat16* q;
   const __nv_bfloat16* k_new;
   const __nv_bfloat16* v_new;
