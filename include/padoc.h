@@ -267,7 +267,7 @@ PADOC_API int padoc_kv_rows_free(padoc_kv_rows* rows);
 typedef struct {
   const float* cos_sin; /* device [n_pos, rot_dim], 16-byte aligned */
   int32_t n_pos;
-  int32_t rot_dim;      /* multiple of 16 in [0, d] */
+  int32_t rot_dim;      /* multiple of 32 in [0, d] */
   int32_t interleaved;
 } padoc_rope;
 

@@ -60,7 +60,8 @@ CASES = [
     (16, 8, 128, False, [1, 1, 1], [0, 5, 31]),
     (3, 1, 64, False, [2, 7, 40], [15, 0, 3]),
     (8, 2, 128, True, [17, 1, 3, 0, 16], [16, 0, 9, 4, 0]),
-    (0, 3, 16, True, [33], [1]),
+    (0, 3, 32, True, [33], [1]),
+    (4, 4, 32, False, [19], [2]),
     (5, 5, 96, False, [4, 2], [0, 14]),
     (2, 2, 0, False, [5, 20], [11, 0]),
 ]

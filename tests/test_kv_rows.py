@@ -69,7 +69,7 @@ def test_write_and_gather_refusals(pool):
     assert w(PTR, PTR, k_stride=255) == I and w(PTR, PTR, v_stride=260) == I
     assert w(PTR, PTR, q=PTR, Hq=4) == I and w(PTR, PTR, q_rot=PTR, Hq=4) == I and w(PTR, PTR, q=PTR, q_rot=PTR, Hq=0) == I
     assert w(PTR, PTR, q=PTR, q_rot=PTR, Hq=4, q_stride=504) == I
-    for rot, n_pos, tab in ((24, 99, PTR), (144, 99, PTR), (-16, 99, PTR), (128, 15, PTR), (128, 99, None), (128, 99, PTR + 4)):
+    for rot, n_pos, tab in ((24, 99, PTR), (48, 99, PTR), (144, 99, PTR), (-16, 99, PTR), (128, 15, PTR), (128, 99, None), (128, 99, PTR + 4)):
         assert w(PTR, PTR, rope=padoc.Rope(tab, rot, n_pos=n_pos)) == I
     assert code(rows.gather, None, PTR) == I and code(rows.gather, PTR, PTR + 8) == I
     empty = padoc.KVRows(pool, [s], [0], [0, 0])

@@ -1253,8 +1253,8 @@ static int check_step(const padoc_kv_pool* pool, const padoc_rope* rope, int32_t
       return fail(PADOC_ERR_INVALID, "%s: the q row stride must be a multiple of 8 of at least Hq * d", what);
   }
   if (!rope) return PADOC_OK;
-  if (rope->rot_dim < 0 || rope->rot_dim > pool->d || rope->rot_dim % 16)
-    return fail(PADOC_ERR_INVALID, "%s: rot_dim must be a multiple of 16 in [0, d]", what);
+  if (rope->rot_dim < 0 || rope->rot_dim > pool->d || rope->rot_dim % 32)
+    return fail(PADOC_ERR_INVALID, "%s: rot_dim must be a multiple of 32 in [0, d]", what);
   if (rope->rot_dim == 0) return PADOC_OK;
   if (!rope->cos_sin || !aligned16(rope->cos_sin))
     return fail(PADOC_ERR_INVALID, "%s: cos_sin must be a 16-byte aligned device pointer", what);
