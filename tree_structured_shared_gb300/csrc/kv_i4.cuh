@@ -27,6 +27,7 @@ namespace padoc {
 constexpr int kI4Unit = kI4UnitBytes;
 constexpr int kI4Scales = 1024;   // offset of its scales
 constexpr float kI4MaxScale = 896.f;
+constexpr uint32_t kI4MaxByte = 0xC6u;  // its byte
 constexpr uint32_t kI4Nan = 0xFFu;  // scale byte of a poisoned group (an fp16 NaN)
 
 // Scale byte of a group whose largest magnitude is 7 * a (a >= 0, finite): a rounded to
@@ -37,6 +38,15 @@ __device__ __forceinline__ uint32_t i4_scale_byte(float a) {
   uint32_t b = __float_as_uint(a);
   b += 0x7FFFFu + ((b >> 20) & 1u);
   return (b >> 20) - (112u << 3);  // exponent bias 127 -> 15
+}
+// Whether a is in [2^-14, 896): a normal scale, and not held at the limit; and
+// such a scale itself, its byte in *byte.
+__device__ __forceinline__ bool i4_plain(float a) { return __float_as_uint(a) - 0x38800000u < 0x44600000u - 0x38800000u; }
+__device__ __forceinline__ float i4_plain_scale(float a, uint32_t* byte) {
+  uint32_t b = __float_as_uint(a);
+  b += 0x7FFFFu + ((b >> 20) & 1u);
+  *byte = (b >> 20) - (112u << 3);
+  return __uint_as_float(b & 0xFFF00000u);
 }
 __device__ __forceinline__ float i4_scale_value(uint32_t byte) {
   return __half2float(__ushort_as_half(static_cast<unsigned short>(byte << 7)));
