@@ -1,18 +1,21 @@
 // Branch decode / verify over a 4-bit pool, warp-level matrix instructions.
 //
-// A unit is one kv head, up to 8 NT query rows (tokens times the query heads of
-// the group, row R = token R / G, head R % G) and a run of cached keys: a chunk
-// of a page's shared prefix with the rows of all its branches (each prefix
-// token is read from HBM once a page), or a branch's own suffix with its own
-// rows and query block.  W warps share a unit and are a CTA: each takes every
-// W-th 16-token block with a running softmax of its own, and their results meet
-// in shared memory as register images (a warp's n-tile against the others').
-// One warp a unit costs least when there are units enough to fill the GPU.
+// A unit is one kv head, up to 8 query rows (tokens times the query heads of the
+// group, row R = token R / G, head R % G) and a run of cached keys: a chunk of a
+// page's shared prefix with rows of its branches, or a branch's own suffix with
+// its own rows and, once, the query block.  W warps share a unit and are a CTA:
+// each takes every W-th 16-token block with a running softmax of its own, and
+// the others' results reach the first as register images in shared memory.  One
+// warp a unit costs least where there are units enough to fill the GPU.
 //
 // Keys go on the matrix instruction's M side, so one query token (G <= 8 rows)
-// fills its N side and a key costs one instruction of each product a row tile:
+// fills its N side and a key costs one instruction of the two products together:
 //     S^T[key][row]  = K  Q^T   m16n8k16, M = 16 keys, K = 16 dims
 //     O^T[dim][row] += V^T P^T  m16n8k16, M = 16 dims, K = 16 keys
+// More rows are more units: tiles of 16 and 32 rows a warp decode a key for more
+// rows at once, but their 64 and 128 accumulators leave too few warps an SM
+// (verify's own pass on 64 pages: 341, 369 and 401 us with tiles of 8, 16, 32).
+//
 // Codes become fp16 operands in registers (n s is exact in fp16), never a
 // wider copy in memory.  Which dims and keys a lane holds is free as long as
 // both operands agree, so lane (i, c) = (lane / 4, lane % 4) reads chunk c of
@@ -155,19 +158,13 @@ __device__ __forceinline__ VRegs read_v(uint32_t src, int i, int c) {
   return b;
 }
 
-// What the warps of a unit exchange: per warp and row tile the lane's 32 sums of O
-// (8 float4) and, of its two rows, the reference and the sum.
-template <int NT, int W>
+template <int W>
 struct Smem {
   uint4 ring[W][kRing * kRingBlock / 16];
-  float4 o[W][NT][8][32];
-  float4 ml[W][NT][32];
-  uint4 q[NT > 2 ? NT : 1][NT > 2 ? 4 : 1][32];  // Q fragments of large units
-};
-template <int NT>
-struct Smem<NT, 1> {
-  uint4 ring[1][kRing * kRingBlock / 16];
-  uint4 q[NT > 2 ? NT : 1][NT > 2 ? 4 : 1][32];
+  // what warps 1 .. W - 1 leave for warp 0: the lane's 32 sums of O and, of its
+  // two rows, the reference and the sum
+  float4 o[W > 1 ? W - 1 : 1][W > 1 ? 8 : 1][32];
+  float4 ml[W > 1 ? W - 1 : 1][32];
 };
 
 // x / G for x below 2^29 (g_inv = 2^32 / G rounded up; 0 for G = 1).
@@ -181,11 +178,10 @@ __device__ __forceinline__ int nth_work(int k) {
   return k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
 }
 
-template <int NT, int W>
-__global__ void __launch_bounds__(32 * W, NT == 1 ? 16 / W : 1) decode_i4_kernel(const I4Args a, const int n_work) {
+template <int W>
+__global__ void __launch_bounds__(32 * W, 16 / W) decode_i4_kernel(const I4Args a, const int n_work) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  Smem<NT, W>& sm = *reinterpret_cast<Smem<NT, W>*>(smem_raw);
-  constexpr bool kQInSmem = NT > 2;
+  Smem<W>& sm = *reinterpret_cast<Smem<W>*>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int i = lane >> 2, c = lane & 3;
   const int G = a.group;
@@ -244,457 +240,414 @@ __global__ void __launch_bounds__(32 * W, NT == 1 ? 16 / W : 1) decode_i4_kernel
   uint32_t stage = ring;
 
   for (int wk = 0, w0 = nth_work(0); w0 < n_work; w0 = nth_work(++wk)) {
-  const int g = w0 % a.Hkv;
-  const I4Unit& un = a.units[a.unit0 + w0 / a.Hkv];
-  const int n_keys = un.n_keys, n_steps = (n_keys + 15) >> 4;
-  const int rows = un.rows, row0 = un.row0, q_first = un.q_first, branch = un.branch;
+    const int g = w0 % a.Hkv;
+    const I4Unit& un = a.units[a.unit0 + w0 / a.Hkv];
+    const int n_keys = un.n_keys, n_steps = (n_keys + 15) >> 4;
+    const int rows = un.rows, row0 = un.row0, q_first = un.q_first, branch = un.branch;
 
-  // Q^T fragments: row nt * 8 + i, dims 32 c .. 32 c + 31
-  auto q_row = [&](int nt) -> const uint4* {
-    const int R = row0 + nt * 8 + i, t = div_g(R, a.g_inv);
-    return reinterpret_cast<const uint4*>(
-        nt * 8 + i < rows ? a.q + (static_cast<int64_t>(q_first + t) * a.Hq + g * G + R - t * G) * kHeadDim + 32 * c : nullptr);
-  };
-  uint32_t q[kQInSmem ? 1 : NT][16];
-  // the largest magnitude as its bf16 bits, which order as the magnitudes do
-  uint32_t most2 = 0;
-  auto most = [&](uint32_t v) { most2 = __vmaxu2(most2, v & 0x7fff7fffu); };
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const uint4* p = q_row(nt);
+    // Q^T fragments: row i, dims 32 c .. 32 c + 31
+    const uint4* q_row = nullptr;
+    if (i < rows) {
+      const int t = div_g(row0 + i, a.g_inv);
+      q_row = reinterpret_cast<const uint4*>(
+          a.q + (static_cast<int64_t>(q_first + t) * a.Hq + g * G + row0 + i - t * G) * kHeadDim + 32 * c);
+    }
+    uint32_t q[16];
+    // the largest magnitude as its bf16 bits, which order as the magnitudes do
+    uint32_t most2 = 0;
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      const uint4 v = p ? p[x] : make_uint4(0, 0, 0, 0);
-      most(v.x);
-      most(v.y);
-      most(v.z);
-      most(v.w);
-      if (!kQInSmem) {
-        q[nt][4 * x] = v.x;
-        q[nt][4 * x + 1] = v.y;
-        q[nt][4 * x + 2] = v.z;
-        q[nt][4 * x + 3] = v.w;
+      const uint4 v = q_row ? q_row[x] : make_uint4(0, 0, 0, 0);
+      q[4 * x] = v.x;
+      q[4 * x + 1] = v.y;
+      q[4 * x + 2] = v.z;
+      q[4 * x + 3] = v.w;
+    }
+#pragma unroll
+    for (int x = 0; x < 16; ++x) most2 = __vmaxu2(most2, q[x] & 0x7fff7fffu);
+    uint32_t mx = __reduce_max_sync(0xffffffffu, max(most2 & 0xffffu, most2 >> 16));
+    if (mx >= 0x7f80u) {
+      // an infinity or a NaN: the largest finite one sets the factor
+      uint32_t m = 0;
+#pragma unroll
+      for (int x = 0; x < 16; ++x) {
+        const uint32_t lo = q[x] & 0x7fffu, hi = (q[x] >> 16) & 0x7fffu;
+        m = max(m, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
       }
+      mx = __reduce_max_sync(0xffffffffu, m);
     }
-  }
-  uint32_t mx = __reduce_max_sync(0xffffffffu, max(most2 & 0xffffu, most2 >> 16));
-  if (mx >= 0x7f80u) {
-    // an infinity or a NaN: the largest finite one sets the factor
-    uint32_t m = 0;
-    for (int nt = 0; nt < NT; ++nt) {
-      const uint4* p = q_row(nt);
-      if (p)
-        for (int x = 0; x < 16; ++x) {
-          const uint32_t v = reinterpret_cast<const uint32_t*>(p)[x];
-          const uint32_t lo = v & 0x7fffu, hi = (v >> 16) & 0x7fffu;
-          m = max(m, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
-        }
-    }
-    mx = __reduce_max_sync(0xffffffffu, m);
-  }
-  const float amax = __uint_as_float(mx << 16);
-  const int kexp = amax > 0.f ? min(100, 14 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127)) : 0;
-  const float qf = __uint_as_float(static_cast<uint32_t>(127 + kexp) << 23);
-  const float sl2q = a.sl2 * kI4Unscale * __uint_as_float(static_cast<uint32_t>(127 - kexp) << 23);
-  auto half2 = [&](uint32_t v) { return pack_f16x2(__uint_as_float(v << 16) * qf, __uint_as_float(v & 0xffff0000u) * qf); };
-  if constexpr (kQInSmem) {
-#pragma unroll 1
-    for (int nt = warp; nt < NT; nt += W) {
-      const uint4* p = q_row(nt);
+    const int kexp = mx ? min(100, 14 - (static_cast<int>(mx >> 7) - 127)) : 0;
+    const float qf = __uint_as_float(static_cast<uint32_t>(127 + kexp) << 23);
+    const float sl2q = a.sl2 * kI4Unscale * __uint_as_float(static_cast<uint32_t>(127 - kexp) << 23);
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const uint4 v = p ? p[x] : make_uint4(0, 0, 0, 0);
-        sm.q[nt][x][lane] = make_uint4(half2(v.x), half2(v.y), half2(v.z), half2(v.w));
-      }
-    }
-    __syncthreads();
-  } else {
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int x = 0; x < 16; ++x) q[nt][x] = half2(q[nt][x]);
-  }
+    for (int x = 0; x < 16; ++x)
+      q[x] = pack_f16x2(__uint_as_float(q[x] << 16) * qf, __uint_as_float(q[x] & 0xffff0000u) * qf);
 
-  // rows 2c, 2c + 1 of each tile: running reference (log2, less kPShift), sums
-  float mo[NT][2], l[NT][2];
-  float o[NT][8][4];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      mo[nt][e] = kNoMax;
-      l[nt][e] = 0.f;
-    }
+    // rows 2c, 2c + 1: running reference (log2, less kPShift), sums, O of dims 16 i + 2 x + {0, 1}
+    float mo[2] = {kNoMax, kNoMax}, l[2] = {0.f, 0.f};
+    float o[8][4];
 #pragma unroll
     for (int x = 0; x < 8; ++x)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[nt][x][e] = 0.f;
-  }
-  // keys a row of a page's prefix may see; a branch's own keys are seen by all its rows
-  auto limit_of = [&](int r) {
-    return branch < 0 && r < rows ? min(n_keys, a.q_plen[q_first + div_g(row0 + r, a.g_inv)] - un.key0) : n_keys;
-  };
-  int lim_min = n_keys;
-  if (branch < 0) {
-    if (lane < 8 * NT) lim_min = limit_of(lane);
-    lim_min = __reduce_min_sync(0xffffffffu, lim_min);
-  }
+      for (int e = 0; e < 4; ++e) o[x][e] = 0.f;
+    // keys a row of a page's prefix may see; a branch's own keys are seen by all its rows
+    auto limit_of = [&](int r) {
+      return branch < 0 && r < rows ? min(n_keys, a.q_plen[q_first + div_g(row0 + r, a.g_inv)] - un.key0) : n_keys;
+    };
+    int lim_min = n_keys;
+    if (branch < 0) lim_min = __reduce_min_sync(0xffffffffu, limit_of(lane & 7));
 
-  // P of H tiles of scores (log2 units) against the running references, which
-  // move first where a score exceeds them by more than kPSlack
-  auto softmax = [&](auto& s) {
-    constexpr int H = sizeof(s) / sizeof(s[0]);
-    float most = -INFINITY;
+    // P of H blocks' scores (log2 units) against the running references, which move
+    // first where a score exceeds them by more than kPSlack
+    auto softmax = [&](auto& s) {
+      constexpr int H = sizeof(s) / sizeof(s[0]);
+      float top[2] = {fmaxf(s[0][0], s[0][2]), fmaxf(s[0][1], s[0][3])};
 #pragma unroll
-    for (int h = 0; h < H; ++h)
+      for (int h = 1; h < H; ++h)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-        most = max3f(most, fmaxf(s[h][nt][0], s[h][nt][2]) - mo[nt][0], fmaxf(s[h][nt][1], s[h][nt][3]) - mo[nt][1]);
-    if (__any_sync(0xffffffffu, most > kPShift + kPSlack)) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
+        for (int e = 0; e < 2; ++e) top[e] = max3f(top[e], s[h][e], s[h][2 + e]);
+      if (__any_sync(0xffffffffu, fmaxf(top[0] - mo[0], top[1] - mo[1]) > kPShift + kPSlack)) {
         float al[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float t = fmaxf(s[0][nt][e], s[0][nt][2 + e]);
-#pragma unroll
-          for (int h = 1; h < H; ++h) t = max3f(t, s[h][nt][e], s[h][nt][2 + e]);
+          float t = top[e];
 #pragma unroll
           for (int k = 4; k < 32; k <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, k));
           al[e] = 1.f;
-          if (t - mo[nt][e] > kPShift + kPSlack) {
-            al[e] = fast_exp2(mo[nt][e] - (t - kPShift));
-            mo[nt][e] = t - kPShift;
+          if (t - mo[e] > kPShift + kPSlack) {
+            al[e] = fast_exp2(mo[e] - (t - kPShift));
+            mo[e] = t - kPShift;
           }
-          l[nt][e] *= al[e];
+          l[e] *= al[e];
         }
 #pragma unroll
         for (int x = 0; x < 8; ++x)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[nt][x][e] *= al[e & 1];
+          for (int e = 0; e < 4; ++e) o[x][e] *= al[e & 1];
       }
-    }
 #pragma unroll
-    for (int h = 0; h < H; ++h)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int h = 0; h < H; ++h)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          s[h][nt][e] = fast_exp2(s[h][nt][e] - mo[nt][e & 1]);
-          l[nt][e & 1] += s[h][nt][e];
+          s[h][e] = fast_exp2(s[h][e] - mo[e & 1]);
+          l[e & 1] += s[h][e];
         }
-  };
-  // S^T of a block, and O^T += V^T P^T of one
-  auto scores = [&](uint32_t src, float (&s)[NT][4]) {
-    const KRegs b = read_k(src, key_a, c);
+    };
+    // S^T of a block, and O^T += V^T P^T of one
+    auto scores = [&](uint32_t src, float (&s)[4]) {
+      const KRegs b = read_k(src, key_a, c);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+      for (int e = 0; e < 4; ++e) s[e] = 0.f;
+      const I4Scale sa0 = i4_scale_both<0>(b.sa), sa1 = i4_scale_both<1>(b.sa);
+      const I4Scale sb0 = i4_scale_both<0>(b.sb), sb1 = i4_scale_both<1>(b.sb);
+      const uint32_t wa[4] = {b.ka.x, b.ka.y, b.ka.z, b.ka.w}, wb[4] = {b.kb.x, b.kb.y, b.kb.z, b.kb.w};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
-    const I4Scale sa0 = i4_scale_both<0>(b.sa), sa1 = i4_scale_both<1>(b.sa);
-    const I4Scale sb0 = i4_scale_both<0>(b.sb), sb1 = i4_scale_both<1>(b.sb);
-    const uint32_t wa[4] = {b.ka.x, b.ka.y, b.ka.z, b.ka.w}, wb[4] = {b.kb.x, b.kb.y, b.kb.z, b.kb.w};
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      // words 0, 1 of the chunk are its first group, 2, 3 its second
-      const I4Scale &sa = w < 2 ? sa0 : sa1, &sb = w < 2 ? sb0 : sb1;
-      const uint32_t va = wa[w] >> 8, vb = wb[w] >> 8;
-      const uint32_t f0[4] = {i4_pair<0>(wa[w], va, sa), i4_pair<0>(wb[w], vb, sb), i4_pair<1>(wa[w], va, sa),
-                              i4_pair<1>(wb[w], vb, sb)};
-      const uint32_t f1[4] = {i4_pair<2>(wa[w], va, sa), i4_pair<2>(wb[w], vb, sb), i4_pair<3>(wa[w], va, sa),
-                              i4_pair<3>(wb[w], vb, sb)};
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        if constexpr (kQInSmem) {
-          const uint4 qv = sm.q[nt][w][lane];
-          mma_f16(s[nt], f0, qv.x, qv.y);
-          mma_f16(s[nt], f1, qv.z, qv.w);
-        } else {
-          mma_f16(s[nt], f0, q[nt][4 * w], q[nt][4 * w + 1]);
-          mma_f16(s[nt], f1, q[nt][4 * w + 2], q[nt][4 * w + 3]);
-        }
+      for (int w = 0; w < 4; ++w) {
+        // words 0, 1 of the chunk are its first group, 2, 3 its second
+        const I4Scale &sa = w < 2 ? sa0 : sa1, &sb = w < 2 ? sb0 : sb1;
+        const uint32_t va = wa[w] >> 8, vb = wb[w] >> 8;
+        const uint32_t f0[4] = {i4_pair<0>(wa[w], va, sa), i4_pair<0>(wb[w], vb, sb), i4_pair<1>(wa[w], va, sa),
+                                i4_pair<1>(wb[w], vb, sb)};
+        const uint32_t f1[4] = {i4_pair<2>(wa[w], va, sa), i4_pair<2>(wb[w], vb, sb), i4_pair<3>(wa[w], va, sa),
+                                i4_pair<3>(wb[w], vb, sb)};
+        mma_f16(s, f0, q[4 * w], q[4 * w + 1]);
+        mma_f16(s, f1, q[4 * w + 2], q[4 * w + 3]);
       }
-    }
-  };
-  auto add_values = [&](uint32_t src, const float (&s)[NT][4]) {
-    const VRegs b = read_v(src, i, c);
-    uint32_t p[NT][2];
+    };
+    auto add_values = [&](uint32_t src, const float (&s)[4]) {
+      const VRegs b = read_v(src, i, c);
+      const uint32_t p0 = transpose8(pack_f16x2(s[0], s[1])), p1 = transpose8(pack_f16x2(s[2], s[3]));
+      const I4Scale s01 = i4_scale_two<0>(b.sv), s23 = i4_scale_two<2>(b.sv);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      p[nt][0] = transpose8(pack_f16x2(s[nt][0], s[nt][1]));
-      p[nt][1] = transpose8(pack_f16x2(s[nt][2], s[nt][3]));
-    }
-    const I4Scale s01 = i4_scale_two<0>(b.sv), s23 = i4_scale_two<2>(b.sv);
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      // low halves: even dims of two keys side by side; high halves: odd dims
-      const uint32_t k0 = w ? b.v0.y : b.v0.x, k1 = w ? b.v0.w : b.v0.z;
-      const uint32_t k2 = w ? b.v1.y : b.v1.x, k3 = w ? b.v1.w : b.v1.z;
-      const uint32_t e01 = __byte_perm(k0, k1, 0x5410), d01 = __byte_perm(k0, k1, 0x7632);
-      const uint32_t e23 = __byte_perm(k2, k3, 0x5410), d23 = __byte_perm(k2, k3, 0x7632);
-      const uint32_t e01v = e01 >> 8, d01v = d01 >> 8, e23v = e23 >> 8, d23v = d23 >> 8;
-      auto pv = [&](int mt, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
-        const uint32_t f[4] = {a0, a1, a2, a3};
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_f16(o[nt][mt], f, p[nt][0], p[nt][1]);
-      };
-      pv(4 * w + 0, i4_pair<0>(e01, e01v, s01), i4_pair<0>(d01, d01v, s01), i4_pair<0>(e23, e23v, s23), i4_pair<0>(d23, d23v, s23));
-      pv(4 * w + 1, i4_pair<1>(e01, e01v, s01), i4_pair<1>(d01, d01v, s01), i4_pair<1>(e23, e23v, s23), i4_pair<1>(d23, d23v, s23));
-      pv(4 * w + 2, i4_pair<2>(e01, e01v, s01), i4_pair<2>(d01, d01v, s01), i4_pair<2>(e23, e23v, s23), i4_pair<2>(d23, d23v, s23));
-      pv(4 * w + 3, i4_pair<3>(e01, e01v, s01), i4_pair<3>(d01, d01v, s01), i4_pair<3>(e23, e23v, s23), i4_pair<3>(d23, d23v, s23));
-    }
-  };
+      for (int w = 0; w < 2; ++w) {
+        // low halves: even dims of two keys side by side; high halves: odd dims
+        const uint32_t k0 = w ? b.v0.y : b.v0.x, k1 = w ? b.v0.w : b.v0.z;
+        const uint32_t k2 = w ? b.v1.y : b.v1.x, k3 = w ? b.v1.w : b.v1.z;
+        const uint32_t e01 = __byte_perm(k0, k1, 0x5410), d01 = __byte_perm(k0, k1, 0x7632);
+        const uint32_t e23 = __byte_perm(k2, k3, 0x5410), d23 = __byte_perm(k2, k3, 0x7632);
+        const uint32_t e01v = e01 >> 8, d01v = d01 >> 8, e23v = e23 >> 8, d23v = d23 >> 8;
+        const uint32_t f0[4] = {i4_pair<0>(e01, e01v, s01), i4_pair<0>(d01, d01v, s01), i4_pair<0>(e23, e23v, s23),
+                                i4_pair<0>(d23, d23v, s23)};
+        mma_f16(o[4 * w + 0], f0, p0, p1);
+        const uint32_t f1[4] = {i4_pair<1>(e01, e01v, s01), i4_pair<1>(d01, d01v, s01), i4_pair<1>(e23, e23v, s23),
+                                i4_pair<1>(d23, d23v, s23)};
+        mma_f16(o[4 * w + 1], f1, p0, p1);
+        const uint32_t f2[4] = {i4_pair<2>(e01, e01v, s01), i4_pair<2>(d01, d01v, s01), i4_pair<2>(e23, e23v, s23),
+                                i4_pair<2>(d23, d23v, s23)};
+        mma_f16(o[4 * w + 2], f2, p0, p1);
+        const uint32_t f3[4] = {i4_pair<3>(e01, e01v, s01), i4_pair<3>(d01, d01v, s01), i4_pair<3>(e23, e23v, s23),
+                                i4_pair<3>(d23, d23v, s23)};
+        mma_f16(o[4 * w + 3], f3, p0, p1);
+      }
+    };
 
 #pragma unroll 1
-  for (int step = warp; step < n_steps; step += 2 * W) {
-    asm volatile("cp.async.wait_group 1;" ::: "memory");
-    __syncwarp();
-    const bool two = step + W < n_steps;  // an odd count's last pair has one block
-    float s[2][NT][4];
-    scores(stage, s[0]);
-    if (two) {
-      scores(stage + kRingBlock, s[1]);
-    } else {
+    for (int step = warp; step < n_steps; step += 2 * W) {
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      __syncwarp();
+      const bool two = step + W < n_steps;  // an odd count's last pair has one block
+      float s[2][4];
+      scores(stage, s[0]);
+      if (two) {
+        scores(stage + kRingBlock, s[1]);
+      } else {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[1][nt][e] = -INFINITY;
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[h][nt][e] *= sl2q;
-    if ((step + W) * 16 + 16 > lim_min) {
+        for (int e = 0; e < 4; ++e) s[1][e] = -INFINITY;
+      }
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int e = 0; e < 4; ++e) s[h][e] *= sl2q;
+      if ((step + W) * 16 + 16 > lim_min) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int lim = limit_of(nt * 8 + 2 * c + e), key0 = (step + h * W) * 16 + key_a;
-            if (key0 >= lim) s[h][nt][e] = -INFINITY;
-            if (key0 + 2 >= lim) s[h][nt][2 + e] = -INFINITY;
+        for (int e = 0; e < 2; ++e) {
+          const int lim = limit_of(2 * c + e);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int key0 = (step + h * W) * 16 + key_a;
+            if (key0 >= lim) s[h][e] = -INFINITY;
+            if (key0 + 2 >= lim) s[h][2 + e] = -INFINITY;
           }
-    }
-    softmax(s);
-    add_values(stage, s[0]);
-    if (two) add_values(stage + kRingBlock, s[1]);
-    __syncwarp();
-    copy_pair(stage);
-    stage = stage == ring ? ring + 2 * kRingBlock : ring;
-  }
-
-  // ---------------------------------------------------------------- query block
-  // scores of all 16 keys by every warp; warp w then takes the keys j % W == w
-  const int q_len = un.q_len;
-  if (q_len > 0) {
-    float s1[1][NT][4];
-    auto& s = s1[0];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
-    const int64_t krow = static_cast<int64_t>(a.Hkv) * kHeadDim;
-    const int64_t at = un.qb_first * krow + g * kHeadDim;
-    const __nv_bfloat16* kn = a.k_new + at + 32 * c;
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const uint4 z = make_uint4(0, 0, 0, 0);
-      const uint4 va = key_a < q_len ? *reinterpret_cast<const uint4*>(kn + key_a * krow + 8 * x) : z;
-      const uint4 vb = key_a + 2 < q_len ? *reinterpret_cast<const uint4*>(kn + (key_a + 2) * krow + 8 * x) : z;
-      const uint32_t f0[4] = {va.x, vb.x, va.y, vb.y}, f1[4] = {va.z, vb.z, va.w, vb.w};
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const uint4* p = q_row(nt);
-        const uint4 qv = p ? p[x] : z;
-        mma_bf16(s[nt], f0, qv.x, qv.y);
-        mma_bf16(s[nt], f1, qv.z, qv.w);
+        }
       }
+      softmax(s);
+      add_values(stage, s[0]);
+      if (two) add_values(stage + kRingBlock, s[1]);
+      __syncwarp();
+      copy_pair(stage);
+      stage = stage == ring ? ring + 2 * kRingBlock : ring;
     }
-    constexpr uint32_t kMine = W == 1 ? 0xffffu : W == 2 ? 0x5555u : W == 4 ? 0x1111u : 0x0101u;
-    uint32_t vis[NT][2];  // bit j: the row sees key j, one of this warp's
+
+    // -------------------------------------------------------------- query block
+    // scores of all 16 keys by every warp; warp w then takes the keys j % W == w
+    const int q_len = un.q_len;
+    if (q_len > 0) {
+      float s1[1][4] = {{0.f, 0.f, 0.f, 0.f}};
+      float(&s)[4] = s1[0];
+      const int64_t krow = static_cast<int64_t>(a.Hkv) * kHeadDim;
+      const int64_t at = un.qb_first * krow + g * kHeadDim;
+      const __nv_bfloat16* kn = a.k_new + at + 32 * c;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+      for (int x = 0; x < 4; ++x) {
+        const uint4 z = make_uint4(0, 0, 0, 0);
+        const uint4 va = key_a < q_len ? *reinterpret_cast<const uint4*>(kn + key_a * krow + 8 * x) : z;
+        const uint4 vb = key_a + 2 < q_len ? *reinterpret_cast<const uint4*>(kn + (key_a + 2) * krow + 8 * x) : z;
+        const uint32_t f0[4] = {va.x, vb.x, va.y, vb.y}, f1[4] = {va.z, vb.z, va.w, vb.w};
+        const uint4 qv = q_row ? q_row[x] : z;
+        mma_bf16(s, f0, qv.x, qv.y);
+        mma_bf16(s, f1, qv.z, qv.w);
+      }
+      constexpr uint32_t kMine = W == 1 ? 0xffffu : W == 2 ? 0x5555u : W == 4 ? 0x1111u : 0x0101u;
+      uint32_t vis[2];  // bit j: the row sees key j, one of this warp's
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int r = nt * 8 + 2 * c + e;
+        const int r = 2 * c + e;
         uint32_t bits = 0;
         if (r < rows) {
           const int qi = div_g(row0 + r, a.g_inv);
           bits = a.tree_bits ? static_cast<uint32_t>(a.tree_bits[un.qb_first + qi]) : (2u << qi) - 1u;
         }
-        vis[nt][e] = bits & ((1u << q_len) - 1u) & (kMine << warp);
+        vis[e] = bits & ((1u << q_len) - 1u) & (kMine << warp);
       }
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        s[nt][e] = ((vis[nt][e & 1] >> (key_a + (e >> 1) * 2)) & 1u) ? s[nt][e] * a.sl2 : -INFINITY;
-    softmax(s1);
-    const __nv_bfloat16* vn = a.v_new + at + 16 * i;
+      for (int e = 0; e < 4; ++e) s[e] = ((vis[e & 1] >> (key_a + (e >> 1) * 2)) & 1u) ? s[e] * a.sl2 : -INFINITY;
+      softmax(s1);
+      const __nv_bfloat16* vn = a.v_new + at + 16 * i;
 #pragma unroll 1
-    for (int j = warp; j < q_len; j += W) {
-      // key j's P sits in lane row 2 (j / 4) + j % 2, first or second register pair
-      const int from = ((2 * (j >> 2) + (j & 1)) << 2) | c;
-      const uint4 x0 = *reinterpret_cast<const uint4*>(vn + j * krow), x1 = *reinterpret_cast<const uint4*>(vn + j * krow + 8);
-      const uint32_t xv[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int j = warp; j < q_len; j += W) {
+        // key j's P sits in lane row 2 (j / 4) + j % 2, first or second register
+        // pair; O of cached keys lacks the factor kI4Unscale
+        const int from = ((2 * (j >> 2) + (j & 1)) << 2) | c;
+        const uint4 x0 = *reinterpret_cast<const uint4*>(vn + j * krow), x1 = *reinterpret_cast<const uint4*>(vn + j * krow + 8);
+        const uint32_t xv[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          // (O of cached keys lacks the factor kI4Unscale)
-          const float pj = __shfl_sync(0xffffffffu, (j & 2) ? s[nt][2 + e] : s[nt][e], from) * (1.f / kI4Unscale);
-          if ((vis[nt][e] >> j) & 1u) {
+          const float pj = __shfl_sync(0xffffffffu, (j & 2) ? s[2 + e] : s[e], from) * (1.f / kI4Unscale);
+          if ((vis[e] >> j) & 1u) {
 #pragma unroll
             for (int x = 0; x < 8; ++x) {
-              o[nt][x][e] = fmaf(pj, __uint_as_float(xv[x] << 16), o[nt][x][e]);
-              o[nt][x][2 + e] = fmaf(pj, __uint_as_float(xv[x] & 0xffff0000u), o[nt][x][2 + e]);
+              o[x][e] = fmaf(pj, __uint_as_float(xv[x] << 16), o[x][e]);
+              o[x][2 + e] = fmaf(pj, __uint_as_float(xv[x] & 0xffff0000u), o[x][2 + e]);
             }
           }
         }
+      }
     }
-  }
 
-  // ---------------------------------------------------------------- results
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+    // -------------------------------------------------------------- results
 #pragma unroll
     for (int e = 0; e < 2; ++e)
 #pragma unroll
-      for (int k = 4; k < 32; k <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], k);
-  if constexpr (W > 1) {
-    // tile nt is finished by warp nt % W: the others leave their image of it
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-      if (nt % W != warp) {
-#pragma unroll
-        for (int x = 0; x < 8; ++x) sm.o[warp][nt][x][lane] = make_float4(o[nt][x][0], o[nt][x][1], o[nt][x][2], o[nt][x][3]);
-        sm.ml[warp][nt][lane] = make_float4(mo[nt][0], mo[nt][1], l[nt][0], l[nt][1]);
-      }
-    __syncthreads();
-  }
-  const int n_pre = un.n_pre;
-  const int64_t pre = un.pre, pre_stride = un.pre_stride, part = un.part;
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    if (W > 1 && nt % W != warp) continue;
+      for (int k = 4; k < 32; k <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], k);
     if constexpr (W > 1) {
+      if (warp > 0) {
 #pragma unroll
-      for (int w = 0; w < W; ++w) {
-        if (w == nt % W) continue;
-        const float4 ml = sm.ml[w][nt][lane];
-        const float m2[2] = {ml.x, ml.y}, l2[2] = {ml.z, ml.w};
-        float f1[2], f2[2];
+        for (int x = 0; x < 8; ++x) sm.o[warp - 1][x][lane] = make_float4(o[x][0], o[x][1], o[x][2], o[x][3]);
+        sm.ml[warp - 1][lane] = make_float4(mo[0], mo[1], l[0], l[1]);
+      }
+      __syncthreads();
+      if (warp == 0) {
+#pragma unroll 1
+        for (int w = 0; w < W - 1; ++w) {
+          const float4 ml = sm.ml[w][lane];
+          const float m2[2] = {ml.x, ml.y}, l2[2] = {ml.z, ml.w};
+          float f1[2], f2[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          // a side that has seen nothing has kNoMax and zero sums
-          const float M = fmaxf(mo[nt][e], m2[e]);
-          f1[e] = fast_exp2(mo[nt][e] - M);
-          f2[e] = fast_exp2(m2[e] - M);
-          mo[nt][e] = M;
-          l[nt][e] = l[nt][e] * f1[e] + l2[e] * f2[e];
+          for (int e = 0; e < 2; ++e) {
+            // a side that has seen nothing has kNoMax and zero sums
+            const float M = fmaxf(mo[e], m2[e]);
+            f1[e] = fast_exp2(mo[e] - M);
+            f2[e] = fast_exp2(m2[e] - M);
+            mo[e] = M;
+            l[e] = l[e] * f1[e] + l2[e] * f2[e];
+          }
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const float4 v = sm.o[w][x][lane];
+            o[x][0] = fmaf(v.x, f2[0], o[x][0] * f1[0]);
+            o[x][1] = fmaf(v.y, f2[1], o[x][1] * f1[1]);
+            o[x][2] = fmaf(v.z, f2[0], o[x][2] * f1[0]);
+            o[x][3] = fmaf(v.w, f2[1], o[x][3] * f1[1]);
+          }
         }
+      }
+    }
+    if (warp == 0) {
+      const int n_pre = un.n_pre;
+      const int64_t pre = un.pre, pre_stride = un.pre_stride, part = un.part;
+      // the lane's two rows: dims 16 i .. 16 i + 15 of each
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 2 * c + e;
+        if (r >= rows) continue;
+        const int t = div_g(row0 + r, a.g_inv);
+        const int64_t qh = static_cast<int64_t>(t) * a.Hq + g * G + row0 + r - t * G;  // (token, head) from q_first
+        float M = mo[e], L = l[e];
+        float acc[16];
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
-          const float4 v = sm.o[w][nt][x][lane];
-          o[nt][x][0] = fmaf(v.x, f2[0], o[nt][x][0] * f1[0]);
-          o[nt][x][1] = fmaf(v.y, f2[1], o[nt][x][1] * f1[1]);
-          o[nt][x][2] = fmaf(v.z, f2[0], o[nt][x][2] * f1[0]);
-          o[nt][x][3] = fmaf(v.w, f2[1], o[nt][x][3] * f1[1]);
+          acc[2 * x] = o[x][e] * kI4Unscale;
+          acc[2 * x + 1] = o[x][2 + e] * kI4Unscale;
         }
-      }
-    }
-    // the lane's two rows: dims 16 i .. 16 i + 15 of each
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = nt * 8 + 2 * c + e;
-      if (r >= rows) continue;
-      const int R = row0 + r, t = div_g(R, a.g_inv);
-      const int64_t qh = static_cast<int64_t>(t) * a.Hq + g * G + R - t * G;  // (token, head) from q_first
-      float M = mo[nt][e], L = l[nt][e];
-      float acc[16];
-#pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        acc[2 * x] = o[nt][x][e] * kI4Unscale;
-        acc[2 * x + 1] = o[nt][x][2 + e] * kI4Unscale;
-      }
 #pragma unroll 1
-      for (int k = 0; k < n_pre; ++k) {
-        const int64_t row = pre + k * pre_stride + qh;
-        const float m2 = a.part_lse[row];
-        const float4* src = reinterpret_cast<const float4*>(a.part_o + row * kHeadDim + 16 * i);
-        const float4 v[4] = {src[0], src[1], src[2], src[3]};
-        if (m2 == -INFINITY) continue;  // the row saw nothing there
-        const float Mn = fmaxf(M, m2);
-        const float f1 = fast_exp2(M - Mn), f2 = fast_exp2(m2 - Mn);
-        M = Mn;
-        L = fmaf(L, f1, f2);
+        for (int k = 0; k < n_pre; k += 2) {
+          // two results on their way at a time; a missing second one is empty
+          float m2[2];
+          float4 v[2][4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          acc[4 * x] = fmaf(v[x].x, f2, acc[4 * x] * f1);
-          acc[4 * x + 1] = fmaf(v[x].y, f2, acc[4 * x + 1] * f1);
-          acc[4 * x + 2] = fmaf(v[x].z, f2, acc[4 * x + 2] * f1);
-          acc[4 * x + 3] = fmaf(v[x].w, f2, acc[4 * x + 3] * f1);
+          for (int y = 0; y < 2; ++y) {
+            const int64_t row = pre + min(k + y, n_pre - 1) * pre_stride + qh;
+            const float4* src = reinterpret_cast<const float4*>(a.part_o + row * kHeadDim + 16 * i);
+            m2[y] = a.part_lse[row];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) v[y][x] = src[x];
+          }
+          if (k + 1 == n_pre) m2[1] = -INFINITY;
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            if (m2[y] == -INFINITY) continue;  // the row saw nothing there
+            const float Mn = fmaxf(M, m2[y]);
+            const float f1 = fast_exp2(M - Mn), f2 = fast_exp2(m2[y] - Mn);
+            M = Mn;
+            L = fmaf(L, f1, f2);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              acc[4 * x] = fmaf(v[y][x].x, f2, acc[4 * x] * f1);
+              acc[4 * x + 1] = fmaf(v[y][x].y, f2, acc[4 * x + 1] * f1);
+              acc[4 * x + 2] = fmaf(v[y][x].z, f2, acc[4 * x + 2] * f1);
+              acc[4 * x + 3] = fmaf(v[y][x].w, f2, acc[4 * x + 3] * f1);
+            }
+          }
+        }
+        const bool any = !(L == 0.f);  // NaN counts
+        const float inv = any ? 1.f / L : 0.f;
+#pragma unroll
+        for (int x = 0; x < 16; ++x) acc[x] *= inv;
+        if (part >= 0) {
+          float4* dst = reinterpret_cast<float4*>(a.part_o + (part + qh) * kHeadDim + 16 * i);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) dst[x] = make_float4(acc[4 * x], acc[4 * x + 1], acc[4 * x + 2], acc[4 * x + 3]);
+          if (i == 0) a.part_lse[part + qh] = any ? M + __log2f(L) : -INFINITY;
+        } else {
+          const int64_t row = static_cast<int64_t>(q_first) * a.Hq + qh;
+          uint4* dst = reinterpret_cast<uint4*>(a.o + row * kHeadDim + 16 * i);
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            dst[x] = make_uint4(pack_bf16x2(acc[8 * x], acc[8 * x + 1]), pack_bf16x2(acc[8 * x + 2], acc[8 * x + 3]),
+                                pack_bf16x2(acc[8 * x + 4], acc[8 * x + 5]), pack_bf16x2(acc[8 * x + 6], acc[8 * x + 7]));
+          if (i == 0) a.lse[row] = any ? (M + __log2f(L)) * kLn2 : -INFINITY;
         }
       }
-      const bool any = !(L == 0.f);  // NaN counts
-      const float inv = any ? 1.f / L : 0.f;
-      if (part >= 0) {
-        float4* dst = reinterpret_cast<float4*>(a.part_o + (part + qh) * kHeadDim + 16 * i);
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-          dst[x] = make_float4(acc[4 * x] * inv, acc[4 * x + 1] * inv, acc[4 * x + 2] * inv, acc[4 * x + 3] * inv);
-        if (i == 0) a.part_lse[part + qh] = any ? M + __log2f(L) : -INFINITY;
-      } else {
-        const int64_t row = static_cast<int64_t>(q_first) * a.Hq + qh;
-        uint4* dst = reinterpret_cast<uint4*>(a.o + row * kHeadDim + 16 * i);
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-          dst[x] = make_uint4(pack_bf16x2(acc[8 * x] * inv, acc[8 * x + 1] * inv), pack_bf16x2(acc[8 * x + 2] * inv, acc[8 * x + 3] * inv),
-                              pack_bf16x2(acc[8 * x + 4] * inv, acc[8 * x + 5] * inv),
-                              pack_bf16x2(acc[8 * x + 6] * inv, acc[8 * x + 7] * inv));
-        if (i == 0) a.lse[row] = any ? (M + __log2f(L)) * kLn2 : -INFINITY;
-      }
     }
-  }
-  if (W > 1) __syncthreads();  // the exchange area is free for the next unit
+    if (W > 1) __syncthreads();  // the exchange area is free for the next unit
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// Rows of branches whose partial results are many: one CTA a (token, head),
-// thread t is head dim t.
-__global__ void __launch_bounds__(kHeadDim) merge_i4_kernel(const I4Args a) {
+// Rows of branches whose partial results are many: one CTA a (token, head), its
+// warps taking every sixteenth result, four of them on their way at a time; lane l
+// sums dims 4 l .. 4 l + 3.
+constexpr int kMergeWarps = 16;
+__global__ void __launch_bounds__(kMergeWarps * 32) merge_i4_kernel(const I4Args a) {
   const I4Merge mg = a.merges[blockIdx.x / a.Hq];
-  const int h = blockIdx.x % a.Hq, t = threadIdx.x;
-  __shared__ float red[2][4];
+  const int h = blockIdx.x % a.Hq, t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  __shared__ float s_m[kMergeWarps], s_l[kMergeWarps];
+  __shared__ float4 s_o[kMergeWarps][32];
   const int n = mg.n_pre + mg.n_own;
   auto row_of = [&](int k) -> int64_t {
     return k < mg.n_pre ? mg.pre + static_cast<int64_t>(k) * mg.pre_stride + h
                         : mg.own + static_cast<int64_t>(k - mg.n_pre) * mg.own_stride + h;
   };
-  float M = kNoMax;
-  for (int k = t; k < n; k += kHeadDim) M = fmaxf(M, a.part_lse[row_of(k)]);
+  float M = kNoMax, L = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int kU = 4;
+  for (int k0 = warp; k0 < n; k0 += kMergeWarps * kU) {
+    float m[kU];
+    float4 v[kU];
 #pragma unroll
-  for (int s = 16; s; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
-  if ((t & 31) == 0) red[0][t >> 5] = M;
-  __syncthreads();
-  M = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
-  float L = 0.f, acc = 0.f;
-#pragma unroll 8
-  for (int k = 0; k < n; ++k) {
-    const int64_t row = row_of(k);
-    const float e = fast_exp2(a.part_lse[row] - M);
-    L += e;
-    const float v = a.part_o[row * kHeadDim + t];
-    acc = e == 0.f ? acc : fmaf(v, e, acc);
+    for (int x = 0; x < kU; ++x) {
+      const int k = k0 + x * kMergeWarps;
+      m[x] = -INFINITY;
+      v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k < n) {
+        const int64_t row = row_of(k);
+        m[x] = a.part_lse[row];
+        v[x] = *reinterpret_cast<const float4*>(a.part_o + row * kHeadDim + 4 * lane);
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < kU; ++x) {
+      if (m[x] == -INFINITY) continue;  // the row saw nothing there
+      const float Mn = fmaxf(M, m[x]);
+      const float f1 = fast_exp2(M - Mn), f2 = fast_exp2(m[x] - Mn);
+      M = Mn;
+      L = fmaf(L, f1, f2);
+      acc = make_float4(fmaf(v[x].x, f2, acc.x * f1), fmaf(v[x].y, f2, acc.y * f1), fmaf(v[x].z, f2, acc.z * f1),
+                        fmaf(v[x].w, f2, acc.w * f1));
+    }
   }
-  const bool any = !(L == 0.f);
+  s_o[warp][lane] = acc;
+  if (lane == 0) {
+    s_m[warp] = M;
+    s_l[warp] = L;
+  }
+  __syncthreads();
+  if (warp) return;
+  for (int w = 1; w < kMergeWarps; ++w) {
+    const float m2 = s_m[w], Mn = fmaxf(M, m2);
+    const float f1 = fast_exp2(M - Mn), f2 = fast_exp2(m2 - Mn);
+    const float4 v = s_o[w][lane];
+    M = Mn;
+    L = L * f1 + s_l[w] * f2;
+    acc = make_float4(fmaf(v.x, f2, acc.x * f1), fmaf(v.y, f2, acc.y * f1), fmaf(v.z, f2, acc.z * f1),
+                      fmaf(v.w, f2, acc.w * f1));
+  }
+  const bool any = !(L == 0.f);  // NaN counts
+  const float inv = any ? 1.f / L : 0.f;
   const int64_t out = static_cast<int64_t>(mg.token) * a.Hq + h;
-  a.o[out * kHeadDim + t] = __float2bfloat16_rn(any ? acc / L : 0.f);
-  if (t == 0) a.lse[out] = any ? (M + __log2f(L)) * kLn2 : -INFINITY;
+  *reinterpret_cast<uint2*>(a.o + out * kHeadDim + 4 * lane) =
+      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  if (lane == 0) a.lse[out] = any ? (M + __log2f(L)) * kLn2 : -INFINITY;
 }
 
 int launch_error(const char* what, std::string* err) {
@@ -704,43 +657,36 @@ int launch_error(const char* what, std::string* err) {
   return PADOC_ERR_CUDA;
 }
 
-template <int NT, int W>
+template <int W>
 int launch_units(I4Args a, int32_t unit0, int32_t n, cudaStream_t s, std::string* err) {
-  const int bytes = sizeof(Smem<NT, W>);
+  const int bytes = sizeof(Smem<W>);
   int per_sm = 0;
   // per device, so asked at each launch (host calls of about a microsecond)
-  cudaError_t e = cudaFuncSetAttribute(decode_i4_kernel<NT, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, decode_i4_kernel<NT, W>, 32 * W, bytes);
+  cudaError_t e = cudaFuncSetAttribute(decode_i4_kernel<W>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, decode_i4_kernel<W>, 32 * W, bytes);
   if (e != cudaSuccess || per_sm < 1) {
     *err = std::string("i4 decode occupancy: ") + cudaGetErrorString(e);
     return PADOC_ERR_CUDA;
   }
   a.unit0 = unit0;
   const int n_work = n * a.Hkv;
-  decode_i4_kernel<NT, W><<<std::min(n_work, per_sm * num_sms()), 32 * W, bytes, s>>>(a, n_work);
+  decode_i4_kernel<W><<<std::min(n_work, per_sm * num_sms()), 32 * W, bytes, s>>>(a, n_work);
   return launch_error("i4 decode launch", err);
-}
-
-template <int NT>
-int launch_rows(const I4Args& a, int32_t unit0, int32_t n, int warps, cudaStream_t s, std::string* err) {
-  if (n == 0) return PADOC_OK;
-  if (warps == 1) return launch_units<NT, 1>(a, unit0, n, s, err);
-  if (warps == 2) return launch_units<NT, 2>(a, unit0, n, s, err);
-  return launch_units<NT, 4>(a, unit0, n, s, err);
 }
 
 }  // namespace
 
-int launch_i4_units(const I4Args& a, const int32_t (&first)[4], int warps, cudaStream_t s, std::string* err) {
-  int rc = launch_rows<1>(a, first[0], first[1] - first[0], warps, s, err);
-  if (!rc) rc = launch_rows<2>(a, first[1], first[2] - first[1], warps, s, err);
-  if (!rc) rc = launch_rows<4>(a, first[2], first[3] - first[2], warps, s, err);
-  return rc;
+int launch_i4_units(const I4Args& a, int32_t unit0, int32_t n, int warps, cudaStream_t s, std::string* err) {
+  if (n == 0) return PADOC_OK;
+  if (warps == 1) return launch_units<1>(a, unit0, n, s, err);
+  if (warps == 2) return launch_units<2>(a, unit0, n, s, err);
+  if (warps == 4) return launch_units<4>(a, unit0, n, s, err);
+  return launch_units<8>(a, unit0, n, s, err);
 }
 
 int launch_i4_merge(const I4Args& a, int32_t n_merges, cudaStream_t s, std::string* err) {
   if (n_merges == 0) return PADOC_OK;
-  merge_i4_kernel<<<static_cast<unsigned>(n_merges) * a.Hq, kHeadDim, 0, s>>>(a);
+  merge_i4_kernel<<<static_cast<unsigned>(n_merges) * a.Hq, kMergeWarps * 32, 0, s>>>(a);
   return launch_error("i4 merge launch", err);
 }
 

@@ -1396,12 +1396,12 @@ struct DecodePlan {
   int64_t part_rows = 0;
   bool tc_own = false;  // own pass on tensor cores (several query rows per branch and kv head)
   bool fused = false;   // verify: own suffix and query block walked by the prefix pass's units
-  // 4-bit pool: units of the prefix pass, then of the own pass, each by row count
+  // 4-bit pool: units of the prefix pass (n_tc of up to 128 rows for the tcgen05
+  // kernel, then n_pre of up to 8), then n_own of the own pass
   std::vector<I4Unit> units;
   std::vector<I4Merge> merges;
-  int32_t pre_first[4] = {0, 0, 0, 0}, own_first[4] = {0, 0, 0, 0};
+  int32_t n_tc = 0, n_pre = 0, n_own = 0;
   int32_t pre_warps = 4, own_warps = 4;  // warps that share a unit
-  int32_t n_tc = 0;  // prefix units of up to 128 rows: the first of all
   size_t off_units = 0, off_merges = 0;
   size_t off_pages = 0, off_items = 0, off_branches = 0, off_qplen = 0, off_qbranch = 0, off_part_o = 0, off_part_lse = 0,
          off_work = 0, total = 0;
@@ -1409,21 +1409,17 @@ struct DecodePlan {
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
-// Units with at most 8, 16 and 32 rows, in this order; first[] are their bounds in `all`.
-// Within each the longest come first (a counting sort by blocks of keys): the
-// kernel deals them out back and forth.
-void add_units(const std::vector<I4Unit> (&by_rows)[3], std::vector<I4Unit>* all, int32_t (&first)[4]) {
-  for (int i = 0; i < 3; ++i) {
-    first[i] = static_cast<int32_t>(all->size());
-    int32_t most = 0;
-    for (const I4Unit& u : by_rows[i]) most = std::max(most, (u.n_keys + 15) / 16);
-    std::vector<int32_t> at(static_cast<size_t>(most) + 2, 0);
-    for (const I4Unit& u : by_rows[i]) ++at[most - (u.n_keys + 15) / 16 + 1];
-    for (int32_t k = 0; k <= most; ++k) at[k + 1] += at[k];
-    all->resize(first[i] + by_rows[i].size());
-    for (const I4Unit& u : by_rows[i]) (*all)[first[i] + at[most - (u.n_keys + 15) / 16]++] = u;
-  }
-  first[3] = static_cast<int32_t>(all->size());
+// Appends units to `all`, the longest first (a counting sort by blocks of keys):
+// the kernel deals them out back and forth.
+void add_units(const std::vector<I4Unit>& units, std::vector<I4Unit>* all) {
+  int32_t most = 0;
+  for (const I4Unit& u : units) most = std::max(most, (u.n_keys + 15) / 16);
+  std::vector<size_t> at(static_cast<size_t>(most) + 2, 0);
+  for (const I4Unit& u : units) ++at[most - (u.n_keys + 15) / 16 + 1];
+  for (int32_t k = 0; k <= most; ++k) at[k + 1] += at[k];
+  const size_t first = all->size();
+  all->resize(first + units.size());
+  for (const I4Unit& u : units) (*all)[first + at[most - (u.n_keys + 15) / 16]++] = u;
 }
 
 // The plan over a 4-bit pool.  The batch has been checked; P[p] is the longest
@@ -1431,7 +1427,7 @@ void add_units(const std::vector<I4Unit> (&by_rows)[3], std::vector<I4Unit>* all
 int plan_i4(const padoc_kv_pool* pool, const padoc_decode_batch* b, int32_t Hq, int n_sms, const std::vector<int32_t>& P,
             DecodePlan* pl) {
   const int32_t G = Hq / pool->Hkv, bs = pool->bs, nq = static_cast<int32_t>(pl->q_plen.size());
-  auto tile_of = [](int32_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; };
+  constexpr int32_t kRows = 8;  // rows of a warp-level unit
   auto on_tc = [](int32_t rows) { return rows > 16; };  // prefix units on the tcgen05 kernel
   auto blocks = [bs](int64_t n) { return (n + bs - 1) / bs; };
   // Chunks of keys: about two units for each CTA the GPU holds, within [8, 128]
@@ -1440,17 +1436,17 @@ int plan_i4(const padoc_kv_pool* pool, const padoc_decode_batch* b, int32_t Hq, 
   for (int32_t p = 0; p < b->n_pages; ++p) {
     const int32_t b0 = b->branch_offsets[p], b1 = b->branch_offsets[p + 1];
     if (b1 == b0) continue;
-    const int32_t rows = (b->q_offsets[b1] - b->q_offsets[b0]) * G, tr = tile_of(rows);
-    if (!on_tc(rows)) pre_steps += (rows + tr - 1) / tr * blocks(P[p]) * pool->Hkv;
+    const int32_t rows = (b->q_offsets[b1] - b->q_offsets[b0]) * G;
+    if (!on_tc(rows)) pre_steps += (rows + kRows - 1) / kRows * blocks(P[p]) * pool->Hkv;
     for (int32_t i = b0; i < b1; ++i) {
       const Seq& s = pool->seqs[b->branch_seq[i]];
-      const int32_t r = (b->q_offsets[i + 1] - b->q_offsets[i]) * G, t = tile_of(r);
-      own_steps += (r + t - 1) / t * blocks(s.len - s.fork_len) * pool->Hkv;
+      const int32_t r = (b->q_offsets[i + 1] - b->q_offsets[i]) * G;
+      own_steps += (r + kRows - 1) / kRows * blocks(s.len - s.fork_len) * pool->Hkv;
     }
   }
   const int64_t slots = 8 * static_cast<int64_t>(n_sms);
   const int64_t pre_chunk = std::max<int64_t>(8, std::min<int64_t>(128, pre_steps / slots));
-  const int64_t own_chunk = std::max<int64_t>(16, std::min<int64_t>(128, own_steps / slots));
+  const int64_t own_chunk = std::max<int64_t>(64, std::min<int64_t>(128, own_steps / slots));
   // The tcgen05 kernel runs one unit an SM at a time, in rounds: of all chunk
   // lengths the one whose rounds take the fewest tiles, with about two tiles'
   // time for starting and ending a unit.
@@ -1469,8 +1465,7 @@ int plan_i4(const padoc_kv_pool* pool, const padoc_decode_batch* b, int32_t Hq, 
       tc_chunk = ct;
     }
   }
-  std::vector<I4Unit> pre[3], own[3];
-  auto put = [](std::vector<I4Unit> (&to)[3], const I4Unit& u, int32_t tile) { to[tile == 8 ? 0 : tile == 16 ? 1 : 2].push_back(u); };
+  std::vector<I4Unit> pre, own;
   int64_t rows = 0;
   for (int32_t p = 0; p < b->n_pages; ++p) {
     const int32_t b0 = b->branch_offsets[p], b1 = b->branch_offsets[p + 1];
@@ -1489,7 +1484,7 @@ int plan_i4(const padoc_kv_pool* pool, const padoc_decode_batch* b, int32_t Hq, 
       // blocks of the page's sequence: its own tokens start in a fresh block
       // only where its shared part ends on one (checked), so key k is in block k / bs
       ++made;
-      const int32_t tr = tc ? kTileRows : tile_of(nqp * G);
+      const int32_t tr = tc ? kTileRows : kRows;
       for (int32_t r0 = 0; r0 < nqp * G; r0 += tr) {
         I4Unit u{};
         u.seq = b->page_seq[p];
@@ -1501,10 +1496,7 @@ int plan_i4(const padoc_kv_pool* pool, const padoc_decode_batch* b, int32_t Hq, 
         u.rows = std::min(tr, nqp * G - r0);
         u.branch = -1;
         u.part = pre_base + c * stride;
-        if (tc)
-          pl->units.push_back(u);
-        else
-          put(pre, u, tr);
+        (tc ? pl->units : pre).push_back(u);
       }
     }
     rows += made * stride;
@@ -1513,7 +1505,9 @@ int plan_i4(const padoc_kv_pool* pool, const padoc_decode_batch* b, int32_t Hq, 
       const int32_t qf = b->q_offsets[i], ql = b->q_offsets[i + 1] - qf, own_len = s.len - s.fork_len;
       for (int32_t r = qf; r < qf + ql; ++r) pl->q_plen[r] = s.fork_len;
       const int64_t osteps = blocks(own_len);
-      const int32_t oc = std::max<int32_t>(1, static_cast<int32_t>((osteps + own_chunk - 1) / own_chunk));
+      // where the merge kernel runs for the branch anyway, shorter chunks cost nothing
+      const int64_t cut = made > 8 ? 16 : own_chunk;
+      const int32_t oc = std::max<int32_t>(1, static_cast<int32_t>((osteps + cut - 1) / cut));
       const int64_t oper = (osteps + oc - 1) / oc;
       const int32_t n_own = oper ? static_cast<int32_t>((osteps + oper - 1) / oper) : 1;
       // Few partial results join in the own unit's epilogue (one after another
@@ -1522,9 +1516,8 @@ int plan_i4(const padoc_kv_pool* pool, const padoc_decode_batch* b, int32_t Hq, 
       const int64_t pre_at = pre_base + static_cast<int64_t>(qf - q0) * Hq;
       const int64_t own_base = rows, own_stride = static_cast<int64_t>(ql) * Hq;
       if (merge) rows += n_own * own_stride;
-      const int32_t tr = tile_of(ql * G);
       for (int32_t c = 0; c < n_own; ++c)
-        for (int32_t r0 = 0; r0 < ql * G; r0 += tr) {
+        for (int32_t r0 = 0; r0 < ql * G; r0 += kRows) {
           I4Unit u{};
           u.seq = b->branch_seq[i];
           u.blk0 = s.n_shared + static_cast<int32_t>(c * oper);
@@ -1532,7 +1525,7 @@ int plan_i4(const padoc_kv_pool* pool, const padoc_decode_batch* b, int32_t Hq, 
           u.n_keys = static_cast<int32_t>(std::min<int64_t>(own_len, (c + 1) * oper * bs)) - u.key0;
           u.q_first = qf;
           u.row0 = r0;
-          u.rows = std::min(tr, ql * G - r0);
+          u.rows = std::min(kRows, ql * G - r0);
           u.branch = i;
           u.qb_first = qf;
           u.q_len = c + 1 == n_own ? ql : 0;
@@ -1540,7 +1533,7 @@ int plan_i4(const padoc_kv_pool* pool, const padoc_decode_batch* b, int32_t Hq, 
           u.n_pre = merge ? 0 : made;
           u.pre = pre_at;
           u.pre_stride = stride;
-          put(own, u, tr);
+          own.push_back(u);
         }
       if (merge)
         for (int32_t r = 0; r < ql; ++r)
@@ -1549,13 +1542,19 @@ int plan_i4(const padoc_kv_pool* pool, const padoc_decode_batch* b, int32_t Hq, 
     }
   }
   pl->n_tc = static_cast<int32_t>(pl->units.size());
-  add_units(pre, &pl->units, pl->pre_first);
-  add_units(own, &pl->units, pl->own_first);
-  // One warp a unit once that fills the GPU's 16 warps an SM twice over; fewer
-  // units are shared by two or four (decode of 2176 branches a page batch: 799,
-  // 837 and 966 us with one, two and four).
-  const int64_t own_n = static_cast<int64_t>(pl->own_first[3] - pl->own_first[0]) * pool->Hkv;
-  pl->own_warps = own_n >= 32 * static_cast<int64_t>(n_sms) ? 1 : own_n >= 8 * static_cast<int64_t>(n_sms) ? 2 : 4;
+  pl->n_pre = static_cast<int32_t>(pre.size());
+  pl->n_own = static_cast<int32_t>(own.size());
+  add_units(pre, &pl->units);
+  add_units(own, &pl->units);
+  // One warp a unit where that gives every SM eight; fewer units are shared by
+  // two, four or eight (own pass of 3040 units: 40, 48, 60 and 93 us with one,
+  // two, four and eight warps; of 192 units: 40, 29, 23 and 21 us).
+  auto warps_of = [&](int64_t units) {
+    const int64_t a_sm = units * pool->Hkv / n_sms;
+    return a_sm >= 8 ? 1 : a_sm >= 4 ? 2 : a_sm >= 2 ? 4 : 8;
+  };
+  pl->pre_warps = warps_of(pl->n_pre);
+  pl->own_warps = warps_of(pl->n_own);
   if (static_cast<int64_t>(pl->units.size()) * pool->Hkv >= (int64_t(1) << 31) ||
       static_cast<int64_t>(nq) * Hq >= (int64_t(1) << 31))
     return fail(PADOC_ERR_UNSUPPORTED, "branch_decode: batch too large");
@@ -1908,7 +1907,7 @@ extern "C" int padoc_decode_prefix_pass(const padoc_decode_plan* plan, const voi
                                         padoc_stream_t stream) {
   if (!plan) return fail(PADOC_ERR_INVALID, "decode_prefix_pass: null plan");
   const bool i4 = plan->pool->dtype == PADOC_I4;
-  if (plan->n_branches == 0 || (i4 ? plan->pl.pre_first[3] == 0 : plan->pl.items.empty())) return PADOC_OK;
+  if (plan->n_branches == 0 || (i4 ? plan->pl.n_tc + plan->pl.n_pre == 0 : plan->pl.items.empty())) return PADOC_OK;
   if (plan->pl.fused) return PADOC_OK;  // the own pass walks the prefix too
   int rc = check_ws(plan, ws, SIZE_MAX);
   if (rc) return rc;
@@ -1918,7 +1917,7 @@ extern "C" int padoc_decode_prefix_pass(const padoc_decode_plan* plan, const voi
     const I4Args a = i4_args(plan, q, nullptr, nullptr, nullptr, nullptr, nullptr, scale, ws);
     std::string err;
     rc = launch_i4_prefix_tc(a, 0, plan->pl.n_tc, reinterpret_cast<cudaStream_t>(stream), &err);
-    if (!rc) rc = launch_i4_units(a, plan->pl.pre_first, plan->pl.pre_warps, reinterpret_cast<cudaStream_t>(stream), &err);
+    if (!rc) rc = launch_i4_units(a, plan->pl.n_tc, plan->pl.n_pre, plan->pl.pre_warps, reinterpret_cast<cudaStream_t>(stream), &err);
     if (rc) return fail(rc, "decode_prefix_pass: %s", err.c_str());
     return PADOC_OK;
   }
@@ -1943,7 +1942,7 @@ extern "C" int padoc_decode_own_pass(const padoc_decode_plan* plan, const void* 
   if (plan->pool->dtype == PADOC_I4) {
     const I4Args a = i4_args(plan, q, k_new, v_new, tree_bits, o, lse, scale, ws);
     std::string err;
-    rc = launch_i4_units(a, plan->pl.own_first, plan->pl.own_warps, reinterpret_cast<cudaStream_t>(stream), &err);
+    rc = launch_i4_units(a, plan->pl.n_tc + plan->pl.n_pre, plan->pl.n_own, plan->pl.own_warps, reinterpret_cast<cudaStream_t>(stream), &err);
     if (!rc)
       rc = launch_i4_merge(a, static_cast<int32_t>(plan->pl.merges.size()), reinterpret_cast<cudaStream_t>(stream), &err);
     if (rc) return fail(rc, "decode_own_pass: %s", err.c_str());

@@ -249,9 +249,8 @@ int launch_accept(const void* logits, int64_t V, int32_t nq, const int32_t* toke
 int launch_commit(void* k_pool, void* v_pool, const void* plan, int64_t n_rows, int32_t Hkv, const void* k,
                   const void* v, cudaStream_t s, std::string* err);
 
-// Units [first[0], first[1]) have at most 8 rows, [first[1], first[2]) 16,
-// [first[2], first[3]) 32; warps (1, 2 or 4) share each.
-int launch_i4_units(const I4Args& a, const int32_t (&first)[4], int warps, cudaStream_t s, std::string* err);
+// n units of up to 8 rows from units[unit0]; warps (1, 2, 4 or 8) share each.
+int launch_i4_units(const I4Args& a, int32_t unit0, int32_t n, int warps, cudaStream_t s, std::string* err);
 // The same for a page's prefix and units of up to 128 rows.
 int launch_i4_prefix_tc(I4Args a, int32_t unit0, int32_t n_units, cudaStream_t s, std::string* err);
 int read_and_clear_i4_error(cudaStream_t s, unsigned* word);
