@@ -167,11 +167,6 @@ struct Smem {
   float4 ml[W > 1 ? W - 1 : 1][32];
 };
 
-// x / G for x below 2^29 (g_inv = 2^32 / G rounded up; 0 for G = 1).
-__device__ __forceinline__ int div_g(int x, uint32_t g_inv) {
-  return g_inv ? static_cast<int>(__umulhi(static_cast<uint32_t>(x), g_inv)) : x;
-}
-
 // A persistent CTA's k-th unit: units come longest first and are dealt back and
 // forth, so that every CTA gets about the same number of keys.
 __device__ __forceinline__ int nth_work(int k) {

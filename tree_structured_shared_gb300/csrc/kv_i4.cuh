@@ -106,4 +106,9 @@ __device__ __forceinline__ uint32_t i4_pair(uint32_t w, uint32_t v, const I4Scal
                  : h2_fma(mask_or(x, 0x000F000Fu, 0x64006400u), s.s, s.lo);
 }
 
+// x / G for x below 2^29 (g_inv = 2^32 / G rounded up; 0 for G = 1).
+__device__ __forceinline__ int div_g(int x, uint32_t g_inv) {
+  return g_inv ? static_cast<int>(__umulhi(static_cast<uint32_t>(x), g_inv)) : x;
+}
+
 }  // namespace padoc

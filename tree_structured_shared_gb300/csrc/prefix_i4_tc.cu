@@ -63,18 +63,20 @@ constexpr int SM_ROW = SM_CV + kCStages * kVStage;  // per unit parity: sl2, m a
 constexpr int kRowBuf = 3 * 128 * 4;
 constexpr int SM_BAR = SM_ROW + 2 * kRowBuf;
 enum {
-  B_Q_FULL = 0,    // count 4: the unit's Q rows are laid out
-  B_ML_FULL = 1,   // count 4: the odd tiles' m and l are in shared memory
-  B_O_FREE = 2,    // count 4: the epilogue has read both O
-  B_K_FULL = 3,    // +stage (2), count 4
-  B_K_EMPTY = 5,   // +stage: S of the tile has run
-  B_V_FULL = 7,    // +stage (2), count 4
-  B_PV_DONE = 9,   // +stage: P V of the tile has run
-  B_S_FULL = 11,   // +half (2): S of the tile is in TMEM
-  B_P_FULL = 13,   // +half (2), count 4: P of the tile is in TMEM
-  B_DRAIN = 15,
-  N_BARS = 16
+  B_Q_FULL = 0,   // count 4: the unit's Q rows are laid out
+  B_ML_FULL = 1,  // count 4: the odd tiles' m and l are in shared memory
+  B_O_FREE = 2,   // count 4: the epilogue has read both O
+  B_K_FULL = 3,   // +tile (2), count 4: K of the CTA's first two tiles
+  B_T_FULL = 5,   // +half (2), count 12: P and V of the tile, and K of the tile two on
+  B_S_FULL = 7,   // +half (2): S of the tile is in TMEM, its K stage free
+  B_PV_DONE = 9,  // +half (2): P V of the tile has run, its V stage free
+  B_DRAIN = 11,
+  N_BARS = 12
 };
+// Everything the MMA thread needs for P V of a tile and S of the tile two on
+// completes one barrier: tcgen05.mma issue stalls while the pipe is full, so each
+// wait and commit between two groups is pipe idle time (with three waits and three
+// commits a tile took 2500 cycles).
 constexpr int SM_MISC = SM_BAR + N_BARS * 8;
 constexpr int kSmemBytes = SM_MISC + 16 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
@@ -135,7 +137,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a, 
   if (threadIdx.x == 0) {
     for (int i = 0; i < N_BARS; ++i) {
       uint32_t cnt = 1;
-      if (i < B_K_EMPTY || (i >= B_V_FULL && i < B_PV_DONE) || (i >= B_P_FULL && i < B_DRAIN)) cnt = 4;
+      if (i < B_T_FULL) cnt = 4;
+      if (i == B_T_FULL || i == B_T_FULL + 1) cnt = 12;
       mbar_init(bar(i), cnt);
     }
     *abort = 0;
@@ -157,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a, 
     // ------------------------------------------------------------ decoders of K (warps 8-11) and V (12-15)
     const bool is_k = warp < 12;
     const int t = threadIdx.x & 127;
-    const int b_full = is_k ? B_K_FULL : B_V_FULL, b_empty = is_k ? B_K_EMPTY : B_PV_DONE;
+    const int b_empty = is_k ? B_S_FULL : B_PV_DONE;
     const uint32_t stage0 = sbase + (is_k ? SM_CK : SM_CV);
     const int stage_bytes = is_k ? kKStage : kVStage;
     // V: piece x * 128 + t is block 2 x + (t >> 6), group (t >> 3) & 7, slots 2 (t & 7), + 1
@@ -267,27 +270,33 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a, 
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(b_full + st));
+        if (lane == 0) mbar_arrive(bar(is_k && kt < 2 ? B_K_FULL + st : B_T_FULL + st));
         copy_tile(cs);  // the thread has read its bytes of this stage
         if (++cs == kCStages) cs = 0;
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+    // the CTA's last two tiles have no K two on
+    for (uint32_t v = kt; is_k && v < kt + 2 && !failed; ++v) {
+      if (v < 2) continue;
+      if (!__all_sync(0xffffffffu, mbar_wait(bar(B_S_FULL + (v & 1)), ((v >> 1) & 1) ^ 1, abort)))
+        failed = true;
+      else if (lane == 0)
+        mbar_arrive(bar(B_T_FULL + (v & 1)));
+    }
     if (failed && lane == 0) raise_abort(abort, is_k ? 0x10000 : 0x20000);
   } else if (warp == 16) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
       constexpr uint32_t id_qk = idesc_f16(128, 128, false), id_pv = idesc_f16(128, 128, true);
-      uint32_t ks = 0, kp = 0;  // tiles whose S / P V are issued
+      uint32_t kt = 0;  // the unit's first tile
       int iu = 0;
       bool failed = false;
       const uint64_t d_q = sdesc_sw128(sbase + SM_Q, 16, 1024);
-      // S of the next tile.  Its half of TMEM last held P of the tile two back,
-      // whose P V this thread has issued before (tcgen05.mma runs in issue order).
-      auto issue_s = [&]() -> bool {
-        const int st = ks & 1;
-        if (!mbar_wait_relaxed(bar(B_K_FULL + st), (ks >> 1) & 1, abort)) return false;
-        tc_fence_after();
+      // S of tile k.  Its half of TMEM last held P of the tile two back, whose P V
+      // this thread has issued before (tcgen05.mma runs in issue order).
+      auto issue_s = [&](uint32_t k) {
+        const int st = k & 1;
         const uint64_t d_k = sdesc_sw128(sbase + SM_K + st * kTileBytes, 16, 1024);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {
@@ -295,21 +304,22 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a, 
           mma_bf16_ss(tmem + st * 128, d_q + off, d_k + off, id_qk, kk > 0);
         }
         mma_commit(bar(B_S_FULL + st));
-        mma_commit(bar(B_K_EMPTY + st));
-        ++ks;
-        return true;
       };
-      for (int w = blockIdx.x; w < n_work && !failed; w += gridDim.x, ++iu) {
+      for (int w = blockIdx.x; w < n_work; w += gridDim.x, ++iu) {
         const int n = (unit_of(w).n_keys + kTileKeys - 1) / kTileKeys;
-        if (!mbar_wait_relaxed(bar(B_Q_FULL), iu & 1, abort)) { failed = true; break; }
-        if (!issue_s() || (n > 1 && !issue_s())) { failed = true; break; }
-        for (int j = 0; j < n; ++j, ++kp) {
-          const int st = kp & 1;
-          if (!mbar_wait_relaxed(bar(B_V_FULL + st), (kp >> 1) & 1, abort) ||
-              !mbar_wait_relaxed(bar(B_P_FULL + st), (kp >> 1) & 1, abort)) {
-            failed = true;
-            break;
-          }
+        if (!mbar_wait_relaxed(bar(B_Q_FULL), iu & 1, abort) ||
+            (kt == 0 && !mbar_wait_relaxed(bar(B_K_FULL), 0, abort)) ||
+            (kt < 2 && kt + n > 1 && !mbar_wait_relaxed(bar(B_K_FULL + 1), 0, abort))) {
+          failed = true;
+          break;
+        }
+        tc_fence_after();
+        issue_s(kt);
+        if (n > 1) issue_s(kt + 1);
+        for (int j = 0; j < n; ++j) {
+          const uint32_t k = kt + j;
+          const int st = k & 1;
+          if (!mbar_wait_relaxed(bar(B_T_FULL + st), (k >> 1) & 1, abort)) { failed = true; break; }
           tc_fence_after();
           const uint64_t d_v = sdesc_sw128(sbase + SM_V + st * kTileBytes, kHalf, 1024);
 #pragma unroll
@@ -317,8 +327,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a, 
             mma_bf16_ts(tmem + kTmemO + st * 128, tmem + st * 128 + kk * 8, d_v + static_cast<uint64_t>(kk * (2048 >> 4)), id_pv,
                         (j > 1 || kk > 0) ? 1u : 0u);
           mma_commit(bar(B_PV_DONE + st));
-          if (j + 2 < n && !issue_s()) { failed = true; break; }
+          if (j + 2 < n) issue_s(k + 2);
         }
+        if (failed) break;
+        kt += n;
       }
       if (failed) raise_abort(abort, 0x40000);
       // every product issued has completed before TMEM is released
@@ -335,55 +347,81 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a, 
     uint32_t kt0 = 0;  // number of the unit's first tile
     bool failed = false;
     auto row_buf = [&](int iu) { return reinterpret_cast<float*>(smem + SM_ROW + (iu & 1) * kRowBuf); };
-    // odd tiles' threads: row r of a unit's Q into shared memory, and its softmax factor
-    auto lay_q = [&](int w, int iu) {
+    // Odd tiles' threads: row r of the next unit's Q.  Its scaling is found after the
+    // unit's first odd tile, while the thread would wait for its next S (which also
+    // brings the row near); once every S of the unit has run, the row goes to shared
+    // memory.
+    int q_for = -1;                 // the unit that the following is of
+    const uint4* q_src = nullptr;   // its row, if it has one
+    float q_scale = 1.f, q_sl2 = a.sl2 * kI4Unscale;
+    auto prepare_q = [&](int w) {
+      if (w >= n_work) return;
       const I4Unit& un = unit_of(w);
-      const int g = w % a.Hkv, R = un.row0 + r;
-      float sl2 = a.sl2;
-      if (r < un.rows) {
-        const uint4* src = reinterpret_cast<const uint4*>(
-            a.q + (static_cast<int64_t>(un.q_first + R / G) * a.Hq + g * G + R % G) * kHeadDim);
-        // twice over the row (the second time from L1), a few registers at a time
-        float amax = 0.f;
-        auto most = [&](uint32_t u) {
-          const float lo = fabsf(__uint_as_float(u << 16)), hi = fabsf(__uint_as_float(u & 0xffff0000u));
-          amax = fmaxf(amax, lo <= 3.4028235e38f ? lo : 0.f);
-          amax = fmaxf(amax, hi <= 3.4028235e38f ? hi : 0.f);
-        };
-#pragma unroll 8
-        for (int x = 0; x < 16; ++x) {
-          const uint4 v = __ldg(src + x);
-          most(v.x);
-          most(v.y);
-          most(v.z);
-          most(v.w);
+      q_for = w;
+      q_src = nullptr;
+      if (r >= un.rows) return;
+      const int R = un.row0 + r, t = div_g(R, a.g_inv);
+      q_src = reinterpret_cast<const uint4*>(
+          a.q + (static_cast<int64_t>(un.q_first + t) * a.Hq + (w % a.Hkv) * G + R - t * G) * kHeadDim);
+      // the largest magnitude as its bf16 bits, which order as the magnitudes do
+      uint32_t most2 = 0, fin = 0;
+#pragma unroll
+      for (int x0 = 0; x0 < 16; x0 += 8) {
+        uint4 v[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) v[x] = __ldg(q_src + x0 + x);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          const uint32_t u[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) most2 = __vmaxu2(most2, u[k] & 0x7fff7fffu);
         }
-        const int kexp = amax > 0.f ? min(100, 14 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127)) : 0;
-        const float qf = __uint_as_float(static_cast<uint32_t>(127 + kexp) << 23);
-        sl2 = a.sl2 * kI4Unscale * __uint_as_float(static_cast<uint32_t>(127 - kexp) << 23);
-        auto h = [&](uint32_t u) { return pack_f16x2(__uint_as_float(u << 16) * qf, __uint_as_float(u & 0xffff0000u) * qf); };
+      }
+      uint32_t mx = max(most2 & 0xffffu, most2 >> 16);
+      if (mx >= 0x7f80u) {
+        // an infinity or a NaN: the largest finite one sets the factor
+        for (int x = 0; x < 64; ++x) {
+          const uint32_t u = __ldg(reinterpret_cast<const uint32_t*>(q_src) + x), lo = u & 0x7fffu, hi = (u >> 16) & 0x7fffu;
+          fin = max(fin, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+        }
+        mx = fin;
+      }
+      const int kexp = mx ? min(100, 14 - (static_cast<int>(mx >> 7) - 127)) : 0;
+      q_scale = __uint_as_float(static_cast<uint32_t>(127 + kexp) << 23);
+      q_sl2 = a.sl2 * kI4Unscale * __uint_as_float(static_cast<uint32_t>(127 - kexp) << 23);
+    };
+    auto put_q = [&](int w, int iu) {
+      if (q_for != w) prepare_q(w);
+      if (q_src) {
+        auto h = [&](uint32_t u) {
+          return pack_f16x2(__uint_as_float(u << 16) * q_scale, __uint_as_float(u & 0xffff0000u) * q_scale);
+        };
         const uint32_t row = sbase + SM_Q + r * 128;
-#pragma unroll 4
-        for (int x = 0; x < 16; ++x) {
-          const uint4 v = __ldg(src + x);
-          st_shared_v4(row + (x >> 3) * kHalf + (((x & 7) ^ (r & 7)) << 4), h(v.x), h(v.y), h(v.z), h(v.w));
+#pragma unroll
+        for (int x0 = 0; x0 < 16; x0 += 8) {
+          uint4 v[8];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) v[x] = __ldg(q_src + x0 + x);
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+            st_shared_v4(row + (x0 >> 3) * kHalf + ((x ^ (r & 7)) << 4), h(v[x].x), h(v[x].y), h(v[x].z), h(v[x].w));
         }
       }
       // rows past the unit's keep what the buffer held: their results are not read
-      row_buf(iu)[r] = sl2;
+      row_buf(iu)[r] = q_sl2;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_Q_FULL));
     };
-    if (odd && blockIdx.x < n_work) lay_q(blockIdx.x, 0);
+    if (odd && blockIdx.x < n_work) put_q(blockIdx.x, 0);
     int iu = 0;
     for (int w = blockIdx.x; w < n_work && !failed; w += gridDim.x, ++iu) {
       const I4Unit& un = unit_of(w);
       const int rows = un.rows, n_keys = un.n_keys;
       const int n = (n_keys + kTileKeys - 1) / kTileKeys;
       const bool valid = r < rows, warp_valid = wq * 32 < rows;
-      const int R = un.row0 + r;
-      const int limit = valid ? min(n_keys, a.q_plen[un.q_first + R / G] - un.key0) : n_keys;
+      const int R = un.row0 + r, tok = div_g(R, a.g_inv);
+      const int limit = valid ? min(n_keys, a.q_plen[un.q_first + tok] - un.key0) : n_keys;
       if (!__all_sync(0xffffffffu, mbar_wait(bar(B_Q_FULL), iu & 1, abort))) {
         failed = true;
         break;
@@ -483,7 +521,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a, 
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B_P_FULL + odd));
+        if (lane == 0) mbar_arrive(bar(B_T_FULL + odd));
+        if (odd && j == j0) prepare_q(w + gridDim.x);
       }
       if (failed) break;
       // the unit's last tile, and the last of the other parity (if it has one)
@@ -503,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a, 
             failed = true;
             break;
           }
-          lay_q(w + gridDim.x, iu + 1);
+          put_q(w + gridDim.x, iu + 1);
         }
         continue;
       }
@@ -523,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a, 
         const float we = any_e ? fast_exp2(m_run - M) : 0.f, wo = any_o ? fast_exp2(m_o - M) : 0.f;
         const float L = (any_e ? l_run * we : 0.f) + (any_o ? l_o * wo : 0.f);
         const float fe = any_e ? we * kI4Unscale / L : 0.f, fo = any_o ? wo * kI4Unscale / L : 0.f;
-        const int64_t row = un.part + static_cast<int64_t>(R / G) * a.Hq + (w % a.Hkv) * G + R % G;
+        const int64_t row = un.part + static_cast<int64_t>(tok) * a.Hq + (w % a.Hkv) * G + R - tok * G;
         float* dst = a.part_o + row * kHeadDim;
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
