@@ -14,13 +14,13 @@
 //                CTA): thread r owns TMEM lane r = query row r; epilogue
 //   warps 4-7    softmax of the odd tiles; lays out the next unit's Q
 //   warps 8-11   K: thread t decodes key t of the tile (128 dims)
-//   warps 12-15  V: thread t decodes two slots of one group of 16 dims, four times
+//   warps 12-15  V: thread t decodes two slots of a block, four groups of 16 dims
 //   warp 16      MMA issuer (one thread)
 // Even and odd tiles have a running maximum, a sum and an O of their own, joined
 // at the unit's end, so neither softmax waits for the other; both halves of TMEM
 // hold an S tile (P in fp16 is written over it) and an O.
 // Shared memory (operand tiles in two 64-column halves, 128-byte swizzle):
-//   Q 32 KB | K 2 x 32 KB | V 2 x 32 KB | codes 3 x 19 KB | row data | barriers
+//   Q 32 KB | K 2 x 32 KB | V 2 x 32 KB | codes 3 x 18 KB | row data | barriers
 // The decoders and the softmax walk their tiles in short loops: long straight-
 // line streams, three a scheduler, starved on instruction fetches (3300 cycles a
 // tile at 0.4 instructions a cycle).
@@ -53,13 +53,13 @@ constexpr int kHalf = 16384;  // one 64-column half of a 128-row tile
 constexpr int kTileBytes = 2 * kHalf;
 constexpr int kCStages = 3;          // ring of codes
 constexpr int kCodes = 4 * 128 * 16;  // a tile's codes, K or V: [4 pieces][thread][16 bytes]
-constexpr int kKStage = kCodes + 128 * 8, kVStage = kCodes + 4 * 128 * 4;  // and its scales
+constexpr int kCStage = kCodes + 8 * 128;  // and its scales
 constexpr int SM_Q = 0;
 constexpr int SM_K = SM_Q + kTileBytes;
 constexpr int SM_V = SM_K + 2 * kTileBytes;
 constexpr int SM_CK = SM_V + 2 * kTileBytes;
-constexpr int SM_CV = SM_CK + kCStages * kKStage;
-constexpr int SM_ROW = SM_CV + kCStages * kVStage;  // per unit parity: sl2, m and l of the odd tiles [128] f32
+constexpr int SM_CV = SM_CK + kCStages * kCStage;
+constexpr int SM_ROW = SM_CV + kCStages * kCStage;  // per unit parity: sl2, m and l of the odd tiles [128] f32
 constexpr int kRowBuf = 3 * 128 * 4;
 constexpr int SM_BAR = SM_ROW + 2 * kRowBuf;
 enum {
@@ -106,6 +106,11 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool o
 __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_shared_u16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
   return v;
 }
 __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
@@ -162,117 +167,118 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a, 
     const int t = threadIdx.x & 127;
     const int b_empty = is_k ? B_S_FULL : B_PV_DONE;
     const uint32_t stage0 = sbase + (is_k ? SM_CK : SM_CV);
-    const int stage_bytes = is_k ? kKStage : kVStage;
-    // V: piece x * 128 + t is block 2 x + (t >> 6), group (t >> 3) & 7, slots 2 (t & 7), + 1
-    const int vg = (t >> 3) & 7, sp = t & 7;
+    // Half a warp takes a block of the tile, thread s = t & 15 of it the 16-byte
+    // pieces s, 16 + s, 32 + s, 48 + s: of K the four chunks of slot s; of V the
+    // slots 2 (s & 7), + 1 of the groups 2 x + (s >> 3).  And 8 bytes of scales: K's
+    // of slot s; V's of group s >> 1, which its half warp shares.
+    const int tb = t >> 4, s16 = t & 15;
     // the copies' own walk over the CTA's tiles, three ahead of the decoding
     int lw = blockIdx.x, lk0 = 0, l_keys = 0;
     const int32_t* l_ids = nullptr;
     const uint8_t* l_pool = nullptr;
-    int32_t id[4] = {0, 0, 0, 0};  // K: block of key t; V: blocks of the four pieces
+    int32_t id = 0;
+    const int64_t stride = static_cast<int64_t>(a.Hkv) * kI4Unit;
     auto open_unit = [&]() {
       if (lw >= n_work) return;
       const I4Unit& un = unit_of(lw);
       l_keys = un.n_keys;
-      l_ids = a.table + static_cast<int64_t>(un.seq) * a.max_bps + un.blk0;
-      l_pool = static_cast<const uint8_t*>(is_k ? a.k_pool : a.v_pool) + (lw % a.Hkv) * kI4Unit;
+      l_ids = a.table + static_cast<int64_t>(un.seq) * a.max_bps + un.blk0 + tb;
+      l_pool = static_cast<const uint8_t*>(is_k ? a.k_pool : a.v_pool) + (lw % a.Hkv) * kI4Unit + s16 * 16;
     };
-    auto block_of = [&](int x) { return (lk0 >> 4) + (is_k ? t >> 4 : 2 * x + (t >> 6)); };
-    auto read_ids = [&]() {
-      if (lw >= n_work) return;
-#pragma unroll
-      for (int x = 0; x < 4; ++x)
-        if (x == 0 || !is_k) id[x] = block_of(x) * 16 < l_keys ? __ldg(l_ids + block_of(x)) : 0;
-    };
-    auto copy_tile = [&](int cs) {
+    auto read_id = [&]() { id = lw < n_work && lk0 + tb * 16 < l_keys ? __ldg(l_ids + (lk0 >> 4)) : 0; };
+    auto copy_tile = [&](uint32_t dst) {
       if (lw < n_work) {
-        const uint32_t dst = stage0 + cs * stage_bytes;
-        const int64_t stride = static_cast<int64_t>(a.Hkv) * kI4Unit;
-        if (is_k) {
-          const uint8_t* p = l_pool + id[0] * stride;
-          const bool ok = block_of(0) * 16 < l_keys;
+        const uint8_t* p = l_pool + id * stride;
+        const bool ok = lk0 + tb * 16 < l_keys;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) copy_async<16>(dst + x * 2048 + t * 16, p + x * 256 + (t & 15) * 16, ok);
-          copy_async<8>(dst + kCodes + t * 8, p + kI4Scales + (t & 15) * 8, ok);
-        } else {
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const uint8_t* p = l_pool + id[x] * stride;
-            const bool ok = block_of(x) * 16 < l_keys;
-            copy_async<16>(dst + x * 2048 + t * 16, p + vg * 128 + sp * 16, ok);
-            copy_async<4>(dst + kCodes + x * 512 + t * 4, p + kI4Scales + vg * 16 + (sp >> 1) * 4, ok);
-          }
-        }
+        for (int x = 0; x < 4; ++x) copy_async<16>(dst + x * 2048 + t * 16, p + x * 256, ok);
+        copy_async<8>(dst + kCodes + t * 8, p + kI4Scales - s16 * 8, ok);
         lk0 += kTileKeys;
         if (lk0 >= l_keys) {
           lk0 = 0;
           lw += gridDim.x;
           open_unit();
         }
-        read_ids();
+        read_id();
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
     open_unit();
-    read_ids();
-    for (int cs = 0; cs < kCStages; ++cs) copy_tile(cs);
-    uint32_t kt = 0;
-    int cs = 0;
+    read_id();
+    for (int cs = 0; cs < kCStages; ++cs) copy_tile(stage0 + cs * kCStage);
+    // where the thread's pieces of an operand tile go: K, row t; V, the rows of its
+    // two slots, the upper four pairs of slots the other way round, so that eight
+    // neighbours write eight different banks' pieces
+    const int hi = s16 >> 3, swap = (s16 >> 2) & 1;
+    const int ka = is_k ? t : tb * 16 + 2 * (s16 & 7) + swap, kb = is_k ? t : ka ^ 1;
+    const int first = is_k ? 0 : 2 * hi;
+    uint32_t to[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int row = is_k || k < 2 ? ka : kb, piece = first + (is_k ? k : k & 1);
+      to[k] = row * 128 + ((piece ^ (row & 7)) << 4);
+    }
+    const uint32_t tiles = sbase + (is_k ? SM_K : SM_V);
+    uint32_t kt = 0, codes = stage0;
     bool failed = false;
     for (int w = blockIdx.x; w < n_work && !failed; w += gridDim.x) {
       const int n_keys = unit_of(w).n_keys;
       for (int k0 = 0; k0 < n_keys; k0 += kTileKeys, ++kt) {
         const int st = kt & 1;
         asm volatile("cp.async.wait_group %0;" ::"n"(kCStages - 1) : "memory");
+        __syncwarp();
         if (!__all_sync(0xffffffffu, mbar_wait(bar(b_empty + st), ((kt >> 1) & 1) ^ 1, abort))) {
           failed = true;
           break;
         }
-        const uint32_t codes = stage0 + cs * stage_bytes;
-        const uint32_t tile = sbase + (is_k ? SM_K : SM_V) + st * kTileBytes;
+        const uint32_t tile = tiles + st * kTileBytes;
         if (is_k) {
           // keys past the end are zero or old bytes: their scores are masked
-          const uint32_t row = tile + t * 128;
-          const int sw = t & 7;
 #pragma unroll 1
-          for (int x = 0; x < 4; ++x) {
-            const uint4 c = ld_shared_v4(codes + x * 2048 + t * 16);
-            const uint32_t sc = ld_shared_u32(codes + kCodes + t * 8 + (x >> 1) * 4) >> (16 * (x & 1));
-            const uint32_t half = row + (x >> 1) * kHalf;
-            const int p0 = (x & 1) * 4;
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t src = codes + x * 4096 + t * 16, dst = tile + x * kHalf;
+            const uint32_t sc = ld_shared_u32(codes + kCodes + t * 8 + x * 4);
+            const uint4 c0 = ld_shared_v4(src), c1 = ld_shared_v4(src + 2048);
             const I4Scale s0 = i4_scale_both<0>(sc), s1 = i4_scale_both<1>(sc);
-            put_word(half + (((p0 + 0) ^ sw) << 4), c.x, s0);
-            put_word(half + (((p0 + 1) ^ sw) << 4), c.y, s0);
-            put_word(half + (((p0 + 2) ^ sw) << 4), c.z, s1);
-            put_word(half + (((p0 + 3) ^ sw) << 4), c.w, s1);
+            put_word(dst + to[0], c0.x, s0);
+            put_word(dst + to[1], c0.y, s0);
+            put_word(dst + to[2], c0.z, s1);
+            put_word(dst + to[3], c0.w, s1);
+            const I4Scale s2 = i4_scale_both<2>(sc), s3 = i4_scale_both<3>(sc);
+            put_word(dst + (to[0] ^ 64), c1.x, s2);
+            put_word(dst + (to[1] ^ 64), c1.y, s2);
+            put_word(dst + (to[2] ^ 64), c1.z, s3);
+            put_word(dst + (to[3] ^ 64), c1.w, s3);
           }
         } else {
-          // the upper four pairs of slots go the other way round, so that eight
-          // neighbours write eight different banks' pieces
-          const int swap = sp >> 2;
-          const uint32_t half = tile + (vg >> 2) * kHalf;
-          const int p0 = (vg & 3) * 2;
+          // keys past the end may hold old bytes and must not be NaN: scales of zero
+          const int left = n_keys - k0 - tb * 16 - 2 * (s16 & 7);
+          const uint32_t keep = left >= 2 ? 0xffffu : left == 1 ? 0xffu : 0u;
+          const uint32_t sel = swap ? 0x4401u : 0x4410u;  // the slots' scales in the order they are written
 #pragma unroll 1
-          for (int x = 0; x < 4; ++x) {
-            const uint4 c = ld_shared_v4(codes + x * 2048 + t * 16);
-            const uint32_t sc = ld_shared_u32(codes + kCodes + x * 512 + t * 4) >> (16 * (sp & 1));
-            const int key = (2 * x + (t >> 6)) * 16 + sp * 2;
-            // keys past the end may hold old bytes and must not be NaN: a scale of zero
-            const uint32_t b0 = k0 + key < n_keys ? sc & 0xffu : 0u, b1 = k0 + key + 1 < n_keys ? sc & 0xff00u : 0u;
-            const uint32_t two = swap ? __byte_perm(b0 | b1, 0u, 0x4401u) : b0 | b1;
-            const int ka = key + swap, kb = key + 1 - swap;
-            const I4Scale s0 = i4_scale_both<0>(two), s1 = i4_scale_both<1>(two);
-            put_word(half + ka * 128 + (((p0 + 0) ^ (ka & 7)) << 4), swap ? c.z : c.x, s0);
-            put_word(half + ka * 128 + (((p0 + 1) ^ (ka & 7)) << 4), swap ? c.w : c.y, s0);
-            put_word(half + kb * 128 + (((p0 + 0) ^ (kb & 7)) << 4), swap ? c.x : c.z, s1);
-            put_word(half + kb * 128 + (((p0 + 1) ^ (kb & 7)) << 4), swap ? c.y : c.w, s1);
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t src = codes + x * 4096 + t * 16, dst = tile + x * kHalf;
+            // groups 4 x + hi and 4 x + 2 + hi
+            const uint32_t sc = codes + kCodes + tb * 128 + (4 * x + hi) * 16 + 2 * (s16 & 7);
+            const uint32_t b0 = __byte_perm(ld_shared_u16(sc) & keep, 0u, sel), b1 = __byte_perm(ld_shared_u16(sc + 32) & keep, 0u, sel);
+            const uint4 c0 = ld_shared_v4(src), c1 = ld_shared_v4(src + 2048);
+            const I4Scale s0 = i4_scale_both<0>(b0), s1 = i4_scale_both<1>(b0);
+            put_word(dst + to[0], swap ? c0.z : c0.x, s0);
+            put_word(dst + to[1], swap ? c0.w : c0.y, s0);
+            put_word(dst + to[2], swap ? c0.x : c0.z, s1);
+            put_word(dst + to[3], swap ? c0.y : c0.w, s1);
+            const I4Scale s2 = i4_scale_both<0>(b1), s3 = i4_scale_both<1>(b1);
+            put_word(dst + (to[0] ^ 64), swap ? c1.z : c1.x, s2);
+            put_word(dst + (to[1] ^ 64), swap ? c1.w : c1.y, s2);
+            put_word(dst + (to[2] ^ 64), swap ? c1.x : c1.z, s3);
+            put_word(dst + (to[3] ^ 64), swap ? c1.y : c1.w, s3);
           }
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(is_k && kt < 2 ? B_K_FULL + st : B_T_FULL + st));
-        copy_tile(cs);  // the thread has read its bytes of this stage
-        if (++cs == kCStages) cs = 0;
+        copy_tile(codes);  // the warp has read its bytes of this stage
+        codes = codes == stage0 + (kCStages - 1) * kCStage ? stage0 : codes + kCStage;
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
