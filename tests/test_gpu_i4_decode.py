@@ -117,6 +117,30 @@ def test_many_branches_and_chunks(harness):
     assert torch.equal(d.o, first[0]) and torch.equal(d.lse, first[1])
 
 
+@pytest.mark.parametrize("prefixes", [(100, 100), (1, 128), (120, 300), (257, 640)])
+def test_many_pages_of_few_tiles(harness, prefixes):
+    """Several units of one to five key tiles for each SM, with 20 to 150 query rows: short units one after another."""
+    rng = np.random.default_rng(prefixes[1])
+    pages = []
+    for _ in range(230):
+        P, N = int(rng.integers(prefixes[0], prefixes[1] + 1)), int(rng.integers(5, 9))
+        q = [int(x) for x in rng.integers(1, 6, N)]
+        pages.append(page(P, [max(0, P - int(x)) for x in rng.integers(0, 9, N)], [int(x) for x in rng.integers(0, 20, N)], q))
+    w = wl.DecodeWorkload("p", pages, 8, 2, 128, 0.7)
+    both(harness, w, prefixes[0], what=str(prefixes))
+
+
+def test_row_tiles_cut_differently(harness):
+    """Pages of several row tiles and uneven lengths: a page's row tiles are cut into different numbers of pieces."""
+    rng = np.random.default_rng(41)
+    pages = []
+    for P, N in ((1812, 6), (795, 19), (2825, 11), (300, 16)):
+        q = [int(x) for x in rng.integers(1, 17, N)]
+        pages.append(page(P, [max(0, P - int(x)) for x in rng.integers(0, 900, N)], [int(x) for x in rng.integers(0, 40, N)], q))
+    w = wl.DecodeWorkload("p", pages, 16, 4, 128, 0.7)
+    both(harness, w, 41, what="uneven")
+
+
 def test_captured_passes(harness):
     """A plan's two passes captured on another stream and replayed over new queries."""
     import torch

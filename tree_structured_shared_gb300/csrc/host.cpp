@@ -1401,8 +1401,9 @@ struct DecodePlan {
   std::vector<I4Unit> units;
   std::vector<I4Merge> merges;
   int32_t n_tc = 0, n_pre = 0, n_own = 0;
+  std::vector<int32_t> tc_first;  // a group of CTAs' first unit on the tcgen05 kernel, and the end
   int32_t pre_warps = 4, own_warps = 4;  // warps that share a unit
-  size_t off_units = 0, off_merges = 0;
+  size_t off_units = 0, off_merges = 0, off_first = 0;
   size_t off_pages = 0, off_items = 0, off_branches = 0, off_qplen = 0, off_qbranch = 0, off_part_o = 0, off_part_lse = 0,
          off_work = 0, total = 0;
 };
@@ -1422,6 +1423,58 @@ void add_units(const std::vector<I4Unit>& units, std::vector<I4Unit>* all) {
   for (const I4Unit& u : units) (*all)[first + at[most - (u.n_keys + 15) / 16]++] = u;
 }
 
+// A run of a page's prefix, in tiles of keys, for one tile of its rows, and the group
+// of CTAs that takes it.
+struct I4Cut {
+  int32_t page, row0, tile0, tiles, group;
+};
+
+// Deals the pages' prefixes out to at most n_groups groups of CTAs (one a kv head),
+// each about as many tiles as the others: a run is cut where a group is full.  A piece
+// costs about two tiles' time beside its own for starting and ending it; pieces
+// shorter than four tiles are left to prefixes of that length.
+void deal_prefixes(const std::vector<I4Cut>& whole, int32_t n_groups, std::vector<I4Cut>* cuts) {
+  constexpr int64_t kUnit = 2, kLeast = 4;
+  int64_t total = 0;
+  for (const I4Cut& w : whole) total += w.tiles + kUnit;
+  auto deal = [&](int64_t room) {
+    cuts->clear();
+    int32_t group = 0;
+    int64_t used = 0;
+    for (const I4Cut& w : whole)
+      for (int64_t at = 0; at < w.tiles;) {
+        const int64_t left = w.tiles - at;
+        int64_t take = room - used - kUnit;
+        if (take >= left) {
+          take = left;
+        } else {
+          take = std::min(take, left - kLeast);
+          if (take < kLeast) {
+            if (used > 0) {
+              ++group;
+              used = 0;
+              continue;
+            }
+            take = left < 2 * kLeast ? left : kLeast;
+          }
+        }
+        cuts->push_back({w.page, w.row0, static_cast<int32_t>(at), static_cast<int32_t>(take), group});
+        used += take + kUnit;
+        at += take;
+      }
+    return group + 1;
+  };
+  int64_t lo = total / n_groups, hi = total;  // the least room that n_groups groups suffice for
+  while (lo < hi) {
+    const int64_t mid = lo + (hi - lo) / 2;
+    if (deal(mid) <= n_groups)
+      hi = mid;
+    else
+      lo = mid + 1;
+  }
+  deal(hi);
+}
+
 // The plan over a 4-bit pool.  The batch has been checked; P[p] is the longest
 // prefix a branch of page p sees.
 int plan_i4(const padoc_kv_pool* pool, const padoc_decode_batch* b, int32_t Hq, int n_sms, const std::vector<int32_t>& P,
@@ -1430,8 +1483,8 @@ int plan_i4(const padoc_kv_pool* pool, const padoc_decode_batch* b, int32_t Hq, 
   constexpr int32_t kRows = 8;  // rows of a warp-level unit
   auto on_tc = [](int32_t rows) { return rows > 16; };  // prefix units on the tcgen05 kernel
   auto blocks = [bs](int64_t n) { return (n + bs - 1) / bs; };
-  // Chunks of keys: about two units for each CTA the GPU holds, within [8, 128]
-  // blocks (a unit's four warps then take at least two blocks each).
+  // Chunks of keys: about eight units an SM, within 128 blocks and no less than 8 (a
+  // page's prefix) or 64 (a branch's own keys, whose chunks cost a merge).
   int64_t pre_steps = 0, own_steps = 0;
   for (int32_t p = 0; p < b->n_pages; ++p) {
     const int32_t b0 = b->branch_offsets[p], b1 = b->branch_offsets[p + 1];
@@ -1447,24 +1500,18 @@ int plan_i4(const padoc_kv_pool* pool, const padoc_decode_batch* b, int32_t Hq, 
   const int64_t slots = 8 * static_cast<int64_t>(n_sms);
   const int64_t pre_chunk = std::max<int64_t>(8, std::min<int64_t>(128, pre_steps / slots));
   const int64_t own_chunk = std::max<int64_t>(64, std::min<int64_t>(128, own_steps / slots));
-  // The tcgen05 kernel runs one unit an SM at a time, in rounds: of all chunk
-  // lengths the one whose rounds take the fewest tiles, with about two tiles'
-  // time for starting and ending a unit.
-  int64_t tc_chunk = 4, tc_best = INT64_MAX;
-  for (int64_t ct = 4; ct <= 64; ++ct) {
-    int64_t units = 0;
+  std::vector<I4Cut> cuts;
+  {
+    std::vector<I4Cut> whole;
     for (int32_t p = 0; p < b->n_pages; ++p) {
       const int32_t b0 = b->branch_offsets[p], b1 = b->branch_offsets[p + 1];
       const int32_t rows = b1 > b0 ? (b->q_offsets[b1] - b->q_offsets[b0]) * G : 0;
-      const int64_t tiles = (P[p] + kTileKeys - 1) / kTileKeys;
-      if (on_tc(rows)) units += (rows + kTileRows - 1) / kTileRows * pool->Hkv * ((tiles + ct - 1) / ct);
+      if (!on_tc(rows) || P[p] == 0) continue;
+      for (int32_t r0 = 0; r0 < rows; r0 += kTileRows) whole.push_back({p, r0, 0, (P[p] + kTileKeys - 1) / kTileKeys, 0});
     }
-    const int64_t cost = (units + n_sms - 1) / n_sms * (ct + 2);
-    if (cost < tc_best) {
-      tc_best = cost;
-      tc_chunk = ct;
-    }
+    deal_prefixes(whole, std::max(1, n_sms / pool->Hkv), &cuts);
   }
+  size_t cut = 0;
   std::vector<I4Unit> pre, own;
   int64_t rows = 0;
   for (int32_t p = 0; p < b->n_pages; ++p) {
@@ -1472,32 +1519,43 @@ int plan_i4(const padoc_kv_pool* pool, const padoc_decode_batch* b, int32_t Hq, 
     if (b1 == b0) continue;
     const int32_t q0 = b->q_offsets[b0], nqp = b->q_offsets[b1] - q0;
     const bool tc = on_tc(nqp * G);
-    const int64_t unit_keys = tc ? kTileKeys : bs, most = tc ? tc_chunk : pre_chunk;
-    const int64_t steps = (P[p] + unit_keys - 1) / unit_keys;
-    const int32_t n_chunks = static_cast<int32_t>((steps + most - 1) / most);
-    const int64_t per = (n_chunks ? (steps + n_chunks - 1) / n_chunks : 0) * unit_keys;  // keys
     const int64_t pre_base = rows, stride = static_cast<int64_t>(nqp) * Hq;
-    int32_t made = 0;
-    for (int32_t c = 0; c < n_chunks; ++c) {
-      const int64_t k0 = c * per, k1 = std::min<int64_t>(P[p], (c + 1) * per);
-      if (k1 <= k0) break;
+    int32_t made = 0;  // partial results of a row
+    auto add_unit = [&](int64_t k0, int64_t k1, int32_t r0, int32_t chunk, std::vector<I4Unit>* to) {
       // blocks of the page's sequence: its own tokens start in a fresh block
       // only where its shared part ends on one (checked), so key k is in block k / bs
-      ++made;
-      const int32_t tr = tc ? kTileRows : kRows;
-      for (int32_t r0 = 0; r0 < nqp * G; r0 += tr) {
-        I4Unit u{};
-        u.seq = b->page_seq[p];
-        u.blk0 = static_cast<int32_t>(k0 / bs);
-        u.key0 = static_cast<int32_t>(k0);
-        u.n_keys = static_cast<int32_t>(k1 - k0);
-        u.q_first = q0;
-        u.row0 = r0;
-        u.rows = std::min(tr, nqp * G - r0);
-        u.branch = -1;
-        u.part = pre_base + c * stride;
-        (tc ? pl->units : pre).push_back(u);
+      I4Unit u{};
+      u.seq = b->page_seq[p];
+      u.blk0 = static_cast<int32_t>(k0 / bs);
+      u.key0 = static_cast<int32_t>(k0);
+      u.n_keys = static_cast<int32_t>(k1 - k0);
+      u.q_first = q0;
+      u.row0 = r0;
+      u.rows = std::min(tc ? kTileRows : kRows, nqp * G - r0);
+      u.branch = -1;
+      u.part = pre_base + chunk * stride;
+      u.pre_stride = stride;
+      to->push_back(u);
+      made = std::max(made, chunk + 1);
+    };
+    if (tc) {
+      std::vector<std::pair<size_t, int32_t>> ends;  // a row tile's last unit, and its pieces
+      for (; cut < cuts.size() && cuts[cut].page == p; ++cut) {
+        const I4Cut& c = cuts[cut];
+        if (c.group == static_cast<int32_t>(pl->tc_first.size())) pl->tc_first.push_back(static_cast<int32_t>(pl->units.size()));
+        const int64_t k0 = static_cast<int64_t>(c.tile0) * kTileKeys;
+        if (c.tile0 == 0) ends.emplace_back(0, 0);
+        add_unit(k0, std::min<int64_t>(P[p], k0 + static_cast<int64_t>(c.tiles) * kTileKeys), c.row0, ends.back().second, &pl->units);
+        ends.back() = {pl->units.size() - 1, ends.back().second + 1};
       }
+      // rows cut into fewer pieces than the page's others have that many results less
+      for (const auto& e : ends) pl->units[e.first].n_pre = made - e.second;
+    } else {
+      const int64_t steps = blocks(P[p]), n_chunks = (steps + pre_chunk - 1) / pre_chunk;
+      const int64_t per = n_chunks ? (steps + n_chunks - 1) / n_chunks * bs : 0;  // keys
+      for (int64_t k0 = 0; k0 < P[p]; k0 += per)
+        for (int32_t r0 = 0; r0 < nqp * G; r0 += kRows)
+          add_unit(k0, std::min<int64_t>(P[p], k0 + per), r0, static_cast<int32_t>(k0 / per), &pre);
     }
     rows += made * stride;
     for (int32_t i = b0; i < b1; ++i) {
@@ -1506,8 +1564,8 @@ int plan_i4(const padoc_kv_pool* pool, const padoc_decode_batch* b, int32_t Hq, 
       for (int32_t r = qf; r < qf + ql; ++r) pl->q_plen[r] = s.fork_len;
       const int64_t osteps = blocks(own_len);
       // where the merge kernel runs for the branch anyway, shorter chunks cost nothing
-      const int64_t cut = made > 8 ? 16 : own_chunk;
-      const int32_t oc = std::max<int32_t>(1, static_cast<int32_t>((osteps + cut - 1) / cut));
+      const int64_t most = made > 8 ? 16 : own_chunk;
+      const int32_t oc = std::max<int32_t>(1, static_cast<int32_t>((osteps + most - 1) / most));
       const int64_t oper = (osteps + oc - 1) / oc;
       const int32_t n_own = oper ? static_cast<int32_t>((osteps + oper - 1) / oper) : 1;
       // Few partial results join in the own unit's epilogue (one after another
@@ -1542,6 +1600,7 @@ int plan_i4(const padoc_kv_pool* pool, const padoc_decode_batch* b, int32_t Hq, 
     }
   }
   pl->n_tc = static_cast<int32_t>(pl->units.size());
+  if (pl->n_tc) pl->tc_first.push_back(pl->n_tc);
   pl->n_pre = static_cast<int32_t>(pre.size());
   pl->n_own = static_cast<int32_t>(own.size());
   add_units(pre, &pl->units);
@@ -1564,6 +1623,8 @@ int plan_i4(const padoc_kv_pool* pool, const padoc_decode_batch* b, int32_t Hq, 
   off = align_up(off + pl->units.size() * sizeof(I4Unit), 256);
   pl->off_merges = off;
   off = align_up(off + pl->merges.size() * sizeof(I4Merge), 256);
+  pl->off_first = off;
+  off = align_up(off + pl->tc_first.size() * sizeof(int32_t), 256);
   pl->off_qplen = off;
   off = align_up(off + pl->q_plen.size() * sizeof(int32_t), 256);
   pl->off_part_o = off;
@@ -1779,6 +1840,8 @@ extern "C" int padoc_decode_plan_create(padoc_kv_pool* pool, const padoc_decode_
       if (!pl.units.empty()) std::memcpy(p->host.data() + pl.off_units, pl.units.data(), pl.units.size() * sizeof(I4Unit));
       if (!pl.merges.empty())
         std::memcpy(p->host.data() + pl.off_merges, pl.merges.data(), pl.merges.size() * sizeof(I4Merge));
+      if (!pl.tc_first.empty())
+        std::memcpy(p->host.data() + pl.off_first, pl.tc_first.data(), pl.tc_first.size() * sizeof(int32_t));
       if (!pl.q_plen.empty())
         std::memcpy(p->host.data() + pl.off_qplen, pl.q_plen.data(), pl.q_plen.size() * sizeof(int32_t));
       *out = p.release();
@@ -1882,6 +1945,7 @@ static I4Args i4_args(const padoc_decode_plan* plan, const void* q, const void* 
   I4Args a{};
   a.units = reinterpret_cast<const I4Unit*>(w + pl.off_units);
   a.merges = reinterpret_cast<const I4Merge*>(w + pl.off_merges);
+  a.tc_first = reinterpret_cast<const int32_t*>(w + pl.off_first);
   a.q_plen = reinterpret_cast<const int32_t*>(w + pl.off_qplen);
   a.table = pool->d_table;
   a.max_bps = pool->max_bps;
@@ -1916,7 +1980,7 @@ extern "C" int padoc_decode_prefix_pass(const padoc_decode_plan* plan, const voi
   if (i4) {
     const I4Args a = i4_args(plan, q, nullptr, nullptr, nullptr, nullptr, nullptr, scale, ws);
     std::string err;
-    rc = launch_i4_prefix_tc(a, 0, plan->pl.n_tc, reinterpret_cast<cudaStream_t>(stream), &err);
+    rc = launch_i4_prefix_tc(a, plan->pl.n_tc ? static_cast<int32_t>(plan->pl.tc_first.size()) - 1 : 0, reinterpret_cast<cudaStream_t>(stream), &err);
     if (!rc) rc = launch_i4_units(a, plan->pl.n_tc, plan->pl.n_pre, plan->pl.pre_warps, reinterpret_cast<cudaStream_t>(stream), &err);
     if (rc) return fail(rc, "decode_prefix_pass: %s", err.c_str());
     return PADOC_OK;

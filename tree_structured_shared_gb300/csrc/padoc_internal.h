@@ -157,7 +157,9 @@ struct I4Unit {
   int32_t q_first, row0, rows;
   int32_t branch;          // own keys of this branch; -1: keys of a page's prefix
   int32_t q_len, qb_first; // query tokens of the branch when the unit takes its query block, else 0
-  int32_t n_pre, pad;      // prefix partial results merged here, one each pre_stride from pre
+  // own keys: prefix partial results merged here, one each pre_stride from pre; a page's
+  // prefix: results behind its own, pre_stride apart, that it marks as empty
+  int32_t n_pre, pad;
   int64_t pre, pre_stride; // partial rows, counted from (q_first, head 0)
   int64_t part;            // where the unit's partial rows go (as pre), or -1: write o and lse
 };
@@ -169,6 +171,7 @@ struct I4Merge {
 struct I4Args {
   const I4Unit* units;
   const I4Merge* merges;
+  const int32_t* tc_first;  // first unit of each group of CTAs of the tcgen05 kernel, and the end
   const int32_t* q_plen;  // [nq] prefix tokens visible to each query token
   const int32_t* table;
   int32_t max_bps, unit0;
@@ -252,7 +255,7 @@ int launch_commit(void* k_pool, void* v_pool, const void* plan, int64_t n_rows, 
 // n units of up to 8 rows from units[unit0]; warps (1, 2, 4 or 8) share each.
 int launch_i4_units(const I4Args& a, int32_t unit0, int32_t n, int warps, cudaStream_t s, std::string* err);
 // The same for a page's prefix and units of up to 128 rows.
-int launch_i4_prefix_tc(I4Args a, int32_t unit0, int32_t n_units, cudaStream_t s, std::string* err);
+int launch_i4_prefix_tc(const I4Args& a, int32_t n_groups, cudaStream_t s, std::string* err);
 int read_and_clear_i4_error(cudaStream_t s, unsigned* word);
 int launch_i4_merge(const I4Args& a, int32_t n_merges, cudaStream_t s, std::string* err);
 int launch_kv_write(const RowsArgs& a, cudaStream_t s, std::string* err);

@@ -2,28 +2,43 @@
 // (sm_103a: tcgen05 + TMEM), for pages with many query rows.
 //
 // A unit is 128 query rows (the rows of every branch of a page, token R / G,
-// head R % G of the group) of one kv head against a chunk of the page's shared
+// head R % G of the group) of one kv head against a run of the page's shared
 // prefix in tiles of 128 keys.  Two warpgroups turn a tile's codes into fp16
 // operand tiles in shared memory, each thread from the 72 bytes it copied there
 // itself three tiles ahead; no wider copy exists outside the SM.  fp16 holds
 // every decoded value exactly (kv_i4.cuh); Q's rows are scaled by a power of two each
 // (largest magnitude in [2^14, 2^15)), and the scale joins the row's softmax.
 //
-// Roles (544 threads, one persistent CTA per SM):
-//   warps 0-3    softmax of the even tiles (numbered across all units of the
-//                CTA): thread r owns TMEM lane r = query row r; epilogue
-//   warps 4-7    softmax of the odd tiles; lays out the next unit's Q
-//   warps 8-11   K: thread t decodes key t of the tile (128 dims)
-//   warps 12-15  V: thread t decodes two slots of a block, four groups of 16 dims
-//   warp 16      MMA issuer (one thread)
-// Even and odd tiles have a running maximum, a sum and an O of their own, joined
-// at the unit's end, so neither softmax waits for the other; both halves of TMEM
-// hold an S tile (P in fp16 is written over it) and an O.
+// Roles (768 threads, one persistent CTA per SM; a kv head's CTAs walk runs of
+// units that the plan made equally long):
+//   warps 0-11   softmax, three groups of four: group b takes the tiles b, b + 3, ...
+//                (numbered across all units of the CTA), thread r TMEM lane r = query
+//                row r; group 0 also stores the results, group 2 lays out the next Q
+//   warps 12-15  K: thread t decodes key t of the tile (128 dims)
+//   warps 16-19  V: thread t decodes two slots of a block, four groups of 16 dims
+//   warps 20, 21 issue S = Q K^T and O += P V (one thread each)
+// TMEM: an S tile for each group (P in fp16 is written over it) and O, 512 columns.
+// The groups keep a sum of their own but share each row's reference: a tile takes
+// over the one of the tile before it (published in shared memory once that tile's
+// maximum is known) and moves it only where it must.
 // Shared memory (operand tiles in two 64-column halves, 128-byte swizzle):
 //   Q 32 KB | K 2 x 32 KB | V 2 x 32 KB | codes 3 x 18 KB | row data | barriers
+//
+// What bounds it: a tile's products take 1024 cycles of the tensor pipe, its 16384
+// exponentials as many, decoding it about 1100; a tile takes about 2100, since the
+// roles' waits on one another do not all overlap.  128 pages of 4000-6144 tokens with
+// 8-60 branches take 380 us (112 us at HBM rate), 64 pages of 4809 tokens with 8-40
+// branches of up to 16 query tokens 601 us.  Steps behind it: one softmax group per
+// tile in turn, of two, made the groups' chains of loads and waits the bound (640 us
+// on the 64 pages); one thread issuing both products spent 2240 cycles a tile on
+// issue and waits; without decoding it takes 490 us, with the products alone 336.
 // The decoders and the softmax walk their tiles in short loops: long straight-
 // line streams, three a scheduler, starved on instruction fetches (3300 cycles a
 // tile at 0.4 instructions a cycle).
+//
+// A wait names a phase by its parity, so every waiter knows the phase before to be
+// over: from the barriers that it waited for, or from what the phase's arrivals
+// themselves waited for.
 //
 // Softmax: P = 2^(x - m + 10) against a running maximum m that moves only when
 // exceeded by 2^4: at most 2^14, so P stays in fp16's range, and what rounds to
@@ -48,7 +63,10 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kThreads = 544;
+constexpr int kThreads = 768;
+// registers a thread of each role, dealt from the 80 a thread that 768 threads start with
+constexpr int kRegsSoft = 104, kRegsDec = 64, kRegsMma = 40;
+static_assert(384 * kRegsSoft + 256 * kRegsDec + 128 * kRegsMma <= 80 * kThreads, "register budget");
 constexpr int kHalf = 16384;  // one 64-column half of a 128-row tile
 constexpr int kTileBytes = 2 * kHalf;
 constexpr int kCStages = 3;          // ring of codes
@@ -59,28 +77,30 @@ constexpr int SM_K = SM_Q + kTileBytes;
 constexpr int SM_V = SM_K + 2 * kTileBytes;
 constexpr int SM_CK = SM_V + 2 * kTileBytes;
 constexpr int SM_CV = SM_CK + kCStages * kCStage;
-constexpr int SM_ROW = SM_CV + kCStages * kCStage;  // per unit parity: sl2, m and l of the odd tiles [128] f32
-constexpr int kRowBuf = 3 * 128 * 4;
-constexpr int SM_BAR = SM_ROW + 2 * kRowBuf;
+constexpr int SM_ROW = SM_CV + kCStages * kCStage;  // per unit parity: sl2, groups 1's and 2's references and sums [128] f32
+constexpr int kRowBuf = 5 * 128 * 4;
+constexpr int SM_M = SM_ROW + 2 * kRowBuf;  // per group: the rows' references [128] f32
+constexpr int SM_BAR = SM_M + 3 * 128 * 4;
 enum {
   B_Q_FULL = 0,   // count 4: the unit's Q rows are laid out
-  B_ML_FULL = 1,  // count 4: the odd tiles' m and l are in shared memory
-  B_O_FREE = 2,   // count 4: the epilogue has read both O
-  B_K_FULL = 3,   // +tile (2), count 4: K of the CTA's first two tiles
-  B_T_FULL = 5,   // +half (2), count 12: P and V of the tile, and K of the tile two on
-  B_S_FULL = 7,   // +half (2): S of the tile is in TMEM, its K stage free
-  B_PV_DONE = 9,  // +half (2): P V of the tile has run, its V stage free
-  B_DRAIN = 11,
-  N_BARS = 12
+  B_O_FREE = 1,   // count 4: the epilogue has read O
+  B_K_FULL = 2,   // +stage (2), count 4
+  B_V_FULL = 4,   // +stage (2), count 4
+  B_M_FULL = 6,   // +group (3), count 4: the tile's references are in shared memory
+  B_P_FULL = 9,   // +group (3), count 4
+  B_ML_FULL = 12, // count 8: groups 1's and 2's references and sums are in shared memory
+  B_E_IN = 13,    // count 8: groups 0 and 1 have entered the unit
+  B_PV_DONE = 14, // +group (3): P V of the tile has run, its V stage and S buffer free
+  B_S_FULL = 17,  // +group (3): S of the tile is in TMEM, its K stage free
+  B_DRAIN = 20,   // count 2: the issuers' last commits
+  N_BARS = 21
 };
-// Everything the MMA thread needs for P V of a tile and S of the tile two on
-// completes one barrier: tcgen05.mma issue stalls while the pipe is full, so each
-// wait and commit between two groups is pipe idle time (with three waits and three
-// commits a tile took 2500 cycles).
+// The commits of S and P V free the stages that they read too: each wait and commit
+// between two groups of products is time in which the issuing thread stands still.
 constexpr int SM_MISC = SM_BAR + N_BARS * 8;
 constexpr int kSmemBytes = SM_MISC + 16 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
-constexpr uint32_t kTmemO = 256;  // S / P of half h at 128 h, O at 256 + 128 h
+constexpr uint32_t kTmemO = 384;  // S / P of buffer b at 128 b
 constexpr float kPShift = 10.f, kPSlack = 4.f;
 
 // kind::f16 with fp16 A and B and f32 accumulation; b_mn selects an MN-major B.
@@ -93,6 +113,13 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+template <int N, bool Up>
+__device__ __forceinline__ void set_max_regs() {
+  if (Up)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+  else
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 // N bytes from global to shared memory; with ok false the N bytes become zero.
 template <int N>
@@ -130,7 +157,7 @@ __device__ __forceinline__ void put_word(uint32_t addr, uint32_t w, const I4Scal
   st_shared_v4(addr, i4_pair<0>(w, v, s), i4_pair<1>(w, v, s), i4_pair<2>(w, v, s), i4_pair<3>(w, v, s));
 }
 
-__global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a, const int n_work) {
+__global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
@@ -141,9 +168,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a, 
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
   if (threadIdx.x == 0) {
     for (int i = 0; i < N_BARS; ++i) {
-      uint32_t cnt = 1;
-      if (i < B_T_FULL) cnt = 4;
-      if (i == B_T_FULL || i == B_T_FULL + 1) cnt = 12;
+      // one arrival a warp, one a commit
+      const uint32_t cnt = i < B_ML_FULL ? 4 : i < B_PV_DONE ? 8 : i == B_DRAIN ? 2 : 1;
       mbar_init(bar(i), cnt);
     }
     *abort = 0;
@@ -158,14 +184,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a, 
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int G = a.group;
+  // a group of CTAs takes a run of units, each CTA one kv head of them
+  const int g = blockIdx.x % a.Hkv, u0 = a.tc_first[blockIdx.x / a.Hkv], u1 = a.tc_first[blockIdx.x / a.Hkv + 1];
 
-  auto unit_of = [&](int w) -> const I4Unit& { return a.units[a.unit0 + w / a.Hkv]; };
-
-  if (warp >= 8 && warp < 16) {
-    // ------------------------------------------------------------ decoders of K (warps 8-11) and V (12-15)
-    const bool is_k = warp < 12;
+  if (warp >= 12 && warp < 20) {
+    // ------------------------------------------------------------ decoders of K (warps 12-15) and V (16-19)
+    set_max_regs<kRegsDec, false>();
+    const bool is_k = warp < 16;
     const int t = threadIdx.x & 127;
-    const int b_empty = is_k ? B_S_FULL : B_PV_DONE;
     const uint32_t stage0 = sbase + (is_k ? SM_CK : SM_CV);
     // Half a warp takes a block of the tile, thread s = t & 15 of it the 16-byte
     // pieces s, 16 + s, 32 + s, 48 + s: of K the four chunks of slot s; of V the
@@ -173,21 +199,21 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a, 
     // of slot s; V's of group s >> 1, which its half warp shares.
     const int tb = t >> 4, s16 = t & 15;
     // the copies' own walk over the CTA's tiles, three ahead of the decoding
-    int lw = blockIdx.x, lk0 = 0, l_keys = 0;
+    int lu = u0, lk0 = 0, l_keys = 0;
     const int32_t* l_ids = nullptr;
     const uint8_t* l_pool = nullptr;
     int32_t id = 0;
     const int64_t stride = static_cast<int64_t>(a.Hkv) * kI4Unit;
     auto open_unit = [&]() {
-      if (lw >= n_work) return;
-      const I4Unit& un = unit_of(lw);
+      if (lu >= u1) return;
+      const I4Unit& un = a.units[lu];
       l_keys = un.n_keys;
       l_ids = a.table + static_cast<int64_t>(un.seq) * a.max_bps + un.blk0 + tb;
-      l_pool = static_cast<const uint8_t*>(is_k ? a.k_pool : a.v_pool) + (lw % a.Hkv) * kI4Unit + s16 * 16;
+      l_pool = static_cast<const uint8_t*>(is_k ? a.k_pool : a.v_pool) + (g) * kI4Unit + s16 * 16;
     };
-    auto read_id = [&]() { id = lw < n_work && lk0 + tb * 16 < l_keys ? __ldg(l_ids + (lk0 >> 4)) : 0; };
+    auto read_id = [&]() { id = lu < u1 && lk0 + tb * 16 < l_keys ? __ldg(l_ids + (lk0 >> 4)) : 0; };
     auto copy_tile = [&](uint32_t dst) {
-      if (lw < n_work) {
+      if (lu < u1) {
         const uint8_t* p = l_pool + id * stride;
         const bool ok = lk0 + tb * 16 < l_keys;
 #pragma unroll
@@ -196,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a, 
         lk0 += kTileKeys;
         if (lk0 >= l_keys) {
           lk0 = 0;
-          lw += gridDim.x;
+          ++lu;
           open_unit();
         }
         read_id();
@@ -221,13 +247,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a, 
     const uint32_t tiles = sbase + (is_k ? SM_K : SM_V);
     uint32_t kt = 0, codes = stage0;
     bool failed = false;
-    for (int w = blockIdx.x; w < n_work && !failed; w += gridDim.x) {
-      const int n_keys = unit_of(w).n_keys;
+    for (int u = u0; u < u1 && !failed; ++u) {
+      const int n_keys = a.units[u].n_keys;
       for (int k0 = 0; k0 < n_keys; k0 += kTileKeys, ++kt) {
         const int st = kt & 1;
         asm volatile("cp.async.wait_group %0;" ::"n"(kCStages - 1) : "memory");
         __syncwarp();
-        if (!__all_sync(0xffffffffu, mbar_wait(bar(b_empty + st), ((kt >> 1) & 1) ^ 1, abort))) {
+        // the stage's last tile, two back: S (K) or P V (V) has run
+        const uint32_t old = kt - 2;
+        if (kt >= 2 &&
+            !__all_sync(0xffffffffu, mbar_wait(bar((is_k ? B_S_FULL : B_PV_DONE) + old % 3), (old / 3) & 1, abort))) {
           failed = true;
           break;
         }
@@ -276,99 +305,114 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a, 
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(is_k && kt < 2 ? B_K_FULL + st : B_T_FULL + st));
+        if (lane == 0) mbar_arrive(bar((is_k ? B_K_FULL : B_V_FULL) + st));
         copy_tile(codes);  // the warp has read its bytes of this stage
         codes = codes == stage0 + (kCStages - 1) * kCStage ? stage0 : codes + kCStage;
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-    // the CTA's last two tiles have no K two on
-    for (uint32_t v = kt; is_k && v < kt + 2 && !failed; ++v) {
-      if (v < 2) continue;
-      if (!__all_sync(0xffffffffu, mbar_wait(bar(B_S_FULL + (v & 1)), ((v >> 1) & 1) ^ 1, abort)))
-        failed = true;
-      else if (lane == 0)
-        mbar_arrive(bar(B_T_FULL + (v & 1)));
-    }
     if (failed && lane == 0) raise_abort(abort, is_k ? 0x10000 : 0x20000);
-  } else if (warp == 16) {
-    // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t id_qk = idesc_f16(128, 128, false), id_pv = idesc_f16(128, 128, true);
-      uint32_t kt = 0;  // the unit's first tile
+  } else if (warp >= 20) {
+    // ------------------------------------------------------------ issuers
+    set_max_regs<kRegsMma, false>();
+    if (warp == 20 && lane == 0) {
+      // S = Q K^T
+      constexpr uint32_t id_qk = idesc_f16(128, 128, false);
+      const uint64_t d_q = sdesc_sw128(sbase + SM_Q, 16, 1024);
+      uint32_t k = 0, sb = 0, round = 0;  // tile, its buffer k % 3, k / 3
       int iu = 0;
       bool failed = false;
-      const uint64_t d_q = sdesc_sw128(sbase + SM_Q, 16, 1024);
-      // S of tile k.  Its half of TMEM last held P of the tile two back, whose P V
-      // this thread has issued before (tcgen05.mma runs in issue order).
-      auto issue_s = [&](uint32_t k) {
-        const int st = k & 1;
-        const uint64_t d_k = sdesc_sw128(sbase + SM_K + st * kTileBytes, 16, 1024);
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const uint64_t off = static_cast<uint64_t>(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4);
-          mma_bf16_ss(tmem + st * 128, d_q + off, d_k + off, id_qk, kk > 0);
-        }
-        mma_commit(bar(B_S_FULL + st));
-      };
-      for (int w = blockIdx.x; w < n_work; w += gridDim.x, ++iu) {
-        const int n = (unit_of(w).n_keys + kTileKeys - 1) / kTileKeys;
-        if (!mbar_wait_relaxed(bar(B_Q_FULL), iu & 1, abort) ||
-            (kt == 0 && !mbar_wait_relaxed(bar(B_K_FULL), 0, abort)) ||
-            (kt < 2 && kt + n > 1 && !mbar_wait_relaxed(bar(B_K_FULL + 1), 0, abort))) {
-          failed = true;
-          break;
-        }
-        tc_fence_after();
-        issue_s(kt);
-        if (n > 1) issue_s(kt + 1);
-        for (int j = 0; j < n; ++j) {
-          const uint32_t k = kt + j;
-          const int st = k & 1;
-          if (!mbar_wait_relaxed(bar(B_T_FULL + st), (k >> 1) & 1, abort)) { failed = true; break; }
+      for (int u = u0; u < u1 && !failed; ++u, ++iu) {
+        const int n = (a.units[u].n_keys + kTileKeys - 1) / kTileKeys;
+        if (!mbar_wait_relaxed(bar(B_Q_FULL), iu & 1, abort)) failed = true;
+        for (int j = 0; j < n && !failed; ++j, ++k) {
+          // the buffer last held P of the tile three back
+          if ((round > 0 && !mbar_wait_relaxed(bar(B_PV_DONE + sb), (round - 1) & 1, abort)) ||
+              !mbar_wait_relaxed(bar(B_K_FULL + (k & 1)), (k >> 1) & 1, abort)) {
+            failed = true;
+            break;
+          }
           tc_fence_after();
-          const uint64_t d_v = sdesc_sw128(sbase + SM_V + st * kTileBytes, kHalf, 1024);
+          const uint64_t d_k = sdesc_sw128(sbase + SM_K + (k & 1) * kTileBytes, 16, 1024);
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_bf16_ts(tmem + kTmemO + st * 128, tmem + st * 128 + kk * 8, d_v + static_cast<uint64_t>(kk * (2048 >> 4)), id_pv,
-                        (j > 1 || kk > 0) ? 1u : 0u);
-          mma_commit(bar(B_PV_DONE + st));
-          if (j + 2 < n) issue_s(k + 2);
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint64_t off = static_cast<uint64_t>(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4);
+            mma_bf16_ss(tmem + sb * 128, d_q + off, d_k + off, id_qk, kk > 0);
+          }
+          mma_commit(bar(B_S_FULL + sb));
+          if (++sb == 3) {
+            sb = 0;
+            ++round;
+          }
         }
-        if (failed) break;
-        kt += n;
       }
       if (failed) raise_abort(abort, 0x40000);
       // every product issued has completed before TMEM is released
       mma_commit(bar(B_DRAIN));
       int never = 0;
       mbar_wait(bar(B_DRAIN), 0, &never);
+    } else if (warp == 21 && lane == 0) {
+      // O += P V
+      constexpr uint32_t id_pv = idesc_f16(128, 128, true);
+      uint32_t k = 0, pb = 0, round = 0;  // tile, its buffer k % 3, k / 3
+      bool failed = false;
+      for (int u = u0; u < u1 && !failed; ++u) {
+        const int n = (a.units[u].n_keys + kTileKeys - 1) / kTileKeys;
+        for (int j = 0; j < n; ++j, ++k) {
+          const int st = k & 1;
+          if (!mbar_wait_relaxed(bar(B_V_FULL + st), (k >> 1) & 1, abort) ||
+              !mbar_wait_relaxed(bar(B_P_FULL + pb), round & 1, abort)) {
+            failed = true;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t d_v = sdesc_sw128(sbase + SM_V + st * kTileBytes, kHalf, 1024);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_bf16_ts(tmem + kTmemO, tmem + pb * 128 + kk * 8, d_v + static_cast<uint64_t>(kk * (2048 >> 4)), id_pv,
+                        (j > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(bar(B_PV_DONE + pb));
+          if (++pb == 3) {
+            pb = 0;
+            ++round;
+          }
+        }
+      }
+      if (failed) raise_abort(abort, 0x100000);
+      mma_commit(bar(B_DRAIN));
+      int never = 0;
+      mbar_wait(bar(B_DRAIN), 0, &never);
     }
-  } else if (warp < 8) {
+  } else {
     // ------------------------------------------------------------ softmax
-    const int odd = warp >> 2;  // this warpgroup's tiles, its half of TMEM
+    set_max_regs<kRegsSoft, true>();
+    const int wg = warp >> 2;  // its tiles are wg, wg + 3, ...: buffer wg
     const int r = threadIdx.x & 127, wq = warp & 3;
     const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
-    const uint32_t t_s = tmem + lane_base + odd * 128, t_o = tmem + kTmemO + lane_base;
-    uint32_t kt0 = 0;  // number of the unit's first tile
+    const uint32_t t_o = tmem + kTmemO + lane_base, t_s = tmem + wg * 128 + lane_base;
+    float* m_sh = reinterpret_cast<float*>(smem + SM_M);
+    const int before = wg ? wg - 1 : 2;  // group of the tile before
+    uint32_t kt0 = 0;     // number of the unit's first tile
+    uint32_t round = 0;   // of the group's tiles
+    int j = wg;           // the group's next tile, from the unit's first
     bool failed = false;
     auto row_buf = [&](int iu) { return reinterpret_cast<float*>(smem + SM_ROW + (iu & 1) * kRowBuf); };
-    // Odd tiles' threads: row r of the next unit's Q.  Its scaling is found after the
-    // unit's first odd tile, while the thread would wait for its next S (which also
-    // brings the row near); once every S of the unit has run, the row goes to shared
-    // memory.
+    // Group 2's threads: row r of the next unit's Q.  Its scaling is found after the
+    // group's first tile of the unit, while the thread would wait for its next S (which
+    // also brings the row near); once every S of the unit has run, the row goes to
+    // shared memory.
     int q_for = -1;                 // the unit that the following is of
     const uint4* q_src = nullptr;   // its row, if it has one
     float q_scale = 1.f, q_sl2 = a.sl2 * kI4Unscale;
-    auto prepare_q = [&](int w) {
-      if (w >= n_work) return;
-      const I4Unit& un = unit_of(w);
-      q_for = w;
+    auto prepare_q = [&](int u) {
+      if (u >= u1) return;
+      const I4Unit& un = a.units[u];
+      q_for = u;
       q_src = nullptr;
       if (r >= un.rows) return;
       const int R = un.row0 + r, t = div_g(R, a.g_inv);
       q_src = reinterpret_cast<const uint4*>(
-          a.q + (static_cast<int64_t>(un.q_first + t) * a.Hq + (w % a.Hkv) * G + R - t * G) * kHeadDim);
+          a.q + (static_cast<int64_t>(un.q_first + t) * a.Hq + (g) * G + R - t * G) * kHeadDim);
       // the largest magnitude as its bf16 bits, which order as the magnitudes do
       uint32_t most2 = 0, fin = 0;
 #pragma unroll
@@ -396,8 +440,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a, 
       q_scale = __uint_as_float(static_cast<uint32_t>(127 + kexp) << 23);
       q_sl2 = a.sl2 * kI4Unscale * __uint_as_float(static_cast<uint32_t>(127 - kexp) << 23);
     };
-    auto put_q = [&](int w, int iu) {
-      if (q_for != w) prepare_q(w);
+    auto put_q = [&](int u, int iu) {
+      if (q_for != u) prepare_q(u);
       if (q_src) {
         auto h = [&](uint32_t u) {
           return pack_f16x2(__uint_as_float(u << 16) * q_scale, __uint_as_float(u & 0xffff0000u) * q_scale);
@@ -419,10 +463,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a, 
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_Q_FULL));
     };
-    if (odd && blockIdx.x < n_work) put_q(blockIdx.x, 0);
+    if (wg == 2 && u0 < u1) put_q(u0, 0);
     int iu = 0;
-    for (int w = blockIdx.x; w < n_work && !failed; w += gridDim.x, ++iu) {
-      const I4Unit& un = unit_of(w);
+    for (int u = u0; u < u1 && !failed; ++u, ++iu) {
+      const I4Unit& un = a.units[u];
       const int rows = un.rows, n_keys = un.n_keys;
       const int n = (n_keys + kTileKeys - 1) / kTileKeys;
       const bool valid = r < rows, warp_valid = wq * 32 < rows;
@@ -433,26 +477,29 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a, 
         break;
       }
       const float sl2 = row_buf(iu)[r];
-      const int j0 = (kt0 & 1) == odd ? 0 : 1;  // the unit's first tile of this parity
-      float m_run = -INFINITY, l_run = 0.f;
-      for (int j = j0; j < n; j += 2) {
-        const uint32_t kt = kt0 + j;
-        if (!__all_sync(0xffffffffu, mbar_wait_relaxed(bar(B_S_FULL + odd), (kt >> 1) & 1, abort))) {
+      if (wg < 2) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_E_IN));
+      }
+      const int j0 = j;
+      float m_run = -INFINITY, l_run = 0.f;     // the reference last used here, the sum against it
+      for (; j < n; j += 3, ++round) {
+        if (!__all_sync(0xffffffffu, mbar_wait_relaxed(bar(B_S_FULL + wg), round & 1, abort))) {
           failed = true;
           break;
         }
         tc_fence_after();
-        if (warp_valid) {
-          const int vis = limit - j * kTileKeys;  // keys [0, vis) of the tile are visible
-          auto mask32 = [&](int c, uint32_t (&v)[32]) {
-            const int left = vis - c * 32;
-            if (left < 32) {
+        const int vis = limit - j * kTileKeys;  // keys [0, vis) of the tile are visible
+        auto mask32 = [&](int c, uint32_t (&v)[32]) {
+          const int left = vis - c * 32;
+          if (left < 32) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (i >= left) v[i] = 0xff800000u;
-            }
-          };
-          float mx = -INFINITY;
+            for (int i = 0; i < 32; ++i)
+              if (i >= left) v[i] = 0xff800000u;
+          }
+        };
+        float mx = -INFINITY;
+        if (warp_valid) {
 #pragma unroll 1
           for (int c = 0; c < 4; c += 2) {
             uint32_t v0[32], v1[32];
@@ -468,16 +515,39 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a, 
               for (int k = 0; k < 4; ++k) m4[k] = max3f(m4[k], __uint_as_float(v0[i + k]), __uint_as_float(v1[i + k]));
             mx = fmaxf(max3f(m4[0], m4[1], m4[2]), m4[3]);
           }
-          const float mt = mx * sl2;
-          const bool grow = mt > m_run + kPSlack;
-          const float alpha = grow ? fast_exp2(m_run - mt) : 1.f;  // 0 while m_run is -inf
-          if (grow) {
-            l_run *= alpha;
-            m_run = mt;
+        }
+        // A tile that opens a unit: the last epilogue must have read O before P V
+        // overwrites it, and the references before this tile's take their place.
+        if (j == 0 && wg > 0 && iu > 0 && !__all_sync(0xffffffffu, mbar_wait(bar(B_O_FREE), (iu - 1) & 1, abort))) {
+          failed = true;
+          break;
+        }
+        // the reference of the tile before, and this tile's
+        float m_old = -INFINITY;
+        const uint32_t kt_before = kt0 + j - 1;
+        if (j > 0) {
+          if (!__all_sync(0xffffffffu, mbar_wait(bar(B_M_FULL + before), (kt_before / 3) & 1, abort))) {
+            failed = true;
+            break;
           }
-          if (j > j0 && __any_sync(0xffffffffu, grow)) {
-            // O holds sums against the old maximum: rescale once P V of the previous tile has run
-            if (!__all_sync(0xffffffffu, mbar_wait_relaxed(bar(B_PV_DONE + odd), ((kt - 2) >> 1) & 1, abort))) {
+          m_old = m_sh[before * 128 + r];
+        }
+        const float mt = mx * sl2;
+        const bool grow = mt > m_old + kPSlack;
+        const float m_new = grow ? mt : m_old;
+        m_sh[wg * 128 + r] = m_new;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_M_FULL + wg));
+        if (warp_valid) {
+          if (m_new != m_run) {
+            l_run *= m_run == -INFINITY ? 0.f : fast_exp2(m_run - m_new);
+            m_run = m_new;
+          }
+          if (j > 0 && __any_sync(0xffffffffu, grow)) {
+            // O holds sums against the old reference: rescale once P V of the tile before
+            // has run (the one before it on that barrier had when S of that tile was issued)
+            const float alpha = grow ? fast_exp2(m_old - mt) : 1.f;  // 0 while m_old is -inf
+            if (!__all_sync(0xffffffffu, mbar_wait_relaxed(bar(B_PV_DONE + before), (kt_before / 3) & 1, abort))) {
               failed = true;
               break;
             }
@@ -485,11 +555,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a, 
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
               uint32_t v[32];
-              tmem_ld32(t_o + odd * 128 + c * 32, v);
+              tmem_ld32(t_o + c * 32, v);
               tmem_wait_ld();
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
-              tmem_st32(t_o + odd * 128 + c * 32, v);
+              tmem_st32(t_o + c * 32, v);
             }
             tmem_wait_st();
           }
@@ -520,76 +590,77 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a, 
           l_run += (l4[0] + l4[1]) + (l4[2] + l4[3]);
           tmem_wait_st();
         }
-        if (odd && j == j0 && iu > 0 &&
-            !__all_sync(0xffffffffu, mbar_wait(bar(B_O_FREE), (iu - 1) & 1, abort))) {
-          failed = true;  // P V may overwrite the odd tiles' O once the last epilogue has read it
-          break;
-        }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B_T_FULL + odd));
-        if (odd && j == j0) prepare_q(w + gridDim.x);
+        if (lane == 0) mbar_arrive(bar(B_P_FULL + wg));
+        if (wg == 2 && j == j0) prepare_q(u + 1);
       }
       if (failed) break;
-      // the unit's last tile, and the last of the other parity (if it has one)
       const uint32_t last = kt0 + n - 1;
       kt0 += n;
-      if (odd) {
-        row_buf(iu)[128 + r] = m_run;
-        row_buf(iu)[256 + r] = l_run;
+      j -= n;
+      if (wg > 0) {
+        // not before group 0 is through with the unit before: it follows these
+        // barriers one phase at a time
+        if (iu > 0 && !__all_sync(0xffffffffu, mbar_wait(bar(B_O_FREE), (iu - 1) & 1, abort))) {
+          failed = true;
+          break;
+        }
+        float* ml = row_buf(iu) + (2 * wg - 1) * 128 + r;
+        ml[0] = m_run;
+        ml[128] = l_run;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B_ML_FULL));
-        if (w + static_cast<int>(gridDim.x) < n_work) {
-          // Q is free once every S of this unit has run; the even tiles' last one
-          // is waited for here (its barrier cannot move on before the next Q is out)
-          const uint32_t k = (last & 1) ? last - 1 : last;
-          if ((n > 1 || !(last & 1)) &&
-              !__all_sync(0xffffffffu, mbar_wait_relaxed(bar(B_S_FULL), (k >> 1) & 1, abort))) {
+        if (wg == 2 && u + 1 < u1) {
+          // Q is free once the unit's last S has run (its barrier cannot move on before
+          // the next Q is out), and Q_FULL once the other groups have seen it
+          if (!__all_sync(0xffffffffu, mbar_wait(bar(B_E_IN), iu & 1, abort)) ||
+              !__all_sync(0xffffffffu, mbar_wait_relaxed(bar(B_S_FULL + last % 3), (last / 3) & 1, abort))) {
             failed = true;
             break;
           }
-          put_q(w + gridDim.x, iu + 1);
+          put_q(u + 1, iu + 1);
         }
         continue;
       }
-      const uint32_t ke = (last & 1) ? last - 1 : last, ko = (last & 1) ? last : last - 1;  // last even, last odd tile
-      const bool has_e = n > 1 || !(last & 1), has_o = n > 1 || (last & 1);
-      if ((has_e && !__all_sync(0xffffffffu, mbar_wait_relaxed(bar(B_PV_DONE), (ke >> 1) & 1, abort))) ||
-          (has_o && !__all_sync(0xffffffffu, mbar_wait_relaxed(bar(B_PV_DONE + 1), (ko >> 1) & 1, abort))) ||
-          !__all_sync(0xffffffffu, mbar_wait(bar(B_ML_FULL), iu & 1, abort))) {
+      // The other groups have handed over all their P; the last P V's commit covers all
+      // before it (the one before it on that barrier had run when the last S was issued).
+      if (!__all_sync(0xffffffffu, mbar_wait(bar(B_ML_FULL), iu & 1, abort)) ||
+          !__all_sync(0xffffffffu, mbar_wait_relaxed(bar(B_PV_DONE + last % 3), (last / 3) & 1, abort))) {
         failed = true;
         break;
       }
       tc_fence_after();
       if (warp_valid) {
-        const float m_o = row_buf(iu)[128 + r], l_o = row_buf(iu)[256 + r];
-        const bool any_e = !(l_run == 0.f), any_o = !(l_o == 0.f);  // NaN counts
-        const float M = fmaxf(any_e ? m_run : -INFINITY, any_o ? m_o : -INFINITY);
-        const float we = any_e ? fast_exp2(m_run - M) : 0.f, wo = any_o ? fast_exp2(m_o - M) : 0.f;
-        const float L = (any_e ? l_run * we : 0.f) + (any_o ? l_o * wo : 0.f);
-        const float fe = any_e ? we * kI4Unscale / L : 0.f, fo = any_o ? wo * kI4Unscale / L : 0.f;
-        const int64_t row = un.part + static_cast<int64_t>(tok) * a.Hq + (w % a.Hkv) * G + R - tok * G;
+        // O is against the last tile's reference, the largest one
+        const float* ml = row_buf(iu) + 128 + r;
+        const float m1 = ml[0], l1 = ml[128], m2 = ml[256], l2 = ml[384];
+        const float M = max3f(m_run, m1, m2);
+        auto part = [&](float m, float l) { return m == -INFINITY ? 0.f : l * fast_exp2(m - M); };
+        const float L = part(m_run, l_run) + part(m1, l1) + part(m2, l2);
+        const bool any = !(L == 0.f);  // NaN counts
+        const float inv = any ? kI4Unscale / L : 0.f;
+        const int64_t row = un.part + static_cast<int64_t>(tok) * a.Hq + (g) * G + R - tok * G;
         float* dst = a.part_o + row * kHeadDim;
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
-          uint32_t ve[32], vo[32];
-          tmem_ld32(t_o + c * 32, ve);
-          tmem_ld32(t_o + 128 + c * 32, vo);
+          uint32_t v[32];
+          tmem_ld32(t_o + c * 32, v);
           tmem_wait_ld();
           if (valid) {
-            // an O that no tile of this unit wrote holds old values: its factor is 0 and it is left out
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
               uint32_t x[8];
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                x[i] = __float_as_uint((any_e ? __uint_as_float(ve[8 * h + i]) * fe : 0.f) +
-                                       (any_o ? __uint_as_float(vo[8 * h + i]) * fo : 0.f));
+              for (int i = 0; i < 8; ++i) x[i] = __float_as_uint(__uint_as_float(v[8 * h + i]) * inv);
               st_global_v8(dst + c * 32 + h * 8, x);
             }
           }
         }
-        if (valid) a.part_lse[row] = any_e || any_o ? M - kPShift + __log2f(L) : -INFINITY;
+        if (valid) {
+          a.part_lse[row] = any ? M - kPShift + __log2f(L) : -INFINITY;
+          for (int k = 1; k <= un.n_pre; ++k) a.part_lse[row + k * un.pre_stride] = -INFINITY;
+        }
       }
       tc_fence_before();
       __syncwarp();
@@ -606,16 +677,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a, 
 
 }  // namespace
 
-int launch_i4_prefix_tc(I4Args a, int32_t unit0, int32_t n_units, cudaStream_t s, std::string* err) {
-  if (n_units == 0) return PADOC_OK;
+int launch_i4_prefix_tc(const I4Args& a, int32_t n_groups, cudaStream_t s, std::string* err) {
+  if (n_groups <= 0) return PADOC_OK;
   cudaError_t e = cudaFuncSetAttribute(prefix_i4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) {
     *err = std::string("cudaFuncSetAttribute: ") + cudaGetErrorString(e);
     return PADOC_ERR_CUDA;
   }
-  a.unit0 = unit0;
-  const int n_work = n_units * a.Hkv;
-  prefix_i4_kernel<<<std::min(n_work, num_sms()), kThreads, kSmemBytes, s>>>(a, n_work);
+  prefix_i4_kernel<<<n_groups * a.Hkv, kThreads, kSmemBytes, s>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) {
     *err = std::string("i4 prefix launch: ") + cudaGetErrorString(e);
