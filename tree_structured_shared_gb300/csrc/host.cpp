@@ -1497,9 +1497,8 @@ int plan_i4(const padoc_kv_pool* pool, const padoc_decode_batch* b, int32_t Hq, 
       own_steps += (r + kRows - 1) / kRows * blocks(s.len - s.fork_len) * pool->Hkv;
     }
   }
-  const int64_t slots = 8 * static_cast<int64_t>(n_sms);
-  const int64_t pre_chunk = std::max<int64_t>(8, std::min<int64_t>(128, pre_steps / slots));
-  const int64_t own_chunk = std::max<int64_t>(64, std::min<int64_t>(128, own_steps / slots));
+  const int64_t pre_chunk = std::max<int64_t>(8, std::min<int64_t>(128, (pre_steps + 2 * n_sms - 1) / (2 * n_sms)));
+  const int64_t own_chunk = std::max<int64_t>(64, std::min<int64_t>(128, own_steps / (8 * n_sms)));
   std::vector<I4Cut> cuts;
   {
     std::vector<I4Cut> whole;
@@ -1609,8 +1608,8 @@ int plan_i4(const padoc_kv_pool* pool, const padoc_decode_batch* b, int32_t Hq, 
   // two, four or eight (own pass of 3040 units: 40, 48, 60 and 93 us with one,
   // two, four and eight warps; of 192 units: 40, 29, 23 and 21 us).
   auto warps_of = [&](int64_t units) {
-    const int64_t a_sm = units * pool->Hkv / n_sms;
-    return a_sm >= 8 ? 1 : a_sm >= 4 ? 2 : a_sm >= 2 ? 4 : 8;
+    const int64_t n = units * pool->Hkv;
+    return n > 8 * n_sms ? 1 : n > 4 * n_sms ? 2 : n > 2 * n_sms ? 4 : 8;
   };
   pl->pre_warps = warps_of(pl->n_pre);
   pl->own_warps = warps_of(pl->n_own);
