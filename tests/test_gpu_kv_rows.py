@@ -260,6 +260,19 @@ def test_refusals_after_upload(torch):
         if what == "trimmed":
             pool.release(b)
             pool.alloc(32)  # the slot lives again, as another sequence
+    c = pool.alloc(32)
+    rows = padoc.KVRows(pool, [c], [0], [0, 32])
+    rows.upload()
+    pool.advance(c, 16)
+    pool.trim(c)                                             # its second block goes ...
+    d = pool.alloc(16)                                       # ... to another sequence,
+    pool.reserve(c, 16)                                      # and a different one comes
+    assert code_of(lambda: rows.write(t, t)) == I
+    kept = padoc.KVRows(pool, [c], [0], [0, 16])
+    kept.upload()
+    pool.release(d)
+    pool.trim(c)
+    assert code_of(lambda: kept.write(t, t)) == 0            # the block it names was kept
     dev = pool.device()
     pool.debug_rehome(dev + 1)
     assert code_of(lambda: padoc.KVRows(pool, [a], [0], [0, 2]).upload()) == I

@@ -568,6 +568,7 @@ struct Seq {
   int32_t fork_len = 0;  // leading tokens shared from the fork parent
   int32_t n_shared = 0;  // leading blocks shared from the fork parent
   uint64_t serial = 0;   // which sequence of the pool's life holds this slot
+  uint64_t trims = 0;    // times it gave blocks back
   std::vector<int32_t> blocks;
 };
 
@@ -776,6 +777,7 @@ extern "C" int padoc_kv_trim(padoc_kv_pool* pool, int32_t seq) {
   if (s.blocks.size() > keep) {
     for (size_t i = s.blocks.size(); i-- > keep;) pool->drop_block(s.blocks[i]);
     s.blocks.resize(keep);
+    ++s.trims;
     pool->mark(seq);
   }
   return PADOC_OK;
@@ -1058,7 +1060,8 @@ struct padoc_kv_rows {
   padoc_kv_pool* pool = nullptr;
   struct Range {
     int32_t seq, first, n;
-    uint64_t serial;
+    uint64_t serial, trims;
+    size_t rec0, rec1;  // its records
   };
   std::vector<Range> ranges;
   std::vector<RowRec> recs;
@@ -1090,7 +1093,7 @@ static int rows_build(padoc_kv_pool* pool, int32_t n_seqs, const int32_t* seqs, 
     if (n == 0) continue;
     if (seen[q]) r->distinct = false;
     seen[q] = 1;
-    r->ranges.push_back({q, f, n, s.serial});
+    const size_t rec0 = r->recs.size();
     // token t < fork_len sits at block t / bs of the shared blocks, an own
     // token at (t - fork_len) / bs of the own ones
     int32_t t = f, row = row_offsets[i];
@@ -1103,6 +1106,7 @@ static int rows_build(padoc_kv_pool* pool, int32_t n_seqs, const int32_t* seqs, 
       t += run;
       row += run;
     }
+    r->ranges.push_back({q, f, n, s.serial, s.trims, rec0, r->recs.size()});
     r->max_pos = std::max(r->max_pos, end - 1);
   }
   if (positions) {
@@ -1199,6 +1203,15 @@ static int rows_check(const padoc_kv_rows* rows, const char* what, bool write, c
     const Seq& s = pool->seqs[g.seq];
     if (static_cast<int64_t>(g.first) + g.n > s.fork_len + static_cast<int64_t>(pool->own_blocks(s)) * pool->bs)
       return fail(PADOC_ERR_INVALID, "%s: sequence %d gave up slots of the rows", what, g.seq);
+    if (s.trims != g.trims) {
+      // blocks given back may have come again as others
+      for (size_t k = g.rec0; k < g.rec1; ++k) {
+        const int32_t t = rows->recs[k].pos;
+        const int32_t b = t < s.fork_len ? t / pool->bs : s.n_shared + (t - s.fork_len) / pool->bs;
+        if (s.blocks[b] != rows->recs[k].block)
+          return fail(PADOC_ERR_INVALID, "%s: sequence %d gave up slots of the rows", what, g.seq);
+      }
+    }
     if (!write) {
       if (g.first + g.n > s.len)
         return fail(PADOC_ERR_INVALID, "%s: tokens [%d, %d) of sequence %d, which holds %d", what, g.first, g.first + g.n,
