@@ -25,16 +25,17 @@
 //   Q 32 KB | K 2 x 32 KB | V 2 x 32 KB | codes 3 x 18 KB | row data | barriers
 //
 // What bounds it: a tile's products take 1024 cycles of the tensor pipe, its 16384
-// exponentials as many, decoding it about 1100; a tile takes about 2100, since the
-// roles' waits on one another do not all overlap.  128 pages of 4000-6144 tokens with
-// 8-60 branches take 380 us (112 us at HBM rate), 64 pages of 4809 tokens with 8-40
-// branches of up to 16 query tokens 601 us.  Steps behind it: one softmax group per
-// tile in turn, of two, made the groups' chains of loads and waits the bound (640 us
-// on the 64 pages); one thread issuing both products spent 2240 cycles a tile on
-// issue and waits; without decoding it takes 490 us, with the products alone 336.
-// The decoders and the softmax walk their tiles in short loops: long straight-
-// line streams, three a scheduler, starved on instruction fetches (3300 cycles a
-// tile at 0.4 instructions a cycle).
+// exponentials as many, decoding it about 1100; a tile takes about 1950.  Five warps a
+// scheduler run different code and starve on instruction fetches, so what shortens the
+// loops counts: first pass over S of 32 columns instead of 64 a round, masked scores put
+// back by the first pass instead of masked again by the second, K and V decoded by the
+// same instructions (380 -> 343 us and 601 -> 572 us on the two cases below); half the
+// columns a round in the second pass, or half the words in the decoders', costs 3 %,
+// twice the columns 10 %.  Two softmax groups instead of three make their chains of
+// loads and waits the bound (640 us); one thread issuing both products spends 2240
+// cycles a tile on issue and waits.  The products alone take 336 us of the 572.
+//   128 pages of 4000-6144 tokens with 8-60 branches: 343 us (112 at HBM rate)
+//   64 pages of 4809 tokens, 8-40 branches of up to 16 query tokens: 572 us
 //
 // A wait names a phase by its parity, so every waiter knows the phase before to be
 // over: from the barriers that it waited for, or from what the phase's arrivals
@@ -66,7 +67,8 @@ using namespace ptx;
 constexpr int kThreads = 768;
 // registers a thread of each role, dealt from the 80 a thread that 768 threads start with
 constexpr int kRegsSoft = 104, kRegsDec = 64, kRegsMma = 40;
-static_assert(384 * kRegsSoft + 256 * kRegsDec + 128 * kRegsMma <= 80 * kThreads, "register budget");
+constexpr int kRegsLaunch = 80;
+static_assert(384 * kRegsSoft + 256 * kRegsDec + 128 * kRegsMma <= kRegsLaunch * kThreads, "register budget");
 constexpr int kHalf = 16384;  // one 64-column half of a 128-row tile
 constexpr int kTileBytes = 2 * kHalf;
 constexpr int kCStages = 3;          // ring of codes
@@ -130,9 +132,9 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool o
   else
     asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(n), "n"(N) : "memory");
 }
-__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+__device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
   return v;
 }
 __device__ __forceinline__ uint32_t ld_shared_u16(uint32_t addr) {
@@ -237,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a) 
     // neighbours write eight different banks' pieces
     const int hi = s16 >> 3, swap = (s16 >> 2) & 1;
     const int ka = is_k ? t : tb * 16 + 2 * (s16 & 7) + swap, kb = is_k ? t : ka ^ 1;
-    const int first = is_k ? 0 : 2 * hi;
+    const int first = is_k ? 0 : 2 * hi, sw = is_k ? 0 : swap * 8;
     uint32_t to[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -261,47 +263,34 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a) 
           break;
         }
         const uint32_t tile = tiles + st * kTileBytes;
-        if (is_k) {
-          // keys past the end are zero or old bytes: their scores are masked
+        // Keys past the end may hold old bytes: K's scores are masked, V's scales become
+        // zero.  K and V run the same instructions (see the top) but for their scales:
+        // K's groups 4 x .. 4 x + 3 of its slot; V's of its two slots, in the order they
+        // are written, in the groups 4 x + hi and 4 x + 2 + hi.
+        const int left = n_keys - k0 - tb * 16 - 2 * (s16 & 7);
+        const uint32_t keep = left >= 2 ? 0xffffu : left == 1 ? 0xffu : 0u;
 #pragma unroll 1
-          for (int x = 0; x < 2; ++x) {
-            const uint32_t src = codes + x * 4096 + t * 16, dst = tile + x * kHalf;
-            const uint32_t sc = ld_shared_u32(codes + kCodes + t * 8 + x * 4);
-            const uint4 c0 = ld_shared_v4(src), c1 = ld_shared_v4(src + 2048);
-            const I4Scale s0 = i4_scale_both<0>(sc), s1 = i4_scale_both<1>(sc);
-            put_word(dst + to[0], c0.x, s0);
-            put_word(dst + to[1], c0.y, s0);
-            put_word(dst + to[2], c0.z, s1);
-            put_word(dst + to[3], c0.w, s1);
-            const I4Scale s2 = i4_scale_both<2>(sc), s3 = i4_scale_both<3>(sc);
-            put_word(dst + (to[0] ^ 64), c1.x, s2);
-            put_word(dst + (to[1] ^ 64), c1.y, s2);
-            put_word(dst + (to[2] ^ 64), c1.z, s3);
-            put_word(dst + (to[3] ^ 64), c1.w, s3);
+        for (int x = 0; x < 2; ++x) {
+          const uint32_t src = codes + x * 4096 + t * 16, dst = tile + x * kHalf;
+          uint32_t sc;
+          if (is_k) {
+            sc = ld_shared_u32(codes + kCodes + t * 8 + x * 4);
+          } else {
+            const uint32_t at = codes + kCodes + tb * 128 + (4 * x + hi) * 16 + 2 * (s16 & 7);
+            sc = __byte_perm(ld_shared_u16(at) & keep, ld_shared_u16(at + 32) & keep, swap ? 0x4501u : 0x5410u);
           }
-        } else {
-          // keys past the end may hold old bytes and must not be NaN: scales of zero
-          const int left = n_keys - k0 - tb * 16 - 2 * (s16 & 7);
-          const uint32_t keep = left >= 2 ? 0xffffu : left == 1 ? 0xffu : 0u;
-          const uint32_t sel = swap ? 0x4401u : 0x4410u;  // the slots' scales in the order they are written
-#pragma unroll 1
-          for (int x = 0; x < 2; ++x) {
-            const uint32_t src = codes + x * 4096 + t * 16, dst = tile + x * kHalf;
-            // groups 4 x + hi and 4 x + 2 + hi
-            const uint32_t sc = codes + kCodes + tb * 128 + (4 * x + hi) * 16 + 2 * (s16 & 7);
-            const uint32_t b0 = __byte_perm(ld_shared_u16(sc) & keep, 0u, sel), b1 = __byte_perm(ld_shared_u16(sc + 32) & keep, 0u, sel);
-            const uint4 c0 = ld_shared_v4(src), c1 = ld_shared_v4(src + 2048);
-            const I4Scale s0 = i4_scale_both<0>(b0), s1 = i4_scale_both<1>(b0);
-            put_word(dst + to[0], swap ? c0.z : c0.x, s0);
-            put_word(dst + to[1], swap ? c0.w : c0.y, s0);
-            put_word(dst + to[2], swap ? c0.x : c0.z, s1);
-            put_word(dst + to[3], swap ? c0.y : c0.w, s1);
-            const I4Scale s2 = i4_scale_both<0>(b1), s3 = i4_scale_both<1>(b1);
-            put_word(dst + (to[0] ^ 64), swap ? c1.z : c1.x, s2);
-            put_word(dst + (to[1] ^ 64), swap ? c1.w : c1.y, s2);
-            put_word(dst + (to[2] ^ 64), swap ? c1.x : c1.z, s3);
-            put_word(dst + (to[3] ^ 64), swap ? c1.y : c1.w, s3);
-          }
+          const uint2 c0 = ld_shared_v2(src + sw), c1 = ld_shared_v2(src + (sw ^ 8));
+          const uint2 c2 = ld_shared_v2(src + 2048 + sw), c3 = ld_shared_v2(src + 2048 + (sw ^ 8));
+          const I4Scale s0 = i4_scale_both<0>(sc), s1 = i4_scale_both<1>(sc);
+          put_word(dst + to[0], c0.x, s0);
+          put_word(dst + to[1], c0.y, s0);
+          put_word(dst + to[2], c1.x, s1);
+          put_word(dst + to[3], c1.y, s1);
+          const I4Scale s2 = i4_scale_both<2>(sc), s3 = i4_scale_both<3>(sc);
+          put_word(dst + (to[0] ^ 64), c2.x, s2);
+          put_word(dst + (to[1] ^ 64), c2.y, s2);
+          put_word(dst + (to[2] ^ 64), c3.x, s3);
+          put_word(dst + (to[3] ^ 64), c3.y, s3);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -472,6 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a) 
       const bool valid = r < rows, warp_valid = wq * 32 < rows;
       const int R = un.row0 + r, tok = div_g(R, a.g_inv);
       const int limit = valid ? min(n_keys, a.q_plen[un.q_first + tok] - un.key0) : n_keys;
+      const int limit_min = __reduce_min_sync(0xffffffffu, limit);
       if (!__all_sync(0xffffffffu, mbar_wait(bar(B_Q_FULL), iu & 1, abort))) {
         failed = true;
         break;
@@ -489,7 +479,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a) 
           break;
         }
         tc_fence_after();
-        const int vis = limit - j * kTileKeys;  // keys [0, vis) of the tile are visible
+        // keys [0, vis) of the tile are visible to the row, [0, vis_min) to the warp's rows
+        const int vis = limit - j * kTileKeys, vis_min = limit_min - j * kTileKeys;
         auto mask32 = [&](int c, uint32_t (&v)[32]) {
           const int left = vis - c * 32;
           if (left < 32) {
@@ -501,18 +492,22 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a) 
         float mx = -INFINITY;
         if (warp_valid) {
 #pragma unroll 1
-          for (int c = 0; c < 4; c += 2) {
-            uint32_t v0[32], v1[32];
+          for (int c = 0; c < 4; ++c) {
+            uint32_t v0[32];
             tmem_ld32(t_s + c * 32, v0);
-            tmem_ld32(t_s + c * 32 + 32, v1);
             tmem_wait_ld();
-            mask32(c, v0);
-            mask32(c + 1, v1);
+            if (vis_min < c * 32 + 32) {
+              // masked scores go back, for the second pass (the whole warp stores)
+              mask32(c, v0);
+              __syncwarp();
+              tmem_st32(t_s + c * 32, v0);
+              tmem_wait_st();
+            }
             float m4[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int i = 0; i < 32; i += 4)
+            for (int i = 0; i < 32; i += 8)
 #pragma unroll
-              for (int k = 0; k < 4; ++k) m4[k] = max3f(m4[k], __uint_as_float(v0[i + k]), __uint_as_float(v1[i + k]));
+              for (int k = 0; k < 4; ++k) m4[k] = max3f(m4[k], __uint_as_float(v0[i + k]), __uint_as_float(v0[i + 4 + k]));
             mx = fmaxf(max3f(m4[0], m4[1], m4[2]), m4[3]);
           }
         }
@@ -571,7 +566,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a) 
             uint32_t v[32], pk[16];
             tmem_ld32(t_s + c * 32, v);
             tmem_wait_ld();
-            mask32(c, v);
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
               float x0, x1;
@@ -682,6 +676,15 @@ int launch_i4_prefix_tc(const I4Args& a, int32_t n_groups, cudaStream_t s, std::
   cudaError_t e = cudaFuncSetAttribute(prefix_i4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) {
     *err = std::string("cudaFuncSetAttribute: ") + cudaGetErrorString(e);
+    return PADOC_ERR_CUDA;
+  }
+  // the roles draw on the registers that the block starts with
+  static const int regs = [] {
+    cudaFuncAttributes f{};
+    return cudaFuncGetAttributes(&f, prefix_i4_kernel) == cudaSuccess ? f.numRegs : 0;
+  }();
+  if (regs < kRegsLaunch) {
+    *err = "the i4 prefix kernel was built for " + std::to_string(regs) + " registers a thread";
     return PADOC_ERR_CUDA;
   }
   prefix_i4_kernel<<<n_groups * a.Hkv, kThreads, kSmemBytes, s>>>(a);
