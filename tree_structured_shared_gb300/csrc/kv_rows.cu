@@ -18,6 +18,14 @@
 // that turn is the pairs' first dims and B their second, so a rotation needs no
 // exchange between lanes; elsewhere A and B are neighbours.
 // Small record lists ride in the kernel's parameters: no upload is needed.
+//
+// Measured (16 query heads, 8 kv heads, all dims turned): 16 x 4809 rows into a bf16
+// pool in 225 us, 6.3 TB/s; 64 x 4809 rows into a 4-bit pool and back out in 1190 us
+// (941 at HBM rate): the write, about 200 warp instructions a (token, kv head) to
+// scale and round, is bound by instruction issue, the way back by HBM (64 pages of
+// 4000-6144 tokens in 260 us, 6.6 TB/s).  384 rows of one token take 4 us.  Finer or
+// coarser splits of a token's heads over the warps: the same or slower (1-16 rows of
+// 1490 sequences, write and way back: 82 us; two warps a token 84, eight 121).
 #include <cuda_bf16.h>
 
 #include <string>
