@@ -222,6 +222,99 @@ def test_nan_stays_with_the_rows_that_see_it(harness):
     assert change("q", None, (5, 2, 3), np.nan) == [5]
 
 
+def test_nan_on_wide_pages(harness):
+    """The same where a page has 80 query rows: a poisoned token of the prefix, infinite and NaN queries."""
+    forks = [400] * 5 + [250] * 5
+    w = wl.DecodeWorkload("n", [page(400, forks, [20] * 10, [4] * 10)], 4, 2, 128, 1.0)
+    clean = wl.decode_values(w, 5)
+    base, lse0, _ = run(harness, w, clean, tree=False)
+
+    def rows_hit(vals):
+        o, lse, _ = run(harness, w, vals, tree=False)
+        hit = np.isnan(o).any(-1) | np.isnan(lse)
+        ok = ~hit
+        # the others see nothing of it: not a bit changes
+        assert np.array_equal(o[ok], base[ok]) and np.array_equal(lse[ok], lse0[ok])
+        return sorted({int(r) for r in np.nonzero(hit)[0]})
+
+    def change(field, i, idx, value):
+        vals = copy.deepcopy(clean)
+        x = getattr(vals, field) if i is None else getattr(vals, field)[i]
+        x[idx] = value
+        return rows_hit(vals)
+
+    assert change("prefix_k", 0, (399, 1, 5), np.nan) == list(range(20))  # branches 5 .. 9 end at 250
+    assert change("prefix_v", 0, (250, 0, 77), np.inf) == list(range(20))
+    assert change("prefix_v", 0, (0, 0, 0), -np.inf) == list(range(40))
+    # 8 rows share a factor in the own pass, the row alone has one in the prefix pass
+    assert change("q", None, (21, 3, 9), np.nan) == [21]
+
+
+def test_noalloc_and_plan_agree(harness):
+    """The workspace call, the plan's two passes and the call without allocation give the same bits."""
+    import torch
+    w = wl.small_decode(21, n_pages=3, max_prefix=700, max_branches=8, max_own=300, Hq=8, Hkv=2)
+    vals = wl.decode_values(w, 21)
+    o, lse, d = run(harness, w, vals)
+    d.o.zero_()
+    padoc.branch_decode_noalloc(d.pool, d.batch, 8, d.q, d.k_new, d.v_new, d.tree_bits, d.o, d.lse)
+    torch.cuda.synchronize()
+    n = w.n_queries
+    assert np.array_equal(d.o.float().cpu().numpy()[:n], o) and np.array_equal(d.lse.cpu().numpy()[:n], lse)
+    d.plan()
+    d.o.zero_()
+    d.prefix_pass()
+    d.own_pass()
+    torch.cuda.synchronize()
+    assert np.array_equal(d.o.float().cpu().numpy()[:n], o) and np.array_equal(d.lse.cpu().numpy()[:n], lse)
+
+
+@pytest.mark.parametrize("dtype", [padoc.BF16, padoc.I4])
+def test_blocks_far_into_a_large_pool(harness, dtype):
+    """Blocks whose bytes start past 2^32: rows written, decoded (few and many query rows) and read back as in a small pool."""
+    import torch
+    Hkv, Hq, rng = 8, 16, np.random.default_rng(9)
+    far = (2 ** 32 // (Hkv * (1152 if dtype == padoc.I4 else 4096))) + 100
+    dev = lambda *s: torch.from_numpy(rng.normal(size=s).astype(np.float32)).to(torch.bfloat16).cuda()  # noqa: E731
+    pk, pv, ok, ov = dev(333, Hkv, 128), dev(333, Hkv, 128), dev(70, Hkv, 128), dev(70, Hkv, 128)
+    q, kn, vn = dev(14, Hq, 128), dev(14, Hkv, 128), dev(14, Hkv, 128)
+    tab = torch.from_numpy(i4ref.rope_table(400, 128)).cuda()
+    got = []
+    for skip in (0, far):
+        nb = skip + 64
+        size = padoc.kv_storage_bytes(nb, Hkv, dtype=dtype)
+        kp, vp = (torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(2))
+        pool = padoc.KVPool(kp, vp, nb, Hkv, max_seqs=8, max_blocks_per_seq=max(skip, 32), dtype=dtype)
+        if skip:
+            pool.alloc(16 * skip)
+        p = pool.alloc(0)
+        pool.append_rope([p], [0, 333], pk, pv, rope=padoc.Rope(tab, 128))
+        assert min(pool.seq_blocks(p)) >= skip
+        br = [pool.fork(p, 333), pool.fork(p, 200)]
+        for b in br:
+            pool.append(b, ok, ov, 70)
+        out = []
+        for off in ([0, 1, 2], [0, 7, 14]):  # 4 and 28 query rows a kv head
+            batch = padoc.Batch([p], [0, 2], br, off)
+            n = padoc.branch_decode_ws_size(pool, batch, Hq)
+            ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+            o = torch.zeros(14, Hq, 128, dtype=torch.bfloat16, device="cuda")
+            lse = torch.zeros(14, Hq, device="cuda")
+            padoc.branch_decode(pool, batch, Hq, q, kn, vn, None, o, lse, ws, n)
+            out += [o, lse]
+        back = padoc.KVRows(pool, br, [0, 0], [0, 403, 673])
+        back.upload()
+        k, v = (torch.empty(673, Hkv, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        back.gather(k, v)
+        torch.cuda.synchronize()
+        padoc.device_status()
+        got.append([x.cpu() for x in out + [k, v]])
+        del kp, vp, pool
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    assert got[0][0].abs().sum() > 0 and got[0][-1].abs().sum() > 0
+
+
 def test_stale_blocks(harness):
     """Slots past a sequence's end keep what an earlier, poisoned sequence left there."""
     import torch
