@@ -33,7 +33,11 @@
 // columns a round in the second pass, or half the words in the decoders', costs 3 %,
 // twice the columns 10 %.  Two softmax groups instead of three make their chains of
 // loads and waits the bound (640 us); one thread issuing both products spends 2240
-// cycles a tile on issue and waits.  The products alone take 336 us of the 572.
+// cycles a tile on issue and waits.  The products alone take 336 us of the 572.  What
+// sets the period now is the way round one S buffer, three tiles long: S issued in 900
+// cycles, first pass 1000, second 1700, P V issued in 800, and some 450 between any
+// two (issue code with constant stages and buffers, or more registers for it: 2 to 6 %
+// slower).
 //   128 pages of 4000-6144 tokens with 8-60 branches: 343 us (112 at HBM rate)
 //   64 pages of 4809 tokens, 8-40 branches of up to 16 query tokens: 572 us
 //
@@ -69,6 +73,8 @@ constexpr int kThreads = 768;
 constexpr int kRegsSoft = 104, kRegsDec = 64, kRegsMma = 40;
 constexpr int kRegsLaunch = 80;
 static_assert(384 * kRegsSoft + 256 * kRegsDec + 128 * kRegsMma <= kRegsLaunch * kThreads, "register budget");
+static_assert(kRegsSoft >= kRegsLaunch && kRegsDec <= kRegsLaunch && kRegsMma <= kRegsLaunch,
+              "a role may only grow by the increasing form and shrink by the other");
 constexpr int kHalf = 16384;  // one 64-column half of a 128-row tile
 constexpr int kTileBytes = 2 * kHalf;
 constexpr int kCStages = 3;          // ring of codes
