@@ -33,13 +33,14 @@
 // columns a round in the second pass, or half the words in the decoders', costs 3 %,
 // twice the columns 10 %.  Two softmax groups instead of three make their chains of
 // loads and waits the bound (640 us); one thread issuing both products spends 2240
-// cycles a tile on issue and waits.  The products alone take 336 us of the 572.  What
+// cycles a tile on issue and waits.  The products alone take 336 us of the 564.  What
 // sets the period now is the way round one S buffer, three tiles long: S issued in 900
 // cycles, first pass 1000, second 1700, P V issued in 800, and some 450 between any
-// two (issue code with constant stages and buffers, or more registers for it: 2 to 6 %
-// slower).
-//   128 pages of 4000-6144 tokens with 8-60 branches: 343 us (112 at HBM rate)
-//   64 pages of 4809 tokens, 8-40 branches of up to 16 query tokens: 572 us
+// two (P handed over in two halves, and the reference waited for ahead of S, took 2 %
+// off; issue code with constant stages and buffers, or more registers for it, costs 2
+// to 6 %).
+//   128 pages of 4000-6144 tokens with 8-60 branches: 336 us (112 at HBM rate)
+//   64 pages of 4809 tokens, 8-40 branches of up to 16 query tokens: 564 us
 //
 // A wait names a phase by its parity, so every waiter knows the phase before to be
 // over: from the barriers that it waited for, or from what the phase's arrivals
@@ -95,13 +96,14 @@ enum {
   B_K_FULL = 2,   // +stage (2), count 4
   B_V_FULL = 4,   // +stage (2), count 4
   B_M_FULL = 6,   // +group (3), count 4: the tile's references are in shared memory
-  B_P_FULL = 9,   // +group (3), count 4
-  B_ML_FULL = 12, // count 8: groups 1's and 2's references and sums are in shared memory
-  B_E_IN = 13,    // count 8: groups 0 and 1 have entered the unit
-  B_PV_DONE = 14, // +group (3): P V of the tile has run, its V stage and S buffer free
-  B_S_FULL = 17,  // +group (3): S of the tile is in TMEM, its K stage free
-  B_DRAIN = 20,   // count 2: the issuers' last commits
-  N_BARS = 21
+  B_P_FULL = 9,   // +group (3), count 4: and of the others
+  B_P_HALF = 12,  // +group (3), count 4: P of the tile's first 64 keys
+  B_ML_FULL = 15, // count 8: groups 1's and 2's references and sums are in shared memory
+  B_E_IN = 16,    // count 8: groups 0 and 1 have entered the unit
+  B_PV_DONE = 17, // +group (3): P V of the tile has run, its V stage and S buffer free
+  B_S_FULL = 20,  // +group (3): S of the tile is in TMEM, its K stage free
+  B_DRAIN = 23,   // count 2: the issuers' last commits
+  N_BARS = 24
 };
 // The commits of S and P V free the stages that they read too: each wait and commit
 // between two groups of products is time in which the issuing thread stands still.
@@ -356,16 +358,24 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a) 
         for (int j = 0; j < n; ++j, ++k) {
           const int st = k & 1;
           if (!mbar_wait_relaxed(bar(B_V_FULL + st), (k >> 1) & 1, abort) ||
-              !mbar_wait_relaxed(bar(B_P_FULL + pb), round & 1, abort)) {
+              !mbar_wait_relaxed(bar(B_P_HALF + pb), round & 1, abort)) {
             failed = true;
             break;
           }
           tc_fence_after();
           const uint64_t d_v = sdesc_sw128(sbase + SM_V + st * kTileBytes, kHalf, 1024);
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
+          for (int kk = 0; kk < 4; ++kk)
             mma_bf16_ts(tmem + kTmemO, tmem + pb * 128 + kk * 8, d_v + static_cast<uint64_t>(kk * (2048 >> 4)), id_pv,
                         (j > 0 || kk > 0) ? 1u : 0u);
+          if (!mbar_wait_relaxed(bar(B_P_FULL + pb), round & 1, abort)) {
+            failed = true;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 4; kk < 8; ++kk)
+            mma_bf16_ts(tmem + kTmemO, tmem + pb * 128 + kk * 8, d_v + static_cast<uint64_t>(kk * (2048 >> 4)), id_pv, 1u);
           mma_commit(bar(B_PV_DONE + pb));
           if (++pb == 3) {
             pb = 0;
@@ -480,6 +490,22 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a) 
       const int j0 = j;
       float m_run = -INFINITY, l_run = 0.f;     // the reference last used here, the sum against it
       for (; j < n; j += 3, ++round) {
+        // A tile that opens a unit: the last epilogue must have read O before P V
+        // overwrites it, and the references before this tile's take their place.
+        if (j == 0 && wg > 0 && iu > 0 && !__all_sync(0xffffffffu, mbar_wait(bar(B_O_FREE), (iu - 1) & 1, abort))) {
+          failed = true;
+          break;
+        }
+        // the reference of the tile before, long there when S of this one is
+        float m_old = -INFINITY;
+        const uint32_t kt_before = kt0 + j - 1;
+        if (j > 0) {
+          if (!__all_sync(0xffffffffu, mbar_wait(bar(B_M_FULL + before), (kt_before / 3) & 1, abort))) {
+            failed = true;
+            break;
+          }
+          m_old = m_sh[before * 128 + r];
+        }
         if (!__all_sync(0xffffffffu, mbar_wait_relaxed(bar(B_S_FULL + wg), round & 1, abort))) {
           failed = true;
           break;
@@ -516,22 +542,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a) 
               for (int k = 0; k < 4; ++k) m4[k] = max3f(m4[k], __uint_as_float(v0[i + k]), __uint_as_float(v0[i + 4 + k]));
             mx = fmaxf(max3f(m4[0], m4[1], m4[2]), m4[3]);
           }
-        }
-        // A tile that opens a unit: the last epilogue must have read O before P V
-        // overwrites it, and the references before this tile's take their place.
-        if (j == 0 && wg > 0 && iu > 0 && !__all_sync(0xffffffffu, mbar_wait(bar(B_O_FREE), (iu - 1) & 1, abort))) {
-          failed = true;
-          break;
-        }
-        // the reference of the tile before, and this tile's
-        float m_old = -INFINITY;
-        const uint32_t kt_before = kt0 + j - 1;
-        if (j > 0) {
-          if (!__all_sync(0xffffffffu, mbar_wait(bar(B_M_FULL + before), (kt_before / 3) & 1, abort))) {
-            failed = true;
-            break;
-          }
-          m_old = m_sh[before * 128 + r];
         }
         const float mt = mx * sl2;
         const bool grow = mt > m_old + kPSlack;
@@ -583,12 +593,21 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a) 
             }
             // over columns of S that this loop has read
             tmem_st16(t_s + c * 16, pk);
+            if (c == 1) {
+              tmem_wait_st();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar(B_P_HALF + wg));
+              __syncwarp();
+            }
           }
           float l4[4];
           f2unpack(l2[0], l4[0], l4[1]);
           f2unpack(l2[1], l4[2], l4[3]);
           l_run += (l4[0] + l4[1]) + (l4[2] + l4[3]);
           tmem_wait_st();
+        } else if (lane == 0) {
+          mbar_arrive(bar(B_P_HALF + wg));
         }
         tc_fence_before();
         __syncwarp();
