@@ -354,6 +354,7 @@ PADOC_API int padoc_tree_desc_bwd_plan(const padoc_tree_desc* desc, int32_t* ite
  * step whose pages each fit one prefix chunk (see padoc_decode_plan_fused)
  * runs as one kernel that walks, per row tile, the prefix, the own suffixes
  * and the query block in a single running softmax.
+ * A pool of either dtype will do; the fused verify step is the bf16 pool's.
  * ---------------------------------------------------------------------- */
 typedef struct {
   int32_t n_pages;

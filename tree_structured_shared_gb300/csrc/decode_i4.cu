@@ -30,9 +30,9 @@
 //
 // What bounds it: a key costs a warp about 25 instructions for a head's 8 rows, and
 // four warps a scheduler (126 registers) issue one every other cycle.  Suffixes of 4500
-// branches (0-1024 tokens, 8 kv heads): 565 us, of which the copies alone take 449 (404
+// branches (0-1024 tokens, 8 kv heads): 564 us, of which the copies alone take 449 (404
 // at HBM rate) and the arithmetic alone 490; 1500 branches with up to 16 query tokens:
-// 336 us (237 at HBM rate).  Neither more independent products (two blocks' score
+// 335 us (237 at HBM rate).  Neither more independent products (two blocks' score
 // chains interleaved, accumulators split) nor shorter loops nor the query block and
 // the partial results fetched ahead change that by more than 1 %.
 //

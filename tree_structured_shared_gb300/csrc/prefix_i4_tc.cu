@@ -25,7 +25,7 @@
 //   Q 32 KB | K 2 x 32 KB | V 2 x 32 KB | codes 3 x 18 KB | row data | barriers
 //
 // What bounds it: a tile's products take 1024 cycles of the tensor pipe, its 16384
-// exponentials as many, decoding it about 1100; a tile takes about 1950.  Five warps a
+// exponentials as many, decoding it about 1100; a tile takes about 1950.  Six warps a
 // scheduler run different code and starve on instruction fetches, so what shortens the
 // loops counts: first pass over S of 32 columns instead of 64 a round, masked scores put
 // back by the first pass instead of masked again by the second, K and V decoded by the
