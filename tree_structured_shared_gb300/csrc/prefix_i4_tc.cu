@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a) 
           }
         }
         const float mt = mx * sl2;
-        const bool grow = mt > m_old + kPSlack;
+        const bool grow = valid && mt > m_old + kPSlack;  // what Q's buffer held in other rows asks for no rescaling
         const float m_new = grow ? mt : m_old;
         m_sh[wg * 128 + r] = m_new;
         __syncwarp();
