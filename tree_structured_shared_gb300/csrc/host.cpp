@@ -1445,7 +1445,9 @@ struct I4Cut {
 // Deals the pages' prefixes out to at most n_groups groups of CTAs (one a kv head),
 // each about as many tiles as the others: a run is cut where a group is full.  A piece
 // costs about two tiles' time beside its own for starting and ending it; pieces
-// shorter than four tiles are left to prefixes of that length.
+// shorter than four tiles are left to prefixes of that length (pieces of two: prefix
+// pass of a page of 2048 tokens 12 us instead of 14, but its own pass, with twice the
+// results to join, 16 instead of 14; 7 uneven pages 57 us instead of 54).
 void deal_prefixes(const std::vector<I4Cut>& whole, int32_t n_groups, std::vector<I4Cut>* cuts) {
   constexpr int64_t kUnit = 2, kLeast = 4;
   int64_t total = 0;
@@ -1494,10 +1496,16 @@ int plan_i4(const padoc_kv_pool* pool, const padoc_decode_batch* b, int32_t Hq, 
             DecodePlan* pl) {
   const int32_t G = Hq / pool->Hkv, bs = pool->bs, nq = static_cast<int32_t>(pl->q_plen.size());
   constexpr int32_t kRows = 8;  // rows of a warp-level unit
-  auto on_tc = [](int32_t rows) { return rows > 16; };  // prefix units on the tcgen05 kernel
+  // Prefix units on the tcgen05 kernel where the rows are more than one warp-level
+  // tile (64 pages of 5000 tokens: 154 us against 91, 172 and 216 us of the warp-level
+  // kernel with 8, 12-16 and 20 rows; 8 pages: 31 against 23, 31 and 37; one page: 15
+  // against 13 with 8 to 20).
+  auto on_tc = [](int32_t rows) { return rows > kRows; };
   auto blocks = [bs](int64_t n) { return (n + bs - 1) / bs; };
-  // Chunks of keys: about eight units an SM, within 128 blocks and no less than 8 (a
-  // page's prefix) or 64 (a branch's own keys, whose chunks cost a merge).
+  // Chunks of keys: of a page's prefix with few rows about two units an SM, which eight
+  // warps each share, within 8 to 128 blocks (one branch on 131072 tokens, with the
+  // merge of its results: 31 us; eight units an SM and one warp each: 41 us).  Of a
+  // branch's own keys, whose chunks cost a merge, no less than 64 blocks.
   int64_t pre_steps = 0, own_steps = 0;
   for (int32_t p = 0; p < b->n_pages; ++p) {
     const int32_t b0 = b->branch_offsets[p], b1 = b->branch_offsets[p + 1];
@@ -1580,8 +1588,9 @@ int plan_i4(const padoc_kv_pool* pool, const padoc_decode_batch* b, int32_t Hq, 
       const int32_t oc = std::max<int32_t>(1, static_cast<int32_t>((osteps + most - 1) / most));
       const int64_t oper = (osteps + oc - 1) / oc;
       const int32_t n_own = oper ? static_cast<int32_t>((osteps + oper - 1) / oper) : 1;
-      // Few partial results join in the own unit's epilogue (one after another
-      // there); many in the merge kernel.
+      // Few partial results join in the own unit's epilogue (one after another there);
+      // many in the merge kernel (own pass of a page with 24 branches: 17 us in the
+      // epilogue and 21 with the kernel for 4 results, 23 and 21 for 12, 31 and 21 for 19).
       const bool merge = n_own > 1 || made > 8;
       const int64_t pre_at = pre_base + static_cast<int64_t>(qf - q0) * Hq;
       const int64_t own_base = rows, own_stride = static_cast<int64_t>(ql) * Hq;
