@@ -242,16 +242,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a) 
     open_unit();
     read_id();
     for (int cs = 0; cs < kCStages; ++cs) copy_tile(stage0 + cs * kCStage);
-    // where the thread's pieces of an operand tile go: K, row t; V, the rows of its
-    // two slots, the upper four pairs of slots the other way round, so that eight
-    // neighbours write eight different banks' pieces
-    const int hi = s16 >> 3, swap = (s16 >> 2) & 1;
-    const int ka = is_k ? t : tb * 16 + 2 * (s16 & 7) + swap, kb = is_k ? t : ka ^ 1;
-    const int first = is_k ? 0 : 2 * hi, sw = is_k ? 0 : swap * 8;
+    // Where the thread's pieces of an operand tile go: K, row t; V, the rows of its two
+    // slots.  A thread reads its 16 bytes of codes in two halves, some the upper one
+    // first (swap), so that sixteen neighbours read every bank once (thread s and s + 8
+    // start with different halves) and eight neighbours write eight different banks'
+    // pieces.  K's halves are two groups of dims, V's the two slots.
+    const int hi = s16 >> 3, swap = is_k ? hi : hi ^ ((s16 >> 2) & 1), sw = swap * 8;
     uint32_t to[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int row = is_k || k < 2 ? ka : kb, piece = first + (is_k ? k : k & 1);
+      const int row = is_k ? t : tb * 16 + 2 * (s16 & 7) + ((k >> 1) ^ swap);
+      const int piece = is_k ? k ^ (2 * swap) : 2 * hi + (k & 1);
       to[k] = row * 128 + ((piece ^ (row & 7)) << 4);
     }
     const uint32_t tiles = sbase + (is_k ? SM_K : SM_V);
@@ -273,8 +274,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a) 
         const uint32_t tile = tiles + st * kTileBytes;
         // Keys past the end may hold old bytes: K's scores are masked, V's scales become
         // zero.  K and V run the same instructions (see the top) but for their scales:
-        // K's groups 4 x .. 4 x + 3 of its slot; V's of its two slots, in the order they
-        // are written, in the groups 4 x + hi and 4 x + 2 + hi.
+        // K's groups 4 x .. 4 x + 3 of its slot, V's of its two slots in the groups 4 x + hi
+        // and 4 x + 2 + hi, in the order in which they are used.
         const int left = n_keys - k0 - tb * 16 - 2 * (s16 & 7);
         const uint32_t keep = left >= 2 ? 0xffffu : left == 1 ? 0xffu : 0u;
 #pragma unroll 1
@@ -282,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a) 
           const uint32_t src = codes + x * 4096 + t * 16, dst = tile + x * kHalf;
           uint32_t sc;
           if (is_k) {
-            sc = ld_shared_u32(codes + kCodes + t * 8 + x * 4);
+            sc = __byte_perm(ld_shared_u32(codes + kCodes + t * 8 + x * 4), 0u, swap ? 0x2301u : 0x3210u);
           } else {
             const uint32_t at = codes + kCodes + tb * 128 + (4 * x + hi) * 16 + 2 * (s16 & 7);
             sc = __byte_perm(ld_shared_u16(at) & keep, ld_shared_u16(at + 32) & keep, swap ? 0x4501u : 0x5410u);
