@@ -24,23 +24,28 @@
 // Shared memory (operand tiles in two 64-column halves, 128-byte swizzle):
 //   Q 32 KB | K 2 x 32 KB | V 2 x 32 KB | codes 3 x 18 KB | row data | barriers
 //
-// What bounds it: a tile's products take 1024 cycles of the tensor pipe, its 16384
-// exponentials as many, decoding it about 1100; a tile takes about 1950.  Six warps a
-// scheduler run different code and starve on instruction fetches, so what shortens the
-// loops counts: first pass over S of 32 columns instead of 64 a round, masked scores put
-// back by the first pass instead of masked again by the second, K and V decoded by the
-// same instructions (380 -> 343 us and 601 -> 572 us on the two cases below); half the
-// columns a round in the second pass, or half the words in the decoders', costs 3 %,
-// twice the columns 10 %.  Two softmax groups instead of three make their chains of
-// loads and waits the bound (640 us); one thread issuing both products spends 2240
-// cycles a tile on issue and waits.  The products alone take 336 us of the 564.  What
-// sets the period now is the way round one S buffer, three tiles long: S issued in 900
-// cycles, first pass 1000, second 1700, P V issued in 800, and some 450 between any
-// two (P handed over in two halves, and the reference waited for ahead of S, took 2 %
-// off; issue code with constant stages and buffers, or more registers for it, costs 2
-// to 6 %).
-//   128 pages of 4000-6144 tokens with 8-60 branches: 336 us (112 at HBM rate)
-//   64 pages of 4809 tokens, 8-40 branches of up to 16 query tokens: 564 us
+// What bounds it: a tile goes round its S buffer in some 6000 cycles, three tiles at a
+// time (S issued in 900, first softmax pass 1000, second 1700, P V issued in 800, some
+// 450 between any two), so 1950 cycles a tile, of which the products need 1024 of the
+// tensor pipe.  The products run slower than that because shared memory's data pipe is
+// 76 % busy: a tile's products read 96 KB, the decoders write 64 KB, and the codes pass
+// twice, 72 KB.  Schedulers issue every other cycle.
+//   128 pages of 4000-6144 tokens with 8-60 branches: 316 us (112 at HBM rate)
+//   64 pages of 4809 tokens, 8-40 branches of up to 16 query tokens: 566 us (the
+//   products alone: 336)
+// What was measured on the way there (the two cases in us):
+//   - two softmax groups instead of three: 640 on the second; one thread issuing both
+//     products spends 2240 cycles a tile on issue and waits;
+//   - loops: six warps a scheduler run different code and starve on instruction
+//     fetches.  First pass of 32 columns a round instead of 64, masked scores put back
+//     instead of masked again by the second pass, K and V decoded by the same
+//     instructions: 380 -> 343, 601 -> 572.  Half the columns a round in the second
+//     pass, or half the words in the decoders', costs 3 %, twice the columns 10 %;
+//   - P handed over in two halves, the reference waited for ahead of S: 336, 564;
+//   - lanes past a unit's rows, whose Q is what the buffer held, no longer ask for
+//     rescalings of O: 324; decoders' reads without bank conflicts: 316;
+//   - issue code with constant stages and buffers, or more registers for it: 2 to 6 %
+//     slower.
 //
 // A wait names a phase by its parity, so every waiter knows the phase before to be
 // over: from the barriers that it waited for, or from what the phase's arrivals
