@@ -175,9 +175,7 @@ def _check(rc: int):
 
 
 def _ptr(x) -> Optional[int]:
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or isinstance(x, int):
         return x
     return x.data_ptr()
 
@@ -415,6 +413,7 @@ class Rope:
         if n_pos is None:
             n_pos = int(cos_sin.shape[0])
         self.c = RopeSpec(_ptr(cos_sin), n_pos, rot_dim, int(bool(interleaved)))
+        self.ref = C.byref(self.c)
 
 
 def _kv_step(pool: "KVPool", k, v, *, k_stride=None, v_stride=None, q=None, Hq: int = 0, q_stride=None, q_rot=None,
@@ -439,7 +438,7 @@ class KVRows:
                                           None if p is None else _p32(p), C.byref(h)))
         self.handle = h
         self.n = int(b[-1]) if len(seqs) else 0
-        self._pool = pool
+        self._pool, self._row, self._lib = pool, pool.Hkv * pool.d, lib()
 
     def ws_size(self) -> int:
         n = C.c_size_t()
@@ -449,12 +448,18 @@ class KVRows:
     def upload(self, ws=None, ws_bytes: int = 0, stream=None):
         _check(lib().padoc_kv_rows_upload(self.handle, _ptr(ws), int(ws_bytes), _stream(stream)))
 
-    def write(self, k, v, ws=None, *, rope: Optional[Rope] = None, stream=None, **step):
+    def write(self, k, v, ws=None, *, rope: Optional[Rope] = None, stream=None, q=None, Hq: int = 0, q_rot=None,
+              k_rot=None, q_stride=None, k_stride=None, v_stride=None):
         """padoc_kv_write.  Optional: q with Hq and q_rot, k_rot, and the row
         strides k_stride, v_stride, q_stride in elements (dense by default)."""
-        st = _kv_step(self._pool, k, v, **step)
-        _check(lib().padoc_kv_write(self.handle, None if rope is None else C.byref(rope.c), C.byref(st), _ptr(ws),
-                                    _stream(stream)))
+        # a step of few rows takes as long as this call: no detours
+        row = self._row
+        st = KVStep(_ptr(q), Hq * self._pool.d if q_stride is None else q_stride, Hq, _ptr(q_rot), _ptr(k),
+                    row if k_stride is None else k_stride, _ptr(v), row if v_stride is None else v_stride, _ptr(k_rot))
+        rc = self._lib.padoc_kv_write(self.handle, None if rope is None else rope.ref, C.byref(st), _ptr(ws),
+                                      _stream(stream))
+        if rc != OK:
+            _check(rc)
 
     def gather(self, k, v, ws=None, stream=None):
         _check(lib().padoc_kv_gather(self.handle, _ptr(k), _ptr(v), _ptr(ws), _stream(stream)))
