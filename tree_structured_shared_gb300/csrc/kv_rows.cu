@@ -11,21 +11,24 @@
 //
 // Both kernels are streams, bound by HBM once the rows fill the GPU and by the
 // launch below that.  A record names up to 16 consecutive rows of one block
-// and is one CTA; a warp takes a token and walks its heads, lanes 0-15 holding
-// the 128 dims of K (or of one query head), lanes 16-31 those of V (or of the
-// next query head), so the table is read once a token.  A lane holds two quads
-// of dims, A and B.  Where pairs are half a rotation apart, quad A of the lanes
-// that turn is the pairs' first dims and B their second, so a rotation needs no
-// exchange between lanes; elsewhere A and B are neighbours.
+// and is one CTA.  To write, a warp takes eight (token, head) at a time, K and V of
+// them together: four lanes a head, each with two whole groups of 16 dims.  Where pairs
+// are half a rotation apart, the two groups are partners, elsewhere neighbours, so
+// neither the rotation nor a group's scale needs an exchange between lanes.  To read
+// back, a warp takes a token, lanes 0-15 K's 128 dims and lanes 16-31 V's.
 // Small record lists ride in the kernel's parameters: no upload is needed.
 //
 // Measured (16 query heads, 8 kv heads, all dims turned): 16 x 4809 rows into a bf16
-// pool in 225 us, 6.3 TB/s; 64 x 4809 rows into a 4-bit pool and back out in 1190 us
-// (941 at HBM rate): the write, about 200 warp instructions a (token, kv head) to
-// scale and round, is bound by instruction issue, the way back by HBM (64 pages of
-// 4000-6144 tokens in 260 us, 6.6 TB/s).  384 rows of one token take 4 us.  Finer or
-// coarser splits of a token's heads over the warps: the same or slower (1-16 rows of
-// 1490 sequences, write and way back: 82 us; two warps a token 84, eight 121).
+// pool in 225 us, 6.3 TB/s; 64 x 4809 rows into a 4-bit pool and back out in 1030 us
+// (941 at HBM rate), the way back at HBM rate (64 pages of 4000-6144 tokens in 260 us,
+// 6.6 TB/s); 1-16 rows of 1490 sequences and back in 74 us.  384 rows of one token take
+// 4 us.  Before, with sixteen lanes a head and 8 dims a lane, a group spread over four
+// lanes, a token cost twice the instructions (1190 and 82 us).  Eight heads of a token
+// instead of eight tokens of a head to a 4-bit pool: 1102 us (its bytes are scattered
+// over the unit, 44 sectors written become 176); to a bf16 pool the other way round:
+// 255 us.  The write holds three CTAs an SM; two, or four (which spills), take 9 and
+// 7 % longer, two query heads on their way at once (which spills) 7 %, rows prefetched
+// to L2 by the CTA nothing.
 #include <cuda_bf16.h>
 
 #include <string>
@@ -42,30 +45,41 @@ using namespace ptx;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kWriteCtas = 3;
 
 struct InlineRecs {
   RowRec r[kInlineRecs];
 };
 struct NoRecs {};
 
-// A lane's two quads of a row whose quad A starts at p, quad B db elements on.
-struct Quads {
-  uint2 a, b;  // bf16
+// A lane's two groups of 16 dims of a row, bf16.
+struct Raw {
+  uint4 a[2], b[2];
 };
-__device__ __forceinline__ Quads load_quads(const __nv_bfloat16* p, int db) {
-  return Quads{__ldcs(reinterpret_cast<const uint2*>(p)), __ldcs(reinterpret_cast<const uint2*>(p + db))};
+__device__ __forceinline__ Raw load_raw(const __nv_bfloat16* row, int ga, int gb) {
+  const uint4 *a = reinterpret_cast<const uint4*>(row + 16 * ga), *b = reinterpret_cast<const uint4*>(row + 16 * gb);
+  return Raw{{__ldcs(a), __ldcs(a + 1)}, {__ldcs(b), __ldcs(b + 1)}};
 }
-__device__ __forceinline__ void unpack(const Quads& u, float (&x)[8]) {
-  const uint32_t w[4] = {u.a.x, u.a.y, u.b.x, u.b.y};
+__device__ __forceinline__ void store_raw(__nv_bfloat16* row, int ga, int gb, const Raw& r) {
+  uint4 *a = reinterpret_cast<uint4*>(row + 16 * ga), *b = reinterpret_cast<uint4*>(row + 16 * gb);
+  a[0] = r.a[0];
+  a[1] = r.a[1];
+  b[0] = r.b[0];
+  b[1] = r.b[1];
+}
+__device__ __forceinline__ void unpack(const uint4 (&u)[2], float (&x)[16]) {
+  const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 8; ++i) {
     x[2 * i] = __uint_as_float(w[i] << 16);
     x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
 }
-__device__ __forceinline__ void store(__nv_bfloat16* p, int db, const float (&x)[8]) {
-  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
-  *reinterpret_cast<uint2*>(p + db) = make_uint2(pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+__device__ __forceinline__ void pack(const float (&x)[16], uint4 (&u)[2]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    u[h] = make_uint4(pack_bf16x2(x[8 * h], x[8 * h + 1]), pack_bf16x2(x[8 * h + 2], x[8 * h + 3]),
+                      pack_bf16x2(x[8 * h + 4], x[8 * h + 5]), pack_bf16x2(x[8 * h + 6], x[8 * h + 7]));
 }
 
 __device__ __forceinline__ RowRec get_rec(const RowsArgs& a, const InlineRecs& in, int r) { return in.r[r]; }
@@ -111,148 +125,158 @@ __device__ __forceinline__ uint32_t i4_quad(const float* x, float s, float y) {
   return (b[0] + b[1] * 65536u) + (b[2] + b[3] * 65536u) * 16u - 0x4B400000u * 0x110011u;
 }
 
+// A group's two words of codes and its scale byte.
+struct Group {
+  uint32_t w0, w1, scale;
+};
+template <bool CLAMP>
+__device__ __forceinline__ void i4_codes(const float (&x)[16], float s, float y, Group* g) {
+  g->w0 = i4_quad<CLAMP>(x, s, y) | i4_quad<CLAMP>(x + 4, s, y) << 8;
+  g->w1 = i4_quad<CLAMP>(x + 8, s, y) | i4_quad<CLAMP>(x + 12, s, y) << 8;
+}
+// The largest magnitude; a NaN if there is one.
+__device__ __forceinline__ float largest(const float (&x)[16]) {
+  float m = fabsf(x[0]);
+#pragma unroll
+  for (int i = 1; i < 16; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(x[i])));
+  return m;
+}
+// A lane's two groups; whether one holds a NaN or an infinity (its codes are then of no
+// use).  The whole warp calls it.
+__device__ __forceinline__ bool quantise(const float (&xa)[16], const float (&xb)[16], Group* a, Group* b) {
+  constexpr float kSeventh = 1.f / 7.f;
+  const float la = largest(xa), lb = largest(xb);
+  const bool bad = !(la < INFINITY) || !(lb < INFINITY);
+  const float ma = quotient(la, 7.f, kSeventh), mb = quotient(lb, 7.f, kSeventh);
+  if (__any_sync(0xffffffffu, !i4_plain(ma) || !i4_plain(mb))) {
+    a->scale = i4_scale_byte(bad ? 0.f : ma);
+    b->scale = i4_scale_byte(bad ? 0.f : mb);
+    const float sa = i4_scale_value(a->scale), sb = i4_scale_value(b->scale);
+    // a scale of zero: every code is that of zero
+    i4_codes<true>(xa, sa, a->scale ? __frcp_rn(sa) : 0.f, a);
+    i4_codes<true>(xb, sb, b->scale ? __frcp_rn(sb) : 0.f, b);
+  } else {
+    const float sa = i4_plain_scale(ma, &a->scale), sb = i4_plain_scale(mb, &b->scale);
+    i4_codes<false>(xa, sa, short_reciprocal(sa), a);
+    i4_codes<false>(xb, sb, short_reciprocal(sb), b);
+  }
+  return bad;
+}
+
 template <bool I4, class RECS>
-__global__ void __launch_bounds__(kThreads, 3) kv_write_kernel(const __grid_constant__ RowsArgs a,
-                                                            const __grid_constant__ RECS in) {
+__global__ void __launch_bounds__(kThreads, kWriteCtas) kv_write_kernel(const __grid_constant__ RowsArgs a,
+                                                                        const __grid_constant__ RECS in) {
   const RowRec rec = get_rec(a, in, blockIdx.x);
   const int n = rec.slot_n >> 8, slot0 = rec.slot_n & 255;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int l = lane & 15, half = lane >> 4;  // K (half 0) or V (half 1)
-  // few tokens: several warps share a token's heads
-  const int hg_n = n == 1 ? 8 : n == 2 ? 4 : n <= 4 ? 2 : 1;
+  const int l = lane & 3, sub = lane >> 2;
+  // the lane's two groups of dims: half a rotation apart where they turn so
   const int hr = a.rot_dim / 2;
-  const bool turns = 8 * l < a.rot_dim;
-  const bool split = turns && !a.interleaved;  // quads a half rotation apart
-  const int da = split ? 4 * l : 8 * l, db = split ? hr : 4;
-  const int n_q = a.q ? (a.Hq + 1) / 2 : 0;  // pairs of query heads
-  // where the lane's word of codes and, if it has one, its scale go (I4)
-  const int word_at = !split ? l : ((l & 1) ? hr / 8 : 0) + (l >> 1);
-  const int grp = word_at >> 1;
-  const bool has_scale = split ? (l & 2) == 0 : (l & 1) == 0;
-  constexpr int kUnroll = 4;
-  for (int item = warp; item < n * hg_n; item += kWarps) {
-    const int t = item / hg_n, hg = item - t * hg_n;
-    const int64_t src = static_cast<int64_t>(rec.row) + t;
-    const int slot = slot0 + t;
-    // the lane's four angles
-    float cs[4], sn[4];
-    if (turns) {
-      const int pos = a.positions ? a.positions[src] : rec.pos + t;
-      const float* tab = a.cos_sin + static_cast<int64_t>(pos) * a.rot_dim + 4 * l;
-      *reinterpret_cast<float4*>(cs) = *reinterpret_cast<const float4*>(tab);
-      *reinterpret_cast<float4*>(sn) = *reinterpret_cast<const float4*>(tab + hr);
-    }
-    auto rotate = [&](float (&x)[8]) {
-      // pair j: dims j of the two quads, or dims 2j, 2j + 1
-      auto turn = [&](float& p, float& q, int j) {
-        const float u = __fsub_rn(__fmul_rn(p, cs[j]), __fmul_rn(q, sn[j]));
-        q = __fadd_rn(__fmul_rn(q, cs[j]), __fmul_rn(p, sn[j]));
-        p = u;
-      };
-      if (!turns) return;
-      if (a.interleaved) {
+  const bool turns = 32 * l < a.rot_dim, split = turns && !a.interleaved;
+  const int ga = split ? l : 2 * l, gb = split ? l + hr / 16 : 2 * l + 1;
+  auto rotate = [&](float (&xa)[16], float (&xb)[16], int64_t row, int t) {
+    if (!turns) return;
+    const int pos = a.positions ? a.positions[row] : rec.pos + t;
+    const float* tab = a.cos_sin + static_cast<int64_t>(pos) * a.rot_dim + 16 * l;
+    auto turn = [](float& p, float& q, float c, float s) {
+      const float u = __fsub_rn(__fmul_rn(p, c), __fmul_rn(q, s));
+      q = __fadd_rn(__fmul_rn(q, c), __fmul_rn(p, s));
+      p = u;
+    };
 #pragma unroll
-        for (int j = 0; j < 4; ++j) turn(x[2 * j], x[2 * j + 1], j);
+    for (int i = 0; i < 16; i += 4) {
+      float cs[4], sn[4];
+      *reinterpret_cast<float4*>(cs) = *reinterpret_cast<const float4*>(tab + i);
+      *reinterpret_cast<float4*>(sn) = *reinterpret_cast<const float4*>(tab + hr + i);
+      if (a.interleaved) {
+        // the lane's pair i + j: dims 2 (i + j), + 1 of its 32
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          turn(i < 8 ? xa[2 * (i + j)] : xb[2 * (i + j) - 16], i < 8 ? xa[2 * (i + j) + 1] : xb[2 * (i + j) - 15], cs[j], sn[j]);
       } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) turn(x[j], x[4 + j], j);
-      }
-    };
-    {
-      const __nv_bfloat16* in = (half ? a.v + src * a.v_stride : a.k + src * a.k_stride) + da;
-      __nv_bfloat16* rot = a.k_rot && !half ? a.k_rot + src * a.Hkv * kHeadDim + da : nullptr;
-      const int64_t bh = static_cast<int64_t>(rec.block) * a.Hkv;
-      uint8_t* pool = static_cast<uint8_t*>(half ? a.v_pool : a.k_pool);
-      // I4: the word's place, the scale's; bf16: the row's
-      uint8_t* dst = I4 ? pool + bh * kI4Unit + (half ? grp * 128 + slot * 8 + (word_at & 1) * 4
-                                                      : (word_at >> 2) * 256 + slot * 16 + (word_at & 3) * 4)
-                        : pool + ((bh * 16 + slot) * kHeadDim + da) * 2;
-      const int scale_at = kI4Scales + (half ? grp * 16 + slot : slot * 8 + grp) -
-                           (half ? grp * 128 + slot * 8 + (word_at & 1) * 4 : (word_at >> 2) * 256 + slot * 16 + (word_at & 3) * 4);
-      for (int u0 = hg; u0 < a.Hkv; u0 += hg_n * kUnroll) {
-        Quads ld[kUnroll];
-#pragma unroll
-        for (int i = 0; i < kUnroll; ++i)
-          if (u0 + i * hg_n < a.Hkv) ld[i] = load_quads(in + (u0 + i * hg_n) * kHeadDim, db);
-#pragma unroll
-        for (int i = 0; i < kUnroll; ++i) {
-          const int u = u0 + i * hg_n;
-          if (u >= a.Hkv) break;
-          float x[8];
-          unpack(ld[i], x);
-          if (!half) rotate(x);
-          if (rot) store(rot + u * kHeadDim, db, x);
-          if (!I4) {
-            store(reinterpret_cast<__nv_bfloat16*>(dst) + u * 16 * kHeadDim, db, x);
-          } else {
-            // the largest magnitude of each quad's group: of four neighbouring lanes
-            // where the quads lie apart, of two lanes' both quads elsewhere
-            float ma = fmaxf(max3f(fabsf(x[0]), fabsf(x[1]), fabsf(x[2])), fabsf(x[3]));
-            float mb = fmaxf(max3f(fabsf(x[4]), fabsf(x[5]), fabsf(x[6])), fabsf(x[7]));
-            // 0 unless one is NaN or infinite
-            float sum = 0.f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) sum = fmaf(x[j], 0.f, sum);
-            if (!split) ma = mb = fmaxf(ma, mb);
-            ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, 1));
-            mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
-            const float ma2 = __shfl_xor_sync(0xffffffffu, ma, 2), mb2 = __shfl_xor_sync(0xffffffffu, mb, 2);
-            if (split) {
-              ma = fmaxf(ma, ma2);
-              mb = fmaxf(mb, mb2);
-            }
-            constexpr float kSeventh = 1.f / 7.f;
-            ma = quotient(ma, 7.f, kSeventh);
-            mb = quotient(mb, 7.f, kSeventh);
-            uint32_t wa, wb, ba, bb;
-            if (__any_sync(0xffffffffu, !(sum == 0.f) || !i4_plain(ma) || !i4_plain(mb))) {
-              ba = i4_scale_byte(ma);
-              bb = i4_scale_byte(mb);
-              const float sa = i4_scale_value(ba), sb = i4_scale_value(bb);
-              // a scale of zero: every code is that of zero
-              wa = i4_quad<true>(x, sa, ba ? __frcp_rn(sa) : 0.f);
-              wb = i4_quad<true>(x + 4, sb, bb ? __frcp_rn(sb) : 0.f);
-              // a NaN or an infinity in this token's K or V of this head: K becomes
-              // NaN (through its first group) and V zero, so every query that sees
-              // the token gets NaN and no other does
-              if (__any_sync(0xffffffffu, !(sum == 0.f))) {
-                wa = wb = 0x00880088u;
-                ba = !half && da < 16 ? kI4Nan : 0u;
-                bb = !half && da + db < 16 ? kI4Nan : 0u;
-              }
-            } else {
-              const float sa = i4_plain_scale(ma, &ba), sb = i4_plain_scale(mb, &bb);
-              wa = i4_quad<false>(x, sa, short_reciprocal(sa));
-              wb = i4_quad<false>(x + 4, sb, short_reciprocal(sb));
-            }
-            // one word a lane: of its own two quads, or of two neighbours' A (even lane) or B (odd lane)
-            const uint32_t other = __shfl_xor_sync(0xffffffffu, (l & 1) ? wa : wb, 1);
-            uint8_t* p = dst + u * kI4Unit;
-            *reinterpret_cast<uint32_t*>(p) = !split ? wa | wb << 8 : (l & 1) ? other | wb << 8 : wa | other << 8;
-            if (has_scale) p[scale_at] = static_cast<uint8_t>(split && (l & 1) ? bb : ba);
-          }
-        }
+        for (int j = 0; j < 4; ++j) turn(xa[i + j], xb[i + j], cs[j], sn[j]);
       }
     }
-    if (n_q) {
-      const __nv_bfloat16* in = a.q + src * a.q_stride + half * kHeadDim + da;
-      __nv_bfloat16* rot = a.q_rot + (src * a.Hq + half) * kHeadDim + da;
-      for (int u0 = hg; u0 < n_q; u0 += hg_n * kUnroll) {
-        Quads ld[kUnroll];
-#pragma unroll
-        for (int i = 0; i < kUnroll; ++i) {
-          const int h = 2 * (u0 + i * hg_n);
-          if (h + half < a.Hq) ld[i] = load_quads(in + h * kHeadDim, db);
-        }
-#pragma unroll
-        for (int i = 0; i < kUnroll; ++i) {
-          const int h = 2 * (u0 + i * hg_n);
-          if (h + half >= a.Hq) continue;
-          float x[8];
-          unpack(ld[i], x);
-          rotate(x);
-          store(rot + h * kHeadDim, db, x);
-        }
+  };
+  // passes of eight (token, head): K and V together, then Q
+  const int n_kv = n * a.Hkv, n_q = a.q ? n * a.Hq : 0;
+  const int kv_passes = (n_kv + 7) / 8, passes = kv_passes + (n_q + 7) / 8;
+  for (int pass = warp; pass < passes; pass += kWarps) {
+    const bool is_q = pass >= kv_passes;
+    const int last = (is_q ? n_q : n_kv) - 1;
+    const int p = (is_q ? pass - kv_passes : pass) * 8 + sub;
+    const bool ok = p <= last;
+    const int at = min(p, last);
+    int t, u;
+    if (I4 && !is_q) {
+      // eight slots of a head fill whole sectors of its unit
+      u = at / n;
+      t = at - u * n;
+    } else {
+      // a token's heads lie side by side and share its angles
+      const int H = is_q ? a.Hq : a.Hkv;
+      t = at / H;
+      u = at - t * H;
+    }
+    const int64_t row = static_cast<int64_t>(rec.row) + t;
+    float xa[16], xb[16];
+    Raw r;
+    if (is_q) {
+      r = load_raw(a.q + row * a.q_stride + u * kHeadDim, ga, gb);
+      unpack(r.a, xa);
+      unpack(r.b, xb);
+      rotate(xa, xb, row, t);
+      pack(xa, r.a);
+      pack(xb, r.b);
+      if (ok) store_raw(a.q_rot + (row * a.Hq + u) * kHeadDim, ga, gb, r);
+      continue;
+    }
+    r = load_raw(a.k + row * a.k_stride + u * kHeadDim, ga, gb);
+    const Raw rv = load_raw(a.v + row * a.v_stride + u * kHeadDim, ga, gb);
+    const int64_t unit = static_cast<int64_t>(rec.block) * a.Hkv + u;
+    const int slot = slot0 + t;
+    unpack(r.a, xa);
+    unpack(r.b, xb);
+    rotate(xa, xb, row, t);
+    if (a.k_rot || !I4) {
+      pack(xa, r.a);
+      pack(xb, r.b);
+      if (ok && a.k_rot) store_raw(a.k_rot + (row * a.Hkv + u) * kHeadDim, ga, gb, r);
+    }
+    if (!I4) {
+      const int64_t dst = (unit * 16 + slot) * kHeadDim;
+      if (ok) {
+        store_raw(static_cast<__nv_bfloat16*>(a.k_pool) + dst, ga, gb, r);
+        store_raw(static_cast<__nv_bfloat16*>(a.v_pool) + dst, ga, gb, rv);
+      }
+    } else {
+      Group k0, k1, v0, v1;
+      bool bad = quantise(xa, xb, &k0, &k1);
+      unpack(rv.a, xa);
+      unpack(rv.b, xb);
+      bad |= quantise(xa, xb, &v0, &v1);
+      // a NaN or an infinity in this token's K or V of this head (its four lanes): K
+      // becomes NaN (through its first group) and V zero, so every query that sees the
+      // token gets NaN and no other does
+      if (__ballot_sync(0xffffffffu, bad) & (15u << (lane & 28))) {
+        k0 = Group{0x88888888u, 0x88888888u, ga == 0 ? kI4Nan : 0u};
+        k1 = v0 = v1 = Group{0x88888888u, 0x88888888u, 0u};
+      }
+      if (ok) {
+        uint8_t *k = static_cast<uint8_t*>(a.k_pool) + unit * kI4Unit, *v = static_cast<uint8_t*>(a.v_pool) + unit * kI4Unit;
+        auto put_k = [&](int g, const Group& x) {
+          *reinterpret_cast<uint2*>(k + (g >> 1) * 256 + slot * 16 + (g & 1) * 8) = make_uint2(x.w0, x.w1);
+          k[kI4Scales + slot * 8 + g] = static_cast<uint8_t>(x.scale);
+        };
+        auto put_v = [&](int g, const Group& x) {
+          *reinterpret_cast<uint2*>(v + g * 128 + slot * 8) = make_uint2(x.w0, x.w1);
+          v[kI4Scales + g * 16 + slot] = static_cast<uint8_t>(x.scale);
+        };
+        put_k(ga, k0);
+        put_k(gb, k1);
+        put_v(ga, v0);
+        put_v(gb, v1);
       }
     }
   }
