@@ -154,6 +154,33 @@ def test_many_records_and_gather(torch, dtype):
         assert np.array_equal(got[:-1].double().cpu().numpy(), exp) and bool((got[-1] == 5).all())
 
 
+def test_extreme_values(torch):
+    """Magnitudes from below a scale's smallest step to beyond its largest, zeros, NaN and infinities, next to ordinary
+    heads in the same warp, rotated on the way (a rotation of large values may overflow, which poisons the token too)."""
+    Hkv, n, rng = 8, 61, np.random.default_rng(17)
+    e = rng.integers(-140, 128, size=(2, n, Hkv, 1)) * (rng.random((2, n, Hkv, 1)) < 0.4)
+    x = wl.round_bf16((rng.normal(size=(2, n, Hkv, 128)) * 2.0 ** e).astype(np.float32))
+    x[rng.random((2, n, Hkv)) < 0.1] = 0
+    for value in (np.nan, np.inf, -np.inf):
+        for which in (0, 1):
+            x[which, rng.integers(n), rng.integers(Hkv), rng.integers(128)] = value
+    x[0, 5, 3, 16:32] = -0.0
+    tab = i4ref.rope_table(80, 128)
+    pool, kp, vp = make_pool(torch, 8, Hkv, padoc.I4)
+    s = pool.alloc(0)
+    k, v = (torch.from_numpy(t).to(torch.bfloat16).cuda() for t in x)
+    pool.append_rope([s], [0, n], k, v, rope=padoc.Rope(torch.from_numpy(tab).cuda(), 128))
+    rows = padoc.KVRows(pool, [s], [0], [0, n])
+    rows.upload()
+    ko, vo = (torch.zeros(n, Hkv, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    rows.gather(ko, vo)
+    with np.errstate(all="ignore"):
+        want = i4ref.stored(rotate32(x[0], tab[:n], 128, False), x[1])
+    assert np.isnan(want[0]).any(-1).sum() >= 6
+    assert np.array_equal(ko.double().cpu().numpy(), want[0], equal_nan=True)
+    assert np.array_equal(vo.double().cpu().numpy(), want[1])
+
+
 def test_commit_and_append_quantise(torch):
     """padoc_kv_append and padoc_kv_commit on a 4-bit pool hold the same values as the rows written one call each."""
     Hkv, rng = 3, np.random.default_rng(5)
