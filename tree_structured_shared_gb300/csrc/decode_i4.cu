@@ -38,8 +38,8 @@
 //
 // The query block (bf16 rows that are not in the cache yet) has its scores and, with P
 // as the sum of two bf16 numbers, its values from bf16 matrix instructions.  Where a
-// value of the block is not finite, the values are added in f32 by key, only for rows
-// that see the key, so a NaN in a hidden draft token stays there.  (Doing so always cost
+// value of the block is not finite (or there are few keys), the values are added in f32
+// by key, only for rows that see the key, so a NaN in a hidden draft token stays there.  (Doing so always cost
 // 130 instructions a key: 335 us instead of 300 on the second case above.)
 #include <cuda_bf16.h>
 
@@ -59,6 +59,10 @@ using namespace ptx;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kPShift = 10.f;  // log2 of P's weight at the running maximum
 constexpr float kPSlack = 4.f;   // how far (log2) a score may exceed it
+// Query blocks up to this long have their values added key by key (one token a branch,
+// 128 pages: 566 us, 568 to 572 by matrix instructions; up to 3 and 4 tokens: 136 and
+// 140 us key by key, 133 and 134 by matrix instructions).
+constexpr int kFewKeys = 2;
 constexpr float kNoMax = -3.0e38f;  // reference of a row that has seen no key: any score exceeds it
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -458,44 +462,47 @@ __global__ void __launch_bounds__(32 * W, 16 / W) decode_i4_kernel(const I4Args 
       for (int e = 0; e < 4; ++e) s[e] = ((vis[e & 1] >> (key_a + (e >> 1) * 2)) & 1u) ? s[e] * a.sl2 : -INFINITY;
       softmax(s1);
       const __nv_bfloat16* vn = a.v_new + at + 16 * i;
-      // group i of the keys 4c .. 4c + 3, this warp's; any that is not finite?
-      uint32_t x[4][8], special = 0;
+      bool added = false;
+      if (q_len > kFewKeys) {
+        // group i of the keys 4c .. 4c + 3, this warp's; any that is not finite?
+        uint32_t x[4][8], special = 0;
 #pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        const int j = 4 * c + y;
-        const bool mine = j < q_len && (((kMine << warp) >> j) & 1u);
+        for (int y = 0; y < 4; ++y) {
+          const int j = 4 * c + y;
+          const bool mine = j < q_len && (((kMine << warp) >> j) & 1u);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint4 v = mine ? *reinterpret_cast<const uint4*>(vn + j * krow + 8 * h) : make_uint4(0, 0, 0, 0);
-          x[y][4 * h] = v.x;
-          x[y][4 * h + 1] = v.y;
-          x[y][4 * h + 2] = v.z;
-          x[y][4 * h + 3] = v.w;
+          for (int h = 0; h < 2; ++h) {
+            const uint4 v = mine ? *reinterpret_cast<const uint4*>(vn + j * krow + 8 * h) : make_uint4(0, 0, 0, 0);
+            x[y][4 * h] = v.x;
+            x[y][4 * h + 1] = v.y;
+            x[y][4 * h + 2] = v.z;
+            x[y][4 * h + 3] = v.w;
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(special) : "r"(x[y][k]), "r"(0u));
         }
+        added = !__any_sync(0xffffffffu, (special & 0x7fff7fffu) != 0u);
+        if (added) {
+          // P as the sum of two bf16 numbers (16 bits of it); O of cached keys lacks the factor kI4Unscale
+          uint32_t ph[2], pl[2];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(special) : "r"(x[y][k]), "r"(0u));
+          for (int h = 0; h < 2; ++h) {
+            const float p0 = s[2 * h] * (1.f / kI4Unscale), p1 = s[2 * h + 1] * (1.f / kI4Unscale);
+            const uint32_t hi = pack_bf16x2(p0, p1);
+            ph[h] = transpose8(hi);
+            pl[h] = transpose8(pack_bf16x2(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xffff0000u)));
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            // even dims of two keys side by side, then odd dims
+            const uint32_t f[4] = {__byte_perm(x[0][k], x[1][k], 0x5410), __byte_perm(x[0][k], x[1][k], 0x7632),
+                                   __byte_perm(x[2][k], x[3][k], 0x5410), __byte_perm(x[2][k], x[3][k], 0x7632)};
+            mma_bf16(o[k], f, ph[0], ph[1]);
+            mma_bf16(o[k], f, pl[0], pl[1]);
+          }
+        }
       }
-      const bool added = !__any_sync(0xffffffffu, (special & 0x7fff7fffu) != 0u);
-      if (added) {
-        // P as the sum of two bf16 numbers (16 bits of it); O of cached keys lacks the factor kI4Unscale
-        uint32_t ph[2], pl[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float p0 = s[2 * h] * (1.f / kI4Unscale), p1 = s[2 * h + 1] * (1.f / kI4Unscale);
-          const uint32_t hi = pack_bf16x2(p0, p1);
-          ph[h] = transpose8(hi);
-          pl[h] = transpose8(pack_bf16x2(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xffff0000u)));
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          // even dims of two keys side by side, then odd dims
-          const uint32_t f[4] = {__byte_perm(x[0][k], x[1][k], 0x5410), __byte_perm(x[0][k], x[1][k], 0x7632),
-                                 __byte_perm(x[2][k], x[3][k], 0x5410), __byte_perm(x[2][k], x[3][k], 0x7632)};
-          mma_bf16(o[k], f, ph[0], ph[1]);
-          mma_bf16(o[k], f, pl[0], pl[1]);
-        }
-      }
-      // some are not: each is added in f32 to the rows that see it, and to no other
+      // a few, or one is not: each is added in f32 to the rows that see it, and to no other
 #pragma unroll 1
       for (int j = added ? q_len : warp; j < q_len; j += W) {
         // key j's P sits in lane row 2 (j / 4) + j % 2, first or second register
