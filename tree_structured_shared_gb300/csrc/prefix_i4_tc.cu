@@ -661,7 +661,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a) 
         const float* ml = row_buf(iu) + 128 + r;
         const float m1 = ml[0], l1 = ml[128], m2 = ml[256], l2 = ml[384];
         const float M = max3f(m_run, m1, m2);
-        auto part = [&](float m, float l) { return m == -INFINITY ? 0.f : l * fast_exp2(m - M); };
+        // Without a reference the sum is zero, or NaN where all that the group's rows saw
+        // were NaN scores, which no maximum shows: it has to reach L.
+        auto part = [&](float m, float l) { return m == -INFINITY ? l : l * fast_exp2(m - M); };
         const float L = part(m_run, l_run) + part(m1, l1) + part(m2, l2);
         const bool any = !(L == 0.f);  // NaN counts
         const float inv = any ? kI4Unscale / L : 0.f;
