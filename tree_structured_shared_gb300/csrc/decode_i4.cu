@@ -324,8 +324,9 @@ __global__ void __launch_bounds__(32 * W, 16 / W) decode_i4_kernel(const I4Args 
           for (int k = 4; k < 32; k <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, k));
           al[e] = 1.f;
           if (t - mo[e] > kPShift + kPSlack) {
-            al[e] = fast_exp2(mo[e] - (t - kPShift));
-            mo[e] = t - kPShift;
+            const float m = __fadd_ru(t, -kPShift);  // up: where floats are 16 apart, down would make P 2^16
+            al[e] = fast_exp2(mo[e] - m);
+            mo[e] = m;
           }
           l[e] *= al[e];
         }
