@@ -27,7 +27,8 @@ def harness(padoc_lib):
 
 
 # prefix, own keys and query tokens of each branch
-PAGES = {"few rows": (333, [70, 200], [2, 2]), "merged": (3000, [40], [4])}
+PAGES = {"few rows": (333, [70, 200], [2, 2]), "many rows": (333, [70, 0, 200, 33], [5, 16, 3, 7]),
+         "merged": (3000, [40], [4])}
 
 
 @pytest.mark.parametrize("e", [0, 6, 12] + list(range(16, 34)) + [40, 60, 90, 110])

@@ -53,7 +53,11 @@
 //
 // Softmax: P = 2^(x - m + 10) against a running maximum m that moves only when
 // exceeded by 2^4: at most 2^14, so P stays in fp16's range, and what rounds to
-// zero is below 2^-34 of the row's largest weight.
+// zero is below 2^-34 of the row's largest weight.  References are scores as they come
+// out of S, and x - m is their difference times the factor: the product of each, rounded
+// on its own, would be off by whole powers of two from scores of 2^24 on, and P infinite
+// or zero (one fma an element less: 863 us instead of 885 on the second case, 872 instead
+// of 884 on the first).
 // Every wait is bounded; a role that gives up raises the CTA's abort flag and
 // the device error word, and all roles leave their loops.
 #include <cuda_bf16.h>
@@ -449,7 +453,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a) 
       }
       const int kexp = mx ? min(100, 14 - (static_cast<int>(mx >> 7) - 127)) : 0;
       q_scale = __uint_as_float(static_cast<uint32_t>(127 + kexp) << 23);
-      q_sl2 = a.sl2 * kI4Unscale * __uint_as_float(static_cast<uint32_t>(127 - kexp) << 23);
+      // never zero: it multiplies infinite references
+      q_sl2 = fmaxf(a.sl2 * kI4Unscale * __uint_as_float(static_cast<uint32_t>(127 - kexp) << 23), 1.2e-38f);
     };
     auto put_q = [&](int u, int iu) {
       if (q_for != u) prepare_q(u);
@@ -549,21 +554,20 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a) 
             mx = fmaxf(max3f(m4[0], m4[1], m4[2]), m4[3]);
           }
         }
-        const float mt = mx * sl2;
-        const bool grow = valid && mt > m_old + kPSlack;  // what Q's buffer held in other rows asks for no rescaling
-        const float m_new = grow ? mt : m_old;
+        const bool grow = valid && (mx - m_old) * sl2 > kPSlack;  // what Q's buffer held in other rows asks for no rescaling
+        const float m_new = grow ? mx : m_old;
         m_sh[wg * 128 + r] = m_new;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B_M_FULL + wg));
         if (warp_valid) {
           if (m_new != m_run) {
-            l_run *= m_run == -INFINITY ? 0.f : fast_exp2(m_run - m_new);
+            l_run *= m_run == -INFINITY ? 0.f : fast_exp2((m_run - m_new) * sl2);
             m_run = m_new;
           }
           if (j > 0 && __any_sync(0xffffffffu, grow)) {
             // O holds sums against the old reference: rescale once P V of the tile before
             // has run (the one before it on that barrier had when S of that tile was issued)
-            const float alpha = grow ? fast_exp2(m_old - mt) : 1.f;  // 0 while m_old is -inf
+            const float alpha = grow ? fast_exp2((m_old - mx) * sl2) : 1.f;  // 0 while m_old is -inf
             if (!__all_sync(0xffffffffu, mbar_wait_relaxed(bar(B_PV_DONE + before), (kt_before / 3) & 1, abort))) {
               failed = true;
               break;
@@ -580,8 +584,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a) 
             }
             tmem_wait_st();
           }
-          const float m_use = (m_run == -INFINITY ? 0.f : m_run) - kPShift;
-          const uint64_t sl2x2 = f2pack(sl2, sl2), negm = f2pack(-m_use, -m_use);
+          const float m_use = m_run == -INFINITY ? 0.f : m_run;
+          const uint64_t sl2x2 = f2pack(sl2, sl2), negm = f2pack(-m_use, -m_use), shift = f2pack(kPShift, kPShift);
           uint64_t l2[2] = {0, 0};
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
@@ -591,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a) 
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
               float x0, x1;
-              f2unpack(fma2(f2pack(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), sl2x2, negm), x0, x1);
+              f2unpack(fma2(add2(f2pack(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), negm), sl2x2, shift), x0, x1);
               x0 = fast_exp2(x0);
               x1 = fast_exp2(x1);
               l2[(i >> 1) & 1] = add2(l2[(i >> 1) & 1], f2pack(x0, x1));
@@ -663,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a) 
         const float M = max3f(m_run, m1, m2);
         // Without a reference the sum is zero, or NaN where all that the group's rows saw
         // were NaN scores, which no maximum shows: it has to reach L.
-        auto part = [&](float m, float l) { return m == -INFINITY ? l : l * fast_exp2(m - M); };
+        auto part = [&](float m, float l) { return m == -INFINITY ? l : l * fast_exp2((m - M) * sl2); };
         const float L = part(m_run, l_run) + part(m1, l1) + part(m2, l2);
         const bool any = !(L == 0.f);  // NaN counts
         const float inv = any ? kI4Unscale / L : 0.f;
@@ -685,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a) 
           }
         }
         if (valid) {
-          a.part_lse[row] = any ? M - kPShift + __log2f(L) : -INFINITY;
+          a.part_lse[row] = any ? fmaf(M, sl2, -kPShift) + __log2f(L) : -INFINITY;
           for (int k = 1; k <= un.n_pre; ++k) a.part_lse[row + k * un.pre_stride] = -INFINITY;
         }
       }
