@@ -21,7 +21,7 @@
 // both operands agree, so lane (i, c) = (lane / 4, lane % 4) reads chunk c of
 // its two keys and group i of its four keys, 16 bytes at a time.
 //
-// Q is scaled by a power of two, one for the unit's rows, so that its largest
+// Each row of Q is scaled by a power of two of its own, so that its largest
 // magnitude lies in [2^14, 2^15): values down to 2^-28 of that keep every bit
 // of their bf16 form, and the scale joins the softmax's.  P is formed as
 // 2^(x - m + 10) with m a running maximum that moves only when exceeded by
@@ -274,23 +274,33 @@ __global__ void __launch_bounds__(32 * W, 16 / W) decode_i4_kernel(const I4Args 
     }
 #pragma unroll
     for (int x = 0; x < 16; ++x) most2 = __vmaxu2(most2, q[x] & 0x7fff7fffu);
-    uint32_t mx = __reduce_max_sync(0xffffffffu, max(most2 & 0xffffu, most2 >> 16));
-    if (mx >= 0x7f80u) {
-      // an infinity or a NaN: the largest finite one sets the factor
+    // of row i: a row's factor is its own, whatever the rows beside it hold
+    auto row_max = [](uint32_t m) {
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    };
+    uint32_t mx = row_max(max(most2 & 0xffffu, most2 >> 16));
+    if (__any_sync(0xffffffffu, mx >= 0x7f80u)) {
+      // an infinity or a NaN: the row's largest finite one sets the factor
       uint32_t m = 0;
 #pragma unroll
       for (int x = 0; x < 16; ++x) {
         const uint32_t lo = q[x] & 0x7fffu, hi = (q[x] >> 16) & 0x7fffu;
         m = max(m, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
       }
-      mx = __reduce_max_sync(0xffffffffu, m);
+      mx = row_max(m);
     }
     const int kexp = mx ? min(100, 14 - (static_cast<int>(mx >> 7) - 127)) : 0;
     const float qf = __uint_as_float(static_cast<uint32_t>(127 + kexp) << 23);
-    const float sl2q = a.sl2 * kI4Unscale * __uint_as_float(static_cast<uint32_t>(127 - kexp) << 23);
 #pragma unroll
     for (int x = 0; x < 16; ++x)
       q[x] = pack_f16x2(__uint_as_float(q[x] << 16) * qf, __uint_as_float(q[x] & 0xffff0000u) * qf);
+    // the scores' factors, of the rows 2c and 2c + 1 that the lane's scores are of
+    float sl2q[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      sl2q[e] = a.sl2 * kI4Unscale *
+                __uint_as_float(static_cast<uint32_t>(127 - __shfl_sync(0xffffffffu, kexp, (2 * c + e) * 4)) << 23);
 
     // rows 2c, 2c + 1: running reference (log2, less kPShift), sums, O of dims 16 i + 2 x + {0, 1}
     float mo[2] = {kNoMax, kNoMax}, l[2] = {0.f, 0.f};
@@ -407,7 +417,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) decode_i4_kernel(const I4Args 
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[h][e] *= sl2q;
+        for (int e = 0; e < 4; ++e) s[h][e] *= sl2q[e & 1];
       if ((step + W) * 16 + 16 > lim_min) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
