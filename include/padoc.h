@@ -275,7 +275,8 @@ typedef struct {
  * 8), so q, k and v may be slices of one fused projection.  q / q_rot and k_rot
  * are optional (NULL): the rotated rows out in bf16, dense, as
  * padoc_branch_decode (q, k_new) and padoc_tree_attn_varlen take them.  q_rot
- * may be q itself when q is dense, k_rot likewise k. */
+ * may be q itself when q is dense, k_rot likewise k; any other overlap of them
+ * with the rows read, or with each other, is refused. */
 typedef struct {
   const void* q; /* device [n, Hq, d] bf16, or NULL */
   int64_t q_stride;

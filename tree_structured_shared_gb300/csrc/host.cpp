@@ -1250,8 +1250,20 @@ static RowsArgs rows_args(const padoc_kv_rows* rows, const void* ws) {
   return a;
 }
 
+// Whether n dense bf16 rows of `row` elements at out share a byte with n rows of in_row
+// elements that lie in_stride apart from in.
+static bool rows_overlap(const void* out, int64_t row, const void* in, int64_t in_row, int64_t in_stride, int64_t n) {
+  if (!out || !in || n <= 0) return false;
+  const __int128 o = reinterpret_cast<uintptr_t>(out), p = reinterpret_cast<uintptr_t>(in);
+  const __int128 len = static_cast<__int128>(in_row) * 2, step = static_cast<__int128>(in_stride) * 2;
+  const __int128 end = o + static_cast<__int128>(n) * row * 2;
+  if (end <= p || o >= p + (n - 1) * step + len) return false;  // apart, as in most calls: no division
+  const __int128 i = o < p + len ? 0 : (o - p - len) / step + 1;  // the first row that ends behind out's start
+  return i < n && p + i * step < end;
+}
+
 static int check_step(const padoc_kv_pool* pool, const padoc_rope* rope, int32_t max_pos, const padoc_kv_step* st,
-                      const char* what) {
+                      int64_t n, const char* what) {
   const int64_t row = static_cast<int64_t>(pool->Hkv) * pool->d;
   if (!st) return fail(PADOC_ERR_INVALID, "%s: null step", what);
   if (!st->k || !st->v || !aligned16(st->k) || !aligned16(st->v) || !aligned16(st->k_rot))
@@ -1265,6 +1277,18 @@ static int check_step(const padoc_kv_pool* pool, const padoc_rope* rope, int32_t
     if (st->q_stride < static_cast<int64_t>(st->Hq) * pool->d || st->q_stride % 8)
       return fail(PADOC_ERR_INVALID, "%s: the q row stride must be a multiple of 8 of at least Hq * d", what);
   }
+  // Rows are turned in no order: an output may lie on its own input, row on row, and on nothing else.
+  const int64_t q_row = st->q ? static_cast<int64_t>(st->Hq) * pool->d : 0;
+  const bool q_on_q = st->q_rot == st->q && (n <= 1 || st->q_stride == q_row);
+  const bool k_on_k = st->k_rot == st->k && (n <= 1 || st->k_stride == row);
+  if ((!q_on_q && rows_overlap(st->q_rot, q_row, st->q, q_row, st->q_stride, n)) ||
+      rows_overlap(st->q_rot, q_row, st->k, row, st->k_stride, n) ||
+      rows_overlap(st->q_rot, q_row, st->v, row, st->v_stride, n) ||
+      rows_overlap(st->q_rot, q_row, st->k_rot, row, row, n) ||
+      rows_overlap(st->k_rot, row, st->q, q_row, st->q_stride, n) ||
+      (!k_on_k && rows_overlap(st->k_rot, row, st->k, row, st->k_stride, n)) ||
+      rows_overlap(st->k_rot, row, st->v, row, st->v_stride, n))
+    return fail(PADOC_ERR_INVALID, "%s: q_rot / k_rot overlap rows that the call reads, or each other", what);
   if (!rope) return PADOC_OK;
   if (rope->rot_dim < 0 || rope->rot_dim > pool->d || rope->rot_dim % 32)
     return fail(PADOC_ERR_INVALID, "%s: rot_dim must be a multiple of 32 in [0, d]", what);
@@ -1279,7 +1303,7 @@ static int check_step(const padoc_kv_pool* pool, const padoc_rope* rope, int32_t
 extern "C" int padoc_kv_write(const padoc_kv_rows* rows, const padoc_rope* rope, const padoc_kv_step* step, void* ws,
                               padoc_stream_t stream) {
   if (!rows) return fail(PADOC_ERR_INVALID, "kv_write: null rows");
-  int rc = check_step(rows->pool, rope, rows->max_pos, step, "kv_write");
+  int rc = check_step(rows->pool, rope, rows->max_pos, step, rows->n_rows, "kv_write");
   if (rc) return rc;
   if (rows->n_rows == 0) return PADOC_OK;
   rc = rows_check(rows, "kv_write", true, ws);
@@ -1356,7 +1380,7 @@ extern "C" int padoc_kv_append_rope(padoc_kv_pool* pool, int32_t n_seqs, const i
       if (positions[j] < 0) return fail(PADOC_ERR_INVALID, "kv_append_rope: positions[%lld] < 0", static_cast<long long>(j));
       max_pos = std::max(max_pos, positions[j]);
     }
-    int rc = check_step(pool, rope, max_pos, step, "kv_append_rope");
+    int rc = check_step(pool, rope, max_pos, step, total, "kv_append_rope");
     if (rc) return rc;
     if (total == 0) return PADOC_OK;
     if (!pool->k || !pool->v) return fail(PADOC_ERR_INVALID, "kv_append_rope: pool has no storage");
