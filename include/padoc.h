@@ -245,7 +245,8 @@ PADOC_API int padoc_debug_kv_pool_rehome(padoc_kv_pool* pool, int32_t device);
  *   padoc_kv_rows_ws_size  device workspace bytes; 0 for short lists
  *   padoc_kv_rows_upload   copies the lists into ws (16-byte aligned); once,
  *                          before the first write or gather.  Those then only
- *                          launch a kernel, so they may be captured.
+ *                          launch a kernel, so they may be captured; the copy
+ *                          itself is refused on a stream that is.
  *   padoc_kv_rows_free
  * A handle belongs to one pool and may be used any number of times, until one of
  * its sequences is released or trims the slots (the calls then return
@@ -309,7 +310,8 @@ PADOC_API int padoc_kv_gather(const padoc_kv_rows* rows, void* k, void* v, void*
  * row_offsets[i + 1]) to sequence seqs[i] (each at most once).  ws: device,
  * 16-byte aligned, 16 bytes for each block touched when those are more than
  * 224, plus 4 bytes a row with positions; may be NULL when that is 0.  Not in
- * use by a running call.  Validation and block reservation come first: on any
+ * use by a running call, and a call that needs it is refused on a stream that is
+ * captured.  Validation and block reservation come first: on any
  * refusal and on PADOC_ERR_OOM the pool is as it was. */
 PADOC_API int padoc_kv_append_rope(padoc_kv_pool* pool, int32_t n_seqs, const int32_t* seqs, const int32_t* row_offsets,
                                    const int32_t* positions, const padoc_rope* rope, const padoc_kv_step* step,

@@ -1165,6 +1165,16 @@ static int rows_check_ws(const padoc_kv_rows* rows, const void* ws, size_t ws_by
   return PADOC_OK;
 }
 
+// A captured copy would read the list's host memory again at each replay, when it may be gone.
+static int check_not_captured(cudaStream_t s, const char* what) {
+  cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+  const cudaError_t e = cudaStreamIsCapturing(s, &st);
+  if (e == cudaErrorStreamCaptureImplicit) (void)cudaGetLastError();
+  if (e == cudaErrorStreamCaptureImplicit || (e == cudaSuccess && st != cudaStreamCaptureStatusNone))
+    return fail(PADOC_ERR_INVALID, "%s: row lists cannot be uploaded while the stream is captured", what);
+  return e == cudaSuccess ? PADOC_OK : cuda_fail(e, what);
+}
+
 extern "C" int padoc_kv_rows_upload(padoc_kv_rows* rows, void* ws, size_t ws_bytes, padoc_stream_t stream) {
   if (!rows) return fail(PADOC_ERR_INVALID, "kv_rows_upload: null rows");
   if (rows->n_rows == 0) {
@@ -1177,6 +1187,7 @@ extern "C" int padoc_kv_rows_upload(padoc_kv_rows* rows, void* ws, size_t ws_byt
   rc = padoc::pool_check_device(rows->pool, "kv_rows_upload");
   if (rc) return rc;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (!rows->host.empty() && (rc = check_not_captured(st, "kv_rows_upload"))) return rc;
   rc = pool_sync(rows->pool, st);  // the storage is zeroed once, before any row is written
   if (rc) return rc;
   if (!rows->host.empty()) {
@@ -1397,6 +1408,7 @@ extern "C" int padoc_kv_append_rope(padoc_kv_pool* pool, int32_t n_seqs, const i
                            (positions ? static_cast<size_t>(total) * sizeof(int32_t) : 0);
     if (need_ws && (!ws || !aligned16(ws) || ws_bytes < need_ws))
       return fail(PADOC_ERR_INVALID, "kv_append_rope: ws must be 16-byte aligned and hold %zu bytes", need_ws);
+    if (need_ws && (rc = check_not_captured(reinterpret_cast<cudaStream_t>(stream), "kv_append_rope"))) return rc;
     std::vector<int32_t> fresh;
     if (extra_total > static_cast<int64_t>(pool->free_blocks.size()) ||
         !pool->take_blocks(static_cast<int32_t>(extra_total), &fresh))
