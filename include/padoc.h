@@ -665,14 +665,14 @@ PADOC_API int padoc_branch_decode_noalloc(padoc_kv_pool* pool, const padoc_decod
 
 /* Testing aid, not for normal use: sets, on the current device, the longest
  * time (nanoseconds) one wait of the verify own pass with keys on the MMA's
- * M side may take before the kernel gives up and reports
- * PADOC_ERR_DEVICE_TIMEOUT through padoc_device_status; 0 restores the
- * default of 2 s.  It applies to that kernel only: when one of its roles
- * gives up, the others leave their loops, its TMA producers wait for the
- * copies they issued and its MMA thread for its products before the CTA
- * releases tensor memory and exits, so a wait that runs out leaves the GPU
- * usable for the next call (HPD-Parsing's failure detection has no GPU-side
- * counterpart; this serves tests of the abort path). */
+ * M side, or of the tcgen05 prefix pass over a 4-bit pool, may take before the
+ * kernel gives up and reports PADOC_ERR_DEVICE_TIMEOUT through
+ * padoc_device_status; 0 restores the default of 2 s.  It applies to those two
+ * kernels only: when one of their roles gives up, the others leave their loops,
+ * their producers wait for the copies they issued and their MMA threads for
+ * their products before the CTA releases tensor memory and exits, so a wait
+ * that runs out leaves the GPU usable for the next call (HPD-Parsing's failure
+ * detection has no GPU-side counterpart; this serves tests of the abort path). */
 PADOC_API int padoc_debug_set_wait_limit(uint64_t ns);
 
 /* Reports and clears the device error word of the current device: 0 when no

@@ -856,6 +856,7 @@ extern "C" int padoc_debug_set_wait_limit(uint64_t ns) {
   const cudaError_t e = cudaMemcpyToSymbol(padoc::g_own_wait_limit_ns, &v, sizeof(v));
   if (e != cudaSuccess)
     return padoc::set_error(PADOC_ERR_CUDA, "debug_set_wait_limit: %s", cudaGetErrorString(e));
+  if (padoc::set_i4_wait_limit(v)) return padoc::set_error(PADOC_ERR_CUDA, "debug_set_wait_limit: 4-bit prefix kernel");
   return PADOC_OK;
 }
 

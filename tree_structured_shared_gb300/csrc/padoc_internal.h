@@ -257,6 +257,7 @@ int launch_i4_units(const I4Args& a, int32_t unit0, int32_t n, int warps, cudaSt
 // The same for a page's prefix and units of up to 128 rows.
 int launch_i4_prefix_tc(const I4Args& a, int32_t n_groups, cudaStream_t s, std::string* err);
 int read_and_clear_i4_error(cudaStream_t s, unsigned* word);
+int set_i4_wait_limit(uint64_t ns);
 int launch_i4_merge(const I4Args& a, int32_t n_merges, cudaStream_t s, std::string* err);
 int launch_kv_write(const RowsArgs& a, cudaStream_t s, std::string* err);
 int launch_kv_gather(const RowsArgs& a, cudaStream_t s, std::string* err);

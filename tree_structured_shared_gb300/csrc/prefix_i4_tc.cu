@@ -59,7 +59,10 @@
 // or zero (one fma an element less: 863 us instead of 885 on the second case, 872 instead
 // of 884 on the first).
 // Every wait is bounded; a role that gives up raises the CTA's abort flag and
-// the device error word, and all roles leave their loops.
+// the device error word, and all roles leave their loops: no warp arrives twice on a
+// barrier's phase, since it first waits for what that phase's completion implies; the
+// decoders wait for their copies, and each issuer commits once more and waits for that,
+// before the CTA's threads meet and TMEM is released.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -73,6 +76,9 @@
 namespace padoc {
 
 __device__ unsigned int g_i4_err;
+// Longest time one wait of the prefix kernel may take before it gives up (nanoseconds of
+// the global timer); settable for tests, read at launch.
+__device__ unsigned long long g_i4_wait_limit_ns = ptx::kWaitLimitNs;
 
 namespace {
 
@@ -116,7 +122,8 @@ enum {
 };
 // The commits of S and P V free the stages that they read too: each wait and commit
 // between two groups of products is time in which the issuing thread stands still.
-constexpr int SM_MISC = SM_BAR + N_BARS * 8;
+constexpr int SM_MISC = SM_BAR + N_BARS * 8;  // TMEM address, abort flag, limit of a wait (64 bits)
+static_assert(SM_MISC % 8 == 0, "the limit's alignment");
 constexpr int kSmemBytes = SM_MISC + 16 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 constexpr uint32_t kTmemO = 384;  // S / P of buffer b at 128 b
@@ -165,6 +172,26 @@ __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
   return v;
 }
 
+// As mbar_wait and mbar_wait_relaxed, with the limit that lies behind the abort flag.
+template <bool RELAXED>
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int* abort) {
+  auto done = [&]() { return RELAXED ? mbar_try_wait_relaxed(bar, parity) : mbar_try_wait(bar, parity); };
+  if (done()) return true;
+  const uint64_t t0 = global_timer();
+  while (true) {
+    for (int i = 0; i < 32; ++i)
+      if (done()) return true;
+    if (*abort) return false;
+    if (global_timer() - t0 > *reinterpret_cast<volatile uint64_t*>(abort + 1)) return false;
+  }
+}
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+  return wait_phase<false>(bar, parity, abort);
+}
+__device__ __forceinline__ bool wait_relaxed(uint32_t bar, uint32_t parity, volatile int* abort) {
+  return wait_phase<true>(bar, parity, abort);
+}
+
 __device__ __forceinline__ void raise_abort(volatile int* abort, unsigned site) {
   *abort = 1;
   atomicOr(&g_i4_err, site);
@@ -192,6 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a) 
       mbar_init(bar(i), cnt);
     }
     *abort = 0;
+    *reinterpret_cast<volatile uint64_t*>(abort + 1) = g_i4_wait_limit_ns;
     fence_mbar_init();
   }
   if (warp == 0) {
@@ -276,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a) 
         // the stage's last tile, two back: S (K) or P V (V) has run
         const uint32_t old = kt - 2;
         if (kt >= 2 &&
-            !__all_sync(0xffffffffu, mbar_wait(bar((is_k ? B_S_FULL : B_PV_DONE) + old % 3), (old / 3) & 1, abort))) {
+            !__all_sync(0xffffffffu, wait(bar((is_k ? B_S_FULL : B_PV_DONE) + old % 3), (old / 3) & 1, abort))) {
           failed = true;
           break;
         }
@@ -331,11 +359,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a) 
       bool failed = false;
       for (int u = u0; u < u1 && !failed; ++u, ++iu) {
         const int n = (a.units[u].n_keys + kTileKeys - 1) / kTileKeys;
-        if (!mbar_wait_relaxed(bar(B_Q_FULL), iu & 1, abort)) failed = true;
+        if (!wait_relaxed(bar(B_Q_FULL), iu & 1, abort)) failed = true;
         for (int j = 0; j < n && !failed; ++j, ++k) {
           // the buffer last held P of the tile three back
-          if ((round > 0 && !mbar_wait_relaxed(bar(B_PV_DONE + sb), (round - 1) & 1, abort)) ||
-              !mbar_wait_relaxed(bar(B_K_FULL + (k & 1)), (k >> 1) & 1, abort)) {
+          if ((round > 0 && !wait_relaxed(bar(B_PV_DONE + sb), (round - 1) & 1, abort)) ||
+              !wait_relaxed(bar(B_K_FULL + (k & 1)), (k >> 1) & 1, abort)) {
             failed = true;
             break;
           }
@@ -367,8 +395,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a) 
         const int n = (a.units[u].n_keys + kTileKeys - 1) / kTileKeys;
         for (int j = 0; j < n; ++j, ++k) {
           const int st = k & 1;
-          if (!mbar_wait_relaxed(bar(B_V_FULL + st), (k >> 1) & 1, abort) ||
-              !mbar_wait_relaxed(bar(B_P_HALF + pb), round & 1, abort)) {
+          if (!wait_relaxed(bar(B_V_FULL + st), (k >> 1) & 1, abort) ||
+              !wait_relaxed(bar(B_P_HALF + pb), round & 1, abort)) {
             failed = true;
             break;
           }
@@ -378,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a) 
           for (int kk = 0; kk < 4; ++kk)
             mma_bf16_ts(tmem + kTmemO, tmem + pb * 128 + kk * 8, d_v + static_cast<uint64_t>(kk * (2048 >> 4)), id_pv,
                         (j > 0 || kk > 0) ? 1u : 0u);
-          if (!mbar_wait_relaxed(bar(B_P_FULL + pb), round & 1, abort)) {
+          if (!wait_relaxed(bar(B_P_FULL + pb), round & 1, abort)) {
             failed = true;
             break;
           }
@@ -489,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a) 
       const int R = un.row0 + r, tok = div_g(R, a.g_inv);
       const int limit = valid ? min(n_keys, a.q_plen[un.q_first + tok] - un.key0) : n_keys;
       const int limit_min = __reduce_min_sync(0xffffffffu, limit);
-      if (!__all_sync(0xffffffffu, mbar_wait(bar(B_Q_FULL), iu & 1, abort))) {
+      if (!__all_sync(0xffffffffu, wait(bar(B_Q_FULL), iu & 1, abort))) {
         failed = true;
         break;
       }
@@ -503,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a) 
       for (; j < n; j += 3, ++round) {
         // A tile that opens a unit: the last epilogue must have read O before P V
         // overwrites it, and the references before this tile's take their place.
-        if (j == 0 && wg > 0 && iu > 0 && !__all_sync(0xffffffffu, mbar_wait(bar(B_O_FREE), (iu - 1) & 1, abort))) {
+        if (j == 0 && wg > 0 && iu > 0 && !__all_sync(0xffffffffu, wait(bar(B_O_FREE), (iu - 1) & 1, abort))) {
           failed = true;
           break;
         }
@@ -511,13 +539,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a) 
         float m_old = -INFINITY;
         const uint32_t kt_before = kt0 + j - 1;
         if (j > 0) {
-          if (!__all_sync(0xffffffffu, mbar_wait(bar(B_M_FULL + before), (kt_before / 3) & 1, abort))) {
+          if (!__all_sync(0xffffffffu, wait(bar(B_M_FULL + before), (kt_before / 3) & 1, abort))) {
             failed = true;
             break;
           }
           m_old = m_sh[before * 128 + r];
         }
-        if (!__all_sync(0xffffffffu, mbar_wait_relaxed(bar(B_S_FULL + wg), round & 1, abort))) {
+        if (!__all_sync(0xffffffffu, wait_relaxed(bar(B_S_FULL + wg), round & 1, abort))) {
           failed = true;
           break;
         }
@@ -568,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a) 
             // O holds sums against the old reference: rescale once P V of the tile before
             // has run (the one before it on that barrier had when S of that tile was issued)
             const float alpha = grow ? fast_exp2((m_old - mx) * sl2) : 1.f;  // 0 while m_old is -inf
-            if (!__all_sync(0xffffffffu, mbar_wait_relaxed(bar(B_PV_DONE + before), (kt_before / 3) & 1, abort))) {
+            if (!__all_sync(0xffffffffu, wait_relaxed(bar(B_PV_DONE + before), (kt_before / 3) & 1, abort))) {
               failed = true;
               break;
             }
@@ -631,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a) 
       if (wg > 0) {
         // not before group 0 is through with the unit before: it follows these
         // barriers one phase at a time
-        if (iu > 0 && !__all_sync(0xffffffffu, mbar_wait(bar(B_O_FREE), (iu - 1) & 1, abort))) {
+        if (iu > 0 && !__all_sync(0xffffffffu, wait(bar(B_O_FREE), (iu - 1) & 1, abort))) {
           failed = true;
           break;
         }
@@ -643,8 +671,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a) 
         if (wg == 2 && u + 1 < u1) {
           // Q is free once the unit's last S has run (its barrier cannot move on before
           // the next Q is out), and Q_FULL once the other groups have seen it
-          if (!__all_sync(0xffffffffu, mbar_wait(bar(B_E_IN), iu & 1, abort)) ||
-              !__all_sync(0xffffffffu, mbar_wait_relaxed(bar(B_S_FULL + last % 3), (last / 3) & 1, abort))) {
+          if (!__all_sync(0xffffffffu, wait(bar(B_E_IN), iu & 1, abort)) ||
+              !__all_sync(0xffffffffu, wait_relaxed(bar(B_S_FULL + last % 3), (last / 3) & 1, abort))) {
             failed = true;
             break;
           }
@@ -654,8 +682,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_i4_kernel(const I4Args a) 
       }
       // The other groups have handed over all their P; the last P V's commit covers all
       // before it (the one before it on that barrier had run when the last S was issued).
-      if (!__all_sync(0xffffffffu, mbar_wait(bar(B_ML_FULL), iu & 1, abort)) ||
-          !__all_sync(0xffffffffu, mbar_wait_relaxed(bar(B_PV_DONE + last % 3), (last / 3) & 1, abort))) {
+      if (!__all_sync(0xffffffffu, wait(bar(B_ML_FULL), iu & 1, abort)) ||
+          !__all_sync(0xffffffffu, wait_relaxed(bar(B_PV_DONE + last % 3), (last / 3) & 1, abort))) {
         failed = true;
         break;
       }
@@ -731,6 +759,11 @@ int launch_i4_prefix_tc(const I4Args& a, int32_t n_groups, cudaStream_t s, std::
     return PADOC_ERR_CUDA;
   }
   return PADOC_OK;
+}
+
+int set_i4_wait_limit(uint64_t ns) {
+  const unsigned long long v = ns;
+  return cudaMemcpyToSymbol(g_i4_wait_limit_ns, &v, sizeof(v)) == cudaSuccess ? PADOC_OK : PADOC_ERR_CUDA;
 }
 
 int read_and_clear_i4_error(cudaStream_t s, unsigned* word) {

@@ -701,6 +701,6 @@ def device_status(stream=None):
 
 def debug_set_wait_limit(ns: int):
     """Testing aid (padoc_debug_set_wait_limit): the wait limit of the
-    verify own pass's keys-on-M kernel on the current device; 0 restores
-    the default."""
+    verify own pass's keys-on-M kernel and of the 4-bit prefix pass's tcgen05
+    kernel on the current device; 0 restores the default."""
     _check(lib().padoc_debug_set_wait_limit(int(ns)))
