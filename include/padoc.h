@@ -300,8 +300,8 @@ typedef struct {
 PADOC_API int padoc_kv_write(const padoc_kv_rows* rows, const padoc_rope* rope, const padoc_kv_step* step, void* ws,
                              padoc_stream_t stream);
 
-/* Reads counted rows back: k, v device [n, Hkv, d] bf16, dense, which may
- * not overlap: to move a sequence to another pool of either dtype (padoc_kv_append
+/* Reads counted rows back: k, v device [n, Hkv, d] bf16, dense, which do not
+ * overlap: to move a sequence to another pool of either dtype (padoc_kv_append
  * takes them as they are) or to use the rows elsewhere.  (padoc_tree_attn_varlen
  * wants a query for every key, so it does not run new rows over gathered ones.)
  * K comes as stored, that is rotated.  A sequence may be named several times, and rows

@@ -79,14 +79,3 @@ def test_against_every_byte(pool):
         hit = any(max(out.start, A + i * 2 * stride) < min(out.stop, A + i * 2 * stride + 2 * ROW) for i in range(n))
         want = hit and not (off == 0 and n == 1)
         assert refused(pool, n=n, **base, k_rot=A + off) == want, (n, off)
-
-
-@pytest.mark.parametrize("off,want", [(0, True), (2 * N * ROW - 16, True), (2 * N * ROW, False), (-2 * N * ROW, False),
-                                      (16 - 2 * N * ROW, True)])
-def test_gather_into_one_buffer(pool, off, want):
-    s = pool.alloc(N)
-    pool.advance(s, N)
-    rows = padoc.KVRows(pool, [s], [0], [0, N])
-    with pytest.raises(padoc.PadocError) as e:
-        rows.gather(A, A + off)
-    assert e.value.code == padoc.ERR_INVALID and ("overlap" in str(e.value)) == want

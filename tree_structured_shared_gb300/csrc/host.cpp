@@ -1345,8 +1345,6 @@ extern "C" int padoc_kv_gather(const padoc_kv_rows* rows, void* k, void* v, void
   if (rows->n_rows == 0) return PADOC_OK;
   if (!k || !v || !aligned16(k) || !aligned16(v))
     return fail(PADOC_ERR_INVALID, "kv_gather: k/v must be 16-byte aligned device pointers");
-  const int64_t row = static_cast<int64_t>(rows->pool->Hkv) * rows->pool->d;
-  if (rows_overlap(k, row, v, row, row, rows->n_rows)) return fail(PADOC_ERR_INVALID, "kv_gather: k and v overlap");
   int rc = rows_check(rows, "kv_gather", false, ws);
   if (rc) return rc;
   RowsArgs a = rows_args(rows, ws);
