@@ -27,7 +27,6 @@ namespace padoc {
 constexpr int kI4Unit = kI4UnitBytes;
 constexpr int kI4Scales = 1024;   // offset of its scales
 constexpr float kI4MaxScale = 896.f;
-constexpr uint32_t kI4MaxByte = 0xC6u;  // its byte
 constexpr uint32_t kI4Nan = 0xFFu;  // scale byte of a poisoned group (an fp16 NaN)
 
 // Scale byte of a group whose largest magnitude is 7 * a (a >= 0, finite): a rounded to
