@@ -29,8 +29,8 @@
 // 2^-35 of the row's largest weight.  Sums, maxima and O are f32.
 //
 // What bounds it: a key costs a warp about 25 instructions for a head's 8 rows, and
-// four warps a scheduler (126 registers) issue one every other cycle.  Suffixes of 4500
-// branches (0-1024 tokens, 8 kv heads): 564 us, of which the copies alone take 449 (404
+// four warps a scheduler (128 registers) issue one every other cycle.  Suffixes of 4500
+// branches (0-1024 tokens, 8 kv heads): 562 us, of which the copies alone take 449 (404
 // at HBM rate) and the arithmetic alone 490; 1500 branches with up to 16 query tokens:
 // 300 us (237 at HBM rate).  Neither more independent products (two blocks' score
 // chains interleaved, accumulators split) nor shorter loops nor the query block and

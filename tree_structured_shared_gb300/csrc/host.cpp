@@ -1533,9 +1533,9 @@ int plan_i4(const padoc_kv_pool* pool, const padoc_decode_batch* b, int32_t Hq, 
   const int32_t G = Hq / pool->Hkv, bs = pool->bs, nq = static_cast<int32_t>(pl->q_plen.size());
   constexpr int32_t kRows = 8;  // rows of a warp-level unit
   // Prefix units on the tcgen05 kernel where the rows are more than one warp-level
-  // tile (64 pages of 5000 tokens: 154 us against 91, 172 and 216 us of the warp-level
-  // kernel with 8, 12-16 and 20 rows; 8 pages: 31 against 23, 31 and 37; one page: 15
-  // against 13 with 8 to 20).
+  // tile (64 pages of 5000 tokens: 162 us against 93, 171-173 and 214 us of the warp-level
+  // kernel with 8, 12-16 and 20 rows; 8 pages: 31 against 23, 31 and 37; one page: 17
+  // against 13 with 8 to 16 and 15 with 20).
   auto on_tc = [](int32_t rows) { return rows > kRows; };
   auto blocks = [bs](int64_t n) { return (n + bs - 1) / bs; };
   // Chunks of keys: of a page's prefix with few rows about two units an SM, which eight

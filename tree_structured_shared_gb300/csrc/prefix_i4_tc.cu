@@ -27,11 +27,12 @@
 // What bounds it: a tile goes round its S buffer in some 6000 cycles, three tiles at a
 // time (S issued in 900, first softmax pass 1000, second 1700, P V issued in 800, some
 // 450 between any two), so 1950 cycles a tile, of which the products need 1024 of the
-// tensor pipe.  The products run slower than that because shared memory's data pipe is
-// 76 % busy: a tile's products read 96 KB, the decoders write 64 KB, and the codes pass
+// tensor pipe.  (These are from before the second pass took the difference of two scores
+// ahead of the factor, see below; the whole pass takes 3 to 4 % longer since.)  The products run slower than that because shared memory's data pipe is
+// 73 % busy: a tile's products read 96 KB, the decoders write 64 KB, and the codes pass
 // twice, 72 KB.  Schedulers issue every other cycle.
-//   128 pages of 4000-6144 tokens with 8-60 branches: 316 us (112 at HBM rate)
-//   64 pages of 4809 tokens, 8-40 branches of up to 16 query tokens: 566 us (the
+//   128 pages of 4000-6144 tokens with 8-60 branches: 326 us (112 at HBM rate)
+//   64 pages of 4809 tokens, 8-40 branches of up to 16 query tokens: 588 us (the
 //   products alone: 336)
 // What was measured on the way there (the two cases in us):
 //   - two softmax groups instead of three: 640 on the second; one thread issuing both
@@ -43,7 +44,8 @@
 //     pass, or half the words in the decoders', costs 3 %, twice the columns 10 %;
 //   - P handed over in two halves, the reference waited for ahead of S: 336, 564;
 //   - lanes past a unit's rows, whose Q is what the buffer held, no longer ask for
-//     rescalings of O: 324; decoders' reads without bank conflicts: 316;
+//     rescalings of O: 324; decoders' reads without bank conflicts: 316, 566;
+//   - scores less the reference before the factor, below: 326, 588;
 //   - issue code with constant stages and buffers, or more registers for it: 2 to 6 %
 //     slower.
 //
@@ -56,8 +58,9 @@
 // zero is below 2^-34 of the row's largest weight.  References are scores as they come
 // out of S, and x - m is their difference times the factor: the product of each, rounded
 // on its own, would be off by whole powers of two from scores of 2^24 on, and P infinite
-// or zero (one fma an element less: 863 us instead of 885 on the second case, 872 instead
-// of 884 on the first).
+// or zero.  (One fma an element and no subtraction: 12 us less on the first case, 22 on
+// the second, own pass included.  Finding such rows by their factor and multiplying their
+// scores ahead of that fma cost 10 to 33 us, though no row took it.)
 // Every wait is bounded; a role that gives up raises the CTA's abort flag and
 // the device error word, and all roles leave their loops: no warp arrives twice on a
 // barrier's phase, since it first waits for what that phase's completion implies; the
