@@ -2,6 +2,8 @@
 replays would read that memory again, an upload and an append_rope that needs
 one are refused and change nothing; a write whose lists were uploaded before is
 captured and replayed as documented."""
+import gc
+
 import numpy as np
 import pytest
 
@@ -14,7 +16,7 @@ pytestmark = pytest.mark.gpu
 
 
 @pytest.mark.parametrize("dtype", [padoc.BF16, padoc.I4])
-def test_lists_are_not_uploaded_into_a_graph(padoc_lib, dtype):
+def test_lists_are_not_uploaded_into_a_graph(padoc_lib, request, dtype):
     import torch
     Hkv, n = 2, 16 * 230
     pool, kp, vp = make_pool(torch, 500, Hkv, dtype, max_bps=480)
@@ -38,6 +40,10 @@ def test_lists_are_not_uploaded_into_a_graph(padoc_lib, dtype):
             codes.append(None)
 
     g, st = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    # an earlier test's pool that is collected now would free its block table, which ends a capture
+    gc.collect()
+    gc.disable()
+    request.addfinalizer(gc.enable)
     with torch.cuda.graph(g, stream=st):
         code(pool.append_rope, [few], [0, 20], k, v, ws, ws.numel(), positions=pos, rope=rope)  # positions
         code(pool.append_rope, [many], [0, n], k, v, ws, ws.numel())                            # more than 224 blocks
