@@ -251,7 +251,8 @@ PADOC_API int padoc_debug_kv_pool_rehome(padoc_kv_pool* pool, int32_t device);
  * A handle belongs to one pool and may be used any number of times, until one of
  * its sequences is released or trims the slots (the calls then return
  * PADOC_ERR_INVALID; a captured launch is not checked again when it is replayed).
- * Creating a handle changes nothing in the pool.
+ * Creating a handle changes nothing in the pool; once the pool is destroyed, a
+ * handle may only be freed.
  * ---------------------------------------------------------------------- */
 typedef struct padoc_kv_rows padoc_kv_rows;
 PADOC_API int padoc_kv_rows_create(padoc_kv_pool* pool, int32_t n_seqs, const int32_t* seqs, const int32_t* first,

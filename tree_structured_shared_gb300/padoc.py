@@ -378,8 +378,7 @@ class KVPool:
     def append_rope(self, seqs: Sequence[int], row_offsets: Sequence[int], k, v, ws=None, ws_bytes: int = 0, *,
                     positions=None, rope: Optional["Rope"] = None, stream=None, **step):
         """padoc_kv_append_rope: reserve, write and advance; step as in KVRows.write."""
-        a, b = _i32(seqs if len(seqs) else [0]), _i32(row_offsets)
-        p = None if positions is None else _i32(positions)
+        a, _, b, p = _row_lists(seqs, None, row_offsets, positions)
         st = _kv_step(self, k, v, **step)
         _check(lib().padoc_kv_append_rope(self.handle, len(seqs), _p32(a), _p32(b), None if p is None else _p32(p),
                                           None if rope is None else C.byref(rope.c), C.byref(st), _ptr(ws),
@@ -424,20 +423,30 @@ def _kv_step(pool: "KVPool", k, v, *, k_stride=None, v_stride=None, q=None, Hq: 
                   row if v_stride is None else int(v_stride), _ptr(k_rot))
 
 
+def _row_lists(seqs, first, row_offsets, positions):
+    """The host arrays of a row list; the library reads len(seqs) of first, one
+    more of row_offsets and a position a row, so shorter ones are refused."""
+    n = len(seqs)
+    a, b = _i32(seqs if n else [0]), _i32(row_offsets)
+    f = None if first is None else _i32(first if len(first) else [0])
+    p = None if positions is None else _i32(positions)
+    if n and (b.size <= n or (f is not None and f.size < n) or (p is not None and p.size < b[n])):
+        raise PadocError(ERR_INVALID, "first, row_offsets or positions is shorter than the sequences and rows need")
+    return a, f, b, p
+
+
 class KVRows:
     """Token ranges of sequences (padoc_kv_rows): written from, or read back
     into, packed rows in one launch."""
 
     def __init__(self, pool: KVPool, seqs: Sequence[int], first: Optional[Sequence[int]], row_offsets: Sequence[int],
                  positions=None):
-        a, b = _i32(seqs if len(seqs) else [0]), _i32(row_offsets)
-        f = None if first is None else _i32(first if len(first) else [0])
-        p = None if positions is None else _i32(positions)
+        a, f, b, p = _row_lists(seqs, first, row_offsets, positions)
         h = C.c_void_p()
         _check(lib().padoc_kv_rows_create(pool.handle, len(seqs), _p32(a), None if f is None else _p32(f), _p32(b),
                                           None if p is None else _p32(p), C.byref(h)))
         self.handle = h
-        self.n = int(b[-1]) if len(seqs) else 0
+        self.n = int(b[len(seqs)]) if len(seqs) else 0
         self._pool, self._row, self._lib = pool, pool.Hkv * pool.d, lib()
 
     def ws_size(self) -> int:
