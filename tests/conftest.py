@@ -1,3 +1,4 @@
+import gc
 import os
 import sys
 
@@ -36,3 +37,11 @@ def padoc_lib():
     from tree_structured_shared_gb300 import build, padoc
     build.build()
     return padoc.lib()
+
+
+@pytest.fixture(autouse=True)
+def _collected_before(request):
+    """Pools of earlier tests are collected now: freeing their block tables while
+    a test captures a graph would end the capture."""
+    if "gpu" in request.keywords:
+        gc.collect()
