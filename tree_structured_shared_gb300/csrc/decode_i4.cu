@@ -280,8 +280,11 @@ __global__ void __launch_bounds__(32 * W, 16 / W) decode_i4_kernel(const I4Args 
       return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
     };
     uint32_t mx = row_max(max(most2 & 0xffffu, most2 >> 16));
-    if (__any_sync(0xffffffffu, mx >= 0x7f80u)) {
-      // an infinity or a NaN: the row's largest finite one sets the factor
+    // an infinity or a NaN: every score is infinite or NaN, and so the softmax NaN, of
+    // scores that are all -inf too, which would pass for keys that the row does not see
+    const bool infinite = mx >= 0x7f80u;
+    if (__any_sync(0xffffffffu, infinite)) {
+      // the row's largest finite one sets the factor
       uint32_t m = 0;
 #pragma unroll
       for (int x = 0; x < 16; ++x) {
@@ -296,11 +299,11 @@ __global__ void __launch_bounds__(32 * W, 16 / W) decode_i4_kernel(const I4Args 
     for (int x = 0; x < 16; ++x)
       q[x] = pack_f16x2(__uint_as_float(q[x] << 16) * qf, __uint_as_float(q[x] & 0xffff0000u) * qf);
     // the scores' factors, of the rows 2c and 2c + 1 that the lane's scores are of
+    const uint32_t back = infinite ? 0x7fc00000u : static_cast<uint32_t>(127 - kexp) << 23;
     float sl2q[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e)
-      sl2q[e] = a.sl2 * kI4Unscale *
-                __uint_as_float(static_cast<uint32_t>(127 - __shfl_sync(0xffffffffu, kexp, (2 * c + e) * 4)) << 23);
+      sl2q[e] = a.sl2 * kI4Unscale * __uint_as_float(__shfl_sync(0xffffffffu, back, (2 * c + e) * 4));
 
     // rows 2c, 2c + 1: running reference (log2, less kPShift), sums, O of dims 16 i + 2 x + {0, 1}
     float mo[2] = {kNoMax, kNoMax}, l[2] = {0.f, 0.f};
@@ -470,7 +473,8 @@ __global__ void __launch_bounds__(32 * W, 16 / W) decode_i4_kernel(const I4Args 
         vis[e] = bits & ((1u << q_len) - 1u) & (kMine << warp);
       }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[e] = ((vis[e & 1] >> (key_a + (e >> 1) * 2)) & 1u) ? s[e] * a.sl2 : -INFINITY;
+      for (int e = 0; e < 4; ++e)  // plus zero, or NaN, times the row's factor
+        s[e] = ((vis[e & 1] >> (key_a + (e >> 1) * 2)) & 1u) ? fmaf(0.f, sl2q[e & 1], s[e] * a.sl2) : -INFINITY;
       softmax(s1);
       const __nv_bfloat16* vn = a.v_new + at + 16 * i;
       bool added = false;
