@@ -30,7 +30,8 @@
 // tensor pipe.  (These are from before the second pass took the difference of two scores
 // ahead of the factor, see below; the whole pass takes 3 to 4 % longer since.)  The
 // products run slower than that because shared memory's data pipe is 73 % busy: a tile's
-// products read 96 KB, the decoders write 64 KB, and the codes pass twice, 72 KB.  Schedulers issue every other cycle.
+// products read 96 KB, the decoders write 64 KB, and the codes pass twice, 72 KB.  Schedulers
+// issue every other cycle.
 //   128 pages of 4000-6144 tokens with 8-60 branches: 326 us (112 at HBM rate)
 //   64 pages of 4809 tokens, 8-40 branches of up to 16 query tokens: 588 us (the
 //   products alone: 336)
