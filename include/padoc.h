@@ -350,6 +350,125 @@ PADOC_API int padoc_tree_desc_bwd_plan(const padoc_tree_desc* desc, int32_t* ite
                                        int64_t* n_items, int64_t* n_entries);
 
 /* ------------------------------------------------------------------------
+ * Around the attention of a training step.  (The pages train through their
+ * decoder as it is; these are its operators that touch the packed tokens.)
+ *
+ * Rotation tables.  Row r of cos_sin gets the rot_dim / 2 cosines, then the
+ * rot_dim / 2 sines, of position first + r, as padoc_rope reads them.  Pair i
+ * turns by f_i a position, from f_i = base^(-2i / rot_dim):
+ *   PLAIN   f_i
+ *   LINEAR  f_i / factor
+ *   BASE    base * factor^(rot_dim / (rot_dim - 2)) in the place of base
+ *   BANDS   f_i (w + (1 - w) / factor), w = (turns_i - turns_lo) / (turns_hi -
+ *           turns_lo) in [0, 1], turns_i = context f_i / 2 pi
+ *   RAMP    the same with w = 1 - (i - a) / (b - a) in [0, 1], a the pair that
+ *           makes turns_hi turns over the context, rounded down (0 at least),
+ *           b the one that makes turns_lo, rounded up (rot_dim - 1 at most)
+ * Cosines and sines are multiplied by amplitude (0: by 1).  Angles are exact to
+ * the rounding of f_i in 64 bits, at every position.  One launch. */
+enum { PADOC_ROPE_PLAIN = 0, PADOC_ROPE_LINEAR = 1, PADOC_ROPE_BASE = 2, PADOC_ROPE_BANDS = 3, PADOC_ROPE_RAMP = 4 };
+typedef struct {
+  double base;       /* above 1 */
+  int32_t rot_dim;   /* multiple of 32 in [32, 128] */
+  int32_t kind;      /* PADOC_ROPE_* */
+  double factor;     /* at least 1 (not read by PLAIN) */
+  double context;    /* positions that the model was trained on (BANDS, RAMP) */
+  double turns_lo, turns_hi; /* 0 < turns_lo < turns_hi (BANDS, RAMP) */
+  double amplitude;  /* at least 0 */
+} padoc_rope_scaling;
+PADOC_API int padoc_rope_table(const padoc_rope_scaling* scaling, int64_t first, int32_t n_pos,
+                               float* cos_sin /* device [n_pos, rot_dim], 16-byte aligned */, padoc_stream_t stream);
+
+/* Turns the rows of up to four tensors (q and k, say) by their positions, or,
+ * with backward set, gradients of turned rows back into gradients of the rows:
+ *   (a, b) -> (a c - b s, b c + a s);  backward (a c + b s, b c - a s),
+ * in f32, each product and sum rounded on its own, then to dtype; the same bits
+ * as padoc_kv_write's q_rot and k_rot.  dtype PADOC_BF16 or PADOC_F32; d 64 or
+ * 128; rope as in padoc_kv_write (rot_dim 0: a copy).  positions: device [n], or
+ * NULL for the rows' indices.  A row whose position is outside the table gets
+ * NaN in the dims that turn.  Strides are elements between rows, multiples of
+ * 16 bytes; out may be x itself with the same stride, and overlaps nothing else
+ * that the call reads or writes.  One launch. */
+typedef struct {
+  const void* x;      /* device [n, heads, d] */
+  int64_t stride;
+  void* out;          /* device [n, heads, d] */
+  int64_t out_stride;
+  int32_t heads;
+} padoc_rope_part;
+PADOC_API int padoc_rope_apply(const padoc_rope* rope, int32_t n_parts, const padoc_rope_part* parts, int32_t dtype,
+                               int32_t d, int64_t n, const int32_t* positions, int32_t backward,
+                               padoc_stream_t stream);
+
+/* Cross entropy of the next token without the logits in memory.  With
+ * x = h w^T (f32):
+ *   lse = log sum_v exp(x_v),  loss = lse - x_target        (f32, one a row)
+ *   G = d_loss (exp(x - lse) - onehot(target)),  dh = G w,  dw = G^T h
+ * G is rounded to bf16 before the two products, whose sums are f32.  A row with
+ * a negative target has no loss: loss and lse are 0, its dh is zero and it takes
+ * no part in dw, whatever h holds there; its products are not computed.  A
+ * target of V or more is treated alike but for a loss of NaN.
+ *   loss, lse  device [n] f32 out; lse goes into the backward call as it is
+ *   d_loss     device [n] f32: the gradient of each row's loss (1 / count for
+ *              a mean); not read where there is no target
+ *   dh, dw     device [n, D], [V, D] bf16, dense, 16-byte aligned, overwritten;
+ *              either may be NULL
+ *   ws         device, 256-byte aligned, padoc_lm_loss_ws_size bytes (of the
+ *              forward call, or with backward set enough for both), not in use
+ *              by a running call; nothing in it has to outlive a call
+ * D must be a multiple of 8.  Outputs and ws overlap nothing else.  The work
+ * follows the number of rows that have a target, which the host need not know.
+ * Results are deterministic (atomics only hand units out).  No host memory is
+ * read after a call returns, so calls may be captured. */
+typedef struct {
+  const void* h;           /* device [n, D] bf16, 16-byte aligned */
+  int64_t h_stride;        /* elements between rows, a multiple of 8 */
+  const void* w;           /* device [V, D] bf16, 16-byte aligned */
+  int64_t w_stride;
+  const int32_t* targets;  /* device [n] */
+  int32_t n, D, V;
+} padoc_lm_head;
+PADOC_API int padoc_lm_loss_ws_size(int32_t n, int32_t D, int32_t V, int32_t backward, size_t* bytes);
+PADOC_API int padoc_lm_loss(const padoc_lm_head* head, float* loss, float* lse, void* ws, size_t ws_bytes,
+                            padoc_stream_t stream);
+PADOC_API int padoc_lm_loss_bwd(const padoc_lm_head* head, const float* lse, const float* d_loss, void* dh, void* dw,
+                                void* ws, size_t ws_bytes, padoc_stream_t stream);
+
+/* Activations kept in 8 bits between a forward and its backward pass.  32
+ * neighbours of a row share a scale 2^(e - 127), the smallest power of two (e
+ * in [1, 248]) of which 127 reach the largest magnitude; a code is the nearest
+ * integer (ties to even) in [-127, 127], and code * scale is exact in bf16.  An
+ * infinity or a NaN makes its group read back as NaN (e = 255).
+ *   kept  n * width code bytes (int8), row by row, then n * width / 32 bytes e
+ *         (padoc_act_bytes in all), device, 16-byte aligned
+ *   rows  device [n, width] bf16, stride elements between rows (a multiple of 8)
+ * keep reads rows and writes kept, restore the other way round; up to eight
+ * tensors in one launch.  An output overlaps nothing else in the call. */
+typedef struct {
+  void* rows;
+  int64_t stride;
+  int64_t n;
+  int32_t width;  /* positive multiple of 32 */
+  void* kept;
+} padoc_act;
+PADOC_API int padoc_act_bytes(int64_t n, int32_t width, size_t* bytes);
+PADOC_API int padoc_act_keep(int32_t n_tensors, const padoc_act* tensors, padoc_stream_t stream);
+PADOC_API int padoc_act_restore(int32_t n_tensors, const padoc_act* tensors, padoc_stream_t stream);
+
+/* padoc_tree_attn_varlen_bwd from checkpoints of q, k, v and o (rows of Hq * d
+ * or Hkv * d values, the forward's [T, H, d]): the gradients at the values that
+ * the checkpoints stand for, with the forward's lse.  d_o, dq, dk and dv are
+ * bf16.  ws of padoc_tree_attn_varlen_bwd_kept_ws_size bytes, 256-byte aligned,
+ * holds q, k and v in bf16 for the time of the call; o is not expanded. */
+PADOC_API int padoc_tree_attn_varlen_bwd_kept_ws_size(const padoc_tree_desc* desc, int32_t Hq, int32_t Hkv, int32_t d,
+                                                      size_t* bytes);
+PADOC_API int padoc_tree_attn_varlen_bwd_kept(padoc_tree_desc* desc, const void* q_kept, const void* k_kept,
+                                              const void* v_kept, const void* o_kept, const float* lse,
+                                              const void* d_o, void* dq, void* dk, void* dv, int32_t Hq, int32_t Hkv,
+                                              int32_t d, float scale, void* ws, size_t ws_bytes,
+                                              padoc_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * Branch-parallel decode and speculative verify over the pool.
  * Every live branch queries 1..16 tokens against the shared prefix of its
  * page plus its own cached suffix; inside the query block each token sees

@@ -1003,7 +1003,7 @@ int make_map(EncodeTiledFn enc, CUtensorMap* m, const void* ptr, cuuint64_t head
 }  // namespace
 
 int launch_bwd_tc(const BwdArgs& a, cudaStream_t s, std::string* err) {
-  int rc = launch_bwd_delta(a, PADOC_BF16, s, err);
+  int rc = a.have_delta ? PADOC_OK : launch_bwd_delta(a, PADOC_BF16, s, err);
   if (rc) return rc;
   EncodeTiledFn enc = get_encode_fn(err);
   if (!enc) return PADOC_ERR_CUDA;

@@ -191,7 +191,8 @@ int launch_typed(const BwdArgs& a, cudaStream_t s, std::string* err) {
   const T* o = static_cast<const T*>(a.o);
   const T* dout = static_cast<const T*>(a.dout);
   const int64_t warps = a.T * a.Hq;
-  delta_kernel<T, D><<<static_cast<unsigned>((warps * 32 + 255) / 256), 256, 0, s>>>(o, dout, a.delta, a.T, a.Hq);
+  if (!a.have_delta)
+    delta_kernel<T, D><<<static_cast<unsigned>((warps * 32 + 255) / 256), 256, 0, s>>>(o, dout, a.delta, a.T, a.Hq);
   if (a.fwd.n_items > 0)
     dq_core_kernel<T, D><<<dim3(a.fwd.n_items, a.Hkv), kWarps * 32, 0, s>>>(
         a.fwd, q, k, v, dout, a.lse, a.delta, static_cast<T*>(a.dq), a.T, a.Hq, a.Hkv, a.scale);

@@ -478,6 +478,30 @@ extern "C" int padoc_tree_attn_varlen_bwd_ws_size(const padoc_tree_desc* desc, i
   return PADOC_OK;
 }
 
+// The backward on checked arguments; ws as bwd_ws_bytes lays it out.
+static int run_bwd(padoc_tree_desc* desc, BwdArgs& a, int32_t dtype, float scale, void* ws, const char* what,
+                   cudaStream_t stream) {
+  DevPlan* plan = nullptr;
+  int rc = upload_desc(desc, a.Hq / a.Hkv, &plan);
+  if (rc) return rc;
+  a.fwd = {plan->qsegs, plan->kvsegs, plan->items, plan->n_items, a.Hq / a.Hkv, plan->tile_tokens};
+  a.bwd = {plan->bitems, plan->bentries, static_cast<int32_t>(desc->bitems.size())};
+  a.delta = static_cast<float*>(ws);
+  a.work = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + bwd_delta_bytes(desc, a.Hq));
+  a.T = desc->T;
+  a.scale = scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(a.d));
+  std::string err;
+  // bf16 at d = 128 runs on the tensor cores; PADOC_BWD_CORE=1 selects the
+  // CUDA-core kernels instead (a second implementation to compare against)
+  static const bool force_core = std::getenv("PADOC_BWD_CORE") && std::atoi(std::getenv("PADOC_BWD_CORE")) != 0;
+  if (dtype == PADOC_BF16 && a.d == kHeadDim && !force_core)
+    rc = launch_bwd_tc(a, stream, &err);
+  else
+    rc = launch_bwd_core(a, dtype, stream, &err);
+  if (rc) return fail(rc, "%s: %s", what, err.c_str());
+  return PADOC_OK;
+}
+
 extern "C" int padoc_tree_attn_varlen_bwd(padoc_tree_desc* desc, const void* q, const void* k, const void* v,
                                           const void* o, const float* lse, const void* d_o, void* dq, void* dk,
                                           void* dv, int32_t dtype, int32_t Hq, int32_t Hkv, int32_t d, float scale,
@@ -499,12 +523,7 @@ extern "C" int padoc_tree_attn_varlen_bwd(padoc_tree_desc* desc, const void* q, 
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255) || ws_bytes < bwd_ws_bytes(desc, Hq))
     return fail(PADOC_ERR_INVALID, "tree_attn_varlen_bwd: ws must be 256-byte aligned and hold %zu bytes",
                 bwd_ws_bytes(desc, Hq));
-  DevPlan* plan = nullptr;
-  int rc = upload_desc(desc, group, &plan);
-  if (rc) return rc;
   BwdArgs a;
-  a.fwd = {plan->qsegs, plan->kvsegs, plan->items, plan->n_items, group, plan->tile_tokens};
-  a.bwd = {plan->bitems, plan->bentries, static_cast<int32_t>(desc->bitems.size())};
   a.q = q;
   a.k = k;
   a.v = v;
@@ -514,23 +533,91 @@ extern "C" int padoc_tree_attn_varlen_bwd(padoc_tree_desc* desc, const void* q, 
   a.dq = dq;
   a.dk = dk;
   a.dv = dv;
-  a.delta = static_cast<float*>(ws);
-  a.work = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + bwd_delta_bytes(desc, Hq));
-  a.T = desc->T;
   a.Hq = Hq;
   a.Hkv = Hkv;
   a.d = d;
-  a.scale = scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(d));
-  std::string err;
-  // bf16 at d = 128 runs on the tensor cores; PADOC_BWD_CORE=1 selects the
-  // CUDA-core kernels instead (a second implementation to compare against)
-  static const bool force_core = std::getenv("PADOC_BWD_CORE") && std::atoi(std::getenv("PADOC_BWD_CORE")) != 0;
-  if (dtype == PADOC_BF16 && d == kHeadDim && !force_core)
-    rc = launch_bwd_tc(a, reinterpret_cast<cudaStream_t>(stream), &err);
-  else
-    rc = launch_bwd_core(a, dtype, reinterpret_cast<cudaStream_t>(stream), &err);
-  if (rc) return fail(rc, "tree_attn_varlen_bwd: %s", err.c_str());
+  return run_bwd(desc, a, dtype, scale, ws, "tree_attn_varlen_bwd", reinterpret_cast<cudaStream_t>(stream));
+}
+
+// The backward from checkpoints.  The workspace: that of the backward, then q, k and v
+// in bf16; O is only read for its row sums, which come straight from its codes.
+static size_t kept_rows_bytes(const padoc_tree_desc* desc, int32_t H, int32_t d) {
+  return (static_cast<size_t>(desc->T) * H * d * 2 + 255) / 256 * 256;
+}
+static size_t bwd_kept_ws_bytes(const padoc_tree_desc* desc, int32_t Hq, int32_t Hkv, int32_t d) {
+  return bwd_ws_bytes(desc, Hq) + kept_rows_bytes(desc, Hq, d) + 2 * kept_rows_bytes(desc, Hkv, d);
+}
+
+extern "C" int padoc_tree_attn_varlen_bwd_kept_ws_size(const padoc_tree_desc* desc, int32_t Hq, int32_t Hkv, int32_t d,
+                                                       size_t* bytes) {
+  if (!desc || !bytes) return fail(PADOC_ERR_INVALID, "tree_attn_varlen_bwd_kept_ws_size: null argument");
+  if (Hq <= 0 || Hkv <= 0 || d <= 0)
+    return fail(PADOC_ERR_INVALID, "tree_attn_varlen_bwd_kept_ws_size: Hq, Hkv and d must be positive");
+  *bytes = bwd_kept_ws_bytes(desc, Hq, Hkv, d);
   return PADOC_OK;
+}
+
+extern "C" int padoc_tree_attn_varlen_bwd_kept(padoc_tree_desc* desc, const void* q_kept, const void* k_kept,
+                                               const void* v_kept, const void* o_kept, const float* lse,
+                                               const void* d_o, void* dq, void* dk, void* dv, int32_t Hq, int32_t Hkv,
+                                               int32_t d, float scale, void* ws, size_t ws_bytes,
+                                               padoc_stream_t stream) {
+  const char* what = "tree_attn_varlen_bwd_kept";
+  if (!desc) return fail(PADOC_ERR_INVALID, "%s: null descriptor", what);
+  if (Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0)
+    return fail(PADOC_ERR_INVALID, "%s: Hq=%d must be a positive multiple of Hkv=%d", what, Hq, Hkv);
+  if (!valid_group(Hq / Hkv)) return fail(PADOC_ERR_UNSUPPORTED, "%s: Hq/Hkv=%d not in {1,2,4,8,16}", what, Hq / Hkv);
+  if (d != 64 && d != 128) return fail(PADOC_ERR_UNSUPPORTED, "%s: d must be 64 or 128", what);
+  if (desc->T == 0) return PADOC_OK;
+  for (const void* p : {q_kept, k_kept, v_kept, o_kept, static_cast<const void*>(lse), d_o,
+                        static_cast<const void*>(dq), static_cast<const void*>(dk), static_cast<const void*>(dv)})
+    if (!p || !aligned16(p)) return fail(PADOC_ERR_INVALID, "%s: tensors must be 16-byte aligned device pointers", what);
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255) || ws_bytes < bwd_kept_ws_bytes(desc, Hq, Hkv, d))
+    return fail(PADOC_ERR_INVALID, "%s: ws must be 256-byte aligned and hold %zu bytes", what,
+                bwd_kept_ws_bytes(desc, Hq, Hkv, d));
+  if (desc->T * Hq * d / 16 > UINT32_MAX) return fail(PADOC_ERR_UNSUPPORTED, "%s: too many values", what);
+  uint8_t* at = static_cast<uint8_t*>(ws) + bwd_ws_bytes(desc, Hq);
+  void* rows[4] = {at, at + kept_rows_bytes(desc, Hq, d),
+                   at + kept_rows_bytes(desc, Hq, d) + kept_rows_bytes(desc, Hkv, d), const_cast<void*>(d_o)};
+  const void* kept[4] = {q_kept, k_kept, v_kept, o_kept};
+  ActArgs r{};
+  r.n = 4;
+  for (int i = 0; i < 4; ++i) {
+    const int32_t H = i == 0 || i == 3 ? Hq : Hkv;
+    r.t[i].rows = rows[i];
+    r.t[i].stride = static_cast<int64_t>(H) * d;
+    r.t[i].kept = static_cast<uint8_t*>(const_cast<void*>(kept[i]));
+    r.t[i].pieces = desc->T * H * d / 16;
+    r.t[i].per_row = static_cast<uint32_t>(H) * d / 16;
+    r.t[i].dense = 1;
+  }
+  r.sums = 3;
+  r.delta = static_cast<float*>(ws);
+  r.T = desc->T;
+  r.heads = Hq;
+  r.head_pieces = d / 16;
+  std::string err;
+  // the descriptor's device copy first: its upload may fail, and nothing has run by then
+  DevPlan* plan = nullptr;
+  int rc = upload_desc(desc, Hq / Hkv, &plan);
+  if (rc) return rc;
+  rc = launch_act(r, false, reinterpret_cast<cudaStream_t>(stream), &err);
+  if (rc) return fail(rc, "%s: %s", what, err.c_str());
+  BwdArgs a;
+  a.q = rows[0];
+  a.k = rows[1];
+  a.v = rows[2];
+  a.o = nullptr;
+  a.lse = lse;
+  a.dout = d_o;
+  a.dq = dq;
+  a.dk = dk;
+  a.dv = dv;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.d = d;
+  a.have_delta = true;
+  return run_bwd(desc, a, PADOC_BF16, scale, ws, what, reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" int padoc_tree_desc_bwd_plan(const padoc_tree_desc* desc, int32_t* items, int32_t* entries,
@@ -2180,13 +2267,14 @@ extern "C" int padoc_depths(const int32_t* layout_len, const int32_t* content_le
 }
 
 extern "C" int padoc_device_status(padoc_stream_t stream) {
-  unsigned w = 0, wb = 0, wo = 0, wi = 0;
+  unsigned w = 0, wb = 0, wo = 0, wi = 0, wl = 0;
   int rc = read_and_clear_tc_error(reinterpret_cast<cudaStream_t>(stream), &w);
   if (!rc) rc = read_and_clear_bwd_error(reinterpret_cast<cudaStream_t>(stream), &wb);
   if (!rc) rc = read_and_clear_own_error(reinterpret_cast<cudaStream_t>(stream), &wo);
   if (!rc) rc = read_and_clear_i4_error(reinterpret_cast<cudaStream_t>(stream), &wi);
+  if (!rc) rc = read_and_clear_lm_error(reinterpret_cast<cudaStream_t>(stream), &wl);
   if (rc) return fail(rc, "device_status: could not read the device error word");
-  w |= wb | wo | wi;
+  w |= wb | wo | wi | wl;
   if (w) return fail(PADOC_ERR_DEVICE_TIMEOUT, "a kernel gave up a bounded wait (site mask 0x%x)", w);
   return PADOC_OK;
 }

@@ -1,0 +1,881 @@
+// Cross entropy of a large vocabulary and its gradient, without the logits in memory
+// (sm_103a: tcgen05 on pairs of CTAs, TMEM, TMA).
+//
+// Rows h [n, D], weights w [V, D] (bf16), a target t a row:
+//   x = h w^T,  lse = log sum_v exp(x_v),  loss = lse - x_t
+//   G = d_loss (exp(x - lse) - onehot(t)),  dh = G w,  dw = G^T h
+// Products accumulate in f32; maxima, sums, lse and loss are f32.  G is rounded to bf16
+// once, since the products that follow take bf16 operands: with the rounding of the
+// gradients themselves that is 2^-8 relative twice.  dh is summed over pieces in f32.
+//
+// Rows without a target take no part: the others are gathered first (rows_kernel,
+// gather_kernel), and the number of them stays on the device, where every kernel here
+// reads it.  A page's prefix has no targets, so that is most of the work saved, and
+// whatever padded rows hold cannot reach a gradient.
+//
+// lm_kernel: persistent pairs of CTAs (two SMs share an MMA of 256 x 256 x 16: each holds
+// half of A's rows, half of B's, and its half of the accumulator's rows).  A 128 x 256
+// tile of one CTA would read 96 bytes a cycle of operands from L2, more than an SM
+// gets; a pair's tile takes 64.  Units are drawn from a counter.  Kinds of unit:
+//   REC  x of 256 rows and R tiles of 256 words.  Forward: running maximum and sum of a
+//        row, written once a unit.  Backward: G in bf16 for a piece of the vocabulary.
+//   DH   dh (256 rows x 256 dims) += G w over a piece, or a part of it when rows are few
+//   DW   dw (256 words x 256 dims) = G^T h over all rows
+// A backward launch runs DH and DW of one piece and REC of the next side by side: long
+// units first, the short ones fill what is left, so no launch ends in a half-empty wave.
+// G lives in two buffers of a piece each.
+//
+// Roles of a CTA (320 threads): warps 0-7 epilogue (TMEM lanes 32 (w % 4), columns
+// 128 (w / 4) of the tile), warp 8 TMA producer (the pair's first CTA also draws the
+// units), warp 9 of the first CTA issues the products.  Shared memory: a ring of six
+// stages of 64 k (A 128 rows, B 128 rows, 16 KB each).  TMEM: two accumulators.
+// Barriers that both CTAs use live in the first: a stage is full when both CTAs' copies
+// are in; an accumulator is free when both have read it.  The commit of a stage's
+// products frees it in both.
+//
+// Every wait is bounded.  A role that gives up raises its CTA's abort flag and the device
+// error word; the others leave their loops, the issuer commits once more and waits for
+// that, copies in flight get a thousand times their latency to land, and the CTAs meet
+// before TMEM is released.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <string>
+
+#include "../../include/padoc.h"
+#include "padoc_internal.h"
+#include "ptx_sm103.cuh"
+
+namespace padoc {
+
+__device__ unsigned int g_lm_err;
+
+namespace {
+
+using namespace ptx;
+
+constexpr int kThreads = 320;
+constexpr int kEpiWarps = 8;
+constexpr int kProducerWarp = 8, kMmaWarp = 9;
+constexpr int kStages = 6;
+constexpr int kOperand = 16384;  // 128 rows of 64 k, or 64 k of 128, bf16
+constexpr int kStage = 2 * kOperand;
+constexpr int kURing = 4;
+constexpr int SM_BAR = kStages * kStage;
+enum {
+  B_FULL = 0,                   // +stage: both CTAs' copies have landed (first CTA)
+  B_EMPTY = B_FULL + kStages,   // +stage: the stage's products have run
+  B_ACC_FULL = B_EMPTY + kStages,   // +accumulator (2)
+  B_ACC_FREE = B_ACC_FULL + 2,      // +accumulator (2), count 16: both CTAs' epilogues (first CTA)
+  B_U_FULL = B_ACC_FREE + 2,        // +slot: the ring's slot holds a unit
+  B_U_FREE = B_U_FULL + kURing,     // +slot, count 18: all readers have it (first CTA)
+  B_DRAIN = B_U_FREE + kURing,
+  N_BARS
+};
+constexpr int SM_UNIT = SM_BAR + N_BARS * 8;     // unit ring
+constexpr int SM_MISC = SM_UNIT + kURing * 4;    // TMEM address, abort flag
+constexpr int kSmemBytes = SM_MISC + 8 + 1024;   // and room to align the ring
+static_assert(kSmemBytes <= 232448, "shared memory budget");
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr int kUReaders = 1 + 2 * kEpiWarps + 1;  // the issuer, both epilogues, the second CTA's producer
+
+// ---------------------------------------------------------------- pairs of CTAs
+__device__ __forceinline__ uint32_t cta_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {  // a shared::cluster address
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort) {
+  if (try_wait_cluster(bar, parity)) return true;
+  const uint64_t t0 = global_timer();
+  while (true) {
+    for (int i = 0; i < 32; ++i)
+      if (try_wait_cluster(bar, parity)) return true;
+    if (*abort) return false;
+    if (global_timer() - t0 > kWaitLimitNs) return false;
+  }
+}
+// A copy into this CTA that counts on a barrier of the pair's first.
+__device__ __forceinline__ void tma_pair_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrives on the barrier at this offset in both CTAs once the products issued so far have run.
+__device__ __forceinline__ void commit_pair(uint32_t bar) {
+  const uint16_t both = 3;
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"(both)
+      : "memory");
+}
+
+// ---------------------------------------------------------------- units
+enum { REC = 0, DH = 1, DW = 2 };
+struct Unit {
+  int kind, m, n, tiles, k0, nkb, part;  // tile row, first tile column and their number; k blocks from k0
+};
+
+struct Counts {
+  int rows, mt, dh, dw, rec_groups, all;
+};
+__device__ __forceinline__ Counts counts(const LmArgs& a) {
+  Counts c;
+  c.rows = *a.n_rows;
+  c.mt = (c.rows + 255) / 256;
+  c.dh = a.dh ? c.mt * a.d_tiles * a.splits : 0;
+  c.dw = a.dw ? ((a.g_cols + 255) / 256) * a.d_tiles : 0;
+  c.rec_groups = (((a.rec_cols + 255) / 256) + a.run - 1) / a.run;
+  c.all = c.dh + c.dw + c.mt * c.rec_groups;
+  return c;
+}
+__device__ __forceinline__ Unit unit_of(const LmArgs& a, const Counts& c, int u) {
+  Unit x;
+  x.tiles = 1;
+  x.k0 = 0;
+  x.part = 0;
+  if (u < c.dh) {  // the dims of a row tile side by side: they share G
+    x.kind = DH;
+    x.n = u % a.d_tiles;
+    u /= a.d_tiles;
+    x.part = u % a.splits;
+    x.m = u / a.splits;
+    const int kb = (a.g_cols + 63) / 64, each = (kb + a.splits - 1) / a.splits;
+    x.k0 = min(x.part * each, kb);
+    x.nkb = min(each, kb - x.k0);
+    return x;
+  }
+  u -= c.dh;
+  if (u < c.dw) {
+    x.kind = DW;
+    x.n = u % a.d_tiles;
+    x.m = u / a.d_tiles;
+    x.nkb = (c.rows + 63) / 64;
+    return x;
+  }
+  u -= c.dw;  // all rows of a few words, then the next words: the weights are read once
+  x.kind = REC;
+  x.m = u % c.mt;
+  const int g = u / c.mt;
+  x.n = g * a.run;
+  x.tiles = min(a.run, (a.rec_cols + 255) / 256 - x.n);
+  x.nkb = a.k_blocks;
+  return x;
+}
+
+__device__ __forceinline__ void give_up(volatile int* abort, unsigned site) {
+  *abort = 1;
+  atomicOr(&g_lm_err, site);
+}
+
+template <bool FWD>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    lm_kernel(const __grid_constant__ LmArgs a, const __grid_constant__ CUtensorMap m_hk,
+              const __grid_constant__ CUtensorMap m_wk, const __grid_constant__ CUtensorMap m_hm,
+              const __grid_constant__ CUtensorMap m_wm, const __grid_constant__ CUtensorMap m_gk,
+              const __grid_constant__ CUtensorMap m_gm) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* sptr = smem_raw + (sbase - smem_u32(smem_raw));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cta_rank();
+  auto bar = [&](int i) { return sbase + SM_BAR + 8u * i; };
+  volatile int32_t* uring = reinterpret_cast<volatile int32_t*>(sptr + SM_UNIT);
+  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(sptr + SM_MISC);
+  volatile int* abort = reinterpret_cast<volatile int*>(sptr + SM_MISC + 4);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < N_BARS; ++i) {
+      const int count = (i >= B_ACC_FREE && i < B_ACC_FREE + 2)       ? 2 * kEpiWarps
+                        : (i >= B_U_FREE && i < B_U_FREE + kURing) ? kUReaders
+                                                                   : 1;
+      mbar_init(bar(i), count);
+    }
+    *abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp)
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sbase + SM_MISC), "r"(512)
+                 : "memory");
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const Counts c = counts(a);
+
+  if (warp == kProducerWarp) {
+    if (lane == 0) {
+      const uint32_t full0 = in_cta(bar(B_FULL), 0);
+      uint32_t k = 0, uk = 0;  // stages and units so far
+      int next = rank == 0 ? atomicAdd(a.counter, 1) : 0;
+      while (true) {
+        int u;
+        const int slot = uk % kURing;
+        if (rank == 0) {
+          u = next < c.all ? next : -1;
+          if (!wait_cluster(bar(B_U_FREE + slot), ((uk / kURing) & 1) ^ 1, abort)) {
+            give_up(abort, 1u);
+            break;
+          }
+          for (uint32_t r = 0; r < 2; ++r) {
+            st_cluster(in_cta(sbase + SM_UNIT + 4 * slot, r), static_cast<uint32_t>(u));
+            arrive_cluster(in_cta(bar(B_U_FULL + slot), r));
+          }
+          if (u >= 0) next = atomicAdd(a.counter, 1);  // needed when this unit's copies are issued
+        } else {
+          if (!wait_cluster(bar(B_U_FULL + slot), (uk / kURing) & 1, abort)) {
+            give_up(abort, 2u);
+            break;
+          }
+          u = uring[slot];
+          arrive_cluster(in_cta(bar(B_U_FREE + slot), 0));
+        }
+        ++uk;
+        if (u < 0) break;
+        const Unit x = unit_of(a, c, u);
+        bool ok = true;
+        for (int t = 0; t < x.tiles && ok; ++t) {
+          for (int j = 0; j < x.nkb; ++j, ++k) {
+            const int s = k % kStages;
+            if (!mbar_wait(bar(B_EMPTY + s), ((k / kStages) & 1) ^ 1, abort)) {
+              give_up(abort, 4u);
+              ok = false;
+              break;
+            }
+            if (rank == 0) mbar_arrive_expect_tx(bar(B_FULL + s), 2 * kStage);
+            const uint32_t sa = sbase + s * kStage, sb = sa + kOperand, full = full0 + 8u * s;
+            const int kk = (x.k0 + j) * 64;
+            if (x.kind == REC) {
+              tma_pair_2d(sa, &m_hk, full, kk, x.m * 256 + 128 * rank);
+              tma_pair_2d(sb, &m_wk, full, kk, a.rec_v0 + (x.n + t) * 256 + 128 * rank);
+            } else if (!FWD && x.kind == DH) {
+              tma_pair_2d(sa, &m_gk, full, kk, x.m * 256 + 128 * rank);
+              tma_pair_2d(sb, &m_wm, full, x.n * 256 + 128 * rank, a.g_v0 + kk);
+              tma_pair_2d(sb + kOperand / 2, &m_wm, full, x.n * 256 + 128 * rank + 64, a.g_v0 + kk);
+            } else if (!FWD) {
+              tma_pair_2d(sa, &m_gm, full, x.m * 256 + 128 * rank, kk);
+              tma_pair_2d(sa + kOperand / 2, &m_gm, full, x.m * 256 + 128 * rank + 64, kk);
+              tma_pair_2d(sb, &m_hm, full, x.n * 256 + 128 * rank, kk);
+              tma_pair_2d(sb + kOperand / 2, &m_hm, full, x.n * 256 + 128 * rank + 64, kk);
+            }
+          }
+        }
+        if (!ok) break;
+      }
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    if (lane == 0 && rank == 0) {
+      uint32_t k = 0, uk = 0, tile = 0;
+      bool ok = true;
+      while (ok) {
+        const int slot = uk % kURing;
+        if (!wait_cluster(bar(B_U_FULL + slot), (uk / kURing) & 1, abort)) {
+          give_up(abort, 8u);
+          break;
+        }
+        const int u = uring[slot];
+        arrive_cluster(in_cta(bar(B_U_FREE + slot), 0));
+        ++uk;
+        if (u < 0) break;
+        const Unit x = unit_of(a, c, u);
+        const bool a_mn = x.kind == DW, b_mn = x.kind != REC;
+        const uint32_t idesc = idesc_bf16_f32(256, 256, a_mn, b_mn);
+        // K-major steps 16 k by 32 bytes of a row; MN-major by 16 rows of 128 bytes, with
+        // the operand's second 64 columns 8 KB further on
+        const uint64_t da = sdesc_sw128(sbase, a_mn ? kOperand / 2 : 16, 1024);
+        const uint64_t db = sdesc_sw128(sbase + kOperand, b_mn ? kOperand / 2 : 16, 1024);
+        const uint32_t step_a = (a_mn ? 2048 : 32) >> 4, step_b = (b_mn ? 2048 : 32) >> 4;
+        for (int t = 0; t < x.tiles && ok; ++t, ++tile) {
+          const int acc = tile & 1;
+          if (!wait_cluster(bar(B_ACC_FREE + acc), ((tile >> 1) & 1) ^ 1, abort)) {
+            give_up(abort, 16u);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t d = tmem + 256 * acc;
+          for (int j = 0; j < x.nkb; ++j, ++k) {
+            const int s = k % kStages;
+            if (!wait_cluster(bar(B_FULL + s), (k / kStages) & 1, abort)) {
+              give_up(abort, 32u);
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t off = static_cast<uint64_t>((s * kStage) >> 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              mma_pair(d, da + off + i * step_a, db + off + i * step_b, idesc, (j | i) != 0);
+            commit_pair(bar(B_EMPTY + s));
+          }
+          if (ok) commit_pair(bar(B_ACC_FULL + acc));
+        }
+      }
+      if (!ok || *abort) {  // nothing may still run when TMEM is released
+        commit_pair(bar(B_DRAIN));
+        const uint64_t t0 = global_timer();
+        while (!mbar_try_wait(bar(B_DRAIN), 0) && global_timer() - t0 < kWaitLimitNs) {
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int quarter = warp & 3, half = warp >> 2;
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + 128 * half;
+    const int r_in = 128 * rank + 32 * quarter + lane;  // the thread's row of the tile
+    uint32_t uk = 0, tile = 0;
+    bool ok = true;
+    while (ok) {
+      const int slot = uk % kURing;
+      if (!__all_sync(0xffffffffu, wait_cluster(bar(B_U_FULL + slot), (uk / kURing) & 1, abort))) {
+        give_up(abort, 64u);
+        break;
+      }
+      const int u = uring[slot];
+      __syncwarp();
+      if (lane == 0) arrive_cluster(in_cta(bar(B_U_FREE + slot), 0));
+      ++uk;
+      if (u < 0) break;
+      const Unit x = unit_of(a, c, u);
+      const int row = x.m * 256 + r_in;
+      int target = -1;
+      float off = 0.f, d_loss = 0.f;
+      int64_t orig = 0;
+      if (x.kind != DW && row < c.rows) {
+        orig = a.rows[row];
+        if (x.kind == REC) {
+          target = a.targets[orig];
+          if (!FWD) {
+            off = a.lse[orig];
+            d_loss = a.d_loss[orig];
+          }
+        }
+      }
+      float top = -INFINITY, sum = 0.f;  // forward: the row's running maximum and sum
+      for (int t = 0; t < x.tiles; ++t, ++tile) {
+        const int acc = tile & 1;
+        if (!__all_sync(0xffffffffu, mbar_wait(bar(B_ACC_FULL + acc), (tile >> 1) & 1, abort))) {
+          give_up(abort, 128u);
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const int col0 = (x.n + t) * 256 + 128 * half;  // of the piece, or of dims
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          uint32_t v[32];
+          tmem_ld32(t_lane + 256 * acc + 32 * q, v);
+          tmem_wait_ld();
+          if (q == 3) {  // all of it is in registers
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_cluster(in_cta(bar(B_ACC_FREE + acc), 0));
+          }
+          const int col = col0 + 32 * q;
+          if (x.kind == REC) {
+            const int word = a.rec_v0 + col;
+            const int hit = target - word;
+            if (FWD) {
+              if (word + 32 > a.V) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (word + i >= a.V) v[i] = 0xff800000u;
+              }
+              float m = top;
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) m = max3f(m, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+              // all -inf so far: any finite reference keeps the exponentials at zero
+              const float ref = m == -INFINITY ? 0.f : m;
+              sum *= fast_exp2((top - ref) * kLog2e);
+              float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {  // the difference first: it is exact where it matters
+                s0 += fast_exp2((__uint_as_float(v[i]) - ref) * kLog2e);
+                s1 += fast_exp2((__uint_as_float(v[i + 1]) - ref) * kLog2e);
+              }
+              sum += s0 + s1;
+              top = m;
+              if (hit >= 0 && hit < 32) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (hit == i) a.picked[row] = __uint_as_float(v[i]);
+              }
+            } else {
+              float p[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) p[i] = fast_exp2((__uint_as_float(v[i]) - off) * kLog2e);
+              if (hit >= 0 && hit < 32) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (hit == i) p[i] -= 1.f;
+              }
+              uint32_t g[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) g[i] = pack_bf16x2(p[2 * i] * d_loss, p[2 * i + 1] * d_loss);
+              if (row >= c.rows || word + 32 > a.V) {  // rows and words that do not exist count nothing
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  if (row >= c.rows || word + 2 * i >= a.V) g[i] = 0u;
+                  if (word + 2 * i + 1 >= a.V) g[i] &= 0xffffu;
+                }
+              }
+              __nv_bfloat16* out = a.g_out + static_cast<int64_t>(row) * a.g_ld + col;
+              st_global_v8(out, g);
+              st_global_v8(out + 16, g + 8);
+            }
+          } else if (!FWD && x.kind == DH) {
+            if (x.nkb == 0) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = 0u;
+            }
+            float* sums = a.acc + (static_cast<int64_t>(x.part) * a.acc_rows + row) * a.acc_ld + col;
+            if (a.add && row < c.rows) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float4 o = reinterpret_cast<const float4*>(sums)[i];
+                v[4 * i] = __float_as_uint(__uint_as_float(v[4 * i]) + o.x);
+                v[4 * i + 1] = __float_as_uint(__uint_as_float(v[4 * i + 1]) + o.y);
+                v[4 * i + 2] = __float_as_uint(__uint_as_float(v[4 * i + 2]) + o.z);
+                v[4 * i + 3] = __float_as_uint(__uint_as_float(v[4 * i + 3]) + o.w);
+              }
+            }
+            if (row < c.rows) {
+              if (a.finish) {
+                __nv_bfloat16* out = a.dh + orig * a.D + col;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  if (col + 8 * i < a.D)
+                    reinterpret_cast<uint4*>(out)[i] = make_uint4(
+                        pack_bf16x2(__uint_as_float(v[8 * i]), __uint_as_float(v[8 * i + 1])),
+                        pack_bf16x2(__uint_as_float(v[8 * i + 2]), __uint_as_float(v[8 * i + 3])),
+                        pack_bf16x2(__uint_as_float(v[8 * i + 4]), __uint_as_float(v[8 * i + 5])),
+                        pack_bf16x2(__uint_as_float(v[8 * i + 6]), __uint_as_float(v[8 * i + 7])));
+              } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) st_global_v8(sums + 8 * i, v + 8 * i);
+              }
+            }
+          } else if (!FWD) {
+            const int in_piece = x.m * 256 + r_in;
+            const int64_t word = a.g_v0 + in_piece;
+            if (in_piece < a.g_cols && word < a.V) {
+              if (x.nkb == 0) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = 0u;
+              }
+              __nv_bfloat16* out = a.dw + word * a.D + col;
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (col + 8 * i < a.D)
+                  reinterpret_cast<uint4*>(out)[i] = make_uint4(
+                      pack_bf16x2(__uint_as_float(v[8 * i]), __uint_as_float(v[8 * i + 1])),
+                      pack_bf16x2(__uint_as_float(v[8 * i + 2]), __uint_as_float(v[8 * i + 3])),
+                      pack_bf16x2(__uint_as_float(v[8 * i + 4]), __uint_as_float(v[8 * i + 5])),
+                      pack_bf16x2(__uint_as_float(v[8 * i + 6]), __uint_as_float(v[8 * i + 7])));
+            }
+          }
+        }
+      }
+      if (FWD && ok && row < c.rows)
+        a.part[static_cast<int64_t>(2 * (x.n / a.run) + half) * a.part_ld + row] = make_float2(top, sum);
+    }
+    __syncwarp();
+  }
+
+  if (*abort) {  // copies in flight: they take microseconds
+    const uint64_t t0 = global_timer();
+    while (global_timer() - t0 < 5000000ull) {
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  }
+  cluster_sync();
+}
+
+// ---------------------------------------------------------------- rows with a target
+constexpr int kRowsThreads = 1024;
+// One CTA: the indices of the rows with a target, in order, and their number; zeros the
+// counters.  A target of V or more is no word: its row's loss is NaN and it takes no part.
+__global__ void __launch_bounds__(kRowsThreads) lm_rows_kernel(const int32_t* __restrict__ targets, int32_t n, int32_t V,
+                                                               int32_t* __restrict__ rows, int32_t* __restrict__ head,
+                                                               int32_t heads, float* loss, float* lse) {
+  __shared__ int32_t warp_sum[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int i = tid + 1; i < heads; i += kRowsThreads) head[i] = 0;
+  const int64_t each = (static_cast<int64_t>(n) + kRowsThreads - 1) / kRowsThreads;
+  const int64_t lo = min(static_cast<int64_t>(n), tid * each), hi = min(static_cast<int64_t>(n), lo + each);
+  int count = 0;
+#pragma unroll 8
+  for (int64_t i = lo; i < hi; ++i) {
+    const int t = targets[i];
+    count += t >= 0 && t < V;
+  }
+  int scan = count;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int y = __shfl_up_sync(0xffffffffu, scan, o);
+    if (lane >= o) scan += y;
+  }
+  if (lane == 31) warp_sum[warp] = scan;
+  __syncthreads();
+  if (warp == 0) {
+    int x = warp_sum[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    warp_sum[lane] = x;
+  }
+  __syncthreads();
+  int at = scan - count + (warp ? warp_sum[warp - 1] : 0);
+  if (tid == 0) head[0] = warp_sum[31];
+#pragma unroll 4
+  for (int64_t i = lo; i < hi; ++i) {
+    const int t = targets[i];
+    if (t >= 0 && t < V) {
+      rows[at++] = static_cast<int32_t>(i);
+    } else if (loss) {
+      loss[i] = t < 0 ? 0.f : __uint_as_float(0x7fffffffu);
+      lse[i] = 0.f;
+    }
+  }
+}
+
+// Rows with a target side by side, zeros up to the next multiple of 256; in the backward
+// pass, zeros for the others' gradients.  A warp a row.
+__global__ void __launch_bounds__(256) lm_gather_kernel(const uint4* __restrict__ h, int64_t stride, uint4* __restrict__ out,
+                                                        const int32_t* __restrict__ rows, const int32_t* __restrict__ head,
+                                                        const int32_t* __restrict__ targets, int32_t n, int32_t V,
+                                                        int32_t vecs, uint4* dh) {
+  const int lane = threadIdx.x & 31;
+  const int i = static_cast<int>(blockIdx.x * 8 + (threadIdx.x >> 5));
+  const int count = *head, padded = (count + 255) & ~255;
+  if (i < padded) {
+    const uint4* src = i < count ? h + rows[i] * stride : nullptr;
+    uint4* dst = out + static_cast<int64_t>(i) * vecs;
+#pragma unroll 4
+    for (int j = lane; j < vecs; j += 32) dst[j] = src ? src[j] : make_uint4(0, 0, 0, 0);
+  }
+  if (dh && i < n) {
+    const int t = targets[i];
+    if (t < 0 || t >= V) {
+      uint4* dst = dh + static_cast<int64_t>(i) * vecs;
+      for (int j = lane; j < vecs; j += 32) dst[j] = make_uint4(0, 0, 0, 0);
+    }
+  }
+}
+
+// lse and loss of 32 rows from their partial maxima and sums.
+__global__ void __launch_bounds__(1024) lm_join_kernel(const float2* __restrict__ part, int64_t ld, int32_t parts,
+                                                       const float* __restrict__ picked, const int32_t* __restrict__ rows,
+                                                       const int32_t* __restrict__ head, float* __restrict__ loss,
+                                                       float* __restrict__ lse) {
+  __shared__ float2 s[32][33];
+  const int r = threadIdx.x & 31, p0 = threadIdx.x >> 5, row = blockIdx.x * 32 + r, count = *head;
+  if (static_cast<int>(blockIdx.x) * 32 >= count) return;
+  float m = -INFINITY, l = 0.f;
+  if (row < count) {
+#pragma unroll 8
+    for (int p = p0; p < parts; p += 32) {
+      const float2 x = part[p * ld + row];
+      const float t = fmaxf(m, x.x);
+      const float ref = t == -INFINITY ? 0.f : t;
+      // a NaN sum stays one: fmaxf drops a NaN maximum
+      l = l * fast_exp2((m - ref) * kLog2e) + x.y * fast_exp2((x.x - ref) * kLog2e);
+      m = t;
+    }
+  }
+  s[p0][r] = make_float2(m, l);
+  __syncthreads();
+  // warp p0 joins row p0's 32
+  const float2 x = s[r][p0];
+  float t = x.x;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
+  const float ref = t == -INFINITY ? 0.f : t;
+  float sum = x.y * fast_exp2((x.x - ref) * kLog2e);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const int mine = blockIdx.x * 32 + p0;
+  if (r == 0 && mine < count) {
+    const float v = t + logf(sum);
+    const int32_t at = rows[mine];
+    lse[at] = v;
+    loss[at] = v - picked[mine];
+  }
+}
+
+// dh of few rows: the parts of the vocabulary added up, in their order.
+__global__ void __launch_bounds__(256) lm_finish_kernel(const float* __restrict__ acc, int64_t acc_rows, int32_t acc_ld,
+                                                        int32_t splits, const int32_t* __restrict__ rows,
+                                                        const int32_t* __restrict__ head, int32_t D,
+                                                        __nv_bfloat16* __restrict__ dh) {
+  const int row = blockIdx.x;
+  if (row >= *head) return;
+  const int64_t at = rows[row];
+  for (int col = 4 * threadIdx.x; col < D; col += 1024) {
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p = 0; p < splits; ++p) {
+      const float4 x = *reinterpret_cast<const float4*>(acc + (p * acc_rows + row) * acc_ld + col);
+      s.x += x.x;
+      s.y += x.y;
+      s.z += x.z;
+      s.w += x.w;
+    }
+    *reinterpret_cast<uint2*>(dh + at * D + col) = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+  }
+}
+
+int make_map(EncodeTiledFn enc, CUtensorMap* m, const void* ptr, int64_t cols, int64_t rows, int64_t ld, int box_rows,
+             std::string* err) {
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)}, one[2] = {1, 1};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, one,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r == CUDA_SUCCESS) return PADOC_OK;
+  *err = "cuTensorMapEncodeTiled failed (" + std::to_string(static_cast<int>(r)) + ")";
+  return PADOC_ERR_CUDA;
+}
+
+int cuda_check(const char* what, std::string* err) {
+  const cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) return PADOC_OK;
+  *err = std::string(what) + ": " + cudaGetErrorString(e);
+  return PADOC_ERR_CUDA;
+}
+
+template <bool FWD>
+int launch_gemm(const LmArgs& a, const CUtensorMap* m, cudaStream_t s, std::string* err) {
+  // an attribute of the current device's copy of the kernel
+  const cudaError_t e = cudaFuncSetAttribute(lm_kernel<FWD>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (e != cudaSuccess) {
+    *err = std::string("cudaFuncSetAttribute: ") + cudaGetErrorString(e);
+    return PADOC_ERR_CUDA;
+  }
+  lm_kernel<FWD><<<num_sms() / 2 * 2, kThreads, kSmemBytes, s>>>(a, m[0], m[1], m[2], m[3], m[4], m[5]);
+  return cuda_check("lm_kernel launch", err);
+}
+
+int rows_and_gather(const LmCall& l, const LmPlan& p, uint8_t* ws, bool backward, cudaStream_t s, std::string* err) {
+  int32_t* head = reinterpret_cast<int32_t*>(ws + p.head);
+  int32_t* rows = reinterpret_cast<int32_t*>(ws + p.rows);
+  lm_rows_kernel<<<1, kRowsThreads, 0, s>>>(l.targets, l.n, l.V, rows, head, p.heads, backward ? nullptr : l.loss,
+                                            backward ? nullptr : l.lse);
+  lm_gather_kernel<<<static_cast<unsigned>(p.n_pad / 8), 256, 0, s>>>(
+      static_cast<const uint4*>(l.h), l.h_stride / 8, reinterpret_cast<uint4*>(ws + p.hc), rows, head, l.targets, l.n, l.V,
+      l.D / 8, backward ? static_cast<uint4*>(l.dh) : nullptr);
+  return cuda_check("row kernels", err);
+}
+
+}  // namespace
+
+// Sizes of a call, from its shape alone.  The number of rows with a target is not known
+// here, so everything is laid out for all of them.
+LmPlan lm_plan(int32_t n, int32_t D, int32_t V, bool backward) {
+  constexpr int pairs = 76;  // of a GB300
+  LmPlan p{};
+  const int64_t word_tiles = (static_cast<int64_t>(V) + 255) / 256, row_tiles = (static_cast<int64_t>(n) + 255) / 256;
+  const int64_t d_tiles = (D + 255) / 256;
+  p.n_pad = row_tiles * 256;
+  // Tiles of words one after another in a REC unit: as many as leave each pair eight units
+  // to draw, so that drawing and (forward) partial results cost little, and the units end
+  // together.
+  p.run = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(16, word_tiles * row_tiles / (8 * pairs))));
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t r = at;
+    at += (bytes + 255) / 256 * 256;
+    return r;
+  };
+  if (!backward) {
+    p.heads = 2;
+    p.head = take(p.heads * sizeof(int32_t));
+    p.rows = take(n * sizeof(int32_t));
+    p.hc = take(static_cast<size_t>(p.n_pad) * D * 2);
+    p.parts = static_cast<int32_t>(2 * ((word_tiles + p.run - 1) / p.run));
+    p.part = take(static_cast<size_t>(p.parts) * p.n_pad * sizeof(float2));
+    p.picked = take(static_cast<size_t>(p.n_pad) * sizeof(float));
+    p.bytes = at;
+    return p;
+  }
+  // A piece of the vocabulary is what 640 MB of G hold: long enough that a piece's
+  // products dwarf the f32 sums of dh which go through memory once a piece, and small
+  // beside the weights' own gradient.
+  const int64_t cap = std::max<int64_t>(1, (640ll << 20) / (2 * 256 * p.n_pad));
+  p.pieces = static_cast<int32_t>((word_tiles + cap - 1) / cap);
+  p.piece_tiles = static_cast<int32_t>((word_tiles + p.pieces - 1) / p.pieces);
+  p.pieces = static_cast<int32_t>((word_tiles + p.piece_tiles - 1) / p.piece_tiles);
+  // Few rows leave few dh tiles with a long sum each: the sum is cut until every pair has
+  // a part of one.
+  p.splits = static_cast<int32_t>(
+      std::max<int64_t>(1, std::min<int64_t>(pairs / (row_tiles * d_tiles), p.piece_tiles)));
+  p.heads = 2 + p.pieces;
+  p.head = take(p.heads * sizeof(int32_t));
+  p.rows = take(n * sizeof(int32_t));
+  p.hc = take(static_cast<size_t>(p.n_pad) * D * 2);
+  p.acc_ld = static_cast<int32_t>(d_tiles * 256);
+  p.acc = take(p.pieces > 1 || p.splits > 1 ? static_cast<size_t>(p.splits) * p.n_pad * p.acc_ld * sizeof(float) : 0);
+  p.g_bytes = static_cast<size_t>(p.n_pad) * p.piece_tiles * 512;
+  p.g = take(p.g_bytes * (p.pieces > 1 ? 2 : 1));
+  p.bytes = at;
+  return p;
+}
+
+int launch_lm_loss(const LmCall& l, void* ws_, cudaStream_t s, std::string* err) {
+  const LmPlan p = lm_plan(l.n, l.D, l.V, false);
+  uint8_t* ws = static_cast<uint8_t*>(ws_);
+  EncodeTiledFn enc = get_encode_fn(err);
+  if (!enc) return PADOC_ERR_CUDA;
+  CUtensorMap m[6];
+  int rc = make_map(enc, &m[0], ws + p.hc, l.D, p.n_pad, l.D, 128, err);
+  if (!rc) rc = make_map(enc, &m[1], l.w, l.D, l.V, l.w_stride, 128, err);
+  if (rc) return rc;
+  for (int i = 2; i < 6; ++i) m[i] = m[0];
+  rc = rows_and_gather(l, p, ws, false, s, err);
+  if (rc) return rc;
+  int32_t* head = reinterpret_cast<int32_t*>(ws + p.head);
+  LmArgs a{};
+  a.n_rows = head;
+  a.counter = head + 1;
+  a.rows = reinterpret_cast<int32_t*>(ws + p.rows);
+  a.targets = l.targets;
+  a.D = l.D;
+  a.V = l.V;
+  a.k_blocks = (l.D + 63) / 64;
+  a.d_tiles = (l.D + 255) / 256;
+  a.run = p.run;
+  a.splits = 1;
+  a.rec_cols = l.V;
+  a.part = reinterpret_cast<float2*>(ws + p.part);
+  a.part_ld = p.n_pad;
+  a.picked = reinterpret_cast<float*>(ws + p.picked);
+  rc = launch_gemm<true>(a, m, s, err);
+  if (rc) return rc;
+  lm_join_kernel<<<static_cast<unsigned>((l.n + 31) / 32), 1024, 0, s>>>(a.part, a.part_ld, p.parts, a.picked, a.rows, head,
+                                                                        l.loss, l.lse);
+  return cuda_check("lm_join_kernel launch", err);
+}
+
+int launch_lm_loss_bwd(const LmCall& l, void* ws_, cudaStream_t s, std::string* err) {
+  const LmPlan p = lm_plan(l.n, l.D, l.V, true);
+  uint8_t* ws = static_cast<uint8_t*>(ws_);
+  EncodeTiledFn enc = get_encode_fn(err);
+  if (!enc) return PADOC_ERR_CUDA;
+  const int32_t g_ld = p.piece_tiles * 256;
+  CUtensorMap m[6], gk[2], gm[2];
+  int rc = make_map(enc, &m[0], ws + p.hc, l.D, p.n_pad, l.D, 128, err);
+  if (!rc) rc = make_map(enc, &m[1], l.w, l.D, l.V, l.w_stride, 128, err);
+  if (!rc) rc = make_map(enc, &m[2], ws + p.hc, l.D, p.n_pad, l.D, 64, err);
+  if (!rc) rc = make_map(enc, &m[3], l.w, l.D, l.V, l.w_stride, 64, err);
+  for (int i = 0; i < (p.pieces > 1 ? 2 : 1) && !rc; ++i) {
+    rc = make_map(enc, &gk[i], ws + p.g + i * p.g_bytes, g_ld, p.n_pad, g_ld, 128, err);
+    if (!rc) rc = make_map(enc, &gm[i], ws + p.g + i * p.g_bytes, g_ld, p.n_pad, g_ld, 64, err);
+  }
+  if (rc) return rc;
+  rc = rows_and_gather(l, p, ws, true, s, err);
+  if (rc) return rc;
+  int32_t* head = reinterpret_cast<int32_t*>(ws + p.head);
+  LmArgs a{};
+  a.n_rows = head;
+  a.rows = reinterpret_cast<int32_t*>(ws + p.rows);
+  a.targets = l.targets;
+  a.D = l.D;
+  a.V = l.V;
+  a.k_blocks = (l.D + 63) / 64;
+  a.d_tiles = (l.D + 255) / 256;
+  a.run = p.run;
+  a.splits = p.splits;
+  a.lse = l.lse;
+  a.d_loss = l.d_loss;
+  a.acc = reinterpret_cast<float*>(ws + p.acc);
+  a.acc_rows = p.n_pad;
+  a.acc_ld = p.acc_ld;
+  a.g_ld = g_ld;
+  // launch i: the gradients of piece i - 1 and G of piece i
+  for (int i = 0; i <= p.pieces; ++i) {
+    const int done = i - 1;
+    a.counter = head + 1 + i;
+    a.dh = nullptr;
+    a.dw = nullptr;
+    if (done >= 0) {
+      a.dh = static_cast<__nv_bfloat16*>(l.dh);
+      a.dw = static_cast<__nv_bfloat16*>(l.dw);
+      a.g_v0 = done * g_ld;
+      a.g_cols = static_cast<int32_t>(std::min<int64_t>(g_ld, static_cast<int64_t>(l.V) - a.g_v0));
+      a.add = done > 0;
+      a.finish = i == p.pieces && p.splits == 1;
+    }
+    a.rec_v0 = i * g_ld;
+    a.rec_cols = i < p.pieces ? static_cast<int32_t>(std::min<int64_t>(g_ld, static_cast<int64_t>(l.V) - a.rec_v0)) : 0;
+    a.g_out = reinterpret_cast<__nv_bfloat16*>(ws + p.g + (i & 1) * p.g_bytes);
+    if (i >= p.pieces) a.g_out = nullptr;
+    m[4] = gk[done > 0 ? done & 1 : 0];
+    m[5] = gm[done > 0 ? done & 1 : 0];
+    rc = launch_gemm<false>(a, m, s, err);
+    if (rc) return rc;
+  }
+  if (l.dh && p.splits > 1) {
+    lm_finish_kernel<<<static_cast<unsigned>(l.n), 256, 0, s>>>(a.acc, a.acc_rows, a.acc_ld, p.splits, a.rows, head, l.D,
+                                                               static_cast<__nv_bfloat16*>(l.dh));
+    return cuda_check("lm_finish_kernel launch", err);
+  }
+  return PADOC_OK;
+}
+
+int read_and_clear_lm_error(cudaStream_t s, unsigned* word) {
+  const unsigned zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbolAsync(word, g_lm_err, sizeof(unsigned), 0, cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e == cudaSuccess && *word) e = cudaMemcpyToSymbolAsync(g_lm_err, &zero, sizeof(unsigned), 0, cudaMemcpyHostToDevice, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  return e == cudaSuccess ? PADOC_OK : PADOC_ERR_CUDA;
+}
+
+}  // namespace padoc

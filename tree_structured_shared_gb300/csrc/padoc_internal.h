@@ -88,6 +88,7 @@ struct BwdArgs {
   void* dv;
   float* delta;       // workspace [Hq, T]: rowsum(dO * O)
   int32_t* work;      // workspace: unit counter of the dK/dV pass (zeroed by its launcher)
+  bool have_delta = false;  // the row sums are in delta already
   int64_t T;
   int32_t Hq, Hkv, d;
   float scale;
@@ -229,7 +230,101 @@ struct RowsArgs {
   __nv_bfloat16* v_out;
 };
 
+// ---------------------------------------------------------------- rotation of packed rows
+constexpr int kRopeParts = 4;
+struct RopeArgs {
+  const float* cos_sin;  // [n_pos][cosines, then sines]
+  const int32_t* positions;  // [n], or null: the row's index
+  int64_t n;
+  int32_t n_pos, rot_dim, interleaved, backward;
+  int32_t heads;              // of all parts together
+  int32_t first[kRopeParts];  // first head of each part (heads: no such part)
+  const void* x[kRopeParts];
+  void* out[kRopeParts];
+  int64_t stride[kRopeParts], out_stride[kRopeParts];  // elements between rows
+};
+struct RopeTableArgs {
+  float* cos_sin;
+  int64_t first, n_pos;
+  int32_t rot_dim;
+  float amplitude;
+  uint64_t turns[64];  // of a pair a position, as a fraction of 2^64
+};
+
+// ---------------------------------------------------------------- 8-bit checkpoints
+constexpr int kActTensors = 8;
+struct ActTensor {
+  void* rows;      // bf16
+  int64_t stride;  // elements between rows
+  uint8_t* kept;   // codes, then scales
+  int64_t pieces;  // of 16 values
+  uint32_t per_row;
+  int32_t dense;   // rows follow one another
+};
+struct ActArgs {
+  ActTensor t[kActTensors];
+  int32_t n;
+  int32_t first_block[kActTensors];
+  // the tensor whose row sums with `rows` are wanted instead of its values, or -1
+  int32_t sums;
+  float* delta;  // [heads][T]
+  int64_t T;
+  uint32_t heads, head_pieces;
+};
+
+// ---------------------------------------------------------------- cross entropy
+struct LmCall {
+  const void* h;
+  int64_t h_stride;
+  const void* w;
+  int64_t w_stride;
+  const int32_t* targets;
+  int32_t n, D, V;
+  float* loss;
+  float* lse;
+  const float* d_loss;
+  void* dh;
+  void* dw;
+};
+// Where things lie in a call's workspace (bytes), and how its work is cut.
+struct LmPlan {
+  int64_t n_pad;
+  int32_t run, parts, pieces, piece_tiles, splits, heads, acc_ld;
+  size_t head, rows, hc, part, picked, acc, g, g_bytes, bytes;
+};
+struct LmArgs {
+  const int32_t* n_rows;
+  int32_t* counter;  // of units, zero at launch
+  const int32_t* rows;
+  const int32_t* targets;
+  int32_t D, V;
+  int32_t k_blocks, d_tiles, run, splits;
+  int32_t rec_v0, rec_cols;  // words of the REC units
+  int32_t g_v0, g_cols;      // words of the piece whose gradients are taken
+  int32_t add, finish;       // dh: sums so far in acc; this launch writes it in bf16
+  // forward
+  float2* part;
+  int64_t part_ld;
+  float* picked;
+  // backward
+  const float* lse;
+  const float* d_loss;
+  __nv_bfloat16* g_out;
+  int64_t g_ld;
+  float* acc;
+  int64_t acc_rows, acc_ld;
+  __nv_bfloat16* dh;
+  __nv_bfloat16* dw;
+};
+
 // Launchers (return 0 or a PADOC_ERR_* code, message in *err).
+int launch_rope_apply(const RopeArgs& a, int32_t dtype, int32_t d, cudaStream_t s, std::string* err);
+int launch_rope_table(const RopeTableArgs& a, cudaStream_t s, std::string* err);
+int launch_act(ActArgs a, bool keep, cudaStream_t s, std::string* err);
+LmPlan lm_plan(int32_t n, int32_t D, int32_t V, bool backward);
+int launch_lm_loss(const LmCall& l, void* ws, cudaStream_t s, std::string* err);
+int launch_lm_loss_bwd(const LmCall& l, void* ws, cudaStream_t s, std::string* err);
+int read_and_clear_lm_error(cudaStream_t s, unsigned* word);
 int launch_fwd_bf16(const FwdArgs& a, cudaStream_t s, std::string* err);
 int launch_fwd_f32(const FwdArgs& a, cudaStream_t s, std::string* err);
 int launch_decode_prefix(const DecodeArgs& a, cudaStream_t s, std::string* err);

@@ -19,6 +19,7 @@ LIB_PATH = os.path.join(_PKG, "libpadoc.so")
 OK, ERR_INVALID, ERR_OOM, ERR_CUDA, ERR_UNSUPPORTED, ERR_DEVICE_TIMEOUT = 0, -1, -2, -3, -4, -5
 F32, BF16, I4 = 0, 1, 2
 PACK_CANONICAL, PACK_DOCUMENT = 0, 1
+ROPE_PLAIN, ROPE_LINEAR, ROPE_BASE, ROPE_BANDS, ROPE_RAMP = 0, 1, 2, 3, 4
 
 EXPORTED = [
     "padoc_last_error", "padoc_version", "padoc_tree_desc_build", "padoc_tree_desc_free",
@@ -35,7 +36,9 @@ EXPORTED = [
     "padoc_sched_create", "padoc_sched_destroy", "padoc_sched_submit", "padoc_sched_schedule", "padoc_sched_update",
     "padoc_sched_request", "padoc_sched_output", "padoc_kv_storage_bytes", "padoc_kv_rows_create",
     "padoc_kv_rows_ws_size", "padoc_kv_rows_upload", "padoc_kv_rows_free", "padoc_kv_write", "padoc_kv_gather",
-    "padoc_kv_append_rope",
+    "padoc_kv_append_rope", "padoc_rope_table", "padoc_rope_apply", "padoc_lm_loss_ws_size", "padoc_lm_loss",
+    "padoc_lm_loss_bwd", "padoc_act_bytes", "padoc_act_keep", "padoc_act_restore",
+    "padoc_tree_attn_varlen_bwd_kept_ws_size", "padoc_tree_attn_varlen_bwd_kept",
 ]
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
@@ -78,6 +81,27 @@ class KVStep(C.Structure):
     _fields_ = [("q", C.c_void_p), ("q_stride", C.c_int64), ("Hq", C.c_int32), ("q_rot", C.c_void_p),
                 ("k", C.c_void_p), ("k_stride", C.c_int64), ("v", C.c_void_p), ("v_stride", C.c_int64),
                 ("k_rot", C.c_void_p)]
+
+
+class RopeScaling(C.Structure):
+    _fields_ = [("base", C.c_double), ("rot_dim", C.c_int32), ("kind", C.c_int32), ("factor", C.c_double),
+                ("context", C.c_double), ("turns_lo", C.c_double), ("turns_hi", C.c_double),
+                ("amplitude", C.c_double)]
+
+
+class RopePart(C.Structure):
+    _fields_ = [("x", C.c_void_p), ("stride", C.c_int64), ("out", C.c_void_p), ("out_stride", C.c_int64),
+                ("heads", C.c_int32)]
+
+
+class LmHead(C.Structure):
+    _fields_ = [("h", C.c_void_p), ("h_stride", C.c_int64), ("w", C.c_void_p), ("w_stride", C.c_int64),
+                ("targets", C.c_void_p), ("n", C.c_int32), ("D", C.c_int32), ("V", C.c_int32)]
+
+
+class Act(C.Structure):
+    _fields_ = [("rows", C.c_void_p), ("stride", C.c_int64), ("n", C.c_int64), ("width", C.c_int32),
+                ("kept", C.c_void_p)]
 
 
 _lib = None
@@ -155,6 +179,17 @@ def lib() -> C.CDLL:
             "padoc_kv_gather": (C.c_int, [vp, vp, vp, vp, vp]),
             "padoc_kv_append_rope": (C.c_int, [vp, i32, p32, p32, p32, C.POINTER(RopeSpec), C.POINTER(KVStep), vp,
                                                C.c_size_t, vp]),
+            "padoc_rope_table": (C.c_int, [C.POINTER(RopeScaling), i64, i32, vp, vp]),
+            "padoc_rope_apply": (C.c_int, [C.POINTER(RopeSpec), i32, C.POINTER(RopePart), i32, i32, i64, vp, i32, vp]),
+            "padoc_lm_loss_ws_size": (C.c_int, [i32, i32, i32, i32, C.POINTER(C.c_size_t)]),
+            "padoc_lm_loss": (C.c_int, [C.POINTER(LmHead), vp, vp, vp, C.c_size_t, vp]),
+            "padoc_lm_loss_bwd": (C.c_int, [C.POINTER(LmHead), vp, vp, vp, vp, vp, C.c_size_t, vp]),
+            "padoc_act_bytes": (C.c_int, [i64, i32, C.POINTER(C.c_size_t)]),
+            "padoc_act_keep": (C.c_int, [i32, C.POINTER(Act), vp]),
+            "padoc_act_restore": (C.c_int, [i32, C.POINTER(Act), vp]),
+            "padoc_tree_attn_varlen_bwd_kept_ws_size": (C.c_int, [vp, i32, i32, i32, C.POINTER(C.c_size_t)]),
+            "padoc_tree_attn_varlen_bwd_kept": (C.c_int, [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, f32,
+                                                          vp, C.c_size_t, vp]),
             "padoc_draft_index_create": (C.c_int, [p32, p64, i32, i32, C.POINTER(vp)]),
             "padoc_draft_index_free": (C.c_int, [vp]),
             "padoc_draft_trie": (C.c_int, [vp, p32, i32, i32, i32, p32, p32, p32]),
@@ -290,6 +325,102 @@ def tree_attn_varlen_bwd(desc: TreeDesc, q, k, v, o, lse, d_o, dq, dk, dv, dtype
     _check(lib().padoc_tree_attn_varlen_bwd(desc.handle, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(d_o),
                                             _ptr(dq), _ptr(dk), _ptr(dv), dtype, Hq, Hkv, d, float(scale), _ptr(ws),
                                             int(ws_bytes), _stream(stream)))
+
+
+# ------------------------------------------------------------------ around the attention of a training step
+
+
+def tree_attn_varlen_bwd_kept_ws_size(desc: TreeDesc, Hq: int, Hkv: int, d: int) -> int:
+    n = C.c_size_t()
+    _check(lib().padoc_tree_attn_varlen_bwd_kept_ws_size(desc.handle, Hq, Hkv, d, C.byref(n)))
+    return n.value
+
+
+def tree_attn_varlen_bwd_kept(desc: TreeDesc, q_kept, k_kept, v_kept, o_kept, lse, d_o, dq, dk, dv, Hq: int, Hkv: int,
+                              d: int, ws, ws_bytes: int, scale: float = 0.0, stream=None):
+    """padoc_tree_attn_varlen_bwd_kept: the backward from checkpoints of q, k, v and o."""
+    _check(lib().padoc_tree_attn_varlen_bwd_kept(desc.handle, _ptr(q_kept), _ptr(k_kept), _ptr(v_kept), _ptr(o_kept),
+                                                 _ptr(lse), _ptr(d_o), _ptr(dq), _ptr(dk), _ptr(dv), Hq, Hkv, d,
+                                                 float(scale), _ptr(ws), int(ws_bytes), _stream(stream)))
+
+
+def rope_table(cos_sin, n_pos: int, rot_dim: int, base: float, *, kind: int = ROPE_PLAIN, factor: float = 1.0,
+               context: float = 0.0, turns_lo: float = 1.0, turns_hi: float = 32.0, amplitude: float = 1.0,
+               first: int = 0, stream=None):
+    """padoc_rope_table: device f32 cos_sin [n_pos, rot_dim] out."""
+    sc = RopeScaling(base, rot_dim, kind, factor, context, turns_lo, turns_hi, amplitude)
+    _check(lib().padoc_rope_table(C.byref(sc), int(first), n_pos, _ptr(cos_sin), _stream(stream)))
+
+
+def rope_apply(rope: "Rope", n: int, d: int, q, q_out, Hq: int, k=None, k_out=None, Hkv: int = 0, *, positions=None,
+               dtype: int = BF16, backward: bool = False, q_stride: Optional[int] = None, k_stride: Optional[int] = None,
+               q_out_stride: Optional[int] = None, k_out_stride: Optional[int] = None, stream=None):
+    """padoc_rope_apply on q and, where given, k; strides in elements, dense where None."""
+    row = lambda s, H: H * d if s is None else int(s)  # noqa: E731
+    parts = (RopePart * 2)(RopePart(_ptr(q), row(q_stride, Hq), _ptr(q_out), row(q_out_stride, Hq), Hq),
+                           RopePart(_ptr(k), row(k_stride, Hkv), _ptr(k_out), row(k_out_stride, Hkv), Hkv))
+    _check(lib().padoc_rope_apply(rope.ref, 1 if k is None else 2, parts, dtype, d, int(n), _ptr(positions),
+                                  int(bool(backward)), _stream(stream)))
+
+
+class LmLoss:
+    """Cross entropy of rows h [n, D] against weights w [V, D], device bf16, and
+    int32 targets [n] (negative: none); padoc_lm_loss and its backward."""
+
+    def __init__(self, h, w, targets):
+        self._keep = (h, w, targets)
+        (n, D), V = h.shape, w.shape[0]
+        if w.shape[1] != D or targets.shape[0] != n:
+            raise PadocError(ERR_INVALID, "LmLoss: h [n, D], w [V, D] and targets [n] do not fit together")
+        if h.stride(1) != 1 or w.stride(1) != 1 or (n > 1 and targets.stride(0) != 1):
+            raise PadocError(ERR_INVALID, "LmLoss: a row's values and the targets must follow one another")
+        if h.element_size() != 2 or w.element_size() != 2 or targets.element_size() != 4:
+            raise PadocError(ERR_INVALID, "LmLoss: h and w must be bf16 and the targets int32")
+        self.c = LmHead(_ptr(h), h.stride(0) if n > 1 else D, _ptr(w), w.stride(0) if V > 1 else D, _ptr(targets), n, D, V)
+        self.ref = C.byref(self.c)
+
+    def ws_size(self, backward: bool = False) -> int:
+        b = C.c_size_t()
+        _check(lib().padoc_lm_loss_ws_size(self.c.n, self.c.D, self.c.V, int(bool(backward)), C.byref(b)))
+        return b.value
+
+    def forward(self, loss, lse, ws, ws_bytes: int, stream=None):
+        _check(lib().padoc_lm_loss(self.ref, _ptr(loss), _ptr(lse), _ptr(ws), int(ws_bytes), _stream(stream)))
+
+    def backward(self, lse, d_loss, dh, dw, ws, ws_bytes: int, stream=None):
+        _check(lib().padoc_lm_loss_bwd(self.ref, _ptr(lse), _ptr(d_loss), _ptr(dh), _ptr(dw), _ptr(ws), int(ws_bytes),
+                                       _stream(stream)))
+
+
+def act_bytes(n: int, width: int) -> int:
+    """Bytes of the checkpoint of n rows of `width` values."""
+    b = C.c_size_t()
+    _check(lib().padoc_act_bytes(int(n), int(width), C.byref(b)))
+    return b.value
+
+
+def _acts(rows, kept):
+    if len(rows) != len(kept):
+        raise PadocError(ERR_INVALID, "act: one checkpoint a tensor is needed")
+    a = (Act * max(len(rows), 1))()
+    for i, (x, b) in enumerate(zip(rows, kept)):
+        if x.dim() != 2 or x.element_size() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+            raise PadocError(ERR_INVALID, "act: rows must be bf16 [n, width] whose rows are dense")
+        if b.numel() * b.element_size() < act_bytes(*x.shape):
+            raise PadocError(ERR_INVALID, "act: a checkpoint is smaller than act_bytes(n, width)")
+        a[i] = Act(_ptr(x), x.stride(0) if x.shape[0] > 1 else x.shape[1], x.shape[0], x.shape[1], _ptr(b))
+    return a
+
+
+def act_keep(rows, kept, stream=None):
+    """padoc_act_keep: bf16 tensors [n, width] into their checkpoints (device
+    bytes, act_bytes(n, width) each); one launch for up to eight."""
+    _check(lib().padoc_act_keep(len(rows), _acts(rows, kept), _stream(stream)))
+
+
+def act_restore(kept, rows, stream=None):
+    """padoc_act_restore: checkpoints back into bf16 tensors [n, width]."""
+    _check(lib().padoc_act_restore(len(rows), _acts(rows, kept), _stream(stream)))
 
 
 # ------------------------------------------------------------------ KV pool
