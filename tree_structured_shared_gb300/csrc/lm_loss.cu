@@ -8,8 +8,8 @@
 // once, since the products that follow take bf16 operands: with the rounding of the
 // gradients themselves that is 2^-8 relative twice.  dh is summed over pieces in f32.
 //
-// Rows without a target take no part: the others are gathered first (rows_kernel,
-// gather_kernel), and the number of them stays on the device, where every kernel here
+// Rows without a target take no part: the others are gathered first (lm_rows_kernel), and
+// the number of them stays on the device, where every kernel here
 // reads it.  A page's prefix has no targets, so that is most of the work saved, and
 // whatever padded rows hold cannot reach a gradient.
 //
@@ -61,7 +61,9 @@ constexpr int kStages = 6;
 constexpr int kOperand = 16384;  // 128 rows of 64 k, or 64 k of 128, bf16
 constexpr int kStage = 2 * kOperand;
 constexpr int kURing = 4;
-constexpr int SM_BAR = kStages * kStage;
+constexpr int kOut = 4096;  // an epilogue warp's 32 rows of 64 values on their way out
+constexpr int SM_OUT = kStages * kStage;
+constexpr int SM_BAR = SM_OUT + kEpiWarps * kOut;
 enum {
   B_FULL = 0,                   // +stage: both CTAs' copies have landed (first CTA)
   B_EMPTY = B_FULL + kStages,   // +stage: the stage's products have run
@@ -145,6 +147,24 @@ __device__ __forceinline__ void commit_pair(uint32_t bar) {
       : "memory");
 }
 
+// Kernels of a call follow one another without a gap: each lets the next one's CTAs
+// start where there is room and waits, past its own set-up, for the one before to end.
+__device__ __forceinline__ void wait_for_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+// A tile of 32 rows of 64 values (128 bytes, swizzled) out of shared memory; what lies
+// outside the tensor is not written.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int32_t x, int32_t y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(src), "r"(x), "r"(y)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void store_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void store_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 // ---------------------------------------------------------------- units
 enum { REC = 0, DH = 1, DW = 2 };
 struct Unit {
@@ -203,12 +223,98 @@ __device__ __forceinline__ void give_up(volatile int* abort, unsigned site) {
   atomicOr(&g_lm_err, site);
 }
 
+__device__ __forceinline__ uint4 pack8(const uint32_t* w) {
+  return make_uint4(pack_bf16x2(__uint_as_float(w[0]), __uint_as_float(w[1])),
+                    pack_bf16x2(__uint_as_float(w[2]), __uint_as_float(w[3])),
+                    pack_bf16x2(__uint_as_float(w[4]), __uint_as_float(w[5])),
+                    pack_bf16x2(__uint_as_float(w[6]), __uint_as_float(w[7])));
+}
+
+// A row's 128 logits of words from `word` into its running maximum and sum; its target's
+// into *picked.  Exponents are x log2(e) - m log2(e) in one fma: the rounding of the second
+// term is common to all of a row and moves lse by half a step of its own.
+__device__ __forceinline__ void reduce_tile(uint32_t (&v)[2][64], int word, int V, int target, float& top, float& sum,
+                                            float* picked) {
+  if (word + 128 > V) {
+#pragma unroll
+    for (int i = 0; i < 128; ++i)
+      if (word + i >= V) v[i >> 6][i & 63] = 0xff800000u;
+  }
+  const int hit = target - word;
+  if (hit >= 0 && hit < 128) {
+    float x = 0.f;
+#pragma unroll
+    for (int i = 0; i < 128; ++i)
+      if (hit == i) x = __uint_as_float(v[i >> 6][i & 63]);
+    *picked = x;
+  }
+  float m[4] = {top, top, top, top};
+#pragma unroll
+  for (int i = 0; i < 64; ++i)
+    m[i & 3] = max3f(m[i & 3], __uint_as_float(v[i >> 5][2 * (i & 31)]), __uint_as_float(v[i >> 5][2 * (i & 31) + 1]));
+  const float t = fmaxf(max3f(m[0], m[1], m[2]), m[3]);
+  // all -inf so far: any finite reference keeps the exponentials at zero
+  const float ref = t == -INFINITY ? 0.f : t * kLog2e;
+  const uint64_t scale = f2pack(kLog2e, kLog2e), less = f2pack(-ref, -ref);
+  uint64_t s[4];
+#pragma unroll
+  for (int i = 0; i < 64; ++i) {
+    const uint64_t y = fma2(f2pack(__uint_as_float(v[i >> 5][2 * (i & 31)]), __uint_as_float(v[i >> 5][2 * (i & 31) + 1])),
+                            scale, less);
+    float lo, hi;
+    f2unpack(y, lo, hi);
+    const uint64_t e = f2pack(fast_exp2(lo), fast_exp2(hi));
+    s[i & 3] = i < 4 ? e : add2(s[i & 3], e);
+  }
+  float lo, hi;
+  f2unpack(add2(add2(s[0], s[1]), add2(s[2], s[3])), lo, hi);
+  sum = fmaf(sum, fast_exp2(fmaf(top, kLog2e, -ref)), lo + hi);
+  top = t;
+}
+
+// G of a row's 128 words from `word`, bf16, to `out`; zero from word V on.
+__device__ __forceinline__ void gradient_tile(const uint32_t (&v)[2][64], int word, int V, int target, float off,
+                                              float d_loss, __nv_bfloat16* out) {
+  const uint64_t scale = f2pack(kLog2e, kLog2e), less = f2pack(-off, -off), by = f2pack(d_loss, d_loss);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int hit = target - word - 32 * q;
+    uint32_t g[16];
+    if (__any_sync(0xffffffffu, (hit >= 0 && hit < 32) || word + 32 * q + 32 > V)) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        float p[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          p[k] = fast_exp2(fmaf(__uint_as_float(v[q >> 1][32 * (q & 1) + 2 * i + k]), kLog2e, -off));
+          if (hit == 2 * i + k) p[k] -= 1.f;
+          p[k] = word + 32 * q + 2 * i + k < V ? p[k] * d_loss : 0.f;
+        }
+        g[i] = pack_bf16x2(p[0], p[1]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        float lo, hi;
+        f2unpack(fma2(f2pack(__uint_as_float(v[q >> 1][32 * (q & 1) + 2 * i]),
+                             __uint_as_float(v[q >> 1][32 * (q & 1) + 2 * i + 1])),
+                      scale, less),
+                 lo, hi);
+        f2unpack(mul2(f2pack(fast_exp2(lo), fast_exp2(hi)), by), lo, hi);
+        g[i] = pack_bf16x2(lo, hi);
+      }
+    }
+    st_global_v8(out + 32 * q, g);
+    st_global_v8(out + 32 * q + 16, g + 8);
+  }
+}
+
 template <bool FWD>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     lm_kernel(const __grid_constant__ LmArgs a, const __grid_constant__ CUtensorMap m_hk,
               const __grid_constant__ CUtensorMap m_wk, const __grid_constant__ CUtensorMap m_hm,
               const __grid_constant__ CUtensorMap m_wm, const __grid_constant__ CUtensorMap m_gk,
-              const __grid_constant__ CUtensorMap m_gm) {
+              const __grid_constant__ CUtensorMap m_gm, const __grid_constant__ CUtensorMap m_wo) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* sptr = smem_raw + (sbase - smem_u32(smem_raw));
@@ -237,6 +343,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  wait_for_previous();
   const Counts c = counts(a);
 
   if (warp == kProducerWarp) {
@@ -376,17 +483,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (u < 0) break;
       const Unit x = unit_of(a, c, u);
       const int row = x.m * 256 + r_in;
+      const bool has_row = row < c.rows;
       int target = -1;
       float off = 0.f, d_loss = 0.f;
-      int64_t orig = 0;
-      if (x.kind != DW && row < c.rows) {
-        orig = a.rows[row];
-        if (x.kind == REC) {
-          target = a.targets[orig];
-          if (!FWD) {
-            off = a.lse[orig];
-            d_loss = a.d_loss[orig];
-          }
+      if (x.kind == REC && has_row) {
+        target = a.targets[row];
+        if (!FWD) {
+          off = a.lse[row] * kLog2e;
+          d_loss = a.d_loss[row];
         }
       }
       float top = -INFINITY, sum = 0.f;  // forward: the row's running maximum and sum
@@ -398,125 +502,70 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
-        const int col0 = (x.n + t) * 256 + 128 * half;  // of the piece, or of dims
-#pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
-          uint32_t v[32];
-          tmem_ld32(t_lane + 256 * acc + 32 * q, v);
-          tmem_wait_ld();
-          if (q == 3) {  // all of it is in registers
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive_cluster(in_cta(bar(B_ACC_FREE + acc), 0));
+        // all of the warp's values, so that the accumulator is free before they are worked on
+        uint32_t v[2][64];
+        tmem_ld64(t_lane + 256 * acc, v[0]);
+        tmem_ld64(t_lane + 256 * acc + 64, v[1]);
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(in_cta(bar(B_ACC_FREE + acc), 0));
+        const int col = (x.n + t) * 256 + 128 * half;  // of the piece, or of dims
+        if (FWD) {
+          reduce_tile(v, col, a.V, target, top, sum, a.picked + row);
+        } else if (x.kind == REC) {
+          gradient_tile(v, a.rec_v0 + col, has_row ? a.V : 0, target, off, d_loss,
+                        a.g_out + static_cast<int64_t>(row) * a.g_ld + col);
+        } else if (x.kind == DH) {
+          if (!has_row) continue;
+          if (x.nkb == 0) {
+#pragma unroll
+            for (int i = 0; i < 128; ++i) v[i >> 6][i & 63] = 0u;
           }
-          const int col = col0 + 32 * q;
-          if (x.kind == REC) {
-            const int word = a.rec_v0 + col;
-            const int hit = target - word;
-            if (FWD) {
-              if (word + 32 > a.V) {
+          float* sums = a.acc + (static_cast<int64_t>(x.part) * a.acc_rows + row) * a.acc_ld + col;
+          __nv_bfloat16* out = a.dh + (a.finish ? static_cast<int64_t>(a.rows[row]) * a.D + col : 0);
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  if (word + i >= a.V) v[i] = 0xff800000u;
-              }
-              float m = top;
-#pragma unroll
-              for (int i = 0; i < 32; i += 2) m = max3f(m, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
-              // all -inf so far: any finite reference keeps the exponentials at zero
-              const float ref = m == -INFINITY ? 0.f : m;
-              sum *= fast_exp2((top - ref) * kLog2e);
-              float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-              for (int i = 0; i < 32; i += 2) {  // the difference first: it is exact where it matters
-                s0 += fast_exp2((__uint_as_float(v[i]) - ref) * kLog2e);
-                s1 += fast_exp2((__uint_as_float(v[i + 1]) - ref) * kLog2e);
-              }
-              sum += s0 + s1;
-              top = m;
-              if (hit >= 0 && hit < 32) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  if (hit == i) a.picked[row] = __uint_as_float(v[i]);
-              }
-            } else {
-              float p[32];
-#pragma unroll
-              for (int i = 0; i < 32; ++i) p[i] = fast_exp2((__uint_as_float(v[i]) - off) * kLog2e);
-              if (hit >= 0 && hit < 32) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  if (hit == i) p[i] -= 1.f;
-              }
-              uint32_t g[16];
-#pragma unroll
-              for (int i = 0; i < 16; ++i) g[i] = pack_bf16x2(p[2 * i] * d_loss, p[2 * i + 1] * d_loss);
-              if (row >= c.rows || word + 32 > a.V) {  // rows and words that do not exist count nothing
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  if (row >= c.rows || word + 2 * i >= a.V) g[i] = 0u;
-                  if (word + 2 * i + 1 >= a.V) g[i] &= 0xffffu;
-                }
-              }
-              __nv_bfloat16* out = a.g_out + static_cast<int64_t>(row) * a.g_ld + col;
-              st_global_v8(out, g);
-              st_global_v8(out + 16, g + 8);
+          for (int i = 0; i < 16; ++i) {
+            uint32_t* w = &v[i >> 3][8 * (i & 7)];
+            if (a.add) {
+              const float4 o = reinterpret_cast<const float4*>(sums)[2 * i], z = reinterpret_cast<const float4*>(sums)[2 * i + 1];
+              w[0] = __float_as_uint(__uint_as_float(w[0]) + o.x);
+              w[1] = __float_as_uint(__uint_as_float(w[1]) + o.y);
+              w[2] = __float_as_uint(__uint_as_float(w[2]) + o.z);
+              w[3] = __float_as_uint(__uint_as_float(w[3]) + o.w);
+              w[4] = __float_as_uint(__uint_as_float(w[4]) + z.x);
+              w[5] = __float_as_uint(__uint_as_float(w[5]) + z.y);
+              w[6] = __float_as_uint(__uint_as_float(w[6]) + z.z);
+              w[7] = __float_as_uint(__uint_as_float(w[7]) + z.w);
             }
-          } else if (!FWD && x.kind == DH) {
-            if (x.nkb == 0) {
+            if (!a.finish)
+              st_global_v8(sums + 8 * i, w);
+            else if (col + 8 * i < a.D)
+              reinterpret_cast<uint4*>(out)[i] = pack8(w);
+          }
+        } else {
+          // 32 words of 64 dims at a time, through shared memory
+          const uint32_t out = sbase + SM_OUT + warp * kOut;
+          const int first = a.g_v0 + x.m * 256 + 128 * rank + 32 * quarter;
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = 0u;
+          for (int h = 0; h < 2; ++h) {
+            if (lane == 0) store_read();  // the copy before has left the buffer
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint4 w = x.nkb ? pack8(&v[h][8 * i]) : make_uint4(0, 0, 0, 0);
+              st_shared_v4(out + lane * 128 + ((i ^ (lane & 7)) << 4), w.x, w.y, w.z, w.w);
             }
-            float* sums = a.acc + (static_cast<int64_t>(x.part) * a.acc_rows + row) * a.acc_ld + col;
-            if (a.add && row < c.rows) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float4 o = reinterpret_cast<const float4*>(sums)[i];
-                v[4 * i] = __float_as_uint(__uint_as_float(v[4 * i]) + o.x);
-                v[4 * i + 1] = __float_as_uint(__uint_as_float(v[4 * i + 1]) + o.y);
-                v[4 * i + 2] = __float_as_uint(__uint_as_float(v[4 * i + 2]) + o.z);
-                v[4 * i + 3] = __float_as_uint(__uint_as_float(v[4 * i + 3]) + o.w);
-              }
-            }
-            if (row < c.rows) {
-              if (a.finish) {
-                __nv_bfloat16* out = a.dh + orig * a.D + col;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  if (col + 8 * i < a.D)
-                    reinterpret_cast<uint4*>(out)[i] = make_uint4(
-                        pack_bf16x2(__uint_as_float(v[8 * i]), __uint_as_float(v[8 * i + 1])),
-                        pack_bf16x2(__uint_as_float(v[8 * i + 2]), __uint_as_float(v[8 * i + 3])),
-                        pack_bf16x2(__uint_as_float(v[8 * i + 4]), __uint_as_float(v[8 * i + 5])),
-                        pack_bf16x2(__uint_as_float(v[8 * i + 6]), __uint_as_float(v[8 * i + 7])));
-              } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) st_global_v8(sums + 8 * i, v + 8 * i);
-              }
-            }
-          } else if (!FWD) {
-            const int in_piece = x.m * 256 + r_in;
-            const int64_t word = a.g_v0 + in_piece;
-            if (in_piece < a.g_cols && word < a.V) {
-              if (x.nkb == 0) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = 0u;
-              }
-              __nv_bfloat16* out = a.dw + word * a.D + col;
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (col + 8 * i < a.D)
-                  reinterpret_cast<uint4*>(out)[i] = make_uint4(
-                      pack_bf16x2(__uint_as_float(v[8 * i]), __uint_as_float(v[8 * i + 1])),
-                      pack_bf16x2(__uint_as_float(v[8 * i + 2]), __uint_as_float(v[8 * i + 3])),
-                      pack_bf16x2(__uint_as_float(v[8 * i + 4]), __uint_as_float(v[8 * i + 5])),
-                      pack_bf16x2(__uint_as_float(v[8 * i + 6]), __uint_as_float(v[8 * i + 7])));
-            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && col + 64 * h < a.D && first < a.V) tma_store_2d(&m_wo, out, col + 64 * h, first);
           }
         }
       }
-      if (FWD && ok && row < c.rows)
-        a.part[static_cast<int64_t>(2 * (x.n / a.run) + half) * a.part_ld + row] = make_float2(top, sum);
+      if (FWD && ok && has_row)
+        a.part[static_cast<int64_t>(row) * a.part_ld + 2 * (x.n / a.run) + half] = make_float2(top, sum);
     }
+    if (!FWD && lane == 0) store_done();
     __syncwarp();
   }
 
@@ -537,116 +586,150 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------- rows with a target
-constexpr int kRowsThreads = 1024;
-// One CTA: the indices of the rows with a target, in order, and their number; zeros the
-// counters.  A target of V or more is no word: its row's loss is NaN and it takes no part.
-__global__ void __launch_bounds__(kRowsThreads) lm_rows_kernel(const int32_t* __restrict__ targets, int32_t n, int32_t V,
-                                                               int32_t* __restrict__ rows, int32_t* __restrict__ head,
-                                                               int32_t heads, float* loss, float* lse) {
-  __shared__ int32_t warp_sum[32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int i = tid + 1; i < heads; i += kRowsThreads) head[i] = 0;
-  const int64_t each = (static_cast<int64_t>(n) + kRowsThreads - 1) / kRowsThreads;
-  const int64_t lo = min(static_cast<int64_t>(n), tid * each), hi = min(static_cast<int64_t>(n), lo + each);
-  int count = 0;
+// The rows with a target side by side, in order, with what the epilogues ask of them, and
+// zeros up to the next multiple of 64 (dw sums over rows in steps of 64).  The others get
+// their zeros here.  A target of V or more is no word: its row's loss is NaN and it takes
+// no part.
+//
+// A CTA takes a run of rows, a warp K of them at a time (one where rows are few, so that
+// they spread over the GPU).  Where they go depends on all targets before them, which every
+// CTA counts for itself: n / 256 reads a thread, which take less time than a launch of
+// their own would up to some 10^5 rows, and the CTAs are at most kRowCtas to bound them.
+constexpr int kRowThreads = 256, kRowCtas = 512;
+template <int K>
+__global__ void __launch_bounds__(kRowThreads) lm_rows_kernel(const LmRows a) {
+  __shared__ int s_all[kRowThreads / 32], s_before[kRowThreads / 32];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * a.rows_cta;
+  auto word = [&](int32_t t) { return static_cast<uint32_t>(t) < static_cast<uint32_t>(a.V); };
+  int all = 0, before = 0;
 #pragma unroll 8
-  for (int64_t i = lo; i < hi; ++i) {
-    const int t = targets[i];
-    count += t >= 0 && t < V;
+  for (int i = threadIdx.x; i < a.n; i += kRowThreads) {
+    const int is = word(a.targets[i]);
+    all += is;
+    before += i < first ? is : 0;
   }
-  int scan = count;
-#pragma unroll
-  for (int o = 1; o < 32; o *= 2) {
-    const int y = __shfl_up_sync(0xffffffffu, scan, o);
-    if (lane >= o) scan += y;
-  }
-  if (lane == 31) warp_sum[warp] = scan;
-  __syncthreads();
-  if (warp == 0) {
-    int x = warp_sum[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-      const int y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    warp_sum[lane] = x;
+  all = __reduce_add_sync(0xffffffffu, all);
+  before = __reduce_add_sync(0xffffffffu, before);
+  if (lane == 0) {
+    s_all[warp] = all;
+    s_before[warp] = before;
   }
   __syncthreads();
-  int at = scan - count + (warp ? warp_sum[warp - 1] : 0);
-  if (tid == 0) head[0] = warp_sum[31];
-#pragma unroll 4
-  for (int64_t i = lo; i < hi; ++i) {
-    const int t = targets[i];
-    if (t >= 0 && t < V) {
-      rows[at++] = static_cast<int32_t>(i);
-    } else if (loss) {
-      loss[i] = t < 0 ? 0.f : __uint_as_float(0x7fffffffu);
-      lse[i] = 0.f;
-    }
+  all = before = 0;
+#pragma unroll
+  for (int i = 0; i < kRowThreads / 32; ++i) {
+    all += s_all[i];
+    before += s_before[i];
   }
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < a.heads; i += kRowThreads) a.head[i] = i == 0 ? all : 0;
+  constexpr int kGroup = 8 * K;
+  for (int64_t g = first; g < first + a.rows_cta && g < a.n; g += kGroup) {
+    const int t = lane < kGroup && g + lane < a.n ? a.targets[g + lane] : -1;
+    const uint32_t who = __ballot_sync(0xffffffffu, word(t));
+    if (warp == 0 && lane < kGroup && g + lane < a.n) {
+      if (word(t)) {
+        const int at = before + __popc(who & ((1u << lane) - 1));
+        a.rows[at] = static_cast<int32_t>(g) + lane;
+        a.t_out[at] = t;
+        if (a.lse_out) {
+          a.lse_out[at] = a.lse[g + lane];
+          a.d_out[at] = a.d_loss[g + lane];
+        }
+      } else if (!a.lse_out) {
+        a.loss[g + lane] = t < 0 ? 0.f : __uint_as_float(0x7fffffffu);
+        a.lse[g + lane] = 0.f;
+      }
+    }
+    const uint4* src[K];
+    uint4* dst[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int r = K * warp + k;
+      const int64_t i = g + r;
+      src[k] = nullptr;
+      dst[k] = a.dh && i < a.n ? a.dh + i * a.vecs : nullptr;
+      if (who >> r & 1) {
+        src[k] = a.h + i * a.h_vecs;
+        dst[k] = a.out + static_cast<int64_t>(before + __popc(who & ((1u << r) - 1))) * a.vecs;
+      }
+    }
+#pragma unroll 2
+    for (int j = lane; j < a.vecs; j += 32) {
+      uint4 v[K];
+#pragma unroll
+      for (int k = 0; k < K; ++k) v[k] = src[k] ? src[k][j] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if (dst[k]) dst[k][j] = v[k];
+    }
+    before += __popc(who);
+  }
+  const int64_t pad = static_cast<int64_t>(-all & 63) * a.vecs;
+  for (int64_t j = static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x; j < pad; j += static_cast<int64_t>(gridDim.x) * kRowThreads)
+    a.out[static_cast<int64_t>(all) * a.vecs + j] = make_uint4(0, 0, 0, 0);
 }
 
-// Rows with a target side by side, zeros up to the next multiple of 256; in the backward
-// pass, zeros for the others' gradients.  A warp a row.
-__global__ void __launch_bounds__(256) lm_gather_kernel(const uint4* __restrict__ h, int64_t stride, uint4* __restrict__ out,
-                                                        const int32_t* __restrict__ rows, const int32_t* __restrict__ head,
-                                                        const int32_t* __restrict__ targets, int32_t n, int32_t V,
-                                                        int32_t vecs, uint4* dh) {
-  const int lane = threadIdx.x & 31;
-  const int i = static_cast<int>(blockIdx.x * 8 + (threadIdx.x >> 5));
-  const int count = *head, padded = (count + 255) & ~255;
-  if (i < padded) {
-    const uint4* src = i < count ? h + rows[i] * stride : nullptr;
-    uint4* dst = out + static_cast<int64_t>(i) * vecs;
-#pragma unroll 4
-    for (int j = lane; j < vecs; j += 32) dst[j] = src ? src[j] : make_uint4(0, 0, 0, 0);
-  }
-  if (dh && i < n) {
-    const int t = targets[i];
-    if (t < 0 || t >= V) {
-      uint4* dst = dh + static_cast<int64_t>(i) * vecs;
-      for (int j = lane; j < vecs; j += 32) dst[j] = make_uint4(0, 0, 0, 0);
-    }
-  }
-}
-
-// lse and loss of 32 rows from their partial maxima and sums.
-__global__ void __launch_bounds__(1024) lm_join_kernel(const float2* __restrict__ part, int64_t ld, int32_t parts,
-                                                       const float* __restrict__ picked, const int32_t* __restrict__ rows,
-                                                       const int32_t* __restrict__ head, float* __restrict__ loss,
-                                                       float* __restrict__ lse) {
-  __shared__ float2 s[32][33];
-  const int r = threadIdx.x & 31, p0 = threadIdx.x >> 5, row = blockIdx.x * 32 + r, count = *head;
-  if (static_cast<int>(blockIdx.x) * 32 >= count) return;
+// lse and loss of a row from its partial maxima and sums, which lie side by side.
+// THREADS a row: a warp, or, of many partial results (few rows), four.
+constexpr int kJoinThreads = 128;
+template <int THREADS>
+__global__ void __launch_bounds__(kJoinThreads) lm_join_kernel(const float2* __restrict__ part, int32_t parts,
+                                                               const float* __restrict__ picked,
+                                                               const int32_t* __restrict__ rows,
+                                                               const int32_t* __restrict__ head, float* __restrict__ loss,
+                                                               float* __restrict__ lse) {
+  __shared__ float s_max[kJoinThreads / 32], s_sum[kJoinThreads / 32];
+  wait_for_previous();
+  constexpr bool kOne = THREADS == 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, me = threadIdx.x % THREADS;
+  const int row = blockIdx.x * (kJoinThreads / THREADS) + threadIdx.x / THREADS;
+  if (row >= *head) return;
+  part += static_cast<int64_t>(row) * parts;
+  constexpr int kAhead = 4;
   float m = -INFINITY, l = 0.f;
-  if (row < count) {
-#pragma unroll 8
-    for (int p = p0; p < parts; p += 32) {
-      const float2 x = part[p * ld + row];
-      const float t = fmaxf(m, x.x);
-      const float ref = t == -INFINITY ? 0.f : t;
-      // a NaN sum stays one: fmaxf drops a NaN maximum
-      l = l * fast_exp2((m - ref) * kLog2e) + x.y * fast_exp2((x.x - ref) * kLog2e);
-      m = t;
-    }
+  for (int p0 = me; p0 < parts; p0 += kAhead * THREADS) {
+    float2 x[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      x[i] = p0 + i * THREADS < parts ? part[p0 + i * THREADS] : make_float2(-INFINITY, 0.f);
+    float t = m;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) t = fmaxf(t, x[i].x);
+    const float ref = t == -INFINITY ? 0.f : t;
+    // a NaN logit is in its sum: fmaxf drops it from the maximum
+    l *= fast_exp2((m - ref) * kLog2e);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) l += x[i].y * fast_exp2((x[i].x - ref) * kLog2e);
+    m = t;
   }
-  s[p0][r] = make_float2(m, l);
-  __syncthreads();
-  // warp p0 joins row p0's 32
-  const float2 x = s[r][p0];
-  float t = x.x;
+  float t = m;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
-  const float ref = t == -INFINITY ? 0.f : t;
-  float sum = x.y * fast_exp2((x.x - ref) * kLog2e);
+  if (!kOne) {
+    if (lane == 0) s_max[warp] = t;
+    __syncthreads();
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  const int mine = blockIdx.x * 32 + p0;
-  if (r == 0 && mine < count) {
-    const float v = t + logf(sum);
-    const int32_t at = rows[mine];
+    for (int i = 0; i < kJoinThreads / 32; ++i) t = fmaxf(t, s_max[i]);
+  }
+  const float ref = t == -INFINITY ? 0.f : t;
+  l *= fast_exp2((m - ref) * kLog2e);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if (!kOne) {
+    if (lane == 0) s_sum[warp] = l;
+    __syncthreads();
+    l = 0.f;
+#pragma unroll
+    for (int i = 0; i < kJoinThreads / 32; ++i) l += s_sum[i];
+  }
+  if (me == 0) {
+    const float v = t + logf(l);
+    const int32_t at = rows[row];
     lse[at] = v;
-    loss[at] = v - picked[mine];
+    loss[at] = v - picked[row];
   }
 }
 
@@ -655,6 +738,7 @@ __global__ void __launch_bounds__(256) lm_finish_kernel(const float* __restrict_
                                                         int32_t splits, const int32_t* __restrict__ rows,
                                                         const int32_t* __restrict__ head, int32_t D,
                                                         __nv_bfloat16* __restrict__ dh) {
+  wait_for_previous();
   const int row = blockIdx.x;
   if (row >= *head) return;
   const int64_t at = rows[row];
@@ -684,12 +768,28 @@ int make_map(EncodeTiledFn enc, CUtensorMap* m, const void* ptr, int64_t cols, i
   return PADOC_ERR_CUDA;
 }
 
-int cuda_check(const char* what, std::string* err) {
-  const cudaError_t e = cudaGetLastError();
+// A launch that may begin its set-up while the kernel before it on the stream, which is
+// one of this file's, still runs.
+template <class... P, class... A>
+int launch_after(void (*kernel)(P...), unsigned grid, int threads, int smem, cudaStream_t s, const char* what,
+                 std::string* err, const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
   if (e == cudaSuccess) return PADOC_OK;
-  *err = std::string(what) + ": " + cudaGetErrorString(e);
+  *err = std::string(what) + " launch: " + cudaGetErrorString(e);
   return PADOC_ERR_CUDA;
 }
+
+enum { M_HK, M_WK, M_HM, M_WM, M_GK, M_GM, M_WO, N_MAPS };
 
 template <bool FWD>
 int launch_gemm(const LmArgs& a, const CUtensorMap* m, cudaStream_t s, std::string* err) {
@@ -699,19 +799,43 @@ int launch_gemm(const LmArgs& a, const CUtensorMap* m, cudaStream_t s, std::stri
     *err = std::string("cudaFuncSetAttribute: ") + cudaGetErrorString(e);
     return PADOC_ERR_CUDA;
   }
-  lm_kernel<FWD><<<num_sms() / 2 * 2, kThreads, kSmemBytes, s>>>(a, m[0], m[1], m[2], m[3], m[4], m[5]);
-  return cuda_check("lm_kernel launch", err);
+  return launch_after(lm_kernel<FWD>, num_sms() / 2 * 2, kThreads, kSmemBytes, s, "lm_kernel", err, a, m[M_HK], m[M_WK],
+                      m[M_HM], m[M_WM], m[M_GK], m[M_GM], m[M_WO]);
 }
 
-int rows_and_gather(const LmCall& l, const LmPlan& p, uint8_t* ws, bool backward, cudaStream_t s, std::string* err) {
-  int32_t* head = reinterpret_cast<int32_t*>(ws + p.head);
-  int32_t* rows = reinterpret_cast<int32_t*>(ws + p.rows);
-  lm_rows_kernel<<<1, kRowsThreads, 0, s>>>(l.targets, l.n, l.V, rows, head, p.heads, backward ? nullptr : l.loss,
-                                            backward ? nullptr : l.lse);
-  lm_gather_kernel<<<static_cast<unsigned>(p.n_pad / 8), 256, 0, s>>>(
-      static_cast<const uint4*>(l.h), l.h_stride / 8, reinterpret_cast<uint4*>(ws + p.hc), rows, head, l.targets, l.n, l.V,
-      l.D / 8, backward ? static_cast<uint4*>(l.dh) : nullptr);
-  return cuda_check("row kernels", err);
+int launch_rows(const LmCall& l, const LmPlan& p, uint8_t* ws, bool backward, cudaStream_t s, std::string* err) {
+  LmRows a{};
+  a.h = static_cast<const uint4*>(l.h);
+  a.h_vecs = l.h_stride / 8;
+  a.targets = l.targets;
+  a.n = l.n;
+  a.V = l.V;
+  a.vecs = l.D / 8;
+  a.heads = p.heads;
+  a.head = reinterpret_cast<int32_t*>(ws + p.head);
+  a.rows = reinterpret_cast<int32_t*>(ws + p.rows);
+  a.t_out = reinterpret_cast<int32_t*>(ws + p.t);
+  a.out = reinterpret_cast<uint4*>(ws + p.hc);
+  a.loss = l.loss;
+  a.lse = l.lse;
+  if (backward) {
+    a.lse_out = reinterpret_cast<float*>(ws + p.lse);
+    a.d_loss = l.d_loss;
+    a.d_out = reinterpret_cast<float*>(ws + p.d);
+    a.dh = static_cast<uint4*>(l.dh);
+  }
+  const bool few = l.n <= 8 * kRowCtas;
+  const int64_t group = few ? 8 : 32, groups = (static_cast<int64_t>(l.n) + group - 1) / group;
+  a.rows_cta = (groups + kRowCtas - 1) / kRowCtas * group;
+  const unsigned grid = static_cast<unsigned>((l.n + a.rows_cta - 1) / a.rows_cta);
+  if (few)
+    lm_rows_kernel<1><<<grid, kRowThreads, 0, s>>>(a);
+  else
+    lm_rows_kernel<4><<<grid, kRowThreads, 0, s>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) return PADOC_OK;
+  *err = std::string("lm_rows_kernel launch: ") + cudaGetErrorString(e);
+  return PADOC_ERR_CUDA;
 }
 
 }  // namespace
@@ -738,6 +862,7 @@ LmPlan lm_plan(int32_t n, int32_t D, int32_t V, bool backward) {
     p.heads = 2;
     p.head = take(p.heads * sizeof(int32_t));
     p.rows = take(n * sizeof(int32_t));
+    p.t = take(n * sizeof(int32_t));
     p.hc = take(static_cast<size_t>(p.n_pad) * D * 2);
     p.parts = static_cast<int32_t>(2 * ((word_tiles + p.run - 1) / p.run));
     p.part = take(static_cast<size_t>(p.parts) * p.n_pad * sizeof(float2));
@@ -759,6 +884,9 @@ LmPlan lm_plan(int32_t n, int32_t D, int32_t V, bool backward) {
   p.heads = 2 + p.pieces;
   p.head = take(p.heads * sizeof(int32_t));
   p.rows = take(n * sizeof(int32_t));
+  p.t = take(n * sizeof(int32_t));
+  p.lse = take(n * sizeof(float));
+  p.d = take(n * sizeof(float));
   p.hc = take(static_cast<size_t>(p.n_pad) * D * 2);
   p.acc_ld = static_cast<int32_t>(d_tiles * 256);
   p.acc = take(p.pieces > 1 || p.splits > 1 ? static_cast<size_t>(p.splits) * p.n_pad * p.acc_ld * sizeof(float) : 0);
@@ -773,19 +901,18 @@ int launch_lm_loss(const LmCall& l, void* ws_, cudaStream_t s, std::string* err)
   uint8_t* ws = static_cast<uint8_t*>(ws_);
   EncodeTiledFn enc = get_encode_fn(err);
   if (!enc) return PADOC_ERR_CUDA;
-  CUtensorMap m[6];
-  int rc = make_map(enc, &m[0], ws + p.hc, l.D, p.n_pad, l.D, 128, err);
-  if (!rc) rc = make_map(enc, &m[1], l.w, l.D, l.V, l.w_stride, 128, err);
+  CUtensorMap m[N_MAPS]{};
+  int rc = make_map(enc, &m[M_HK], ws + p.hc, l.D, p.n_pad, l.D, 128, err);
+  if (!rc) rc = make_map(enc, &m[M_WK], l.w, l.D, l.V, l.w_stride, 128, err);
   if (rc) return rc;
-  for (int i = 2; i < 6; ++i) m[i] = m[0];
-  rc = rows_and_gather(l, p, ws, false, s, err);
+  rc = launch_rows(l, p, ws, false, s, err);
   if (rc) return rc;
   int32_t* head = reinterpret_cast<int32_t*>(ws + p.head);
   LmArgs a{};
   a.n_rows = head;
   a.counter = head + 1;
   a.rows = reinterpret_cast<int32_t*>(ws + p.rows);
-  a.targets = l.targets;
+  a.targets = reinterpret_cast<int32_t*>(ws + p.t);
   a.D = l.D;
   a.V = l.V;
   a.k_blocks = (l.D + 63) / 64;
@@ -794,13 +921,14 @@ int launch_lm_loss(const LmCall& l, void* ws_, cudaStream_t s, std::string* err)
   a.splits = 1;
   a.rec_cols = l.V;
   a.part = reinterpret_cast<float2*>(ws + p.part);
-  a.part_ld = p.n_pad;
+  a.part_ld = p.parts;
   a.picked = reinterpret_cast<float*>(ws + p.picked);
   rc = launch_gemm<true>(a, m, s, err);
   if (rc) return rc;
-  lm_join_kernel<<<static_cast<unsigned>((l.n + 31) / 32), 1024, 0, s>>>(a.part, a.part_ld, p.parts, a.picked, a.rows, head,
-                                                                        l.loss, l.lse);
-  return cuda_check("lm_join_kernel launch", err);
+  const bool many = p.parts > 256;
+  return launch_after(many ? lm_join_kernel<kJoinThreads> : lm_join_kernel<32>,
+                      many ? static_cast<unsigned>(l.n) : static_cast<unsigned>((l.n + 3) / 4), kJoinThreads, 0, s,
+                      "lm_join_kernel", err, a.part, p.parts, a.picked, a.rows, head, l.loss, l.lse);
 }
 
 int launch_lm_loss_bwd(const LmCall& l, void* ws_, cudaStream_t s, std::string* err) {
@@ -809,31 +937,32 @@ int launch_lm_loss_bwd(const LmCall& l, void* ws_, cudaStream_t s, std::string* 
   EncodeTiledFn enc = get_encode_fn(err);
   if (!enc) return PADOC_ERR_CUDA;
   const int32_t g_ld = p.piece_tiles * 256;
-  CUtensorMap m[6], gk[2], gm[2];
-  int rc = make_map(enc, &m[0], ws + p.hc, l.D, p.n_pad, l.D, 128, err);
-  if (!rc) rc = make_map(enc, &m[1], l.w, l.D, l.V, l.w_stride, 128, err);
-  if (!rc) rc = make_map(enc, &m[2], ws + p.hc, l.D, p.n_pad, l.D, 64, err);
-  if (!rc) rc = make_map(enc, &m[3], l.w, l.D, l.V, l.w_stride, 64, err);
+  CUtensorMap m[N_MAPS]{}, gk[2], gm[2];
+  int rc = make_map(enc, &m[M_HK], ws + p.hc, l.D, p.n_pad, l.D, 128, err);
+  if (!rc) rc = make_map(enc, &m[M_WK], l.w, l.D, l.V, l.w_stride, 128, err);
+  if (!rc) rc = make_map(enc, &m[M_HM], ws + p.hc, l.D, p.n_pad, l.D, 64, err);
+  if (!rc) rc = make_map(enc, &m[M_WM], l.w, l.D, l.V, l.w_stride, 64, err);
+  if (!rc && l.dw) rc = make_map(enc, &m[M_WO], l.dw, l.D, l.V, l.D, 32, err);
   for (int i = 0; i < (p.pieces > 1 ? 2 : 1) && !rc; ++i) {
     rc = make_map(enc, &gk[i], ws + p.g + i * p.g_bytes, g_ld, p.n_pad, g_ld, 128, err);
     if (!rc) rc = make_map(enc, &gm[i], ws + p.g + i * p.g_bytes, g_ld, p.n_pad, g_ld, 64, err);
   }
   if (rc) return rc;
-  rc = rows_and_gather(l, p, ws, true, s, err);
+  rc = launch_rows(l, p, ws, true, s, err);
   if (rc) return rc;
   int32_t* head = reinterpret_cast<int32_t*>(ws + p.head);
   LmArgs a{};
   a.n_rows = head;
   a.rows = reinterpret_cast<int32_t*>(ws + p.rows);
-  a.targets = l.targets;
+  a.targets = reinterpret_cast<int32_t*>(ws + p.t);
   a.D = l.D;
   a.V = l.V;
   a.k_blocks = (l.D + 63) / 64;
   a.d_tiles = (l.D + 255) / 256;
   a.run = p.run;
   a.splits = p.splits;
-  a.lse = l.lse;
-  a.d_loss = l.d_loss;
+  a.lse = reinterpret_cast<float*>(ws + p.lse);
+  a.d_loss = reinterpret_cast<float*>(ws + p.d);
   a.acc = reinterpret_cast<float*>(ws + p.acc);
   a.acc_rows = p.n_pad;
   a.acc_ld = p.acc_ld;
@@ -854,17 +983,16 @@ int launch_lm_loss_bwd(const LmCall& l, void* ws_, cudaStream_t s, std::string* 
     }
     a.rec_v0 = i * g_ld;
     a.rec_cols = i < p.pieces ? static_cast<int32_t>(std::min<int64_t>(g_ld, static_cast<int64_t>(l.V) - a.rec_v0)) : 0;
-    a.g_out = reinterpret_cast<__nv_bfloat16*>(ws + p.g + (i & 1) * p.g_bytes);
-    if (i >= p.pieces) a.g_out = nullptr;
-    m[4] = gk[done > 0 ? done & 1 : 0];
-    m[5] = gm[done > 0 ? done & 1 : 0];
+    const int from = done > 0 ? done & 1 : 0;
+    a.g_out = reinterpret_cast<__nv_bfloat16*>(ws + p.g + (i < p.pieces && i & 1 ? p.g_bytes : 0));
+    m[M_GK] = gk[from];
+    m[M_GM] = gm[from];
     rc = launch_gemm<false>(a, m, s, err);
     if (rc) return rc;
   }
   if (l.dh && p.splits > 1) {
-    lm_finish_kernel<<<static_cast<unsigned>(l.n), 256, 0, s>>>(a.acc, a.acc_rows, a.acc_ld, p.splits, a.rows, head, l.D,
-                                                               static_cast<__nv_bfloat16*>(l.dh));
-    return cuda_check("lm_finish_kernel launch", err);
+    return launch_after(lm_finish_kernel, static_cast<unsigned>(l.n), 256, 0, s, "lm_finish_kernel", err, a.acc, a.acc_rows,
+                        static_cast<int32_t>(a.acc_ld), p.splits, a.rows, head, l.D, static_cast<__nv_bfloat16*>(l.dh));
   }
   return PADOC_OK;
 }

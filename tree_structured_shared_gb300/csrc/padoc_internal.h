@@ -238,6 +238,7 @@ struct RopeArgs {
   int64_t n;
   int32_t n_pos, rot_dim, interleaved, backward;
   int32_t heads;              // of all parts together
+  int32_t slots, rows_warp;   // heads of a row that a warp holds at once, and rows (the launcher's)
   int32_t first[kRopeParts];  // first head of each part (heads: no such part)
   const void* x[kRopeParts];
   void* out[kRopeParts];
@@ -290,12 +291,29 @@ struct LmCall {
 struct LmPlan {
   int64_t n_pad;
   int32_t run, parts, pieces, piece_tiles, splits, heads, acc_ld;
-  size_t head, rows, hc, part, picked, acc, g, g_bytes, bytes;
+  size_t head, rows, t, lse, d, hc, part, picked, acc, g, g_bytes, bytes;
+};
+struct LmRows {
+  const uint4* h;
+  int64_t h_vecs;  // 16-byte vectors between rows
+  const int32_t* targets;
+  int32_t n, V, vecs, heads;
+  int64_t rows_cta;
+  int32_t* head;   // number of rows with a target, then unit counters
+  int32_t* rows;   // their indices
+  int32_t* t_out;  // their targets
+  uint4* out;      // their h
+  float* loss;     // forward
+  float* lse;      // forward: out, backward: in
+  const float* d_loss;
+  float* lse_out;  // backward: theirs
+  float* d_out;
+  uint4* dh;       // backward, may be null
 };
 struct LmArgs {
   const int32_t* n_rows;
   int32_t* counter;  // of units, zero at launch
-  const int32_t* rows;
+  const int32_t* rows;     // of the rows with a target: index, target (and lse, d_loss below)
   const int32_t* targets;
   int32_t D, V;
   int32_t k_blocks, d_tiles, run, splits;
@@ -318,7 +336,7 @@ struct LmArgs {
 };
 
 // Launchers (return 0 or a PADOC_ERR_* code, message in *err).
-int launch_rope_apply(const RopeArgs& a, int32_t dtype, int32_t d, cudaStream_t s, std::string* err);
+int launch_rope_apply(RopeArgs a, int32_t dtype, int32_t d, cudaStream_t s, std::string* err);
 int launch_rope_table(const RopeTableArgs& a, cudaStream_t s, std::string* err);
 int launch_act(ActArgs a, bool keep, cudaStream_t s, std::string* err);
 LmPlan lm_plan(int32_t n, int32_t D, int32_t V, bool backward);

@@ -10,16 +10,15 @@
 // transpose (a c + b s, b c - a s); that is the rotation back times the amplitude's
 // square where the table holds an amplitude other than 1.
 //
-// Both are streams.  A warp takes a row: eight lanes a head of 128 dims (four of 64),
-// each with 16 dims that hold both partners of its eight pairs, so no lane needs
-// another's values, and cosines and sines are read once for the heads that follow one
-// another through the warp.
+// Both are streams.  A warp takes a row (or more, of few heads): a lane holds two chunks
+// of 16 bytes of a head with both partners of its pairs, so no lane needs another's
+// values, and cosines and sines are read once for the heads that follow one another
+// through the warp.
 //
 // Angles: a position and an angle a step are an integer and a fraction of a turn, so a
 // position's fraction is their product modulo 2^64 with the step as a 64-bit binary
 // fraction.  That is exact but for the step's own rounding (2^-53 of it), at any
-// position, without a 64-bit floating operation; the remainder within half a turn goes
-// to sincospif.
+// position, without a 64-bit floating operation.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -37,21 +36,16 @@ using namespace ptx;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
-// 16 dims of a row: 8 from each of two places.
+// Values of 16 bytes, and their arithmetic in f32.
 template <class T>
-struct Item;
+struct Chunk;
 template <>
-struct Item<__nv_bfloat16> {
-  uint4 a, b;
-  __device__ __forceinline__ void load(const __nv_bfloat16* pa, const __nv_bfloat16* pb) {
-    a = __ldcs(reinterpret_cast<const uint4*>(pa));
-    b = __ldcs(reinterpret_cast<const uint4*>(pb));
-  }
-  __device__ __forceinline__ void store(__nv_bfloat16* pa, __nv_bfloat16* pb) const {
-    *reinterpret_cast<uint4*>(pa) = a;
-    *reinterpret_cast<uint4*>(pb) = b;
-  }
-  static __device__ __forceinline__ void up(const uint4& u, float* x) {
+struct Chunk<__nv_bfloat16> {
+  static constexpr int V = 8;
+  uint4 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = __ldcs(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = u; }
+  __device__ __forceinline__ void get(float* x) const {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -59,47 +53,23 @@ struct Item<__nv_bfloat16> {
       x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
   }
-  static __device__ __forceinline__ uint4 down(const float* x) {
-    return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                      pack_bf16x2(x[6], x[7]));
-  }
-  __device__ __forceinline__ void get(float (&x)[16]) const {
-    up(a, x);
-    up(b, x + 8);
-  }
-  __device__ __forceinline__ void put(const float (&x)[16]) {
-    a = down(x);
-    b = down(x + 8);
+  __device__ __forceinline__ void put(const float* x) {
+    u = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
   }
 };
 template <>
-struct Item<float> {
-  float4 v[4];
-  __device__ __forceinline__ void load(const float* pa, const float* pb) {
-    v[0] = __ldcs(reinterpret_cast<const float4*>(pa));
-    v[1] = __ldcs(reinterpret_cast<const float4*>(pa) + 1);
-    v[2] = __ldcs(reinterpret_cast<const float4*>(pb));
-    v[3] = __ldcs(reinterpret_cast<const float4*>(pb) + 1);
+struct Chunk<float> {
+  static constexpr int V = 4;
+  float4 u;
+  __device__ __forceinline__ void load(const float* p) { u = __ldcs(reinterpret_cast<const float4*>(p)); }
+  __device__ __forceinline__ void store(float* p) const { *reinterpret_cast<float4*>(p) = u; }
+  __device__ __forceinline__ void get(float* x) const {
+    x[0] = u.x;
+    x[1] = u.y;
+    x[2] = u.z;
+    x[3] = u.w;
   }
-  __device__ __forceinline__ void store(float* pa, float* pb) const {
-    reinterpret_cast<float4*>(pa)[0] = v[0];
-    reinterpret_cast<float4*>(pa)[1] = v[1];
-    reinterpret_cast<float4*>(pb)[0] = v[2];
-    reinterpret_cast<float4*>(pb)[1] = v[3];
-  }
-  __device__ __forceinline__ void get(float (&x)[16]) const {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[4 * i] = v[i].x;
-      x[4 * i + 1] = v[i].y;
-      x[4 * i + 2] = v[i].z;
-      x[4 * i + 3] = v[i].w;
-    }
-  }
-  __device__ __forceinline__ void put(const float (&x)[16]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-  }
+  __device__ __forceinline__ void put(const float* x) { u = make_float4(x[0], x[1], x[2], x[3]); }
 };
 
 // (a, b) in place; sn is negated by the caller for the gradient.
@@ -109,45 +79,84 @@ __device__ __forceinline__ void turn(float& a, float& b, float c, float sn) {
   a = x;
 }
 
+// N consecutive f32 of the table, 8-byte aligned at least.
+template <int N>
+__device__ __forceinline__ void table(const float* p, float* x) {
+  if (N == 2) {
+    const float2 v = __ldg(reinterpret_cast<const float2*>(p));
+    x[0] = v.x;
+    x[1] = v.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const float4 v = __ldg(reinterpret_cast<const float4*>(p) + i);
+      x[4 * i] = v.x;
+      x[4 * i + 1] = v.y;
+      x[4 * i + 2] = v.z;
+      x[4 * i + 3] = v.w;
+    }
+  }
+}
+
 template <class T, int D, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads) rope_apply_kernel(const __grid_constant__ RopeArgs a) {
-  constexpr int ITEMS = D / 16, SLOTS = 32 / ITEMS;  // lanes a head, heads a warp
-  constexpr int U = sizeof(T) == 2 ? 4 : 2;          // heads of a lane on their way at once
-  const int lane = threadIdx.x & 31, item = lane % ITEMS, slot = lane / ITEMS;
-  const int half = a.rot_dim / 2, turning = a.rot_dim / 16;
-  // places of the lane's dims in a head
-  const bool turns = item < turning;
-  int pa = 16 * item, pb = pa + 8;
-  if (turns && !INTERLEAVED) {
-    pa = 8 * item;
-    pb = half + 8 * item;
+  constexpr int V = Chunk<T>::V, ITEMS = D / (2 * V), SLOTS = 32 / ITEMS;  // lanes a head, heads a warp
+  constexpr int U = 4;  // heads of a lane on their way at once
+  const int lane = threadIdx.x & 31, item = lane % ITEMS;
+  // A warp takes one row, or as many as it has heads for.
+  const int slots = a.slots, sub = lane / ITEMS / slots, slot = lane / ITEMS % slots;
+  const int half = a.rot_dim / 2;
+  // The lane's two chunks of a head, neighbours' chunks beside them.  Partners half the
+  // rotation apart: the same place of both halves; else any two.
+  int ca = item, cb = item + ITEMS;
+  bool ta = ca * V < a.rot_dim, tb = cb * V < a.rot_dim;
+  if (!INTERLEAVED) {
+    const int turning = half / V;
+    if (item < turning) {
+      cb = item + turning;
+      ta = tb = true;
+    } else {
+      ca = 2 * turning + (item - turning);
+      cb = ca + (ITEMS - turning);
+      ta = tb = false;
+    }
   }
-  const int64_t rows = static_cast<int64_t>(gridDim.x) * kWarps;
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); t < a.n; t += rows) {
-    float c[8], s[8];
-    if (turns) {
+  const int pa = ca * V, pb = cb * V;
+  const int64_t rows = static_cast<int64_t>(gridDim.x) * kWarps * a.rows_warp;
+  for (int64_t t = (static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * a.rows_warp + sub; t < a.n; t += rows) {
+    float c[V], s[V];  // half a rotation apart: of the pairs; else of a's pairs, then b's
+    if (ta || tb) {
       const int64_t p = a.positions ? a.positions[t] : t;
       if (p >= 0 && p < a.n_pos) {
-        const float4* w = reinterpret_cast<const float4*>(a.cos_sin + p * a.rot_dim + 8 * item);
-        const float4* z = reinterpret_cast<const float4*>(a.cos_sin + p * a.rot_dim + half + 8 * item);
-        const float4 w0 = __ldg(w), w1 = __ldg(w + 1), z0 = __ldg(z), z1 = __ldg(z + 1);
-        c[0] = w0.x, c[1] = w0.y, c[2] = w0.z, c[3] = w0.w, c[4] = w1.x, c[5] = w1.y, c[6] = w1.z, c[7] = w1.w;
-        s[0] = z0.x, s[1] = z0.y, s[2] = z0.z, s[3] = z0.w, s[4] = z1.x, s[5] = z1.y, s[6] = z1.z, s[7] = z1.w;
+        const float* w = a.cos_sin + p * a.rot_dim;
+        if (!INTERLEAVED) {
+          table<V>(w + pa, c);
+          table<V>(w + half + pa, s);
+        } else {
+          if (ta) {
+            table<V / 2>(w + pa / 2, c);
+            table<V / 2>(w + half + pa / 2, s);
+          }
+          if (tb) {
+            table<V / 2>(w + pb / 2, c + V / 2);
+            table<V / 2>(w + half + pb / 2, s + V / 2);
+          }
+        }
         if (a.backward) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) s[i] = -s[i];
+          for (int i = 0; i < V; ++i) s[i] = -s[i];
         }
       } else {  // a position outside the table is no position: the row says so
 #pragma unroll
-        for (int i = 0; i < 8; ++i) c[i] = s[i] = __uint_as_float(0x7fffffffu);
+        for (int i = 0; i < V; ++i) c[i] = s[i] = __uint_as_float(0x7fffffffu);
       }
     }
-    for (int h0 = slot; h0 < a.heads; h0 += SLOTS * U) {
-      Item<T> x[U];
+    for (int h0 = slot; h0 < a.heads; h0 += slots * U) {
+      Chunk<T> x[U], y[U];
       T* out[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int h = h0 + u * SLOTS;
+        const int h = h0 + u * slots;
         out[u] = nullptr;
         if (h >= a.heads) continue;
         int p = 0;
@@ -156,27 +165,55 @@ __global__ void __launch_bounds__(kThreads) rope_apply_kernel(const __grid_const
         const int64_t at = static_cast<int64_t>(h - a.first[p]) * D;
         const T* row = static_cast<const T*>(a.x[p]) + t * a.stride[p] + at;
         out[u] = static_cast<T*>(a.out[p]) + t * a.out_stride[p] + at;
-        x[u].load(row + pa, row + pb);
+        x[u].load(row + pa);
+        y[u].load(row + pb);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (!out[u]) continue;
-        if (turns) {
-          float v[16];
+        if (ta || tb) {
+          float v[V], w[V];
           x[u].get(v);
+          y[u].get(w);
+          if (!INTERLEAVED) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (INTERLEAVED)
-              turn(v[2 * i], v[2 * i + 1], c[i], s[i]);
-            else
-              turn(v[i], v[8 + i], c[i], s[i]);
+            for (int i = 0; i < V; ++i) turn(v[i], w[i], c[i], s[i]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) {
+              if (ta) turn(v[2 * i], v[2 * i + 1], c[i], s[i]);
+              if (tb) turn(w[2 * i], w[2 * i + 1], c[V / 2 + i], s[V / 2 + i]);
+            }
           }
           x[u].put(v);
+          y[u].put(w);
         }
-        x[u].store(out[u] + pa, out[u] + pb);
+        x[u].store(out[u] + pa);
+        y[u].store(out[u] + pb);
       }
     }
   }
+}
+
+// Cosine and sine of an angle given as a fraction of 2^64 of a turn: the nearest quarter
+// turn, and the Taylor polynomials of what is left (pi / 4 at most; the first terms left
+// out are below 2^-30).
+__device__ __forceinline__ void turn_of(uint64_t part, float amplitude, float& c, float& s) {
+  const uint32_t quarter = static_cast<uint32_t>((part + (1ull << 61)) >> 62);
+  const int64_t rest = static_cast<int64_t>(part - (static_cast<uint64_t>(quarter) << 62));
+  const float x = __ll2float_rn(rest) * 3.4061215800304255e-19f /* 2 pi 2^-64 */, z = x * x;
+  float si = fmaf(z, 2.7557319e-6f, -1.9841270e-4f);
+  si = fmaf(z, si, 8.3333333e-3f);
+  si = fmaf(z, si, -1.6666667e-1f);
+  si = fmaf(x * z, si, x);
+  float co = fmaf(z, -2.7557319e-7f, 2.4801587e-5f);
+  co = fmaf(z, co, -1.3888889e-3f);
+  co = fmaf(z, co, 4.1666667e-2f);
+  co = fmaf(z, co, -0.5f);
+  co = fmaf(z, co, 1.f);
+  const float a = quarter & 1 ? si : co, b = quarter & 1 ? co : si;
+  c = (quarter + 1) & 2 ? -amplitude * a : amplitude * a;
+  s = quarter & 2 ? -amplitude * b : amplitude * b;
 }
 
 // A thread: four neighbouring pairs of a position, and kTableRows positions one after
@@ -195,12 +232,7 @@ __global__ void __launch_bounds__(kThreads) rope_table_kernel(const __grid_const
     const uint64_t p = static_cast<uint64_t>(a.first + t);
     float c[4], s[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t part = static_cast<int64_t>(p * f[i]);  // of a turn, in [-2^63, 2^63)
-      sincospif(__ll2float_rn(part) * 1.0842021724855044e-19f /* 2^-63: half turns */, &s[i], &c[i]);
-      c[i] *= a.amplitude;
-      s[i] *= a.amplitude;
-    }
+    for (int i = 0; i < 4; ++i) turn_of(p * f[i], a.amplitude, c[i], s[i]);
     float* row = a.cos_sin + t * a.rot_dim + 4 * q;
     *reinterpret_cast<float4*>(row) = make_float4(c[0], c[1], c[2], c[3]);
     *reinterpret_cast<float4*>(row + a.rot_dim / 2) = make_float4(s[0], s[1], s[2], s[3]);
@@ -224,9 +256,13 @@ int launched(const char* what, std::string* err) {
 
 }  // namespace
 
-int launch_rope_apply(const RopeArgs& a, int32_t dtype, int32_t d, cudaStream_t s, std::string* err) {
-  const int64_t want = (a.n + kWarps - 1) / kWarps;
-  const int grid = static_cast<int>(std::min<int64_t>(want, static_cast<int64_t>(num_sms()) * 32));
+int launch_rope_apply(RopeArgs a, int32_t dtype, int32_t d, cudaStream_t s, std::string* err) {
+  const int slots = 32 / (d / (dtype == PADOC_BF16 ? 16 : 8));
+  a.slots = 1;
+  while (a.slots < slots && a.slots < a.heads) a.slots *= 2;
+  a.rows_warp = slots / a.slots;
+  const int64_t cta = static_cast<int64_t>(kWarps) * a.rows_warp;
+  const int grid = static_cast<int>(std::min<int64_t>((a.n + cta - 1) / cta, static_cast<int64_t>(num_sms()) * 32));
   if (dtype == PADOC_BF16) {
     if (d == 128)
       apply<__nv_bfloat16, 128>(a, grid, s);

@@ -9,6 +9,8 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
+import sys
 from typing import Optional, Sequence
 
 import numpy as np
@@ -104,6 +106,10 @@ class Act(C.Structure):
                 ("kept", C.c_void_p)]
 
 
+# the same two as packed bytes, which cost a tenth to make: two parts, and one act
+_PARTS = struct.Struct("@PqPqi4xPqPqi4x").pack
+_ACT = struct.Struct("@Pqqi4xP").pack
+
 _lib = None
 
 
@@ -180,13 +186,13 @@ def lib() -> C.CDLL:
             "padoc_kv_append_rope": (C.c_int, [vp, i32, p32, p32, p32, C.POINTER(RopeSpec), C.POINTER(KVStep), vp,
                                                C.c_size_t, vp]),
             "padoc_rope_table": (C.c_int, [C.POINTER(RopeScaling), i64, i32, vp, vp]),
-            "padoc_rope_apply": (C.c_int, [C.POINTER(RopeSpec), i32, C.POINTER(RopePart), i32, i32, i64, vp, i32, vp]),
+            "padoc_rope_apply": (C.c_int, [C.POINTER(RopeSpec), i32, vp, i32, i32, i64, vp, i32, vp]),
             "padoc_lm_loss_ws_size": (C.c_int, [i32, i32, i32, i32, C.POINTER(C.c_size_t)]),
             "padoc_lm_loss": (C.c_int, [C.POINTER(LmHead), vp, vp, vp, C.c_size_t, vp]),
             "padoc_lm_loss_bwd": (C.c_int, [C.POINTER(LmHead), vp, vp, vp, vp, vp, C.c_size_t, vp]),
             "padoc_act_bytes": (C.c_int, [i64, i32, C.POINTER(C.c_size_t)]),
-            "padoc_act_keep": (C.c_int, [i32, C.POINTER(Act), vp]),
-            "padoc_act_restore": (C.c_int, [i32, C.POINTER(Act), vp]),
+            "padoc_act_keep": (C.c_int, [i32, vp, vp]),
+            "padoc_act_restore": (C.c_int, [i32, vp, vp]),
             "padoc_tree_attn_varlen_bwd_kept_ws_size": (C.c_int, [vp, i32, i32, i32, C.POINTER(C.c_size_t)]),
             "padoc_tree_attn_varlen_bwd_kept": (C.c_int, [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, f32,
                                                           vp, C.c_size_t, vp]),
@@ -356,11 +362,14 @@ def rope_apply(rope: "Rope", n: int, d: int, q, q_out, Hq: int, k=None, k_out=No
                dtype: int = BF16, backward: bool = False, q_stride: Optional[int] = None, k_stride: Optional[int] = None,
                q_out_stride: Optional[int] = None, k_out_stride: Optional[int] = None, stream=None):
     """padoc_rope_apply on q and, where given, k; strides in elements, dense where None."""
-    row = lambda s, H: H * d if s is None else int(s)  # noqa: E731
-    parts = (RopePart * 2)(RopePart(_ptr(q), row(q_stride, Hq), _ptr(q_out), row(q_out_stride, Hq), Hq),
-                           RopePart(_ptr(k), row(k_stride, Hkv), _ptr(k_out), row(k_out_stride, Hkv), Hkv))
-    _check(lib().padoc_rope_apply(rope.ref, 1 if k is None else 2, parts, dtype, d, int(n), _ptr(positions),
-                                  int(bool(backward)), _stream(stream)))
+    hq, hk = Hq * d, Hkv * d
+    parts = _PARTS(_ptr(q) or 0, hq if q_stride is None else q_stride, _ptr(q_out) or 0,
+                   hq if q_out_stride is None else q_out_stride, Hq, _ptr(k) or 0, hk if k_stride is None else k_stride,
+                   _ptr(k_out) or 0, hk if k_out_stride is None else k_out_stride, Hkv)
+    rc = lib().padoc_rope_apply(rope.ref, 1 if k is None else 2, parts, dtype, d, n, _ptr(positions),
+                                1 if backward else 0, _stream(stream))
+    if rc:
+        _check(rc)
 
 
 class LmLoss:
@@ -374,7 +383,7 @@ class LmLoss:
             raise PadocError(ERR_INVALID, "LmLoss: h [n, D], w [V, D] and targets [n] do not fit together")
         if h.stride(1) != 1 or w.stride(1) != 1 or (n > 1 and targets.stride(0) != 1):
             raise PadocError(ERR_INVALID, "LmLoss: a row's values and the targets must follow one another")
-        if h.element_size() != 2 or w.element_size() != 2 or targets.element_size() != 4:
+        if not (_is_bf16(h) and _is_bf16(w)) or targets.dtype is not sys.modules["torch"].int32:
             raise PadocError(ERR_INVALID, "LmLoss: h and w must be bf16 and the targets int32")
         self.c = LmHead(_ptr(h), h.stride(0) if n > 1 else D, _ptr(w), w.stride(0) if V > 1 else D, _ptr(targets), n, D, V)
         self.ref = C.byref(self.c)
@@ -399,28 +408,40 @@ def act_bytes(n: int, width: int) -> int:
     return b.value
 
 
-def _acts(rows, kept):
+def _is_bf16(x) -> bool:
+    return x.dtype is sys.modules["torch"].bfloat16  # a tensor is there, so torch is
+
+
+def _acts(rows, kept) -> bytes:
+    """The padoc_act array of the tensors and their checkpoints."""
     if len(rows) != len(kept):
         raise PadocError(ERR_INVALID, "act: one checkpoint a tensor is needed")
-    a = (Act * max(len(rows), 1))()
-    for i, (x, b) in enumerate(zip(rows, kept)):
-        if x.dim() != 2 or x.element_size() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
-            raise PadocError(ERR_INVALID, "act: rows must be bf16 [n, width] whose rows are dense")
-        if b.numel() * b.element_size() < act_bytes(*x.shape):
+    out = b""
+    for x, b in zip(rows, kept):
+        if x.dim() != 2 or not _is_bf16(x):
+            raise PadocError(ERR_INVALID, "act: rows must be bf16 [n, width]")
+        (n, width), (step, one) = x.shape, x.stride()
+        if one != 1 and width > 1:
+            raise PadocError(ERR_INVALID, "act: a row's values must follow one another")
+        if b.numel() * b.element_size() < n * width + n * width // 32:
             raise PadocError(ERR_INVALID, "act: a checkpoint is smaller than act_bytes(n, width)")
-        a[i] = Act(_ptr(x), x.stride(0) if x.shape[0] > 1 else x.shape[1], x.shape[0], x.shape[1], _ptr(b))
-    return a
+        out += _ACT(x.data_ptr(), step if n > 1 else width, n, width, b.data_ptr())
+    return out
 
 
 def act_keep(rows, kept, stream=None):
     """padoc_act_keep: bf16 tensors [n, width] into their checkpoints (device
     bytes, act_bytes(n, width) each); one launch for up to eight."""
-    _check(lib().padoc_act_keep(len(rows), _acts(rows, kept), _stream(stream)))
+    rc = lib().padoc_act_keep(len(rows), _acts(rows, kept), _stream(stream))
+    if rc:
+        _check(rc)
 
 
 def act_restore(kept, rows, stream=None):
     """padoc_act_restore: checkpoints back into bf16 tensors [n, width]."""
-    _check(lib().padoc_act_restore(len(rows), _acts(rows, kept), _stream(stream)))
+    rc = lib().padoc_act_restore(len(rows), _acts(rows, kept), _stream(stream))
+    if rc:
+        _check(rc)
 
 
 # ------------------------------------------------------------------ KV pool
