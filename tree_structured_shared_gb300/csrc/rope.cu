@@ -18,7 +18,7 @@
 // Angles: a position and an angle a step are an integer and a fraction of a turn, so a
 // position's fraction is their product modulo 2^64 with the step as a 64-bit binary
 // fraction.  That is exact but for the step's own rounding (2^-53 of it), at any
-// position, without a 64-bit floating operation.
+// position, without a 64-bit floating operation; its upper 32 bits are used.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -100,8 +100,8 @@ __device__ __forceinline__ void table(const float* p, float* x) {
 
 template <class T, int D, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads) rope_apply_kernel(const __grid_constant__ RopeArgs a) {
-  constexpr int V = Chunk<T>::V, ITEMS = D / (2 * V), SLOTS = 32 / ITEMS;  // lanes a head, heads a warp
-  constexpr int U = 4;  // heads of a lane on their way at once
+  constexpr int V = Chunk<T>::V, ITEMS = D / (2 * V);  // lanes a head
+  constexpr int U = sizeof(T) == 2 ? 4 : 2;  // heads of a lane on their way at once
   const int lane = threadIdx.x & 31, item = lane % ITEMS;
   // A warp takes one row, or as many as it has heads for.
   const int slots = a.slots, sub = lane / ITEMS / slots, slot = lane / ITEMS % slots;
@@ -124,6 +124,25 @@ __global__ void __launch_bounds__(kThreads) rope_apply_kernel(const __grid_const
   const int pa = ca * V, pb = cb * V;
   const int64_t rows = static_cast<int64_t>(gridDim.x) * kWarps * a.rows_warp;
   for (int64_t t = (static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * a.rows_warp + sub; t < a.n; t += rows) {
+    Chunk<T> x[U], y[U];
+    T* out[U];
+    auto load = [&](int h0) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int h = h0 + u * slots;
+        out[u] = nullptr;
+        if (h >= a.heads) continue;
+        int p = 0;
+#pragma unroll
+        for (int i = 1; i < kRopeParts; ++i) p += h >= a.first[i];
+        const int64_t at = static_cast<int64_t>(h - a.first[p]) * D;
+        const T* row = static_cast<const T*>(a.x[p]) + t * a.stride[p] + at;
+        out[u] = static_cast<T*>(a.out[p]) + t * a.out_stride[p] + at;
+        x[u].load(row + pa);
+        y[u].load(row + pb);
+      }
+    };
+    load(slot);  // on its way while the position and then the table are
     float c[V], s[V];  // half a rotation apart: of the pairs; else of a's pairs, then b's
     if (ta || tb) {
       const int64_t p = a.positions ? a.positions[t] : t;
@@ -151,23 +170,7 @@ __global__ void __launch_bounds__(kThreads) rope_apply_kernel(const __grid_const
         for (int i = 0; i < V; ++i) c[i] = s[i] = __uint_as_float(0x7fffffffu);
       }
     }
-    for (int h0 = slot; h0 < a.heads; h0 += slots * U) {
-      Chunk<T> x[U], y[U];
-      T* out[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int h = h0 + u * slots;
-        out[u] = nullptr;
-        if (h >= a.heads) continue;
-        int p = 0;
-#pragma unroll
-        for (int i = 1; i < kRopeParts; ++i) p += h >= a.first[i];
-        const int64_t at = static_cast<int64_t>(h - a.first[p]) * D;
-        const T* row = static_cast<const T*>(a.x[p]) + t * a.stride[p] + at;
-        out[u] = static_cast<T*>(a.out[p]) + t * a.out_stride[p] + at;
-        x[u].load(row + pa);
-        y[u].load(row + pb);
-      }
+    for (int h0 = slot; h0 < a.heads;) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (!out[u]) continue;
@@ -191,49 +194,64 @@ __global__ void __launch_bounds__(kThreads) rope_apply_kernel(const __grid_const
         x[u].store(out[u] + pa);
         y[u].store(out[u] + pb);
       }
+      h0 += slots * U;
+      if (h0 < a.heads) load(h0);
     }
   }
 }
 
-// Cosine and sine of an angle given as a fraction of 2^64 of a turn: the nearest quarter
-// turn, and the Taylor polynomials of what is left (pi / 4 at most; the first terms left
-// out are below 2^-30).
-__device__ __forceinline__ void turn_of(uint64_t part, float amplitude, float& c, float& s) {
-  const uint32_t quarter = static_cast<uint32_t>((part + (1ull << 61)) >> 62);
-  const int64_t rest = static_cast<int64_t>(part - (static_cast<uint64_t>(quarter) << 62));
-  const float x = __ll2float_rn(rest) * 3.4061215800304255e-19f /* 2 pi 2^-64 */, z = x * x;
-  float si = fmaf(z, 2.7557319e-6f, -1.9841270e-4f);
-  si = fmaf(z, si, 8.3333333e-3f);
-  si = fmaf(z, si, -1.6666667e-1f);
-  si = fmaf(x * z, si, x);
-  float co = fmaf(z, -2.7557319e-7f, 2.4801587e-5f);
-  co = fmaf(z, co, -1.3888889e-3f);
-  co = fmaf(z, co, 4.1666667e-2f);
-  co = fmaf(z, co, -0.5f);
-  co = fmaf(z, co, 1.f);
-  const float a = quarter & 1 ? si : co, b = quarter & 1 ? co : si;
-  c = (quarter + 1) & 2 ? -amplitude * a : amplitude * a;
-  s = quarter & 2 ? -amplitude * b : amplitude * b;
+// Cosines and sines of two angles given as fractions of 2^32 of a turn: the nearest
+// quarter turn, and the Taylor polynomials of what is left (pi / 4 at most; the first
+// terms left out are below 2^-30).  The angles are off by 2^-32 of a turn, 1.5e-9, at most.
+__device__ __forceinline__ void turns_of(uint32_t p0, uint32_t p1, float amplitude, float* c, float* s) {
+  const uint32_t q0 = (p0 + (1u << 29)) >> 30, q1 = (p1 + (1u << 29)) >> 30;
+  const auto both = [](float v) { return f2pack(v, v); };
+  const uint64_t x = mul2(f2pack(__int2float_rn(static_cast<int32_t>(p0 - (q0 << 30))),
+                                 __int2float_rn(static_cast<int32_t>(p1 - (q1 << 30)))),
+                          both(1.4629180792671596e-9f) /* 2 pi 2^-32 */);
+  const uint64_t z = mul2(x, x);
+  uint64_t si = fma2(z, both(2.7557319e-6f), both(-1.9841270e-4f));
+  si = fma2(z, si, both(8.3333333e-3f));
+  si = fma2(z, si, both(-1.6666667e-1f));
+  si = fma2(mul2(x, z), si, x);
+  uint64_t co = fma2(z, both(-2.7557319e-7f), both(2.4801587e-5f));
+  co = fma2(z, co, both(-1.3888889e-3f));
+  co = fma2(z, co, both(4.1666667e-2f));
+  co = fma2(z, co, both(-0.5f));
+  co = fma2(z, co, both(1.f));
+  float s0, s1, c0, c1;
+  f2unpack(mul2(si, both(amplitude)), s0, s1);
+  f2unpack(mul2(co, both(amplitude)), c0, c1);
+  // quarter turns: (c, s), (-s, c), (-c, -s), (s, -c)
+  const auto sign = [](float v, uint32_t bit) { return __uint_as_float(__float_as_uint(v) ^ (bit << 31)); };
+  c[0] = sign(q0 & 1 ? s0 : c0, (q0 + 1) >> 1 & 1);
+  s[0] = sign(q0 & 1 ? c0 : s0, q0 >> 1 & 1);
+  c[1] = sign(q1 & 1 ? s1 : c1, (q1 + 1) >> 1 & 1);
+  s[1] = sign(q1 & 1 ? c1 : s1, q1 >> 1 & 1);
 }
 
-// A thread: four neighbouring pairs of a position, and kTableRows positions one after
-// another (the steps stay in registers).
-constexpr int kTableRows = 4;
+// A thread: four neighbouring pairs, and every so many positions of its CTA's run (the
+// steps stay in registers).
+constexpr int kTableRun = 128;  // positions of a CTA
 __global__ void __launch_bounds__(kThreads) rope_table_kernel(const __grid_constant__ RopeTableArgs a) {
-  const int per_row = a.rot_dim / 8;  // threads a position
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const int q = static_cast<int>(id % per_row);
-  int64_t t = id / per_row;
-  const int64_t step = (static_cast<int64_t>(gridDim.x) * kThreads) / per_row;  // the grid is whole rows
+  const int per_row = a.rot_dim / 8, rows = kThreads / per_row;  // threads a position, positions at once
+  const int q = threadIdx.x % per_row, r = threadIdx.x / per_row;
+  if (r >= rows) return;
   uint64_t f[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) f[i] = a.turns[4 * q + i];
-  for (; t < a.n_pos; t += step) {
-    const uint64_t p = static_cast<uint64_t>(a.first + t);
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTableRun;
+  const int n = static_cast<int>(min(static_cast<int64_t>(kTableRun), a.n_pos - t0));
+  const uint32_t first = static_cast<uint32_t>(a.first + t0);
+  float* out = a.cos_sin + t0 * a.rot_dim + 4 * q;
+#pragma unroll 4
+  for (int t = r; t < n; t += rows) {
+    const uint64_t p = first + static_cast<uint32_t>(t);
     float c[4], s[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) turn_of(p * f[i], a.amplitude, c[i], s[i]);
-    float* row = a.cos_sin + t * a.rot_dim + 4 * q;
+    for (int i = 0; i < 4; i += 2)
+      turns_of(static_cast<uint32_t>((p * f[i]) >> 32), static_cast<uint32_t>((p * f[i + 1]) >> 32), a.amplitude, c + i, s + i);
+    float* row = out + t * a.rot_dim;
     *reinterpret_cast<float4*>(row) = make_float4(c[0], c[1], c[2], c[3]);
     *reinterpret_cast<float4*>(row + a.rot_dim / 2) = make_float4(s[0], s[1], s[2], s[3]);
   }
@@ -261,8 +279,13 @@ int launch_rope_apply(RopeArgs a, int32_t dtype, int32_t d, cudaStream_t s, std:
   a.slots = 1;
   while (a.slots < slots && a.slots < a.heads) a.slots *= 2;
   a.rows_warp = slots / a.slots;
-  const int64_t cta = static_cast<int64_t>(kWarps) * a.rows_warp;
-  const int grid = static_cast<int>(std::min<int64_t>((a.n + cta - 1) / cta, static_cast<int64_t>(num_sms()) * 32));
+  // A CTA costs its launch: short rows are taken several a warp, as many as come to the
+  // 6 KB of 24 heads of 128 (50003 rows of 1.5 KB: 28 us, with a row a warp 37), unless
+  // that leaves SMs without work.
+  const int64_t row_bytes = static_cast<int64_t>(a.heads) * d * (dtype == PADOC_BF16 ? 2 : 4);
+  const int64_t cta = static_cast<int64_t>(kWarps) * a.rows_warp, want = (a.n + cta - 1) / cta;
+  const int64_t each = std::max<int64_t>(1, 6144 / (row_bytes * a.rows_warp));
+  const int grid = static_cast<int>(std::min<int64_t>(std::max<int64_t>((want + each - 1) / each, std::min<int64_t>(want, 4 * num_sms())), 1 << 20));
   if (dtype == PADOC_BF16) {
     if (d == 128)
       apply<__nv_bfloat16, 128>(a, grid, s);
@@ -278,11 +301,7 @@ int launch_rope_apply(RopeArgs a, int32_t dtype, int32_t d, cudaStream_t s, std:
 }
 
 int launch_rope_table(const RopeTableArgs& a, cudaStream_t s, std::string* err) {
-  // whole positions a grid: per_row divides kThreads * 3 for every rot_dim
-  const int64_t per_row = a.rot_dim / 8;
-  int64_t grid = (a.n_pos * per_row + kThreads * kTableRows - 1) / (kThreads * kTableRows);
-  grid = (grid + 2) / 3 * 3;
-  rope_table_kernel<<<static_cast<int>(std::min<int64_t>(grid, 1 << 20) / 3 * 3), kThreads, 0, s>>>(a);
+  rope_table_kernel<<<static_cast<unsigned>((a.n_pos + kTableRun - 1) / kTableRun), kThreads, 0, s>>>(a);
   return launched("rope_table_kernel", err);
 }
 
