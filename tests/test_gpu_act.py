@@ -172,9 +172,9 @@ def gradients(w, kept, o, lse, d_o, order):
 @pytest.mark.parametrize("order", [padoc.PACK_CANONICAL, padoc.PACK_DOCUMENT])
 @pytest.mark.parametrize("G", [1, 2, 4, 8, 16])
 def test_gradients_are_those_of_the_values(padoc_lib, G, order):
-    """Bit for bit the backward of the values that the checkpoints stand for, up to
-    the row sums' order of addition; and near the oracle, whose o is not rounded to 8
-    bits: its row sums are replaced by those of the checkpoint."""
+    """The backward of the values that the checkpoints stand for, up to the order of
+    additions (row sums; dk and dv where a key tile's queries are cut into parts); and
+    dv, which o does not enter, near the oracle's."""
     import torch
     from tree_structured_shared_gb300 import harness
     w = wl.random_pages(80 + G, n_pages=3, max_prefix=300, max_regions=5, max_layout=20, max_content=150,
@@ -191,14 +191,65 @@ def test_gradients_are_those_of_the_values(padoc_lib, G, order):
     want = b.run()
     torch.cuda.synchronize()
     for g, r, name in zip(grads, want, ("dq", "dk", "dv")):
-        r = r[:T]
-        if name == "dv":
-            assert torch.equal(g, r)
-        else:
-            check_grad(g.float().cpu().numpy(), r.float().cpu().numpy(), "bf16", name)
-    # the oracle at the same q, k, v: d(sum dO O) with o exact; o's 8 bits enter through the row sums alone
+        check_grad(g.float().cpu().numpy(), r[:T].float().cpu().numpy(), "bf16", name)
     ref = tb.tree_backward(q, k, v, d_o, w.pages, order)
     check_grad(grads[2].float().cpu().numpy(), ref[2], "bf16", "dv")
+
+
+def test_many_key_tiles(padoc_lib):
+    """Enough of them that no key tile's queries are cut: dv, which the row sums do not
+    enter, is bit for bit that of the plain backward."""
+    import torch
+    from tree_structured_shared_gb300 import harness
+    w = wl.TreeWorkload("pages", [wl.Page(900, [12] * 5, [130, 7, 64, 200, 1]), wl.Page(640, [], []), wl.Page(0, [3], [90])],
+                        16, 8, 128, "bf16", 1.0, [0, 0, 0])
+    T = w.n_tokens
+    assert -(-T // 128) * 8 > 76
+    q, k, v, kept = kept_workload(w, 2)
+    f = harness.Forward(w, q, k, v)
+    f.run()
+    b = harness.Backward(f, wl.round_bf16(wl.normal_f32(5, (T, 16, 128), 1.0)))
+    o = f.o.flatten(1)[:T]
+    grads, o_back = gradients(w, kept, o, f.lse, b.d_o, padoc.PACK_CANONICAL)
+    f.o[:T] = o_back.view(T, 16, 128)
+    want = b.run()
+    torch.cuda.synchronize()
+    assert torch.equal(grads[2], want[2][:T])
+    for g, r, name in zip(grads, want, ("dq", "dk", "dv")):
+        check_grad(g.float().cpu().numpy(), r[:T].float().cpu().numpy(), "bf16", name)
+
+
+def test_parts_repeat_bit_for_bit_and_in_a_graph(padoc_lib):
+    import torch
+    from tree_structured_shared_gb300 import harness
+    w = wl.random_pages(5, n_pages=2, max_prefix=500, max_regions=5, max_layout=20, max_content=150, Hq=4, Hkv=1,
+                        d=128, dtype="bf16")
+    T = w.n_tokens
+    q, k, v, kept = kept_workload(w, 1)
+    f = harness.Forward(w, q, k, v)
+    f.run()
+    o_kept = buf(f.o.flatten(1)[:T])
+    padoc.act_keep([f.o.flatten(1)[:T]], [o_kept])
+    d_o = torch.randn(T, 4, 128, device="cuda").to(torch.bfloat16)
+    grads = [torch.zeros(T, H, 128, dtype=torch.bfloat16, device="cuda") for H in (4, 1, 1)]
+    size = padoc.tree_attn_varlen_bwd_kept_ws_size(f.desc, 4, 1, 128)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    run = lambda: padoc.tree_attn_varlen_bwd_kept(f.desc, *kept, o_kept, f.lse, d_o, *grads, 4, 1, 128, ws, size)  # noqa: E731
+    run()
+    torch.cuda.synchronize()
+    first = [g.clone() for g in grads]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run()
+    for _ in range(4):
+        for x in grads:
+            x.fill_(7)
+        ws.fill_(0xFF)
+        g.replay()
+        torch.cuda.synchronize()
+        padoc.device_status()
+        for x, y in zip(grads, first):
+            assert torch.equal(x, y)
 
 
 def dense_gradients(w, q, k, v, o, lse, d_o):

@@ -116,6 +116,7 @@ __global__ void __launch_bounds__(kThreads) restore_kernel(const __grid_constant
   const int ti = find(a, blockIdx.x);
   const ActTensor& x = a.t[ti];
   const int64_t i0 = static_cast<int64_t>(blockIdx.x - a.first_block[ti]) * kPiecesCta + threadIdx.x;
+  if (a.zero && blockIdx.x == 0 && threadIdx.x < 2) a.zero[threadIdx.x] = 0;
   const bool sums = ti == a.sums;  // rows is dO, and the row sums of dO * value are wanted
   uint4 c[kUnroll];
   uint8_t e[kUnroll];

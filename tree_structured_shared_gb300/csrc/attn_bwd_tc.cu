@@ -88,6 +88,7 @@ struct DkvParams {
   __nv_bfloat16* dk;
   __nv_bfloat16* dv;
   int32_t* work;  // unit counter, zero at launch
+  float* parts;   // SPLIT: of dv, then of dk: [item][128 keys][Hkv][d] f32
 };
 
 // Both passes draw their units in order from a counter in the workspace as
@@ -218,6 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int32_t* uring = reinterpret_cast<volatile int32_t*>(smem + Q_SM_URING);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // for the split dK/dV pass
   if (threadIdx.x == 0) {
     for (int i = 0; i < QB_N; ++i)
       mbar_init(bar(i), (i == QB_DS_FULL || i == QB_ACC_FREE || i == QB_RD)
@@ -560,6 +562,10 @@ __device__ __forceinline__ bool q_next(const DkvParams& p, QIter& q) {
   return true;
 }
 
+// Few key tiles leave most of the GPU idle, each with all of its queries to walk.  With
+// SPLIT, an item is a part of a key tile's queries (the host cuts them) and leaves its sums
+// in f32; dkv_join_kernel adds the parts up in their order.
+template <bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     bwd_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -959,7 +965,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t v[32];
           tmem_ld32(tmem + lb + col0 + c * 32, v);
           tmem_wait_ld();
-          if (valid) {
+          if (SPLIT && valid) {
+            uint4* dst = reinterpret_cast<uint4*>(
+                p.parts +
+                (((static_cast<int64_t>(part) * p.plan.n_items + u % p.plan.n_items) * kTileKeys + r) * p.Hkv + g) * kHeadDim +
+                wg * 64 + c * 32);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dst[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          } else if (valid) {
             uint4* dst = reinterpret_cast<uint4*>(out + (static_cast<int64_t>(key) * p.Hkv + g) * kHeadDim + wg * 64 +
                                                   c * 32);
 #pragma unroll
@@ -982,6 +995,34 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 0) tmem_dealloc(tmem, 512);
+  // started beside the dQ pass, of which nothing here is needed: what follows on the
+  // stream waits for both
+  if (SPLIT) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// dK and dV of a key tile and kv head from their parts, in their order.
+__global__ void __launch_bounds__(256) dkv_join_kernel(const DkvParams p, const int32_t* __restrict__ first) {
+  const int g = blockIdx.y, lo = first[blockIdx.x], parts = first[blockIdx.x + 1] - lo;
+  const BwdItem it = p.plan.items[lo];
+  const int64_t step = static_cast<int64_t>(kTileKeys) * p.Hkv * kHeadDim;  // from part to part
+  for (int i = blockIdx.z * 256 + threadIdx.x; i < it.k_len * 2 * (kHeadDim / 4); i += gridDim.z * 256) {
+    const int which = i / (kHeadDim / 4) & 1, c = 4 * (i % (kHeadDim / 4)), r = i / (2 * (kHeadDim / 4));
+    const int64_t row = (static_cast<int64_t>(r) * p.Hkv + g) * kHeadDim + c;
+    const float* x = p.parts + (static_cast<int64_t>(which) * p.plan.n_items + lo) * step + row;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int k = 0; k < parts; ++k) {
+      const float4 y = *reinterpret_cast<const float4*>(x + k * step);
+      sum.x += y.x;
+      sum.y += y.y;
+      sum.z += y.z;
+      sum.w += y.w;
+    }
+    const float mul = which ? p.scale : 1.f;
+    const int64_t at = static_cast<int64_t>(it.k_start) * p.Hkv * kHeadDim + row;
+    *reinterpret_cast<uint2*>((which ? p.dk : p.dv) + at) =
+        make_uint2(pack_bf16x2(sum.x * mul, sum.y * mul), pack_bf16x2(sum.z * mul, sum.w * mul));
+  }
 }
 
 int make_map(EncodeTiledFn enc, CUtensorMap* m, const void* ptr, cuuint64_t heads, cuuint64_t T, cuuint32_t rows,
@@ -1017,7 +1058,8 @@ int launch_bwd_tc(const BwdArgs& a, cudaStream_t s, std::string* err) {
   static bool attr = false;
   if (!attr) {
     cudaError_t e = cudaFuncSetAttribute(bwd_dq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDqSmem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(bwd_dkv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDkvSmem);
+    for (auto* k : {bwd_dkv_kernel<false>, bwd_dkv_kernel<true>})
+      if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kDkvSmem);
     if (e != cudaSuccess) {
       *err = std::string("cudaFuncSetAttribute: ") + cudaGetErrorString(e);
       return PADOC_ERR_CUDA;
@@ -1028,7 +1070,7 @@ int launch_bwd_tc(const BwdArgs& a, cudaStream_t s, std::string* err) {
   if (a.fwd.n_items > 0) {
     DqParams p{};
     p.work = a.work + 1;  // the dK/dV pass counts in a.work[0]
-    {
+    if (!a.have_delta) {
       const cudaError_t e = cudaMemsetAsync(p.work, 0, sizeof(int32_t), s);
       if (e != cudaSuccess) {
         *err = std::string("cudaMemsetAsync of the unit counter: ") + cudaGetErrorString(e);
@@ -1051,7 +1093,7 @@ int launch_bwd_tc(const BwdArgs& a, cudaStream_t s, std::string* err) {
   if (a.bwd.n_items > 0) {
     DkvParams p{};
     p.work = a.work;
-    {
+    if (!a.have_delta) {
       // units are drawn from this counter in order
       const cudaError_t e = cudaMemsetAsync(a.work, 0, sizeof(int32_t), s);
       if (e != cudaSuccess) {
@@ -1072,7 +1114,29 @@ int launch_bwd_tc(const BwdArgs& a, cudaStream_t s, std::string* err) {
     p.delta = a.delta;
     p.dk = static_cast<__nv_bfloat16*>(a.dk);
     p.dv = static_cast<__nv_bfloat16*>(a.dv);
-    bwd_dkv_kernel<<<std::min(p.n_units, num_sms()), kThreads, kDkvSmem, s>>>(mq, mdo, mk, mv, p);
+    p.parts = a.parts;
+    if (a.parts) {
+      p.plan = a.split;
+      p.n_units = a.split.n_items * a.Hkv;
+      cudaLaunchConfig_t cfg{};
+      cfg.gridDim = dim3(std::min(p.n_units, num_sms()));
+      cfg.blockDim = dim3(kThreads);
+      cfg.dynamicSmemBytes = kDkvSmem;
+      cfg.stream = s;
+      cudaLaunchAttribute at{};
+      at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      at.val.programmaticStreamSerializationAllowed = 1;
+      cfg.attrs = &at;
+      cfg.numAttrs = a.fwd.n_items > 0 ? 1 : 0;  // beside the dQ pass
+      const cudaError_t e = cudaLaunchKernelEx(&cfg, bwd_dkv_kernel<true>, mq, mdo, mk, mv, p);
+      if (e != cudaSuccess) {
+        *err = std::string("backward kernel launch: ") + cudaGetErrorString(e);
+        return PADOC_ERR_CUDA;
+      }
+      dkv_join_kernel<<<dim3(a.bwd.n_items, a.Hkv, 32), 256, 0, s>>>(p, a.split_first);
+    } else {
+      bwd_dkv_kernel<false><<<std::min(p.n_units, num_sms()), kThreads, kDkvSmem, s>>>(mq, mdo, mk, mv, p);
+    }
   }
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) {

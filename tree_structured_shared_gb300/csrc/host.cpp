@@ -92,6 +92,11 @@ struct DevPlan {
   int32_t n_items = 0;
   BwdItem* bitems = nullptr;
   BwdEntry* bentries = nullptr;
+  // the key tiles' queries in parts (few key tiles only)
+  BwdItem* sitems = nullptr;
+  BwdEntry* sentries = nullptr;
+  int32_t* sfirst = nullptr;
+  int32_t n_sitems = 0;
 };
 
 struct padoc_tree_desc {
@@ -101,6 +106,7 @@ struct padoc_tree_desc {
   std::vector<KVSeg> kvsegs;
   std::vector<BwdItem> bitems;
   std::vector<BwdEntry> bentries;
+  int32_t n_parts[5] = {};  // parts of all key tiles' queries (build_parts), for groups 1, 2, 4, 8, 16
   std::vector<DevPlan> dev;
   ~padoc_tree_desc() {
     for (auto& d : dev) {
@@ -112,6 +118,9 @@ struct padoc_tree_desc {
       cudaFree(d.items);
       cudaFree(d.bitems);
       cudaFree(d.bentries);
+      cudaFree(d.sitems);
+      cudaFree(d.sentries);
+      cudaFree(d.sfirst);
       if (cur >= 0) cudaSetDevice(cur);
     }
   }
@@ -156,6 +165,63 @@ static void build_bwd(padoc_tree_desc* desc) {
     desc->bitems.push_back(it);
     desc->bentries.insert(desc->bentries.end(), per[i].begin(), per[i].end());
   }
+}
+
+// The dK/dV pass from checkpoints cuts the queries of a key tile into parts when its units
+// would not fill half of a GB300's 152 SMs.  A part holds enough query tiles that a kv head
+// comes to kParts of them, and kPartTiles at least: below that the parts' f32 sums cost more
+// than the shorter units save.  (8 query heads on 2 kv heads, a page of 919 tokens: 31 us,
+// whole 87, with 2 tiles a part 39, with 6 34; one of 4549 tokens on 16 query heads: 4 tiles
+// a part 489, 6 419.)
+constexpr int32_t kPartTiles = 4, kParts = 128, kFewUnits = 76;
+static int32_t entry_tiles(const BwdEntry& b, int32_t tile_tokens) {
+  return (b.q_hi - b.q_lo + tile_tokens - 1) / tile_tokens;
+}
+static int32_t item_tiles(const padoc_tree_desc* desc, const BwdItem& it, int32_t tile_tokens) {
+  int32_t n = 0;
+  for (int32_t e = 0; e < it.e_count; ++e) n += entry_tiles(desc->bentries[it.e_first + e], tile_tokens);
+  return n;
+}
+static int32_t part_tiles(const padoc_tree_desc* desc, int32_t tile_tokens) {
+  int64_t all = 0;
+  for (const BwdItem& it : desc->bitems) all += item_tiles(desc, it, tile_tokens);
+  return static_cast<int32_t>(std::max<int64_t>(kPartTiles, (all + kParts - 1) / kParts));
+}
+static int32_t count_parts(const padoc_tree_desc* desc, int32_t tile_tokens) {
+  const int32_t most = part_tiles(desc, tile_tokens);
+  int32_t n = 0;
+  for (const BwdItem& it : desc->bitems) n += (item_tiles(desc, it, tile_tokens) + most - 1) / most;
+  return n;
+}
+static bool few_units(const padoc_tree_desc* desc, int32_t Hkv) {
+  return static_cast<int64_t>(desc->bitems.size()) * Hkv <= kFewUnits;
+}
+// Entries are cut where a query tile ends, so the tiles are those of the whole key tile.
+static void build_parts(const padoc_tree_desc* desc, int32_t tile_tokens, std::vector<BwdItem>* items,
+                        std::vector<BwdEntry>* entries, std::vector<int32_t>* first) {
+  const int32_t most = part_tiles(desc, tile_tokens);
+  for (const BwdItem& it : desc->bitems) {
+    first->push_back(static_cast<int32_t>(items->size()));
+    const int32_t tiles = item_tiles(desc, it, tile_tokens), parts = (tiles + most - 1) / most;
+    const int32_t each = parts ? (tiles + parts - 1) / parts : 0;
+    int32_t left = 0;  // tiles that the open part may still take
+    for (int32_t e = 0; e < it.e_count; ++e) {
+      BwdEntry b = desc->bentries[it.e_first + e];
+      while (b.q_lo < b.q_hi) {
+        if (left == 0) {
+          items->push_back({it.k_start, it.k_len, static_cast<int32_t>(entries->size()), 0});
+          left = each;
+        }
+        BwdEntry part = b;
+        part.q_hi = static_cast<int32_t>(std::min<int64_t>(b.q_hi, b.q_lo + static_cast<int64_t>(left) * tile_tokens));
+        left -= entry_tiles(part, tile_tokens);
+        b.q_lo = part.q_hi;
+        entries->push_back(part);
+        ++items->back().e_count;
+      }
+    }
+  }
+  first->push_back(static_cast<int32_t>(items->size()));
 }
 
 namespace {
@@ -292,6 +358,8 @@ extern "C" int padoc_tree_desc_build(const padoc_tree_spec* spec, padoc_tree_des
     }
     desc->pairs = pairs;
     build_bwd(desc.get());
+    if (few_units(desc.get(), 1))
+      for (int i = 0; i < 5; ++i) desc->n_parts[i] = count_parts(desc.get(), kTileRows >> i);
     d = desc.release();
   });
   *out = d;
@@ -400,12 +468,30 @@ static int upload_desc(padoc_tree_desc* desc, int group, DevPlan** plan_out) {
   if (e == cudaSuccess)
     e = alloc_copy(reinterpret_cast<void**>(&p.bentries), desc->bentries.data(),
                    desc->bentries.size() * sizeof(BwdEntry));
+  if (e == cudaSuccess && few_units(desc, 1)) {
+    std::vector<BwdItem> sitems;
+    std::vector<BwdEntry> sentries;
+    std::vector<int32_t> sfirst;
+    try {
+      build_parts(desc, p.tile_tokens, &sitems, &sentries, &sfirst);
+    } catch (...) {
+      e = cudaErrorMemoryAllocation;
+    }
+    p.n_sitems = static_cast<int32_t>(sitems.size());
+    if (e == cudaSuccess) e = alloc_copy(reinterpret_cast<void**>(&p.sitems), sitems.data(), sitems.size() * sizeof(BwdItem));
+    if (e == cudaSuccess)
+      e = alloc_copy(reinterpret_cast<void**>(&p.sentries), sentries.data(), sentries.size() * sizeof(BwdEntry));
+    if (e == cudaSuccess) e = alloc_copy(reinterpret_cast<void**>(&p.sfirst), sfirst.data(), sfirst.size() * sizeof(int32_t));
+  }
   if (e != cudaSuccess) {
     cudaFree(p.qsegs);
     cudaFree(p.kvsegs);
     cudaFree(p.items);
     cudaFree(p.bitems);
     cudaFree(p.bentries);
+    cudaFree(p.sitems);
+    cudaFree(p.sentries);
+    cudaFree(p.sfirst);
     return cuda_fail(e, "tree descriptor upload");
   }
   desc->dev.push_back(p);
@@ -544,8 +630,16 @@ extern "C" int padoc_tree_attn_varlen_bwd(padoc_tree_desc* desc, const void* q, 
 static size_t kept_rows_bytes(const padoc_tree_desc* desc, int32_t H, int32_t d) {
   return (static_cast<size_t>(desc->T) * H * d * 2 + 255) / 256 * 256;
 }
+// The parts' f32 sums, 128 keys of every kv head each.
+static size_t bwd_parts_bytes(const padoc_tree_desc* desc, int32_t Hq, int32_t Hkv, int32_t d) {
+  if (d != kHeadDim || desc->bitems.empty() || !few_units(desc, Hkv) || !valid_group(Hq / Hkv)) return 0;
+  int i = 0;
+  while (1 << i < Hq / Hkv) ++i;
+  return 2 * sizeof(float) * static_cast<size_t>(desc->n_parts[i]) * kTileKeys * Hkv * d;
+}
 static size_t bwd_kept_ws_bytes(const padoc_tree_desc* desc, int32_t Hq, int32_t Hkv, int32_t d) {
-  return bwd_ws_bytes(desc, Hq) + kept_rows_bytes(desc, Hq, d) + 2 * kept_rows_bytes(desc, Hkv, d);
+  return bwd_ws_bytes(desc, Hq) + kept_rows_bytes(desc, Hq, d) + 2 * kept_rows_bytes(desc, Hkv, d) +
+         bwd_parts_bytes(desc, Hq, Hkv, d);
 }
 
 extern "C" int padoc_tree_attn_varlen_bwd_kept_ws_size(const padoc_tree_desc* desc, int32_t Hq, int32_t Hkv, int32_t d,
@@ -596,6 +690,7 @@ extern "C" int padoc_tree_attn_varlen_bwd_kept(padoc_tree_desc* desc, const void
   r.T = desc->T;
   r.heads = Hq;
   r.head_pieces = d / 16;
+  r.zero = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + bwd_delta_bytes(desc, Hq));
   std::string err;
   // the descriptor's device copy first: its upload may fail, and nothing has run by then
   DevPlan* plan = nullptr;
@@ -617,6 +712,11 @@ extern "C" int padoc_tree_attn_varlen_bwd_kept(padoc_tree_desc* desc, const void
   a.Hkv = Hkv;
   a.d = d;
   a.have_delta = true;
+  if (bwd_parts_bytes(desc, Hq, Hkv, d) > 0) {
+    a.split = {plan->sitems, plan->sentries, plan->n_sitems};
+    a.split_first = plan->sfirst;
+    a.parts = reinterpret_cast<float*>(at + kept_rows_bytes(desc, Hq, d) + 2 * kept_rows_bytes(desc, Hkv, d));
+  }
   return run_bwd(desc, a, PADOC_BF16, scale, ws, what, reinterpret_cast<cudaStream_t>(stream));
 }
 

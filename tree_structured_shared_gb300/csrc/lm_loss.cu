@@ -57,25 +57,34 @@ using namespace ptx;
 constexpr int kThreads = 320;
 constexpr int kEpiWarps = 8;
 constexpr int kProducerWarp = 8, kMmaWarp = 9;
-constexpr int kStages = 6;
 constexpr int kOperand = 16384;  // 128 rows of 64 k, or 64 k of 128, bf16
-constexpr int kStage = 2 * kOperand;
+// A ring of stages, A then B.  With at most 32 rows A is 4 KB, in the first CTA alone: the
+// product reads on into B for the other rows of the tile, which nothing looks at, and the
+// ring holds nearly twice the words.
+template <bool FEW>
+struct Ring {
+  static constexpr int kA = FEW ? 4096 : kOperand, kStage = kA + kOperand, kStages = FEW ? 11 : 6;
+  static constexpr int kBytes = FEW ? kA + 2 * kOperand : 2 * kStage;  // of both CTAs
+};
+constexpr int kMaxStages = 11, kFewRows = 32;
 constexpr int kURing = 4;
 constexpr int kOut = 4096;  // an epilogue warp's 32 rows of 64 values on their way out
-constexpr int SM_OUT = kStages * kStage;
+constexpr int SM_OUT = 6 * 2 * kOperand;
 constexpr int SM_BAR = SM_OUT + kEpiWarps * kOut;
+static_assert(Ring<true>::kStages * Ring<true>::kStage <= SM_BAR, "the ring of few rows, with no rows on their way out");
+static_assert(Ring<false>::kStages * Ring<false>::kStage <= SM_OUT, "ring");
 enum {
   B_FULL = 0,                   // +stage: both CTAs' copies have landed (first CTA)
-  B_EMPTY = B_FULL + kStages,   // +stage: the stage's products have run
-  B_ACC_FULL = B_EMPTY + kStages,   // +accumulator (2)
+  B_EMPTY = B_FULL + kMaxStages,   // +stage: the stage's products have run
+  B_ACC_FULL = B_EMPTY + kMaxStages,   // +accumulator (2)
   B_ACC_FREE = B_ACC_FULL + 2,      // +accumulator (2), count 16: both CTAs' epilogues (first CTA)
   B_U_FULL = B_ACC_FREE + 2,        // +slot: the ring's slot holds a unit
   B_U_FREE = B_U_FULL + kURing,     // +slot, count 18: all readers have it (first CTA)
   B_DRAIN = B_U_FREE + kURing,
   N_BARS
 };
-constexpr int SM_UNIT = SM_BAR + N_BARS * 8;     // unit ring
-constexpr int SM_MISC = SM_UNIT + kURing * 4;    // TMEM address, abort flag
+constexpr int SM_UNIT = (SM_BAR + N_BARS * 8 + 15) / 16 * 16;  // unit ring
+constexpr int SM_MISC = SM_UNIT + kURing * 32;   // TMEM address, abort flag
 constexpr int kSmemBytes = SM_MISC + 8 + 1024;   // and room to align the ring
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -98,8 +107,16 @@ __device__ __forceinline__ void cluster_sync() {
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {  // a shared::cluster address
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+__device__ __forceinline__ void st_cluster_v4(uint32_t addr, int a, int b, int c, int d) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ int4 ld_shared_v4(uint32_t addr) {
+  int4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
 }
 __device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
   uint32_t ok;
@@ -166,7 +183,7 @@ __device__ __forceinline__ void store_read() { asm volatile("cp.async.bulk.wait_
 __device__ __forceinline__ void store_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // ---------------------------------------------------------------- units
-enum { REC = 0, DH = 1, DW = 2 };
+enum { END = -1, REC = 0, DH = 1, DW = 2 };
 struct Unit {
   int kind, m, n, tiles, k0, nkb, part;  // tile row, first tile column and their number; k blocks from k0
 };
@@ -189,6 +206,10 @@ __device__ __forceinline__ Unit unit_of(const LmArgs& a, const Counts& c, int u)
   x.tiles = 1;
   x.k0 = 0;
   x.part = 0;
+  if (u >= c.all) {
+    x.kind = END;
+    return x;
+  }
   if (u < c.dh) {  // the dims of a row tile side by side: they share G
     x.kind = DH;
     x.n = u % a.d_tiles;
@@ -216,6 +237,16 @@ __device__ __forceinline__ Unit unit_of(const LmArgs& a, const Counts& c, int u)
   x.tiles = min(a.run, (a.rec_cols + 255) / 256 - x.n);
   x.nkb = a.k_blocks;
   return x;
+}
+
+// A unit goes to the roles worked out: its divisions would stall each of them.
+__device__ __forceinline__ void publish(uint32_t slot, const Unit& x) {  // a shared::cluster address
+  st_cluster_v4(slot, x.kind, x.m, x.n, x.tiles);
+  st_cluster_v4(slot + 16, x.k0, x.nkb, x.part, 0);
+}
+__device__ __forceinline__ Unit taken(uint32_t slot) {
+  const int4 a = ld_shared_v4(slot), b = ld_shared_v4(slot + 16);
+  return Unit{a.x, a.y, a.z, a.w, b.x, b.y, b.z};
 }
 
 __device__ __forceinline__ void give_up(volatile int* abort, unsigned site) {
@@ -309,19 +340,20 @@ __device__ __forceinline__ void gradient_tile(const uint32_t (&v)[2][64], int wo
   }
 }
 
-template <bool FWD>
+template <bool FWD, bool FEW>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     lm_kernel(const __grid_constant__ LmArgs a, const __grid_constant__ CUtensorMap m_hk,
               const __grid_constant__ CUtensorMap m_wk, const __grid_constant__ CUtensorMap m_hm,
               const __grid_constant__ CUtensorMap m_wm, const __grid_constant__ CUtensorMap m_gk,
               const __grid_constant__ CUtensorMap m_gm, const __grid_constant__ CUtensorMap m_wo) {
+  using R = Ring<FEW>;
+  constexpr int kStages = R::kStages, kStage = R::kStage;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* sptr = smem_raw + (sbase - smem_u32(smem_raw));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cta_rank();
   auto bar = [&](int i) { return sbase + SM_BAR + 8u * i; };
-  volatile int32_t* uring = reinterpret_cast<volatile int32_t*>(sptr + SM_UNIT);
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(sptr + SM_MISC);
   volatile int* abort = reinterpret_cast<volatile int*>(sptr + SM_MISC + 4);
 
@@ -350,32 +382,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       const uint32_t full0 = in_cta(bar(B_FULL), 0);
       uint32_t k = 0, uk = 0;  // stages and units so far
-      int next = rank == 0 ? atomicAdd(a.counter, 1) : 0;
+      int next = blockIdx.x / 2;  // the first without a draw
       while (true) {
-        int u;
+        Unit x;
         const int slot = uk % kURing;
         if (rank == 0) {
-          u = next < c.all ? next : -1;
+          x = unit_of(a, c, next);
           if (!wait_cluster(bar(B_U_FREE + slot), ((uk / kURing) & 1) ^ 1, abort)) {
             give_up(abort, 1u);
             break;
           }
           for (uint32_t r = 0; r < 2; ++r) {
-            st_cluster(in_cta(sbase + SM_UNIT + 4 * slot, r), static_cast<uint32_t>(u));
+            publish(in_cta(sbase + SM_UNIT + 32 * slot, r), x);
             arrive_cluster(in_cta(bar(B_U_FULL + slot), r));
           }
-          if (u >= 0) next = atomicAdd(a.counter, 1);  // needed when this unit's copies are issued
+          if (x.kind != END) next = gridDim.x / 2 + atomicAdd(a.counter, 1);  // needed when this unit's copies are issued
         } else {
           if (!wait_cluster(bar(B_U_FULL + slot), (uk / kURing) & 1, abort)) {
             give_up(abort, 2u);
             break;
           }
-          u = uring[slot];
+          x = taken(sbase + SM_UNIT + 32 * slot);
           arrive_cluster(in_cta(bar(B_U_FREE + slot), 0));
         }
         ++uk;
-        if (u < 0) break;
-        const Unit x = unit_of(a, c, u);
+        if (x.kind == END) break;
         bool ok = true;
         for (int t = 0; t < x.tiles && ok; ++t) {
           for (int j = 0; j < x.nkb; ++j, ++k) {
@@ -385,11 +416,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               ok = false;
               break;
             }
-            if (rank == 0) mbar_arrive_expect_tx(bar(B_FULL + s), 2 * kStage);
-            const uint32_t sa = sbase + s * kStage, sb = sa + kOperand, full = full0 + 8u * s;
+            if (rank == 0) mbar_arrive_expect_tx(bar(B_FULL + s), R::kBytes);
+            const uint32_t sa = sbase + s * kStage, sb = sa + R::kA, full = full0 + 8u * s;
             const int kk = (x.k0 + j) * 64;
             if (x.kind == REC) {
-              tma_pair_2d(sa, &m_hk, full, kk, x.m * 256 + 128 * rank);
+              if (!FEW || rank == 0) tma_pair_2d(sa, &m_hk, full, kk, x.m * 256 + 128 * rank);
               tma_pair_2d(sb, &m_wk, full, kk, a.rec_v0 + (x.n + t) * 256 + 128 * rank);
             } else if (!FWD && x.kind == DH) {
               tma_pair_2d(sa, &m_gk, full, kk, x.m * 256 + 128 * rank);
@@ -417,17 +448,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           give_up(abort, 8u);
           break;
         }
-        const int u = uring[slot];
+        const Unit x = taken(sbase + SM_UNIT + 32 * slot);
         arrive_cluster(in_cta(bar(B_U_FREE + slot), 0));
         ++uk;
-        if (u < 0) break;
-        const Unit x = unit_of(a, c, u);
+        if (x.kind == END) break;
         const bool a_mn = x.kind == DW, b_mn = x.kind != REC;
         const uint32_t idesc = idesc_bf16_f32(256, 256, a_mn, b_mn);
         // K-major steps 16 k by 32 bytes of a row; MN-major by 16 rows of 128 bytes, with
         // the operand's second 64 columns 8 KB further on
         const uint64_t da = sdesc_sw128(sbase, a_mn ? kOperand / 2 : 16, 1024);
-        const uint64_t db = sdesc_sw128(sbase + kOperand, b_mn ? kOperand / 2 : 16, 1024);
+        const uint64_t db = sdesc_sw128(sbase + R::kA, b_mn ? kOperand / 2 : 16, 1024);
         const uint32_t step_a = (a_mn ? 2048 : 32) >> 4, step_b = (b_mn ? 2048 : 32) >> 4;
         for (int t = 0; t < x.tiles && ok; ++t, ++tile) {
           const int acc = tile & 1;
@@ -476,12 +506,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         give_up(abort, 64u);
         break;
       }
-      const int u = uring[slot];
+      const Unit x = taken(sbase + SM_UNIT + 32 * slot);
       __syncwarp();
       if (lane == 0) arrive_cluster(in_cta(bar(B_U_FREE + slot), 0));
       ++uk;
-      if (u < 0) break;
-      const Unit x = unit_of(a, c, u);
+      if (x.kind == END) break;
       const int row = x.m * 256 + r_in;
       const bool has_row = row < c.rows;
       int target = -1;
@@ -791,15 +820,15 @@ int launch_after(void (*kernel)(P...), unsigned grid, int threads, int smem, cud
 
 enum { M_HK, M_WK, M_HM, M_WM, M_GK, M_GM, M_WO, N_MAPS };
 
-template <bool FWD>
+template <bool FWD, bool FEW>
 int launch_gemm(const LmArgs& a, const CUtensorMap* m, cudaStream_t s, std::string* err) {
   // an attribute of the current device's copy of the kernel
-  const cudaError_t e = cudaFuncSetAttribute(lm_kernel<FWD>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  const cudaError_t e = cudaFuncSetAttribute(lm_kernel<FWD, FEW>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) {
     *err = std::string("cudaFuncSetAttribute: ") + cudaGetErrorString(e);
     return PADOC_ERR_CUDA;
   }
-  return launch_after(lm_kernel<FWD>, num_sms() / 2 * 2, kThreads, kSmemBytes, s, "lm_kernel", err, a, m[M_HK], m[M_WK],
+  return launch_after(lm_kernel<FWD, FEW>, num_sms() / 2 * 2, kThreads, kSmemBytes, s, "lm_kernel", err, a, m[M_HK], m[M_WK],
                       m[M_HM], m[M_WM], m[M_GK], m[M_GM], m[M_WO]);
 }
 
@@ -902,7 +931,8 @@ int launch_lm_loss(const LmCall& l, void* ws_, cudaStream_t s, std::string* err)
   EncodeTiledFn enc = get_encode_fn(err);
   if (!enc) return PADOC_ERR_CUDA;
   CUtensorMap m[N_MAPS]{};
-  int rc = make_map(enc, &m[M_HK], ws + p.hc, l.D, p.n_pad, l.D, 128, err);
+  const bool few = l.n <= kFewRows;
+  int rc = make_map(enc, &m[M_HK], ws + p.hc, l.D, p.n_pad, l.D, few ? kFewRows : 128, err);
   if (!rc) rc = make_map(enc, &m[M_WK], l.w, l.D, l.V, l.w_stride, 128, err);
   if (rc) return rc;
   rc = launch_rows(l, p, ws, false, s, err);
@@ -923,7 +953,7 @@ int launch_lm_loss(const LmCall& l, void* ws_, cudaStream_t s, std::string* err)
   a.part = reinterpret_cast<float2*>(ws + p.part);
   a.part_ld = p.parts;
   a.picked = reinterpret_cast<float*>(ws + p.picked);
-  rc = launch_gemm<true>(a, m, s, err);
+  rc = few ? launch_gemm<true, true>(a, m, s, err) : launch_gemm<true, false>(a, m, s, err);
   if (rc) return rc;
   const bool many = p.parts > 256;
   return launch_after(many ? lm_join_kernel<kJoinThreads> : lm_join_kernel<32>,
@@ -987,7 +1017,7 @@ int launch_lm_loss_bwd(const LmCall& l, void* ws_, cudaStream_t s, std::string* 
     a.g_out = reinterpret_cast<__nv_bfloat16*>(ws + p.g + (i < p.pieces && i & 1 ? p.g_bytes : 0));
     m[M_GK] = gk[from];
     m[M_GM] = gm[from];
-    rc = launch_gemm<false>(a, m, s, err);
+    rc = launch_gemm<false, false>(a, m, s, err);
     if (rc) return rc;
   }
   if (l.dh && p.splits > 1) {

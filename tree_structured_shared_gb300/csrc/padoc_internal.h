@@ -88,7 +88,12 @@ struct BwdArgs {
   void* dv;
   float* delta;       // workspace [Hq, T]: rowsum(dO * O)
   int32_t* work;      // workspace: unit counter of the dK/dV pass (zeroed by its launcher)
-  bool have_delta = false;  // the row sums are in delta already
+  bool have_delta = false;  // the row sums are in delta already, and the unit counters are zero
+  // parts of the key tiles' queries, the first part of each tile (and the end), and room
+  // for their sums: null where the tiles are not cut
+  BwdPlan split{};
+  const int32_t* split_first = nullptr;
+  float* parts = nullptr;
   int64_t T;
   int32_t Hq, Hkv, d;
   float scale;
@@ -271,6 +276,7 @@ struct ActArgs {
   float* delta;  // [heads][T]
   int64_t T;
   uint32_t heads, head_pieces;
+  int32_t* zero;  // two counters that restore_kernel zeroes, or null
 };
 
 // ---------------------------------------------------------------- cross entropy
