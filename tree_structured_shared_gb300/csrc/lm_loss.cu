@@ -58,25 +58,16 @@ constexpr int kThreads = 320;
 constexpr int kEpiWarps = 8;
 constexpr int kProducerWarp = 8, kMmaWarp = 9;
 constexpr int kOperand = 16384;  // 128 rows of 64 k, or 64 k of 128, bf16
-// A ring of stages, A then B.  With at most 32 rows A is 4 KB, in the first CTA alone: the
-// product reads on into B for the other rows of the tile, which nothing looks at, and the
-// ring holds nearly twice the words.
-template <bool FEW>
-struct Ring {
-  static constexpr int kA = FEW ? 4096 : kOperand, kStage = kA + kOperand, kStages = FEW ? 11 : 6;
-  static constexpr int kBytes = FEW ? kA + 2 * kOperand : 2 * kStage;  // of both CTAs
-};
-constexpr int kMaxStages = 11, kFewRows = 32;
+constexpr int kStages = 6;
+constexpr int kStage = 2 * kOperand;  // A, then B
 constexpr int kURing = 4;
 constexpr int kOut = 4096;  // an epilogue warp's 32 rows of 64 values on their way out
-constexpr int SM_OUT = 6 * 2 * kOperand;
+constexpr int SM_OUT = kStages * kStage;
 constexpr int SM_BAR = SM_OUT + kEpiWarps * kOut;
-static_assert(Ring<true>::kStages * Ring<true>::kStage <= SM_BAR, "the ring of few rows, with no rows on their way out");
-static_assert(Ring<false>::kStages * Ring<false>::kStage <= SM_OUT, "ring");
 enum {
   B_FULL = 0,                   // +stage: both CTAs' copies have landed (first CTA)
-  B_EMPTY = B_FULL + kMaxStages,   // +stage: the stage's products have run
-  B_ACC_FULL = B_EMPTY + kMaxStages,   // +accumulator (2)
+  B_EMPTY = B_FULL + kStages,   // +stage: the stage's products have run
+  B_ACC_FULL = B_EMPTY + kStages,   // +accumulator (2)
   B_ACC_FREE = B_ACC_FULL + 2,      // +accumulator (2), count 16: both CTAs' epilogues (first CTA)
   B_U_FULL = B_ACC_FREE + 2,        // +slot: the ring's slot holds a unit
   B_U_FREE = B_U_FULL + kURing,     // +slot, count 18: all readers have it (first CTA)
@@ -340,14 +331,12 @@ __device__ __forceinline__ void gradient_tile(const uint32_t (&v)[2][64], int wo
   }
 }
 
-template <bool FWD, bool FEW>
+template <bool FWD>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     lm_kernel(const __grid_constant__ LmArgs a, const __grid_constant__ CUtensorMap m_hk,
               const __grid_constant__ CUtensorMap m_wk, const __grid_constant__ CUtensorMap m_hm,
               const __grid_constant__ CUtensorMap m_wm, const __grid_constant__ CUtensorMap m_gk,
               const __grid_constant__ CUtensorMap m_gm, const __grid_constant__ CUtensorMap m_wo) {
-  using R = Ring<FEW>;
-  constexpr int kStages = R::kStages, kStage = R::kStage;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* sptr = smem_raw + (sbase - smem_u32(smem_raw));
@@ -416,11 +405,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               ok = false;
               break;
             }
-            if (rank == 0) mbar_arrive_expect_tx(bar(B_FULL + s), R::kBytes);
-            const uint32_t sa = sbase + s * kStage, sb = sa + R::kA, full = full0 + 8u * s;
+            if (rank == 0) mbar_arrive_expect_tx(bar(B_FULL + s), 2 * kStage);
+            const uint32_t sa = sbase + s * kStage, sb = sa + kOperand, full = full0 + 8u * s;
             const int kk = (x.k0 + j) * 64;
             if (x.kind == REC) {
-              if (!FEW || rank == 0) tma_pair_2d(sa, &m_hk, full, kk, x.m * 256 + 128 * rank);
+              tma_pair_2d(sa, &m_hk, full, kk, x.m * 256 + 128 * rank);
               tma_pair_2d(sb, &m_wk, full, kk, a.rec_v0 + (x.n + t) * 256 + 128 * rank);
             } else if (!FWD && x.kind == DH) {
               tma_pair_2d(sa, &m_gk, full, kk, x.m * 256 + 128 * rank);
@@ -457,7 +446,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // K-major steps 16 k by 32 bytes of a row; MN-major by 16 rows of 128 bytes, with
         // the operand's second 64 columns 8 KB further on
         const uint64_t da = sdesc_sw128(sbase, a_mn ? kOperand / 2 : 16, 1024);
-        const uint64_t db = sdesc_sw128(sbase + R::kA, b_mn ? kOperand / 2 : 16, 1024);
+        const uint64_t db = sdesc_sw128(sbase + kOperand, b_mn ? kOperand / 2 : 16, 1024);
         const uint32_t step_a = (a_mn ? 2048 : 32) >> 4, step_b = (b_mn ? 2048 : 32) >> 4;
         for (int t = 0; t < x.tiles && ok; ++t, ++tile) {
           const int acc = tile & 1;
@@ -820,15 +809,15 @@ int launch_after(void (*kernel)(P...), unsigned grid, int threads, int smem, cud
 
 enum { M_HK, M_WK, M_HM, M_WM, M_GK, M_GM, M_WO, N_MAPS };
 
-template <bool FWD, bool FEW>
+template <bool FWD>
 int launch_gemm(const LmArgs& a, const CUtensorMap* m, cudaStream_t s, std::string* err) {
   // an attribute of the current device's copy of the kernel
-  const cudaError_t e = cudaFuncSetAttribute(lm_kernel<FWD, FEW>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  const cudaError_t e = cudaFuncSetAttribute(lm_kernel<FWD>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) {
     *err = std::string("cudaFuncSetAttribute: ") + cudaGetErrorString(e);
     return PADOC_ERR_CUDA;
   }
-  return launch_after(lm_kernel<FWD, FEW>, num_sms() / 2 * 2, kThreads, kSmemBytes, s, "lm_kernel", err, a, m[M_HK], m[M_WK],
+  return launch_after(lm_kernel<FWD>, num_sms() / 2 * 2, kThreads, kSmemBytes, s, "lm_kernel", err, a, m[M_HK], m[M_WK],
                       m[M_HM], m[M_WM], m[M_GK], m[M_GM], m[M_WO]);
 }
 
@@ -931,8 +920,7 @@ int launch_lm_loss(const LmCall& l, void* ws_, cudaStream_t s, std::string* err)
   EncodeTiledFn enc = get_encode_fn(err);
   if (!enc) return PADOC_ERR_CUDA;
   CUtensorMap m[N_MAPS]{};
-  const bool few = l.n <= kFewRows;
-  int rc = make_map(enc, &m[M_HK], ws + p.hc, l.D, p.n_pad, l.D, few ? kFewRows : 128, err);
+  int rc = make_map(enc, &m[M_HK], ws + p.hc, l.D, p.n_pad, l.D, 128, err);
   if (!rc) rc = make_map(enc, &m[M_WK], l.w, l.D, l.V, l.w_stride, 128, err);
   if (rc) return rc;
   rc = launch_rows(l, p, ws, false, s, err);
@@ -953,7 +941,7 @@ int launch_lm_loss(const LmCall& l, void* ws_, cudaStream_t s, std::string* err)
   a.part = reinterpret_cast<float2*>(ws + p.part);
   a.part_ld = p.parts;
   a.picked = reinterpret_cast<float*>(ws + p.picked);
-  rc = few ? launch_gemm<true, true>(a, m, s, err) : launch_gemm<true, false>(a, m, s, err);
+  rc = launch_gemm<true>(a, m, s, err);
   if (rc) return rc;
   const bool many = p.parts > 256;
   return launch_after(many ? lm_join_kernel<kJoinThreads> : lm_join_kernel<32>,
@@ -1017,7 +1005,7 @@ int launch_lm_loss_bwd(const LmCall& l, void* ws_, cudaStream_t s, std::string* 
     a.g_out = reinterpret_cast<__nv_bfloat16*>(ws + p.g + (i < p.pieces && i & 1 ? p.g_bytes : 0));
     m[M_GK] = gk[from];
     m[M_GM] = gm[from];
-    rc = launch_gemm<false, false>(a, m, s, err);
+    rc = launch_gemm<false>(a, m, s, err);
     if (rc) return rc;
   }
   if (l.dh && p.splits > 1) {
