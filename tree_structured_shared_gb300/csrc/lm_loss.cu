@@ -25,9 +25,9 @@
 // units first, the short ones fill what is left, so no launch ends in a half-empty wave.
 // G lives in two buffers of a piece each.
 //
-// Roles of a CTA (320 threads): warps 0-7 epilogue (TMEM lanes 32 (w % 4), columns
-// 128 (w / 4) of the tile), warp 8 TMA producer (the pair's first CTA also draws the
-// units), warp 9 of the first CTA issues the products.  Shared memory: a ring of six
+// Roles of a CTA (352 threads): warps 0-7 epilogue (TMEM lanes 32 (w % 4), columns
+// 128 (w / 4) of the tile), warp 8 TMA producer; of the pair's first CTA, warp 9 issues
+// the products and warp 10 draws the units.  Shared memory: a ring of six
 // stages of 64 k (A 128 rows, B 128 rows, 16 KB each).  TMEM: two accumulators.
 // Barriers that both CTAs use live in the first: a stage is full when both CTAs' copies
 // are in; an accumulator is free when both have read it.  The commit of a stage's
@@ -54,9 +54,10 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 352;
 constexpr int kEpiWarps = 8;
-constexpr int kProducerWarp = 8, kMmaWarp = 9;
+constexpr int kProducerWarp = 8, kMmaWarp = 9, kDrawWarp = 10;
+constexpr int kLongUnit = 32;  // stages; see the drawing warp
 constexpr int kOperand = 16384;  // 128 rows of 64 k, or 64 k of 128, bf16
 constexpr int kStages = 6;
 constexpr int kStage = 2 * kOperand;  // A, then B
@@ -70,16 +71,16 @@ enum {
   B_ACC_FULL = B_EMPTY + kStages,   // +accumulator (2)
   B_ACC_FREE = B_ACC_FULL + 2,      // +accumulator (2), count 16: both CTAs' epilogues (first CTA)
   B_U_FULL = B_ACC_FREE + 2,        // +slot: the ring's slot holds a unit
-  B_U_FREE = B_U_FULL + kURing,     // +slot, count 18: all readers have it (first CTA)
+  B_U_FREE = B_U_FULL + kURing,     // +slot, count 19: all readers have it (first CTA)
   B_DRAIN = B_U_FREE + kURing,
   N_BARS
 };
 constexpr int SM_UNIT = (SM_BAR + N_BARS * 8 + 15) / 16 * 16;  // unit ring
-constexpr int SM_MISC = SM_UNIT + kURing * 32;   // TMEM address, abort flag
-constexpr int kSmemBytes = SM_MISC + 8 + 1024;   // and room to align the ring
+constexpr int SM_MISC = SM_UNIT + kURing * 32;   // TMEM address, abort flag, units that the producer has begun
+constexpr int kSmemBytes = SM_MISC + 16 + 1024;   // and room to align the ring
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr int kUReaders = 1 + 2 * kEpiWarps + 1;  // the issuer, both epilogues, the second CTA's producer
+constexpr int kUReaders = 1 + 2 * kEpiWarps + 2;  // the issuer, both epilogues and producers
 
 // ---------------------------------------------------------------- pairs of CTAs
 __device__ __forceinline__ uint32_t cta_rank() {
@@ -95,7 +96,14 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void arrive_cluster(uint32_t bar) {  // a shared::cluster address
+// Arrivals at a shared::cluster address.  The first says that a slot or accumulator has
+// been read; it orders nothing beyond this CTA, so it does not wait for the caller's stores
+// to global memory (which a release at cluster scope does, about a microsecond a time).
+__device__ __forceinline__ void arrive_read(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// What the caller wrote to either CTA's shared memory comes before it.
+__device__ __forceinline__ void arrive_written(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void st_cluster_v4(uint32_t addr, int a, int b, int c, int d) {
@@ -262,14 +270,6 @@ __device__ __forceinline__ void reduce_tile(uint32_t (&v)[2][64], int word, int 
     for (int i = 0; i < 128; ++i)
       if (word + i >= V) v[i >> 6][i & 63] = 0xff800000u;
   }
-  const int hit = target - word;
-  if (hit >= 0 && hit < 128) {
-    float x = 0.f;
-#pragma unroll
-    for (int i = 0; i < 128; ++i)
-      if (hit == i) x = __uint_as_float(v[i >> 6][i & 63]);
-    *picked = x;
-  }
   float m[4] = {top, top, top, top};
 #pragma unroll
   for (int i = 0; i < 64; ++i)
@@ -292,6 +292,15 @@ __device__ __forceinline__ void reduce_tile(uint32_t (&v)[2][64], int word, int 
   f2unpack(add2(add2(s[0], s[1]), add2(s[2], s[3])), lo, hi);
   sum = fmaf(sum, fast_exp2(fmaf(top, kLog2e, -ref)), lo + hi);
   top = t;
+  // last, so that the target has arrived
+  const int hit = target - word;
+  if (hit >= 0 && hit < 128) {
+    float x = 0.f;
+#pragma unroll
+    for (int i = 0; i < 128; ++i)
+      if (hit == i) x = __uint_as_float(v[i >> 6][i & 63]);
+    *picked = x;
+  }
 }
 
 // G of a row's 128 words from `word`, bf16, to `out`; zero from word V on.
@@ -345,6 +354,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   auto bar = [&](int i) { return sbase + SM_BAR + 8u * i; };
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(sptr + SM_MISC);
   volatile int* abort = reinterpret_cast<volatile int*>(sptr + SM_MISC + 4);
+  volatile uint32_t* begun = reinterpret_cast<volatile uint32_t*>(sptr + SM_MISC + 8);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < N_BARS; ++i) {
@@ -354,6 +364,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(bar(i), count);
     }
     *abort = 0;
+    *begun = 0;
     fence_mbar_init();
   }
   if (warp == kMmaWarp)
@@ -371,30 +382,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       const uint32_t full0 = in_cta(bar(B_FULL), 0);
       uint32_t k = 0, uk = 0;  // stages and units so far
-      int next = blockIdx.x / 2;  // the first without a draw
       while (true) {
-        Unit x;
         const int slot = uk % kURing;
-        if (rank == 0) {
-          x = unit_of(a, c, next);
-          if (!wait_cluster(bar(B_U_FREE + slot), ((uk / kURing) & 1) ^ 1, abort)) {
-            give_up(abort, 1u);
-            break;
-          }
-          for (uint32_t r = 0; r < 2; ++r) {
-            publish(in_cta(sbase + SM_UNIT + 32 * slot, r), x);
-            arrive_cluster(in_cta(bar(B_U_FULL + slot), r));
-          }
-          if (x.kind != END) next = gridDim.x / 2 + atomicAdd(a.counter, 1);  // needed when this unit's copies are issued
-        } else {
-          if (!wait_cluster(bar(B_U_FULL + slot), (uk / kURing) & 1, abort)) {
-            give_up(abort, 2u);
-            break;
-          }
-          x = taken(sbase + SM_UNIT + 32 * slot);
-          arrive_cluster(in_cta(bar(B_U_FREE + slot), 0));
+        if (!wait_cluster(bar(B_U_FULL + slot), (uk / kURing) & 1, abort)) {
+          give_up(abort, 2u);
+          break;
         }
-        ++uk;
+        const Unit x = taken(sbase + SM_UNIT + 32 * slot);
+        arrive_read(in_cta(bar(B_U_FREE + slot), 0));
+        *begun = ++uk;
         if (x.kind == END) break;
         bool ok = true;
         for (int t = 0; t < x.tiles && ok; ++t) {
@@ -427,6 +423,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
+  } else if (warp == kDrawWarp) {
+    // Draws units, works them out and publishes them to both CTAs, as far ahead as the ring
+    // goes: a draw takes about as long as four stages.  Behind a long unit it waits until
+    // the producer has begun that one, so that what is left at the end goes to whoever is free.
+    if (lane == 0 && rank == 0) {
+      int next = blockIdx.x / 2;  // the first without a draw
+      for (uint32_t uk = 0;; ++uk) {
+        const int slot = uk % kURing;
+        const Unit x = unit_of(a, c, next);
+        if (!mbar_wait(bar(B_U_FREE + slot), ((uk / kURing) & 1) ^ 1, abort)) {
+          give_up(abort, 1u);
+          break;
+        }
+        for (uint32_t r = 0; r < 2; ++r) {
+          publish(in_cta(sbase + SM_UNIT + 32 * slot, r), x);
+          arrive_written(in_cta(bar(B_U_FULL + slot), r));
+        }
+        if (x.kind == END) break;
+        if (x.nkb * x.tiles > kLongUnit) {
+          const uint64_t t0 = global_timer();
+          while (*begun <= uk && !*abort && global_timer() - t0 < kWaitLimitNs) __nanosleep(100);
+        }
+        next = gridDim.x / 2 + atomicAdd(a.counter, 1);
+      }
+    }
+    __syncwarp();
   } else if (warp == kMmaWarp) {
     if (lane == 0 && rank == 0) {
       uint32_t k = 0, uk = 0, tile = 0;
@@ -438,7 +460,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           break;
         }
         const Unit x = taken(sbase + SM_UNIT + 32 * slot);
-        arrive_cluster(in_cta(bar(B_U_FREE + slot), 0));
+        arrive_read(in_cta(bar(B_U_FREE + slot), 0));
         ++uk;
         if (x.kind == END) break;
         const bool a_mn = x.kind == DW, b_mn = x.kind != REC;
@@ -450,7 +472,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t step_a = (a_mn ? 2048 : 32) >> 4, step_b = (b_mn ? 2048 : 32) >> 4;
         for (int t = 0; t < x.tiles && ok; ++t, ++tile) {
           const int acc = tile & 1;
-          if (!wait_cluster(bar(B_ACC_FREE + acc), ((tile >> 1) & 1) ^ 1, abort)) {
+          if (!mbar_wait(bar(B_ACC_FREE + acc), ((tile >> 1) & 1) ^ 1, abort)) {
             give_up(abort, 16u);
             ok = false;
             break;
@@ -459,7 +481,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t d = tmem + 256 * acc;
           for (int j = 0; j < x.nkb; ++j, ++k) {
             const int s = k % kStages;
-            if (!wait_cluster(bar(B_FULL + s), (k / kStages) & 1, abort)) {
+            if (!mbar_wait(bar(B_FULL + s), (k / kStages) & 1, abort)) {
               give_up(abort, 32u);
               ok = false;
               break;
@@ -497,7 +519,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       const Unit x = taken(sbase + SM_UNIT + 32 * slot);
       __syncwarp();
-      if (lane == 0) arrive_cluster(in_cta(bar(B_U_FREE + slot), 0));
+      if (lane == 0) arrive_read(in_cta(bar(B_U_FREE + slot), 0));
       ++uk;
       if (x.kind == END) break;
       const int row = x.m * 256 + r_in;
@@ -527,7 +549,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_cluster(in_cta(bar(B_ACC_FREE + acc), 0));
+        if (lane == 0) arrive_read(in_cta(bar(B_ACC_FREE + acc), 0));
         const int col = (x.n + t) * 256 + 128 * half;  // of the piece, or of dims
         if (FWD) {
           reduce_tile(v, col, a.V, target, top, sum, a.picked + row);
