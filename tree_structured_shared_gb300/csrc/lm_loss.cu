@@ -303,9 +303,10 @@ __device__ __forceinline__ void reduce_tile(uint32_t (&v)[2][64], int word, int 
   }
 }
 
-// G of a row's 128 words from `word`, bf16, to `out`; zero from word V on.
+// G of a row's 128 words from `word`, bf16, to `out`, the second 64 `block` on; zero from
+// word V on.
 __device__ __forceinline__ void gradient_tile(const uint32_t (&v)[2][64], int word, int V, int target, float off,
-                                              float d_loss, __nv_bfloat16* out) {
+                                              float d_loss, __nv_bfloat16* out, int64_t block) {
   const uint64_t scale = f2pack(kLog2e, kLog2e), less = f2pack(-off, -off), by = f2pack(d_loss, d_loss);
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
@@ -335,8 +336,9 @@ __device__ __forceinline__ void gradient_tile(const uint32_t (&v)[2][64], int wo
         g[i] = pack_bf16x2(lo, hi);
       }
     }
-    st_global_v8(out + 32 * q, g);
-    st_global_v8(out + 32 * q + 16, g + 8);
+    __nv_bfloat16* to = out + (q >> 1) * block + 32 * (q & 1);
+    st_global_v8(to, g);
+    st_global_v8(to + 16, g + 8);
   }
 }
 
@@ -408,12 +410,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               tma_pair_2d(sa, &m_hk, full, kk, x.m * 256 + 128 * rank);
               tma_pair_2d(sb, &m_wk, full, kk, a.rec_v0 + (x.n + t) * 256 + 128 * rank);
             } else if (!FWD && x.kind == DH) {
-              tma_pair_2d(sa, &m_gk, full, kk, x.m * 256 + 128 * rank);
+              tma_pair_2d(sa, &m_gk, full, 0, (x.k0 + j) * a.g_rows + x.m * 256 + 128 * rank);
               tma_pair_2d(sb, &m_wm, full, x.n * 256 + 128 * rank, a.g_v0 + kk);
               tma_pair_2d(sb + kOperand / 2, &m_wm, full, x.n * 256 + 128 * rank + 64, a.g_v0 + kk);
             } else if (!FWD) {
-              tma_pair_2d(sa, &m_gm, full, x.m * 256 + 128 * rank, kk);
-              tma_pair_2d(sa + kOperand / 2, &m_gm, full, x.m * 256 + 128 * rank + 64, kk);
+              const int block = 4 * x.m + 2 * rank;  // of 64 words
+              tma_pair_2d(sa, &m_gm, full, 0, block * a.g_rows + kk);
+              tma_pair_2d(sa + kOperand / 2, &m_gm, full, 0, (block + 1) * a.g_rows + kk);
               tma_pair_2d(sb, &m_hm, full, x.n * 256 + 128 * rank, kk);
               tma_pair_2d(sb + kOperand / 2, &m_hm, full, x.n * 256 + 128 * rank + 64, kk);
             }
@@ -555,7 +558,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           reduce_tile(v, col, a.V, target, top, sum, a.picked + row);
         } else if (x.kind == REC) {
           gradient_tile(v, a.rec_v0 + col, has_row ? a.V : 0, target, off, d_loss,
-                        a.g_out + static_cast<int64_t>(row) * a.g_ld + col);
+                        a.g_out + (static_cast<int64_t>(col / 64) * a.g_rows + row) * 64, static_cast<int64_t>(a.g_rows) * 64);
         } else if (x.kind == DH) {
           if (!has_row) continue;
           if (x.nkb == 0) {
@@ -984,8 +987,10 @@ int launch_lm_loss_bwd(const LmCall& l, void* ws_, cudaStream_t s, std::string* 
   if (!rc) rc = make_map(enc, &m[M_WM], l.w, l.D, l.V, l.w_stride, 64, err);
   if (!rc && l.dw) rc = make_map(enc, &m[M_WO], l.dw, l.D, l.V, l.D, 32, err);
   for (int i = 0; i < (p.pieces > 1 ? 2 : 1) && !rc; ++i) {
-    rc = make_map(enc, &gk[i], ws + p.g + i * p.g_bytes, g_ld, p.n_pad, g_ld, 128, err);
-    if (!rc) rc = make_map(enc, &gm[i], ws + p.g + i * p.g_bytes, g_ld, p.n_pad, g_ld, 64, err);
+    // G lies in blocks of 64 words, all rows of a block together: what a copy takes of it,
+    // for either product, is then one run of bytes
+    rc = make_map(enc, &gk[i], ws + p.g + i * p.g_bytes, 64, p.n_pad * (g_ld / 64), 64, 128, err);
+    if (!rc) rc = make_map(enc, &gm[i], ws + p.g + i * p.g_bytes, 64, p.n_pad * (g_ld / 64), 64, 64, err);
   }
   if (rc) return rc;
   rc = launch_rows(l, p, ws, true, s, err);
@@ -1006,7 +1011,7 @@ int launch_lm_loss_bwd(const LmCall& l, void* ws_, cudaStream_t s, std::string* 
   a.acc = reinterpret_cast<float*>(ws + p.acc);
   a.acc_rows = p.n_pad;
   a.acc_ld = p.acc_ld;
-  a.g_ld = g_ld;
+  a.g_rows = static_cast<int32_t>(p.n_pad);
   // launch i: the gradients of piece i - 1 and G of piece i
   for (int i = 0; i <= p.pieces; ++i) {
     const int done = i - 1;

@@ -333,8 +333,8 @@ struct LmArgs {
   // backward
   const float* lse;
   const float* d_loss;
-  __nv_bfloat16* g_out;
-  int64_t g_ld;
+  __nv_bfloat16* g_out;  // [64 words][row][word]
+  int32_t g_rows;
   float* acc;
   int64_t acc_rows, acc_ld;
   __nv_bfloat16* dh;
