@@ -88,7 +88,7 @@ def check(got, ref, bound):
 
 
 CASES = [(1, 64, 256), (1, 1024, 1000), (2, 8, 7), (3, 72, 1), (255, 64, 255), (256, 128, 256), (257, 200, 257),
-         (300, 64, 5000), (611, 896, 3001), (1000, 256, 513), (130, 1024, 32003), (700, 1032, 777)]
+         (300, 64, 5000), (1, 64, 70001), (3, 72, 151936), (100, 4104, 300), (611, 896, 3001), (1000, 256, 513), (130, 1024, 32003), (700, 1032, 777)]
 
 
 @pytest.mark.parametrize("n,D,V", CASES)
@@ -154,6 +154,28 @@ def test_one_gradient(padoc_lib, which):
 def test_several_pieces(padoc_lib, n, V):
     h, w, t, d = make(n, 64, V, seed=9, masked=0.2)
     check(launch(h, w, t, d), *reference(h, w, t, d))
+
+
+def test_rows_on_their_own_or_among_others(padoc_lib):
+    """A row's loss does not depend on which others have a target."""
+    import torch
+    h, w, t, d = make(700, 136, 2100, seed=21)
+    whole = launch(h, w, t, d)
+    few = t.clone()
+    few[torch.arange(700, device="cuda") % 7 != 3] = -1
+    part = launch(h, w, few, d)
+    on = few >= 0
+    for i in (0, 1, 2):
+        assert torch.equal(whole[i][on], part[i][on])
+
+
+def test_the_same_row_twice(padoc_lib):
+    import torch
+    h, w, t, d = make(520, 64, 700, seed=22)
+    h[400], t[400], d[400] = h[3], t[3], d[3]
+    loss, lse, dh, dw = launch(h, w, t, d)
+    assert torch.equal(loss[400], loss[3]) and torch.equal(lse[400], lse[3]) and torch.equal(dh[400], dh[3])
+    check((loss, lse, dh, dw), *reference(h, w, t, d))
 
 
 def test_large_logits(padoc_lib):

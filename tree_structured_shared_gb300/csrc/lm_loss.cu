@@ -913,10 +913,10 @@ LmPlan lm_plan(int32_t n, int32_t D, int32_t V, bool backward) {
     p.bytes = at;
     return p;
   }
-  // A piece of the vocabulary is what 640 MB of G hold: long enough that a piece's
-  // products dwarf the f32 sums of dh which go through memory once a piece, and small
-  // beside the weights' own gradient.
-  const int64_t cap = std::max<int64_t>(1, (640ll << 20) / (2 * 256 * p.n_pad));
+  // A piece of the vocabulary is what 640 MB of G hold, or 4096 words where rows are many:
+  // long enough that a piece's products dwarf the f32 sums of dh which go through memory
+  // once a piece.
+  const int64_t cap = std::max<int64_t>(16, (640ll << 20) / (2 * 256 * p.n_pad));
   p.pieces = static_cast<int32_t>((word_tiles + cap - 1) / cap);
   p.piece_tiles = static_cast<int32_t>((word_tiles + p.pieces - 1) / p.pieces);
   p.pieces = static_cast<int32_t>((word_tiles + p.piece_tiles - 1) / p.piece_tiles);
