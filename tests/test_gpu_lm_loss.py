@@ -5,8 +5,8 @@ Tolerances.  A logit is a sum of D products in f32, taken 16 at a time: at most
 D / 16 + 2 additions that are each off by a step, 2^-23 of the running sum, which
 is below S = max_v sum_k |h_k w_vk|.  lse is a weighted mean of such errors, and
 its exponentials and sums add less than 2^-17.  G carries the relative error of its
-exponential (that of the logit and of lse) and one rounding to bf16, 2^-8 (half of finfo.eps, 2^-7); dh and dw
-one more of their own, and f32 sums.  Element by element these are bounds; by the
+exponential (that of the logit and of lse) and one rounding to bf16, 2^-8 (half of finfo.eps, 2^-7),
+or, with 128 rows at most, the rounding of a second part, 2^-16; dh and dw one more of their own, and f32 sums.  Element by element these are bounds; by the
 norm, where roundings do not all add up, each rounding counts 2^-8 at most."""
 import numpy as np
 import pytest
@@ -51,7 +51,7 @@ def reference(h, w, t, d):
         p = torch.exp(logits - ls[:, None])
         G = p.scatter_add(1, tt, -torch.ones_like(tt, dtype=torch.float64)) * d[r].double()[:, None]
         # the exponential's error is relative to p, the rounding's to G
-        eG = G.abs() * 2.0 ** -8 * 1.01 + p * d[r].double()[:, None] * (2 * e_logit + 2.0 ** -17)[:, None]
+        eG = G.abs() * 2.0 ** (-8 if len(rows) > 128 else -16) * 1.01 + p * d[r].double()[:, None] * (2 * e_logit + 2.0 ** -17)[:, None]
         dh[r] = G @ W
         dw += G.T @ x
         e_dh[r] = eG @ W.abs() + 2.0 ** -8 * dh[r].abs() + 2.0 ** -14 * (G.abs() @ W.abs())
@@ -88,7 +88,7 @@ def check(got, ref, bound):
 
 
 CASES = [(1, 64, 256), (1, 1024, 1000), (2, 8, 7), (3, 72, 1), (255, 64, 255), (256, 128, 256), (257, 200, 257),
-         (300, 64, 5000), (1, 64, 70001), (3, 72, 151936), (100, 4104, 300), (611, 896, 3001), (1000, 256, 513), (130, 1024, 32003), (700, 1032, 777)]
+         (128, 200, 900), (129, 200, 900), (65, 64, 300), (300, 64, 5000), (1, 64, 70001), (3, 72, 151936), (100, 4104, 300), (611, 896, 3001), (1000, 256, 513), (130, 1024, 32003), (700, 1032, 777)]
 
 
 @pytest.mark.parametrize("n,D,V", CASES)
@@ -157,12 +157,13 @@ def test_several_pieces(padoc_lib, n, V):
 
 
 def test_rows_on_their_own_or_among_others(padoc_lib):
-    """A row's loss does not depend on which others have a target."""
+    """A row's loss does not depend on which others have a target, nor does its dh while
+    there are enough of them."""
     import torch
     h, w, t, d = make(700, 136, 2100, seed=21)
     whole = launch(h, w, t, d)
     few = t.clone()
-    few[torch.arange(700, device="cuda") % 7 != 3] = -1
+    few[torch.arange(700, device="cuda") % 7 == 3] = -1
     part = launch(h, w, few, d)
     on = few >= 0
     for i in (0, 1, 2):

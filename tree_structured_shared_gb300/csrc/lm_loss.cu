@@ -187,12 +187,22 @@ struct Unit {
   int kind, m, n, tiles, k0, nkb, part;  // tile row, first tile column and their number; k blocks from k0
 };
 
+// Roundings of G average out over many rows; of a few, each shows in dw.  Up to kTwice rows
+// with a target G is held in two bf16 parts: they fill half of a row tile, so its other
+// half takes the same rows and what the first rounding left over, at no further product's
+// cost but a step of dw's sum.  (dw of one row: 2^-8 of its values off by two roundings at
+// worst, now by its own.)
+constexpr int kTwice = 128;
+
 struct Counts {
+  bool twice;
   int rows, mt, dh, dw, rec_groups, all;
 };
+template <bool FWD>
 __device__ __forceinline__ Counts counts(const LmArgs& a) {
   Counts c;
   c.rows = *a.n_rows;
+  c.twice = !FWD && c.rows <= kTwice;
   c.mt = (c.rows + 255) / 256;
   c.dh = a.dh ? c.mt * a.d_tiles * a.splits : 0;
   c.dw = a.dw ? ((a.g_cols + 255) / 256) * a.d_tiles : 0;
@@ -225,7 +235,7 @@ __device__ __forceinline__ Unit unit_of(const LmArgs& a, const Counts& c, int u)
     x.kind = DW;
     x.n = u % a.d_tiles;
     x.m = u / a.d_tiles;
-    x.nkb = (c.rows + 63) / 64;
+    x.nkb = (c.rows + 63) / 64 * (c.twice ? 2 : 1);
     return x;
   }
   u -= c.dw;  // all rows of a few words, then the next words: the weights are read once
@@ -303,16 +313,16 @@ __device__ __forceinline__ void reduce_tile(uint32_t (&v)[2][64], int word, int 
   }
 }
 
-// G of a row's 128 words from `word`, bf16, to `out`, the second 64 `block` on; zero from
-// word V on.
+// G of a row's 128 words from `word`, bf16 (or what that rounding leaves of it), to `out`,
+// the second 64 `block` on; zero from word V on.
 __device__ __forceinline__ void gradient_tile(const uint32_t (&v)[2][64], int word, int V, int target, float off,
-                                              float d_loss, __nv_bfloat16* out, int64_t block) {
+                                              float d_loss, bool rest, __nv_bfloat16* out, int64_t block) {
   const uint64_t scale = f2pack(kLog2e, kLog2e), less = f2pack(-off, -off), by = f2pack(d_loss, d_loss);
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const int hit = target - word - 32 * q;
     uint32_t g[16];
-    if (__any_sync(0xffffffffu, (hit >= 0 && hit < 32) || word + 32 * q + 32 > V)) {
+    if (rest || __any_sync(0xffffffffu, (hit >= 0 && hit < 32) || word + 32 * q + 32 > V)) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         float p[2];
@@ -323,6 +333,8 @@ __device__ __forceinline__ void gradient_tile(const uint32_t (&v)[2][64], int wo
           p[k] = word + 32 * q + 2 * i + k < V ? p[k] * d_loss : 0.f;
         }
         g[i] = pack_bf16x2(p[0], p[1]);
+        if (rest)
+          g[i] = pack_bf16x2(p[0] - __uint_as_float(g[i] << 16), p[1] - __uint_as_float(g[i] & 0xffff0000u));
       }
     } else {
 #pragma unroll
@@ -378,7 +390,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   wait_for_previous();
-  const Counts c = counts(a);
+  const Counts c = counts<FWD>(a);
 
   if (warp == kProducerWarp) {
     if (lane == 0) {
@@ -405,7 +417,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             if (rank == 0) mbar_arrive_expect_tx(bar(B_FULL + s), 2 * kStage);
             const uint32_t sa = sbase + s * kStage, sb = sa + kOperand, full = full0 + 8u * s;
-            const int kk = (x.k0 + j) * 64;
+            int kk = (x.k0 + j) * 64;
             if (x.kind == REC) {
               tma_pair_2d(sa, &m_hk, full, kk, x.m * 256 + 128 * rank);
               tma_pair_2d(sb, &m_wk, full, kk, a.rec_v0 + (x.n + t) * 256 + 128 * rank);
@@ -415,6 +427,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               tma_pair_2d(sb + kOperand / 2, &m_wm, full, x.n * 256 + 128 * rank + 64, a.g_v0 + kk);
             } else if (!FWD) {
               const int block = 4 * x.m + 2 * rank;  // of 64 words
+              // the second parts' rows
+              if (c.twice && j >= x.nkb / 2) kk += kTwice - 64 * (x.nkb / 2);
               tma_pair_2d(sa, &m_gm, full, 0, block * a.g_rows + kk);
               tma_pair_2d(sa + kOperand / 2, &m_gm, full, 0, (block + 1) * a.g_rows + kk);
               tma_pair_2d(sb, &m_hm, full, x.n * 256 + 128 * rank, kk);
@@ -526,14 +540,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ++uk;
       if (x.kind == END) break;
       const int row = x.m * 256 + r_in;
-      const bool has_row = row < c.rows;
+      const int place = c.twice ? row & (kTwice - 1) : row;  // among the rows with a target
+      const bool has_row = place < c.rows;
       int target = -1;
       float off = 0.f, d_loss = 0.f;
       if (x.kind == REC && has_row) {
-        target = a.targets[row];
+        target = a.targets[place];
         if (!FWD) {
-          off = a.lse[row] * kLog2e;
-          d_loss = a.d_loss[row];
+          off = a.lse[place] * kLog2e;
+          d_loss = a.d_loss[place];
         }
       }
       float top = -INFINITY, sum = 0.f;  // forward: the row's running maximum and sum
@@ -558,7 +573,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           reduce_tile(v, col, a.V, target, top, sum, a.picked + row);
         } else if (x.kind == REC) {
           gradient_tile(v, a.rec_v0 + col, has_row ? a.V : 0, target, off, d_loss,
-                        a.g_out + (static_cast<int64_t>(col / 64) * a.g_rows + row) * 64, static_cast<int64_t>(a.g_rows) * 64);
+                        c.twice && rank == 1, a.g_out + (static_cast<int64_t>(col / 64) * a.g_rows + row) * 64, static_cast<int64_t>(a.g_rows) * 64);
         } else if (x.kind == DH) {
           if (!has_row) continue;
           if (x.nkb == 0) {
@@ -566,7 +581,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 128; ++i) v[i >> 6][i & 63] = 0u;
           }
           float* sums = a.acc + (static_cast<int64_t>(x.part) * a.acc_rows + row) * a.acc_ld + col;
-          __nv_bfloat16* out = a.dh + (a.finish ? static_cast<int64_t>(a.rows[row]) * a.D + col : 0);
+          const bool finish = a.finish && !c.twice;
+          __nv_bfloat16* out = a.dh + (finish ? static_cast<int64_t>(a.rows[row]) * a.D + col : 0);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             uint32_t* w = &v[i >> 3][8 * (i & 7)];
@@ -581,7 +597,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               w[6] = __float_as_uint(__uint_as_float(w[6]) + z.z);
               w[7] = __float_as_uint(__uint_as_float(w[7]) + z.w);
             }
-            if (!a.finish)
+            if (!finish)
               st_global_v8(sums + 8 * i, w);
             else if (col + 8 * i < a.D)
               reinterpret_cast<uint4*>(out)[i] = pack8(w);
@@ -688,6 +704,7 @@ __global__ void __launch_bounds__(kRowThreads) lm_rows_kernel(const LmRows a) {
     }
     const uint4* src[K];
     uint4* dst[K];
+    const int64_t again = a.lse_out && all <= kTwice ? static_cast<int64_t>(kTwice) * a.vecs : 0;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int r = K * warp + k;
@@ -706,13 +723,17 @@ __global__ void __launch_bounds__(kRowThreads) lm_rows_kernel(const LmRows a) {
       for (int k = 0; k < K; ++k) v[k] = src[k] ? src[k][j] : make_uint4(0, 0, 0, 0);
 #pragma unroll
       for (int k = 0; k < K; ++k)
-        if (dst[k]) dst[k][j] = v[k];
+        if (dst[k]) {
+          dst[k][j] = v[k];
+          if (again && src[k]) dst[k][again + j] = v[k];
+        }
     }
     before += __popc(who);
   }
   const int64_t pad = static_cast<int64_t>(-all & 63) * a.vecs;
   for (int64_t j = static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x; j < pad; j += static_cast<int64_t>(gridDim.x) * kRowThreads)
-    a.out[static_cast<int64_t>(all) * a.vecs + j] = make_uint4(0, 0, 0, 0);
+    for (int k = 0; k < (a.lse_out && all <= kTwice ? 2 : 1); ++k)
+      a.out[(static_cast<int64_t>(all) + k * kTwice) * a.vecs + j] = make_uint4(0, 0, 0, 0);
 }
 
 // lse and loss of a row from its partial maxima and sums, which lie side by side.
@@ -776,25 +797,45 @@ __global__ void __launch_bounds__(kJoinThreads) lm_join_kernel(const float2* __r
   }
 }
 
-// dh of few rows: the parts of the vocabulary added up, in their order.
-__global__ void __launch_bounds__(256) lm_finish_kernel(const float* __restrict__ acc, int64_t acc_rows, int32_t acc_ld,
-                                                        int32_t splits, const int32_t* __restrict__ rows,
-                                                        const int32_t* __restrict__ head, int32_t D,
-                                                        __nv_bfloat16* __restrict__ dh) {
+// dh of few rows: the parts of the vocabulary added up, in their order, and both parts of
+// G.  `done`: dh is there already, but where G has two parts.
+// GROUPS of 256 threads share a row's parts.
+template <int GROUPS>
+__global__ void __launch_bounds__(256 * GROUPS) lm_finish_kernel(const float* __restrict__ acc, int64_t acc_rows,
+                                                                   int32_t acc_ld, int32_t splits,
+                                                                   const int32_t* __restrict__ rows,
+                                                                   const int32_t* __restrict__ head, int32_t D, bool done,
+                                                                   __nv_bfloat16* __restrict__ dh) {
+  __shared__ float4 s_sum[GROUPS][256];
   wait_for_previous();
-  const int row = blockIdx.x;
-  if (row >= *head) return;
+  const int row = blockIdx.x, count = *head, lane = threadIdx.x & 255, group = threadIdx.x >> 8;
+  const bool twice = count <= kTwice;
+  if (row >= count || (done && !twice)) return;
   const int64_t at = rows[row];
-  for (int col = 4 * threadIdx.x; col < D; col += 1024) {
+  for (int c0 = 0; c0 < D; c0 += 1024) {
+    const int col = c0 + 4 * lane;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int p = 0; p < splits; ++p) {
-      const float4 x = *reinterpret_cast<const float4*>(acc + (p * acc_rows + row) * acc_ld + col);
-      s.x += x.x;
-      s.y += x.y;
-      s.z += x.z;
-      s.w += x.w;
+    if (col < D) {
+      const float* x = acc + static_cast<int64_t>(row) * acc_ld + col;
+#pragma unroll 8
+      for (int p = group; p < splits; p += GROUPS) {
+        const float4 y = *reinterpret_cast<const float4*>(x + p * acc_rows * acc_ld);
+        const float4 z = twice ? *reinterpret_cast<const float4*>(x + (p * acc_rows + kTwice) * acc_ld)
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+        s = make_float4(s.x + (y.x + z.x), s.y + (y.y + z.y), s.z + (y.z + z.z), s.w + (y.w + z.w));
+      }
     }
-    *reinterpret_cast<uint2*>(dh + at * D + col) = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+    if (group) s_sum[group][lane] = s;
+    __syncthreads();
+    if (!group && col < D) {
+#pragma unroll
+      for (int i = 1; i < GROUPS; ++i) {
+        const float4 y = s_sum[i][lane];
+        s = make_float4(s.x + y.x, s.y + y.y, s.z + y.z, s.w + y.w);
+      }
+      *reinterpret_cast<uint2*>(dh + at * D + col) = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+    }
+    __syncthreads();
   }
 }
 
@@ -932,7 +973,7 @@ LmPlan lm_plan(int32_t n, int32_t D, int32_t V, bool backward) {
   p.d = take(n * sizeof(float));
   p.hc = take(static_cast<size_t>(p.n_pad) * D * 2);
   p.acc_ld = static_cast<int32_t>(d_tiles * 256);
-  p.acc = take(p.pieces > 1 || p.splits > 1 ? static_cast<size_t>(p.splits) * p.n_pad * p.acc_ld * sizeof(float) : 0);
+  p.acc = take(static_cast<size_t>(p.pieces > 1 || p.splits > 1 ? p.splits * p.n_pad : 2 * kTwice) * p.acc_ld * sizeof(float));
   p.g_bytes = static_cast<size_t>(p.n_pad) * p.piece_tiles * 512;
   p.g = take(p.g_bytes * (p.pieces > 1 ? 2 : 1));
   p.bytes = at;
@@ -1035,9 +1076,12 @@ int launch_lm_loss_bwd(const LmCall& l, void* ws_, cudaStream_t s, std::string* 
     rc = launch_gemm<false>(a, m, s, err);
     if (rc) return rc;
   }
-  if (l.dh && p.splits > 1) {
-    return launch_after(lm_finish_kernel, static_cast<unsigned>(l.n), 256, 0, s, "lm_finish_kernel", err, a.acc, a.acc_rows,
-                        static_cast<int32_t>(a.acc_ld), p.splits, a.rows, head, l.D, static_cast<__nv_bfloat16*>(l.dh));
+  if (l.dh) {
+    const bool done = p.splits == 1;
+    const bool few = l.n <= kTwice;
+    return launch_after(few ? lm_finish_kernel<4> : lm_finish_kernel<1>,
+                        static_cast<unsigned>(done ? std::min(l.n, kTwice) : l.n), few ? 1024 : 256, 0, s, "lm_finish_kernel", err, a.acc, a.acc_rows,
+                        static_cast<int32_t>(a.acc_ld), p.splits, a.rows, head, l.D, done, static_cast<__nv_bfloat16*>(l.dh));
   }
   return PADOC_OK;
 }
