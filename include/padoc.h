@@ -404,7 +404,8 @@ PADOC_API int padoc_rope_apply(const padoc_rope* rope, int32_t n_parts, const pa
  * x = h w^T (f32):
  *   lse = log sum_v exp(x_v),  loss = lse - x_target        (f32, one a row)
  *   G = d_loss (exp(x - lse) - onehot(target)),  dh = G w,  dw = G^T h
- * G is rounded to bf16 before the two products, whose sums are f32.  A row with
+ * G is rounded to bf16 before the two products, whose sums are f32 (up to 128
+ * rows with a target it has two bf16 parts).  A row with
  * a negative target has no loss: loss and lse are 0, its dh is zero and it takes
  * no part in dw, whatever h holds there; its products are not computed.  A
  * target of V or more is treated alike but for a loss of NaN.

@@ -16,6 +16,9 @@
 // share a group, so its largest magnitude takes one exchange, and a lane moves 32 bytes
 // of values and 16 of codes.  Magnitudes are compared as integers, two at a time: bf16
 // bits without the sign are in the order of the values, infinities and NaNs on top.
+//
+// 131072 rows of 6144 values in four tensors: kept in 377 us, restored in 390, 6.5 and 6.3
+// TB/s (360 each at the copy rate).  462 rows of 1536: 4 us each, a launch.
 #include <cuda_bf16.h>
 
 #include <algorithm>

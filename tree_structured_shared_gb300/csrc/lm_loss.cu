@@ -6,12 +6,13 @@
 //   G = d_loss (exp(x - lse) - onehot(t)),  dh = G w,  dw = G^T h
 // Products accumulate in f32; maxima, sums, lse and loss are f32.  G is rounded to bf16
 // once, since the products that follow take bf16 operands: with the rounding of the
-// gradients themselves that is 2^-8 relative twice.  dh is summed over pieces in f32.
+// gradients themselves that is 2^-8 relative twice (up to 128 rows G has two bf16 parts).
+// dh is summed over pieces in f32.
 //
 // Rows without a target take no part: the others are gathered first (lm_rows_kernel), and
-// the number of them stays on the device, where every kernel here
-// reads it.  A page's prefix has no targets, so that is most of the work saved, and
-// whatever padded rows hold cannot reach a gradient.
+// the number of them stays on the device, where every kernel here reads it.  A page's
+// prefix has no targets, so that is most of the work saved, and whatever padded rows hold
+// cannot reach a gradient.
 //
 // lm_kernel: persistent pairs of CTAs (two SMs share an MMA of 256 x 256 x 16: each holds
 // half of A's rows, half of B's, and its half of the accumulator's rows).  A 128 x 256
@@ -37,6 +38,25 @@
 // error word; the others leave their loops, the issuer commits once more and waits for
 // that, copies in flight get a thousand times their latency to land, and the CTAs meet
 // before TMEM is released.
+//
+// What bounds it.  Many rows: the tensor cores.  16384 rows, 14746 of them with a target,
+// 151936 words, D = 1024: lm_kernel<forward> 2.30 ms, 2.0 PFLOP/s; a backward launch, three
+// products of a piece of 19200 words, 0.915 ms, 1.9 PFLOP/s (tensor pipe 93 % busy on 4096
+// rows); back to back the power limit makes that 2.4 and 8.2 ms.  Copies then run at 54
+// bytes a cycle and SM, which is what they reach without products too.  Few rows: reading
+// the weights, and latency.  One row, 151936 words: 54 us for 311 MB of weights (a plain
+// read of them takes 57).  397 rows, 32003 words, D = 896: forward 32 us, of which 15 are
+// products (four rounds of tiles, the last a third full), 4 the gathering of rows, 3 until
+// the first stage is there, 3 from the last one to the end and 3 the join; backward 88.
+// Steps on the way, 16384 rows and 397 rows, forward and backward together (ms, us):
+//   first right kernel 11.3, 169
+//   a tile leaves TMEM at once, before it is worked on, packed arithmetic 11.0, 137
+//   units worked out by the thread that draws them, which is a warp of its own 10.7, 132
+//   "read" signalled by an arrival that does not wait for the thread's stores 10.6, 120
+// Tried without gain: copies of a row tile's rows that exist in boxes of 32 (10 % slower),
+// another k to start with for each tile, waits without acquire in the issuer, a ring of
+// eleven smaller stages for few rows, the first words asked for ahead of the rows, dw stored
+// from registers by lines instead of by TMA, the next unit taken ahead by the producer.
 #include <cuda_bf16.h>
 
 #include <algorithm>

@@ -19,6 +19,14 @@
 // position's fraction is their product modulo 2^64 with the step as a 64-bit binary
 // fraction.  That is exact but for the step's own rounding (2^-53 of it), at any
 // position, without a 64-bit floating operation; its upper 32 bits are used.
+//
+// Bound by HBM, and by launches below some 10 MB.  131072 rows of 24 heads of 128 in bf16:
+// 246 us, 6.6 TB/s of reads and writes (240 at the copy rate).  50003 rows of 6 heads of 64
+// in f32: 30 us (23.4): rows of 1.5 KB are short for a warp, and a GPU of CTAs takes 2.7
+// rounds of them; with each lane's 16 dims side by side, which spreads a load over twice
+// the lines, 37.  384 rows: 6 us, a launch.  A table of 131072 positions of 128: 14.3 us
+// for 67 MB (a fill of them takes 12.5); with sincospif on the remainder of a 64-bit
+// product 20.6.
 #include <cuda_bf16.h>
 
 #include <algorithm>
