@@ -60,6 +60,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
 #include <string>
 
 #include "../../include/padoc.h"
@@ -69,6 +70,9 @@
 namespace padoc {
 
 __device__ unsigned int g_lm_err;
+// Longest time one wait of lm_kernel may take before it gives up (nanoseconds of the global
+// timer); settable for tests, and part of each launch's arguments.
+static std::atomic<uint64_t> g_wait_limit_ns{ptx::kWaitLimitNs};
 
 namespace {
 
@@ -148,14 +152,18 @@ __device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) 
       : "memory");
   return ok != 0;
 }
-__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort) {
-  if (try_wait_cluster(bar, parity)) return true;
+// Waits for a phase; false when `limit` nanoseconds ran out or another role of the CTA gave
+// up.  CLUSTER: what the other CTA wrote before it arrived is wanted.
+template <bool CLUSTER>
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit) {
+  const auto is_over = [&] { return CLUSTER ? try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
+  if (is_over()) return true;
   const uint64_t t0 = global_timer();
   while (true) {
     for (int i = 0; i < 32; ++i)
-      if (try_wait_cluster(bar, parity)) return true;
+      if (is_over()) return true;
     if (*abort) return false;
-    if (global_timer() - t0 > kWaitLimitNs) return false;
+    if (global_timer() - t0 > limit) return false;
   }
 }
 // A copy into this CTA that counts on a barrier of the pair's first.
@@ -418,7 +426,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t k = 0, uk = 0;  // stages and units so far
       while (true) {
         const int slot = uk % kURing;
-        if (!wait_cluster(bar(B_U_FULL + slot), (uk / kURing) & 1, abort)) {
+        if (!wait<true>(bar(B_U_FULL + slot), (uk / kURing) & 1, abort, a.wait_limit)) {
           give_up(abort, 2u);
           break;
         }
@@ -430,7 +438,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int t = 0; t < x.tiles && ok; ++t) {
           for (int j = 0; j < x.nkb; ++j, ++k) {
             const int s = k % kStages;
-            if (!mbar_wait(bar(B_EMPTY + s), ((k / kStages) & 1) ^ 1, abort)) {
+            if (!wait<false>(bar(B_EMPTY + s), ((k / kStages) & 1) ^ 1, abort, a.wait_limit)) {
               give_up(abort, 4u);
               ok = false;
               break;
@@ -469,7 +477,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (uint32_t uk = 0;; ++uk) {
         const int slot = uk % kURing;
         const Unit x = unit_of(a, c, next);
-        if (!mbar_wait(bar(B_U_FREE + slot), ((uk / kURing) & 1) ^ 1, abort)) {
+        if (!wait<false>(bar(B_U_FREE + slot), ((uk / kURing) & 1) ^ 1, abort, a.wait_limit)) {
           give_up(abort, 1u);
           break;
         }
@@ -480,7 +488,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (x.kind == END) break;
         if (x.nkb * x.tiles > kLongUnit) {
           const uint64_t t0 = global_timer();
-          while (*begun <= uk && !*abort && global_timer() - t0 < kWaitLimitNs) __nanosleep(100);
+          while (*begun <= uk && !*abort && global_timer() - t0 < a.wait_limit) __nanosleep(100);
         }
         next = gridDim.x / 2 + atomicAdd(a.counter, 1);
       }
@@ -492,7 +500,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       bool ok = true;
       while (ok) {
         const int slot = uk % kURing;
-        if (!wait_cluster(bar(B_U_FULL + slot), (uk / kURing) & 1, abort)) {
+        if (!wait<true>(bar(B_U_FULL + slot), (uk / kURing) & 1, abort, a.wait_limit)) {
           give_up(abort, 8u);
           break;
         }
@@ -509,7 +517,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t step_a = (a_mn ? 2048 : 32) >> 4, step_b = (b_mn ? 2048 : 32) >> 4;
         for (int t = 0; t < x.tiles && ok; ++t, ++tile) {
           const int acc = tile & 1;
-          if (!mbar_wait(bar(B_ACC_FREE + acc), ((tile >> 1) & 1) ^ 1, abort)) {
+          if (!wait<false>(bar(B_ACC_FREE + acc), ((tile >> 1) & 1) ^ 1, abort, a.wait_limit)) {
             give_up(abort, 16u);
             ok = false;
             break;
@@ -518,7 +526,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t d = tmem + 256 * acc;
           for (int j = 0; j < x.nkb; ++j, ++k) {
             const int s = k % kStages;
-            if (!mbar_wait(bar(B_FULL + s), (k / kStages) & 1, abort)) {
+            if (!wait<false>(bar(B_FULL + s), (k / kStages) & 1, abort, a.wait_limit)) {
               give_up(abort, 32u);
               ok = false;
               break;
@@ -550,7 +558,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     bool ok = true;
     while (ok) {
       const int slot = uk % kURing;
-      if (!__all_sync(0xffffffffu, wait_cluster(bar(B_U_FULL + slot), (uk / kURing) & 1, abort))) {
+      if (!__all_sync(0xffffffffu, wait<true>(bar(B_U_FULL + slot), (uk / kURing) & 1, abort, a.wait_limit))) {
         give_up(abort, 64u);
         break;
       }
@@ -574,7 +582,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       float top = -INFINITY, sum = 0.f;  // forward: the row's running maximum and sum
       for (int t = 0; t < x.tiles; ++t, ++tile) {
         const int acc = tile & 1;
-        if (!__all_sync(0xffffffffu, mbar_wait(bar(B_ACC_FULL + acc), (tile >> 1) & 1, abort))) {
+        if (!__all_sync(0xffffffffu, wait<false>(bar(B_ACC_FULL + acc), (tile >> 1) & 1, abort, a.wait_limit))) {
           give_up(abort, 128u);
           ok = false;
           break;
@@ -896,7 +904,9 @@ int launch_after(void (*kernel)(P...), unsigned grid, int threads, int smem, cud
 enum { M_HK, M_WK, M_HM, M_WM, M_GK, M_GM, M_WO, N_MAPS };
 
 template <bool FWD>
-int launch_gemm(const LmArgs& a, const CUtensorMap* m, cudaStream_t s, std::string* err) {
+int launch_gemm(const LmArgs& args, const CUtensorMap* m, cudaStream_t s, std::string* err) {
+  LmArgs a = args;
+  a.wait_limit = g_wait_limit_ns.load(std::memory_order_relaxed);
   // an attribute of the current device's copy of the kernel
   const cudaError_t e = cudaFuncSetAttribute(lm_kernel<FWD>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) {
@@ -1105,6 +1115,8 @@ int launch_lm_loss_bwd(const LmCall& l, void* ws_, cudaStream_t s, std::string* 
   }
   return PADOC_OK;
 }
+
+void set_lm_wait_limit(uint64_t ns) { g_wait_limit_ns.store(ns ? ns : ptx::kWaitLimitNs); }
 
 int read_and_clear_lm_error(cudaStream_t s, unsigned* word) {
   const unsigned zero = 0;

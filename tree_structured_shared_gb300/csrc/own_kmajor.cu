@@ -857,6 +857,7 @@ extern "C" int padoc_debug_set_wait_limit(uint64_t ns) {
   if (e != cudaSuccess)
     return padoc::set_error(PADOC_ERR_CUDA, "debug_set_wait_limit: %s", cudaGetErrorString(e));
   if (padoc::set_i4_wait_limit(v)) return padoc::set_error(PADOC_ERR_CUDA, "debug_set_wait_limit: 4-bit prefix kernel");
+  padoc::set_lm_wait_limit(ns);
   return PADOC_OK;
 }
 

@@ -317,6 +317,7 @@ struct LmRows {
   uint4* dh;       // backward, may be null
 };
 struct LmArgs {
+  uint64_t wait_limit;  // the launcher's
   const int32_t* n_rows;
   int32_t* counter;  // of units, zero at launch
   const int32_t* rows;     // of the rows with a target: index, target (and lse, d_loss below)
@@ -348,6 +349,7 @@ int launch_act(ActArgs a, bool keep, cudaStream_t s, std::string* err);
 LmPlan lm_plan(int32_t n, int32_t D, int32_t V, bool backward);
 int launch_lm_loss(const LmCall& l, void* ws, cudaStream_t s, std::string* err);
 int launch_lm_loss_bwd(const LmCall& l, void* ws, cudaStream_t s, std::string* err);
+void set_lm_wait_limit(uint64_t ns);
 int read_and_clear_lm_error(cudaStream_t s, unsigned* word);
 int launch_fwd_bf16(const FwdArgs& a, cudaStream_t s, std::string* err);
 int launch_fwd_f32(const FwdArgs& a, cudaStream_t s, std::string* err);
