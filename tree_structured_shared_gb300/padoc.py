@@ -408,8 +408,14 @@ def act_bytes(n: int, width: int) -> int:
     return b.value
 
 
+_BF16 = None  # torch.bfloat16, once a tensor was seen
+
+
 def _is_bf16(x) -> bool:
-    return x.dtype is sys.modules["torch"].bfloat16  # a tensor is there, so torch is
+    global _BF16
+    if _BF16 is None:
+        _BF16 = sys.modules["torch"].bfloat16  # a tensor is there, so torch is
+    return x.dtype is _BF16
 
 
 def _acts(rows, kept) -> bytes:
@@ -423,8 +429,8 @@ def _acts(rows, kept) -> bytes:
         (n, width), (step, one) = x.shape, x.stride()
         if one != 1 and width > 1:
             raise PadocError(ERR_INVALID, "act: a row's values must follow one another")
-        if b.numel() * b.element_size() < n * width + n * width // 32:
-            raise PadocError(ERR_INVALID, "act: a checkpoint is smaller than act_bytes(n, width)")
+        if b.nbytes < n * width + n * width // 32 or not b.is_contiguous():
+            raise PadocError(ERR_INVALID, "act: a checkpoint is smaller than act_bytes(n, width), or not dense")
         out += _ACT(x.data_ptr(), step if n > 1 else width, n, width, b.data_ptr())
     return out
 
