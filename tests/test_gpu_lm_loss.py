@@ -187,6 +187,27 @@ def test_large_logits(padoc_lib):
     check(launch(h, w, t, d), *reference(h, w, t, d))
 
 
+def test_a_sure_row(padoc_lib):
+    """A target far above all other words: the loss is small, and right to a few steps of
+    the sum of exponentials, 1 + something, whatever the logits' size."""
+    import torch
+    n, D, V = 200, 64, 500
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    w = torch.randn(V, D, generator=g, device="cuda").sign().to(torch.bfloat16)  # products of halves and ones are exact
+    t = torch.randint(V, (n,), generator=g, device="cuda").to(torch.int32)
+    h = (w[t.long()].float() * 0.5).to(torch.bfloat16)
+    x = h.double() @ w.double().T
+    want = torch.logsumexp(x, -1) - x.gather(1, t.long()[:, None])[:, 0]
+    head = padoc.LmLoss(h, w, t)
+    ws = torch.empty(head.ws_size(), dtype=torch.uint8, device="cuda")
+    loss, lse = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+    head.forward(loss, lse, ws, ws.numel())
+    assert float(want.max()) < 0.1
+    # 500 exponentials, each within 2^-21 of itself, added in f32 to a sum of some 1
+    assert float((loss.double() - want).abs().max()) <= 8 * 2.0 ** -23
+
+
 def test_a_bad_row_stays_alone(padoc_lib):
     """A NaN or an infinity in a row with a target: that row's loss and gradient are
     NaN, every other row's are what they were; dw holds the NaN, as its formula does."""

@@ -818,10 +818,11 @@ __global__ void __launch_bounds__(kJoinThreads) lm_join_kernel(const float2* __r
     for (int i = 0; i < kJoinThreads / 32; ++i) l += s_sum[i];
   }
   if (me == 0) {
-    const float v = t + logf(l);
+    const float over = logf(l);  // of lse over the largest logit
     const int32_t at = rows[row];
-    lse[at] = v;
-    loss[at] = v - picked[row];
+    lse[at] = t + over;
+    // not lse - picked: where the target is the largest, and the loss small, this cancels nothing
+    loss[at] = (t - picked[row]) + over;
   }
 }
 
