@@ -73,6 +73,17 @@ def test_there_and_back(padoc_lib, n, width, pad):
     assert bool((back[:, width:] == 3).all())
 
 
+def test_long_tensors(padoc_lib):
+    """More than the GPU takes in one round of CTAs, and a short one behind."""
+    import torch
+    x = [rows(10007, 2080, 1, 16), rows(11, 64, 2)]
+    kept, back = [buf(v) for v in x], [torch.empty(v.shape, dtype=v.dtype, device="cuda") for v in x]
+    padoc.act_keep(x, kept)
+    padoc.act_restore(kept, back)
+    for v, b, r in zip(x, kept, back):
+        check_one(v, b, r)
+
+
 def test_special_values(padoc_lib):
     import torch
     x = torch.zeros(64, 64, dtype=torch.bfloat16, device="cuda")
@@ -196,12 +207,13 @@ def test_gradients_are_those_of_the_values(padoc_lib, G, order):
     check_grad(grads[2].float().cpu().numpy(), ref[2], "bf16", "dv")
 
 
-def test_many_key_tiles(padoc_lib):
+@pytest.mark.parametrize("prefix", [900, 2700])
+def test_many_key_tiles(padoc_lib, prefix):
     """Enough of them that no key tile's queries are cut: dv, which the row sums do not
     enter, is bit for bit that of the plain backward."""
     import torch
     from tree_structured_shared_gb300 import harness
-    w = wl.TreeWorkload("pages", [wl.Page(900, [12] * 5, [130, 7, 64, 200, 1]), wl.Page(640, [], []), wl.Page(0, [3], [90])],
+    w = wl.TreeWorkload("pages", [wl.Page(prefix, [12] * 5, [130, 7, 64, 200, 1]), wl.Page(640, [], []), wl.Page(0, [3], [90])],
                         16, 8, 128, "bf16", 1.0, [0, 0, 0])
     T = w.n_tokens
     assert -(-T // 128) * 8 > 76

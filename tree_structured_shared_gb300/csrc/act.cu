@@ -17,8 +17,8 @@
 // of values and 16 of codes.  Magnitudes are compared as integers, two at a time: bf16
 // bits without the sign are in the order of the values, infinities and NaNs on top.
 //
-// 131072 rows of 6144 values in four tensors: kept in 377 us, restored in 390, 6.5 and 6.3
-// TB/s (360 each at the copy rate).  462 rows of 1536: 4 us each, a launch.
+// 131072 rows of 6144 values in four tensors: kept in 360 us, restored in 367, 6.7 TB/s (360
+// each at the copy rate).  462 rows of 1536: 4 us each, a launch.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -35,7 +35,11 @@ using namespace ptx;
 
 constexpr int kThreads = 256;
 constexpr int kUnroll = 2;  // pieces of 16 values a thread, kThreads apart
-constexpr int64_t kPiecesCta = kThreads * kUnroll;
+constexpr int64_t kPiecesRound = kThreads * kUnroll;
+// A CTA costs its launch: long tensors take kRounds of them one after another (131072 rows
+// of 6144 values 365 and 367 us, with one 379 and 404, with 16 370 and 372); short ones
+// spread over the GPU (462 rows of 1536 4.3 us, with four rounds 6.3).
+constexpr int kRounds = 4, kManyRounds = 16 * 152;
 
 // 16 values from a place that is 16-byte aligned.
 struct Piece {
@@ -63,45 +67,48 @@ __device__ __forceinline__ int find(const ActArgs& a, int block) {
 __global__ void __launch_bounds__(kThreads) keep_kernel(const __grid_constant__ ActArgs a) {
   const int ti = find(a, blockIdx.x);
   const ActTensor& x = a.t[ti];
-  const int64_t i0 = static_cast<int64_t>(blockIdx.x - a.first_block[ti]) * kPiecesCta + threadIdx.x;
-  Piece p[kUnroll];
+  const int64_t begin = static_cast<int64_t>(blockIdx.x - a.first_block[ti]) * a.pieces_cta;
+  const int64_t end = min(x.pieces, begin + a.pieces_cta);
+  for (int64_t i0 = begin + threadIdx.x; i0 - threadIdx.x < end; i0 += kPiecesRound) {
+    Piece p[kUnroll];
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u)
-    if (i0 + u * kThreads < x.pieces)
-      p[u] = load_piece(static_cast<const __nv_bfloat16*>(x.rows) + piece_at(x, static_cast<uint32_t>(i0 + u * kThreads)));
+    for (int u = 0; u < kUnroll; ++u)
+      if (i0 + u * kThreads < x.pieces)
+        p[u] = load_piece(static_cast<const __nv_bfloat16*>(x.rows) + piece_at(x, static_cast<uint32_t>(i0 + u * kThreads)));
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    const int64_t i = i0 + u * kThreads;
-    const bool in = i < x.pieces;  // both lanes of a pair or neither: pieces are even
-    uint32_t m = 0;
-    if (in) {
+    for (int u = 0; u < kUnroll; ++u) {
+      const int64_t i = i0 + u * kThreads;
+      const bool in = i < x.pieces;  // both lanes of a pair or neither: pieces are even
+      uint32_t m = 0;
+      if (in) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) m = __vmaxu2(m, p[u].w[j] & 0x7fff7fffu);
-    }
-    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m & 0xffffu, m >> 16);
-    if (!in) continue;
-    const bool bad = m >= 0x7f80u;
-    // of bf16's largest value 127 steps of 2^121 fall short, but 64 of 2^122 are infinite
-    const uint32_t e = min(max(static_cast<int>(m >> 7) - 6 + ((m & 0x7f) == 0x7f), 1), 248);
-    const float inv = __uint_as_float((254u - e) << 23);
-    uint32_t code[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint32_t b[4];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        uint32_t w = p[u].w[2 * j + k];
-        if (m == 0x7f7fu) w -= __vcmpeq2(w & 0x7fff7fffu, 0x7f7f7f7fu) & 0x00010001u;  // the value below it is 127 steps
-        // the product is exact; the sum rounds it to an integer, whose low byte is the code
-        b[2 * k] = __float_as_uint(fmaf(__uint_as_float(w << 16), inv, 12582912.f));
-        b[2 * k + 1] = __float_as_uint(fmaf(__uint_as_float(w & 0xffff0000u), inv, 12582912.f));
+        for (int j = 0; j < 8; ++j) m = __vmaxu2(m, p[u].w[j] & 0x7fff7fffu);
       }
-      code[j] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
-      if (bad) code[j] = 0;
+      m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = max(m & 0xffffu, m >> 16);
+      if (!in) continue;
+      const bool bad = m >= 0x7f80u;
+      // of bf16's largest value 127 steps of 2^121 fall short, but 64 of 2^122 are infinite
+      const uint32_t e = min(max(static_cast<int>(m >> 7) - 6 + ((m & 0x7f) == 0x7f), 1), 248);
+      const float inv = __uint_as_float((254u - e) << 23);
+      uint32_t code[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t b[4];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint32_t w = p[u].w[2 * j + k];
+          if (m == 0x7f7fu) w -= __vcmpeq2(w & 0x7fff7fffu, 0x7f7f7f7fu) & 0x00010001u;  // the value below it is 127 steps
+          // the product is exact; the sum rounds it to an integer, whose low byte is the code
+          b[2 * k] = __float_as_uint(fmaf(__uint_as_float(w << 16), inv, 12582912.f));
+          b[2 * k + 1] = __float_as_uint(fmaf(__uint_as_float(w & 0xffff0000u), inv, 12582912.f));
+        }
+        code[j] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+        if (bad) code[j] = 0;
+      }
+      *reinterpret_cast<uint4*>(x.kept + i * 16) = make_uint4(code[0], code[1], code[2], code[3]);
+      if (!(i & 1)) x.kept[x.pieces * 16 + i / 2] = static_cast<uint8_t>(bad ? 255u : e);
     }
-    *reinterpret_cast<uint4*>(x.kept + i * 16) = make_uint4(code[0], code[1], code[2], code[3]);
-    if (!(i & 1)) x.kept[x.pieces * 16 + i / 2] = static_cast<uint8_t>(bad ? 255u : e);
   }
 }
 
@@ -118,54 +125,57 @@ __device__ __forceinline__ void codes_up(uint32_t c, float* x) {
 __global__ void __launch_bounds__(kThreads) restore_kernel(const __grid_constant__ ActArgs a) {
   const int ti = find(a, blockIdx.x);
   const ActTensor& x = a.t[ti];
-  const int64_t i0 = static_cast<int64_t>(blockIdx.x - a.first_block[ti]) * kPiecesCta + threadIdx.x;
+  const int64_t begin = static_cast<int64_t>(blockIdx.x - a.first_block[ti]) * a.pieces_cta;
+  const int64_t end = min(x.pieces, begin + a.pieces_cta);
   if (a.zero && blockIdx.x == 0 && threadIdx.x < 2) a.zero[threadIdx.x] = 0;
   const bool sums = ti == a.sums;  // rows is dO, and the row sums of dO * value are wanted
-  uint4 c[kUnroll];
-  uint8_t e[kUnroll];
-  Piece d[kUnroll];
+  for (int64_t i0 = begin + threadIdx.x; i0 - threadIdx.x < end; i0 += kPiecesRound) {
+    uint4 c[kUnroll];
+    uint8_t e[kUnroll];
+    Piece d[kUnroll];
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    const int64_t i = i0 + u * kThreads;
-    if (i >= x.pieces) continue;
-    c[u] = __ldcs(reinterpret_cast<const uint4*>(x.kept + i * 16));
-    e[u] = x.kept[x.pieces * 16 + i / 2];
-    if (sums) d[u] = load_piece(static_cast<const __nv_bfloat16*>(x.rows) + i * 16);
-  }
-#pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    const int64_t i = i0 + u * kThreads;
-    const bool in = i < x.pieces;
-    float v[16];
-    if (in) {
-      const uint32_t w[4] = {c[u].x, c[u].y, c[u].z, c[u].w};
-      const float s = scale_of(e[u]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) codes_up(w[j], v + 4 * j);
-#pragma unroll
-      for (int j = 0; j < 16; ++j) v[j] *= s;
+    for (int u = 0; u < kUnroll; ++u) {
+      const int64_t i = i0 + u * kThreads;
+      if (i >= x.pieces) continue;
+      c[u] = __ldcs(reinterpret_cast<const uint4*>(x.kept + i * 16));
+      e[u] = x.kept[x.pieces * 16 + i / 2];
+      if (sums) d[u] = load_piece(static_cast<const __nv_bfloat16*>(x.rows) + i * 16);
     }
-    if (!sums) {
-      if (!in) continue;
-      uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(x.rows) + piece_at(x, static_cast<uint32_t>(i)));
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        out[h] = make_uint4(pack_bf16x2(v[8 * h], v[8 * h + 1]), pack_bf16x2(v[8 * h + 2], v[8 * h + 3]),
-                            pack_bf16x2(v[8 * h + 4], v[8 * h + 5]), pack_bf16x2(v[8 * h + 6], v[8 * h + 7]));
-      continue;
-    }
-    float sum = 0.f;
-    if (in) {
+    for (int u = 0; u < kUnroll; ++u) {
+      const int64_t i = i0 + u * kThreads;
+      const bool in = i < x.pieces;
+      float v[16];
+      if (in) {
+        const uint32_t w[4] = {c[u].x, c[u].y, c[u].z, c[u].w};
+        const float s = scale_of(e[u]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        sum = fmaf(__uint_as_float(d[u].w[j] << 16), v[2 * j], sum);
-        sum = fmaf(__uint_as_float(d[u].w[j] & 0xffff0000u), v[2 * j + 1], sum);
+        for (int j = 0; j < 4; ++j) codes_up(w[j], v + 4 * j);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] *= s;
       }
+      if (!sums) {
+        if (!in) continue;
+        uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(x.rows) + piece_at(x, static_cast<uint32_t>(i)));
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          out[h] = make_uint4(pack_bf16x2(v[8 * h], v[8 * h + 1]), pack_bf16x2(v[8 * h + 2], v[8 * h + 3]),
+                              pack_bf16x2(v[8 * h + 4], v[8 * h + 5]), pack_bf16x2(v[8 * h + 6], v[8 * h + 7]));
+        continue;
+      }
+      float sum = 0.f;
+      if (in) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          sum = fmaf(__uint_as_float(d[u].w[j] << 16), v[2 * j], sum);
+          sum = fmaf(__uint_as_float(d[u].w[j] & 0xffff0000u), v[2 * j + 1], sum);
+        }
+      }
+      // a head's lanes lie side by side, and its pieces begin at a multiple of their number
+      for (int k = 1; k < a.head_pieces; k *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+      const uint32_t place = static_cast<uint32_t>(i), th = place / a.head_pieces;
+      if (in && place % a.head_pieces == 0) a.delta[static_cast<int64_t>(th % a.heads) * a.T + th / a.heads] = sum;
     }
-    // a head's lanes lie side by side, and its pieces begin at a multiple of their number
-    for (int k = 1; k < a.head_pieces; k *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, k);
-    const uint32_t place = static_cast<uint32_t>(i), th = place / a.head_pieces;
-    if (in && place % a.head_pieces == 0) a.delta[static_cast<int64_t>(th % a.heads) * a.T + th / a.heads] = sum;
   }
 }
 
@@ -179,9 +189,12 @@ int launched(const char* what, std::string* err) {
 // Deals the tensors out to CTAs; false when there are too many.
 bool deal(ActArgs* a, int64_t* blocks) {
   int64_t b = 0;
+  for (int i = 0; i < a->n; ++i) b += (a->t[i].pieces + kPiecesRound - 1) / kPiecesRound;
+  a->pieces_cta = kPiecesRound * (b > kManyRounds ? kRounds : 1);
+  b = 0;
   for (int i = 0; i < kActTensors; ++i) {
     a->first_block[i] = static_cast<int32_t>(b);
-    if (i < a->n) b += (a->t[i].pieces + kPiecesCta - 1) / kPiecesCta;
+    if (i < a->n) b += (a->t[i].pieces + a->pieces_cta - 1) / a->pieces_cta;
     if (b > INT32_MAX) return false;
   }
   // tensors without CTAs (an empty one, or none) are stepped over: the next one's first

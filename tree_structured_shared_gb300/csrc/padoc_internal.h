@@ -271,6 +271,7 @@ struct ActArgs {
   ActTensor t[kActTensors];
   int32_t n;
   int32_t first_block[kActTensors];
+  int64_t pieces_cta;  // the launcher's
   // the tensor whose row sums with `rows` are wanted instead of its values, or -1
   int32_t sums;
   float* delta;  // [heads][T]
