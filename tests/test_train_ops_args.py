@@ -28,7 +28,7 @@ def scaling(**kw):
 @pytest.mark.parametrize("kw", [dict(base=1.0), dict(base=float("inf")), dict(base=float("nan")), dict(rot_dim=0), dict(rot_dim=48),
                                 dict(rot_dim=160), dict(kind=-1), dict(kind=5), dict(factor=0.5), dict(factor=float("nan")),
                                 dict(context=0.0), dict(turns_lo=0.0), dict(turns_lo=33.0), dict(amplitude=-1.0),
-                                dict(amplitude=float("inf")), dict(kind=padoc.ROPE_BASE, base=1e300, factor=1e300)])
+                                dict(amplitude=float("inf")), dict(amplitude=1e39), dict(kind=padoc.ROPE_BASE, base=1e300, factor=1e300)])
 def test_table(L, kw):
     refused(L.padoc_rope_table(C.byref(scaling(**kw)), 0, 16, A, None))
 
@@ -59,6 +59,7 @@ def test_apply(L):
     refused(apply(L, [q], rot=48))
     refused(apply(L, [q], rot=160))
     refused(apply(L, [q], n=-1))
+    refused(apply(L, [q], pos=A + 2))
     refused(apply(L, [q], n=101))                       # no positions, and a shorter table
     refused(apply(L, [q], table=None))
     refused(apply(L, [q], table=A + 4))
@@ -137,7 +138,7 @@ LOSS, LSE, WS = A + (3 << 32), A + (4 << 32), A + (5 << 32)
 @pytest.mark.parametrize("kw,code", [(dict(n=-1), INV), (dict(D=0), INV), (dict(D=60), INV), (dict(V=0), INV), (dict(h=None), INV),
                                      (dict(w=None), INV), (dict(targets=None), INV), (dict(h=A + 2), INV), (dict(w=A + 8), INV),
                                      (dict(h_stride=56), INV), (dict(h_stride=68), INV), (dict(w_stride=56), INV),
-                                     (dict(n=(1 << 28) + 1), UNS), (dict(V=1 << 29), UNS), (dict(n=1 << 28, V=1 << 28), UNS)])
+                                     (dict(n=(1 << 25) + 1), UNS), (dict(targets=A + 1), INV), (dict(V=1 << 29), UNS), (dict(n=1 << 28, V=1 << 28), UNS)])
 def test_loss(L, kw, code):
     h = head(**kw)
     refused(L.padoc_lm_loss(C.byref(h), LOSS, LSE, WS, 1 << 32, None), code)
@@ -154,12 +155,13 @@ def test_loss_places(L):
     for args in ((None, LSE, WS, 1 << 32), (LOSS, None, WS, 1 << 32), (LOSS, LSE, None, 1 << 32), (LOSS, LSE, WS + 16, 1 << 32),
                  (LOSS, LSE, WS, size.value - 1), (LOSS, LOSS, WS, 1 << 32), (LOSS, LOSS + 36, WS, 1 << 32),
                  (h.h + 64, LSE, WS, 1 << 32), (h.targets, LSE, WS, 1 << 32), (LOSS, WS + 64, WS, 1 << 32),
-                 (LOSS, LSE, h.w - 256, 1 << 32)):
+                 (LOSS, LSE, h.w - 256, 1 << 32), (LOSS + 2, LSE, WS, 1 << 32), (LOSS, LSE + 1, WS, 1 << 32)):
         refused(L.padoc_lm_loss(C.byref(h), *args, None))
     dh, dw = A + (6 << 32), A + (7 << 32)
     for args in ((None, LOSS, dh, dw, WS), (LSE, None, dh, dw, WS), (LSE, LOSS, dh + 2, dw, WS), (LSE, LOSS, dh, dw + 8, WS),
                  (LSE, LOSS, dh, dh + 128, WS), (LSE, LOSS, h.h, dw, WS), (LSE, LOSS, dh, h.w, WS), (LSE, LOSS, LSE, dw, WS),
-                 (LSE, LOSS, dh, dw, None), (LSE, LOSS, WS + 256, dw, WS)):
+                 (LSE, LOSS, dh, dw, None), (LSE, LOSS, WS + 256, dw, WS), (LSE + 2, LOSS, dh, dw, WS),
+                 (LSE, LOSS + 3, dh, dw, WS)):
         refused(L.padoc_lm_loss_bwd(C.byref(h), *args, 1 << 32, None))
     refused(L.padoc_lm_loss_bwd(C.byref(h), LSE, LOSS, dh, dw, WS, both.value - 1, None))
     assert L.padoc_lm_loss_bwd(C.byref(h), LSE, LOSS, None, None, WS, 1 << 32, None) == 0  # nothing is wanted

@@ -13,6 +13,7 @@ using namespace padoc;
 namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // n rows of `row` bytes, `step` bytes apart.
 struct Rows {
@@ -64,7 +65,7 @@ extern "C" int padoc_rope_table(const padoc_rope_scaling* sc, int64_t first, int
     if (!(sc->turns_lo > 0.0) || !(sc->turns_hi > sc->turns_lo) || !std::isfinite(sc->turns_hi))
       return set_error(PADOC_ERR_INVALID, "rope_table: turns must satisfy 0 < turns_lo < turns_hi");
   }
-  if (!(sc->amplitude >= 0.0) || !std::isfinite(sc->amplitude))
+  if (!(sc->amplitude >= 0.0) || !std::isfinite(static_cast<float>(sc->amplitude)))
     return set_error(PADOC_ERR_INVALID, "rope_table: amplitude must be a finite number of at least 0 (0 means 1)");
   if (first < 0 || n_pos < 0 || first > INT32_MAX - static_cast<int64_t>(n_pos))
     return set_error(PADOC_ERR_INVALID, "rope_table: positions must lie in [0, 2^31)");
@@ -118,6 +119,7 @@ extern "C" int padoc_rope_apply(const padoc_rope* rope, int32_t n_parts, const p
   if (rope->rot_dim < 0 || rope->rot_dim > d || rope->rot_dim % 32)
     return set_error(PADOC_ERR_INVALID, "rope_apply: rot_dim must be a multiple of 32 in [0, d]");
   if (n < 0) return set_error(PADOC_ERR_INVALID, "rope_apply: negative row count");
+  if (!aligned4(positions)) return set_error(PADOC_ERR_INVALID, "rope_apply: positions must be aligned to 4 bytes");
   const int size = dtype == PADOC_BF16 ? 2 : 4, vec = 16 / size;
   RopeArgs a{};
   int64_t heads = 0;
@@ -243,7 +245,7 @@ static int lm_shape(int32_t n, int32_t D, int32_t V, const char* what) {
   if (n < 0 || D <= 0 || V <= 0 || D % 8)
     return set_error(PADOC_ERR_INVALID, "%s: n must not be negative, V positive, and D a positive multiple of 8", what);
   const int64_t tiles = ((static_cast<int64_t>(n) + 255) / 256) * ((static_cast<int64_t>(V) + 255) / 256);
-  if (n > (1 << 28) || D > (1 << 20) || V > (1 << 28) || tiles > (1 << 28))
+  if (n > (1 << 25) || D > (1 << 20) || V > (1 << 28) || tiles > (1 << 28))
     return set_error(PADOC_ERR_UNSUPPORTED, "%s: n, D, V or n * V is too large", what);
   return PADOC_OK;
 }
@@ -262,8 +264,8 @@ static int lm_check(const padoc_lm_head* head, const void* ws, size_t ws_bytes, 
   const int rc = lm_shape(head->n, head->D, head->V, what);
   if (rc) return rc;
   if (head->n == 0) return PADOC_OK;
-  if (!head->h || !head->w || !head->targets || !aligned16(head->h) || !aligned16(head->w))
-    return set_error(PADOC_ERR_INVALID, "%s: h and w must be 16-byte aligned device pointers, and targets a device pointer", what);
+  if (!head->h || !head->w || !head->targets || !aligned16(head->h) || !aligned16(head->w) || !aligned4(head->targets))
+    return set_error(PADOC_ERR_INVALID, "%s: h and w must be 16-byte aligned device pointers, and targets a 4-byte aligned one", what);
   if (head->h_stride < head->D || head->w_stride < head->D || head->h_stride % 8 || head->w_stride % 8)
     return set_error(PADOC_ERR_INVALID, "%s: row strides must be multiples of 8 of at least D", what);
   const size_t need = lm_plan(head->n, head->D, head->V, backward).bytes;
@@ -300,7 +302,8 @@ extern "C" int padoc_lm_loss(const padoc_lm_head* head, float* loss, float* lse,
   LmCall l{};
   int rc = lm_check(head, ws, ws_bytes, false, &l, "lm_loss");
   if (rc || head->n == 0) return rc;
-  if (!loss || !lse) return set_error(PADOC_ERR_INVALID, "lm_loss: null output");
+  if (!loss || !lse || !aligned4(loss) || !aligned4(lse))
+    return set_error(PADOC_ERR_INVALID, "lm_loss: loss and lse must be 4-byte aligned device pointers");
   const int64_t n4 = static_cast<int64_t>(l.n) * 4;
   const Rows out[3] = {range(loss, n4), range(lse, n4), range(ws, static_cast<int64_t>(lm_plan(l.n, l.D, l.V, false).bytes))};
   rc = lm_apart(head, nullptr, 0, out, 3, "lm_loss");
@@ -325,7 +328,8 @@ extern "C" int padoc_lm_loss_bwd(const padoc_lm_head* head, const float* lse, co
     const cudaError_t e = cudaMemsetAsync(dw, 0, static_cast<size_t>(w_bytes), reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PADOC_OK : set_error(PADOC_ERR_CUDA, "lm_loss_bwd: cudaMemsetAsync: %s", cudaGetErrorString(e));
   }
-  if (!lse || !d_loss) return set_error(PADOC_ERR_INVALID, "lm_loss_bwd: null lse or d_loss");
+  if (!lse || !d_loss || !aligned4(lse) || !aligned4(d_loss))
+    return set_error(PADOC_ERR_INVALID, "lm_loss_bwd: lse and d_loss must be 4-byte aligned device pointers");
   if (!dh && !dw) return PADOC_OK;
   const int64_t n4 = static_cast<int64_t>(l.n) * 4;
   const Rows in[2] = {range(lse, n4), range(d_loss, n4)};
