@@ -417,7 +417,8 @@ PADOC_API int padoc_rope_apply(const padoc_rope* rope, int32_t n_parts, const pa
  *   ws         device, 256-byte aligned, padoc_lm_loss_ws_size bytes (of the
  *              forward call, or with backward set enough for both), not in use
  *              by a running call; nothing in it has to outlive a call
- * D must be a multiple of 8.  Outputs and ws overlap nothing else.  The work
+ * D must be a multiple of 8; n up to 2^25, D to 2^20, V to 2^28, and 2^28 tiles
+ * of 256 rows and words.  Outputs and ws overlap nothing else.  The work
  * follows the number of rows that have a target, which the host need not know.
  * Results are deterministic (atomics only hand units out).  No host memory is
  * read after a call returns, so calls may be captured. */
