@@ -28,7 +28,8 @@
 //
 // Roles of a CTA (352 threads): warps 0-7 epilogue (TMEM lanes 32 (w % 4), columns
 // 128 (w / 4) of the tile), warp 8 TMA producer; of the pair's first CTA, warp 9 issues
-// the products and warp 10 draws the units.  Shared memory: a ring of six
+// the products and warp 10 draws the units (of the second, it passes on that they were
+// read).  Shared memory: a ring of six
 // stages of 64 k (A 128 rows, B 128 rows, 16 KB each).  TMEM: two accumulators.
 // Barriers that both CTAs use live in the first: a stage is full when both CTAs' copies
 // are in; an accumulator is free when both have read it.  The commit of a stage's
@@ -53,6 +54,7 @@
 //   a tile leaves TMEM at once, before it is worked on, packed arithmetic 11.0, 137
 //   units worked out by the thread that draws them, which is a warp of its own 10.7, 132
 //   "read" signalled by an arrival that does not wait for the thread's stores 10.6, 120
+//   (as a release at cluster scope, which does: one row's forward 71 us instead of 63)
 // Tried without gain: copies of a row tile's rows that exist in boxes of 32 (10 % slower),
 // another k to start with for each tile, waits without acquire in the issuer, a ring of
 // eleven smaller stages for few rows, the first words asked for ahead of the rows, dw stored
@@ -95,8 +97,9 @@ enum {
   B_ACC_FULL = B_EMPTY + kStages,   // +accumulator (2)
   B_ACC_FREE = B_ACC_FULL + 2,      // +accumulator (2), count 16: both CTAs' epilogues (first CTA)
   B_U_FULL = B_ACC_FREE + 2,        // +slot: the ring's slot holds a unit
-  B_U_FREE = B_U_FULL + kURing,     // +slot, count 19: all readers have it (first CTA)
-  B_DRAIN = B_U_FREE + kURing,
+  B_U_FREE = B_U_FULL + kURing,     // +slot, count 11: all readers have it (first CTA)
+  B_U_READ = B_U_FREE + kURing,     // +slot, count 9: the second CTA's readers have it (there)
+  B_DRAIN = B_U_READ + kURing,
   N_BARS
 };
 constexpr int SM_UNIT = (SM_BAR + N_BARS * 8 + 15) / 16 * 16;  // unit ring
@@ -104,7 +107,7 @@ constexpr int SM_MISC = SM_UNIT + kURing * 32;   // TMEM address, abort flag, un
 constexpr int kSmemBytes = SM_MISC + 16 + 1024;   // and room to align the ring
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr int kUReaders = 1 + 2 * kEpiWarps + 2;  // the issuer, both epilogues and producers
+constexpr int kUReaders = 1 + kEpiWarps;  // of a CTA, but for the issuer: its producer and epilogue
 
 // ---------------------------------------------------------------- pairs of CTAs
 __device__ __forceinline__ uint32_t cta_rank() {
@@ -120,14 +123,15 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Arrivals at a shared::cluster address.  The first says that a slot or accumulator has
-// been read; it orders nothing beyond this CTA, so it does not wait for the caller's stores
-// to global memory (which a release at cluster scope does, about a microsecond a time).
+// Arrivals at a shared::cluster address.  The first says that an accumulator has been read,
+// by loads that the caller has waited for.  It does not wait for the caller's stores to
+// global memory (which a release at cluster scope does, about a microsecond a time).
 __device__ __forceinline__ void arrive_read(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// What the caller wrote to either CTA's shared memory comes before it.
-__device__ __forceinline__ void arrive_written(uint32_t bar) {
+// What the caller read from or wrote to either CTA's shared memory comes before it, and what
+// others of its CTA did before they arrived at a barrier that the caller waited for.
+__device__ __forceinline__ void arrive_released(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void st_cluster_v4(uint32_t addr, int a, int b, int c, int d) {
@@ -153,7 +157,7 @@ __device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) 
   return ok != 0;
 }
 // Waits for a phase; false when `limit` nanoseconds ran out or another role of the CTA gave
-// up.  CLUSTER: what the other CTA wrote before it arrived is wanted.
+// up.  CLUSTER: what the other CTA did before it arrived comes before what follows.
 template <bool CLUSTER>
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit) {
   const auto is_over = [&] { return CLUSTER ? try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
@@ -401,7 +405,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < N_BARS; ++i) {
       const int count = (i >= B_ACC_FREE && i < B_ACC_FREE + 2)       ? 2 * kEpiWarps
-                        : (i >= B_U_FREE && i < B_U_FREE + kURing) ? kUReaders
+                        : (i >= B_U_FREE && i < B_U_FREE + kURing) ? kUReaders + 2
+                        : (i >= B_U_READ && i < B_U_READ + kURing) ? kUReaders
                                                                    : 1;
       mbar_init(bar(i), count);
     }
@@ -420,6 +425,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   wait_for_previous();
   const Counts c = counts<FWD>(a);
 
+  // A unit has been read: said within the CTA; the second CTA's draw warp passes it on.
+  const int unit_read = rank == 0 ? B_U_FREE : B_U_READ;
+
   if (warp == kProducerWarp) {
     if (lane == 0) {
       const uint32_t full0 = in_cta(bar(B_FULL), 0);
@@ -431,7 +439,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           break;
         }
         const Unit x = taken(sbase + SM_UNIT + 32 * slot);
-        arrive_read(in_cta(bar(B_U_FREE + slot), 0));
+        mbar_arrive(bar(unit_read + slot));
         *begun = ++uk;
         if (x.kind == END) break;
         bool ok = true;
@@ -477,13 +485,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (uint32_t uk = 0;; ++uk) {
         const int slot = uk % kURing;
         const Unit x = unit_of(a, c, next);
-        if (!wait<false>(bar(B_U_FREE + slot), ((uk / kURing) & 1) ^ 1, abort, a.wait_limit)) {
+        if (!wait<true>(bar(B_U_FREE + slot), ((uk / kURing) & 1) ^ 1, abort, a.wait_limit)) {
           give_up(abort, 1u);
           break;
         }
         for (uint32_t r = 0; r < 2; ++r) {
           publish(in_cta(sbase + SM_UNIT + 32 * slot, r), x);
-          arrive_written(in_cta(bar(B_U_FULL + slot), r));
+          arrive_released(in_cta(bar(B_U_FULL + slot), r));
         }
         if (x.kind == END) break;
         if (x.nkb * x.tiles > kLongUnit) {
@@ -491,6 +499,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           while (*begun <= uk && !*abort && global_timer() - t0 < a.wait_limit) __nanosleep(100);
         }
         next = gridDim.x / 2 + atomicAdd(a.counter, 1);
+      }
+    } else if (lane == 0) {
+      for (uint32_t uk = 0;; ++uk) {
+        const int slot = uk % kURing;
+        const uint32_t phase = (uk / kURing) & 1;
+        if (!wait<true>(bar(B_U_FULL + slot), phase, abort, a.wait_limit)) {
+          give_up(abort, 256u);
+          break;
+        }
+        const bool last = taken(sbase + SM_UNIT + 32 * slot).kind == END;
+        if (!wait<false>(bar(B_U_READ + slot), phase, abort, a.wait_limit)) {
+          give_up(abort, 512u);
+          break;
+        }
+        arrive_released(in_cta(bar(B_U_FREE + slot), 0));
+        if (last) break;
       }
     }
     __syncwarp();
@@ -505,7 +529,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           break;
         }
         const Unit x = taken(sbase + SM_UNIT + 32 * slot);
-        arrive_read(in_cta(bar(B_U_FREE + slot), 0));
+        mbar_arrive(bar(unit_read + slot));
         ++uk;
         if (x.kind == END) break;
         const bool a_mn = x.kind == DW, b_mn = x.kind != REC;
@@ -564,7 +588,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       const Unit x = taken(sbase + SM_UNIT + 32 * slot);
       __syncwarp();
-      if (lane == 0) arrive_read(in_cta(bar(B_U_FREE + slot), 0));
+      if (lane == 0) mbar_arrive(bar(unit_read + slot));
       ++uk;
       if (x.kind == END) break;
       const int row = x.m * 256 + r_in;
