@@ -303,8 +303,10 @@ __device__ __forceinline__ uint4 pack8(const uint32_t* w) {
 }
 
 // A row's 128 logits of words from `word` into its running maximum and sum; its target's
-// into *picked.  Exponents are x log2(e) - m log2(e) in one fma: the rounding of the second
-// term is common to all of a row and moves lse by half a step of its own.
+// into *picked.  The maximum comes off before log2(e) multiplies: its own exponential is 1
+// and a sum whose maximum stays is kept as it is, so the sum is that of exp(x - maximum) at
+// any size of the logits.  (Taken off as the rounded product m log2(e), in one fma, the sum
+// is a factor of up to 2^(|m| 2^-24) off, once more each tile.)
 __device__ __forceinline__ void reduce_tile(uint32_t (&v)[2][64], int word, int V, int target, float& top, float& sum,
                                             float* picked) {
   if (word + 128 > V) {
@@ -318,13 +320,13 @@ __device__ __forceinline__ void reduce_tile(uint32_t (&v)[2][64], int word, int 
     m[i & 3] = max3f(m[i & 3], __uint_as_float(v[i >> 5][2 * (i & 31)]), __uint_as_float(v[i >> 5][2 * (i & 31) + 1]));
   const float t = fmaxf(max3f(m[0], m[1], m[2]), m[3]);
   // all -inf so far: any finite reference keeps the exponentials at zero
-  const float ref = t == -INFINITY ? 0.f : t * kLog2e;
+  const float ref = t == -INFINITY ? 0.f : t;
   const uint64_t scale = f2pack(kLog2e, kLog2e), less = f2pack(-ref, -ref);
   uint64_t s[4];
 #pragma unroll
   for (int i = 0; i < 64; ++i) {
-    const uint64_t y = fma2(f2pack(__uint_as_float(v[i >> 5][2 * (i & 31)]), __uint_as_float(v[i >> 5][2 * (i & 31) + 1])),
-                            scale, less);
+    const uint64_t y = mul2(
+        add2(f2pack(__uint_as_float(v[i >> 5][2 * (i & 31)]), __uint_as_float(v[i >> 5][2 * (i & 31) + 1])), less), scale);
     float lo, hi;
     f2unpack(y, lo, hi);
     const uint64_t e = f2pack(fast_exp2(lo), fast_exp2(hi));
@@ -332,7 +334,7 @@ __device__ __forceinline__ void reduce_tile(uint32_t (&v)[2][64], int word, int 
   }
   float lo, hi;
   f2unpack(add2(add2(s[0], s[1]), add2(s[2], s[3])), lo, hi);
-  sum = fmaf(sum, fast_exp2(fmaf(top, kLog2e, -ref)), lo + hi);
+  sum = fmaf(sum, fast_exp2((top - ref) * kLog2e), lo + hi);
   top = t;
   // last, so that the target has arrived
   const int hit = target - word;
