@@ -348,10 +348,11 @@ __device__ __forceinline__ void reduce_tile(uint32_t (&v)[2][64], int word, int 
 }
 
 // G of a row's 128 words from `word`, bf16 (or what that rounding leaves of it), to `out`,
-// the second 64 `block` on; zero from word V on.
-__device__ __forceinline__ void gradient_tile(const uint32_t (&v)[2][64], int word, int V, int target, float off,
+// the second 64 `block` on; zero from word V on.  As above, lse comes off first: of a sure
+// target, whose logit is nearly lse, the difference is exact.
+__device__ __forceinline__ void gradient_tile(const uint32_t (&v)[2][64], int word, int V, int target, float lse,
                                               float d_loss, bool rest, __nv_bfloat16* out, int64_t block) {
-  const uint64_t scale = f2pack(kLog2e, kLog2e), less = f2pack(-off, -off), by = f2pack(d_loss, d_loss);
+  const uint64_t scale = f2pack(kLog2e, kLog2e), less = f2pack(-lse, -lse), by = f2pack(d_loss, d_loss);
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const int hit = target - word - 32 * q;
@@ -362,7 +363,7 @@ __device__ __forceinline__ void gradient_tile(const uint32_t (&v)[2][64], int wo
         float p[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          p[k] = fast_exp2(fmaf(__uint_as_float(v[q >> 1][32 * (q & 1) + 2 * i + k]), kLog2e, -off));
+          p[k] = fast_exp2((__uint_as_float(v[q >> 1][32 * (q & 1) + 2 * i + k]) - lse) * kLog2e);
           if (hit == 2 * i + k) p[k] -= 1.f;
           p[k] = word + 32 * q + 2 * i + k < V ? p[k] * d_loss : 0.f;
         }
@@ -374,9 +375,10 @@ __device__ __forceinline__ void gradient_tile(const uint32_t (&v)[2][64], int wo
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         float lo, hi;
-        f2unpack(fma2(f2pack(__uint_as_float(v[q >> 1][32 * (q & 1) + 2 * i]),
-                             __uint_as_float(v[q >> 1][32 * (q & 1) + 2 * i + 1])),
-                      scale, less),
+        f2unpack(mul2(add2(f2pack(__uint_as_float(v[q >> 1][32 * (q & 1) + 2 * i]),
+                                  __uint_as_float(v[q >> 1][32 * (q & 1) + 2 * i + 1])),
+                           less),
+                      scale),
                  lo, hi);
         f2unpack(mul2(f2pack(fast_exp2(lo), fast_exp2(hi)), by), lo, hi);
         g[i] = pack_bf16x2(lo, hi);
@@ -597,11 +599,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int place = c.twice ? row & (kTwice - 1) : row;  // among the rows with a target
       const bool has_row = place < c.rows;
       int target = -1;
-      float off = 0.f, d_loss = 0.f;
+      float lse = 0.f, d_loss = 0.f;
       if (x.kind == REC && has_row) {
         target = a.targets[place];
         if (!FWD) {
-          off = a.lse[place] * kLog2e;
+          lse = a.lse[place];
           d_loss = a.d_loss[place];
         }
       }
@@ -626,7 +628,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (FWD) {
           reduce_tile(v, col, a.V, target, top, sum, a.picked + row);
         } else if (x.kind == REC) {
-          gradient_tile(v, a.rec_v0 + col, has_row ? a.V : 0, target, off, d_loss,
+          gradient_tile(v, a.rec_v0 + col, has_row ? a.V : 0, target, lse, d_loss,
                         c.twice && rank == 1, a.g_out + (static_cast<int64_t>(col / 64) * a.g_rows + row) * 64, static_cast<int64_t>(a.g_rows) * 64);
         } else if (x.kind == DH) {
           if (!has_row) continue;
