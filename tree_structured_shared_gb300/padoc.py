@@ -385,6 +385,8 @@ class LmLoss:
             raise PadocError(ERR_INVALID, "LmLoss: a row's values and the targets must follow one another")
         if not (_is_bf16(h) and _is_bf16(w)) or targets.dtype is not sys.modules["torch"].int32:
             raise PadocError(ERR_INVALID, "LmLoss: h and w must be bf16 and the targets int32")
+        if h.device != w.device or h.device != targets.device:
+            raise PadocError(ERR_INVALID, "LmLoss: h, w and targets must be on one device")
         self.c = LmHead(_ptr(h), h.stride(0) if n > 1 else D, _ptr(w), w.stride(0) if V > 1 else D, _ptr(targets), n, D, V)
         self.ref = C.byref(self.c)
 
@@ -393,10 +395,33 @@ class LmLoss:
         _check(lib().padoc_lm_loss_ws_size(self.c.n, self.c.D, self.c.V, int(bool(backward)), C.byref(b)))
         return b.value
 
+    def _dense(self, **tensors):
+        """Refuses tensors (name=(x, bf16 or else f32, values)) that the library would read or
+        write past their end, or as another type or layout than theirs."""
+        torch, at = sys.modules["torch"], self._keep[0].device
+        for name, (x, bf16, m) in tensors.items():
+            if x is None or isinstance(x, int):
+                continue
+            if x.dtype is not (torch.bfloat16 if bf16 else torch.float32) or x.numel() < m or not x.is_contiguous() or x.device != at:
+                raise PadocError(ERR_INVALID, f"LmLoss: {name} must be {m} dense {'bf16' if bf16 else 'f32'} values beside h")
+
+    def _room(self, ws, ws_bytes: int):
+        if not (ws is None or isinstance(ws, int)) and (ws.nbytes < ws_bytes or not ws.is_contiguous()):
+            raise PadocError(ERR_INVALID, "LmLoss: ws is smaller than ws_bytes, or not dense")
+
     def forward(self, loss, lse, ws, ws_bytes: int, stream=None):
+        """loss and lse: dense f32 of n values."""
+        n = self.c.n
+        self._dense(loss=(loss, False, n), lse=(lse, False, n))
+        self._room(ws, ws_bytes)
         _check(lib().padoc_lm_loss(self.ref, _ptr(loss), _ptr(lse), _ptr(ws), int(ws_bytes), _stream(stream)))
 
     def backward(self, lse, d_loss, dh, dw, ws, ws_bytes: int, stream=None):
+        """lse and d_loss: dense f32 of n values (an expanded one is refused: make it
+        contiguous); dh, dw: dense bf16 of n * D and V * D, or None."""
+        n, D = self.c.n, self.c.D
+        self._dense(lse=(lse, False, n), d_loss=(d_loss, False, n), dh=(dh, True, n * D), dw=(dw, True, self.c.V * D))
+        self._room(ws, ws_bytes)
         _check(lib().padoc_lm_loss_bwd(self.ref, _ptr(lse), _ptr(d_loss), _ptr(dh), _ptr(dw), _ptr(ws), int(ws_bytes),
                                        _stream(stream)))
 
