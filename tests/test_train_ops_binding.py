@@ -74,3 +74,42 @@ def test_inputs_on_one_device():
         a = [h, w, t]
         a[i] = a[i].to("meta")
         refused(padoc.LmLoss, *a)
+
+
+def rope(x, out, H=2, d=64, n=6, **kw):
+    padoc.rope_apply(padoc.Rope(4096, 64, n_pos=100), n, d, x, out, H, **kw)
+
+
+def test_rope_rows():
+    bf = dict(dtype=torch.bfloat16)
+    x, out = torch.zeros(6, 128, **bf), torch.zeros(6, 2, 64, **bf)
+    i32 = torch.zeros(6, dtype=torch.int32)
+    f32 = x.float()
+    for bad in (f32, x[:5], torch.zeros(6, 128, dtype=torch.float16), torch.zeros(6, 256, **bf)[:, ::2], torch.zeros(128, 6, **bf).T,
+                torch.zeros(6, 2, 72, **bf)[..., :64], torch.zeros(2, 3, 256, **bf)[..., :128]):
+        refused(rope, bad, out)
+        refused(rope, x, bad)
+        refused(rope, x, out, k=bad, k_out=out.clone(), Hkv=2)
+        refused(rope, x, out, k=x.clone(), k_out=bad, Hkv=2)
+    refused(rope, f32, out, q_stride=128)               # a stride does not change the type
+    refused(rope, x[:5], out, q_stride=128)
+    refused(rope, x, out, dtype=padoc.F32)
+    for bad in (i32.long(), i32[:5], torch.zeros(12, dtype=torch.int32)[::2]):
+        refused(rope, x, out, positions=bad)
+
+
+def test_rope_table():
+    for bad in (torch.zeros(10, 64, dtype=torch.float64), torch.zeros(9, 64), torch.zeros(10, 128)[:, :64]):
+        refused(padoc.rope_table, bad, 10, 64, 1.0e4)
+
+
+@pytest.mark.parametrize("make,stride", [
+    (lambda x: x, 256), (lambda x: x[:, :128], 256), (lambda x: x.view(6, 4, 64)[:, :2], 256), (lambda x: x[:, :128].contiguous(), 128),
+    (lambda x: x[:, :128].reshape(12, 64), 128), (lambda x: x[:, :128].reshape(-1), 128), (lambda x: x[:, :128].reshape(2, 3, 2, 64).contiguous(), 128),
+    (lambda x: torch.cat([x, x])[:, :128], 256), (lambda x: x.data_ptr(), 128), (lambda x: torch.cat([x, x])[:, :128].contiguous(), 128)])
+def test_rope_strides_of_tensors(make, stride):
+    """The rows that a call without strides takes."""
+    x = torch.zeros(6, 256, dtype=torch.bfloat16)
+    y = make(x)
+    assert padoc._rows(y, 6, 128, None, torch.bfloat16) == (y if isinstance(y, int) else y.data_ptr(), stride)
+    assert padoc._rows(y, 6, 128, 264, torch.bfloat16)[1] == 264

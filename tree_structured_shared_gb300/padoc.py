@@ -354,18 +354,52 @@ def rope_table(cos_sin, n_pos: int, rot_dim: int, base: float, *, kind: int = RO
                context: float = 0.0, turns_lo: float = 1.0, turns_hi: float = 32.0, amplitude: float = 1.0,
                first: int = 0, stream=None):
     """padoc_rope_table: device f32 cos_sin [n_pos, rot_dim] out."""
+    if not (cos_sin is None or isinstance(cos_sin, int)) and (
+            cos_sin.dtype is not sys.modules["torch"].float32 or cos_sin.numel() < n_pos * rot_dim or not cos_sin.is_contiguous()):
+        raise PadocError(ERR_INVALID, "rope_table: cos_sin must be n_pos * rot_dim dense f32 values")
     sc = RopeScaling(base, rot_dim, kind, factor, context, turns_lo, turns_hi, amplitude)
     _check(lib().padoc_rope_table(C.byref(sc), int(first), n_pos, _ptr(cos_sin), _stream(stream)))
+
+
+_DTYPES = {}  # F32, BF16 -> torch's, once a tensor was seen
+
+
+def _row_stride(x, n: int, row: int) -> int:
+    """Elements between the n rows of `row` values that x holds, where no stride was given."""
+    if x.dim() >= 2 and x.size(0) >= n and x[0].numel() >= row and x[0].is_contiguous():
+        return x.stride(0)  # a row each, or the head of a wider one
+    if x.is_contiguous() and (x.dim() < 2 or x[0].numel() <= row):
+        return row
+    raise PadocError(ERR_INVALID, "rope_apply: rows must be dense, or their stride be given")
+
+
+def _rows(x, n: int, row: int, stride, dtype):
+    """Address and row stride of n rows of `row` values, of a tensor or an address."""
+    if x is None or isinstance(x, int):
+        return x or 0, row if stride is None else stride
+    m = x.numel()
+    if (dtype is not None and x.dtype is not dtype) or m < n * row:
+        raise PadocError(ERR_INVALID, f"rope_apply: a tensor must be {dtype} and hold n rows of its heads")
+    if stride is None:
+        # the usual case without detours: a step of few tokens takes as long as this call
+        stride = row if m == n * row and x.is_contiguous() else _row_stride(x, n, row)
+    return x.data_ptr(), stride
 
 
 def rope_apply(rope: "Rope", n: int, d: int, q, q_out, Hq: int, k=None, k_out=None, Hkv: int = 0, *, positions=None,
                dtype: int = BF16, backward: bool = False, q_stride: Optional[int] = None, k_stride: Optional[int] = None,
                q_out_stride: Optional[int] = None, k_out_stride: Optional[int] = None, stream=None):
-    """padoc_rope_apply on q and, where given, k; strides in elements, dense where None."""
-    hq, hk = Hq * d, Hkv * d
-    parts = _PARTS(_ptr(q) or 0, hq if q_stride is None else q_stride, _ptr(q_out) or 0,
-                   hq if q_out_stride is None else q_out_stride, Hq, _ptr(k) or 0, hk if k_stride is None else k_stride,
-                   _ptr(k_out) or 0, hk if k_out_stride is None else k_out_stride, Hkv)
+    """padoc_rope_apply on q and, where given, k, whose type is dtype; strides in elements
+    between rows are taken as they are, and a tensor's own where None.  positions: int32."""
+    if not _DTYPES and (t := sys.modules.get("torch")):
+        _DTYPES.update({F32: t.float32, BF16: t.bfloat16, "positions": t.int32})
+    dt, hq, hk = _DTYPES.get(dtype), Hq * d, Hkv * d
+    if not (positions is None or isinstance(positions, int)) and (
+            positions.dtype is not _DTYPES["positions"] or positions.numel() < n or not positions.is_contiguous()):
+        raise PadocError(ERR_INVALID, "rope_apply: positions must be n dense int32 values")
+    x, o = _rows(q, n, hq, q_stride, dt), _rows(q_out, n, hq, q_out_stride, dt)
+    y, p = _rows(k, n, hk, k_stride, dt), _rows(k_out, n, hk, k_out_stride, dt)
+    parts = _PARTS(*x, *o, Hq, *y, *p, Hkv)
     rc = lib().padoc_rope_apply(rope.ref, 1 if k is None else 2, parts, dtype, d, n, _ptr(positions),
                                 1 if backward else 0, _stream(stream))
     if rc:
