@@ -461,7 +461,8 @@ PADOC_API int padoc_act_restore(int32_t n_tensors, const padoc_act* tensors, pad
  * or Hkv * d values, the forward's [T, H, d]): the gradients at the values that
  * the checkpoints stand for, with the forward's lse.  d_o, dq, dk and dv are
  * bf16.  ws of padoc_tree_attn_varlen_bwd_kept_ws_size bytes, 256-byte aligned,
- * holds q, k and v in bf16 for the time of the call; o is not expanded. */
+ * holds q, k and v in bf16 for the time of the call; o is not expanded.  dq, dk,
+ * dv and ws overlap nothing else in the call. */
 PADOC_API int padoc_tree_attn_varlen_bwd_kept_ws_size(const padoc_tree_desc* desc, int32_t Hq, int32_t Hkv, int32_t d,
                                                       size_t* bytes);
 PADOC_API int padoc_tree_attn_varlen_bwd_kept(padoc_tree_desc* desc, const void* q_kept, const void* k_kept,

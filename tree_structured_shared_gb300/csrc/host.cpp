@@ -670,6 +670,21 @@ extern "C" int padoc_tree_attn_varlen_bwd_kept(padoc_tree_desc* desc, const void
     return fail(PADOC_ERR_INVALID, "%s: ws must be 256-byte aligned and hold %zu bytes", what,
                 bwd_kept_ws_bytes(desc, Hq, Hkv, d));
   if (desc->T * Hq * d / 16 > UINT32_MAX) return fail(PADOC_ERR_UNSUPPORTED, "%s: too many values", what);
+  // Both passes read d_o, lse and the restored rows, and dq is written by the first: the
+  // outputs and the workspace lie apart from each other and from what is read.
+  const int64_t q_n = desc->T * Hq * d, k_n = desc->T * Hkv * d;
+  const struct {
+    const void* p;
+    int64_t bytes;
+  } ranges[] = {{dq, 2 * q_n}, {dk, 2 * k_n}, {dv, 2 * k_n}, {ws, static_cast<int64_t>(bwd_kept_ws_bytes(desc, Hq, Hkv, d))},
+                {q_kept, q_n + q_n / 32}, {k_kept, k_n + k_n / 32}, {v_kept, k_n + k_n / 32}, {o_kept, q_n + q_n / 32},
+                {lse, 4 * desc->T * Hq}, {d_o, 2 * q_n}};
+  for (int i = 0; i < 4; ++i)
+    for (int j = i + 1; j < 10; ++j) {
+      const uintptr_t x = reinterpret_cast<uintptr_t>(ranges[i].p), y = reinterpret_cast<uintptr_t>(ranges[j].p);
+      if (x < y + ranges[j].bytes && y < x + ranges[i].bytes)
+        return fail(PADOC_ERR_INVALID, "%s: an output or the workspace overlaps what the call reads or writes elsewhere", what);
+    }
   uint8_t* at = static_cast<uint8_t*>(ws) + bwd_ws_bytes(desc, Hq);
   void* rows[4] = {at, at + kept_rows_bytes(desc, Hq, d),
                    at + kept_rows_bytes(desc, Hq, d) + kept_rows_bytes(desc, Hkv, d), const_cast<void*>(d_o)};
