@@ -361,7 +361,7 @@ def rope_table(cos_sin, n_pos: int, rot_dim: int, base: float, *, kind: int = RO
     _check(lib().padoc_rope_table(C.byref(sc), int(first), n_pos, _ptr(cos_sin), _stream(stream)))
 
 
-_DTYPES = {}  # F32, BF16 -> torch's, once a tensor was seen
+_DTYPES = {}  # F32, BF16 -> torch's type and its bytes, once a tensor was seen
 
 
 def _row_stride(x, n: int, row: int) -> int:
@@ -373,16 +373,16 @@ def _row_stride(x, n: int, row: int) -> int:
     raise PadocError(ERR_INVALID, "rope_apply: rows must be dense, or their stride be given")
 
 
-def _rows(x, n: int, row: int, stride, dtype):
-    """Address and row stride of n rows of `row` values, of a tensor or an address."""
-    if x is None or isinstance(x, int):
+def _rows(x, n: int, row: int, stride, dtype, size: int):
+    """Address and row stride of n rows of `row` values, of a tensor or an address.  A step of
+    few tokens takes as long as the calls of this, so the usual tensor meets few of its own."""
+    if x is None or type(x) is int:
         return x or 0, row if stride is None else stride
-    m = x.numel()
-    if (dtype is not None and x.dtype is not dtype) or m < n * row:
+    m = x.nbytes
+    if x.dtype is not dtype or m < n * row * size:
         raise PadocError(ERR_INVALID, f"rope_apply: a tensor must be {dtype} and hold n rows of its heads")
     if stride is None:
-        # the usual case without detours: a step of few tokens takes as long as this call
-        stride = row if m == n * row and x.is_contiguous() else _row_stride(x, n, row)
+        stride = row if m == n * row * size and x.is_contiguous() else _row_stride(x, n, row)
     return x.data_ptr(), stride
 
 
@@ -392,16 +392,22 @@ def rope_apply(rope: "Rope", n: int, d: int, q, q_out, Hq: int, k=None, k_out=No
     """padoc_rope_apply on q and, where given, k, whose type is dtype; strides in elements
     between rows are taken as they are, and a tensor's own where None.  positions: int32."""
     if not _DTYPES and (t := sys.modules.get("torch")):
-        _DTYPES.update({F32: t.float32, BF16: t.bfloat16, "positions": t.int32})
-    dt, hq, hk = _DTYPES.get(dtype), Hq * d, Hkv * d
-    if not (positions is None or isinstance(positions, int)) and (
-            positions.dtype is not _DTYPES["positions"] or positions.numel() < n or not positions.is_contiguous()):
-        raise PadocError(ERR_INVALID, "rope_apply: positions must be n dense int32 values")
-    x, o = _rows(q, n, hq, q_stride, dt), _rows(q_out, n, hq, q_out_stride, dt)
-    y, p = _rows(k, n, hk, k_stride, dt), _rows(k_out, n, hk, k_out_stride, dt)
-    parts = _PARTS(*x, *o, Hq, *y, *p, Hkv)
-    rc = lib().padoc_rope_apply(rope.ref, 1 if k is None else 2, parts, dtype, d, n, _ptr(positions),
-                                1 if backward else 0, _stream(stream))
+        _DTYPES.update({F32: (t.float32, 4), BF16: (t.bfloat16, 2), "positions": t.int32})
+    dt, size = _DTYPES.get(dtype, (None, 0))
+    hq, hk = Hq * d, Hkv * d
+    x, xs = _rows(q, n, hq, q_stride, dt, size)
+    y, ys = _rows(q_out, n, hq, q_out_stride, dt, size)
+    if k is None:
+        count, parts = 1, _PARTS(x, xs, y, ys, Hq, 0, 0, 0, 0, 0)
+    else:
+        v, vs = _rows(k, n, hk, k_stride, dt, size)
+        w, ws = _rows(k_out, n, hk, k_out_stride, dt, size)
+        count, parts = 2, _PARTS(x, xs, y, ys, Hq, v, vs, w, ws, Hkv)
+    if positions is not None and type(positions) is not int:
+        if positions.dtype is not _DTYPES["positions"] or positions.nbytes < 4 * n or not positions.is_contiguous():
+            raise PadocError(ERR_INVALID, "rope_apply: positions must be n dense int32 values")
+        positions = positions.data_ptr()
+    rc = lib().padoc_rope_apply(rope.ref, count, parts, dtype, d, n, positions, 1 if backward else 0, _stream(stream))
     if rc:
         _check(rc)
 
