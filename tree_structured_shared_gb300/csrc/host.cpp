@@ -4,6 +4,7 @@
 #include "padoc_internal.h"
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -82,10 +83,12 @@ struct Run {
   bool causal;
 };
 
+// A descriptor's copy on a device, for a group: one allocation.
 struct DevPlan {
   int device = -1;
   int group = 0;
   int tile_tokens = 0;
+  void* base = nullptr;
   QSeg* qsegs = nullptr;
   KVSeg* kvsegs = nullptr;
   FwdItem* items = nullptr;
@@ -106,21 +109,15 @@ struct padoc_tree_desc {
   std::vector<KVSeg> kvsegs;
   std::vector<BwdItem> bitems;
   std::vector<BwdEntry> bentries;
-  int32_t n_parts[5] = {};  // parts of all key tiles' queries (build_parts), for groups 1, 2, 4, 8, 16
+  // parts of all key tiles' queries (build_parts), for groups 1, 2, 4, 8, 16: counted when asked for
+  mutable std::atomic<int32_t> n_parts[5] = {-1, -1, -1, -1, -1};
   std::vector<DevPlan> dev;
   ~padoc_tree_desc() {
     for (auto& d : dev) {
       int cur = -1;
       cudaGetDevice(&cur);
       if (d.device >= 0) cudaSetDevice(d.device);
-      cudaFree(d.qsegs);
-      cudaFree(d.kvsegs);
-      cudaFree(d.items);
-      cudaFree(d.bitems);
-      cudaFree(d.bentries);
-      cudaFree(d.sitems);
-      cudaFree(d.sentries);
-      cudaFree(d.sfirst);
+      cudaFree(d.base);
       if (cur >= 0) cudaSetDevice(cur);
     }
   }
@@ -358,8 +355,6 @@ extern "C" int padoc_tree_desc_build(const padoc_tree_spec* spec, padoc_tree_des
     }
     desc->pairs = pairs;
     build_bwd(desc.get());
-    if (few_units(desc.get(), 1))
-      for (int i = 0; i < 5; ++i) desc->n_parts[i] = count_parts(desc.get(), kTileRows >> i);
     d = desc.release();
   });
   *out = d;
@@ -451,49 +446,47 @@ static int upload_desc(padoc_tree_desc* desc, int group, DevPlan** plan_out) {
   std::vector<FwdItem> items;
   PADOC_TRY(items = build_items(desc, p.tile_tokens));
   p.n_items = static_cast<int32_t>(items.size());
-  auto alloc_copy = [](void** dst, const void* src, size_t bytes) -> cudaError_t {
-    if (bytes == 0) bytes = 16;
-    cudaError_t e2 = cudaMalloc(dst, bytes);
-    if (e2 != cudaSuccess) return e2;
-    if (src) return cudaMemcpy(*dst, src, bytes, cudaMemcpyHostToDevice);
-    return cudaSuccess;
+  // The parts go along with the rest: a captured call of the kept backward may be the first
+  // to want them, and what they add to the one copy is next to nothing.
+  std::vector<BwdItem> sitems;
+  std::vector<BwdEntry> sentries;
+  std::vector<int32_t> sfirst;
+  if (few_units(desc, 1)) PADOC_TRY(build_parts(desc, p.tile_tokens, &sitems, &sentries, &sfirst));
+  p.n_sitems = static_cast<int32_t>(sitems.size());
+  std::vector<uint8_t> image;
+  auto place = [&image](const auto& v) {
+    const size_t at = image.size(), bytes = v.size() * sizeof(v[0]);
+    image.resize(at + (bytes + 255) / 256 * 256);
+    if (bytes) std::memcpy(image.data() + at, v.data(), bytes);
+    return at;
   };
-  e = alloc_copy(reinterpret_cast<void**>(&p.qsegs), desc->qsegs.data(), desc->qsegs.size() * sizeof(QSeg));
-  if (e == cudaSuccess)
-    e = alloc_copy(reinterpret_cast<void**>(&p.kvsegs), desc->kvsegs.data(), desc->kvsegs.size() * sizeof(KVSeg));
-  if (e == cudaSuccess)
-    e = alloc_copy(reinterpret_cast<void**>(&p.items), items.data(), items.size() * sizeof(FwdItem));
-  if (e == cudaSuccess)
-    e = alloc_copy(reinterpret_cast<void**>(&p.bitems), desc->bitems.data(), desc->bitems.size() * sizeof(BwdItem));
-  if (e == cudaSuccess)
-    e = alloc_copy(reinterpret_cast<void**>(&p.bentries), desc->bentries.data(),
-                   desc->bentries.size() * sizeof(BwdEntry));
-  if (e == cudaSuccess && few_units(desc, 1)) {
-    std::vector<BwdItem> sitems;
-    std::vector<BwdEntry> sentries;
-    std::vector<int32_t> sfirst;
-    try {
-      build_parts(desc, p.tile_tokens, &sitems, &sentries, &sfirst);
-    } catch (...) {
-      e = cudaErrorMemoryAllocation;
-    }
-    p.n_sitems = static_cast<int32_t>(sitems.size());
-    if (e == cudaSuccess) e = alloc_copy(reinterpret_cast<void**>(&p.sitems), sitems.data(), sitems.size() * sizeof(BwdItem));
-    if (e == cudaSuccess)
-      e = alloc_copy(reinterpret_cast<void**>(&p.sentries), sentries.data(), sentries.size() * sizeof(BwdEntry));
-    if (e == cudaSuccess) e = alloc_copy(reinterpret_cast<void**>(&p.sfirst), sfirst.data(), sfirst.size() * sizeof(int32_t));
-  }
+  size_t at[8] = {};
+  PADOC_TRY({
+    at[0] = place(desc->qsegs);
+    at[1] = place(desc->kvsegs);
+    at[2] = place(items);
+    at[3] = place(desc->bitems);
+    at[4] = place(desc->bentries);
+    at[5] = place(sitems);
+    at[6] = place(sentries);
+    at[7] = place(sfirst);
+    desc->dev.reserve(desc->dev.size() + 1);
+  });
+  e = cudaMalloc(&p.base, std::max<size_t>(image.size(), 256));
+  if (e == cudaSuccess && !image.empty()) e = cudaMemcpy(p.base, image.data(), image.size(), cudaMemcpyHostToDevice);
   if (e != cudaSuccess) {
-    cudaFree(p.qsegs);
-    cudaFree(p.kvsegs);
-    cudaFree(p.items);
-    cudaFree(p.bitems);
-    cudaFree(p.bentries);
-    cudaFree(p.sitems);
-    cudaFree(p.sentries);
-    cudaFree(p.sfirst);
+    cudaFree(p.base);
     return cuda_fail(e, "tree descriptor upload");
   }
+  uint8_t* b = static_cast<uint8_t*>(p.base);
+  p.qsegs = reinterpret_cast<QSeg*>(b + at[0]);
+  p.kvsegs = reinterpret_cast<KVSeg*>(b + at[1]);
+  p.items = reinterpret_cast<FwdItem*>(b + at[2]);
+  p.bitems = reinterpret_cast<BwdItem*>(b + at[3]);
+  p.bentries = reinterpret_cast<BwdEntry*>(b + at[4]);
+  p.sitems = reinterpret_cast<BwdItem*>(b + at[5]);
+  p.sentries = reinterpret_cast<BwdEntry*>(b + at[6]);
+  p.sfirst = reinterpret_cast<int32_t*>(b + at[7]);
   desc->dev.push_back(p);
   *plan_out = &desc->dev.back();
   return PADOC_OK;
@@ -635,7 +628,12 @@ static size_t bwd_parts_bytes(const padoc_tree_desc* desc, int32_t Hq, int32_t H
   if (d != kHeadDim || desc->bitems.empty() || !few_units(desc, Hkv) || !valid_group(Hq / Hkv)) return 0;
   int i = 0;
   while (1 << i < Hq / Hkv) ++i;
-  return 2 * sizeof(float) * static_cast<size_t>(desc->n_parts[i]) * kTileKeys * Hkv * d;
+  int32_t n = desc->n_parts[i].load(std::memory_order_relaxed);
+  if (n < 0) {
+    n = count_parts(desc, kTileRows >> i);
+    desc->n_parts[i].store(n, std::memory_order_relaxed);
+  }
+  return 2 * sizeof(float) * static_cast<size_t>(n) * kTileKeys * Hkv * d;
 }
 static size_t bwd_kept_ws_bytes(const padoc_tree_desc* desc, int32_t Hq, int32_t Hkv, int32_t d) {
   return bwd_ws_bytes(desc, Hq) + kept_rows_bytes(desc, Hq, d) + 2 * kept_rows_bytes(desc, Hkv, d) +
