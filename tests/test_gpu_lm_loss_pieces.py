@@ -1,6 +1,6 @@
 """The loss's gradients with the vocabulary in several pieces, in the forms that many rows do
 not reach: few rows with a target among many (G in two parts whose sums add up over pieces),
-sums of dh cut into parts that a shorter last piece leaves empty, and several tiles of dims.
+sums of dh both over pieces and in parts, and several tiles of dims.
 Definition and tolerances as in test_gpu_lm_loss."""
 import pytest
 
@@ -18,10 +18,11 @@ def some_targets(t, keep, seed):
     return t
 
 
-# 20001 rows: pieces of 66 tiles, 67 tiles of words.  9000: 145 tiles a piece and two parts of each,
-# 594 tiles of words.  D = 264 and 520: tiles of dims that end inside.
+# 20001 rows: two pieces, of 34 and 33 tiles of 256 words.  9000: five, each in two parts for dh.  300
+# rows and 700001 words: two pieces in 38 parts.  D = 264 and 520: tiles of dims that end inside.
 @pytest.mark.parametrize("n,D,V,keep", [(20001, 64, 17000, 1), (20001, 64, 17000, 100), (20001, 72, 17000, 128), (20001, 64, 17000, 129),
-                                        (20001, 264, 17000, 90), (9000, 64, 151936, 128), (9000, 64, 151936, 300)])
+                                        (20001, 264, 17000, 90), (9000, 64, 151936, 128), (9000, 64, 151936, 300),
+                                        (300, 72, 700001, 100), (300, 72, 700001, 300)])
 def test_few_targets_among_many_rows(padoc_lib, n, D, V, keep):
     h, w, t, d = make(n, D, V, seed=n + keep)
     t = some_targets(t, keep, 1)
