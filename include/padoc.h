@@ -458,9 +458,17 @@ PADOC_API int padoc_act_keep(int32_t n_tensors, const padoc_act* tensors, padoc_
 PADOC_API int padoc_act_restore(int32_t n_tensors, const padoc_act* tensors, padoc_stream_t stream);
 
 /* padoc_tree_attn_varlen_bwd from checkpoints of q, k, v and o (rows of Hq * d
- * or Hkv * d values, the forward's [T, H, d]): the gradients at the values that
- * the checkpoints stand for, with the forward's lse.  d_o, dq, dk and dv are
- * bf16.  ws of padoc_tree_attn_varlen_bwd_kept_ws_size bytes, 256-byte aligned,
+ * or Hkv * d values, the forward's [T, H, d]): its formula with P =
+ * exp(scale q.k - lse) and the row sums dO.o at the values that the checkpoints
+ * stand for.  Where the forward ran on those values (kept and restored before
+ * it), these are its gradients.  Where it ran first and q, k, v and o were kept
+ * after it, scores have moved by what the codes leave of q and k, rows of P sum
+ * to 1 only as far as that goes, and the gradients are off from the forward's:
+ * with q and k like N(0, 1) and d = 128, scores by 0.012 and dq, dk, dv by 1.9,
+ * 1.9 and 1.2 % of their norms; twice as large 5.7, 5.6 and 5.0 %; a few channels
+ * four times as strong as the others 6.1, 5.2 and 5.0 %.  P and dS are rounded to
+ * bf16 before their products, as in padoc_tree_attn_varlen_bwd.  d_o, dq, dk and
+ * dv are bf16.  ws of padoc_tree_attn_varlen_bwd_kept_ws_size bytes, 256-byte aligned,
  * holds q, k and v in bf16 for the time of the call; o is not expanded.  dq, dk,
  * dv and ws overlap nothing else in the call. */
 PADOC_API int padoc_tree_attn_varlen_bwd_kept_ws_size(const padoc_tree_desc* desc, int32_t Hq, int32_t Hkv, int32_t d,
