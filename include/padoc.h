@@ -368,8 +368,9 @@ PADOC_API int padoc_tree_desc_bwd_plan(const padoc_tree_desc* desc, int32_t* ite
  * Cosines and sines are multiplied by amplitude (0: by 1).  Positions lie in
  * [0, 2^31).  An angle is the position times f_i / 2 pi, computed in doubles
  * (2^-53, a few times over), modulo a turn and without a further rounding, then
- * cut off at 2^-32 of a turn, 1.5e-9; cosines and sines are then off by 4 2^-24 of
- * the amplitude (which is rounded to f32) at most.  One launch. */
+ * cut off at 2^-32 of a turn (its step at 2^-64), 2.2e-9 together at most;
+ * cosines and sines are then off by 4 2^-24 of the amplitude (which is rounded to
+ * f32) at most.  One launch. */
 enum { PADOC_ROPE_PLAIN = 0, PADOC_ROPE_LINEAR = 1, PADOC_ROPE_BASE = 2, PADOC_ROPE_BANDS = 3, PADOC_ROPE_RAMP = 4 };
 typedef struct {
   double base;       /* above 1 */

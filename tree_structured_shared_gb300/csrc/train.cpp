@@ -67,7 +67,7 @@ extern "C" int padoc_rope_table(const padoc_rope_scaling* sc, int64_t first, int
   }
   if (!(sc->amplitude >= 0.0) || !std::isfinite(static_cast<float>(sc->amplitude)))
     return set_error(PADOC_ERR_INVALID, "rope_table: amplitude must be a finite number of at least 0 (0 means 1)");
-  if (first < 0 || n_pos < 0 || first > INT32_MAX - static_cast<int64_t>(n_pos))
+  if (first < 0 || n_pos < 0 || first > (1ll << 31) - n_pos)
     return set_error(PADOC_ERR_INVALID, "rope_table: positions must lie in [0, 2^31)");
   if (n_pos == 0) return PADOC_OK;
   if (!cos_sin || !aligned16(cos_sin))
