@@ -16,6 +16,7 @@ def refused(f, *a, **kw):
 
 @pytest.fixture(autouse=True)
 def no_library(monkeypatch):
+    monkeypatch.setattr(padoc, "_lib", None)
     monkeypatch.setattr(padoc, "lib", lambda: pytest.fail("the library was called"))
 
 
@@ -111,5 +112,5 @@ def test_rope_strides_of_tensors(make, stride):
     """The rows that a call without strides takes."""
     x = torch.zeros(6, 256, dtype=torch.bfloat16)
     y = make(x)
-    assert padoc._rows(y, 6, 128, None, torch.bfloat16, 2) == (y if isinstance(y, int) else y.data_ptr(), stride)
-    assert padoc._rows(y, 6, 128, 264, torch.bfloat16, 2)[1] == 264
+    assert padoc._rows(y, 6, 128, 6 * 256, None, torch.bfloat16) == (y if isinstance(y, int) else y.data_ptr(), stride)
+    assert padoc._rows(y, 6, 128, 6 * 256, 264, torch.bfloat16)[1] == 264

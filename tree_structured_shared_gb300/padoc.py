@@ -361,6 +361,7 @@ def rope_table(cos_sin, n_pos: int, rot_dim: int, base: float, *, kind: int = RO
     _check(lib().padoc_rope_table(C.byref(sc), int(first), n_pos, _ptr(cos_sin), _stream(stream)))
 
 
+_NO_TYPE = (None, 0)
 _DTYPES = {}  # F32, BF16 -> torch's type and its bytes, once a tensor was seen
 
 
@@ -373,16 +374,17 @@ def _row_stride(x, n: int, row: int) -> int:
     raise PadocError(ERR_INVALID, "rope_apply: rows must be dense, or their stride be given")
 
 
-def _rows(x, n: int, row: int, stride, dtype, size: int):
-    """Address and row stride of n rows of `row` values, of a tensor or an address.  A step of
-    few tokens takes as long as the calls of this, so the usual tensor meets few of its own."""
+def _rows(x, n: int, row: int, nbytes: int, stride, dtype):
+    """Address and row stride of n rows of `row` values, `nbytes` in all, of a tensor or an
+    address."""
     if x is None or type(x) is int:
         return x or 0, row if stride is None else stride
+    # a step of few tokens takes as long as the host's calls: a dense tensor meets three here
     m = x.nbytes
-    if x.dtype is not dtype or m < n * row * size:
+    if x.dtype is not dtype or m < nbytes:
         raise PadocError(ERR_INVALID, f"rope_apply: a tensor must be {dtype} and hold n rows of its heads")
     if stride is None:
-        stride = row if m == n * row * size and x.is_contiguous() else _row_stride(x, n, row)
+        stride = row if m == nbytes and x.is_contiguous() else _row_stride(x, n, row)
     return x.data_ptr(), stride
 
 
@@ -393,21 +395,25 @@ def rope_apply(rope: "Rope", n: int, d: int, q, q_out, Hq: int, k=None, k_out=No
     between rows are taken as they are, and a tensor's own where None.  positions: int32."""
     if not _DTYPES and (t := sys.modules.get("torch")):
         _DTYPES.update({F32: (t.float32, 4), BF16: (t.bfloat16, 2), "positions": t.int32})
-    dt, size = _DTYPES.get(dtype, (None, 0))
-    hq, hk = Hq * d, Hkv * d
-    x, xs = _rows(q, n, hq, q_stride, dt, size)
-    y, ys = _rows(q_out, n, hq, q_out_stride, dt, size)
+    dt, size = _DTYPES.get(dtype, _NO_TYPE)
+    hq = Hq * d
+    m = n * hq * size
+    x, xs = _rows(q, n, hq, m, q_stride, dt)
+    y, ys = _rows(q_out, n, hq, m, q_out_stride, dt)
     if k is None:
         count, parts = 1, _PARTS(x, xs, y, ys, Hq, 0, 0, 0, 0, 0)
     else:
-        v, vs = _rows(k, n, hk, k_stride, dt, size)
-        w, ws = _rows(k_out, n, hk, k_out_stride, dt, size)
+        hk = Hkv * d
+        m = n * hk * size
+        v, vs = _rows(k, n, hk, m, k_stride, dt)
+        w, ws = _rows(k_out, n, hk, m, k_out_stride, dt)
         count, parts = 2, _PARTS(x, xs, y, ys, Hq, v, vs, w, ws, Hkv)
     if positions is not None and type(positions) is not int:
         if positions.dtype is not _DTYPES["positions"] or positions.nbytes < 4 * n or not positions.is_contiguous():
             raise PadocError(ERR_INVALID, "rope_apply: positions must be n dense int32 values")
         positions = positions.data_ptr()
-    rc = lib().padoc_rope_apply(rope.ref, count, parts, dtype, d, n, positions, 1 if backward else 0, _stream(stream))
+    s = _current_stream() or None if stream is None and _current_stream else _stream(stream)
+    rc = (_lib or lib()).padoc_rope_apply(rope.ref, count, parts, dtype, d, n, positions, 1 if backward else 0, s)
     if rc:
         _check(rc)
 
