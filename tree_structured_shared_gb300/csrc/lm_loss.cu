@@ -512,13 +512,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           give_up(abort, 256u);
           break;
         }
-        const bool last = taken(sbase + SM_UNIT + 32 * slot).kind == END;
+        if (taken(sbase + SM_UNIT + 32 * slot).kind == END) break;  // its slot is not written again
         if (!wait<false>(bar(B_U_READ + slot), phase, abort, a.wait_limit)) {
           give_up(abort, 512u);
           break;
         }
         arrive_released(in_cta(bar(B_U_FREE + slot), 0));
-        if (last) break;
       }
     }
     __syncwarp();
