@@ -409,11 +409,16 @@ PADOC_API int padoc_rope_apply(const padoc_rope* rope, int32_t n_parts, const pa
  * x = h w^T (f32):
  *   lse = log sum_v exp(x_v),  loss = lse - x_target        (f32, one a row)
  *   G = d_loss (exp(x - lse) - onehot(target)),  dh = G w,  dw = G^T h
- * G is rounded to bf16 before the two products, whose sums are f32 (up to 128
- * rows with a target it has two bf16 parts).  A row with
- * a negative target has no loss: loss and lse are 0, its dh is zero and it takes
- * no part in dw, whatever h holds there; its products are not computed.  A
- * target of V or more is treated alike but for a loss of NaN.
+ * Sums are f32.  G is rounded to bf16 before the two products, by 2^-8 of it; with
+ * the rounding of dh and dw themselves that is 0.0023 of their norms, where one
+ * rounding is 0.0017.  A call with 128 rows with a target or fewer, a number that
+ * the host need not know, holds G in two bf16 parts (2^-16).  loss and lse come
+ * from exponentials within 2^-22 of themselves (4e-7 to 6e-7 of their norms), and
+ * no loss is negative.  lse is rounded to f32, which moves exp(x - lse) of the
+ * backward call by up to |lse| 2^-24 of itself.  A row with a negative target has
+ * no loss: loss and lse are 0, its dh is zero and it takes no part in dw, whatever
+ * h holds there; its products are not computed.  A target of V or more is treated
+ * alike but for a loss of NaN.
  *   loss, lse  device [n] f32 out; lse goes into the backward call as it is
  *   d_loss     device [n] f32: the gradient of each row's loss (1 / count for
  *              a mean); not read where there is no target
@@ -472,8 +477,10 @@ PADOC_API int padoc_act_restore(int32_t n_tensors, const padoc_act* tensors, pad
  * with q and k like N(0, 1) and d = 128, scores by 0.012 and dq, dk, dv by 1.9,
  * 1.9 and 1.2 % of their norms; twice as large 5.7, 5.6 and 5.0 %; a few channels
  * four times as strong as the others 6.1, 5.2 and 5.0 %.  P and dS are rounded to
- * bf16 before their products, as in padoc_tree_attn_varlen_bwd.  d_o, dq, dk and
- * dv are bf16.  ws of padoc_tree_attn_varlen_bwd_kept_ws_size bytes, 256-byte aligned,
+ * bf16 before their products, as in padoc_tree_attn_varlen_bwd (0.0024 of the
+ * norms).  d is 128, or 64, which runs on the CUDA cores and takes a hundred
+ * times as long and more.  d_o, dq, dk and dv are bf16.  ws of
+ * padoc_tree_attn_varlen_bwd_kept_ws_size bytes, 256-byte aligned,
  * holds q, k and v in bf16 for the time of the call; o is not expanded.  dq, dk,
  * dv and ws overlap nothing else in the call. */
 PADOC_API int padoc_tree_attn_varlen_bwd_kept_ws_size(const padoc_tree_desc* desc, int32_t Hq, int32_t Hkv, int32_t d,

@@ -17,7 +17,7 @@
 // of values and 16 of codes.  Magnitudes are compared as integers, two at a time: bf16
 // bits without the sign are in the order of the values, infinities and NaNs on top.
 //
-// 131072 rows of 6144 values in four tensors: kept in 360 us, restored in 367, 6.7 TB/s (360
+// 131072 rows of 6144 values in four tensors: kept in 360 us, restored in 364, 6.7 TB/s (360
 // each at the copy rate).  462 rows of 1536: 4 us each, a launch.
 #include <cuda_bf16.h>
 
@@ -37,7 +37,8 @@ constexpr int kThreads = 256;
 constexpr int kUnroll = 2;  // pieces of 16 values a thread, kThreads apart
 constexpr int64_t kPiecesRound = kThreads * kUnroll;
 // A CTA costs its launch: long tensors take kRounds of them one after another (131072 rows
-// of 6144 values 365 and 367 us, with one 379 and 404, with 16 370 and 372); short ones
+// of 6144 values 360 and 364 us; with one round 379 and 404, with 16 5 us more than with
+// four); short ones
 // spread over the GPU (462 rows of 1536 4.3 us, with four rounds 6.3).
 constexpr int kRounds = 4, kManyRounds = 16 * 152;
 

@@ -42,13 +42,13 @@
 //
 // What bounds it.  Many rows: the tensor cores.  16384 rows, 14746 of them with a target,
 // 151936 words, D = 1024: lm_kernel<forward> 2.30 ms, 2.0 PFLOP/s; a backward launch, three
-// products of a piece of 19200 words, 0.915 ms, 1.9 PFLOP/s (tensor pipe 93 % busy on 4096
-// rows); back to back the power limit makes that 2.4 and 8.2 ms.  Copies then run at 54
+// products of a piece of 19200 words, 0.92 ms, 1.9 PFLOP/s (tensor pipe 92 % busy on 4096
+// rows); back to back the power limit makes that 2.5 and 8.4 ms.  Copies then run at 54
 // bytes a cycle and SM, which is what they reach without products too.  Few rows: reading
-// the weights, and latency.  One row, 151936 words: 54 us for 311 MB of weights (a plain
-// read of them takes 57).  397 rows, 32003 words, D = 896: forward 32 us, of which 15 are
+// the weights, and latency.  One row, 151936 words: 54 to 57 us for 311 MB of weights (a plain
+// read of them takes 57).  397 rows, 32003 words, D = 896: forward 33 us, of which 15 are
 // products (four rounds of tiles, the last a third full), 4 the gathering of rows, 3 until
-// the first stage is there, 3 from the last one to the end and 3 the join; backward 88.
+// the first stage is there, 3 from the last one to the end and 3 the join; backward 90.
 // Steps on the way, 16384 rows and 397 rows, forward and backward together (ms, us):
 //   first right kernel 11.3, 169
 //   a tile leaves TMEM at once, before it is worked on, packed arithmetic 11.0, 137

@@ -25,7 +25,7 @@
 // 246 us, 6.6 TB/s of reads and writes (240 at the copy rate).  50003 rows of 6 heads of 64
 // in f32: 30 us (23.4): rows of 1.5 KB are short for a warp, and a GPU of CTAs takes 2.7
 // rounds of them; with each lane's 16 dims side by side, which spreads a load over twice
-// the lines, 37.  384 rows: 6 us, a launch.  A table of 131072 positions of 128: 14.3 us
+// the lines, 37.  384 rows: 6 us, the host's call.  A table of 131072 positions of 128: 14.3 us
 // for 67 MB (a fill of them takes 12.5); with sincospif on the remainder of a 64-bit
 // product 20.6.
 #include <cuda_bf16.h>
